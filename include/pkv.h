@@ -338,6 +338,67 @@ pkv_status pkv_qk_norm_rope_store(const void *qkv, int64_t qkv_tok_stride, int64
                                   void *v_cache, int64_t num_slots, int32_t num_q_heads,
                                   int32_t num_kv_heads, int32_t head_dim, void *stream);
 
+/* ------------------------------------------------------------------ the 8-bit cache
+ *
+ * A second form of a layer's pools: [num_blocks, block_size, num_kv_heads, 128] e4m3 codes (one
+ * byte a value), and for each pool the scales [num_blocks, num_kv_heads, block_size / 64] fp32,
+ * one for every PKV_FP8_GROUP consecutive tokens of a block and head. A cached value is code *
+ * scale. pkv_kv_store_fp8 writes power-of-two scales: 2^e with e the smallest integer >= -90
+ * for which the group's largest finite |x| is at most 448 * 2^e.
+ */
+#define PKV_FP8_GROUP 64
+
+/*
+ * kv_store_fp8 -- append new K/V rows to the 8-bit cache. The new tokens of sequence b are its
+ * last positions: rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of k and v are positions
+ * context_lens[b] - n .. context_lens[b] - 1, n = cu_seqlens[b + 1] - cu_seqlens[b] >= 0. With
+ * cu_seqlens == NULL row b is position context_lens[b] - 1 of sequence b (a decode step;
+ * num_tokens must equal num_seqs), and a context length of 0 stores nothing (a padding row).
+ *
+ * Per group, head and pool: let s0 be the scale of the group's rows from before the call (its
+ * positions below context_lens[b] - n; 0 if there are none) and s1 the scale of the new rows
+ * alone. The group's scale becomes s = max(s0, s1); if s > s0 the codes from before become
+ * e4m3(code * s0 / s); the new codes are e4m3(x / s). e4m3() rounds to nearest even; +-inf
+ * becomes +-448, NaN stays NaN. Rows of the group past the context are left as they are.
+ *
+ * k, v:          [num_tokens, num_kv_heads, head_dim] bf16, token strides in elements
+ *                (multiples of 8), dense rows.
+ * cu_seqlens:    NULL, or [num_seqs + 1] int32, non-decreasing, within [0, num_tokens].
+ * context_lens:  [num_seqs] int32, the lengths with the new tokens.
+ * block_tables:  [num_seqs, block_table_width] int32. A block that the call writes belongs to
+ *                one sequence of the call (blocks shared with others, e.g. a cached prefix, hold
+ *                earlier positions only).
+ * A bad cu_seqlens entry (PKV_DEVERR_SEQLEN_RANGE) or context length
+ * (PKV_DEVERR_CONTEXT_RANGE) skips the sequence, a bad block id (PKV_DEVERR_BLOCK_RANGE) the
+ * rows that go there.
+ * Implemented: head_dim == 128, block_size a multiple of 256, 16-byte aligned pointers.
+ */
+pkv_status pkv_kv_store_fp8(const void *k, int64_t k_tok_stride, const void *v,
+                            int64_t v_tok_stride, const int32_t *cu_seqlens,
+                            const int32_t *context_lens, const int32_t *block_tables,
+                            int32_t block_table_width, int32_t num_seqs, int64_t num_tokens,
+                            void *k_cache, void *v_cache, float *k_scale, float *v_scale,
+                            int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                            int64_t num_blocks, void *stream);
+
+/*
+ * kv_gather_fp8 -- cached rows back to packed bf16, for pkv_varlen_prefill_attn over an 8-bit
+ * cache (a cached prefix, or a chunk of a prompt whose earlier chunks are cached): row
+ * cu_seqlens_k[n] + j of k_out / v_out [total_k, num_kv_heads, head_dim] becomes code * scale of
+ * position j of sequence n, for 0 <= j < cu_seqlens_k[n + 1] - cu_seqlens_k[n]. The products
+ * are exact in bf16 for the scales that pkv_kv_store_fp8 writes. Rows of no sequence are left
+ * as they are; rows of a bad block id become zeros (PKV_DEVERR_BLOCK_RANGE).
+ * block_table: [num_seqs, block_table_width] int32 (blocks may be shared); cu_seqlens_k:
+ * [num_seqs + 1] int32, within [0, total_k].
+ * Implemented: head_dim == 128, block_size a multiple of 256, 16-byte aligned pointers.
+ */
+pkv_status pkv_kv_gather_fp8(const void *k_cache, const void *v_cache, const float *k_scale,
+                             const float *v_scale, const int32_t *block_table,
+                             int32_t block_table_width, const int32_t *cu_seqlens_k,
+                             int32_t num_seqs, int64_t total_k, void *k_out, void *v_out,
+                             int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                             int64_t num_blocks, void *stream);
+
 /* ------------------------------------------------------------------ block manager (host)
  *
  * The owner of the pool's blocks on the host: «nano-vLLM 最小化vLLM重新实现», 架构 3 (块管理器)

@@ -47,6 +47,10 @@ SIGNATURES = {
                                        _P, _SZ, _P, _P]),
     "pkv_qk_norm_rope_store": (_I32, [_P, _I64, _I64, _P, _P, _P, _F, _P, _I64, _P, _P, _P,
                                       _P, _I64, _I32, _I32, _I32, _P]),
+    "pkv_kv_store_fp8": (_I32, [_P, _I64, _P, _I64, _P, _P, _P, _I32, _I32, _I64, _P, _P, _P, _P,
+                                _I32, _I32, _I32, _I64, _P]),
+    "pkv_kv_gather_fp8": (_I32, [_P, _P, _P, _P, _P, _I32, _P, _I32, _I64, _P, _P, _I32, _I32,
+                                 _I32, _I64, _P]),
     "pkv_bm_create": (_P, [_I32, _I32]),
     "pkv_bm_destroy": (None, [_P]),
     "pkv_bm_num_free": (_I32, [_P]),
@@ -336,6 +340,110 @@ def qk_norm_rope_store(qkv, positions, q_norm_weight, k_norm_weight, eps, cos_si
         q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), num_slots, num_q_heads,
         num_kv_heads, D, _stream(stream)))
     return q_out
+
+
+# ----------------------------------------------------------------------------- the 8-bit cache
+FP8_GROUP = 64  # tokens of a block that share a scale
+
+
+def _need_fp8_cache(k_cache, v_cache, k_scale, v_scale):
+    """Checks the four tensors of an 8-bit cache; returns (num_blocks, block_size, hkv, d)."""
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _need(t, n, torch.float8_e4m3fn)
+    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        _need(t, n, torch.float32)
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+        raise ValueError("caches must be [NB, bs, Hkv, D], the same for K and V")
+    nb, bs, hkv, d = k_cache.shape
+    want = (nb, hkv, bs // FP8_GROUP)
+    if tuple(k_scale.shape) != want or tuple(v_scale.shape) != want:
+        raise ValueError(f"scales must be [NB, Hkv, bs / {FP8_GROUP}] = {list(want)}")
+    if not all(t.is_contiguous() for t in (k_cache, v_cache, k_scale, v_scale)):
+        raise ValueError("caches and scales must be contiguous")
+    return nb, bs, hkv, d
+
+
+def _need_list(t, name, shape, device):
+    """An int32 tensor of this shape (None: any size), contiguous, on the caches' device."""
+    _need(t, name, torch.int32)
+    if (t.dim() != len(shape) or any(a is not None and a != b for a, b in zip(shape, t.shape))
+            or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape "
+                         f"{['*' if a is None else a for a in shape]}")
+    _same_device(t, name, device)
+
+
+def _same_device(t, name, device):
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the caches on {device}")
+
+
+def _on(device) -> torch.cuda.device:
+    """Launches go to the tensors' device, whichever is current."""
+    return torch.cuda.device(device)
+
+
+def kv_store_fp8(k: torch.Tensor, v: torch.Tensor, context_lens: torch.Tensor,
+                 block_tables: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                 k_scale: torch.Tensor, v_scale: torch.Tensor,
+                 cu_seqlens: torch.Tensor | None = None, stream=None) -> None:
+    """Append new K/V rows to an 8-bit cache: sequence b's rows cu_seqlens[b]..cu_seqlens[b+1]
+    are its last positions before context_lens[b] (without cu_seqlens: one row per sequence).
+
+    k, v: [T, Hkv, D] bf16 with dense rows (token stride may be larger); context_lens [B],
+    block_tables [B, W], cu_seqlens [B + 1] int32; caches [NB, bs, Hkv, D] float8_e4m3fn;
+    scales [NB, Hkv, bs / 64] float32. A group of 64 positions keeps one power-of-two scale per
+    head; it grows, and the group's earlier rows are re-rounded, when a new row needs it."""
+    nb, bs, hkv, d = _need_fp8_cache(k_cache, v_cache, k_scale, v_scale)
+    dev = k_cache.device
+    for t, n in ((k, "k"), (v, "v")):
+        _need(t, n, torch.bfloat16)
+        _same_device(t, n, dev)
+        if t.dim() != 3 or t.shape[1:] != (hkv, d) or t.stride(2) != 1 or (
+                t.stride(1) != d and hkv > 1):
+            raise ValueError(f"{n} must be [T, {hkv}, {d}] with dense rows")
+    T = k.shape[0]
+    if v.shape[0] != T:
+        raise ValueError("k and v must hold the same tokens")
+    _need_list(context_lens, "context_lens", (None,), dev)
+    B = context_lens.shape[0]
+    _need_list(block_tables, "block_tables", (B, None), dev)
+    if cu_seqlens is not None:
+        _need_list(cu_seqlens, "cu_seqlens", (B + 1,), dev)
+    with _on(dev):
+        _check("pkv_kv_store_fp8", _LIB.pkv_kv_store_fp8(
+            _ptr(k), k.stride(0) if T > 1 else hkv * d, _ptr(v),
+            v.stride(0) if T > 1 else hkv * d, _ptr(cu_seqlens), _ptr(context_lens),
+            _ptr(block_tables), block_tables.shape[1], B, T, _ptr(k_cache), _ptr(v_cache),
+            _ptr(k_scale), _ptr(v_scale), hkv, d, bs, nb, _stream(stream)))
+
+
+def kv_gather_fp8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                  v_scale: torch.Tensor, block_table: torch.Tensor, cu_seqlens_k: torch.Tensor,
+                  total_k: int, k_out: torch.Tensor | None = None,
+                  v_out: torch.Tensor | None = None, stream=None):
+    """Rows of an 8-bit cache as packed bf16 (k, v) [total_k, Hkv, D]: positions 0 .. of sequence
+    n at rows cu_seqlens_k[n] .. cu_seqlens_k[n + 1], as varlen_prefill_attn takes them."""
+    nb, bs, hkv, d = _need_fp8_cache(k_cache, v_cache, k_scale, v_scale)
+    dev = k_cache.device
+    _need_list(cu_seqlens_k, "cu_seqlens_k", (None,), dev)
+    N = cu_seqlens_k.shape[0] - 1
+    _need_list(block_table, "block_table", (N, None), dev)
+    outs = []
+    for t, n in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is None:
+            t = torch.empty((int(total_k), hkv, d), dtype=torch.bfloat16, device=dev)
+        _need(t, n, torch.bfloat16)
+        _same_device(t, n, dev)
+        if tuple(t.shape) != (int(total_k), hkv, d) or not t.is_contiguous():
+            raise ValueError(f"{n} must be a contiguous [{int(total_k)}, {hkv}, {d}] tensor")
+        outs.append(t)
+    with _on(dev):
+        _check("pkv_kv_gather_fp8", _LIB.pkv_kv_gather_fp8(
+            _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
+            block_table.shape[1], _ptr(cu_seqlens_k), N, int(total_k), _ptr(outs[0]),
+            _ptr(outs[1]), hkv, d, bs, nb, _stream(stream)))
+    return outs[0], outs[1]
 
 
 # ----------------------------------------------------------------------------- block manager

@@ -1,0 +1,441 @@
+// fp8_cache.cu -- writing the 8-bit cache (kv_store_fp8) and reading it back as bf16
+// (kv_gather_fp8). The format is in fp8_cache.cuh.
+//
+// Store: the new tokens are each sequence's last positions. One CTA owns one run (the new rows
+// of one sequence that lie in one group of 64 positions) of one KV head, K and V together, so
+// nothing else touches the group's scale: it holds the run's rows in registers, reduces
+// max |x| over them, takes the larger of the scale that asks for and the scale of the rows the
+// group already held, and writes the codes. Each row is read once and written once:
+// 512 + 256 bytes per token and head, nothing else of that order. When the scale grows, the
+// rows from before the call are re-rounded to it in place (at most 63 rows of 128 bytes).
+// A step of one token per sequence takes a warp per (sequence, head) instead of a CTA.
+//
+// Gather: one CTA per (run, head); 128 bytes in and 256 bytes out per token, head and K or V.
+//
+// Both are bound by HBM.
+#include <math.h>
+
+#include "device_common.cuh"
+#include "fp8_cache.cuh"
+#include "launch.h"
+#include "pkv.h"
+
+namespace pkv {
+namespace {
+
+constexpr int kD = 128;
+constexpr unsigned kFull = 0xffffffffu;
+constexpr unsigned int kErrBlock = 2u, kErrContext = 4u, kErrSeqlen = 8u;  // PKV_DEVERR_*
+
+struct StoreParams {
+  const uint8_t *k, *v;           // bf16 rows
+  int64_t k_stride, v_stride;     // bytes per token
+  const int32_t *cu;              // nullptr: one token per sequence
+  const int32_t *context_lens;
+  const int32_t *block_tables;
+  int32_t table_width, num_seqs;
+  int64_t num_tokens;
+  uint8_t *k_cache, *v_cache;
+  float *k_scale, *v_scale;
+  int32_t hkv, block_size;
+  int64_t num_blocks;
+  unsigned int *err;
+};
+
+// Block of position pos of a sequence's table row, or -1 (recorded) for a bad id.
+__device__ __forceinline__ int64_t block_of(const int32_t *table, int64_t pos, int32_t block_size,
+                                            int64_t num_blocks, unsigned int *err, bool record) {
+  const int32_t b = __ldg(table + pos / block_size);
+  if (b >= 0 && b < num_blocks) return b;
+  if (record) record_error(err, kErrBlock);
+  return -1;
+}
+
+// The batch's lengths, looked over once (by the first CTA): every sequence whose cu or context
+// length is bad, which the runs' own checks leave out.
+template <bool kStore>
+__device__ __forceinline__ void check_lengths(const int32_t *cu, const int32_t *context_lens,
+                                              int32_t num_seqs, int64_t total, int64_t capacity,
+                                              unsigned int *err) {
+  for (int i = threadIdx.x; i < num_seqs; i += blockDim.x) {
+    const int32_t c0 = __ldg(cu + i), c1 = __ldg(cu + i + 1);
+    const int64_t ctx = kStore ? (int64_t)__ldg(context_lens + i) : (int64_t)c1 - c0;
+    if (c0 < 0 || c1 < c0 || c1 > total || ctx < (int64_t)c1 - c0) record_error(err, kErrSeqlen);
+    else if (ctx > capacity) record_error(err, kErrContext);
+  }
+}
+
+// One CTA: a run of one head. Thread t holds bytes [16 (t % 16), +16) of rows t / 16 + 16 i of
+// the run, for K and for V.
+constexpr int kRunThreads = 256;
+constexpr int kRowsPerPass = kRunThreads / 16;
+constexpr int kPasses = kFp8Group / kRowsPerPass;
+
+__global__ void __launch_bounds__(kRunThreads)
+    kv_store_fp8_run_kernel(const StoreParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ uint32_t warp_max[2][kRunThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t r = blockIdx.x / p.hkv;
+  const int h = (int)(blockIdx.x % p.hkv);
+  const int n = find_sequence(p.cu, p.num_seqs, r, lane);
+  const int32_t c0 = __ldg(p.cu + n), c1 = __ldg(p.cu + n + 1), ctx = __ldg(p.context_lens + n);
+  const int64_t j = r - run_base(c0, n);
+  const int64_t capacity = (int64_t)p.table_width * p.block_size;
+  if (blockIdx.x == 0)
+    check_lengths<true>(p.cu, p.context_lens, p.num_seqs, p.num_tokens, capacity, p.err);
+  if (c0 < 0 || c1 < c0 || c1 > p.num_tokens || ctx < (int64_t)c1 - c0 ||
+      ctx > capacity)
+    return;
+  const int start = ctx - (c1 - c0);                          // first new position
+  const int64_t group = (int64_t)(start / kFp8Group) + j;     // group index in the sequence
+  const int64_t begin = max((int64_t)start, group * kFp8Group);
+  const int64_t end = min((int64_t)ctx, (group + 1) * kFp8Group);
+  if (j < 0 || begin >= end) return;
+  const int64_t blk = block_of(p.block_tables + (int64_t)n * p.table_width, begin, p.block_size,
+                               p.num_blocks, p.err, threadIdx.x == 0 && h == 0);
+  if (blk < 0) return;
+  const int in_block = (int)(begin % p.block_size);
+  const int before = in_block % kFp8Group;  // rows of the group from before the call
+  const int rows = (int)(end - begin);
+  const int64_t sc = (blk * p.hkv + h) * (p.block_size / kFp8Group) + in_block / kFp8Group;
+
+  const int part = threadIdx.x & 15, row0 = threadIdx.x >> 4;
+  const uint8_t *ks = p.k + (c0 + begin - start) * p.k_stride + h * (kD * 2) + part * 16;
+  const uint8_t *vs = p.v + (c0 + begin - start) * p.v_stride + h * (kD * 2) + part * 16;
+  uint4 x[2][kPasses];
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int row = row0 + i * kRowsPerPass;
+    x[0][i] = x[1][i] = make_uint4(0, 0, 0, 0);
+    if (row < rows) {
+      x[0][i] = ld_stream_u4(reinterpret_cast<const uint4 *>(ks + row * p.k_stride));
+      x[1][i] = ld_stream_u4(reinterpret_cast<const uint4 *>(vs + row * p.v_stride));
+    }
+  }
+  float old[2] = {0.f, 0.f};
+  if (before) {
+    old[0] = p.k_scale[sc];
+    old[1] = p.v_scale[sc];
+  }
+  // max |x| of the run, then of its finite values if there is an infinity or a NaN
+  uint32_t amax[2];
+  for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) {
+        uint4 w = x[s][i];
+        if (pass) {
+          w.x = bf16x2_finite(w.x);
+          w.y = bf16x2_finite(w.y);
+          w.z = bf16x2_finite(w.z);
+          w.w = bf16x2_finite(w.w);
+        }
+        m = __vmaxu2(m, __vmaxu2(bf16x2_absmax(w.x, w.y), bf16x2_absmax(w.z, w.w)));
+      }
+      m = max(m & 0xffffu, m >> 16);
+      m = __reduce_max_sync(kFull, m);
+      if (lane == 0) warp_max[s][warp] = m;
+    }
+    // an earlier wait gave up somewhere: write nothing (decided by the CTA together)
+    if (__syncthreads_or(threadIdx.x == 0 && aborted(p.err))) return;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      amax[s] = 0;
+#pragma unroll
+      for (int w = 0; w < kRunThreads / 32; ++w) amax[s] = max(amax[s], warp_max[s][w]);
+    }
+    if (max(amax[0], amax[1]) < 0x7f80u) break;
+    __syncthreads();
+  }
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    uint8_t *cache = s ? p.v_cache : p.k_cache;
+    const int e = fp8_scale_exp(amax[s]);
+    const float scale = fmaxf(pow2f(e), old[s]);
+    const int64_t rstride = (int64_t)p.hkv * kD;
+    uint8_t *dst = cache + (blk * p.block_size + in_block) * rstride + h * kD;
+    if (before && scale > old[s]) {  // the rows from before, at the scale that grew
+      const float ratio = old[s] / scale;
+      for (int i = threadIdx.x; i < before * 8; i += kRunThreads) {
+        uint4 *q = reinterpret_cast<uint4 *>(dst - (int64_t)(before - i / 8) * rstride + (i % 8) * 16);
+        uint4 w = *q;
+        w.x = rescale4(w.x, ratio);
+        w.y = rescale4(w.y, ratio);
+        w.z = rescale4(w.z, ratio);
+        w.w = rescale4(w.w, ratio);
+        *q = w;
+      }
+    }
+    const float inv = 1.f / scale;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int row = row0 + i * kRowsPerPass;
+      if (row < rows) {
+        const uint4 w = x[s][i];
+        *reinterpret_cast<uint2 *>(dst + row * rstride + part * 8) =
+            make_uint2(quantize4(w.x, w.y, inv), quantize4(w.z, w.w, inv));
+      }
+    }
+    if (threadIdx.x == 0) (s ? p.v_scale : p.k_scale)[sc] = scale;
+  }
+}
+
+// One warp: the new token of one sequence, one head. Lanes 0-15 hold K, lanes 16-31 V, eight
+// values each.
+constexpr int kTokenWarps = 4;
+__global__ void __launch_bounds__(kTokenWarps * 32)
+    kv_store_fp8_token_kernel(const StoreParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int lane = threadIdx.x & 31, part = lane & 15;
+  const bool is_v = lane >= 16;
+  const int64_t unit = (int64_t)blockIdx.x * kTokenWarps + (threadIdx.x >> 5);
+  if (unit >= (int64_t)p.num_seqs * p.hkv) return;
+  const int n = (int)(unit / p.hkv), h = (int)(unit % p.hkv);
+  const uint8_t *src = is_v ? p.v + n * p.v_stride : p.k + n * p.k_stride;
+  const uint4 x = ld_stream_u4(reinterpret_cast<const uint4 *>(src + h * (kD * 2) + part * 16));
+  const int32_t ctx = __ldg(p.context_lens + n);
+  if (ctx == 0) return;  // a padding row
+  if (ctx < 0 || (int64_t)ctx > (int64_t)p.table_width * p.block_size) {
+    if (lane == 0 && h == 0) record_error(p.err, kErrContext);
+    return;
+  }
+  if (aborted(p.err)) return;
+  const int64_t blk = block_of(p.block_tables + (int64_t)n * p.table_width, ctx - 1, p.block_size,
+                               p.num_blocks, p.err, lane == 0 && h == 0);
+  if (blk < 0) return;
+  const int in_block = (ctx - 1) % p.block_size;
+  const int before = in_block % kFp8Group;
+  const int64_t sc = (blk * p.hkv + h) * (p.block_size / kFp8Group) + in_block / kFp8Group;
+  float *scales = is_v ? p.v_scale : p.k_scale;
+  const float old = before ? scales[sc] : 0.f;
+  uint32_t m = __vmaxu2(bf16x2_absmax(x.x, x.y), bf16x2_absmax(x.z, x.w));
+  m = max(m & 0xffffu, m >> 16);
+  if (m >= 0x7f80u) {
+    m = __vmaxu2(bf16x2_absmax(bf16x2_finite(x.x), bf16x2_finite(x.y)),
+                 bf16x2_absmax(bf16x2_finite(x.z), bf16x2_finite(x.w)));
+    m = max(m & 0xffffu, m >> 16);
+  }
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
+  const float scale = fmaxf(pow2f(fp8_scale_exp(m)), old);
+  const int64_t rstride = (int64_t)p.hkv * kD;
+  uint8_t *dst = (is_v ? p.v_cache : p.k_cache) + (blk * p.block_size + in_block) * rstride +
+                 h * kD + part * 8;
+  if (before && scale > old) {
+    const float ratio = old / scale;
+#pragma unroll 4
+    for (int i = 1; i <= before; ++i) {
+      uint2 *q = reinterpret_cast<uint2 *>(dst - i * rstride);
+      const uint2 w = *q;
+      *q = make_uint2(rescale4(w.x, ratio), rescale4(w.y, ratio));
+    }
+  }
+  const float inv = 1.f / scale;
+  *reinterpret_cast<uint2 *>(dst) = make_uint2(quantize4(x.x, x.y, inv), quantize4(x.z, x.w, inv));
+  if (part == 0) scales[sc] = scale;
+}
+
+struct GatherParams {
+  const uint8_t *k_cache, *v_cache;
+  const float *k_scale, *v_scale;
+  const int32_t *block_table;
+  int32_t table_width;
+  const int32_t *cu;
+  int32_t num_seqs;
+  int64_t total;
+  uint8_t *k_out, *v_out;
+  int32_t hkv, block_size;
+  int64_t num_blocks;
+  unsigned int *err;
+};
+
+// One CTA: a run (up to 64 positions of one group) of one head. Eight lanes read a row (16 codes
+// each) and write its 16 bf16.
+__global__ void __launch_bounds__(kRunThreads) kv_gather_fp8_kernel(const GatherParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  const int64_t r = blockIdx.x / p.hkv;
+  const int h = (int)(blockIdx.x % p.hkv);
+  const int n = find_sequence(p.cu, p.num_seqs, r, lane);
+  const int32_t c0 = __ldg(p.cu + n), c1 = __ldg(p.cu + n + 1);
+  const int64_t j = r - run_base(c0, n);
+  const int64_t capacity = (int64_t)p.table_width * p.block_size;
+  if (blockIdx.x == 0)
+    check_lengths<false>(p.cu, nullptr, p.num_seqs, p.total, capacity, p.err);
+  const int64_t len = (int64_t)c1 - c0;
+  if (c0 < 0 || len < 0 || c1 > p.total || len > capacity) return;
+  const int64_t begin = j * kFp8Group, end = min(len, begin + kFp8Group);
+  if (j < 0 || begin >= end || aborted(p.err)) return;
+  const int64_t blk = block_of(p.block_table + (int64_t)n * p.table_width, begin, p.block_size,
+                               p.num_blocks, p.err, threadIdx.x == 0 && h == 0);
+  const int in_block = (int)(begin % p.block_size), rows = (int)(end - begin);
+  const int part = threadIdx.x & 7, row0 = threadIdx.x >> 3;
+  constexpr int kPer = kRunThreads / 8;
+  uint4 x[2][kFp8Group / kPer];
+  float scale[2] = {0.f, 0.f};
+  const int64_t rstride = (int64_t)p.hkv * kD;
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int i = 0; i < kFp8Group / kPer; ++i) x[s][i] = make_uint4(0, 0, 0, 0);
+  if (blk >= 0) {  // the rows of a bad block id are zeros, as in the attention kernels
+    const int64_t sc = (blk * p.hkv + h) * (p.block_size / kFp8Group) + in_block / kFp8Group;
+    scale[0] = __ldg(p.k_scale + sc);
+    scale[1] = __ldg(p.v_scale + sc);
+    const int64_t at = (blk * p.block_size + in_block) * rstride + h * kD + part * 16;
+#pragma unroll
+    for (int i = 0; i < kFp8Group / kPer; ++i) {
+      const int row = row0 + i * kPer;
+      if (row < rows) {
+        x[0][i] = ld_stream_u4(reinterpret_cast<const uint4 *>(p.k_cache + at + row * rstride));
+        x[1][i] = ld_stream_u4(reinterpret_cast<const uint4 *>(p.v_cache + at + row * rstride));
+      }
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    uint8_t *out = (s ? p.v_out : p.k_out) + ((c0 + begin) * rstride + h * kD + part * 16) * 2;
+#pragma unroll
+    for (int i = 0; i < kFp8Group / kPer; ++i) {
+      const int row = row0 + i * kPer;
+      if (row < rows) {
+        const uint4 w = x[s][i];
+        const uint2 a = dequantize4(w.x, scale[s]), b = dequantize4(w.y, scale[s]);
+        const uint2 c = dequantize4(w.z, scale[s]), d = dequantize4(w.w, scale[s]);
+        uint4 *q = reinterpret_cast<uint4 *>(out + row * rstride * 2);
+        q[0] = make_uint4(a.x, a.y, b.x, b.y);
+        q[1] = make_uint4(c.x, c.y, d.x, d.y);
+      }
+    }
+  }
+}
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Launch as a programmatic dependent of the stream's previous kernel (every kernel here waits
+// for it before it reads anything).
+template <class P>
+cudaError_t launch_after(void (*kernel)(P), int64_t grid, int threads, const P &prm,
+                         cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, prm);
+}
+
+}  // namespace
+}  // namespace pkv
+
+extern "C" pkv_status pkv_kv_store_fp8(const void *k, int64_t k_tok_stride, const void *v,
+                                       int64_t v_tok_stride, const int32_t *cu_seqlens,
+                                       const int32_t *context_lens, const int32_t *block_tables,
+                                       int32_t block_table_width, int32_t num_seqs,
+                                       int64_t num_tokens, void *k_cache, void *v_cache,
+                                       float *k_scale, float *v_scale, int32_t num_kv_heads,
+                                       int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                                       void *stream) {
+  using namespace pkv;
+  if (num_seqs < 0 || num_tokens < 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 ||
+      num_blocks <= 0 || block_table_width <= 0)
+    return PKV_ERR_INVALID_ARG;
+  const int64_t row = (int64_t)num_kv_heads * head_dim;
+  if (k_tok_stride < row || v_tok_stride < row) return PKV_ERR_INVALID_ARG;
+  if (!cu_seqlens && num_tokens != num_seqs) return PKV_ERR_INVALID_ARG;
+  if (num_seqs == 0 || num_tokens == 0) return PKV_OK;
+  if (!k || !v || !context_lens || !block_tables || !k_cache || !v_cache || !k_scale || !v_scale)
+    return PKV_ERR_INVALID_ARG;
+  if (head_dim != kD || block_size % 256 != 0 || num_tokens > INT32_MAX)
+    return PKV_ERR_UNSUPPORTED;
+  if (k_tok_stride % 8 != 0 || v_tok_stride % 8 != 0 || !aligned16(k) || !aligned16(v) ||
+      !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scale) || !aligned16(v_scale))
+    return PKV_ERR_UNSUPPORTED;
+  unsigned int *err = current_error_word();
+  if (!err) return PKV_ERR_CUDA;
+  StoreParams prm{};
+  prm.k = static_cast<const uint8_t *>(k);
+  prm.v = static_cast<const uint8_t *>(v);
+  prm.k_stride = k_tok_stride * 2;
+  prm.v_stride = v_tok_stride * 2;
+  prm.cu = cu_seqlens;
+  prm.context_lens = context_lens;
+  prm.block_tables = block_tables;
+  prm.table_width = block_table_width;
+  prm.num_seqs = num_seqs;
+  prm.num_tokens = num_tokens;
+  prm.k_cache = static_cast<uint8_t *>(k_cache);
+  prm.v_cache = static_cast<uint8_t *>(v_cache);
+  prm.k_scale = k_scale;
+  prm.v_scale = v_scale;
+  prm.hkv = num_kv_heads;
+  prm.block_size = block_size;
+  prm.num_blocks = num_blocks;
+  prm.err = err;
+  const int64_t units =
+      (cu_seqlens ? num_tokens / kFp8Group + 2 * (int64_t)num_seqs : (int64_t)num_seqs) *
+      num_kv_heads;
+  const int64_t grid = cu_seqlens ? units : (units + kTokenWarps - 1) / kTokenWarps;
+  if (grid > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+  const cudaError_t e =
+      cu_seqlens ? launch_after(kv_store_fp8_run_kernel, grid, kRunThreads, prm,
+                                static_cast<cudaStream_t>(stream))
+                 : launch_after(kv_store_fp8_token_kernel, grid, kTokenWarps * 32, prm,
+                                static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+extern "C" pkv_status pkv_kv_gather_fp8(const void *k_cache, const void *v_cache,
+                                        const float *k_scale, const float *v_scale,
+                                        const int32_t *block_table, int32_t block_table_width,
+                                        const int32_t *cu_seqlens_k, int32_t num_seqs,
+                                        int64_t total_k, void *k_out, void *v_out,
+                                        int32_t num_kv_heads, int32_t head_dim,
+                                        int32_t block_size, int64_t num_blocks, void *stream) {
+  using namespace pkv;
+  if (num_seqs < 0 || total_k < 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 ||
+      num_blocks <= 0 || block_table_width <= 0)
+    return PKV_ERR_INVALID_ARG;
+  if (num_seqs == 0 || total_k == 0) return PKV_OK;
+  if (!k_cache || !v_cache || !k_scale || !v_scale || !block_table || !cu_seqlens_k || !k_out ||
+      !v_out)
+    return PKV_ERR_INVALID_ARG;
+  if (head_dim != kD || block_size % 256 != 0 || total_k > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+  if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scale) || !aligned16(v_scale) ||
+      !aligned16(k_out) || !aligned16(v_out))
+    return PKV_ERR_UNSUPPORTED;
+  unsigned int *err = current_error_word();
+  if (!err) return PKV_ERR_CUDA;
+  GatherParams prm{};
+  prm.k_cache = static_cast<const uint8_t *>(k_cache);
+  prm.v_cache = static_cast<const uint8_t *>(v_cache);
+  prm.k_scale = k_scale;
+  prm.v_scale = v_scale;
+  prm.block_table = block_table;
+  prm.table_width = block_table_width;
+  prm.cu = cu_seqlens_k;
+  prm.num_seqs = num_seqs;
+  prm.total = total_k;
+  prm.k_out = static_cast<uint8_t *>(k_out);
+  prm.v_out = static_cast<uint8_t *>(v_out);
+  prm.hkv = num_kv_heads;
+  prm.block_size = block_size;
+  prm.num_blocks = num_blocks;
+  prm.err = err;
+  const int64_t grid = (total_k / kFp8Group + 2 * (int64_t)num_seqs) * num_kv_heads;
+  if (grid > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+  return launch_after(kv_gather_fp8_kernel, grid, kRunThreads, prm,
+                      static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PKV_OK
+             : PKV_ERR_CUDA;
+}
