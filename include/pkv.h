@@ -399,6 +399,64 @@ pkv_status pkv_kv_gather_fp8(const void *k_cache, const void *v_cache, const flo
                              int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
                              int64_t num_blocks, void *stream);
 
+/*
+ * paged_decode_attn_fp8 -- pkv_paged_decode_attn over the 8-bit cache: key and value i of
+ * sequence b and head h are code * scale of position i. q and out stay bf16; products and sums
+ * are exact to fp32, the softmax weights enter the value sum rounded to fp16.
+ *
+ * k_cache, v_cache: [num_blocks, block_size, num_kv_heads, head_dim] e4m3.
+ * k_scale, v_scale: [num_blocks, num_kv_heads, block_size / 64] fp32, positive and finite, at
+ *                least 2^-100 (pkv_kv_store_fp8 writes powers of two from 2^-90).
+ * weights_out:   NULL, or the attention weights too: see pkv_paged_decode_attn_weights.
+ * workspace:     pkv_decode_fp8_workspace_bytes(..., weights = weights_out != NULL) bytes, with
+ *                the contract of pkv_paged_decode_attn's (its first word zeroed once).
+ * Everything else as for pkv_paged_decode_attn.
+ */
+size_t pkv_decode_fp8_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                      int32_t head_dim, int32_t max_context_len,
+                                      int32_t num_splits, int32_t weights);
+pkv_status pkv_paged_decode_attn_fp8(
+    const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+    const float *v_scale, const int32_t *block_tables, int32_t block_table_width,
+    const int32_t *context_lens, int32_t batch, int32_t max_context_len, int32_t num_q_heads,
+    int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int64_t num_blocks, float scale,
+    int32_t num_splits, const float *weights_in, int64_t weights_in_stride, float *weights_out,
+    int64_t weights_out_stride, void *workspace, size_t workspace_bytes, void *out,
+    void *stream);
+
+/* ------------------------------------------------------------------ attention weights and eviction
+ *
+ * paged_decode_attn_weights -- pkv_paged_decode_attn that also gives every cached token's
+ * attention weight, summed over the query heads of its KV head:
+ *
+ *     weights_out[b, h, i] = weights_in[b, h, i] + sum over the query heads hq of h of
+ *                            softmax_j(scale * q[b, hq] . k_j)_i          for 0 <= i < L
+ *
+ * in fp32 (the weights are not rounded to bf16 on the way). Entries i >= L are neither read nor
+ * written. Accumulated over the steps of a conversation (start a sequence's row at zero) they
+ * tell pkv_kv_evict which tokens the model looks at.
+ *
+ * weights_in:    [batch, num_kv_heads, *] fp32, row (b, h) weights_in_stride elements after the
+ *                one before (>= max_context_len); NULL: nothing is added.
+ * weights_out:   likewise; the same pointer and stride as weights_in accumulate in place, any
+ *                other overlap of the two is not allowed.
+ * workspace:     pkv_decode_weights_workspace_bytes(...) bytes (the scores of every query head
+ *                and token lie there between the kernels), with the contract of
+ *                pkv_paged_decode_attn's.
+ * Everything else as for pkv_paged_decode_attn.
+ */
+size_t pkv_decode_weights_workspace_bytes(int32_t batch, int32_t num_q_heads,
+                                          int32_t num_kv_heads, int32_t head_dim,
+                                          int32_t max_context_len, int32_t num_splits);
+pkv_status pkv_paged_decode_attn_weights(
+    const void *q, const void *k_cache, const void *v_cache, const int32_t *block_tables,
+    int32_t block_table_width, const int32_t *context_lens, int32_t batch,
+    int32_t max_context_len, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+    int32_t block_size, int64_t num_blocks, float scale, int32_t num_splits,
+    const float *weights_in, int64_t weights_in_stride, float *weights_out,
+    int64_t weights_out_stride, void *workspace, size_t workspace_bytes, void *out,
+    void *stream);
+
 /* ------------------------------------------------------------------ block manager (host)
  *
  * The owner of the pool's blocks on the host: «nano-vLLM 最小化vLLM重新实现», 架构 3 (块管理器)

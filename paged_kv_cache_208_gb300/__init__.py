@@ -51,6 +51,14 @@ SIGNATURES = {
                                 _I32, _I32, _I32, _I64, _P]),
     "pkv_kv_gather_fp8": (_I32, [_P, _P, _P, _P, _P, _I32, _P, _I32, _I64, _P, _P, _I32, _I32,
                                  _I32, _I64, _P]),
+    "pkv_decode_fp8_workspace_bytes": (_SZ, [_I32] * 7),
+    "pkv_paged_decode_attn_fp8": (_I32, [_P, _P, _P, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32,
+                                         _I32, _I32, _I64, _F, _I32, _P, _I64, _P, _I64, _P, _SZ,
+                                         _P, _P]),
+    "pkv_decode_weights_workspace_bytes": (_SZ, [_I32] * 6),
+    "pkv_paged_decode_attn_weights": (_I32, [_P, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32,
+                                             _I32, _I32, _I64, _F, _I32, _P, _I64, _P, _I64, _P,
+                                             _SZ, _P, _P]),
     "pkv_bm_create": (_P, [_I32, _I32]),
     "pkv_bm_destroy": (None, [_P]),
     "pkv_bm_num_free": (_I32, [_P]),
@@ -360,6 +368,8 @@ def _need_fp8_cache(k_cache, v_cache, k_scale, v_scale):
         raise ValueError(f"scales must be [NB, Hkv, bs / {FP8_GROUP}] = {list(want)}")
     if not all(t.is_contiguous() for t in (k_cache, v_cache, k_scale, v_scale)):
         raise ValueError("caches and scales must be contiguous")
+    for t, n in ((v_cache, "v_cache"), (k_scale, "k_scale"), (v_scale, "v_scale")):
+        _same_device(t, n, k_cache.device)
     return nb, bs, hkv, d
 
 
@@ -444,6 +454,156 @@ def kv_gather_fp8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.T
             block_table.shape[1], _ptr(cu_seqlens_k), N, int(total_k), _ptr(outs[0]),
             _ptr(outs[1]), hkv, d, bs, nb, _stream(stream)))
     return outs[0], outs[1]
+
+
+def _zeroed_workspace(nbytes: int, device, stream) -> torch.Tensor:
+    """A decode workspace whose work counter (its first word) is zero, on `stream`."""
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+        ws[:16].zero_()
+    return ws
+
+
+def decode_fp8_workspace(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                         max_context_len: int, num_splits: int = 0, weights: bool = False,
+                         device="cuda", stream=None) -> torch.Tensor:
+    """A workspace for paged_decode_attn_fp8 (with weights=True also for its weights_out), ready
+    for use on `stream` (the current stream when None)."""
+    device = torch.device(device)
+    with _on(device):
+        n = int(_LIB.pkv_decode_fp8_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim,
+                                                    max_context_len, num_splits, int(weights)))
+        return _zeroed_workspace(n, device, stream)
+
+
+def decode_weights_workspace(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                             max_context_len: int, num_splits: int = 0, device="cuda",
+                             stream=None) -> torch.Tensor:
+    """A workspace for paged_decode_attn_weights, ready for use on `stream` (the current stream
+    when None)."""
+    device = torch.device(device)
+    with _on(device):
+        n = int(_LIB.pkv_decode_weights_workspace_bytes(
+            batch, num_q_heads, num_kv_heads, head_dim, max_context_len, num_splits))
+        return _zeroed_workspace(n, device, stream)
+
+
+def _need_decode(q, k_cache, block_tables, context_lens, out):
+    """Checks what every decode call takes; returns (batch, num_q_heads, out)."""
+    _need(q, "q", torch.bfloat16)
+    dev = k_cache.device
+    _same_device(q, "q", dev)
+    if q.dim() != 3 or q.shape[2] != k_cache.shape[3] or not q.is_contiguous():
+        raise ValueError(f"q must be a contiguous [B, Hq, {k_cache.shape[3]}] tensor")
+    B, hq, _ = q.shape
+    _need_list(block_tables, "block_tables", (B, None), dev)
+    _need_list(context_lens, "context_lens", (B,), dev)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _need(out, "out", torch.bfloat16)
+        _same_device(out, "out", dev)
+        if out.shape != q.shape or not out.is_contiguous():
+            raise ValueError("out must be a contiguous tensor of q's shape")
+    return B, hq, out
+
+
+def _need_weights(t, name, batch, hkv, max_context_len, device):
+    """A [B, Hkv, S] float32 tensor of dense rows that lie one stride apart; returns it."""
+    _need(t, name, torch.float32)
+    _same_device(t, name, device)
+    if (t.dim() != 3 or t.shape[:2] != (batch, hkv) or t.shape[2] < max_context_len
+            or (t.shape[2] > 1 and t.stride(2) != 1)
+            or (batch > 1 and t.stride(0) != hkv * t.stride(1))):
+        raise ValueError(f"{name} must be [{batch}, {hkv}, >= {max_context_len}] with dense, "
+                         "evenly spaced rows")
+    return t.stride(1) if hkv > 1 else t.stride(0) if batch > 1 else t.shape[2]
+
+
+def _weights_args(weights, weights_out, batch, hkv, max_context_len, device):
+    """(in pointer, in stride, out pointer, out stride); without weights_out in place."""
+    if weights is None and weights_out is None:
+        return None, 0, None, 0
+    if weights_out is None:
+        weights_out = weights
+    in_stride = 0
+    if weights is not None:
+        in_stride = _need_weights(weights, "weights", batch, hkv, max_context_len, device)
+    out_stride = _need_weights(weights_out, "weights_out", batch, hkv, max_context_len, device)
+    if (weights is not None and weights_out.data_ptr() == weights.data_ptr()
+            and in_stride != out_stride):
+        raise ValueError("weights and weights_out overlap with different strides")
+    return _ptr(weights), in_stride, _ptr(weights_out), out_stride
+
+
+def paged_decode_attn_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                          k_scale: torch.Tensor, v_scale: torch.Tensor,
+                          block_tables: torch.Tensor, context_lens: torch.Tensor,
+                          max_context_len: int, scale: float, num_splits: int = 0,
+                          weights: torch.Tensor | None = None,
+                          weights_out: torch.Tensor | None = None,
+                          workspace: torch.Tensor | None = None,
+                          out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """paged_decode_attn over an 8-bit cache. q: [B, Hq, D] bf16; caches [NB, bs, Hkv, D]
+    float8_e4m3fn with scales [NB, Hkv, bs / 64] float32 (see kv_store_fp8). With weights and / or
+    weights_out the attention weights too, as paged_decode_attn_weights gives them."""
+    nb, bs, hkv, d = _need_fp8_cache(k_cache, v_cache, k_scale, v_scale)
+    dev = k_cache.device
+    B, hq, out = _need_decode(q, k_cache, block_tables, context_lens, out)
+    w = _weights_args(weights, weights_out, B, hkv, int(max_context_len), dev)
+    with _on(dev):
+        if workspace is None:
+            workspace = decode_fp8_workspace(B, hq, hkv, d, int(max_context_len), num_splits,
+                                             w[2] is not None, dev, stream)
+        _check("pkv_paged_decode_attn_fp8", _LIB.pkv_paged_decode_attn_fp8(
+            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+            _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), B,
+            int(max_context_len), hq, hkv, d, bs, nb, float(scale), int(num_splits), *w,
+            _ptr(workspace), _ws_bytes(workspace, dev), _ptr(out), _stream(stream)))
+    return out
+
+
+def paged_decode_attn_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                              block_tables: torch.Tensor, context_lens: torch.Tensor,
+                              max_context_len: int, scale: float,
+                              weights: torch.Tensor | None = None, num_splits: int = 0,
+                              weights_out: torch.Tensor | None = None,
+                              workspace: torch.Tensor | None = None,
+                              out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """paged_decode_attn that also adds each cached token's attention weight, summed over the
+    query heads of its KV head, to `weights` [B, Hkv, >= max_context_len] float32: in place, or
+    into weights_out (without weights: weights_out receives this step's alone)."""
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _need(t, n, torch.bfloat16)
+    if (k_cache.dim() != 4 or k_cache.shape != v_cache.shape
+            or not (k_cache.is_contiguous() and v_cache.is_contiguous())):
+        raise ValueError("caches must be contiguous [NB, bs, Hkv, D], the same for K and V")
+    nb, bs, hkv, d = k_cache.shape
+    dev = k_cache.device
+    _same_device(v_cache, "v_cache", dev)
+    B, hq, out = _need_decode(q, k_cache, block_tables, context_lens, out)
+    if weights is None and weights_out is None:
+        raise ValueError("weights or weights_out must be given")
+    w = _weights_args(weights, weights_out, B, hkv, int(max_context_len), dev)
+    with _on(dev):
+        if workspace is None:
+            workspace = decode_weights_workspace(B, hq, hkv, d, int(max_context_len), num_splits,
+                                                 dev, stream)
+        _check("pkv_paged_decode_attn_weights", _LIB.pkv_paged_decode_attn_weights(
+            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), block_tables.shape[1],
+            _ptr(context_lens), B, int(max_context_len), hq, hkv, d, bs, nb, float(scale),
+            int(num_splits), *w, _ptr(workspace), _ws_bytes(workspace, dev), _ptr(out),
+            _stream(stream)))
+    return out
+
+
+def _ws_bytes(workspace, device) -> int:
+    _same_device(workspace, "workspace", device)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.numel() * workspace.element_size()
 
 
 # ----------------------------------------------------------------------------- block manager

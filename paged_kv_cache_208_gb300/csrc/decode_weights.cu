@@ -1,0 +1,228 @@
+// decode_weights.cu -- the attention weights of a decode step, and the entry points of decode
+// attention over the 8-bit cache and of decode attention with weights.
+//
+// The split kernel has left every key's scaled score s (log2 domain) and every query head's
+// log2-sum-exp; the weight that KV head h's query heads give to position i is
+//
+//     w[b, h, i] = sum_g 2^(s[b, hG + g, i] - lse[b, hG + g]),     w_out = w_in + w
+//
+// Keeping the scores costs 4 bytes written and read per (query head, token) -- for two heads to
+// a KV head 3% of the K and V bytes of a bf16 cache, 6% of an 8-bit one -- where a second pass
+// over K would cost a half; up to 126 MB of them stay in L2. The sum over g runs in a fixed
+// order and every weight has one writer.
+#include <math.h>
+
+#include <algorithm>
+
+#include "device_common.cuh"
+#include "launch.h"
+#include "pkv.h"
+
+namespace pkv {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPerThread = 4;
+constexpr int kSpan = kThreads * kPerThread;  // positions of a CTA
+
+struct WeightsParams {
+  const float *scores;
+  int64_t score_stride;
+  const float *lse;
+  const int32_t *context_lens;
+  int64_t cap;  // longest context the decode call took
+  const float *in;
+  int64_t in_stride;
+  float *out;
+  int64_t out_stride;
+  int32_t hkv, group;
+  const unsigned int *err;
+};
+
+__global__ void __launch_bounds__(kThreads) decode_weights_kernel(const WeightsParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (aborted(p.err)) return;  // an earlier wait gave up: the scores are not complete
+  const int64_t bh = blockIdx.x;
+  const int64_t b = bh / p.hkv;
+  int64_t L = p.context_lens[b];
+  L = L < 0 ? 0 : min(L, p.cap);
+  for (int64_t i0 = (int64_t)blockIdx.y * kSpan + threadIdx.x; i0 < L;
+       i0 += (int64_t)gridDim.y * kSpan) {
+    float w[kPerThread] = {};
+    const float *s = p.scores + bh * p.group * p.score_stride;
+    for (int g = 0; g < p.group; ++g, s += p.score_stride) {
+      const float lse = p.lse[bh * p.group + g];
+#pragma unroll
+      for (int j = 0; j < kPerThread; ++j) {
+        const int64_t i = i0 + j * kThreads;
+        if (i < L) w[j] += fast_exp2(s[i] - lse);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j) {
+      const int64_t i = i0 + j * kThreads;
+      if (i < L) p.out[bh * p.out_stride + i] = (p.in ? p.in[bh * p.in_stride + i] : 0.f) + w[j];
+    }
+  }
+}
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+struct Call {
+  DecodeArgs a;
+  int32_t max_context_len, head_dim, num_splits;
+  size_t workspace_bytes;
+  bool fp8;
+  bool weights;
+  const float *weights_in;
+  int64_t weights_in_stride;
+  float *weights_out;
+  int64_t weights_out_stride;
+};
+
+pkv_status decode_with_weights(Call c, cudaStream_t stream) {
+  DecodeArgs &a = c.a;
+  if (a.batch < 0 || c.max_context_len < 0 || c.num_splits < 0 || a.num_q_heads <= 0 ||
+      a.num_kv_heads <= 0 || a.num_q_heads % a.num_kv_heads != 0 || c.head_dim <= 0 ||
+      a.block_size <= 0 || a.num_blocks <= 0 || a.table_width <= 0 || !isfinite(a.scale))
+    return PKV_ERR_INVALID_ARG;
+  if (c.weights && (c.weights_out_stride < c.max_context_len ||
+                    (c.weights_in && c.weights_in_stride < c.max_context_len)))
+    return PKV_ERR_INVALID_ARG;
+  if (a.batch == 0) return PKV_OK;
+  if (!a.q || !a.k_cache || !a.v_cache || !a.block_tables || !a.context_lens || !a.out ||
+      (c.fp8 && (!a.k_scale || !a.v_scale)) || (c.weights && !c.weights_out))
+    return PKV_ERR_INVALID_ARG;
+  if (c.head_dim != 128 || a.block_size % 256 != 0) return PKV_ERR_UNSUPPORTED;
+  if (a.num_blocks * (int64_t)a.block_size > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+  if (!aligned16(a.q) || !aligned16(a.k_cache) || !aligned16(a.v_cache) || !aligned16(a.out) ||
+      (c.fp8 && (!aligned16(a.k_scale) || !aligned16(a.v_scale))))
+    return PKV_ERR_UNSUPPORTED;
+  const int64_t rows = (int64_t)a.batch * a.num_kv_heads;
+  if (c.weights && rows > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+  a.num_sms = current_sm_count();
+  a.err = current_error_word();
+  if (a.num_sms <= 0 || !a.err) return PKV_ERR_CUDA;
+  const DecodePlan plan = plan_decode(a.batch, a.num_q_heads, a.num_kv_heads, c.max_context_len,
+                                      c.num_splits, a.num_sms, c.fp8, c.weights);
+  if (!a.workspace || c.workspace_bytes < plan.workspace_bytes || !aligned16(a.workspace))
+    return PKV_ERR_WORKSPACE;
+  cudaError_t e = c.fp8 ? launch_paged_decode_fp8(a, plan, stream)
+                        : launch_paged_decode(a, plan, stream);
+  if (e != cudaSuccess || !c.weights || c.max_context_len == 0)
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  uint8_t *ws = static_cast<uint8_t *>(a.workspace);
+  WeightsParams w{};
+  w.scores = reinterpret_cast<const float *>(ws + plan.scores_at);
+  w.score_stride = plan.score_stride;
+  w.lse = reinterpret_cast<const float *>(ws + plan.lse_at);
+  w.context_lens = a.context_lens;
+  // what the decode kernels clamp a context to, and no more than the rows of weights hold
+  w.cap = std::min({(int64_t)a.table_width * a.block_size, (int64_t)plan.splits * plan.chunk,
+                    (int64_t)c.max_context_len});
+  w.in = c.weights_in;
+  w.in_stride = c.weights_in_stride;
+  w.out = c.weights_out;
+  w.out_stride = c.weights_out_stride;
+  w.hkv = a.num_kv_heads;
+  w.group = a.num_q_heads / a.num_kv_heads;
+  w.err = a.err;
+  cudaLaunchConfig_t cfg{};
+  const int64_t spans = ((int64_t)c.max_context_len + kSpan - 1) / kSpan;
+  cfg.gridDim = dim3((unsigned)rows, (unsigned)std::min<int64_t>(spans, 65535));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, decode_weights_kernel, w);
+  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+size_t workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                       int32_t head_dim, int32_t max_context_len, int32_t num_splits, bool fp8,
+                       bool weights) {
+  if (batch <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
+      head_dim != 128 || max_context_len < 0 || num_splits < 0)
+    return 0;
+  const int num_sms = current_sm_count();
+  if (num_sms <= 0) return 0;
+  return plan_decode(batch, num_q_heads, num_kv_heads, max_context_len, num_splits, num_sms, fp8,
+                     weights)
+      .workspace_bytes;
+}
+
+}  // namespace
+}  // namespace pkv
+
+extern "C" size_t pkv_decode_weights_workspace_bytes(int32_t batch, int32_t num_q_heads,
+                                                     int32_t num_kv_heads, int32_t head_dim,
+                                                     int32_t max_context_len,
+                                                     int32_t num_splits) {
+  return pkv::workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim, max_context_len,
+                              num_splits, false, true);
+}
+
+extern "C" size_t pkv_decode_fp8_workspace_bytes(int32_t batch, int32_t num_q_heads,
+                                                 int32_t num_kv_heads, int32_t head_dim,
+                                                 int32_t max_context_len, int32_t num_splits,
+                                                 int32_t weights) {
+  return pkv::workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim, max_context_len,
+                              num_splits, true, weights != 0);
+}
+
+extern "C" pkv_status pkv_paged_decode_attn_weights(
+    const void *q, const void *k_cache, const void *v_cache, const int32_t *block_tables,
+    int32_t block_table_width, const int32_t *context_lens, int32_t batch,
+    int32_t max_context_len, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+    int32_t block_size, int64_t num_blocks, float scale, int32_t num_splits,
+    const float *weights_in, int64_t weights_in_stride, float *weights_out,
+    int64_t weights_out_stride, void *workspace, size_t workspace_bytes, void *out,
+    void *stream) {
+  pkv::Call c{};
+  c.a = pkv::DecodeArgs{q,          k_cache,      v_cache,     block_tables, block_table_width,
+                        context_lens, batch,      num_q_heads, num_kv_heads, block_size,
+                        num_blocks, scale,        workspace,   out,          nullptr,
+                        0};
+  c.max_context_len = max_context_len;
+  c.head_dim = head_dim;
+  c.num_splits = num_splits;
+  c.workspace_bytes = workspace_bytes;
+  c.weights = true;
+  c.weights_in = weights_in;
+  c.weights_in_stride = weights_in_stride;
+  c.weights_out = weights_out;
+  c.weights_out_stride = weights_out_stride;
+  return pkv::decode_with_weights(c, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" pkv_status pkv_paged_decode_attn_fp8(
+    const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+    const float *v_scale, const int32_t *block_tables, int32_t block_table_width,
+    const int32_t *context_lens, int32_t batch, int32_t max_context_len, int32_t num_q_heads,
+    int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int64_t num_blocks, float scale,
+    int32_t num_splits, const float *weights_in, int64_t weights_in_stride, float *weights_out,
+    int64_t weights_out_stride, void *workspace, size_t workspace_bytes, void *out,
+    void *stream) {
+  pkv::Call c{};
+  c.a = pkv::DecodeArgs{q,          k_cache,      v_cache,     block_tables, block_table_width,
+                        context_lens, batch,      num_q_heads, num_kv_heads, block_size,
+                        num_blocks, scale,        workspace,   out,          nullptr,
+                        0};
+  c.a.k_scale = k_scale;
+  c.a.v_scale = v_scale;
+  c.max_context_len = max_context_len;
+  c.head_dim = head_dim;
+  c.num_splits = num_splits;
+  c.workspace_bytes = workspace_bytes;
+  c.fp8 = true;
+  c.weights = weights_out != nullptr;
+  c.weights_in = weights_in;
+  c.weights_in_stride = weights_in_stride;
+  c.weights_out = weights_out;
+  c.weights_out_stride = weights_out_stride;
+  return pkv::decode_with_weights(c, static_cast<cudaStream_t>(stream));
+}

@@ -11,22 +11,30 @@
 
 namespace pkv {
 
+inline size_t align16(size_t x) { return (x + 15) & ~size_t(15); }
+
 // kv_store.cu
 cudaError_t launch_kv_store(const void *k, int64_t k_tok_stride, const void *v,
                             int64_t v_tok_stride, const int64_t *slot_mapping, int64_t num_tokens,
                             void *k_cache, void *v_cache, int64_t num_slots, int64_t row_elems,
                             unsigned int *err, int num_sms, cudaStream_t stream);
 
-// decode.cu
+// decode.cu (the kernel template: decode_kernel.cuh)
 struct DecodePlan {
   int32_t chunk;       // logical tokens per split (multiple of 64)
   int32_t splits;      // splits of the longest context
   int32_t head_groups; // CTAs per KV head (query heads handled two at a time)
   int32_t heads_per_cta;
   size_t workspace_bytes;
+  // with weights: where the log2-sum-exps and the scores [batch, num_q_heads, score_stride]
+  // lie in the workspace (0: no weights)
+  size_t lse_at;
+  size_t scores_at;
+  int64_t score_stride;
 };
 DecodePlan plan_decode(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
-                       int32_t max_context_len, int32_t num_splits, int num_sms);
+                       int32_t max_context_len, int32_t num_splits, int num_sms,
+                       bool fp8 = false, bool weights = false);
 
 struct DecodeArgs {
   const void *q;
@@ -53,10 +61,17 @@ struct DecodeArgs {
   int64_t v_new_stride = 0;
   const int64_t *slot_mapping = nullptr;
   int64_t num_slots = 0;
+  // 8-bit cache: [num_blocks, num_kv_heads, block_size / 64]
+  const float *k_scale = nullptr;
+  const float *v_scale = nullptr;
 };
 constexpr size_t kDecodeQueueBytes = 16;  // the workspace's header: the work counters
 cudaError_t launch_paged_decode(const DecodeArgs &a, const DecodePlan &plan,
                                 cudaStream_t stream);
+
+// decode_fp8.cu
+cudaError_t launch_paged_decode_fp8(const DecodeArgs &a, const DecodePlan &plan,
+                                    cudaStream_t stream);
 
 // prefill.cu
 struct PrefillArgs {
@@ -94,7 +109,6 @@ struct PrefillWorkspace {
   int64_t max_units;
   int32_t levels;  // ceil(max_seqlen_q / 128): the query blocks of the longest sequence
 };
-inline size_t align16(size_t x) { return (x + 15) & ~size_t(15); }
 inline PrefillWorkspace prefill_workspace_layout(int32_t num_seqs, int32_t max_seqlen_q) {
   PrefillWorkspace w{};
   w.levels = (int32_t)(((int64_t)max_seqlen_q + 127) / 128);
