@@ -457,6 +457,54 @@ pkv_status pkv_paged_decode_attn_weights(
     int64_t weights_out_stride, void *workspace, size_t workspace_bytes, void *out,
     void *stream);
 
+/*
+ * kv_evict -- cut long sequences down to `budget` tokens per KV head, by accumulated attention
+ * weight. For every sequence b with L = context_lens[b] and every KV head h:
+ *   L <= budget: every position is kept.
+ *   L > budget:  the last `recent` positions are kept, and of the others the budget - recent
+ *                with the largest weights[b, h, i] (equal weights: the lower position; NaN is
+ *                smaller than every number, -0 equals +0).
+ * With the kept positions in ascending order i_0 < i_1 < .. < i_(n-1), n = min(L, budget):
+ *   row j of the sequence in the blocks of dst_block_tables (position j, head h, K and V) becomes
+ *   row i_j; kept[b, h, j] = i_j; weights_out[b, h, j] = weights[b, h, i_j]; and
+ *   new_context_lens[b] = n.
+ * Entries j in [n, budget) of kept become -1 and of weights_out 0; pool rows past n are left as
+ * they are. Each head keeps tokens of its own, so afterwards position j of two heads may be
+ * different tokens: the cached keys carry their rotary positions with them, and new tokens go on
+ * counting positions from the original length, while context lengths, slots and block tables
+ * go by the new one. Attention over the compacted rows is attention over the kept tokens.
+ *
+ * The source blocks are only read (they may be shared, or registered for prefix reuse); the
+ * destination blocks must be others, belong to one sequence each and hold nothing needed:
+ * pkv_bm_take hands them out. Release the source table afterwards.
+ *
+ * weights:       [batch, num_kv_heads, *] fp32, rows weights_stride elements apart (>=
+ *                max_context_len). weights_out: NULL, or likewise (stride >= budget); not
+ *                overlapping weights.
+ * dst_block_tables: [batch, dst_block_table_width] int32, ceil(n / block_size) entries of a row
+ *                are used. It, new_context_lens and weights_out must not be block_tables,
+ *                context_lens and weights (PKV_ERR_INVALID_ARG).
+ * k_scale, v_scale: both NULL for bf16 pools; for an 8-bit cache its scales. There a destination
+ *                group takes the largest scale s of its rows' groups, a row of a group with scale
+ *                s0 becomes e4m3(code * s0 / s).
+ * kept:          [batch, num_kv_heads, budget] int32. new_context_lens: [batch] int32.
+ * 1 <= budget, 0 <= recent <= budget. A context length that is negative, above max_context_len
+ * or longer than its tables sets PKV_DEVERR_CONTEXT_RANGE, and the sequence becomes empty
+ * (new_context_lens 0, kept -1); a bad source block id gives zero rows, a bad destination
+ * block's rows are skipped (PKV_DEVERR_BLOCK_RANGE).
+ * Implemented: head_dim == 128, block_size a multiple of 64 (bf16) or 256 (8-bit), 16-byte
+ * aligned pools.
+ */
+pkv_status pkv_kv_evict(const float *weights, int64_t weights_stride,
+                        const int32_t *context_lens, int32_t batch, int32_t max_context_len,
+                        int32_t budget, int32_t recent, const int32_t *block_tables,
+                        int32_t block_table_width, const int32_t *dst_block_tables,
+                        int32_t dst_block_table_width, void *k_cache, void *v_cache,
+                        float *k_scale, float *v_scale, int32_t num_kv_heads, int32_t head_dim,
+                        int32_t block_size, int64_t num_blocks, int32_t *kept,
+                        float *weights_out, int64_t weights_out_stride,
+                        int32_t *new_context_lens, void *stream);
+
 /* ------------------------------------------------------------------ block manager (host)
  *
  * The owner of the pool's blocks on the host: «nano-vLLM 最小化vLLM重新实现», 架构 3 (块管理器)
@@ -497,6 +545,14 @@ pkv_status pkv_bm_block_hash(const pkv_block_manager *bm, int32_t block, uint64_
 pkv_status pkv_bm_allocate(pkv_block_manager *bm, const int32_t *token_ids, int32_t num_tokens,
                            int32_t *block_table, int32_t table_capacity,
                            int32_t *num_table_blocks, int32_t *num_cached_tokens);
+
+/* num_blocks fresh blocks with no tokens of their own, for contents that are not a prefix of
+ * token ids: the destination of pkv_kv_evict, and further blocks of a sequence that was evicted
+ * from (its positions no longer match its tokens, so its blocks must not be registered: use
+ * this instead of pkv_bm_may_append when its length reaches a multiple of the block size).
+ * Oldest free blocks first, reference count 1, never registered; release them with
+ * pkv_bm_deallocate. PKV_ERR_NO_BLOCKS, with nothing changed, when fewer are free. */
+pkv_status pkv_bm_take(pkv_block_manager *bm, int32_t num_blocks, int32_t *blocks);
 
 /* Release a finished or preempted sequence: each block's reference count drops by one (last
  * block first); blocks that reach zero go to the back of the free list. PKV_ERR_INVALID_ARG,

@@ -59,6 +59,9 @@ SIGNATURES = {
     "pkv_paged_decode_attn_weights": (_I32, [_P, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32,
                                              _I32, _I32, _I64, _F, _I32, _P, _I64, _P, _I64, _P,
                                              _SZ, _P, _P]),
+    "pkv_kv_evict": (_I32, [_P, _I64, _P, _I32, _I32, _I32, _I32, _P, _I32, _P, _I32, _P, _P, _P,
+                            _P, _I32, _I32, _I32, _I64, _P, _P, _I64, _P, _P]),
+    "pkv_bm_take": (_I32, [_P, _I32, _P]),
     "pkv_bm_create": (_P, [_I32, _I32]),
     "pkv_bm_destroy": (None, [_P]),
     "pkv_bm_num_free": (_I32, [_P]),
@@ -599,6 +602,62 @@ def paged_decode_attn_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: t
     return out
 
 
+def kv_evict(weights: torch.Tensor, context_lens: torch.Tensor, max_context_len: int,
+             block_tables: torch.Tensor, dst_block_tables: torch.Tensor, budget: int,
+             recent: int, k_cache: torch.Tensor, v_cache: torch.Tensor,
+             k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None,
+             kept: torch.Tensor | None = None, weights_out: torch.Tensor | None = None,
+             new_context_lens: torch.Tensor | None = None, stream=None):
+    """Keep `budget` tokens of every sequence and KV head: the `recent` last ones and the ones
+    with the largest weights [B, Hkv, >= max_context_len] float32 (as paged_decode_attn_weights
+    accumulates them), their K and V rows compacted in order into the blocks of dst_block_tables
+    [B, W'] int32 (other blocks than those of block_tables, e.g. from BlockManager.take).
+
+    caches: bf16 [NB, bs, Hkv, D], or float8_e4m3fn with k_scale and v_scale. Returns (kept
+    positions [B, Hkv, budget] int32 (-1 past a sequence's length), their weights
+    [B, Hkv, budget], the new context lengths [B] int32)."""
+    if k_scale is None and v_scale is None:
+        for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+            _need(t, n, torch.bfloat16)
+        if (k_cache.dim() != 4 or k_cache.shape != v_cache.shape
+                or not (k_cache.is_contiguous() and v_cache.is_contiguous())):
+            raise ValueError("caches must be contiguous [NB, bs, Hkv, D], the same for K and V")
+        nb, bs, hkv, d = k_cache.shape
+        _same_device(v_cache, "v_cache", k_cache.device)
+    elif k_scale is None or v_scale is None:
+        raise ValueError("k_scale and v_scale go together")
+    else:
+        nb, bs, hkv, d = _need_fp8_cache(k_cache, v_cache, k_scale, v_scale)
+    dev = k_cache.device
+    budget, recent, max_context_len = int(budget), int(recent), int(max_context_len)
+    _need_list(context_lens, "context_lens", (None,), dev)
+    B = context_lens.shape[0]
+    _need_list(block_tables, "block_tables", (B, None), dev)
+    _need_list(dst_block_tables, "dst_block_tables", (B, None), dev)
+    w_stride = _need_weights(weights, "weights", B, hkv, max_context_len, dev)
+    if budget < 1 or not 0 <= recent <= budget:
+        raise ValueError("budget must be at least 1 and recent between 0 and budget")
+    if kept is None:
+        kept = torch.empty((B, hkv, budget), dtype=torch.int32, device=dev)
+    else:
+        _need_list(kept, "kept", (B, hkv, budget), dev)
+    if weights_out is None:
+        weights_out = torch.empty((B, hkv, budget), dtype=torch.float32, device=dev)
+    o_stride = _need_weights(weights_out, "weights_out", B, hkv, budget, dev)
+    if new_context_lens is None:
+        new_context_lens = torch.empty_like(context_lens)
+    else:
+        _need_list(new_context_lens, "new_context_lens", (B,), dev)
+    with _on(dev):
+        _check("pkv_kv_evict", _LIB.pkv_kv_evict(
+            _ptr(weights), w_stride, _ptr(context_lens), B, max_context_len, budget, recent,
+            _ptr(block_tables), block_tables.shape[1], _ptr(dst_block_tables),
+            dst_block_tables.shape[1], _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+            _ptr(v_scale), hkv, d, bs, nb, _ptr(kept), _ptr(weights_out), o_stride,
+            _ptr(new_context_lens), _stream(stream)))
+    return kept, weights_out, new_context_lens
+
+
 def _ws_bytes(workspace, device) -> int:
     _same_device(workspace, "workspace", device)
     if not workspace.is_contiguous():
@@ -659,6 +718,13 @@ class BlockManager:
         _check("pkv_bm_allocate", _LIB.pkv_bm_allocate(self._h, toks, n, table, cap,
                                                        ctypes.byref(nb), ctypes.byref(cached)))
         return list(table[:nb.value]), int(cached.value)
+
+    def take(self, n: int):
+        """n fresh blocks that hold no tokens' prefix: the destination of kv_evict, or a further
+        block of a sequence that was evicted from. Release them with deallocate."""
+        blocks = (ctypes.c_int32 * max(1, int(n)))()
+        _check("pkv_bm_take", _LIB.pkv_bm_take(self._h, int(n), blocks))
+        return list(blocks[:int(n)])
 
     def deallocate(self, table) -> None:
         t, n = self._ints(table)

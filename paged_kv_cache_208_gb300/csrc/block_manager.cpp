@@ -250,6 +250,13 @@ pkv_status pkv_bm_allocate(pkv_block_manager *bm, const int32_t *token_ids, int3
   return PKV_OK;
 }
 
+pkv_status pkv_bm_take(pkv_block_manager *bm, int32_t num_blocks, int32_t *blocks) {
+  if (!bm || num_blocks < 0 || (num_blocks > 0 && !blocks)) return PKV_ERR_INVALID_ARG;
+  if ((int64_t)bm->free_list.size() < num_blocks) return PKV_ERR_NO_BLOCKS;
+  for (int32_t i = 0; i < num_blocks; ++i) blocks[i] = bm->take_free();
+  return PKV_OK;
+}
+
 pkv_status pkv_bm_deallocate(pkv_block_manager *bm, const int32_t *block_table,
                              int32_t num_table_blocks) {
   if (!bm || num_table_blocks < 0 || (num_table_blocks > 0 && !block_table))

@@ -467,6 +467,17 @@ __device__ __forceinline__ void record_error(unsigned int *err, unsigned int bit
   if (err) atomicOr(err, bit);
 }
 
+// 16 bytes that are read once, by a kernel that started before its predecessor ended (a plain
+// load, not one through the read-only path: the data may be the predecessor's).
+__device__ __forceinline__ uint4 ld_once_u4(const uint4 *p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
+
 __device__ __forceinline__ uint4 ld_stream_u4(const uint4 *p) {
   uint4 r;
   asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"

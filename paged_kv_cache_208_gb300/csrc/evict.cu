@@ -1,0 +1,376 @@
+// evict.cu -- eviction from the cache by accumulated attention weight (kv_evict).
+//
+// Of a sequence of L > budget tokens each KV head keeps `budget`: the `recent` last ones, and of
+// the earlier ones those with the largest weights (ties: the lower position; a NaN weight counts
+// as smaller than every number). Their rows are compacted, in order, into the blocks of a
+// second table: row kept[j] becomes row j. The source blocks are only read, so blocks shared
+// with other sequences, or registered in the prefix cache, keep their contents.
+//
+// Two kernels. evict_select_kernel, one CTA per (sequence, head): a radix select over the
+// weights' ordered bits (11 + 11 + 10, histograms in shared memory; the weights are read again
+// per pass, from L2) finds the smallest kept key and how many of its equals are kept, then one
+// ordered pass with block-wide prefix sums writes the kept positions and their weights.
+// evict_copy_kernel, one CTA per (sequence, 64 kept rows, head), moves the K and V rows; it is
+// bound by HBM: each kept row is read once and written once. In an 8-bit cache the 64 rows are
+// one group of the destination, whose scale is the largest of its rows' scales (powers of two:
+// rows of a smaller one lose only what falls below e4m3's normal range).
+#include <algorithm>
+
+#include "device_common.cuh"
+#include "fp8_cache.cuh"
+#include "launch.h"
+#include "pkv.h"
+
+namespace pkv {
+namespace {
+
+constexpr int kD = 128;
+constexpr unsigned kFull = 0xffffffffu;
+constexpr unsigned int kErrBlock = 2u, kErrContext = 4u;  // PKV_DEVERR_*
+constexpr int kGroup = kFp8Group;
+
+struct EvictParams {
+  const float *weights;
+  int64_t weights_stride;
+  const int32_t *context_lens;
+  int32_t batch, max_context_len, budget, recent;
+  const int32_t *src_tables, *dst_tables;
+  int32_t src_width, dst_width;
+  uint8_t *k_cache, *v_cache;
+  float *k_scale, *v_scale;
+  int32_t hkv, block_size;
+  int64_t num_blocks;
+  int32_t *kept;
+  float *weights_out;
+  int64_t weights_out_stride;
+  int32_t *new_lens;
+  unsigned int *err;
+};
+
+// Bits that order like the numbers (NaN first, -0 equal to +0).
+__device__ __forceinline__ uint32_t ordered(float x) {
+  if (x != x) return 0u;
+  const uint32_t b = __float_as_uint(x + 0.f);
+  return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
+}
+
+constexpr int kSelThreads = 1024;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kPer = 4;  // elements of a thread in the ordered pass
+
+// Inclusive sum over the warp's lanes up to this one.
+__device__ __forceinline__ uint32_t warp_scan(uint32_t x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(kFull, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+// Exclusive sum over the CTA's threads up to this one, and the total. `sums` (kSelWarps words)
+// may be used again after the next __syncthreads.
+__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t *sums, uint32_t &total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t inc = warp_scan(x, lane);
+  if (lane == 31) sums[warp] = inc;
+  __syncthreads();
+  const uint32_t w = warp_scan(lane < kSelWarps ? sums[lane] : 0u, lane);
+  total = __shfl_sync(kFull, w, kSelWarps - 1);
+  const uint32_t before = __shfl_sync(kFull, w, max(warp - 1, 0));
+  return inc - x + (warp ? before : 0u);
+}
+
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ uint32_t hist[kBins];
+  __shared__ uint32_t sums[2][kSelWarps];
+  __shared__ uint32_t found_bin, found_above;
+  if (__syncthreads_or(threadIdx.x == 0 && aborted(p.err))) return;
+  const int64_t bh = blockIdx.x;
+  const int b = (int)(bh / p.hkv), h = (int)(bh % p.hkv);
+  const int32_t L = *(p.context_lens + b);
+  const bool bad = L < 0 || L > p.max_context_len ||
+                   (int64_t)L > (int64_t)p.src_width * p.block_size ||
+                   (int64_t)min(L, p.budget) > (int64_t)p.dst_width * p.block_size;
+  const int32_t n = bad ? 0 : min(L, p.budget);
+  if (threadIdx.x == 0 && h == 0) {
+    p.new_lens[b] = n;
+    if (bad) record_error(p.err, kErrContext);
+  }
+  const float *w = p.weights + bh * p.weights_stride;
+  int32_t *kept = p.kept + bh * p.budget;
+  float *w_out = p.weights_out ? p.weights_out + bh * p.weights_out_stride : nullptr;
+
+  // the smallest key that is kept among the positions below `older`, and how many of its equals
+  // (with L <= budget every position is kept)
+  const int32_t older = L > p.budget ? L - p.recent : 0;
+  uint32_t threshold = 0u, equals = 0u;
+  if (!bad && older > 0) {
+    uint32_t want = (uint32_t)(p.budget - p.recent);  // of the keys that share `prefix`
+    uint32_t prefix = 0u, mask = 0u;
+    if (want == 0) {
+      threshold = 0xffffffffu;  // (no number has this key: nothing older is kept)
+    } else {
+      for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+        const uint32_t digit = pass == 2 ? 1023u : 2047u;
+        for (int i = threadIdx.x; i < kBins; i += kSelThreads) hist[i] = 0u;
+        __syncthreads();
+        for (int64_t i = threadIdx.x; i < older; i += kSelThreads) {
+          const uint32_t key = ordered(w[i]);
+          if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & digit], 1u);
+        }
+        __syncthreads();
+        // thread t owns bins 2t, 2t + 1 counted from the top
+        const int hi = kBins - 1 - 2 * threadIdx.x;
+        const uint32_t c0 = hist[hi], c1 = hist[hi - 1];
+        uint32_t total;
+        const uint32_t above = block_scan(c0 + c1, sums[0], total);
+        if (above < want && want <= above + c0 + c1) {
+          const bool first = want <= above + c0;
+          found_bin = (uint32_t)(first ? hi : hi - 1);
+          found_above = first ? above : above + c0;
+        }
+        __syncthreads();
+        want -= found_above;
+        prefix |= found_bin << shift;
+        mask |= digit << shift;
+      }
+      threshold = prefix;
+      equals = want;
+    }
+  }
+
+  // the ordered pass: position i is kept if its key is above the threshold, or equal and among
+  // the first `equals` of those, or if it is recent
+  uint32_t above0 = 0u, equal0 = 0u;  // so far
+  int buf = 0;
+  for (int64_t base = 0; base < (bad ? 0 : L); base += kSelThreads * kPer, buf ^= 1) {
+    float x[kPer];
+    uint32_t cnt = 0u, is_eq = 0u, is_above = 0u;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int64_t i = base + threadIdx.x * kPer + j;
+      x[j] = i < L ? w[i] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int64_t i = base + threadIdx.x * kPer + j;
+      const uint32_t key = ordered(x[j]);
+      if (i < L && (i >= older || key > threshold)) is_above |= 1u << j;
+      else if (i < L && key == threshold && equals) is_eq |= 1u << j;
+    }
+    cnt = __popc(is_above) << 16 | __popc(is_eq);
+    uint32_t total;
+    const uint32_t ex = block_scan(cnt, sums[buf], total);
+    uint32_t a = above0 + (ex >> 16), e = equal0 + (ex & 0xffffu);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const bool ab = is_above >> j & 1u, eq = is_eq >> j & 1u;
+      if (ab || (eq && e < equals)) {
+        const uint32_t at = a + min(e, equals);
+        kept[at] = (int32_t)(base + threadIdx.x * kPer + j);
+        if (w_out) w_out[at] = x[j];
+      }
+      a += ab;
+      e += eq;
+    }
+    above0 += total >> 16;
+    equal0 += total & 0xffffu;
+  }
+  for (int64_t j = n + (int64_t)threadIdx.x; j < p.budget; j += kSelThreads) {
+    kept[j] = -1;
+    if (w_out) w_out[j] = 0.f;
+  }
+}
+
+// One CTA: 64 kept rows (one group of the destination) of one head. 16 (bf16) or 8 (8-bit)
+// lanes move a row, 16 bytes each; all the loads of the CTA's K and V rows are in flight at
+// once.
+constexpr int kCopyThreads = 256;
+
+template <bool FP8>
+__global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const EvictParams p, int chunks) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  constexpr int kRowBytes = FP8 ? kD : 2 * kD;
+  constexpr int kLanes = kRowBytes / 16, kRowsPerPass = kCopyThreads / kLanes;
+  constexpr int kPasses = kGroup / kRowsPerPass;
+  __shared__ int64_t src_slot[kGroup];       // pool row of a kept row, -1: none
+  __shared__ float ratio[2][kGroup];         // 8-bit: its scale over the group's
+  __shared__ float new_scale[2];
+  const int h = (int)(blockIdx.x % p.hkv);
+  const int64_t bc = blockIdx.x / p.hkv;
+  const int c = (int)(bc % chunks), b = (int)(bc / chunks);
+  const int n = *(p.new_lens + b), j0 = c * kGroup;
+  if (j0 >= n || aborted(p.err)) return;
+  const int rows = min(kGroup, n - j0);
+  const int32_t dst_blk =
+      *(p.dst_tables + (int64_t)b * p.dst_width + j0 / p.block_size);
+  if (dst_blk < 0 || dst_blk >= p.num_blocks) {
+    if (threadIdx.x == 0 && h == 0) record_error(p.err, kErrBlock);
+    return;
+  }
+  const int dst_in = j0 % p.block_size;
+  const int t = threadIdx.x;
+  if (t < kGroup) {
+    int64_t slot = -1;
+    float s[2] = {0.f, 0.f};
+    if (t < rows) {
+      const int32_t i = *(p.kept + ((int64_t)b * p.hkv + h) * p.budget + j0 + t);
+      const int32_t blk = *(p.src_tables + (int64_t)b * p.src_width + i / p.block_size);
+      if (blk >= 0 && blk < p.num_blocks) {
+        const int in = i % p.block_size;
+        slot = (int64_t)blk * p.block_size + in;
+        if constexpr (FP8) {
+          const int64_t at = ((int64_t)blk * p.hkv + h) * (p.block_size / kGroup) + in / kGroup;
+          s[0] = p.k_scale[at];
+          s[1] = p.v_scale[at];
+        }
+      } else {
+        record_error(p.err, kErrBlock);  // its row becomes zeros
+      }
+    }
+    src_slot[t] = slot;
+    if constexpr (FP8) {
+      ratio[0][t] = s[0];
+      ratio[1][t] = s[1];
+    }
+  }
+  __syncthreads();
+  if constexpr (FP8) {
+    if (t < 64) {  // warp 0: K's largest scale, warp 1: V's
+      const int kv = t >> 5, l = t & 31;
+      float m = fmaxf(ratio[kv][l], ratio[kv][l + 32]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+      if (l == 0) {
+        m = m > 0.f ? m : pow2f(kFp8MinExp);
+        new_scale[kv] = m;
+        const int64_t at =
+            ((int64_t)dst_blk * p.hkv + h) * (p.block_size / kGroup) + dst_in / kGroup;
+        (kv ? p.v_scale : p.k_scale)[at] = m;
+      }
+    }
+    __syncthreads();
+  }
+  const int part = t % kLanes, row0 = t / kLanes;
+  const int64_t rstride = (int64_t)p.hkv * kRowBytes;
+  const int64_t col = (int64_t)h * kRowBytes + part * 16;
+  uint4 x[2][kPasses];
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int row = row0 + i * kRowsPerPass;
+    const int64_t slot = src_slot[row];
+    x[0][i] = x[1][i] = make_uint4(0, 0, 0, 0);
+    if (slot >= 0) {
+      x[0][i] = ld_once_u4(reinterpret_cast<const uint4 *>(p.k_cache + slot * rstride + col));
+      x[1][i] = ld_once_u4(reinterpret_cast<const uint4 *>(p.v_cache + slot * rstride + col));
+    }
+  }
+  const int64_t dst0 = ((int64_t)dst_blk * p.block_size + dst_in) * rstride + col;
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int row = row0 + i * kRowsPerPass;
+      if (row >= rows) continue;
+      uint4 v = x[kv][i];
+      if constexpr (FP8) {
+        const float f = ratio[kv][row] / new_scale[kv];
+        if (f != 1.f) {
+          v.x = rescale4(v.x, f);
+          v.y = rescale4(v.y, f);
+          v.z = rescale4(v.z, f);
+          v.w = rescale4(v.w, f);
+        }
+      }
+      *reinterpret_cast<uint4 *>((kv ? p.v_cache : p.k_cache) + dst0 + row * rstride) = v;
+    }
+}
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+template <class... Formal, class... Args>
+cudaError_t launch_after(void (*kernel)(Formal...), int64_t grid, int threads,
+                         cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+}  // namespace
+}  // namespace pkv
+
+extern "C" pkv_status pkv_kv_evict(const float *weights, int64_t weights_stride,
+                                   const int32_t *context_lens, int32_t batch,
+                                   int32_t max_context_len, int32_t budget, int32_t recent,
+                                   const int32_t *block_tables, int32_t block_table_width,
+                                   const int32_t *dst_block_tables, int32_t dst_block_table_width,
+                                   void *k_cache, void *v_cache, float *k_scale, float *v_scale,
+                                   int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                   int64_t num_blocks, int32_t *kept, float *weights_out,
+                                   int64_t weights_out_stride, int32_t *new_context_lens,
+                                   void *stream) {
+  using namespace pkv;
+  if (batch < 0 || max_context_len < 0 || budget <= 0 || recent < 0 || recent > budget ||
+      num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 || num_blocks <= 0 ||
+      block_table_width <= 0 || dst_block_table_width <= 0 || weights_stride < max_context_len ||
+      (weights_out && weights_out_stride < budget))
+    return PKV_ERR_INVALID_ARG;
+  if (batch == 0) return PKV_OK;
+  if (!weights || !context_lens || !block_tables || !dst_block_tables || !k_cache || !v_cache ||
+      !kept || !new_context_lens || !k_scale != !v_scale)
+    return PKV_ERR_INVALID_ARG;
+  // the call reads these while it writes those
+  if (dst_block_tables == block_tables || new_context_lens == context_lens ||
+      weights_out == weights)
+    return PKV_ERR_INVALID_ARG;
+  const bool fp8 = k_scale != nullptr;
+  if (head_dim != kD || block_size % (fp8 ? 256 : kGroup) != 0) return PKV_ERR_UNSUPPORTED;
+  if (!aligned16(k_cache) || !aligned16(v_cache)) return PKV_ERR_UNSUPPORTED;
+  const int64_t rows = (int64_t)batch * num_kv_heads;
+  const int64_t chunks = ((int64_t)std::min(budget, std::max(max_context_len, 1)) + kGroup - 1) / kGroup;
+  if (rows * chunks > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+  EvictParams prm{};
+  prm.err = current_error_word();
+  if (!prm.err) return PKV_ERR_CUDA;
+  prm.weights = weights;
+  prm.weights_stride = weights_stride;
+  prm.context_lens = context_lens;
+  prm.batch = batch;
+  prm.max_context_len = max_context_len;
+  prm.budget = budget;
+  prm.recent = recent;
+  prm.src_tables = block_tables;
+  prm.dst_tables = dst_block_tables;
+  prm.src_width = block_table_width;
+  prm.dst_width = dst_block_table_width;
+  prm.k_cache = static_cast<uint8_t *>(k_cache);
+  prm.v_cache = static_cast<uint8_t *>(v_cache);
+  prm.k_scale = k_scale;
+  prm.v_scale = v_scale;
+  prm.hkv = num_kv_heads;
+  prm.block_size = block_size;
+  prm.num_blocks = num_blocks;
+  prm.kept = kept;
+  prm.weights_out = weights_out;
+  prm.weights_out_stride = weights_out_stride;
+  prm.new_lens = new_context_lens;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_after(evict_select_kernel, rows, kSelThreads, s, prm);
+  if (e == cudaSuccess)
+    e = launch_after(fp8 ? evict_copy_kernel<true> : evict_copy_kernel<false>, rows * chunks,
+                     kCopyThreads, s, prm, (int)chunks);
+  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}

@@ -45,7 +45,7 @@ struct StoreParams {
 // Block of position pos of a sequence's table row, or -1 (recorded) for a bad id.
 __device__ __forceinline__ int64_t block_of(const int32_t *table, int64_t pos, int32_t block_size,
                                             int64_t num_blocks, unsigned int *err, bool record) {
-  const int32_t b = __ldg(table + pos / block_size);
+  const int32_t b = *(table + pos / block_size);
   if (b >= 0 && b < num_blocks) return b;
   if (record) record_error(err, kErrBlock);
   return -1;
@@ -58,8 +58,8 @@ __device__ __forceinline__ void check_lengths(const int32_t *cu, const int32_t *
                                               int32_t num_seqs, int64_t total, int64_t capacity,
                                               unsigned int *err) {
   for (int i = threadIdx.x; i < num_seqs; i += blockDim.x) {
-    const int32_t c0 = __ldg(cu + i), c1 = __ldg(cu + i + 1);
-    const int64_t ctx = kStore ? (int64_t)__ldg(context_lens + i) : (int64_t)c1 - c0;
+    const int32_t c0 = *(cu + i), c1 = *(cu + i + 1);
+    const int64_t ctx = kStore ? (int64_t)*(context_lens + i) : (int64_t)c1 - c0;
     if (c0 < 0 || c1 < c0 || c1 > total || ctx < (int64_t)c1 - c0) record_error(err, kErrSeqlen);
     else if (ctx > capacity) record_error(err, kErrContext);
   }
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kRunThreads)
   const int64_t r = blockIdx.x / p.hkv;
   const int h = (int)(blockIdx.x % p.hkv);
   const int n = find_sequence(p.cu, p.num_seqs, r, lane);
-  const int32_t c0 = __ldg(p.cu + n), c1 = __ldg(p.cu + n + 1), ctx = __ldg(p.context_lens + n);
+  const int32_t c0 = *(p.cu + n), c1 = *(p.cu + n + 1), ctx = *(p.context_lens + n);
   const int64_t j = r - run_base(c0, n);
   const int64_t capacity = (int64_t)p.table_width * p.block_size;
   if (blockIdx.x == 0)
@@ -110,8 +110,8 @@ __global__ void __launch_bounds__(kRunThreads)
     const int row = row0 + i * kRowsPerPass;
     x[0][i] = x[1][i] = make_uint4(0, 0, 0, 0);
     if (row < rows) {
-      x[0][i] = ld_stream_u4(reinterpret_cast<const uint4 *>(ks + row * p.k_stride));
-      x[1][i] = ld_stream_u4(reinterpret_cast<const uint4 *>(vs + row * p.v_stride));
+      x[0][i] = ld_once_u4(reinterpret_cast<const uint4 *>(ks + row * p.k_stride));
+      x[1][i] = ld_once_u4(reinterpret_cast<const uint4 *>(vs + row * p.v_stride));
     }
   }
   float old[2] = {0.f, 0.f};
@@ -197,8 +197,8 @@ __global__ void __launch_bounds__(kTokenWarps * 32)
   if (unit >= (int64_t)p.num_seqs * p.hkv) return;
   const int n = (int)(unit / p.hkv), h = (int)(unit % p.hkv);
   const uint8_t *src = is_v ? p.v + n * p.v_stride : p.k + n * p.k_stride;
-  const uint4 x = ld_stream_u4(reinterpret_cast<const uint4 *>(src + h * (kD * 2) + part * 16));
-  const int32_t ctx = __ldg(p.context_lens + n);
+  const uint4 x = ld_once_u4(reinterpret_cast<const uint4 *>(src + h * (kD * 2) + part * 16));
+  const int32_t ctx = *(p.context_lens + n);
   if (ctx == 0) return;  // a padding row
   if (ctx < 0 || (int64_t)ctx > (int64_t)p.table_width * p.block_size) {
     if (lane == 0 && h == 0) record_error(p.err, kErrContext);
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kRunThreads) kv_gather_fp8_kernel(const Gather
   const int64_t r = blockIdx.x / p.hkv;
   const int h = (int)(blockIdx.x % p.hkv);
   const int n = find_sequence(p.cu, p.num_seqs, r, lane);
-  const int32_t c0 = __ldg(p.cu + n), c1 = __ldg(p.cu + n + 1);
+  const int32_t c0 = *(p.cu + n), c1 = *(p.cu + n + 1);
   const int64_t j = r - run_base(c0, n);
   const int64_t capacity = (int64_t)p.table_width * p.block_size;
   if (blockIdx.x == 0)
@@ -286,15 +286,15 @@ __global__ void __launch_bounds__(kRunThreads) kv_gather_fp8_kernel(const Gather
     for (int i = 0; i < kFp8Group / kPer; ++i) x[s][i] = make_uint4(0, 0, 0, 0);
   if (blk >= 0) {  // the rows of a bad block id are zeros, as in the attention kernels
     const int64_t sc = (blk * p.hkv + h) * (p.block_size / kFp8Group) + in_block / kFp8Group;
-    scale[0] = __ldg(p.k_scale + sc);
-    scale[1] = __ldg(p.v_scale + sc);
+    scale[0] = *(p.k_scale + sc);
+    scale[1] = *(p.v_scale + sc);
     const int64_t at = (blk * p.block_size + in_block) * rstride + h * kD + part * 16;
 #pragma unroll
     for (int i = 0; i < kFp8Group / kPer; ++i) {
       const int row = row0 + i * kPer;
       if (row < rows) {
-        x[0][i] = ld_stream_u4(reinterpret_cast<const uint4 *>(p.k_cache + at + row * rstride));
-        x[1][i] = ld_stream_u4(reinterpret_cast<const uint4 *>(p.v_cache + at + row * rstride));
+        x[0][i] = ld_once_u4(reinterpret_cast<const uint4 *>(p.k_cache + at + row * rstride));
+        x[1][i] = ld_once_u4(reinterpret_cast<const uint4 *>(p.v_cache + at + row * rstride));
       }
     }
   }

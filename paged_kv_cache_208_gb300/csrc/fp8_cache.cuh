@@ -104,7 +104,7 @@ __device__ __forceinline__ int find_sequence(const int32_t *cu, int n, int64_t r
   while (len > 1) {
     const int stride = (len + 31) >> 5;
     const int i = lane * stride;
-    const bool le = i < len && (int64_t)(__ldg(cu + lo + i) >> 6) + 2 * (int64_t)(lo + i) <= r;
+    const bool le = i < len && (int64_t)(*(cu + lo + i) >> 6) + 2 * (int64_t)(lo + i) <= r;
     const int c = __popc(__ballot_sync(0xffffffffu, le));
     const int step = (c > 0 ? c - 1 : 0) * stride;
     lo += step;
