@@ -11,6 +11,7 @@ PyTorch is used for device memory and streams only.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -356,44 +357,135 @@ def qk_norm_rope_store(qkv, positions, q_norm_weight, k_norm_weight, eps, cos_si
 # ----------------------------------------------------------------------------- the 8-bit cache
 FP8_GROUP = 64  # tokens of a block that share a scale
 
+_E4M3, _BF16, _F32, _INT32 = torch.float8_e4m3fn, torch.bfloat16, torch.float32, torch.int32
 
-def _need_fp8_cache(k_cache, v_cache, k_scale, v_scale):
-    """Checks the four tensors of an 8-bit cache; returns (num_blocks, block_size, hkv, d)."""
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _need(t, n, torch.float8_e4m3fn)
-    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        _need(t, n, torch.float32)
+# These calls run once per layer and step: the checks below take a short path over what is right
+# and look for the message only when something is not. Every tensor has to be on the caches'
+# device, which need not be the current one.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_HERE_ALREADY = contextlib.nullcontext()
+
+
+def _on(index: int):
+    """Launches go to the tensors' device, whichever is current."""
+    return _HERE_ALREADY if index == _current_device() else torch.cuda.device(index)
+
+
+def _stream_on(stream, index: int) -> int:
+    """The stream's handle; for None the current stream of the device (made current by _on)."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(index)
+    return _stream(stream)
+
+
+def _need_on(t, name: str, dtype, index: int) -> None:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
+    _need(t, name, dtype)
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the caches on cuda:{index}")
+
+
+def _need_cache(k_cache, v_cache, k_scale=None, v_scale=None):
+    """Checks the pools of a bf16 cache, or of an 8-bit one with its scales; returns (device index,
+    num_blocks, block_size, hkv, d)."""
+    if k_scale is None and v_scale is None:
+        pools, dtype = ((k_cache, "k_cache"), (v_cache, "v_cache")), _BF16
+        if (k_cache.dtype is _BF16 and v_cache.dtype is _BF16 and k_cache.dim() == 4
+                and (shape := k_cache.shape) == v_cache.shape and k_cache.is_contiguous()
+                and v_cache.is_contiguous() and (index := k_cache.get_device()) >= 0
+                and v_cache.get_device() == index):
+            return index, *shape
+    else:
+        pools, dtype = ((k_cache, "k_cache"), (v_cache, "v_cache")), _E4M3
+        if (k_cache.dtype is _E4M3 and v_cache.dtype is _E4M3 and k_cache.dim() == 4
+                and (shape := k_cache.shape) == v_cache.shape and k_scale is not None
+                and v_scale is not None and k_scale.dtype is _F32 and v_scale.dtype is _F32
+                and (index := k_cache.get_device()) >= 0 and v_cache.get_device() == index
+                and k_scale.get_device() == index and v_scale.get_device() == index
+                and k_scale.shape == (want := (shape[0], shape[2], shape[1] // FP8_GROUP))
+                and v_scale.shape == want and k_cache.is_contiguous()
+                and v_cache.is_contiguous() and k_scale.is_contiguous()
+                and v_scale.is_contiguous()):
+            return index, *shape
+    if (k_scale is None) != (v_scale is None):
+        raise ValueError("k_scale and v_scale go together")
+    for t, n in pools:
+        _need(t, n, dtype)
+        _need_on(t, n, dtype, k_cache.get_device())
     if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
         raise ValueError("caches must be [NB, bs, Hkv, D], the same for K and V")
-    nb, bs, hkv, d = k_cache.shape
-    want = (nb, hkv, bs // FP8_GROUP)
-    if tuple(k_scale.shape) != want or tuple(v_scale.shape) != want:
-        raise ValueError(f"scales must be [NB, Hkv, bs / {FP8_GROUP}] = {list(want)}")
-    if not all(t.is_contiguous() for t in (k_cache, v_cache, k_scale, v_scale)):
-        raise ValueError("caches and scales must be contiguous")
-    for t, n in ((v_cache, "v_cache"), (k_scale, "k_scale"), (v_scale, "v_scale")):
-        _same_device(t, n, k_cache.device)
-    return nb, bs, hkv, d
+    if k_scale is not None:
+        want = [k_cache.shape[0], k_cache.shape[2], k_cache.shape[1] // FP8_GROUP]
+        for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            _need_on(t, n, _F32, k_cache.get_device())
+            if list(t.shape) != want:
+                raise ValueError(f"{n} must be [NB, Hkv, bs / {FP8_GROUP}] = {want}")
+    raise ValueError("caches and scales must be contiguous")
 
 
-def _need_list(t, name, shape, device):
-    """An int32 tensor of this shape (None: any size), contiguous, on the caches' device."""
-    _need(t, name, torch.int32)
-    if (t.dim() != len(shape) or any(a is not None and a != b for a, b in zip(shape, t.shape))
-            or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape "
-                         f"{['*' if a is None else a for a in shape]}")
-    _same_device(t, name, device)
+def _need_ints(t, name: str, shape: tuple, index: int) -> None:
+    """An int32 tensor of this shape, contiguous, on the caches' device."""
+    if not (t.dtype is _INT32 and t.shape == shape and t.get_device() == index
+            and t.is_contiguous()):
+        _need_on(t, name, _INT32, index)
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)}, got "
+                         f"{list(t.shape)}")
 
 
-def _same_device(t, name, device):
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the caches on {device}")
+def _need_lists(context_lens, block_tables, index: int):
+    """Context lengths [B] and block tables [B, W]; returns (B, W)."""
+    if context_lens.dim() != 1 or block_tables.dim() != 2:
+        raise ValueError("context_lens must be [B] and block tables [B, W] int32 tensors")
+    B, W = block_tables.shape
+    _need_ints(context_lens, "context_lens", (B,), index)
+    _need_ints(block_tables, "block_tables", (B, W), index)
+    return B, W
 
 
-def _on(device) -> torch.cuda.device:
-    """Launches go to the tensors' device, whichever is current."""
-    return torch.cuda.device(device)
+def _need_rows(t, name: str, hkv: int, d: int, index: int) -> int:
+    """[T, Hkv, D] bf16 rows, each token's dense; returns the token stride."""
+    if not (t.dtype is _BF16 and t.get_device() == index and t.dim() == 3 and t.shape[1] == hkv
+            and t.shape[2] == d):
+        _need_on(t, name, _BF16, index)
+        raise ValueError(f"{name} must be [T, {hkv}, {d}]")
+    tok, head, elem = t.stride()
+    if elem != 1 or (head != d and hkv > 1):
+        raise ValueError(f"{name}: each token's heads must be dense")
+    return tok if t.shape[0] > 1 else hkv * d
+
+
+def _need_weights(t, name: str, batch: int, hkv: int, length: int, index: int) -> int:
+    """A [B, Hkv, >= length] float32 tensor of dense rows that lie one stride apart; returns the
+    stride."""
+    if t.dtype is not _F32 or t.get_device() != index:
+        _need_on(t, name, _F32, index)
+    if t.dim() == 3:
+        b, h, n = t.shape
+        sb, sh, sn = t.stride()
+        if (b == batch and h == hkv and n >= length and (sn == 1 or n <= 1)
+                and (b <= 1 or sb == (h * sh if h > 1 else sb))):
+            return sh if h > 1 else sb if b > 1 else n
+    raise ValueError(f"{name} must be [{batch}, {hkv}, >= {length}] with dense, evenly spaced "
+                     "rows")
+
+
+def _weights_args(weights, weights_out, batch, hkv, length, index):
+    """(in pointer, in stride, out pointer, out stride); without weights_out in place."""
+    if weights is None:
+        if weights_out is None:
+            return None, 0, None, 0
+        return None, 0, weights_out.data_ptr(), _need_weights(weights_out, "weights_out", batch,
+                                                              hkv, length, index)
+    in_stride = _need_weights(weights, "weights", batch, hkv, length, index)
+    ptr = weights.data_ptr()
+    if weights_out is None:
+        return ptr, in_stride, ptr, in_stride
+    out_stride = _need_weights(weights_out, "weights_out", batch, hkv, length, index)
+    out = weights_out.data_ptr()
+    if out == ptr and in_stride != out_stride:
+        raise ValueError("weights and weights_out overlap with different strides")
+    return ptr, in_stride, out, out_stride
 
 
 def kv_store_fp8(k: torch.Tensor, v: torch.Tensor, context_lens: torch.Tensor,
@@ -407,28 +499,25 @@ def kv_store_fp8(k: torch.Tensor, v: torch.Tensor, context_lens: torch.Tensor,
     block_tables [B, W], cu_seqlens [B + 1] int32; caches [NB, bs, Hkv, D] float8_e4m3fn;
     scales [NB, Hkv, bs / 64] float32. A group of 64 positions keeps one power-of-two scale per
     head; it grows, and the group's earlier rows are re-rounded, when a new row needs it."""
-    nb, bs, hkv, d = _need_fp8_cache(k_cache, v_cache, k_scale, v_scale)
-    dev = k_cache.device
-    for t, n in ((k, "k"), (v, "v")):
-        _need(t, n, torch.bfloat16)
-        _same_device(t, n, dev)
-        if t.dim() != 3 or t.shape[1:] != (hkv, d) or t.stride(2) != 1 or (
-                t.stride(1) != d and hkv > 1):
-            raise ValueError(f"{n} must be [T, {hkv}, {d}] with dense rows")
+    if k_scale is None or v_scale is None:
+        raise ValueError("k_scale and v_scale must be given")
+    index, nb, bs, hkv, d = _need_cache(k_cache, v_cache, k_scale, v_scale)
+    ks, vs = _need_rows(k, "k", hkv, d, index), _need_rows(v, "v", hkv, d, index)
     T = k.shape[0]
     if v.shape[0] != T:
         raise ValueError("k and v must hold the same tokens")
-    _need_list(context_lens, "context_lens", (None,), dev)
-    B = context_lens.shape[0]
-    _need_list(block_tables, "block_tables", (B, None), dev)
+    B, W = _need_lists(context_lens, block_tables, index)
+    cu = None
     if cu_seqlens is not None:
-        _need_list(cu_seqlens, "cu_seqlens", (B + 1,), dev)
-    with _on(dev):
-        _check("pkv_kv_store_fp8", _LIB.pkv_kv_store_fp8(
-            _ptr(k), k.stride(0) if T > 1 else hkv * d, _ptr(v),
-            v.stride(0) if T > 1 else hkv * d, _ptr(cu_seqlens), _ptr(context_lens),
-            _ptr(block_tables), block_tables.shape[1], B, T, _ptr(k_cache), _ptr(v_cache),
-            _ptr(k_scale), _ptr(v_scale), hkv, d, bs, nb, _stream(stream)))
+        _need_ints(cu_seqlens, "cu_seqlens", (B + 1,), index)
+        cu = cu_seqlens.data_ptr()
+    with _on(index):
+        status = _LIB.pkv_kv_store_fp8(
+            k.data_ptr(), ks, v.data_ptr(), vs, cu, context_lens.data_ptr(),
+            block_tables.data_ptr(), W, B, T, k_cache.data_ptr(), v_cache.data_ptr(),
+            k_scale.data_ptr(), v_scale.data_ptr(), hkv, d, bs, nb, _stream_on(stream, index))
+    if status:
+        raise PkvError("pkv_kv_store_fp8", status)
 
 
 def kv_gather_fp8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
@@ -437,25 +526,31 @@ def kv_gather_fp8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.T
                   v_out: torch.Tensor | None = None, stream=None):
     """Rows of an 8-bit cache as packed bf16 (k, v) [total_k, Hkv, D]: positions 0 .. of sequence
     n at rows cu_seqlens_k[n] .. cu_seqlens_k[n + 1], as varlen_prefill_attn takes them."""
-    nb, bs, hkv, d = _need_fp8_cache(k_cache, v_cache, k_scale, v_scale)
-    dev = k_cache.device
-    _need_list(cu_seqlens_k, "cu_seqlens_k", (None,), dev)
-    N = cu_seqlens_k.shape[0] - 1
-    _need_list(block_table, "block_table", (N, None), dev)
+    if k_scale is None or v_scale is None:
+        raise ValueError("k_scale and v_scale must be given")
+    index, nb, bs, hkv, d = _need_cache(k_cache, v_cache, k_scale, v_scale)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be a [N, W] int32 tensor")
+    N, W = block_table.shape
+    _need_ints(block_table, "block_table", (N, W), index)
+    _need_ints(cu_seqlens_k, "cu_seqlens_k", (N + 1,), index)
+    shape = (int(total_k), hkv, d)
     outs = []
     for t, n in ((k_out, "k_out"), (v_out, "v_out")):
         if t is None:
-            t = torch.empty((int(total_k), hkv, d), dtype=torch.bfloat16, device=dev)
-        _need(t, n, torch.bfloat16)
-        _same_device(t, n, dev)
-        if tuple(t.shape) != (int(total_k), hkv, d) or not t.is_contiguous():
-            raise ValueError(f"{n} must be a contiguous [{int(total_k)}, {hkv}, {d}] tensor")
+            t = torch.empty(shape, dtype=_BF16, device=k_cache.device)
+        elif not (t.dtype is _BF16 and t.shape == shape and t.get_device() == index
+                  and t.is_contiguous()):
+            _need_on(t, n, _BF16, index)
+            raise ValueError(f"{n} must be a contiguous {list(shape)} tensor")
         outs.append(t)
-    with _on(dev):
-        _check("pkv_kv_gather_fp8", _LIB.pkv_kv_gather_fp8(
-            _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
-            block_table.shape[1], _ptr(cu_seqlens_k), N, int(total_k), _ptr(outs[0]),
-            _ptr(outs[1]), hkv, d, bs, nb, _stream(stream)))
+    with _on(index):
+        status = _LIB.pkv_kv_gather_fp8(
+            k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            block_table.data_ptr(), W, cu_seqlens_k.data_ptr(), N, shape[0], outs[0].data_ptr(),
+            outs[1].data_ptr(), hkv, d, bs, nb, _stream_on(stream, index))
+    if status:
+        raise PkvError("pkv_kv_gather_fp8", status)
     return outs[0], outs[1]
 
 
@@ -474,8 +569,7 @@ def decode_fp8_workspace(batch: int, num_q_heads: int, num_kv_heads: int, head_d
                          device="cuda", stream=None) -> torch.Tensor:
     """A workspace for paged_decode_attn_fp8 (with weights=True also for its weights_out), ready
     for use on `stream` (the current stream when None)."""
-    device = torch.device(device)
-    with _on(device):
+    with torch.cuda.device(device):
         n = int(_LIB.pkv_decode_fp8_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim,
                                                     max_context_len, num_splits, int(weights)))
         return _zeroed_workspace(n, device, stream)
@@ -486,59 +580,35 @@ def decode_weights_workspace(batch: int, num_q_heads: int, num_kv_heads: int, he
                              stream=None) -> torch.Tensor:
     """A workspace for paged_decode_attn_weights, ready for use on `stream` (the current stream
     when None)."""
-    device = torch.device(device)
-    with _on(device):
+    with torch.cuda.device(device):
         n = int(_LIB.pkv_decode_weights_workspace_bytes(
             batch, num_q_heads, num_kv_heads, head_dim, max_context_len, num_splits))
         return _zeroed_workspace(n, device, stream)
 
 
-def _need_decode(q, k_cache, block_tables, context_lens, out):
-    """Checks what every decode call takes; returns (batch, num_q_heads, out)."""
-    _need(q, "q", torch.bfloat16)
-    dev = k_cache.device
-    _same_device(q, "q", dev)
-    if q.dim() != 3 or q.shape[2] != k_cache.shape[3] or not q.is_contiguous():
-        raise ValueError(f"q must be a contiguous [B, Hq, {k_cache.shape[3]}] tensor")
-    B, hq, _ = q.shape
-    _need_list(block_tables, "block_tables", (B, None), dev)
-    _need_list(context_lens, "context_lens", (B,), dev)
+def _need_decode(q, d, block_tables, context_lens, out, index):
+    """Checks what every decode call takes; returns (batch, num_q_heads, table width, out)."""
+    if not (q.dtype is _BF16 and q.dim() == 3 and q.get_device() == index and q.is_contiguous()
+            and q.shape[2] == d):
+        _need_on(q, "q", _BF16, index)
+        raise ValueError(f"q must be a contiguous [B, Hq, {d}] tensor")
+    B, W = _need_lists(context_lens, block_tables, index)
+    if q.shape[0] != B:
+        raise ValueError(f"q holds {q.shape[0]} sequences, block_tables {B}")
     if out is None:
         out = torch.empty_like(q)
-    else:
-        _need(out, "out", torch.bfloat16)
-        _same_device(out, "out", dev)
-        if out.shape != q.shape or not out.is_contiguous():
-            raise ValueError("out must be a contiguous tensor of q's shape")
-    return B, hq, out
+    elif not (out.dtype is _BF16 and out.shape == q.shape and out.get_device() == index
+              and out.is_contiguous()):
+        _need_on(out, "out", _BF16, index)
+        raise ValueError("out must be a contiguous tensor of q's shape")
+    return B, q.shape[1], W, out
 
 
-def _need_weights(t, name, batch, hkv, max_context_len, device):
-    """A [B, Hkv, S] float32 tensor of dense rows that lie one stride apart; returns it."""
-    _need(t, name, torch.float32)
-    _same_device(t, name, device)
-    if (t.dim() != 3 or t.shape[:2] != (batch, hkv) or t.shape[2] < max_context_len
-            or (t.shape[2] > 1 and t.stride(2) != 1)
-            or (batch > 1 and t.stride(0) != hkv * t.stride(1))):
-        raise ValueError(f"{name} must be [{batch}, {hkv}, >= {max_context_len}] with dense, "
-                         "evenly spaced rows")
-    return t.stride(1) if hkv > 1 else t.stride(0) if batch > 1 else t.shape[2]
-
-
-def _weights_args(weights, weights_out, batch, hkv, max_context_len, device):
-    """(in pointer, in stride, out pointer, out stride); without weights_out in place."""
-    if weights is None and weights_out is None:
-        return None, 0, None, 0
-    if weights_out is None:
-        weights_out = weights
-    in_stride = 0
-    if weights is not None:
-        in_stride = _need_weights(weights, "weights", batch, hkv, max_context_len, device)
-    out_stride = _need_weights(weights_out, "weights_out", batch, hkv, max_context_len, device)
-    if (weights is not None and weights_out.data_ptr() == weights.data_ptr()
-            and in_stride != out_stride):
-        raise ValueError("weights and weights_out overlap with different strides")
-    return _ptr(weights), in_stride, _ptr(weights_out), out_stride
+def _need_workspace(t, index) -> int:
+    """A contiguous tensor on the caches' device; returns its bytes."""
+    if t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
+    return t.numel() * t.element_size()
 
 
 def paged_decode_attn_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -552,19 +622,25 @@ def paged_decode_attn_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     """paged_decode_attn over an 8-bit cache. q: [B, Hq, D] bf16; caches [NB, bs, Hkv, D]
     float8_e4m3fn with scales [NB, Hkv, bs / 64] float32 (see kv_store_fp8). With weights and / or
     weights_out the attention weights too, as paged_decode_attn_weights gives them."""
-    nb, bs, hkv, d = _need_fp8_cache(k_cache, v_cache, k_scale, v_scale)
-    dev = k_cache.device
-    B, hq, out = _need_decode(q, k_cache, block_tables, context_lens, out)
-    w = _weights_args(weights, weights_out, B, hkv, int(max_context_len), dev)
-    with _on(dev):
+    if k_scale is None or v_scale is None:
+        raise ValueError("k_scale and v_scale must be given")
+    index, nb, bs, hkv, d = _need_cache(k_cache, v_cache, k_scale, v_scale)
+    B, hq, W, out = _need_decode(q, d, block_tables, context_lens, out, index)
+    longest = int(max_context_len)
+    w_in, w_in_stride, w_out, w_out_stride = _weights_args(weights, weights_out, B, hkv, longest,
+                                                           index)
+    with _on(index):
         if workspace is None:
-            workspace = decode_fp8_workspace(B, hq, hkv, d, int(max_context_len), num_splits,
-                                             w[2] is not None, dev, stream)
-        _check("pkv_paged_decode_attn_fp8", _LIB.pkv_paged_decode_attn_fp8(
-            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-            _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), B,
-            int(max_context_len), hq, hkv, d, bs, nb, float(scale), int(num_splits), *w,
-            _ptr(workspace), _ws_bytes(workspace, dev), _ptr(out), _stream(stream)))
+            workspace = decode_fp8_workspace(B, hq, hkv, d, longest, num_splits,
+                                             w_out is not None, index, stream)
+        status = _LIB.pkv_paged_decode_attn_fp8(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+            v_scale.data_ptr(), block_tables.data_ptr(), W, context_lens.data_ptr(), B, longest,
+            hq, hkv, d, bs, nb, scale, num_splits, w_in, w_in_stride, w_out, w_out_stride,
+            workspace.data_ptr(), _need_workspace(workspace, index), out.data_ptr(),
+            _stream_on(stream, index))
+    if status:
+        raise PkvError("pkv_paged_decode_attn_fp8", status)
     return out
 
 
@@ -578,30 +654,27 @@ def paged_decode_attn_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: t
     """paged_decode_attn that also adds each cached token's attention weight, summed over the
     query heads of its KV head, to `weights` [B, Hkv, >= max_context_len] float32: in place, or
     into weights_out (without weights: weights_out receives this step's alone)."""
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _need(t, n, torch.bfloat16)
-    if (k_cache.dim() != 4 or k_cache.shape != v_cache.shape
-            or not (k_cache.is_contiguous() and v_cache.is_contiguous())):
-        raise ValueError("caches must be contiguous [NB, bs, Hkv, D], the same for K and V")
-    nb, bs, hkv, d = k_cache.shape
-    dev = k_cache.device
-    _same_device(v_cache, "v_cache", dev)
-    B, hq, out = _need_decode(q, k_cache, block_tables, context_lens, out)
+    index, nb, bs, hkv, d = _need_cache(k_cache, v_cache)
+    B, hq, W, out = _need_decode(q, d, block_tables, context_lens, out, index)
     if weights is None and weights_out is None:
         raise ValueError("weights or weights_out must be given")
-    w = _weights_args(weights, weights_out, B, hkv, int(max_context_len), dev)
-    with _on(dev):
+    longest = int(max_context_len)
+    w_in, w_in_stride, w_out, w_out_stride = _weights_args(weights, weights_out, B, hkv, longest,
+                                                           index)
+    with _on(index):
         if workspace is None:
-            workspace = decode_weights_workspace(B, hq, hkv, d, int(max_context_len), num_splits,
-                                                 dev, stream)
-        _check("pkv_paged_decode_attn_weights", _LIB.pkv_paged_decode_attn_weights(
-            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), block_tables.shape[1],
-            _ptr(context_lens), B, int(max_context_len), hq, hkv, d, bs, nb, float(scale),
-            int(num_splits), *w, _ptr(workspace), _ws_bytes(workspace, dev), _ptr(out),
-            _stream(stream)))
+            workspace = decode_weights_workspace(B, hq, hkv, d, longest, num_splits, index, stream)
+        status = _LIB.pkv_paged_decode_attn_weights(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), W,
+            context_lens.data_ptr(), B, longest, hq, hkv, d, bs, nb, scale, num_splits, w_in,
+            w_in_stride, w_out, w_out_stride, workspace.data_ptr(),
+            _need_workspace(workspace, index), out.data_ptr(), _stream_on(stream, index))
+    if status:
+        raise PkvError("pkv_paged_decode_attn_weights", status)
     return out
 
 
+# ----------------------------------------------------------------------------- eviction
 def kv_evict(weights: torch.Tensor, context_lens: torch.Tensor, max_context_len: int,
              block_tables: torch.Tensor, dst_block_tables: torch.Tensor, budget: int,
              recent: int, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -616,53 +689,40 @@ def kv_evict(weights: torch.Tensor, context_lens: torch.Tensor, max_context_len:
     caches: bf16 [NB, bs, Hkv, D], or float8_e4m3fn with k_scale and v_scale. Returns (kept
     positions [B, Hkv, budget] int32 (-1 past a sequence's length), their weights
     [B, Hkv, budget], the new context lengths [B] int32)."""
-    if k_scale is None and v_scale is None:
-        for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-            _need(t, n, torch.bfloat16)
-        if (k_cache.dim() != 4 or k_cache.shape != v_cache.shape
-                or not (k_cache.is_contiguous() and v_cache.is_contiguous())):
-            raise ValueError("caches must be contiguous [NB, bs, Hkv, D], the same for K and V")
-        nb, bs, hkv, d = k_cache.shape
-        _same_device(v_cache, "v_cache", k_cache.device)
-    elif k_scale is None or v_scale is None:
-        raise ValueError("k_scale and v_scale go together")
-    else:
-        nb, bs, hkv, d = _need_fp8_cache(k_cache, v_cache, k_scale, v_scale)
-    dev = k_cache.device
-    budget, recent, max_context_len = int(budget), int(recent), int(max_context_len)
-    _need_list(context_lens, "context_lens", (None,), dev)
-    B = context_lens.shape[0]
-    _need_list(block_tables, "block_tables", (B, None), dev)
-    _need_list(dst_block_tables, "dst_block_tables", (B, None), dev)
-    w_stride = _need_weights(weights, "weights", B, hkv, max_context_len, dev)
+    index, nb, bs, hkv, d = _need_cache(k_cache, v_cache, k_scale, v_scale)
+    B, W = _need_lists(context_lens, block_tables, index)
+    if dst_block_tables.dim() != 2:
+        raise ValueError("dst_block_tables must be a [B, W'] int32 tensor")
+    dst_width = dst_block_tables.shape[1]
+    _need_ints(dst_block_tables, "dst_block_tables", (B, dst_width), index)
+    budget, recent, longest = int(budget), int(recent), int(max_context_len)
+    w_stride = _need_weights(weights, "weights", B, hkv, longest, index)
     if budget < 1 or not 0 <= recent <= budget:
         raise ValueError("budget must be at least 1 and recent between 0 and budget")
+    shape = (B, hkv, budget)
     if kept is None:
-        kept = torch.empty((B, hkv, budget), dtype=torch.int32, device=dev)
+        kept = torch.empty(shape, dtype=_INT32, device=k_cache.device)
     else:
-        _need_list(kept, "kept", (B, hkv, budget), dev)
+        _need_ints(kept, "kept", shape, index)
     if weights_out is None:
-        weights_out = torch.empty((B, hkv, budget), dtype=torch.float32, device=dev)
-    o_stride = _need_weights(weights_out, "weights_out", B, hkv, budget, dev)
+        weights_out = torch.empty(shape, dtype=_F32, device=k_cache.device)
+        o_stride = budget
+    else:
+        o_stride = _need_weights(weights_out, "weights_out", B, hkv, budget, index)
     if new_context_lens is None:
         new_context_lens = torch.empty_like(context_lens)
     else:
-        _need_list(new_context_lens, "new_context_lens", (B,), dev)
-    with _on(dev):
-        _check("pkv_kv_evict", _LIB.pkv_kv_evict(
-            _ptr(weights), w_stride, _ptr(context_lens), B, max_context_len, budget, recent,
-            _ptr(block_tables), block_tables.shape[1], _ptr(dst_block_tables),
-            dst_block_tables.shape[1], _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
-            _ptr(v_scale), hkv, d, bs, nb, _ptr(kept), _ptr(weights_out), o_stride,
-            _ptr(new_context_lens), _stream(stream)))
+        _need_ints(new_context_lens, "new_context_lens", (B,), index)
+    with _on(index):
+        status = _LIB.pkv_kv_evict(
+            weights.data_ptr(), w_stride, context_lens.data_ptr(), B, longest, budget, recent,
+            block_tables.data_ptr(), W, dst_block_tables.data_ptr(), dst_width,
+            k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale), _ptr(v_scale), hkv, d, bs, nb,
+            kept.data_ptr(), weights_out.data_ptr(), o_stride, new_context_lens.data_ptr(),
+            _stream_on(stream, index))
+    if status:
+        raise PkvError("pkv_kv_evict", status)
     return kept, weights_out, new_context_lens
-
-
-def _ws_bytes(workspace, device) -> int:
-    _same_device(workspace, "workspace", device)
-    if not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    return workspace.numel() * workspace.element_size()
 
 
 # ----------------------------------------------------------------------------- block manager

@@ -128,17 +128,10 @@ pkv_status decode_with_weights(Call c, cudaStream_t stream) {
   w.hkv = a.num_kv_heads;
   w.group = a.num_q_heads / a.num_kv_heads;
   w.err = a.err;
-  cudaLaunchConfig_t cfg{};
   const int64_t spans = ((int64_t)c.max_context_len + kSpan - 1) / kSpan;
-  cfg.gridDim = dim3((unsigned)rows, (unsigned)std::min<int64_t>(spans, 65535));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, decode_weights_kernel, w);
+  e = launch_after(decode_weights_kernel,
+                   dim3((unsigned)rows, (unsigned)std::min<int64_t>(spans, 65535)), kThreads,
+                   stream, w);
   return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 

@@ -15,6 +15,8 @@
 // Both are bound by HBM.
 #include <math.h>
 
+#include <algorithm>
+
 #include "device_common.cuh"
 #include "fp8_cache.cuh"
 #include "launch.h"
@@ -65,122 +67,128 @@ __device__ __forceinline__ void check_lengths(const int32_t *cu, const int32_t *
   }
 }
 
-// One CTA: a run of one head. Thread t holds bytes [16 (t % 16), +16) of rows t / 16 + 16 i of
-// the run, for K and for V.
-constexpr int kRunThreads = 256;
+// One CTA: K or V of a run (up to 64 rows of one group) for `heads_per_cta` consecutive heads, one
+// head at a time while the next one's rows are on their way: thread t holds bytes
+// [16 (t % 16), +16) of rows t / 16 + 8 i. A CTA has 32 KiB in flight and five fit on an SM;
+// going through the heads in one CTA pays the dependent loads of its start (cu_seqlens, the
+// table, 2-3 us) once: 145k tokens of 8 heads take XX us (YY of HBM's rate), 255 us with a CTA of
+// 256 threads for each head, K and V together.
+constexpr int kRunThreads = 128;
+constexpr int kRunWarps = kRunThreads / 32;
 constexpr int kRowsPerPass = kRunThreads / 16;
 constexpr int kPasses = kFp8Group / kRowsPerPass;
 
-__global__ void __launch_bounds__(kRunThreads)
-    kv_store_fp8_run_kernel(const StoreParams p) {
+__global__ void __launch_bounds__(kRunThreads, 5)
+    kv_store_fp8_run_kernel(const StoreParams p, int heads_per_cta) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  __shared__ uint32_t warp_max[2][kRunThreads / 32];
+  __shared__ uint32_t warp_max[2][kRunWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t r = blockIdx.x / p.hkv;
-  const int h = (int)(blockIdx.x % p.hkv);
+  const int parts = (p.hkv + heads_per_cta - 1) / heads_per_cta;
+  const bool is_v = blockIdx.x & 1;
+  const int64_t r = (blockIdx.x >> 1) / parts;
+  const int h0 = (int)((blockIdx.x >> 1) % parts) * heads_per_cta;
+  const int h1 = min(p.hkv, h0 + heads_per_cta);
   const int n = find_sequence(p.cu, p.num_seqs, r, lane);
-  const int32_t c0 = *(p.cu + n), c1 = *(p.cu + n + 1), ctx = *(p.context_lens + n);
+  const int32_t c0 = p.cu[n], c1 = p.cu[n + 1], ctx = p.context_lens[n];
   const int64_t j = r - run_base(c0, n);
   const int64_t capacity = (int64_t)p.table_width * p.block_size;
   if (blockIdx.x == 0)
     check_lengths<true>(p.cu, p.context_lens, p.num_seqs, p.num_tokens, capacity, p.err);
-  if (c0 < 0 || c1 < c0 || c1 > p.num_tokens || ctx < (int64_t)c1 - c0 ||
-      ctx > capacity)
-    return;
-  const int start = ctx - (c1 - c0);                          // first new position
-  const int64_t group = (int64_t)(start / kFp8Group) + j;     // group index in the sequence
+  if (c0 < 0 || c1 < c0 || c1 > p.num_tokens || ctx < (int64_t)c1 - c0 || ctx > capacity) return;
+  const int start = ctx - (c1 - c0);                        // first new position
+  const int64_t group = (int64_t)(start / kFp8Group) + j;   // group index in the sequence
   const int64_t begin = max((int64_t)start, group * kFp8Group);
   const int64_t end = min((int64_t)ctx, (group + 1) * kFp8Group);
   if (j < 0 || begin >= end) return;
+  const int rows = (int)(end - begin);
+  const int part = threadIdx.x & 15, row0 = threadIdx.x >> 4;
+  const int64_t stride = is_v ? p.v_stride : p.k_stride;
+  const uint8_t *src = (is_v ? p.v : p.k) + (c0 + begin - start + row0) * stride + part * 16;
+  uint4 x[2][kPasses];
+  auto load = [&](uint4(&y)[kPasses], int h) {
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      y[i] = make_uint4(0, 0, 0, 0);
+      if (row0 + i * kRowsPerPass < rows)
+        y[i] = ld_once_u4(
+            reinterpret_cast<const uint4 *>(src + i * kRowsPerPass * stride + h * (kD * 2)));
+    }
+  };
+  load(x[0], h0);
   const int64_t blk = block_of(p.block_tables + (int64_t)n * p.table_width, begin, p.block_size,
-                               p.num_blocks, p.err, threadIdx.x == 0 && h == 0);
-  if (blk < 0) return;
+                               p.num_blocks, p.err, threadIdx.x == 0 && h0 == 0);
+  // an earlier wait gave up somewhere: write nothing (decided by the CTA together)
+  if (__syncthreads_or(threadIdx.x == 0 && aborted(p.err)) || blk < 0) return;
   const int in_block = (int)(begin % p.block_size);
   const int before = in_block % kFp8Group;  // rows of the group from before the call
-  const int rows = (int)(end - begin);
-  const int64_t sc = (blk * p.hkv + h) * (p.block_size / kFp8Group) + in_block / kFp8Group;
+  const int64_t rstride = (int64_t)p.hkv * kD;
+  float *const scales = is_v ? p.v_scale : p.k_scale;
+  uint8_t *const dst0 =
+      (is_v ? p.v_cache : p.k_cache) + (blk * p.block_size + in_block) * rstride;
 
-  const int part = threadIdx.x & 15, row0 = threadIdx.x >> 4;
-  const uint8_t *ks = p.k + (c0 + begin - start) * p.k_stride + h * (kD * 2) + part * 16;
-  const uint8_t *vs = p.v + (c0 + begin - start) * p.v_stride + h * (kD * 2) + part * 16;
-  uint4 x[2][kPasses];
-#pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int row = row0 + i * kRowsPerPass;
-    x[0][i] = x[1][i] = make_uint4(0, 0, 0, 0);
-    if (row < rows) {
-      x[0][i] = ld_once_u4(reinterpret_cast<const uint4 *>(ks + row * p.k_stride));
-      x[1][i] = ld_once_u4(reinterpret_cast<const uint4 *>(vs + row * p.v_stride));
-    }
-  }
-  float old[2] = {0.f, 0.f};
-  if (before) {
-    old[0] = p.k_scale[sc];
-    old[1] = p.v_scale[sc];
-  }
-  // max |x| of the run, then of its finite values if there is an infinity or a NaN
-  uint32_t amax[2];
-  for (int pass = 0; pass < 2; ++pass) {
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < kPasses; ++i) {
-        uint4 w = x[s][i];
-        if (pass) {
-          w.x = bf16x2_finite(w.x);
-          w.y = bf16x2_finite(w.y);
-          w.z = bf16x2_finite(w.z);
-          w.w = bf16x2_finite(w.w);
-        }
-        m = __vmaxu2(m, __vmaxu2(bf16x2_absmax(w.x, w.y), bf16x2_absmax(w.z, w.w)));
-      }
-      m = max(m & 0xffffu, m >> 16);
-      m = __reduce_max_sync(kFull, m);
-      if (lane == 0) warp_max[s][warp] = m;
-    }
-    // an earlier wait gave up somewhere: write nothing (decided by the CTA together)
-    if (__syncthreads_or(threadIdx.x == 0 && aborted(p.err))) return;
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      amax[s] = 0;
-#pragma unroll
-      for (int w = 0; w < kRunThreads / 32; ++w) amax[s] = max(amax[s], warp_max[s][w]);
-    }
-    if (max(amax[0], amax[1]) < 0x7f80u) break;
+  // max |x| over the CTA, as bf16 bits
+  int buf = 0;
+  auto cta_max = [&](uint32_t m) {
+    m = __reduce_max_sync(kFull, max(m & 0xffffu, m >> 16));
+    if (lane == 0) warp_max[buf][warp] = m;
     __syncthreads();
-  }
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    uint8_t *cache = s ? p.v_cache : p.k_cache;
-    const int e = fp8_scale_exp(amax[s]);
-    const float scale = fmaxf(pow2f(e), old[s]);
-    const int64_t rstride = (int64_t)p.hkv * kD;
-    uint8_t *dst = cache + (blk * p.block_size + in_block) * rstride + h * kD;
-    if (before && scale > old[s]) {  // the rows from before, at the scale that grew
-      const float ratio = old[s] / scale;
-      for (int i = threadIdx.x; i < before * 8; i += kRunThreads) {
-        uint4 *q = reinterpret_cast<uint4 *>(dst - (int64_t)(before - i / 8) * rstride + (i % 8) * 16);
-        uint4 w = *q;
-        w.x = rescale4(w.x, ratio);
-        w.y = rescale4(w.y, ratio);
-        w.z = rescale4(w.z, ratio);
-        w.w = rescale4(w.w, ratio);
-        *q = w;
-      }
+    for (int w = 0; w < kRunWarps; ++w) m = max(m, warp_max[buf][w]);
+    buf ^= 1;  // (the next use of this half is two barriers away)
+    return m;
+  };
+  auto store = [&](const uint4(&y)[kPasses], int h) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i)
+      m = __vmaxu2(m, __vmaxu2(bf16x2_absmax(y[i].x, y[i].y), bf16x2_absmax(y[i].z, y[i].w)));
+    m = cta_max(m);
+    if (m >= 0x7f80u) {  // infinities or NaNs: the largest finite value counts
+      m = 0;
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i)
+        m = __vmaxu2(m, __vmaxu2(bf16x2_absmax(bf16x2_finite(y[i].x), bf16x2_finite(y[i].y)),
+                                 bf16x2_absmax(bf16x2_finite(y[i].z), bf16x2_finite(y[i].w))));
+      m = cta_max(m);
     }
+    const int64_t sc = (blk * p.hkv + h) * (p.block_size / kFp8Group) + in_block / kFp8Group;
+    float scale = pow2f(fp8_scale_exp(m));
+    uint8_t *dst = dst0 + h * kD;
+    if (before) {
+      const float old = scales[sc];
+      scale = fmaxf(scale, old);
+      if (scale > old) {  // the rows from before, at the scale that grew
+        const float ratio = old / scale;
+        for (int i = threadIdx.x; i < before * 8; i += kRunThreads) {
+          uint4 *q =
+              reinterpret_cast<uint4 *>(dst - (int64_t)(before - i / 8) * rstride + (i % 8) * 16);
+          uint4 w = *q;
+          w.x = rescale4(w.x, ratio);
+          w.y = rescale4(w.y, ratio);
+          w.z = rescale4(w.z, ratio);
+          w.w = rescale4(w.w, ratio);
+          *q = w;
+        }
+      }
+      __syncthreads();  // every thread has read the old scale
+    }
+    if (threadIdx.x == 0) scales[sc] = scale;
     const float inv = 1.f / scale;
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
       const int row = row0 + i * kRowsPerPass;
-      if (row < rows) {
-        const uint4 w = x[s][i];
+      if (row < rows)
         *reinterpret_cast<uint2 *>(dst + row * rstride + part * 8) =
-            make_uint2(quantize4(w.x, w.y, inv), quantize4(w.z, w.w, inv));
-      }
+            make_uint2(quantize4(y[i].x, y[i].y, inv), quantize4(y[i].z, y[i].w, inv));
     }
-    if (threadIdx.x == 0) (s ? p.v_scale : p.k_scale)[sc] = scale;
+  };
+  for (int h = h0; h < h1; h += 2) {
+    if (h + 1 < h1) load(x[1], h + 1);
+    store(x[0], h);
+    if (h + 1 >= h1) break;
+    if (h + 2 < h1) load(x[0], h + 2);
+    store(x[1], h + 1);
   }
 }
 
@@ -256,7 +264,8 @@ struct GatherParams {
 
 // One CTA: a run (up to 64 positions of one group) of one head. Eight lanes read a row (16 codes
 // each) and write its 16 bf16.
-__global__ void __launch_bounds__(kRunThreads) kv_gather_fp8_kernel(const GatherParams p) {
+constexpr int kGatherThreads = 256;
+__global__ void __launch_bounds__(kGatherThreads) kv_gather_fp8_kernel(const GatherParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
@@ -276,7 +285,7 @@ __global__ void __launch_bounds__(kRunThreads) kv_gather_fp8_kernel(const Gather
                                p.num_blocks, p.err, threadIdx.x == 0 && h == 0);
   const int in_block = (int)(begin % p.block_size), rows = (int)(end - begin);
   const int part = threadIdx.x & 7, row0 = threadIdx.x >> 3;
-  constexpr int kPer = kRunThreads / 8;
+  constexpr int kPer = kGatherThreads / 8;
   uint4 x[2][kFp8Group / kPer];
   float scale[2] = {0.f, 0.f};
   const int64_t rstride = (int64_t)p.hkv * kD;
@@ -317,23 +326,6 @@ __global__ void __launch_bounds__(kRunThreads) kv_gather_fp8_kernel(const Gather
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Launch as a programmatic dependent of the stream's previous kernel (every kernel here waits
-// for it before it reads anything).
-template <class P>
-cudaError_t launch_after(void (*kernel)(P), int64_t grid, int threads, const P &prm,
-                         cudaStream_t stream) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, prm);
-}
 
 }  // namespace
 }  // namespace pkv
@@ -382,17 +374,26 @@ extern "C" pkv_status pkv_kv_store_fp8(const void *k, int64_t k_tok_stride, cons
   prm.block_size = block_size;
   prm.num_blocks = num_blocks;
   prm.err = err;
-  const int64_t units =
-      (cu_seqlens ? num_tokens / kFp8Group + 2 * (int64_t)num_seqs : (int64_t)num_seqs) *
-      num_kv_heads;
-  const int64_t grid = cu_seqlens ? units : (units + kTokenWarps - 1) / kTokenWarps;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!cu_seqlens) {
+    const int64_t units = (int64_t)num_seqs * num_kv_heads;
+    const int64_t grid = (units + kTokenWarps - 1) / kTokenWarps;
+    if (grid > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+    return launch_after(kv_store_fp8_token_kernel, grid, kTokenWarps * 32, st, prm) == cudaSuccess
+               ? PKV_OK
+               : PKV_ERR_CUDA;
+  }
+  // as many heads to a CTA as still leave every SM about ten CTAs
+  const int num_sms = current_sm_count();
+  const int64_t runs = num_tokens / kFp8Group + 2 * (int64_t)num_seqs;
+  const int64_t heads_per_cta = std::max<int64_t>(
+      1, std::min<int64_t>(num_kv_heads, 2 * runs * num_kv_heads / (10 * (int64_t)num_sms)));
+  const int64_t grid = 2 * runs * ((num_kv_heads + heads_per_cta - 1) / heads_per_cta);
   if (grid > INT32_MAX) return PKV_ERR_UNSUPPORTED;
-  const cudaError_t e =
-      cu_seqlens ? launch_after(kv_store_fp8_run_kernel, grid, kRunThreads, prm,
-                                static_cast<cudaStream_t>(stream))
-                 : launch_after(kv_store_fp8_token_kernel, grid, kTokenWarps * 32, prm,
-                                static_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  return launch_after(kv_store_fp8_run_kernel, grid, kRunThreads, st, prm, (int)heads_per_cta) ==
+                 cudaSuccess
+             ? PKV_OK
+             : PKV_ERR_CUDA;
 }
 
 extern "C" pkv_status pkv_kv_gather_fp8(const void *k_cache, const void *v_cache,
@@ -434,8 +435,8 @@ extern "C" pkv_status pkv_kv_gather_fp8(const void *k_cache, const void *v_cache
   prm.err = err;
   const int64_t grid = (total_k / kFp8Group + 2 * (int64_t)num_seqs) * num_kv_heads;
   if (grid > INT32_MAX) return PKV_ERR_UNSUPPORTED;
-  return launch_after(kv_gather_fp8_kernel, grid, kRunThreads, prm,
-                      static_cast<cudaStream_t>(stream)) == cudaSuccess
+  return launch_after(kv_gather_fp8_kernel, grid, kGatherThreads, static_cast<cudaStream_t>(stream),
+                      prm) == cudaSuccess
              ? PKV_OK
              : PKV_ERR_CUDA;
 }

@@ -126,6 +126,24 @@ inline PrefillWorkspace prefill_workspace_layout(int32_t num_seqs, int32_t max_s
 cudaError_t launch_varlen_prefill(const PrefillArgs &a, int num_sms, cudaStream_t stream);
 bool prefill_group_supported(int group);  // num_q_heads / num_kv_heads
 
+// Launch as a programmatic dependent of the stream's previous kernel: the launch overlaps that
+// kernel's tail. The kernel has to wait for it (griddepcontrol.wait) before it reads or writes
+// anything another kernel touches.
+template <class... Formal, class... Args>
+inline cudaError_t launch_after(void (*kernel)(Formal...), dim3 grid, int threads,
+                                cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // the current device's SM count and the address of the device error word (pkv_api.cu);
 // 0 / nullptr when the CUDA runtime cannot answer
 int current_sm_count();
