@@ -552,21 +552,18 @@ __global__ void __maxnreg__(96)
   // take what the rounding left, P - bf16(P), so that O is the same weights' sum: the second
   // product has the columns to spare.
   //
-  // 8-bit: warp w owns tokens [16w, 16w + 16) of every 128-token tile;
-  //   S   (16 x 16 tokens) = Q (16 x 128) K^T     e4m3 m16n8k32 on K's codes as they are, 4 steps
-  //                                               for each half of the tokens
-  //   O^T (16 dims x 8 heads) += V^T (16 x 16 tokens) P^T  fp16 m16n8k16 (e4m3 is a subset of it)
-  // Rows g and g + 8 of Q are the two parts of head g: with q' = q times the power of two that
-  // brings the head's maximum into [128, 256), hi = e4m3(q'), lo = e4m3(32 (q' - hi)): 4 + 4 bits
-  // hold bf16's 8, exactly down to 2^-14 of the maximum and within 2^-22 of it below. Converting
-  // K's codes to fp16 instead took 32 conversions (3.3 cycles of a sub-partition each) and
-  // twice the MMAs, at twice the cycles. K's scale multiplies the
+  // 8-bit: warp w owns tokens [16w, 16w + 16) of every 128-token tile. Codes become fp16 (e4m3
+  // is a subset of it) and the products are fp16 MMAs m16n8k16. K's scale multiplies the
   // scores, V's joins the exponent: with ev = log2 V's scale of the group and
   //   R = the largest s_i + ev_i so far,   w_i = 2^(s_i + ev_i - R + 15)
   // the second product is sum w_i code_i = 2^(15 - R) sum 2^(s_i) v_i and l sums w_i 2^-ev_i =
   // 2^(15 - R) 2^(s_i), in fp32. The largest term has w = 2^15 (below fp16's 65504), one
   // 2^-29 times smaller is still a normal fp16 number, and w's rounding to fp16 (2^-12) is
-  // under a tenth of the output's rounding to bf16.
+  // under a tenth of the output's rounding to bf16. q becomes fp16 after a power-of-two scaling
+  // of each head to a maximum in [8, 16): exact down to 2^-17 of the maximum, off by at most
+  // 2^-28 of it below. (e4m3 MMAs on the codes as they are, with q in two e4m3 parts on rows g
+  // and g + 8, were slower: mma.sync has no e4m3 unit here, each one converts both operands to
+  // fp16 -- 104 us against 97 us for 256 ragged contexts.)
   const int gq = lane >> 2, tq = lane & 3;
   const int tok = FP8 ? warp * 16 + 2 * tq : warp * 8 + 2 * tq;  // tile-relative: S column 2tq
   // ldmatrix row addresses. bf16: lanes 8i..8i+7 give matrix i of load j = dims chunk 4j + i of
@@ -599,9 +596,8 @@ __global__ void __maxnreg__(96)
     float qscale = p.qscale;
     // bf16: q's A fragments, held in registers for the unit: load j gives dims [32j, 32j + 32)
     // as a0, a2 of k-step 2j and a0, a2 of k-step 2j + 1 (rows 8-15, a1 and a3, are zero).
-    // 8-bit: k-step j takes dims [32j, 32j + 32); a0, a1 are the hi and lo codes of dims 32j +
-    // 4tq .. + 3, a2, a3 of dims 32j + 16 + 4tq .. + 3, as a lane's word of an ldmatrix row
-    // holds four codes of K.
+    // 8-bit: k-step c takes dims [16c, 16c + 16); the lane's a0, a2 are dims 16c + 4tq .. + 3,
+    // as a lane's word of an ldmatrix row holds four codes of K.
     uint32_t qa[4][4];
     if constexpr (FP8) {
       uint2 qw[8];
@@ -615,22 +611,13 @@ __global__ void __maxnreg__(96)
       }
       top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
       top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
-      const int e = min(max((int)(__float_as_uint(top) >> 23), 8), 254);  // 2^(e - 127) <= top
-      const float up = __uint_as_float((uint32_t)(261 - e) << 23);        // 2^(134 - e)
-      // 1 / up; an infinite q makes every score of its head NaN
-      qscale *= isinf(top) ? __uint_as_float(0x7fffffffu)
-                           : __uint_as_float((uint32_t)(e - 7) << 23);
+      const int e = min(max((int)(__float_as_uint(top) >> 23), 4), 254);  // 2^(e - 127) <= top
+      const float up = __uint_as_float((uint32_t)(257 - e) << 23);        // 2^(130 - e)
+      qscale *= __uint_as_float((uint32_t)(e - 3) << 23);                 // 1 / up
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        const float x[4] = {bf16_lo(qw[c].x) * up, bf16_hi(qw[c].x) * up, bf16_lo(qw[c].y) * up,
-                            bf16_hi(qw[c].y) * up};
-        const uint32_t hi = cvt_e4m3x2(x[0], x[1]) | (cvt_e4m3x2(x[2], x[3]) << 16);
-        const float2 r0 = f16x2_to_f32(cvt_f16x2_e4m3x2(hi));
-        const float2 r1 = f16x2_to_f32(cvt_f16x2_e4m3x2_hi(hi));
-        qa[c >> 1][2 * (c & 1)] = hi;
-        qa[c >> 1][2 * (c & 1) + 1] =
-            cvt_e4m3x2((x[0] - r0.x) * 32.f, (x[1] - r0.y) * 32.f) |
-            (cvt_e4m3x2((x[2] - r1.x) * 32.f, (x[3] - r1.y) * 32.f) << 16);
+        qa[c >> 1][2 * (c & 1)] = pack_f16x2(bf16_lo(qw[c].x) * up, bf16_hi(qw[c].x) * up);
+        qa[c >> 1][2 * (c & 1) + 1] = pack_f16x2(bf16_lo(qw[c].y) * up, bf16_hi(qw[c].y) * up);
       }
     } else {
       const uint32_t q_base =
@@ -705,11 +692,17 @@ __global__ void __maxnreg__(96)
         // ---- S = Q K^T for the warp's 16 tokens: columns 0-7 and 8-15
         float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {  // dims [32j, 32j + 32)
+        for (int j = 0; j < 4; ++j) {  // dims [32j, 32j + 32): two k-steps
           uint32_t kb[4];
           ldsm_x4(kt + off_ld[j], kb);
-          mma_e4m3_16832(s0, qa[j][0], qa[j][1], qa[j][2], qa[j][3], kb[0], kb[2]);
-          mma_e4m3_16832(s1, qa[j][0], qa[j][1], qa[j][2], qa[j][3], kb[1], kb[3]);
+          mma_f16_16816(s0, qa[j][0], 0u, qa[j][1], 0u, cvt_f16x2_e4m3x2(kb[0]),
+                        cvt_f16x2_e4m3x2_hi(kb[0]));
+          mma_f16_16816(s1, qa[j][0], 0u, qa[j][1], 0u, cvt_f16x2_e4m3x2(kb[1]),
+                        cvt_f16x2_e4m3x2_hi(kb[1]));
+          mma_f16_16816(s0, qa[j][2], 0u, qa[j][3], 0u, cvt_f16x2_e4m3x2(kb[2]),
+                        cvt_f16x2_e4m3x2_hi(kb[2]));
+          mma_f16_16816(s1, qa[j][2], 0u, qa[j][3], 0u, cvt_f16x2_e4m3x2(kb[3]),
+                        cvt_f16x2_e4m3x2_hi(kb[3]));
         }
         // vb[4j + 2c + t]: dims chunk 2j + c of tokens 16w + 8t .. + 7, transposed: the lane's
         // word is dims 2gq, 2gq + 1 of token 2tq, then of token 2tq + 1
@@ -717,9 +710,7 @@ __global__ void __maxnreg__(96)
 #pragma unroll
         for (int j = 0; j < 4; ++j) ldsm_x4_trans(vt + off_ld[j], &vb[4 * j]);
 
-        constexpr float kLo = 1.f / 32.f;
-        float s[4] = {fmaf(s0[2], kLo, s0[0]) * ks, fmaf(s0[3], kLo, s0[1]) * ks,
-                      fmaf(s1[2], kLo, s1[0]) * ks, fmaf(s1[3], kLo, s1[1]) * ks};
+        float s[4] = {s0[0] * ks, s0[1] * ks, s1[0] * ks, s1[1] * ks};
         if (W && score_row) {
           float *dst = score_row + tok_begin + it * kTile + tok;
           *reinterpret_cast<float2 *>(dst) = make_float2(s[0], s[1]);

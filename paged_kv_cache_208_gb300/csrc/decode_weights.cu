@@ -22,7 +22,7 @@ namespace pkv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPerThread = 4;
+constexpr int kPerThread = 8;
 constexpr int kSpan = kThreads * kPerThread;  // positions of a CTA
 
 struct WeightsParams {
@@ -49,7 +49,12 @@ __global__ void __launch_bounds__(kThreads) decode_weights_kernel(const WeightsP
   L = L < 0 ? 0 : min(L, p.cap);
   for (int64_t i0 = (int64_t)blockIdx.y * kSpan + threadIdx.x; i0 < L;
        i0 += (int64_t)gridDim.y * kSpan) {
-    float w[kPerThread] = {};
+    float before[kPerThread], w[kPerThread] = {};
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j) {
+      const int64_t i = i0 + j * kThreads;
+      before[j] = p.in && i < L ? p.in[bh * p.in_stride + i] : 0.f;
+    }
     const float *s = p.scores + bh * p.group * p.score_stride;
     for (int g = 0; g < p.group; ++g, s += p.score_stride) {
       const float lse = p.lse[bh * p.group + g];
@@ -62,7 +67,7 @@ __global__ void __launch_bounds__(kThreads) decode_weights_kernel(const WeightsP
 #pragma unroll
     for (int j = 0; j < kPerThread; ++j) {
       const int64_t i = i0 + j * kThreads;
-      if (i < L) p.out[bh * p.out_stride + i] = (p.in ? p.in[bh * p.in_stride + i] : 0.f) + w[j];
+      if (i < L) p.out[bh * p.out_stride + i] = before[j] + w[j];
     }
   }
 }

@@ -57,7 +57,11 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kPer = 4;  // elements of a thread in the ordered pass
+constexpr int kChunk = 4 * kSelThreads;  // a thread's four consecutive elements, of every thread
+// Chunks whose elements stay in registers between the passes: rows of up to 32768 are loaded
+// once, all of a thread's loads in flight together (128 rows of 32768: XX us, 36 us when every
+// pass read its elements one by one); a longer row's other chunks are loaded again by each pass.
+constexpr int kHeld = 8;
 
 // Inclusive sum over the warp's lanes up to this one.
 __device__ __forceinline__ uint32_t warp_scan(uint32_t x, int lane) {
@@ -104,6 +108,27 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
   int32_t *kept = p.kept + bh * p.budget;
   float *w_out = p.weights_out ? p.weights_out + bh * p.weights_out_stride : nullptr;
 
+  const int32_t len = bad ? 0 : L;
+  // elements [i, i + 4) of the row, i a multiple of 4 (zeros past the row)
+  const bool vec = (reinterpret_cast<uintptr_t>(w) & 15u) == 0;
+  auto load4 = [&](int64_t i) {
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (vec && i + 4 <= len) {
+      x = *reinterpret_cast<const float4 *>(w + i);
+    } else {
+      if (i < len) x.x = w[i];
+      if (i + 1 < len) x.y = w[i + 1];
+      if (i + 2 < len) x.z = w[i + 2];
+      if (i + 3 < len) x.w = w[i + 3];
+    }
+    return x;
+  };
+  const int64_t mine = 4 * (int64_t)threadIdx.x;
+  float4 held[kHeld];
+#pragma unroll
+  for (int c = 0; c < kHeld; ++c)
+    held[c] = c * kChunk < len ? load4(c * (int64_t)kChunk + mine) : make_float4(0.f, 0.f, 0.f, 0.f);
+
   // the smallest key that is kept among the positions below `older`, and how many of its equals
   // (with L <= budget every position is kept)
   const int32_t older = L > p.budget ? L - p.recent : 0;
@@ -119,9 +144,25 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
         const uint32_t digit = pass == 2 ? 1023u : 2047u;
         for (int i = threadIdx.x; i < kBins; i += kSelThreads) hist[i] = 0u;
         __syncthreads();
-        for (int64_t i = threadIdx.x; i < older; i += kSelThreads) {
-          const uint32_t key = ordered(w[i]);
-          if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & digit], 1u);
+        auto count = [&](float v, int64_t i) {
+          const uint32_t key = ordered(v);
+          if (i < older && (key & mask) == prefix) atomicAdd(&hist[(key >> shift) & digit], 1u);
+        };
+        auto count4 = [&](const float4 &x, int64_t i) {
+          count(x.x, i);
+          count(x.y, i + 1);
+          count(x.z, i + 2);
+          count(x.w, i + 3);
+        };
+#pragma unroll
+        for (int c = 0; c < kHeld; ++c)
+          if (c * kChunk < older) count4(held[c], c * (int64_t)kChunk + mine);
+        for (int64_t base = (int64_t)kHeld * kChunk; base < older; base += 4 * kChunk) {
+          float4 x[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) x[c] = load4(base + c * (int64_t)kChunk + mine);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) count4(x[c], base + c * (int64_t)kChunk + mine);
         }
         __syncthreads();
         // thread t owns bins 2t, 2t + 1 counted from the top
@@ -148,31 +189,26 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
   // the first `equals` of those, or if it is recent
   uint32_t above0 = 0u, equal0 = 0u;  // so far
   int buf = 0;
-  for (int64_t base = 0; base < (bad ? 0 : L); base += kSelThreads * kPer, buf ^= 1) {
-    float x[kPer];
-    uint32_t cnt = 0u, is_eq = 0u, is_above = 0u;
+  auto emit = [&](const float4 &x4, int64_t i0) {
+    const float x[4] = {x4.x, x4.y, x4.z, x4.w};
+    uint32_t is_eq = 0u, is_above = 0u;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int64_t i = base + threadIdx.x * kPer + j;
-      x[j] = i < L ? w[i] : 0.f;
-    }
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int64_t i = base + threadIdx.x * kPer + j;
+    for (int j = 0; j < 4; ++j) {
+      const int64_t i = i0 + j;
       const uint32_t key = ordered(x[j]);
-      if (i < L && (i >= older || key > threshold)) is_above |= 1u << j;
-      else if (i < L && key == threshold && equals) is_eq |= 1u << j;
+      if (i < len && (i >= older || key > threshold)) is_above |= 1u << j;
+      else if (i < len && key == threshold && equals) is_eq |= 1u << j;
     }
-    cnt = __popc(is_above) << 16 | __popc(is_eq);
     uint32_t total;
-    const uint32_t ex = block_scan(cnt, sums[buf], total);
+    const uint32_t ex = block_scan(__popc(is_above) << 16 | __popc(is_eq), sums[buf], total);
+    buf ^= 1;
     uint32_t a = above0 + (ex >> 16), e = equal0 + (ex & 0xffffu);
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
+    for (int j = 0; j < 4; ++j) {
       const bool ab = is_above >> j & 1u, eq = is_eq >> j & 1u;
       if (ab || (eq && e < equals)) {
         const uint32_t at = a + min(e, equals);
-        kept[at] = (int32_t)(base + threadIdx.x * kPer + j);
+        kept[at] = (int32_t)(i0 + j);
         if (w_out) w_out[at] = x[j];
       }
       a += ab;
@@ -180,7 +216,12 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
     }
     above0 += total >> 16;
     equal0 += total & 0xffffu;
-  }
+  };
+#pragma unroll
+  for (int c = 0; c < kHeld; ++c)
+    if (c * kChunk < len) emit(held[c], c * (int64_t)kChunk + mine);
+  for (int64_t base = (int64_t)kHeld * kChunk; base < len; base += kChunk)
+    emit(load4(base + mine), base + mine);
   for (int64_t j = n + (int64_t)threadIdx.x; j < p.budget; j += kSelThreads) {
     kept[j] = -1;
     if (w_out) w_out[j] = 0.f;

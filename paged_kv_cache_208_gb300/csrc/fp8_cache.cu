@@ -262,64 +262,64 @@ struct GatherParams {
   unsigned int *err;
 };
 
-// One CTA: a run (up to 64 positions of one group) of one head. Eight lanes read a row (16 codes
-// each) and write its 16 bf16.
+// One CTA: K or V of `rows_per_cta` rows of a run (up to 64 positions of one group), all heads: the
+// rows are read and written whole (hkv x 128 bytes in, twice that out), 16 codes to a lane, eight
+// loads of a thread in flight.
 constexpr int kGatherThreads = 256;
-__global__ void __launch_bounds__(kGatherThreads) kv_gather_fp8_kernel(const GatherParams p) {
+constexpr int kGatherLoads = 8;
+__global__ void __launch_bounds__(kGatherThreads)
+    kv_gather_fp8_kernel(const GatherParams p, int rows_per_cta) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
-  const int64_t r = blockIdx.x / p.hkv;
-  const int h = (int)(blockIdx.x % p.hkv);
+  const int parts = kFp8Group / rows_per_cta;
+  const bool is_v = blockIdx.x & 1;
+  const int64_t r = (blockIdx.x >> 1) / parts;
+  const int row_from = (int)((blockIdx.x >> 1) % parts) * rows_per_cta;
   const int n = find_sequence(p.cu, p.num_seqs, r, lane);
-  const int32_t c0 = *(p.cu + n), c1 = *(p.cu + n + 1);
+  const int32_t c0 = p.cu[n], c1 = p.cu[n + 1];
   const int64_t j = r - run_base(c0, n);
   const int64_t capacity = (int64_t)p.table_width * p.block_size;
   if (blockIdx.x == 0)
     check_lengths<false>(p.cu, nullptr, p.num_seqs, p.total, capacity, p.err);
   const int64_t len = (int64_t)c1 - c0;
   if (c0 < 0 || len < 0 || c1 > p.total || len > capacity) return;
-  const int64_t begin = j * kFp8Group, end = min(len, begin + kFp8Group);
-  if (j < 0 || begin >= end || aborted(p.err)) return;
+  const int64_t begin = j * kFp8Group + row_from;
+  if (j < 0 || begin >= len || aborted(p.err)) return;
+  const int rows = (int)min(len - begin, (int64_t)rows_per_cta);
   const int64_t blk = block_of(p.block_table + (int64_t)n * p.table_width, begin, p.block_size,
-                               p.num_blocks, p.err, threadIdx.x == 0 && h == 0);
-  const int in_block = (int)(begin % p.block_size), rows = (int)(end - begin);
-  const int part = threadIdx.x & 7, row0 = threadIdx.x >> 3;
-  constexpr int kPer = kGatherThreads / 8;
-  uint4 x[2][kFp8Group / kPer];
-  float scale[2] = {0.f, 0.f};
+                               p.num_blocks, p.err, threadIdx.x == 0);
+  const int in_block = (int)(begin % p.block_size), groups = p.block_size / kFp8Group;
   const int64_t rstride = (int64_t)p.hkv * kD;
+  const uint4 *const src = reinterpret_cast<const uint4 *>(
+      (is_v ? p.v_cache : p.k_cache) + (blk * p.block_size + in_block) * rstride);
+  const float *const scales =
+      (is_v ? p.v_scale : p.k_scale) + blk * p.hkv * groups + in_block / kFp8Group;
+  uint4 *const dst =
+      reinterpret_cast<uint4 *>((is_v ? p.v_out : p.k_out) + (c0 + begin) * rstride * 2);
+  const uint32_t cols = (uint32_t)p.hkv * 8u;  // 16-byte pieces of a row, 8 to a head
+  const uint32_t all = (uint32_t)rows * cols;
+  for (uint32_t u0 = threadIdx.x; u0 < all; u0 += kGatherThreads * kGatherLoads) {
+    uint4 x[kGatherLoads];
+    float scale[kGatherLoads];
 #pragma unroll
-  for (int s = 0; s < 2; ++s)
-#pragma unroll
-    for (int i = 0; i < kFp8Group / kPer; ++i) x[s][i] = make_uint4(0, 0, 0, 0);
-  if (blk >= 0) {  // the rows of a bad block id are zeros, as in the attention kernels
-    const int64_t sc = (blk * p.hkv + h) * (p.block_size / kFp8Group) + in_block / kFp8Group;
-    scale[0] = *(p.k_scale + sc);
-    scale[1] = *(p.v_scale + sc);
-    const int64_t at = (blk * p.block_size + in_block) * rstride + h * kD + part * 16;
-#pragma unroll
-    for (int i = 0; i < kFp8Group / kPer; ++i) {
-      const int row = row0 + i * kPer;
-      if (row < rows) {
-        x[0][i] = ld_once_u4(reinterpret_cast<const uint4 *>(p.k_cache + at + row * rstride));
-        x[1][i] = ld_once_u4(reinterpret_cast<const uint4 *>(p.v_cache + at + row * rstride));
+    for (int i = 0; i < kGatherLoads; ++i) {
+      const uint32_t u = u0 + i * kGatherThreads;
+      x[i] = make_uint4(0, 0, 0, 0);  // the rows of a bad block id are zeros, as in attention
+      scale[i] = 0.f;
+      if (u < all && blk >= 0) {
+        x[i] = ld_once_u4(src + u);
+        scale[i] = scales[(int64_t)((u % cols) >> 3) * groups];
       }
     }
-  }
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    uint8_t *out = (s ? p.v_out : p.k_out) + ((c0 + begin) * rstride + h * kD + part * 16) * 2;
-#pragma unroll
-    for (int i = 0; i < kFp8Group / kPer; ++i) {
-      const int row = row0 + i * kPer;
-      if (row < rows) {
-        const uint4 w = x[s][i];
-        const uint2 a = dequantize4(w.x, scale[s]), b = dequantize4(w.y, scale[s]);
-        const uint2 c = dequantize4(w.z, scale[s]), d = dequantize4(w.w, scale[s]);
-        uint4 *q = reinterpret_cast<uint4 *>(out + row * rstride * 2);
-        q[0] = make_uint4(a.x, a.y, b.x, b.y);
-        q[1] = make_uint4(c.x, c.y, d.x, d.y);
+    for (int i = 0; i < kGatherLoads; ++i) {
+      const uint32_t u = u0 + i * kGatherThreads;
+      if (u < all) {
+        const uint2 a = dequantize4(x[i].x, scale[i]), b = dequantize4(x[i].y, scale[i]);
+        const uint2 c = dequantize4(x[i].z, scale[i]), d = dequantize4(x[i].w, scale[i]);
+        dst[2 * (int64_t)u] = make_uint4(a.x, a.y, b.x, b.y);
+        dst[2 * (int64_t)u + 1] = make_uint4(c.x, c.y, d.x, d.y);
       }
     }
   }
@@ -384,10 +384,10 @@ extern "C" pkv_status pkv_kv_store_fp8(const void *k, int64_t k_tok_stride, cons
                : PKV_ERR_CUDA;
   }
   // as many heads to a CTA as still leave every SM about ten CTAs
-  const int num_sms = current_sm_count();
   const int64_t runs = num_tokens / kFp8Group + 2 * (int64_t)num_seqs;
-  const int64_t heads_per_cta = std::max<int64_t>(
-      1, std::min<int64_t>(num_kv_heads, 2 * runs * num_kv_heads / (10 * (int64_t)num_sms)));
+  const int64_t heads_per_cta =
+      std::max<int64_t>(1, std::min<int64_t>(num_kv_heads, 2 * runs * num_kv_heads /
+                                                               (10 * (int64_t)current_sm_count())));
   const int64_t grid = 2 * runs * ((num_kv_heads + heads_per_cta - 1) / heads_per_cta);
   if (grid > INT32_MAX) return PKV_ERR_UNSUPPORTED;
   return launch_after(kv_store_fp8_run_kernel, grid, kRunThreads, st, prm, (int)heads_per_cta) ==
@@ -433,10 +433,15 @@ extern "C" pkv_status pkv_kv_gather_fp8(const void *k_cache, const void *v_cache
   prm.block_size = block_size;
   prm.num_blocks = num_blocks;
   prm.err = err;
-  const int64_t grid = (total_k / kFp8Group + 2 * (int64_t)num_seqs) * num_kv_heads;
-  if (grid > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+  // runs in parts of fewer rows while there are less than about ten CTAs for an SM
+  const int64_t runs = total_k / kFp8Group + 2 * (int64_t)num_seqs;
+  int rows_per_cta = kFp8Group;
+  while (rows_per_cta > 8 && 2 * runs * (kFp8Group / rows_per_cta) < 10 * (int64_t)current_sm_count())
+    rows_per_cta /= 2;
+  const int64_t grid = 2 * runs * (kFp8Group / rows_per_cta);
+  if (grid > INT32_MAX || num_kv_heads > (1 << 20)) return PKV_ERR_UNSUPPORTED;
   return launch_after(kv_gather_fp8_kernel, grid, kGatherThreads, static_cast<cudaStream_t>(stream),
-                      prm) == cudaSuccess
+                      prm, rows_per_cta) == cudaSuccess
              ? PKV_OK
              : PKV_ERR_CUDA;
 }

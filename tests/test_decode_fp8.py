@@ -4,9 +4,8 @@ against softmax attention in 64 bits over the cache's own values.
 Tolerances, from the arithmetic (u16 = 2^-11 and ub = 2^-8 are half steps of fp16 and bf16, u =
 2^-24 of fp32):
   scores   products are exact, the sum of 128 and the scaling round in fp32: |ds| <= 140 u A with
-           A = scale log2(e) sum |q_d k_d| in the log2 domain; q's form in two e4m3 parts is off by
-           at most 2^-22 max|q| per dimension (8 bits of q' in [128, 256): the low part, scaled
-           by 32, has a spacing of 2^-9, so q' is off by 2^-10 / 32 = 2^-15)
+           A = scale log2(e) sum |q_d k_d| in the log2 domain, q's fp16 form adds 2^-28 max|q|
+           per term, below that
   weights  relative 2 ln2 max|ds| + rounding of the log-sum-exp and of the approximate exp2 and
            log2 (2^-22 each, |lse| u): e_w
   output   (ub |ref| + (u16 + e_w) sum p |v|) (the 8-bit kernel rounds each weight to fp16, the
@@ -86,7 +85,7 @@ class Case:
                 c = SCALE * np.log2(np.e)
                 x = c * (k[:, h] @ self.q[b, hq])
                 A = c * np.abs(k[:, h]) @ np.abs(self.q[b, hq])
-                ds = 140 * U * A.max() + 2.0 ** -22 * c * np.abs(self.q[b, hq]).max() * \
+                ds = 140 * U * A.max() + 2.0 ** -28 * c * np.abs(self.q[b, hq]).max() * \
                     np.abs(k[:, h]).sum(1).max()
                 top = x.max()
                 p = np.exp2(x - top)
