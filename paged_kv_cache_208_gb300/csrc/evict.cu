@@ -7,9 +7,9 @@
 // with other sequences, or registered in the prefix cache, keep their contents.
 //
 // Two kernels. evict_select_kernel, one CTA per (sequence, head): a radix select over the
-// weights' ordered bits (11 + 11 + 10, histograms in shared memory; the weights are read again
-// per pass, from L2) finds the smallest kept key and how many of its equals are kept, then one
-// ordered pass with block-wide prefix sums writes the kept positions and their weights.
+// weights' ordered bits (11 + 11 + 10, histograms in shared memory) finds the smallest kept key
+// and how many of its equals are kept, then one ordered pass with prefix sums writes the kept
+// positions and their weights.
 // evict_copy_kernel, one CTA per (sequence, 64 kept rows, head), moves the K and V rows; it is
 // bound by HBM: each kept row is read once and written once. In an 8-bit cache the 64 rows are
 // one group of the destination, whose scale is the largest of its rows' scales (powers of two:
@@ -48,20 +48,30 @@ struct EvictParams {
 };
 
 // Bits that order like the numbers (NaN first, -0 equal to +0).
-__device__ __forceinline__ uint32_t ordered(float x) {
-  if (x != x) return 0u;
-  const uint32_t b = __float_as_uint(x + 0.f);
-  return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
+__device__ __forceinline__ uint32_t ordered(uint32_t b) {
+  const uint32_t mag = b & 0x7fffffffu;
+  if (mag == 0u) b = 0u;
+  const uint32_t key = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+  return mag > 0x7f800000u ? 0u : key;
+}
+
+// The number with these bits (key 0: NaN).
+__device__ __forceinline__ float number(uint32_t key) {
+  if (key == 0u) return __uint_as_float(0x7fffffffu);
+  return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kChunk = 4 * kSelThreads;  // a thread's four consecutive elements, of every thread
-// Chunks whose elements stay in registers between the passes: rows of up to 32768 are loaded
-// once, all of a thread's loads in flight together (128 rows of 32768: XX us, 36 us when every
-// pass read its elements one by one); a longer row's other chunks are loaded again by each pass.
+// A warp's part of a row, up to kHeld chunks of 128 elements, stays in its lanes' registers as
+// ordered keys, so a row of up to 32768 weights is loaded once, all loads in flight together; a
+// longer row is taken in pieces of 32768 that each pass loads again. What bounds the kernel is
+// its instructions (128 rows of 32768: XX us; 28 us when every element compared 64-bit
+// positions and mapped its key again in every pass, 36 us with the elements loaded one by one).
 constexpr int kHeld = 8;
+constexpr int kPiece = kHeld * 128 * kSelWarps;
+constexpr uint32_t kTopKey = 0xffffffffu;  // a recent position's: above every number's
 
 // Inclusive sum over the warp's lanes up to this one.
 __device__ __forceinline__ uint32_t warp_scan(uint32_t x, int lane) {
@@ -108,120 +118,139 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
   int32_t *kept = p.kept + bh * p.budget;
   float *w_out = p.weights_out ? p.weights_out + bh * p.weights_out_stride : nullptr;
 
-  const int32_t len = bad ? 0 : L;
-  // elements [i, i + 4) of the row, i a multiple of 4 (zeros past the row)
-  const bool vec = (reinterpret_cast<uintptr_t>(w) & 15u) == 0;
-  auto load4 = [&](int64_t i) {
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (vec && i + 4 <= len) {
-      x = *reinterpret_cast<const float4 *>(w + i);
-    } else {
-      if (i < len) x.x = w[i];
-      if (i + 1 < len) x.y = w[i + 1];
-      if (i + 2 < len) x.z = w[i + 2];
-      if (i + 3 < len) x.w = w[i + 3];
-    }
-    return x;
-  };
-  const int64_t mine = 4 * (int64_t)threadIdx.x;
-  float4 held[kHeld];
-#pragma unroll
-  for (int c = 0; c < kHeld; ++c)
-    held[c] = c * kChunk < len ? load4(c * (int64_t)kChunk + mine) : make_float4(0.f, 0.f, 0.f, 0.f);
-
-  // the smallest key that is kept among the positions below `older`, and how many of its equals
-  // (with L <= budget every position is kept)
-  const int32_t older = L > p.budget ? L - p.recent : 0;
-  uint32_t threshold = 0u, equals = 0u;
-  if (!bad && older > 0) {
-    uint32_t want = (uint32_t)(p.budget - p.recent);  // of the keys that share `prefix`
-    uint32_t prefix = 0u, mask = 0u;
-    if (want == 0) {
-      threshold = 0xffffffffu;  // (no number has this key: nothing older is kept)
-    } else {
-      for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-        const uint32_t digit = pass == 2 ? 1023u : 2047u;
-        for (int i = threadIdx.x; i < kBins; i += kSelThreads) hist[i] = 0u;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (L > p.budget && !bad) {
+    const uint32_t len = (uint32_t)L, older = (uint32_t)(L - p.recent);
+    const bool vec = (reinterpret_cast<uintptr_t>(w) & 15u) == 0;
+    const uint32_t pieces = (len + kPiece - 1) / kPiece;
+    uint32_t key[kHeld][4];
+    uint32_t want = (uint32_t)p.budget;  // still to be kept, of the keys that share `prefix`
+    uint32_t prefix = 0u;
+    uint32_t above0 = 0u, equal0 = 0u;   // last pass: kept in the pieces before
+    // Passes 0-2 count the keys' digits and find the smallest kept key, `prefix` in the end, and
+    // how many of its equals are kept, `want`. Pass 3 writes, in order: a larger key is kept, an
+    // equal one if it is among the first `want`. (One loop: the code of a pass per pass did not
+    // fit the instruction cache.)
+#pragma unroll 1
+    for (int pass = 0; pass < 4; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+      const uint32_t digit = pass == 2 ? 1023u : 2047u;
+      const uint32_t mask = pass == 0 ? 0u : pass == 1 ? 0xffe00000u : 0xfffffc00u;
+      if (pass < 3) {
+        hist[threadIdx.x] = hist[threadIdx.x + kSelThreads] = 0u;
         __syncthreads();
-        auto count = [&](float v, int64_t i) {
-          const uint32_t key = ordered(v);
-          if (i < older && (key & mask) == prefix) atomicAdd(&hist[(key >> shift) & digit], 1u);
-        };
-        auto count4 = [&](const float4 &x, int64_t i) {
-          count(x.x, i);
-          count(x.y, i + 1);
-          count(x.z, i + 2);
-          count(x.w, i + 3);
-        };
-#pragma unroll
-        for (int c = 0; c < kHeld; ++c)
-          if (c * kChunk < older) count4(held[c], c * (int64_t)kChunk + mine);
-        for (int64_t base = (int64_t)kHeld * kChunk; base < older; base += 4 * kChunk) {
-          float4 x[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) x[c] = load4(base + c * (int64_t)kChunk + mine);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) count4(x[c], base + c * (int64_t)kChunk + mine);
-        }
-        __syncthreads();
-        // thread t owns bins 2t, 2t + 1 counted from the top
-        const int hi = kBins - 1 - 2 * threadIdx.x;
-        const uint32_t c0 = hist[hi], c1 = hist[hi - 1];
-        uint32_t total;
-        const uint32_t above = block_scan(c0 + c1, sums[0], total);
-        if (above < want && want <= above + c0 + c1) {
-          const bool first = want <= above + c0;
-          found_bin = (uint32_t)(first ? hi : hi - 1);
-          found_above = first ? above : above + c0;
-        }
-        __syncthreads();
-        want -= found_above;
-        prefix |= found_bin << shift;
-        mask |= digit << shift;
       }
-      threshold = prefix;
-      equals = want;
+#pragma unroll 1
+      for (uint32_t piece = 0; piece < pieces; ++piece) {
+        const uint32_t base = piece * kPiece;
+        const uint32_t in_piece = min(len - base, (uint32_t)kPiece);
+        const int chunks = (int)((in_piece + 128 * kSelWarps - 1) / (128 * kSelWarps));
+        const uint32_t at0 = base + (uint32_t)(warp * chunks * 128 + lane * 4);
+        if (pass == 0 || pieces > 1) {
+          // The keys: recent positions get the top one, what lies past the row the lowest (0, a
+          // NaN's: it is never kept, the row has `budget` elements at lower positions).
+#pragma unroll
+          for (int c = 0; c < kHeld; ++c) {
+            const uint32_t i = at0 + c * 128;
+            if (vec && c < chunks && i + 4 <= len) {
+              const uint4 x = *reinterpret_cast<const uint4 *>(w + i);
+              key[c][0] = x.x;
+              key[c][1] = x.y;
+              key[c][2] = x.z;
+              key[c][3] = x.w;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                key[c][e] = c < chunks && i + e < len ? __float_as_uint(w[i + e]) : 0x7fffffffu;
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < kHeld; ++c) {
+            const uint32_t i = at0 + c * 128;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              key[c][e] = ordered(key[c][e]);
+              if (i + e >= older && i + e < len && c < chunks) key[c][e] = kTopKey;
+            }
+          }
+        }
+        if (pass < 3) {
+#pragma unroll
+          for (int c = 0; c < kHeld; ++c) {
+            if (c >= chunks) break;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if ((key[c][e] & mask) == prefix) atomicAdd(&hist[(key[c][e] >> shift) & digit], 1u);
+          }
+          continue;
+        }
+        // each warp counts its keys, the block sums the counts up, then each warp walks its chunks
+        uint32_t cnt[kHeld], mine = 0u;  // larger in the upper half, equal in the lower
+#pragma unroll
+        for (int c = 0; c < kHeld; ++c) {
+          cnt[c] = 0u;
+          if (c >= chunks) continue;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            cnt[c] += key[c][e] > prefix ? 0x10000u : key[c][e] == prefix ? 1u : 0u;
+          mine += cnt[c];
+        }
+        mine = __reduce_add_sync(kFull, mine);  // (at most 1024 of each)
+        __syncthreads();  // the sums of the step before have been read
+        if (lane == 0) {
+          sums[0][warp] = mine >> 16;
+          sums[1][warp] = mine & 0xffffu;
+        }
+        __syncthreads();
+        const uint32_t sa = warp_scan(sums[0][lane], lane), se = warp_scan(sums[1][lane], lane);
+        const uint32_t pa = __shfl_sync(kFull, sa, max(warp - 1, 0));
+        const uint32_t pe = __shfl_sync(kFull, se, max(warp - 1, 0));
+        uint32_t a = above0 + (warp ? pa : 0u), q = equal0 + (warp ? pe : 0u);
+        above0 += __shfl_sync(kFull, sa, 31);
+        equal0 += __shfl_sync(kFull, se, 31);
+#pragma unroll
+        for (int c = 0; c < kHeld; ++c) {
+          if (c >= chunks) break;
+          const uint32_t inc = warp_scan(cnt[c], lane);
+          const uint32_t all = __shfl_sync(kFull, inc, 31);
+          uint32_t la = a + ((inc - cnt[c]) >> 16), le = q + ((inc - cnt[c]) & 0xffffu);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t k = key[c][e];
+            if (k > prefix || (k == prefix && le < want)) {
+              const uint32_t at = la + min(le, want), i = at0 + c * 128 + e;
+              kept[at] = (int32_t)i;
+              if (w_out) w_out[at] = k == kTopKey ? w[i] : number(k);
+            }
+            la += k > prefix;
+            le += k == prefix;
+          }
+          a += all >> 16;
+          q += all & 0xffffu;
+        }
+      }
+      if (pass == 3) break;
+      __syncthreads();
+      // thread t owns bins 2t, 2t + 1 counted from the top
+      const int hi = kBins - 1 - 2 * threadIdx.x;
+      const uint32_t c0 = hist[hi], c1 = hist[hi - 1];
+      uint32_t total;
+      const uint32_t above = block_scan(c0 + c1, sums[0], total);
+      if (above < want && want <= above + c0 + c1) {
+        const bool upper = want <= above + c0;
+        found_bin = (uint32_t)(upper ? hi : hi - 1);
+        found_above = upper ? above : above + c0;
+      }
+      __syncthreads();
+      want -= found_above;
+      prefix |= found_bin << shift;
+    }
+  } else {
+    for (int64_t j = threadIdx.x; j < n; j += kSelThreads) {
+      kept[j] = (int32_t)j;
+      if (w_out) w_out[j] = w[j];
     }
   }
-
-  // the ordered pass: position i is kept if its key is above the threshold, or equal and among
-  // the first `equals` of those, or if it is recent
-  uint32_t above0 = 0u, equal0 = 0u;  // so far
-  int buf = 0;
-  auto emit = [&](const float4 &x4, int64_t i0) {
-    const float x[4] = {x4.x, x4.y, x4.z, x4.w};
-    uint32_t is_eq = 0u, is_above = 0u;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t i = i0 + j;
-      const uint32_t key = ordered(x[j]);
-      if (i < len && (i >= older || key > threshold)) is_above |= 1u << j;
-      else if (i < len && key == threshold && equals) is_eq |= 1u << j;
-    }
-    uint32_t total;
-    const uint32_t ex = block_scan(__popc(is_above) << 16 | __popc(is_eq), sums[buf], total);
-    buf ^= 1;
-    uint32_t a = above0 + (ex >> 16), e = equal0 + (ex & 0xffffu);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const bool ab = is_above >> j & 1u, eq = is_eq >> j & 1u;
-      if (ab || (eq && e < equals)) {
-        const uint32_t at = a + min(e, equals);
-        kept[at] = (int32_t)(i0 + j);
-        if (w_out) w_out[at] = x[j];
-      }
-      a += ab;
-      e += eq;
-    }
-    above0 += total >> 16;
-    equal0 += total & 0xffffu;
-  };
-#pragma unroll
-  for (int c = 0; c < kHeld; ++c)
-    if (c * kChunk < len) emit(held[c], c * (int64_t)kChunk + mine);
-  for (int64_t base = (int64_t)kHeld * kChunk; base < len; base += kChunk)
-    emit(load4(base + mine), base + mine);
   for (int64_t j = n + (int64_t)threadIdx.x; j < p.budget; j += kSelThreads) {
     kept[j] = -1;
     if (w_out) w_out[j] = 0.f;
