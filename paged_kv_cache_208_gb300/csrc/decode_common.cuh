@@ -1,0 +1,188 @@
+// decode_common.cuh -- what the decode kernels of the two caches share: the work units and their
+// order, the kernels' parameters, and the merge of the splits that did not meet in a cluster.
+#pragma once
+
+#include <math.h>
+
+#include <algorithm>
+
+#include "device_common.cuh"
+#include "launch.h"
+
+namespace pkv {
+namespace {
+
+constexpr int kD = 128;
+constexpr int kMaxCluster = 8;  // largest portable thread-block cluster
+constexpr int kChunkRows = 8;   // a context's last tile is loaded in 8-row chunks
+constexpr int kChunkBytes = kChunkRows * 128;
+constexpr unsigned int kErrWorkspace = 64u;  // PKV_DEVERR_WORKSPACE
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr unsigned kFull = 0xffffffffu;
+
+struct Unit {
+  int32_t b, s, xg, ntiles;  // ntiles < 0: no more work
+  int32_t store;             // store the sequence's new token (its last position) first
+  int32_t skip;              // 1: the ring's next tile is a discarded speculative load
+};
+
+struct DecodeParams {
+  const uint16_t *q;
+  const int32_t *block_tables;
+  const int32_t *context_lens;
+  float *part_o;
+  float *part_lse;
+  uint16_t *out;
+  int32_t *queue;  // next unit to hand out (the workspace's first word); nullptr: CTA i takes
+                   // unit i only
+  // > 0: the splits of one (sequence, head group) form a cluster of this many CTAs (CTA i
+  // takes unit i, ordered split-minor); rank 0 merges them through distributed shared memory
+  int32_t cluster;
+  unsigned int *err;
+  int64_t num_blocks;
+  int64_t cap;  // longest context the table rows and the split grid can address
+  int32_t table_width;
+  int32_t batch;
+  int32_t num_q_heads;
+  int32_t group;
+  int32_t head_groups;
+  int32_t xgroups;  // num_kv_heads * head_groups
+  int32_t block_size;
+  int32_t chunk;
+  int32_t splits;
+  int32_t units;    // splits * batch * xgroups
+  float qscale;
+  // the step's new tokens (k_new == nullptr: nothing to store)
+  const uint16_t *k_new;
+  const uint16_t *v_new;
+  int64_t k_new_stride, v_new_stride;  // elements per token
+  const int64_t *slots;
+  int64_t num_slots;
+  uint16_t *k_cache_w;
+  uint16_t *v_cache_w;
+  int32_t num_kv_heads;
+  // 8-bit cache: [num_blocks, num_kv_heads, block_size / 64]
+  const float *k_scale;
+  const float *v_scale;
+  // for the weights kernel: scores [batch, num_q_heads, score_stride] (log2 domain) and the
+  // log2-sum-exp of each query head
+  float *scores;
+  int64_t score_stride;
+  float *lse;
+};
+
+// Unit u -> (split s, sequence b, head group xg). A cluster launch orders the units
+// split-minor (the splits of one sequence and head group adjacent), otherwise split-major.
+__device__ __forceinline__ void unit_coords(const DecodeParams &p, int u, int &s, int &b,
+                                            int &xg) {
+  if (p.cluster) {
+    s = u % p.splits;
+    b = (u / p.splits) / p.xgroups;
+    xg = (u / p.splits) % p.xgroups;
+  } else {
+    s = u / (p.batch * p.xgroups);
+    const int r = u % (p.batch * p.xgroups);
+    b = r / p.xgroups;
+    xg = r % p.xgroups;
+  }
+}
+
+// One warp per (sequence, query head): out = sum_s 2^(lse_s - lse) o_s over the sequence's
+// splits, lse = log2 sum_s 2^lse_s. A sequence with no token gets zeros; one whose context
+// fits one split was written by the split kernel.
+__global__ void __launch_bounds__(128)
+    decode_combine_kernel(const float *__restrict__ part_o, const float *__restrict__ part_lse,
+                          const int32_t *__restrict__ context_lens, int32_t batch,
+                          int32_t num_q_heads, int32_t chunk, int32_t splits, int64_t cap,
+                          uint16_t *__restrict__ out, float *__restrict__ lse_out,
+                          const unsigned int *err) {
+  // the stream's next kernel (the next call's split kernel) may be scheduled now: it waits
+  // for this grid's completion before it touches global memory
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // launched as a programmatic dependent of the split kernel: wait until that grid has
+  // completed and its partial results are visible
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (aborted(err)) return;  // an earlier wait gave up: the partials are not complete
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (row >= (int64_t)batch * num_q_heads) return;
+  const int lane = threadIdx.x & 31;
+  const int b = (int)(row / num_q_heads);
+  int64_t L = context_lens[b];
+  L = L < 0 ? 0 : (L > cap ? cap : L);
+  const int ns = (int)((L + chunk - 1) / chunk);
+  if (ns == 1) return;  // one split: the split kernel wrote this row itself
+  const float *lse = part_lse + row * splits;
+  float M = -INFINITY;
+  for (int s = lane; s < ns; s += 32) M = fmaxf(M, lse[s]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float wsum = 0.f;
+  if (M != -INFINITY) {
+    for (int s = 0; s < ns; ++s) {
+      const float wgt = fast_exp2(lse[s] - M);
+      const float4 o4 = *reinterpret_cast<const float4 *>(part_o + (row * splits + s) * kD + 4 * lane);
+      wsum += wgt;
+      acc.x = fmaf(wgt, o4.x, acc.x);
+      acc.y = fmaf(wgt, o4.y, acc.y);
+      acc.z = fmaf(wgt, o4.z, acc.z);
+      acc.w = fmaf(wgt, o4.w, acc.w);
+    }
+  }
+  if (lse_out && lane == 0) lse_out[row] = M + __log2f(wsum);  // ns == 0: -inf, not read
+  const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+  const uint32_t lo = (uint32_t)bf16_bits_rn(acc.x * inv) | ((uint32_t)bf16_bits_rn(acc.y * inv) << 16);
+  const uint32_t hi = (uint32_t)bf16_bits_rn(acc.z * inv) | ((uint32_t)bf16_bits_rn(acc.w * inv) << 16);
+  *reinterpret_cast<uint2 *>(out + row * kD + 4 * lane) = make_uint2(lo, hi);
+}
+
+// The parameters both kernels take from a call and its plan.
+inline DecodeParams decode_params(const DecodeArgs &a, const DecodePlan &p) {
+  uint8_t *ws = static_cast<uint8_t *>(a.workspace);
+  float *const part_base = reinterpret_cast<float *>(ws + kDecodeQueueBytes);  // after the counter
+  DecodeParams prm{};
+  prm.q = static_cast<const uint16_t *>(a.q);
+  prm.block_tables = a.block_tables;
+  prm.context_lens = a.context_lens;
+  prm.part_o = p.splits > 1 ? part_base : nullptr;
+  prm.part_lse = p.splits > 1 ? prm.part_o + (size_t)a.batch * a.num_q_heads * p.splits * kD
+                              : nullptr;
+  prm.out = static_cast<uint16_t *>(a.out);
+  prm.queue = reinterpret_cast<int32_t *>(ws);
+  prm.err = a.err;
+  prm.num_blocks = a.num_blocks;
+  prm.cap = std::min((int64_t)a.table_width * a.block_size, (int64_t)p.splits * p.chunk);
+  prm.table_width = a.table_width;
+  prm.batch = a.batch;
+  prm.num_q_heads = a.num_q_heads;
+  prm.group = a.num_q_heads / a.num_kv_heads;
+  prm.head_groups = p.head_groups;
+  prm.xgroups = a.num_kv_heads * p.head_groups;
+  prm.block_size = a.block_size;
+  prm.chunk = p.chunk;
+  prm.splits = p.splits;
+  prm.qscale = a.scale * kLog2e;
+  prm.num_kv_heads = a.num_kv_heads;
+  prm.k_scale = a.k_scale;
+  prm.v_scale = a.v_scale;
+  if (p.scores_at) {
+    prm.scores = reinterpret_cast<float *>(ws + p.scores_at);
+    prm.score_stride = p.score_stride;
+    prm.lse = reinterpret_cast<float *>(ws + p.lse_at);
+  }
+  return prm;
+}
+
+// The merge kernel of a call whose splits left their partials in the workspace.
+inline cudaError_t launch_combine(const DecodeArgs &a, const DecodePlan &p, const DecodeParams &prm,
+                                  cudaStream_t stream) {
+  const int64_t rows_out = (int64_t)a.batch * a.num_q_heads;
+  // programmatic dependent launch: the merge grid is set up while the split kernel runs
+  return launch_after(decode_combine_kernel, dim3((unsigned)((rows_out + 3) / 4)), 128, stream,
+                      (const float *)prm.part_o, (const float *)prm.part_lse, a.context_lens,
+                      a.batch, a.num_q_heads, p.chunk, p.splits, prm.cap,
+                      static_cast<uint16_t *>(a.out), prm.lse, (const unsigned int *)a.err);
+}
+
+}  // namespace
+}  // namespace pkv

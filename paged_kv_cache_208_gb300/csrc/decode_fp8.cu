@@ -1,13 +1,885 @@
-// decode_fp8.cu -- paged decode attention over the 8-bit cache (the kernel is in
-// decode_kernel.cuh, the format in fp8_cache.cuh).
-#include "decode_kernel.cuh"
+// decode_fp8.cu -- paged decode attention over the 8-bit cache on the 5th-generation tensor cores
+// (sm_103a). The format is in fp8_cache.cuh.
+//
+// Work units, their queue, the clusters of splits and the merges are the bf16 decode kernel's
+// (decode.cu): a unit is one sequence, one KV head, up to eight of its query heads and one split
+// of the context. What differs is that half the bytes leave half the time for each token. With
+// warp MMAs every code has to be converted (K and V to fp16: 64 conversions and 24 MMAs per warp
+// and 16 tokens kept the SM's ALUs 45% busy, 97 us for 256 ragged contexts where the bytes take
+// 77); tcgen05 reads the e4m3 tiles from shared memory as TMA left them. Per 128-token tile, M =
+// 128 both times:
+//
+//   S^T (128 tokens x 16)   = K (128 x 128 dims) Q^T      A = the K tile, K-major
+//   O^T (128 dims x N)     += V^T (128 x 128 tokens) P^T  A = the V tile, M-major
+//
+// q and P enter as sums of e4m3 numbers, in columns of their own (N is at least 16 anyway):
+//   q:  q' = q times the power of two that brings the head's maximum into [128, 256);
+//       hi = e4m3(q'), lo = e4m3(32 (q' - hi)). 4 + 4 bits hold bf16's 8: exact down to 2^-14 of
+//       the maximum, within 2^-22 of it below.
+//   P:  w = 2^(s + ev - R + 5) with ev = log2 of V's scale of the group and R a reference that
+//       no s + ev exceeds by more than 3, so w <= 256; w = t1 + t2 / 32 + t3 / 1024, each t the
+//       e4m3 of what the ones before left: within 2^-15 of w, and within 2^-20 absolutely (2^-25
+//       of the reference's own weight).
+// K's scale multiplies the scores. V's scale is in the exponent, so that one accumulator serves
+// groups of any scales: it holds sum w code = 2^(5 - R) sum 2^s v, and l sums w 2^-ev =
+// 2^(5 - R) 2^s in fp32 from the unrounded w; their quotient is the output.
+//
+// R is the maximum over the unit's first tile; later tiles raise it (and rescale O in tensor
+// memory and l) only when a token exceeds it by more than 3, which the 128 softmax threads agree
+// on with one barrier reduction per tile.
+//
+// Warps (224 threads, two CTAs per SM): 0-3 softmax (thread = token of the tile, and in the
+// epilogue = dimension of O), 4 issues S (and turns each unit's q into its two parts), 5 issues
+// PV, 6 loads: TMA tiles of K and of V in rings of three 16 KiB slots each, the scales of the
+// tile's 256-token page (16 bytes each of K and V) with V's tile. S and P have two buffers, so
+// S(t + 1) is computed while the softmax works on tile t; O has two, so a unit's first PV does
+// not wait for the last unit's epilogue.
+//
+// Rows of a context's last tile past its tokens are not loaded (8-row chunks); V's are zeroed in
+// shared memory, as 0 x NaN from a stale row would poison O.
+#include "decode_common.cuh"
+#include "fp8_cache.cuh"
+#include "tcgen05.cuh"
 
 namespace pkv {
+namespace {
 
-cudaError_t launch_paged_decode_fp8(const DecodeArgs &a, const DecodePlan &plan,
+constexpr int kTile = 128;
+constexpr int kTileBytes = kTile * kD;  // one head's K or V codes of a tile: 16 KiB
+constexpr int kSlots = 3;
+constexpr int kSoftmaxWarps = 4;
+constexpr int kSoftmaxThreads = kSoftmaxWarps * 32;
+constexpr int kSWarp = 4, kPvWarp = 5, kLoadWarp = 6;
+constexpr int kThreads = 7 * 32;
+constexpr int kUnitConsumers = kSoftmaxWarps + 2;
+constexpr float kTop = 5.f;       // log2 of the reference's own w
+constexpr float kHeadroom = 3.f;  // log2 of how far a w may exceed it
+constexpr float kMinScale = 7.8886090522101181e-31f;  // 2^-100
+
+template <int GC>
+struct Kind {
+  static constexpr int kRing = GC <= 4 ? 4 : 2;  // units in flight
+  static constexpr int kQRows = GC <= 4 ? 8 : 16;   // 2 GC rows used: hi, lo
+  static constexpr int kPRows = GC <= 2 ? 8 : GC == 4 ? 16 : 24;  // 3 GC rows used: t1, t2, t3
+  static constexpr int kSCols = 2 * GC < 4 ? 4 : 2 * GC;  // columns of S that are read
+  static constexpr int kOCols = GC <= 2 ? 8 : GC == 4 ? 16 : 32;  // columns of O that are read
+  static constexpr int kNO = GC <= 4 ? 16 : 32;     // N of the second product
+  static constexpr uint32_t kOBase = 32;            // TMEM: S buffers at 0 and 16, then O's
+  static constexpr uint32_t kTmemCols = GC <= 4 ? 64 : 128;
+  // Where a cluster's rank 0 receives its peers' results: with up to this many splits in an
+  // area past the fixed layout (two CTAs still fit on an SM), else in its K slots, lent once it
+  // needs them no more. (splits - 1) x GC x kD outputs, then (splits - 1) x GC log2-sum-exps.
+  static constexpr int kLandSplits = GC <= 2 ? 4 : 1;
+};
+
+// Q and P tiles have rows of 128 bytes, 128-byte swizzle. N = 16 (or 32) rows are multiplied;
+// those past the allocated ones run into what follows in shared memory (the next buffer; from
+// the last Q tile the queued q rows), and give columns that nothing reads.
+template <int GC>
+struct DecodeFp8Smem {
+  using K = Kind<GC>;
+  uint8_t k[kSlots][kTileBytes];  // 1024-byte aligned (128-byte swizzle atoms)
+  uint8_t v[kSlots][kTileBytes];
+  uint8_t p[2][K::kPRows * 128];
+  uint8_t q[2][K::kQRows * 128];
+  uint16_t qs[K::kRing][GC][kD];  // q rows of the queued units, as they came
+  alignas(16) float tile_scale[kSlots][2][4];  // scales of the tile's page: K's, V's
+  float qscale[2][GC];                         // softmax scale log2(e) over q's power of two
+  float warp_max[kSoftmaxWarps][GC];
+  float warp_l[2][kSoftmaxWarps][GC];
+  Unit unit[K::kRing];
+  int32_t stop;  // set by the producer: an earlier wait gave up, this CTA does no work
+  uint32_t tmem_base;
+  uint64_t k_full[kSlots], k_empty[kSlots], v_full[kSlots], v_empty[kSlots];
+  uint64_t q_ready[2], s_full[2], p_full[2], pv_done[2], o_full[2], o_free[2];
+  uint64_t unit_full[K::kRing], unit_empty[K::kRing];
+  uint64_t drain[2];
+  uint64_t cl_bar, cl_ready;  // cluster merge: the peers' results have landed; the area is lent
+};
+
+template <int GC>
+__host__ __device__ constexpr size_t land_offset() {
+  return (sizeof(DecodeFp8Smem<GC>) + 15) / 16 * 16;
+}
+template <int GC>
+__host__ __device__ constexpr size_t fp8_smem_bytes(int cluster) {
+  return (cluster >= 2 && cluster <= Kind<GC>::kLandSplits
+              ? land_offset<GC>() + (size_t)(cluster - 1) * GC * (kD + 1) * sizeof(float)
+              : sizeof(DecodeFp8Smem<GC>)) + 1024;  // + 1024: the layout starts 1024-aligned
+}
+// two CTAs per SM: 228 KiB less 1 KiB each that the system keeps
+static_assert(fp8_smem_bytes<2>(4) <= 113 * 1024 && fp8_smem_bytes<4>(1) <= 113 * 1024 &&
+                  fp8_smem_bytes<8>(1) <= 113 * 1024,
+              "two CTAs fit on an SM");
+static_assert((kMaxCluster - 1) * 8 * (kD + 1) * sizeof(float) <= kSlots * kTileBytes,
+              "the peers' results fit in rank 0's K slots");
+
+__device__ __forceinline__ float redux_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Three e4m3 parts of a pair of weights (0 <= w <= 256), each pair's codes in 16 bits.
+__device__ __forceinline__ void split3(float a, float b, uint32_t (&t)[3]) {
+  t[0] = cvt_e4m3x2(a, b);
+  float2 f = f16x2_to_f32(cvt_f16x2_e4m3x2(t[0]));
+  a = (a - f.x) * 32.f;
+  b = (b - f.y) * 32.f;
+  t[1] = cvt_e4m3x2(a, b);
+  f = f16x2_to_f32(cvt_f16x2_e4m3x2(t[1]));
+  t[2] = cvt_e4m3x2((a - f.x) * 32.f, (b - f.y) * 32.f);
+}
+
+template <int GC, bool W>
+__global__ void __launch_bounds__(kThreads, 2)
+    decode_fp8_kernel(const __grid_constant__ CUtensorMap kmap,
+                      const __grid_constant__ CUtensorMap vmap,
+                      const __grid_constant__ CUtensorMap kmap8,
+                      const __grid_constant__ CUtensorMap vmap8, const DecodeParams p) {
+  using K = Kind<GC>;
+  constexpr int kRing = K::kRing;
+  extern __shared__ uint8_t smem_raw[];
+  DecodeFp8Smem<GC> &sm = *reinterpret_cast<DecodeFp8Smem<GC> *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    sm.stop = 0;
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&sm.k_full[i], 1);
+      mbar_init(&sm.k_empty[i], 1);
+      mbar_init(&sm.v_full[i], 1);
+      mbar_init(&sm.v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.q_ready[i], 1);
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.p_full[i], kSoftmaxWarps);
+      mbar_init(&sm.pv_done[i], 1);
+      mbar_init(&sm.o_full[i], 1);
+      mbar_init(&sm.o_free[i], kSoftmaxWarps);
+      mbar_init(&sm.drain[i], 1);
+    }
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&sm.unit_full[i], 1);
+      mbar_init(&sm.unit_empty[i], kUnitConsumers);
+    }
+    if (p.cluster) {
+      mbar_init(&sm.cl_bar, p.cluster - 1);  // one arrival per peer
+      mbar_init(&sm.cl_ready, 1);
+    }
+    fence_mbar_init();
+  }
+  if (warp == kSWarp) {
+    tmem_alloc(&sm.tmem_base, K::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = sm.tmem_base;
+  // in a cluster: this CTA's barriers are set up (waited for before the first remote access)
+  if (p.cluster) cluster_arrive_relaxed();
+  // cluster merge: this CTA's normalised output of dimension threadIdx.x and its log2-sum-exps
+  float cl_o[GC], cl_lse[GC];
+#pragma unroll
+  for (int g = 0; g < GC; ++g) {
+    cl_o[g] = 0.f;
+    cl_lse[g] = -INFINITY;
+  }
+
+  // Launched as a programmatic dependent of the stream's previous kernel: everything above may
+  // overlap its tail; wait for that grid's completion and memory before touching global memory.
+  // While it finishes, the loader of a static grid warms L2 with its context length, and with
+  // its first tiles through a block id read ahead of the wait (only a hint: every value used
+  // below is read again).
+  int32_t spec_blk = -1, spec_row = -1, spec_h = 0;
+  if (threadIdx.x == kLoadWarp * 32) {
+    prefetch_tensormap(&kmap);
+    prefetch_tensormap(&vmap);
+    prefetch_tensormap(&kmap8);
+    prefetch_tensormap(&vmap8);
+    if (!p.queue) {
+      int s, b, xg;
+      unit_coords(p, blockIdx.x, s, b, xg);
+      prefetch_l2(p.context_lens + b);
+      const int64_t begin = (int64_t)s * p.chunk;
+      if (begin < p.cap) {
+        const int32_t blk =
+            ld_global_cg_s32(p.block_tables + (int64_t)b * p.table_width + begin / p.block_size);
+        if (blk >= 0 && blk < p.num_blocks) {
+          const int in_block = (int)(begin % p.block_size);
+          const int n = min(2 * kSlots, min(p.chunk, p.block_size - in_block) / kTile);
+          spec_h = xg / p.head_groups;
+          spec_blk = blk;
+          spec_row = (int32_t)((int64_t)blk * p.block_size + in_block);
+          for (int t = 0; t < n; ++t) {
+            tma_prefetch_3d(&kmap, 0, spec_row + t * kTile, spec_h);
+            tma_prefetch_3d(&vmap, 0, spec_row + t * kTile, spec_h);
+          }
+        }
+      }
+    }
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the kernel that follows may be scheduled now: it waits for this grid's completion (and its
+  // memory) before reading anything
+  if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  if (warp == kLoadWarp) {
+    // ------------------------------------------------------------------------ loads
+    if (lane == 0) {
+      const uint64_t policy = policy_evict_first();
+      uint32_t pushed = 0, k_tiles = 0, v_tiles = 0;  // issued
+      bool ok = true, first_unit = true;
+      int static_next = blockIdx.x;  // without a queue: unit blockIdx.x, then nothing
+      // The work counter (queued grid): as in decode.cu, every CTA draws until it draws past the
+      // last unit, once, and the CTA with the last of those draws sets it back to zero.
+      bool first_draw = true, past_end = false;
+      auto draw = [&]() -> int {
+        const int u = atomicAdd(p.queue, 1);
+        if (first_draw) {
+          first_draw = false;
+          if (u < 0 || u >= p.units + (int)gridDim.x) record_error(p.err, kErrWorkspace);
+        }
+        if (u < 0 || u >= p.units) {
+          past_end = true;
+          if (u == p.units + (int)gridDim.x - 1) atomicExch(p.queue, 0);
+        }
+        return u;
+      };
+      // the scales of the 256-token page around row in_block of a block, 16 bytes each
+      auto load_scales = [&](int slot, int64_t blk, int in_block, int h) {
+        const int64_t at = (blk * p.num_kv_heads + h) * (p.block_size / kFp8Group) +
+                           (in_block & ~255) / kFp8Group;
+        bulk_copy_g2s(sm.tile_scale[slot][0], p.k_scale + at, 16, &sm.v_full[slot]);
+        bulk_copy_g2s(sm.tile_scale[slot][1], p.v_scale + at, 16, &sm.v_full[slot]);
+      };
+      constexpr uint32_t kScaleBytes = 32;
+      // The first tile, at once, with the block id read ahead of the wait; kept if the id still
+      // holds when the table is read again, else dropped (Unit::skip) and loaded again.
+      bool spec_pending = false;
+      if (spec_row >= 0) {
+        mbar_arrive_expect_tx(&sm.k_full[0], kTileBytes);
+        tma_load_3d(sm.k[0], &kmap, &sm.k_full[0], 0, spec_row, spec_h, policy);
+        mbar_arrive_expect_tx(&sm.v_full[0], kTileBytes + kScaleBytes);
+        tma_load_3d(sm.v[0], &vmap, &sm.v_full[0], 0, spec_row, spec_h, policy);
+        load_scales(0, spec_blk, (int)(spec_row - (int64_t)spec_blk * p.block_size), spec_h);
+        k_tiles = v_tiles = 1;
+        spec_pending = true;
+      }
+      while (ok) {
+        // next unit with work (or one that must write zeros); ntiles < 0 ends the walk
+        Unit un{0, 0, 0, -1, 0, 0};
+        int32_t first_blk = -1;   // block id of the unit's first tile
+        int first_it = 0;         // tiles of the unit already loaded
+        int last_rows = kTile;    // tokens in the unit's last tile
+        while (true) {
+          int u;
+          if (p.queue) {
+            u = draw();
+          } else {
+            u = static_next;
+            static_next = p.units;
+          }
+          if (u < 0 || u >= p.units) break;
+          int s, b, xg;
+          unit_coords(p, u, s, b, xg);
+          // the first tile's block id does not depend on the context length: both loads are in
+          // flight together (a unit that starts past the table's end reads no entry)
+          const int64_t begin = (int64_t)s * p.chunk;
+          const uint32_t err_now =
+              first_unit ? (uint32_t)ld_global_s32(reinterpret_cast<const int32_t *>(p.err)) : 0u;
+          int64_t L = ld_global_s32(p.context_lens + b);
+          if (begin < p.cap)
+            first_blk = ld_global_s32(p.block_tables + (int64_t)b * p.table_width +
+                                      begin / p.block_size);
+          if (first_unit) {
+            first_unit = false;
+            if (err_now & kErrTimeout) {  // an earlier wait gave up somewhere: end the walk
+              sm.stop = 1;
+              break;
+            }
+          }
+          if (L < 0 || L > p.cap) {
+            if (s == 0 && xg == 0) record_error(p.err, 4u /* CONTEXT_RANGE */);
+            L = L < 0 ? 0 : p.cap;
+          }
+          if (begin < L) {
+            const int64_t end = min(L, begin + p.chunk);
+            un = Unit{b, s, xg, (int)((end - begin + kTile - 1) / kTile), 0, 0};
+            last_rows = (int)(end - begin - (int64_t)(un.ntiles - 1) * kTile);
+            if (spec_pending) {
+              if (first_blk == spec_blk) first_it = 1;
+              else un.skip = 1;
+              spec_pending = false;
+            }
+            break;
+          }
+          if (p.cluster || (L == 0 && s == 0 && p.splits == 1)) {
+            // nothing to read: zeros (empty context), or in a cluster no result (the unit
+            // still leaves its -inf log2-sum-exp for the merge)
+            un = Unit{b, s, xg, 0, 0, spec_pending ? 1 : 0};
+            spec_pending = false;
+            break;
+          }
+        }
+        const int slot = pushed % kRing;
+        if (pushed >= kRing &&
+            !wait_parity(&sm.unit_empty[slot], ((pushed / kRing) - 1) & 1, p.err)) {
+          ok = false;
+          break;
+        }
+        sm.unit[slot] = un;
+        ++pushed;
+        if (un.ntiles < 0) {
+          mbar_arrive(&sm.unit_full[slot]);
+          break;
+        }
+        const int h = un.xg / p.head_groups, hg = un.xg % p.head_groups;
+        const uint32_t q_bytes = min(GC, p.group - hg * GC) * kD * 2;
+        mbar_arrive_expect_tx(&sm.unit_full[slot], q_bytes);
+        bulk_copy_g2s(sm.qs[slot],
+                      p.q + ((int64_t)un.b * p.num_q_heads + h * p.group + hg * GC) * kD, q_bytes,
+                      &sm.unit_full[slot]);
+        const int32_t *table = p.block_tables + (int64_t)un.b * p.table_width;
+        const int tok_begin = un.s * p.chunk;
+        for (int it = first_it; it < un.ntiles; ++it) {
+          const int pos = tok_begin + it * kTile, in_block = pos % p.block_size;
+          const int64_t blk = it == 0 ? first_blk : table[pos / p.block_size];
+          const bool blk_ok = blk >= 0 && blk < p.num_blocks;
+          if (!blk_ok) record_error(p.err, 2u /* BLOCK_RANGE */);
+          // (a row wholly outside the pool: TMA fills zeros, nothing is read)
+          const int32_t row = blk_ok ? (int32_t)(blk * p.block_size + in_block) : -2 * kTile;
+          const int rows_here = it == un.ntiles - 1 ? last_rows : kTile;
+          const int chunks = rows_here < kTile && blk_ok ? (rows_here + kChunkRows - 1) / kChunkRows
+                                                         : 0;  // 0: the whole tile in one load
+          const uint32_t bytes = chunks ? chunks * kChunkBytes : kTileBytes;
+          const int ks = k_tiles % kSlots, vs = v_tiles % kSlots;
+          if (k_tiles >= kSlots && !wait_parity(&sm.k_empty[ks], ((k_tiles / kSlots) - 1) & 1, p.err)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&sm.k_full[ks], bytes);
+          if (chunks)
+            for (int c = 0; c < chunks; ++c)
+              tma_load_3d(sm.k[ks] + c * kChunkBytes, &kmap8, &sm.k_full[ks], 0,
+                          row + kChunkRows * c, h, policy);
+          else
+            tma_load_3d(sm.k[ks], &kmap, &sm.k_full[ks], 0, row, h, policy);
+          ++k_tiles;
+          if (v_tiles >= kSlots && !wait_parity(&sm.v_empty[vs], ((v_tiles / kSlots) - 1) & 1, p.err)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&sm.v_full[vs], bytes + kScaleBytes);
+          // (the zero rows of a bad block id take block 0's scales)
+          load_scales(vs, blk_ok ? blk : 0, blk_ok ? in_block : 0, h);
+          if (chunks)
+            for (int c = 0; c < chunks; ++c)
+              tma_load_3d(sm.v[vs] + c * kChunkBytes, &vmap8, &sm.v_full[vs], 0,
+                          row + kChunkRows * c, h, policy);
+          else
+            tma_load_3d(sm.v[vs], &vmap, &sm.v_full[vs], 0, row, h, policy);
+          ++v_tiles;
+        }
+      }
+      // a CTA that stopped early still draws past the last unit once, so that the counter goes
+      // back to zero
+      if (p.queue)
+        while (!past_end) draw();
+      // keep the CTA alive until every copy it issued has landed (these waits ignore the abort
+      // bit; the counts are of issued copies)
+      bool drained = true;
+      for (uint32_t t = k_tiles > kSlots ? k_tiles - kSlots : 0; drained && t < k_tiles; ++t)
+        drained = wait_own(&sm.k_full[t % kSlots], (t / kSlots) & 1, p.err);
+      for (uint32_t t = v_tiles > kSlots ? v_tiles - kSlots : 0; drained && t < v_tiles; ++t)
+        drained = wait_own(&sm.v_full[t % kSlots], (t / kSlots) & 1, p.err);
+      for (uint32_t t = pushed > kRing ? pushed - kRing : 0; drained && t < pushed; ++t)
+        drained = wait_own(&sm.unit_full[t % kRing], (t / kRing) & 1, p.err);
+    }
+    __syncwarp();
+  } else if (warp == kSWarp) {
+    // ------------------------------------------------------------------------ S = K Q^T
+    constexpr uint32_t kId = idesc_e4m3_f32(128, 16, 0, 0);
+    const uint64_t dk = smem_desc_sw128(smem_addr(sm.k[0]), 16, 1024);
+    const uint64_t dq = smem_desc_sw128(smem_addr(sm.q[0]), 16, 1024);
+    auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
+      return __all_sync(kFull, wait_parity(bar, parity, p.err));
+    };
+    uint32_t taken = 0, units = 0, kt = 0, t = 0;  // kt: tiles of the ring, t: tiles computed
+    bool ok = true;
+    while (ok) {
+      const int slot = taken % kRing;
+      if (!(ok = wait_all(&sm.unit_full[slot], (taken / kRing) & 1))) break;
+      const Unit un = sm.unit[slot];
+      ++taken;
+      if (un.ntiles < 0) break;
+      if (un.skip) {  // a speculative load that did not hold: let it land, drop it
+        if (!(ok = wait_all(&sm.k_full[kt % kSlots], (kt / kSlots) & 1))) break;
+        if (lane == 0) mbar_arrive(&sm.k_empty[kt % kSlots]);
+        ++kt;
+      }
+      if (un.ntiles > 0) {
+        // This unit's Q tile was last read by the unit before the last one, all of whose tiles
+        // precede tile t - 1: their S is complete once the softmax has answered tile t - 2 (the
+        // wait that S(t) needs for its buffer too).
+        if (t >= 2 && !(ok = wait_all(&sm.p_full[t & 1], ((t - 2) >> 1) & 1))) break;
+        const int qb = units & 1;
+        const int heads = min(GC, p.group - (un.xg % p.head_groups) * GC);
+        uint8_t *qt = sm.q[qb];
+        // row r, lane's four dimensions: byte 4 lane of the 128, swizzled by 16-byte chunks
+        auto at = [&](int r) {
+          return reinterpret_cast<uint32_t *>(qt + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) +
+                                              (lane & 3) * 4);
+        };
+#pragma unroll
+        for (int g = 0; g < GC; ++g) {
+          uint32_t hi = 0u, lo = 0u;
+          if (g < heads) {
+            const uint2 w = *reinterpret_cast<const uint2 *>(&sm.qs[slot][g][4 * lane]);
+            const float a[4] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
+            // the head's largest |q| as bits (a NaN is larger than everything, and its own code
+            // makes the scores NaN)
+            const uint32_t top = __reduce_max_sync(
+                kFull, max(max(__float_as_uint(a[0]) & 0x7fffffffu, __float_as_uint(a[1]) & 0x7fffffffu),
+                           max(__float_as_uint(a[2]) & 0x7fffffffu, __float_as_uint(a[3]) & 0x7fffffffu)));
+            const int e = min(max((int)(top >> 23), 8), 254);             // 2^(e - 127) <= max |q|
+            const float up = __uint_as_float((uint32_t)(261 - e) << 23);  // 2^(134 - e)
+            hi = cvt_e4m3x2(a[0] * up, a[1] * up) | (cvt_e4m3x2(a[2] * up, a[3] * up) << 16);
+            const float2 r0 = f16x2_to_f32(cvt_f16x2_e4m3x2(hi));
+            const float2 r1 = f16x2_to_f32(cvt_f16x2_e4m3x2_hi(hi));
+            lo = cvt_e4m3x2(fmaf(a[0], up, -r0.x) * 32.f, fmaf(a[1], up, -r0.y) * 32.f) |
+                 (cvt_e4m3x2(fmaf(a[2], up, -r1.x) * 32.f, fmaf(a[3], up, -r1.y) * 32.f) << 16);
+            // softmax scale / up; an infinite q makes its head's scores NaN
+            if (lane == 0)
+              sm.qscale[qb][g] = top == 0x7f800000u
+                                     ? __uint_as_float(0x7fffffffu)
+                                     : p.qscale * __uint_as_float((uint32_t)(e - 7) << 23);
+          } else if (lane == 0) {
+            sm.qscale[qb][g] = 0.f;
+          }
+          *at(g) = hi;
+          *at(GC + g) = lo;
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sm.q_ready[qb]);
+          mbar_arrive(&sm.unit_empty[slot]);
+        }
+        ++units;
+        for (int it = 0; it < un.ntiles; ++it, ++t, ++kt) {
+          const int ks = kt % kSlots;
+          if (!(ok = wait_all(&sm.k_full[ks], (kt / kSlots) & 1))) break;
+          // S(t)'s buffer was tile t - 2's, which the softmax has read
+          if (it > 0 && t >= 2 && !(ok = wait_all(&sm.p_full[t & 1], ((t - 2) >> 1) & 1))) break;
+          tc_fence_after_sync();
+          if (elect_one()) {
+            const uint64_t a = dk + ks * (kTileBytes >> 4);
+            const uint64_t b = dq + qb * (K::kQRows * 128 >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)  // 32 dims: 32 bytes along the swizzled rows
+              umma_e4m3_ss(tmem + 16 * (t & 1), a + 2 * kk, b + 2 * kk, kId, kk > 0);
+            umma_commit(&sm.s_full[t & 1]);
+            umma_commit(&sm.k_empty[ks]);
+          }
+          __syncwarp();
+        }
+      } else if (lane == 0) {
+        mbar_arrive(&sm.unit_empty[slot]);
+      }
+    }
+    // every UMMA must be complete before the CTA exits, also after an abort
+    if (elect_one()) umma_commit(&sm.drain[0]);
+    __syncwarp();
+    wait_own(&sm.drain[0], 0, p.err);
+    __syncwarp();
+  } else if (warp == kPvWarp) {
+    // ------------------------------------------------------------------------ O += V^T P^T
+    constexpr uint32_t kId = idesc_e4m3_f32(128, K::kNO, 1, 0);
+    const uint64_t dv = smem_desc_sw128(smem_addr(sm.v[0]), kTileBytes, 1024);
+    const uint64_t dp = smem_desc_sw128(smem_addr(sm.p[0]), 16, 1024);
+    auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
+      return __all_sync(kFull, wait_parity(bar, parity, p.err));
+    };
+    uint32_t taken = 0, units = 0, vt = 0, t = 0;
+    bool ok = true;
+    while (ok) {
+      const int slot = taken % kRing;
+      if (!(ok = wait_all(&sm.unit_full[slot], (taken / kRing) & 1))) break;
+      const int ntiles = sm.unit[slot].ntiles, skip = sm.unit[slot].skip;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.unit_empty[slot]);
+      ++taken;
+      if (ntiles < 0) break;
+      if (skip) {
+        if (!(ok = wait_all(&sm.v_full[vt % kSlots], (vt / kSlots) & 1))) break;
+        if (lane == 0) mbar_arrive(&sm.v_empty[vt % kSlots]);
+        ++vt;
+      }
+      if (ntiles == 0) continue;
+      const int ob = units & 1;
+      // the unit before the last one's epilogue has read this accumulator
+      if (units >= 2 && !(ok = wait_all(&sm.o_free[ob], ((units >> 1) - 1) & 1))) break;
+      ++units;
+      for (int it = 0; it < ntiles; ++it, ++t, ++vt) {
+        const int vs = vt % kSlots;
+        if (!(ok = wait_all(&sm.v_full[vs], (vt / kSlots) & 1))) break;
+        if (!(ok = wait_all(&sm.p_full[t & 1], (t >> 1) & 1))) break;
+        tc_fence_after_sync();
+        if (elect_one()) {
+          const uint64_t a = dv + vs * (kTileBytes >> 4);
+          const uint64_t b = dp + (t & 1) * (K::kPRows * 128 >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)  // 32 tokens: 32 rows of V, 32 bytes of P's rows
+            umma_e4m3_ss(tmem + K::kOBase + ob * K::kNO, a + kk * (32 * 128 >> 4), b + 2 * kk, kId,
+                         it > 0 || kk > 0);
+          umma_commit(&sm.pv_done[t & 1]);
+          umma_commit(&sm.v_empty[vs]);
+          if (it == ntiles - 1) umma_commit(&sm.o_full[ob]);
+        }
+        __syncwarp();
+      }
+    }
+    if (elect_one()) umma_commit(&sm.drain[1]);
+    __syncwarp();
+    wait_own(&sm.drain[1], 0, p.err);
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------------------ softmax
+    // Thread i: token i of every tile, lane i of tensor memory; in the epilogue dimension i. Every
+    // decision to leave the loops is taken by the 128 threads together, and a thread whose wait
+    // gave up (ok = false) still takes part in the barriers of its unit.
+    const int i = threadIdx.x;
+    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+    uint32_t taken = 0, units = 0, vt = 0, t = 0;
+    while (true) {
+      const int slot = taken % kRing;
+      const bool got = wait_parity(&sm.unit_full[slot], (taken / kRing) & 1, p.err);
+      if (barrier_or(1, kSoftmaxThreads, !got)) break;
+      const Unit un = sm.unit[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.unit_empty[slot]);
+      ++taken;
+      if (un.ntiles < 0) break;
+      vt += un.skip;
+      const int h = un.xg / p.head_groups, hg = un.xg % p.head_groups;
+      const int hq0 = h * p.group + hg * GC, heads = min(GC, p.group - hg * GC);
+      int64_t L = p.context_lens[un.b];
+      L = L < 0 ? 0 : (L > p.cap ? p.cap : L);
+      const int tok_begin = un.s * p.chunk;
+      const int tok_end = (int)min(L, (int64_t)tok_begin + p.chunk);
+      const int64_t row0 = (int64_t)un.b * p.num_q_heads + hq0;
+      const int ub = units & 1;
+      const uint32_t o_addr = lanes + K::kOBase + ub * K::kNO;
+
+      float ref[GC], l[GC], qsc[GC];
+#pragma unroll
+      for (int g = 0; g < GC; ++g) {
+        ref[g] = -INFINITY;
+        l[g] = qsc[g] = 0.f;
+      }
+      bool ok = true;
+      if (un.ntiles > 0) {
+        ok = wait_parity(&sm.q_ready[ub], (units >> 1) & 1, p.err);
+#pragma unroll
+        for (int g = 0; g < GC; ++g) qsc[g] = sm.qscale[ub][g];
+      }
+      for (int it = 0; it < un.ntiles; ++it, ++t, ++vt) {
+        const int vs = vt % kSlots, buf = t & 1;
+        const int n_valid = tok_end - (tok_begin + it * kTile);  // >= 1; < 128 only in a last tile
+        const bool valid = i < n_valid;
+        // (all lanes of a warp together: the loads of tensor memory are the warp's)
+        ok = __all_sync(kFull, ok && wait_parity(&sm.v_full[vs], (vt / kSlots) & 1, p.err) &&
+                                   wait_parity(&sm.s_full[buf], (t >> 1) & 1, p.err));
+        float s[GC], x[GC], ev = 0.f, inv_vs = 1.f;
+        bool over = false;
+        if (ok) {
+          tc_fence_after_sync();
+          uint32_t c[K::kSCols];
+          tmem_ld_cols(lanes + 16 * buf, c);
+          const int grp = (((tok_begin + it * kTile) & 255) >> 6) + (warp >> 1);
+          const float ks = sm.tile_scale[vs][0][grp];
+          // (a group past the context has no scale: whatever is there must not enter R or l)
+          if ((warp >> 1) * 64 < n_valid) {
+            const float v_scale = fmaxf(sm.tile_scale[vs][1][grp], kMinScale);
+            ev = log2_approx(v_scale);
+            inv_vs = rcp_approx(v_scale);
+          }
+#pragma unroll
+          for (int g = 0; g < GC; ++g) {
+            s[g] = fmaf(__uint_as_float(c[GC + g]), 1.f / 32.f, __uint_as_float(c[g])) * (ks * qsc[g]);
+            x[g] = valid ? s[g] + ev : -INFINITY;
+            over = over || x[g] > ref[g] + kHeadroom;
+          }
+          if (W) {
+            float *dst = p.scores + row0 * p.score_stride + tok_begin + it * kTile + i;
+#pragma unroll
+            for (int g = 0; g < GC; ++g)
+              if (g < heads) dst[g * p.score_stride] = s[g];
+          }
+        }
+        // a token above the reference (always in the unit's first tile): raise it
+        if (barrier_or(2, kSoftmaxThreads, over)) {
+#pragma unroll
+          for (int g = 0; g < GC; ++g) {
+            const float m = redux_max(ok ? x[g] : -INFINITY);
+            if (lane == 0) sm.warp_max[warp][g] = m;
+          }
+          named_barrier_sync(3, kSoftmaxThreads);
+          float alpha[GC];
+#pragma unroll
+          for (int g = 0; g < GC; ++g) {
+            float m = ref[g];
+#pragma unroll
+            for (int w = 0; w < kSoftmaxWarps; ++w) m = fmaxf(m, sm.warp_max[w][g]);
+            alpha[g] = m == -INFINITY ? 1.f : fast_exp2(ref[g] - m);
+            ref[g] = m;
+            l[g] *= alpha[g];
+          }
+          if (it > 0) {  // O's columns t1, t2, t3 of head g: wait for the PVs so far, scale
+            ok = __all_sync(kFull, ok && wait_parity(&sm.pv_done[buf ^ 1], ((t - 1) >> 1) & 1, p.err));
+            if (ok) {
+              tc_fence_after_sync();
+              uint32_t o[K::kOCols];
+              tmem_ld_cols(o_addr, o);
+#pragma unroll
+              for (int part = 0; part < 3; ++part)
+#pragma unroll
+                for (int g = 0; g < GC; ++g)
+                  o[part * GC + g] = __float_as_uint(__uint_as_float(o[part * GC + g]) * alpha[g]);
+              tmem_st_cols(o_addr, o);
+              tmem_st_wait();
+            }
+          }
+        }
+        // P(t)'s buffer was tile t - 2's, which its PV has read
+        if (t >= 2)
+          ok = __all_sync(kFull, ok && wait_parity(&sm.pv_done[buf], ((t - 2) >> 1) & 1, p.err));
+        if (ok) {
+          uint8_t *pt = sm.p[buf] + (i & 15);
+          float w[GC + 1];
+#pragma unroll
+          for (int g = 0; g < GC; ++g) {
+            w[g] = valid ? fast_exp2(x[g] - ref[g] + kTop) : 0.f;
+            l[g] = fmaf(w[g], inv_vs, l[g]);
+          }
+#pragma unroll
+          for (int g = 0; g < GC; g += 2) {
+            uint32_t part[3];
+            split3(w[g], w[g + 1 < GC ? g + 1 : g], part);
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                if (g + e >= GC) continue;
+                const int r = j * GC + g + e;
+                pt[r * 128 + (((i >> 4) ^ (r & 7)) << 4)] = (uint8_t)(part[j] >> (8 * e));
+              }
+          }
+          if (!valid) {  // this token's V row is whatever the slot held: zero it (0 x NaN)
+            uint4 *v = reinterpret_cast<uint4 *>(sm.v[vs] + i * 128);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = make_uint4(0, 0, 0, 0);
+          }
+          fence_async_shared();
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.p_full[buf]);
+        }
+      }
+
+      // ---- the unit's output: l over the 128 tokens, O from tensor memory
+      if (un.ntiles > 0) {
+#pragma unroll
+        for (int g = 0; g < GC; ++g) {
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) l[g] += __shfl_xor_sync(kFull, l[g], o);
+          if (lane == 0) sm.warp_l[ub][warp][g] = l[g];
+        }
+        ok = __all_sync(kFull, ok && wait_parity(&sm.o_full[ub], (units >> 1) & 1, p.err));
+        ++units;
+      }
+      if (barrier_or(1, kSoftmaxThreads, !ok)) break;  // a wait gave up: stop together
+      uint32_t o[K::kOCols];
+      if (un.ntiles > 0) {
+        tc_fence_after_sync();
+        tmem_ld_cols(o_addr, o);
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.o_free[ub]);
+      }
+#pragma unroll
+      for (int g = 0; g < GC; ++g) {
+        float out = 0.f, lse = -INFINITY;
+        if (un.ntiles > 0) {
+          float sum = 0.f;
+#pragma unroll
+          for (int w = 0; w < kSoftmaxWarps; ++w) sum += sm.warp_l[ub][w][g];
+          const float acc = fmaf(__uint_as_float(o[2 * GC + g]), 1.f / 1024.f,
+                                 fmaf(__uint_as_float(o[GC + g]), 1.f / 32.f,
+                                      __uint_as_float(o[g])));
+          // sum lies far inside the normal range (2^5 over a scale in [2^-100, 2^120], times the
+          // tokens); the approximate division and log2 err far below one bf16 rounding
+          out = __fdividef(acc, sum);
+          lse = ref[g] - kTop + __log2f(sum);
+        }
+        if (p.cluster) {  // merged by the cluster's rank 0 at the end
+          cl_o[g] = out;
+          cl_lse[g] = lse;
+        } else if (g < heads) {
+          const int64_t row = row0 + g;
+          if (p.splits == 1 || (un.s == 0 && tok_end == L)) {
+            // the unit holds the whole context: the output itself (the merge kernel skips it)
+            p.out[row * kD + i] = bf16_bits_rn(out);
+            if (W && i == 0) p.lse[row] = lse;
+          } else {
+            p.part_o[(row * p.splits + un.s) * kD + i] = out;
+            if (i == 0) p.part_lse[row * p.splits + un.s] = lse;
+          }
+        }
+      }
+      if (!p.queue) break;  // a static grid gives each CTA one unit: nothing follows
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();  // every load has landed, every UMMA is complete
+  if (warp == kSWarp) tmem_dealloc(tmem, K::kTmemCols);
+  if (!p.cluster) return;
+  // ---------------------------------------------------------------- cluster merge
+  // As in decode.cu: each peer sends its result into rank 0's landing area with asynchronous
+  // stores counted on rank 0's barrier and leaves; rank 0 merges. (With more than kLandSplits
+  // splits the area is rank 0's K slots, lent now that nothing uses them.) The waits ignore the
+  // abort bit: every CTA reaches this point, rank 0 always lends and every peer always sends.
+  cluster_wait();  // every CTA's barriers are set up
+  if (threadIdx.x >= kSoftmaxThreads) return;
+  const uint32_t rank = cluster_ctarank();
+  const bool lend = p.cluster > K::kLandSplits;
+  float *land_o = lend ? reinterpret_cast<float *>(sm.k[0])  // peer r + 1's outputs at [r][g][d]
+                       : reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(&sm) +
+                                                   land_offset<GC>());
+  float *land_lse = land_o + (size_t)(p.cluster - 1) * GC * kD;
+  const int d = threadIdx.x;
+  if (rank != 0) {
+    if (lend && !wait_own(&sm.cl_ready, 0, p.err)) return;
+    const uint32_t bar = cluster_addr(smem_addr(&sm.cl_bar), 0);
+    if (threadIdx.x == 0) mbar_arrive_expect_tx_remote(bar, GC * (kD + 1) * sizeof(float));
+    const int r = (int)rank - 1;
+#pragma unroll
+    for (int g = 0; g < GC; ++g) {
+      st_async_f32(cluster_addr(smem_addr(land_o + ((size_t)r * GC + g) * kD + d), 0), cl_o[g], bar);
+      if (d == 0) st_async_f32(cluster_addr(smem_addr(land_lse + r * GC + g), 0), cl_lse[g], bar);
+    }
+    return;
+  }
+  if (lend && threadIdx.x == 0)
+    for (int r = 1; r < p.cluster; ++r)
+      mbar_arrive_remote(cluster_addr(smem_addr(&sm.cl_ready), r));
+  if (!wait_own(&sm.cl_bar, 0, p.err)) return;
+  const int unit0 = blockIdx.x;  // rank 0 holds split 0
+  const int b = (unit0 / p.splits) / p.xgroups, xg = (unit0 / p.splits) % p.xgroups;
+  const int h = xg / p.head_groups, hg = xg % p.head_groups;
+#pragma unroll
+  for (int g = 0; g < GC; ++g) {
+    float M = cl_lse[g];
+    for (int r = 0; r < p.cluster - 1; ++r) M = fmaxf(M, land_lse[r * GC + g]);
+    float acc = 0.f, wsum = 0.f;
+    if (M != -INFINITY) {
+      const float w0 = fast_exp2(cl_lse[g] - M);  // 0 for a split with no keys
+      wsum = w0;
+      acc = w0 * cl_o[g];
+      for (int r = 0; r < p.cluster - 1; ++r) {
+        const float wgt = fast_exp2(land_lse[r * GC + g] - M);
+        wsum += wgt;
+        acc = fmaf(wgt, land_o[((size_t)r * GC + g) * kD + d], acc);
+      }
+    }
+    const int64_t row = (int64_t)b * p.num_q_heads + h * p.group + hg * GC + g;
+    if (!sm.stop && hg * GC + g < p.group) {
+      p.out[row * kD + d] = bf16_bits_rn(wsum > 0.f ? acc / wsum : 0.f);
+      if (W && d == 0) p.lse[row] = M + __log2f(wsum);
+    }
+  }
+}
+
+template <int GC, bool W>
+cudaError_t launch_split_fp8(const CUtensorMap &km, const CUtensorMap &vm, const CUtensorMap &km8,
+                             const CUtensorMap &vm8, const DecodeParams &prm, int num_sms,
+                             cudaStream_t stream) {
+  static bool configured[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 64 || !configured[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(decode_fp8_kernel<GC, W>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)fp8_smem_bytes<GC>(Kind<GC>::kLandSplits));
+    if (e != cudaSuccess) return e;
+    // all of the unified L1/shared storage as shared memory, so two CTAs fit on an SM
+    e = cudaFuncSetAttribute(decode_fp8_kernel<GC, W>,
+                             cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) configured[dev] = true;
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>((int64_t)num_sms * 2, prm.units));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = fp8_smem_bytes<GC>(prm.cluster);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (prm.cluster) {  // one CTA per unit, the splits of a (sequence, head group) in a cluster
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)prm.cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
+  return cudaLaunchKernelEx(&cfg, decode_fp8_kernel<GC, W>, km, vm, km8, vm8, prm);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_decode_fp8(const DecodeArgs &a, const DecodePlan &p,
                                     cudaStream_t stream) {
-  return plan.scores_at ? launch_decode<true, true>(a, plan, stream)
-                        : launch_decode<true, false>(a, plan, stream);
+  // TMA views of the two pools: {128 dims, num_blocks * block_size rows, Hkv heads} of bytes, a
+  // box per tile, and a box per 8 rows for a context's last tile
+  CUtensorMap km, vm, km8, vm8;
+  const uint64_t rows = (uint64_t)a.num_blocks * a.block_size;
+  const uint64_t dims[3] = {kD, rows, (uint64_t)a.num_kv_heads};
+  const uint64_t strides[2] = {(uint64_t)a.num_kv_heads * kD, kD};
+  const uint32_t box[3] = {kD, kTile, 1};
+  const uint32_t box8[3] = {kD, kChunkRows, 1};
+  auto encode = [&](CUtensorMap *map, const void *pool, const uint32_t *bx) {
+    return encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(pool), dims,
+                             strides, bx, CU_TENSOR_MAP_SWIZZLE_128B,
+                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B) == CUDA_SUCCESS;
+  };
+  if (!encode(&km, a.k_cache, box) || !encode(&vm, a.v_cache, box) ||
+      !encode(&km8, a.k_cache, box8) || !encode(&vm8, a.v_cache, box8))
+    return cudaErrorInvalidValue;
+  DecodeParams prm = decode_params(a, p);
+  const int64_t units = (int64_t)p.splits * a.batch * prm.xgroups;
+  // the work counter runs to units + grid size - 1 (an int): keep that in range
+  if (units + 2 * (int64_t)a.num_sms > INT32_MAX) return cudaErrorInvalidValue;
+  prm.units = (int32_t)units;
+  // as for the bf16 cache: with no more units than CTAs each CTA takes one and the splits of a
+  // (sequence, head group) meet in a cluster; else the queue, and a merge kernel
+  const bool queued = (int64_t)a.num_sms * 2 < units;
+  if (!queued) prm.queue = nullptr;
+  prm.cluster = !queued && p.splits >= 2 && p.splits <= kMaxCluster ? p.splits : 0;
+  const bool w = p.scores_at != 0;
+  auto split = [&](auto launch) { return launch(km, vm, km8, vm8, prm, a.num_sms, stream); };
+  const cudaError_t e =
+      p.heads_per_cta == 8   ? split(w ? launch_split_fp8<8, true> : launch_split_fp8<8, false>)
+      : p.heads_per_cta == 4 ? split(w ? launch_split_fp8<4, true> : launch_split_fp8<4, false>)
+                             : split(w ? launch_split_fp8<2, true> : launch_split_fp8<2, false>);
+  if (e != cudaSuccess || p.splits == 1 || prm.cluster) return e;
+  return launch_combine(a, p, prm, stream);
 }
 
 }  // namespace pkv

@@ -1,7 +1,7 @@
-// tcgen05.cuh -- inline-PTX wrappers for the 5th-generation tensor cores (sm_100 family) as a
-// CTA pair uses them: tensor-memory allocation, UMMA issue/commit, TMEM loads and stores, and
-// the shared-memory matrix and instruction descriptors for bf16 operands with 128-byte
-// swizzle.
+// tcgen05.cuh -- inline-PTX wrappers for the 5th-generation tensor cores (sm_100 family):
+// tensor-memory allocation, UMMA issue/commit as a CTA pair uses them on bf16 operands and as
+// one CTA does on e4m3 operands, TMEM loads and stores, and the shared-memory matrix and
+// instruction descriptors with 128-byte swizzle.
 #pragma once
 
 #include <stdint.h>
@@ -10,7 +10,7 @@
 
 namespace pkv {
 
-// Every tcgen05 instruction of a kernel uses the same CTA group. The kernels here run on CTA
+// Every tcgen05 instruction of a kernel uses the same CTA group. The prefill kernel runs on CTA
 // pairs (a cluster of two CTAs on two SMs): allocation and release are done by one warp of
 // each CTA together, and one thread of the pair's leader (cluster rank 0) issues UMMAs that
 // read both CTAs' shared memory and write both CTAs' tensor memory.
@@ -90,6 +90,46 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(uint32_t M, uint32_t N, ui
   return (1u << 4)            // D format: f32
          | (1u << 7)          // A format: bf16
          | (1u << 10)         // B format: bf16
+         | (a_mn << 15) | (b_mn << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+// ------------------------------------------------------------------ UMMA (one CTA)
+// The same for kernels whose CTAs work alone (cta_group::1).
+__device__ __forceinline__ void tmem_alloc(uint32_t *dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   smem_addr(dst_smem)),
+               "r"(ncols)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
+               : "memory");
+}
+
+// D[tmem] (+)= A * B, kind::f8f6f4 (e4m3 in, fp32 accumulate), M = 128, K = 32.
+__device__ __forceinline__ void umma_e4m3_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                             uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+
+// Arrive (once) on this CTA's mbarrier when every UMMA this thread issued so far has completed.
+__device__ __forceinline__ void umma_commit(uint64_t *bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                   smem_addr(bar))
+               : "memory");
+}
+
+// Instruction descriptor, kind::f8f6f4: D fp32, A and B e4m3, dense, M x N tile.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N, uint32_t a_mn,
+                                                      uint32_t b_mn) {
+  return (1u << 4)  // D format: f32 (A and B formats 0: e4m3)
          | (a_mn << 15) | (b_mn << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
@@ -194,6 +234,59 @@ __device__ __forceinline__ void tmem_st16x2_16(uint32_t taddr, const uint32_t (&
       "{%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17};" ::"r"(taddr),
       "n"(kSplit), PKV_W8(0), PKV_W8(8)
       : "memory");
+}
+
+// This warp's 32 TMEM lanes, N consecutive 32-bit columns (4, 8, 16 or 32), waited for.
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[N]) {
+  static_assert(N == 4 || N == 8 || N == 16 || N == 32, "");
+  if constexpr (N == 4) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+        : "r"(taddr)
+        : "memory");
+  } else if constexpr (N == 8) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : PKV_R8(0)
+        : "r"(taddr)
+        : "memory");
+  } else if constexpr (N == 16) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : PKV_R8(0), PKV_R8(8)
+        : "r"(taddr)
+        : "memory");
+  } else {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : PKV_R8(0), PKV_R8(8), PKV_R8(16), PKV_R8(24)
+        : "r"(taddr)
+        : "memory");
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t (&r)[N]) {
+  static_assert(N == 8 || N == 16 || N == 32, "");
+  if constexpr (N == 8)
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
+            taddr),
+        PKV_W8(0)
+        : "memory");
+  else if constexpr (N == 16)
+    tmem_st16(taddr, r);
+  else
+    tmem_st32(taddr, r);
 }
 
 #undef PKV_R8

@@ -1,15 +1,17 @@
 """Decode attention over the 8-bit cache, and decode attention with weights on either cache,
 against softmax attention in 64 bits over the cache's own values.
 
-Tolerances, from the arithmetic (u16 = 2^-11 and ub = 2^-8 are half steps of fp16 and bf16, u =
-2^-24 of fp32):
+Tolerances, from the arithmetic (ub = 2^-8 is a half step of bf16, u = 2^-24 of fp32):
   scores   products are exact, the sum of 128 and the scaling round in fp32: |ds| <= 140 u A with
-           A = scale log2(e) sum |q_d k_d| in the log2 domain, q's fp16 form adds 2^-28 max|q|
-           per term, below that
+           A = scale log2(e) sum |q_d k_d| in the log2 domain; q's form in two e4m3 parts is off by
+           at most 2^-22 max|q| per dimension (8 bits of q' in [128, 256): the low part, scaled
+           by 32, has a spacing of 2^-9, so q' is off by 2^-10 / 32 = 2^-15)
   weights  relative 2 ln2 max|ds| + rounding of the log-sum-exp and of the approximate exp2 and
            log2 (2^-22 each, |lse| u): e_w
-  output   (ub |ref| + (u16 + e_w) sum p |v|) (the 8-bit kernel rounds each weight to fp16, the
-           bf16 kernel with weights splits it in two bf16, 2^-17)
+  output   ub |ref| + (2^-15 + e_w) sum p |v| for the bf16 kernel with weights (it splits each
+           weight in two bf16: 2^-17) and for the 8-bit kernel, whose three e4m3 parts of a weight
+           w <= 256 hold it within 2^-15 w or 2^-20, the reference's own weight being 2^5:
+           2^-25 max_i(p_i scale_i) sum_i |v_i| / scale_i besides
 """
 import numpy as np
 import pytest
@@ -44,7 +46,7 @@ class Case:
         for b, n in enumerate(ctx):
             for j in range(-(-int(n) // bs)):
                 live[self.tables[b, j], :min(bs, n - j * bs)] = True
-        self.pools, self.values = [], []
+        self.pools, self.values, self.v_scale = [], [], None
         for i in range(2):
             if fp8:
                 codes, scale = f8.random_cache(nb, bs, hkv, g)
@@ -56,6 +58,9 @@ class Case:
                 self.pools.append((codes, scale))
                 self.values.append([f8.rows(codes, scale, self.tables[b], int(n))
                                     for b, n in enumerate(ctx)])
+                ones = np.full_like(codes, 0x38)        # 1.0
+                self.v_scale = [f8.rows(ones, scale, self.tables[b], int(n))[:, :, 0]
+                                for b, n in enumerate(ctx)]
             else:
                 bits = w.host_bf16_normal(g, (nb, bs, hkv, D))
                 bits[~live] = w.BF16_NAN_CANARY
@@ -85,7 +90,7 @@ class Case:
                 c = SCALE * np.log2(np.e)
                 x = c * (k[:, h] @ self.q[b, hq])
                 A = c * np.abs(k[:, h]) @ np.abs(self.q[b, hq])
-                ds = 140 * U * A.max() + 2.0 ** -28 * c * np.abs(self.q[b, hq]).max() * \
+                ds = 140 * U * A.max() + 2.0 ** -22 * c * np.abs(self.q[b, hq]).max() * \
                     np.abs(k[:, h]).sum(1).max()
                 top = x.max()
                 p = np.exp2(x - top)
@@ -93,7 +98,10 @@ class Case:
                 p /= p.sum()
                 e = 2 * np.log(2) * ds + 2.0 ** -20 + 8 * U * (abs(lse) + abs(top))
                 out[b, hq] = p @ v[:, h]
-                tol[b, hq] = 2.0 ** -8 * np.abs(out[b, hq]) + (2.0 ** -11 + e) * (p @ np.abs(v[:, h]))
+                tol[b, hq] = 2.0 ** -8 * np.abs(out[b, hq]) + (2.0 ** -15 + e) * (p @ np.abs(v[:, h]))
+                if self.v_scale:
+                    vs = self.v_scale[b][:, h]
+                    tol[b, hq] += 2.0 ** -25 * (p * vs).max() * (np.abs(v[:, h]) / vs[:, None]).sum(0)
                 wb[h] += p
                 tb[h] += p * e + TINY
             ws.append(wb)
