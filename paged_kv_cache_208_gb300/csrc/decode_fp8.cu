@@ -25,12 +25,12 @@
 // 2^(5 - R) 2^s in fp32 from the unrounded w; their quotient is the output.
 //
 // R is the maximum over the unit's first tile; later tiles raise it (and rescale O in tensor
-// memory and l) only when a token exceeds it by more than 3, which the 128 softmax threads agree
-// on with one barrier reduction per tile.
+// memory and l) only when a token exceeds it by more than 3, which the softmax threads agree on
+// with one barrier reduction per tile.
 //
-// Warps (224 threads, two CTAs per SM): 0-3 softmax (thread = token of the tile, and in the
-// epilogue = dimension of O), 4 issues S (and turns each unit's q into its two parts), 5 issues
-// PV, 6 loads: TMA tiles of K and of V in rings of three 16 KiB slots each, the scales of the
+// Warps (352 threads, two CTAs per SM): 0-7 softmax (two threads per token of the tile, each for
+// half of the heads; in the epilogue two per dimension of O), 8 issues S (and turns each unit's q
+// into its two parts), 9 issues PV, 10 loads: TMA tiles of K and of V in rings of three 16 KiB slots each, the scales of the
 // tile's 256-token page (16 bytes each of K and V) with V's tile. S and P have two buffers, so
 // S(t + 1) is computed while the softmax works on tile t; O has two, so a unit's first PV does
 // not wait for the last unit's epilogue.
@@ -47,10 +47,10 @@ namespace {
 constexpr int kTile = 128;
 constexpr int kTileBytes = kTile * kD;  // one head's K or V codes of a tile: 16 KiB
 constexpr int kSlots = 3;
-constexpr int kSoftmaxWarps = 4;
+constexpr int kSoftmaxWarps = 8;  // two for each quadrant of tensor memory's lanes
 constexpr int kSoftmaxThreads = kSoftmaxWarps * 32;
-constexpr int kSWarp = 4, kPvWarp = 5, kLoadWarp = 6;
-constexpr int kThreads = 7 * 32;
+constexpr int kSWarp = 8, kPvWarp = 9, kLoadWarp = 10;
+constexpr int kThreads = 11 * 32;
 constexpr int kUnitConsumers = kSoftmaxWarps + 2;
 constexpr float kTop = 5.f;       // log2 of the reference's own w
 constexpr float kHeadroom = 3.f;  // log2 of how far a w may exceed it
@@ -58,11 +58,13 @@ constexpr float kMinScale = 7.8886090522101181e-31f;  // 2^-100
 
 template <int GC>
 struct Kind {
+  // Heads of a softmax thread: the first or the second half of the unit's. Rows of Q (columns of
+  // S) are hi then lo of the first half's heads, then of the second's; rows of P (columns of O)
+  // likewise t1, t2, t3.
+  static constexpr int kGH = GC / 2;
   static constexpr int kRing = GC <= 4 ? 4 : 2;  // units in flight
-  static constexpr int kQRows = GC <= 4 ? 8 : 16;   // 2 GC rows used: hi, lo
-  static constexpr int kPRows = GC <= 2 ? 8 : GC == 4 ? 16 : 24;  // 3 GC rows used: t1, t2, t3
-  static constexpr int kSCols = 2 * GC < 4 ? 4 : 2 * GC;  // columns of S that are read
-  static constexpr int kOCols = GC <= 2 ? 8 : GC == 4 ? 16 : 32;  // columns of O that are read
+  static constexpr int kQRows = GC <= 4 ? 8 : 16;   // 2 GC rows used
+  static constexpr int kPRows = GC <= 2 ? 8 : GC == 4 ? 16 : 24;  // 3 GC rows used
   static constexpr int kNO = GC <= 4 ? 16 : 32;     // N of the second product
   static constexpr uint32_t kOBase = 32;            // TMEM: S buffers at 0 and 16, then O's
   static constexpr uint32_t kTmemCols = GC <= 4 ? 64 : 128;
@@ -85,8 +87,8 @@ struct DecodeFp8Smem {
   uint16_t qs[K::kRing][GC][kD];  // q rows of the queued units, as they came
   alignas(16) float tile_scale[kSlots][2][4];  // scales of the tile's page: K's, V's
   float qscale[2][GC];                         // softmax scale log2(e) over q's power of two
-  float warp_max[kSoftmaxWarps][GC];
-  float warp_l[2][kSoftmaxWarps][GC];
+  float warp_max[kSoftmaxWarps][GC / 2];
+  float warp_l[2][kSoftmaxWarps][GC / 2];
   Unit unit[K::kRing];
   int32_t stop;  // set by the producer: an earlier wait gave up, this CTA does no work
   uint32_t tmem_base;
@@ -138,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                       const __grid_constant__ CUtensorMap kmap8,
                       const __grid_constant__ CUtensorMap vmap8, const DecodeParams p) {
   using K = Kind<GC>;
-  constexpr int kRing = K::kRing;
+  constexpr int kRing = K::kRing, GH = K::kGH;
   extern __shared__ uint8_t smem_raw[];
   DecodeFp8Smem<GC> &sm = *reinterpret_cast<DecodeFp8Smem<GC> *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -180,10 +182,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t tmem = sm.tmem_base;
   // in a cluster: this CTA's barriers are set up (waited for before the first remote access)
   if (p.cluster) cluster_arrive_relaxed();
-  // cluster merge: this CTA's normalised output of dimension threadIdx.x and its log2-sum-exps
-  float cl_o[GC], cl_lse[GC];
+  // cluster merge: this CTA's normalised outputs of dimension threadIdx.x % 128 (the thread's
+  // heads) and their log2-sum-exps
+  float cl_o[GH], cl_lse[GH];
 #pragma unroll
-  for (int g = 0; g < GC; ++g) {
+  for (int g = 0; g < GH; ++g) {
     cl_o[g] = 0.f;
     cl_lse[g] = -INFINITY;
   }
@@ -459,8 +462,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           } else if (lane == 0) {
             sm.qscale[qb][g] = 0.f;
           }
-          *at(g) = hi;
-          *at(GC + g) = lo;
+          *at((g / GH) * 2 * GH + g % GH) = hi;
+          *at((g / GH) * 2 * GH + GH + g % GH) = lo;
         }
         fence_async_shared();
         __syncwarp();
@@ -548,11 +551,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncwarp();
   } else {
     // ------------------------------------------------------------------------ softmax
-    // Thread i: token i of every tile, lane i of tensor memory; in the epilogue dimension i. Every
-    // decision to leave the loops is taken by the 128 threads together, and a thread whose wait
-    // gave up (ok = false) still takes part in the barriers of its unit.
-    const int i = threadIdx.x;
-    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+    // Threads i and i + 128: token i of every tile, lane i of tensor memory; in the epilogue
+    // dimension i. Each has half of the heads, g0 .. g0 + GH - 1. Every decision to leave the loops
+    // is taken by the softmax threads together, and a thread whose wait gave up (ok = false) still
+    // takes part in the barriers of its unit.
+    const int i = threadIdx.x & 127, half = warp >> 2, quad = warp & 3;
+    const int g0 = half * GH;
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     uint32_t taken = 0, units = 0, vt = 0, t = 0;
     while (true) {
       const int slot = taken % kRing;
@@ -565,18 +570,18 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (un.ntiles < 0) break;
       vt += un.skip;
       const int h = un.xg / p.head_groups, hg = un.xg % p.head_groups;
-      const int hq0 = h * p.group + hg * GC, heads = min(GC, p.group - hg * GC);
+      const int heads = min(GC, p.group - hg * GC) - g0;  // of this thread (may be <= 0)
       int64_t L = p.context_lens[un.b];
       L = L < 0 ? 0 : (L > p.cap ? p.cap : L);
       const int tok_begin = un.s * p.chunk;
       const int tok_end = (int)min(L, (int64_t)tok_begin + p.chunk);
-      const int64_t row0 = (int64_t)un.b * p.num_q_heads + hq0;
+      const int64_t row0 = (int64_t)un.b * p.num_q_heads + h * p.group + hg * GC + g0;
       const int ub = units & 1;
-      const uint32_t o_addr = lanes + K::kOBase + ub * K::kNO;
+      const uint32_t o_addr = lanes + K::kOBase + ub * K::kNO + 3 * g0;
 
-      float ref[GC], l[GC], qsc[GC];
+      float ref[GH], l[GH], qsc[GH];
 #pragma unroll
-      for (int g = 0; g < GC; ++g) {
+      for (int g = 0; g < GH; ++g) {
         ref[g] = -INFINITY;
         l[g] = qsc[g] = 0.f;
       }
@@ -584,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (un.ntiles > 0) {
         ok = wait_parity(&sm.q_ready[ub], (units >> 1) & 1, p.err);
 #pragma unroll
-        for (int g = 0; g < GC; ++g) qsc[g] = sm.qscale[ub][g];
+        for (int g = 0; g < GH; ++g) qsc[g] = sm.qscale[ub][g0 + g];
       }
       for (int it = 0; it < un.ntiles; ++it, ++t, ++vt) {
         const int vs = vt % kSlots, buf = t & 1;
@@ -593,47 +598,45 @@ __global__ void __launch_bounds__(kThreads, 2)
         // (all lanes of a warp together: the loads of tensor memory are the warp's)
         ok = __all_sync(kFull, ok && wait_parity(&sm.v_full[vs], (vt / kSlots) & 1, p.err) &&
                                    wait_parity(&sm.s_full[buf], (t >> 1) & 1, p.err));
-        float s[GC], x[GC], ev = 0.f, inv_vs = 1.f;
+        float x[GH], inv_vs = 1.f;
         bool over = false;
         if (ok) {
           tc_fence_after_sync();
-          uint32_t c[K::kSCols];
-          tmem_ld_cols(lanes + 16 * buf, c);
-          const int grp = (((tok_begin + it * kTile) & 255) >> 6) + (warp >> 1);
+          uint32_t c[2 * GH];
+          tmem_ld_cols(lanes + 16 * buf + 2 * g0, c);
+          const int grp = (((tok_begin + it * kTile) & 255) >> 6) + (quad >> 1);
           const float ks = sm.tile_scale[vs][0][grp];
           // (a group past the context has no scale: whatever is there must not enter R or l)
-          if ((warp >> 1) * 64 < n_valid) {
+          float ev = 0.f;
+          if ((quad >> 1) * 64 < n_valid) {
             const float v_scale = fmaxf(sm.tile_scale[vs][1][grp], kMinScale);
             ev = log2_approx(v_scale);
             inv_vs = rcp_approx(v_scale);
           }
+          float *const scores = p.scores + row0 * p.score_stride + tok_begin + it * kTile + i;
 #pragma unroll
-          for (int g = 0; g < GC; ++g) {
-            s[g] = fmaf(__uint_as_float(c[GC + g]), 1.f / 32.f, __uint_as_float(c[g])) * (ks * qsc[g]);
-            x[g] = valid ? s[g] + ev : -INFINITY;
+          for (int g = 0; g < GH; ++g) {
+            const float s = fmaf(__uint_as_float(c[GH + g]), 1.f / 32.f, __uint_as_float(c[g])) *
+                            (ks * qsc[g]);
+            if (W && g < heads) scores[g * p.score_stride] = s;
+            x[g] = valid ? s + ev : -INFINITY;
             over = over || x[g] > ref[g] + kHeadroom;
-          }
-          if (W) {
-            float *dst = p.scores + row0 * p.score_stride + tok_begin + it * kTile + i;
-#pragma unroll
-            for (int g = 0; g < GC; ++g)
-              if (g < heads) dst[g * p.score_stride] = s[g];
           }
         }
         // a token above the reference (always in the unit's first tile): raise it
         if (barrier_or(2, kSoftmaxThreads, over)) {
 #pragma unroll
-          for (int g = 0; g < GC; ++g) {
+          for (int g = 0; g < GH; ++g) {
             const float m = redux_max(ok ? x[g] : -INFINITY);
             if (lane == 0) sm.warp_max[warp][g] = m;
           }
           named_barrier_sync(3, kSoftmaxThreads);
-          float alpha[GC];
+          float alpha[GH];
 #pragma unroll
-          for (int g = 0; g < GC; ++g) {
+          for (int g = 0; g < GH; ++g) {
             float m = ref[g];
 #pragma unroll
-            for (int w = 0; w < kSoftmaxWarps; ++w) m = fmaxf(m, sm.warp_max[w][g]);
+            for (int w = 0; w < 4; ++w) m = fmaxf(m, sm.warp_max[4 * half + w][g]);
             alpha[g] = m == -INFINITY ? 1.f : fast_exp2(ref[g] - m);
             ref[g] = m;
             l[g] *= alpha[g];
@@ -642,14 +645,14 @@ __global__ void __launch_bounds__(kThreads, 2)
             ok = __all_sync(kFull, ok && wait_parity(&sm.pv_done[buf ^ 1], ((t - 1) >> 1) & 1, p.err));
             if (ok) {
               tc_fence_after_sync();
-              uint32_t o[K::kOCols];
-              tmem_ld_cols(o_addr, o);
+              uint32_t o[3 * GH];
+              tmem_ld_3(o_addr, o);
 #pragma unroll
               for (int part = 0; part < 3; ++part)
 #pragma unroll
-                for (int g = 0; g < GC; ++g)
-                  o[part * GC + g] = __float_as_uint(__uint_as_float(o[part * GC + g]) * alpha[g]);
-              tmem_st_cols(o_addr, o);
+                for (int g = 0; g < GH; ++g)
+                  o[part * GH + g] = __float_as_uint(__uint_as_float(o[part * GH + g]) * alpha[g]);
+              tmem_st_3(o_addr, o);
               tmem_st_wait();
             }
           }
@@ -659,29 +662,29 @@ __global__ void __launch_bounds__(kThreads, 2)
           ok = __all_sync(kFull, ok && wait_parity(&sm.pv_done[buf], ((t - 2) >> 1) & 1, p.err));
         if (ok) {
           uint8_t *pt = sm.p[buf] + (i & 15);
-          float w[GC + 1];
+          float w[GH + 1];
 #pragma unroll
-          for (int g = 0; g < GC; ++g) {
+          for (int g = 0; g < GH; ++g) {
             w[g] = valid ? fast_exp2(x[g] - ref[g] + kTop) : 0.f;
             l[g] = fmaf(w[g], inv_vs, l[g]);
           }
 #pragma unroll
-          for (int g = 0; g < GC; g += 2) {
+          for (int g = 0; g < GH; g += 2) {
             uint32_t part[3];
-            split3(w[g], w[g + 1 < GC ? g + 1 : g], part);
+            split3(w[g], w[g + 1 < GH ? g + 1 : g], part);
 #pragma unroll
             for (int j = 0; j < 3; ++j)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                if (g + e >= GC) continue;
-                const int r = j * GC + g + e;
+                if (g + e >= GH) continue;
+                const int r = 3 * g0 + j * GH + g + e;
                 pt[r * 128 + (((i >> 4) ^ (r & 7)) << 4)] = (uint8_t)(part[j] >> (8 * e));
               }
           }
           if (!valid) {  // this token's V row is whatever the slot held: zero it (0 x NaN)
-            uint4 *v = reinterpret_cast<uint4 *>(sm.v[vs] + i * 128);
+            uint4 *v = reinterpret_cast<uint4 *>(sm.v[vs] + i * 128 + half * 64);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = make_uint4(0, 0, 0, 0);
+            for (int j = 0; j < 4; ++j) v[j] = make_uint4(0, 0, 0, 0);
           }
           fence_async_shared();
           tc_fence_before_sync();
@@ -693,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       // ---- the unit's output: l over the 128 tokens, O from tensor memory
       if (un.ntiles > 0) {
 #pragma unroll
-        for (int g = 0; g < GC; ++g) {
+        for (int g = 0; g < GH; ++g) {
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) l[g] += __shfl_xor_sync(kFull, l[g], o);
           if (lane == 0) sm.warp_l[ub][warp][g] = l[g];
@@ -702,23 +705,23 @@ __global__ void __launch_bounds__(kThreads, 2)
         ++units;
       }
       if (barrier_or(1, kSoftmaxThreads, !ok)) break;  // a wait gave up: stop together
-      uint32_t o[K::kOCols];
+      uint32_t o[3 * GH];
       if (un.ntiles > 0) {
         tc_fence_after_sync();
-        tmem_ld_cols(o_addr, o);
+        tmem_ld_3(o_addr, o);
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.o_free[ub]);
       }
 #pragma unroll
-      for (int g = 0; g < GC; ++g) {
+      for (int g = 0; g < GH; ++g) {
         float out = 0.f, lse = -INFINITY;
         if (un.ntiles > 0) {
           float sum = 0.f;
 #pragma unroll
-          for (int w = 0; w < kSoftmaxWarps; ++w) sum += sm.warp_l[ub][w][g];
-          const float acc = fmaf(__uint_as_float(o[2 * GC + g]), 1.f / 1024.f,
-                                 fmaf(__uint_as_float(o[GC + g]), 1.f / 32.f,
+          for (int w = 0; w < 4; ++w) sum += sm.warp_l[ub][4 * half + w][g];
+          const float acc = fmaf(__uint_as_float(o[2 * GH + g]), 1.f / 1024.f,
+                                 fmaf(__uint_as_float(o[GH + g]), 1.f / 32.f,
                                       __uint_as_float(o[g])));
           // sum lies far inside the normal range (2^5 over a scale in [2^-100, 2^120], times the
           // tokens); the approximate division and log2 err far below one bf16 rounding
@@ -760,16 +763,17 @@ __global__ void __launch_bounds__(kThreads, 2)
                        : reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(&sm) +
                                                    land_offset<GC>());
   float *land_lse = land_o + (size_t)(p.cluster - 1) * GC * kD;
-  const int d = threadIdx.x;
+  const int d = threadIdx.x & 127, g0 = (threadIdx.x >> 7) * GH;
   if (rank != 0) {
     if (lend && !wait_own(&sm.cl_ready, 0, p.err)) return;
     const uint32_t bar = cluster_addr(smem_addr(&sm.cl_bar), 0);
     if (threadIdx.x == 0) mbar_arrive_expect_tx_remote(bar, GC * (kD + 1) * sizeof(float));
     const int r = (int)rank - 1;
 #pragma unroll
-    for (int g = 0; g < GC; ++g) {
-      st_async_f32(cluster_addr(smem_addr(land_o + ((size_t)r * GC + g) * kD + d), 0), cl_o[g], bar);
-      if (d == 0) st_async_f32(cluster_addr(smem_addr(land_lse + r * GC + g), 0), cl_lse[g], bar);
+    for (int g = 0; g < GH; ++g) {
+      const int at = r * GC + g0 + g;
+      st_async_f32(cluster_addr(smem_addr(land_o + (size_t)at * kD + d), 0), cl_o[g], bar);
+      if (d == 0) st_async_f32(cluster_addr(smem_addr(land_lse + at), 0), cl_lse[g], bar);
     }
     return;
   }
@@ -781,22 +785,23 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int b = (unit0 / p.splits) / p.xgroups, xg = (unit0 / p.splits) % p.xgroups;
   const int h = xg / p.head_groups, hg = xg % p.head_groups;
 #pragma unroll
-  for (int g = 0; g < GC; ++g) {
+  for (int g = 0; g < GH; ++g) {
     float M = cl_lse[g];
-    for (int r = 0; r < p.cluster - 1; ++r) M = fmaxf(M, land_lse[r * GC + g]);
+    for (int r = 0; r < p.cluster - 1; ++r) M = fmaxf(M, land_lse[r * GC + g0 + g]);
     float acc = 0.f, wsum = 0.f;
     if (M != -INFINITY) {
       const float w0 = fast_exp2(cl_lse[g] - M);  // 0 for a split with no keys
       wsum = w0;
       acc = w0 * cl_o[g];
       for (int r = 0; r < p.cluster - 1; ++r) {
-        const float wgt = fast_exp2(land_lse[r * GC + g] - M);
+        const float wgt = fast_exp2(land_lse[r * GC + g0 + g] - M);
         wsum += wgt;
-        acc = fmaf(wgt, land_o[((size_t)r * GC + g) * kD + d], acc);
+        acc = fmaf(wgt, land_o[((size_t)r * GC + g0 + g) * kD + d], acc);
       }
     }
-    const int64_t row = (int64_t)b * p.num_q_heads + h * p.group + hg * GC + g;
-    if (!sm.stop && hg * GC + g < p.group) {
+    const int in_group = hg * GC + g0 + g;
+    const int64_t row = (int64_t)b * p.num_q_heads + h * p.group + in_group;
+    if (!sm.stop && in_group < p.group) {
       p.out[row * kD + d] = bf16_bits_rn(wsum > 0.f ? acc / wsum : 0.f);
       if (W && d == 0) p.lse[row] = M + __log2f(wsum);
     }

@@ -236,57 +236,86 @@ __device__ __forceinline__ void tmem_st16x2_16(uint32_t taddr, const uint32_t (&
       : "memory");
 }
 
-// This warp's 32 TMEM lanes, N consecutive 32-bit columns (4, 8, 16 or 32), waited for.
+// This warp's 32 TMEM lanes, N consecutive 32-bit columns (2, 4 or 8), waited for.
 template <int N>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[N]) {
-  static_assert(N == 4 || N == 8 || N == 16 || N == 32, "");
-  if constexpr (N == 4) {
+  static_assert(N == 2 || N == 4 || N == 8, "");
+  if constexpr (N == 2)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1])
+        : "r"(taddr)
+        : "memory");
+  else if constexpr (N == 4)
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
         : "r"(taddr)
         : "memory");
-  } else if constexpr (N == 8) {
+  else
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
         : PKV_R8(0)
         : "r"(taddr)
         : "memory");
-  } else if constexpr (N == 16) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : PKV_R8(0), PKV_R8(8)
-        : "r"(taddr)
-        : "memory");
-  } else {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : PKV_R8(0), PKV_R8(8), PKV_R8(16), PKV_R8(24)
-        : "r"(taddr)
-        : "memory");
-  }
 }
 
+// Three times 1, 2 or 4 columns: exactly 3, 6 or 12 of them, loaded (and waited for) or stored, so
+// that the columns next to them may be another warp's.
 template <int N>
-__device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t (&r)[N]) {
-  static_assert(N == 8 || N == 16 || N == 32, "");
-  if constexpr (N == 8)
+__device__ __forceinline__ void tmem_ld_3(uint32_t taddr, uint32_t (&r)[N]) {
+  static_assert(N == 3 || N == 6 || N == 12, "");
+  if constexpr (N == 3)
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
-            taddr),
-        PKV_W8(0)
+        "tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%3];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%2}, [%4];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=&r"(r[0]), "=&r"(r[1]), "=r"(r[2])
+        : "r"(taddr), "r"(taddr + 2)
         : "memory");
-  else if constexpr (N == 16)
-    tmem_st16(taddr, r);
+  else if constexpr (N == 6)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%6];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x2.b32 {%4, %5}, [%7];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=r"(r[4]), "=r"(r[5])
+        : "r"(taddr), "r"(taddr + 4)
+        : "memory");
   else
-    tmem_st32(taddr, r);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%12];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%8, %9, %10, %11}, [%13];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]),
+          "=&r"(r[6]), "=&r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11])
+        : "r"(taddr), "r"(taddr + 8)
+        : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tmem_st_3(uint32_t taddr, const uint32_t (&r)[N]) {
+  static_assert(N == 3 || N == 6 || N == 12, "");
+  if constexpr (N == 3)
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x2.b32 [%3], {%0, %1};\n\t"
+        "tcgen05.st.sync.aligned.32x32b.x1.b32 [%4], {%2};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(taddr), "r"(taddr + 2)
+        : "memory");
+  else if constexpr (N == 6)
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x4.b32 [%6], {%0, %1, %2, %3};\n\t"
+        "tcgen05.st.sync.aligned.32x32b.x2.b32 [%7], {%4, %5};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(taddr), "r"(taddr + 4)
+        : "memory");
+  else
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%12], {%0, %1, %2, %3, %4, %5, %6, %7};\n\t"
+        "tcgen05.st.sync.aligned.32x32b.x4.b32 [%13], {%8, %9, %10, %11};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(taddr), "r"(taddr + 8)
+        : "memory");
 }
 
 #undef PKV_R8
