@@ -30,7 +30,7 @@
 //
 // Warps (352 threads, two CTAs per SM): 0-7 softmax (two threads per token of the tile, each for
 // half of the heads; in the epilogue two per dimension of O), 8 issues S (and turns each unit's q
-// into its two parts), 9 issues PV, 10 loads: TMA tiles of K and of V in rings of three 16 KiB slots each, the scales of the
+// into its two parts), 9 issues PV, 10 loads: TMA tiles of K and of V in rings of 16 KiB slots, the scales of the
 // tile's 256-token page (16 bytes each of K and V) with V's tile. S and P have two buffers, so
 // S(t + 1) is computed while the softmax works on tile t; O has two, so a unit's first PV does
 // not wait for the last unit's epilogue.
@@ -46,7 +46,10 @@ namespace {
 
 constexpr int kTile = 128;
 constexpr int kTileBytes = kTile * kD;  // one head's K or V codes of a tile: 16 KiB
-constexpr int kSlots = 3;
+// Slots of the K ring and of the V ring. A slot of V is taken from the load's issue until its PV
+// has completed, some 2 us, so a ring of three moves a tile every 0.65 us: enough when two CTAs
+// share an SM's bandwidth. A grid of no more CTAs than SMs has the SM's shared memory to itself.
+constexpr int kSlotsShared = 3, kMaxSlots = 6;
 constexpr int kSoftmaxWarps = 8;  // two for each quadrant of tensor memory's lanes
 constexpr int kSoftmaxThreads = kSoftmaxWarps * 32;
 constexpr int kSWarp = 8, kPvWarp = 9, kLoadWarp = 10;
@@ -77,22 +80,21 @@ struct Kind {
 // Q and P tiles have rows of 128 bytes, 128-byte swizzle. N = 16 (or 32) rows are multiplied;
 // those past the allocated ones run into what follows in shared memory (the next buffer; from
 // the last Q tile the queued q rows), and give columns that nothing reads.
+// Before this structure lie the K ring and the V ring, `slots` tiles of 16 KiB each.
 template <int GC>
 struct DecodeFp8Smem {
   using K = Kind<GC>;
-  uint8_t k[kSlots][kTileBytes];  // 1024-byte aligned (128-byte swizzle atoms)
-  uint8_t v[kSlots][kTileBytes];
-  uint8_t p[2][K::kPRows * 128];
+  uint8_t p[2][K::kPRows * 128];  // 1024-byte aligned (128-byte swizzle atoms)
   uint8_t q[2][K::kQRows * 128];
   uint16_t qs[K::kRing][GC][kD];  // q rows of the queued units, as they came
-  alignas(16) float tile_scale[kSlots][2][4];  // scales of the tile's page: K's, V's
+  alignas(16) float tile_scale[kMaxSlots][2][4];  // scales of the tile's page: K's, V's
   float qscale[2][GC];                         // softmax scale log2(e) over q's power of two
   float warp_max[kSoftmaxWarps][GC / 2];
   float warp_l[2][kSoftmaxWarps][GC / 2];
   Unit unit[K::kRing];
   int32_t stop;  // set by the producer: an earlier wait gave up, this CTA does no work
   uint32_t tmem_base;
-  uint64_t k_full[kSlots], k_empty[kSlots], v_full[kSlots], v_empty[kSlots];
+  uint64_t k_full[kMaxSlots], k_empty[kMaxSlots], v_full[kMaxSlots], v_empty[kMaxSlots];
   uint64_t q_ready[2], s_full[2], p_full[2], pv_done[2], o_full[2], o_free[2];
   uint64_t unit_full[K::kRing], unit_empty[K::kRing];
   uint64_t drain[2];
@@ -104,17 +106,34 @@ __host__ __device__ constexpr size_t land_offset() {
   return (sizeof(DecodeFp8Smem<GC>) + 15) / 16 * 16;
 }
 template <int GC>
-__host__ __device__ constexpr size_t fp8_smem_bytes(int cluster) {
-  return (cluster >= 2 && cluster <= Kind<GC>::kLandSplits
+__host__ __device__ constexpr size_t fp8_smem_bytes(int slots, int cluster) {
+  return 2 * (size_t)slots * kTileBytes +
+         (cluster >= 2 && cluster <= Kind<GC>::kLandSplits
               ? land_offset<GC>() + (size_t)(cluster - 1) * GC * (kD + 1) * sizeof(float)
               : sizeof(DecodeFp8Smem<GC>)) + 1024;  // + 1024: the layout starts 1024-aligned
 }
-// two CTAs per SM: 228 KiB less 1 KiB each that the system keeps
-static_assert(fp8_smem_bytes<2>(4) <= 113 * 1024 && fp8_smem_bytes<4>(1) <= 113 * 1024 &&
-                  fp8_smem_bytes<8>(1) <= 113 * 1024,
+// two CTAs per SM: 228 KiB less 1 KiB each that the system keeps; one: 227 KiB
+static_assert(fp8_smem_bytes<2>(kSlotsShared, 4) <= 113 * 1024 &&
+                  fp8_smem_bytes<4>(kSlotsShared, 1) <= 113 * 1024 &&
+                  fp8_smem_bytes<8>(kSlotsShared, 1) <= 113 * 1024,
               "two CTAs fit on an SM");
-static_assert((kMaxCluster - 1) * 8 * (kD + 1) * sizeof(float) <= kSlots * kTileBytes,
+static_assert(fp8_smem_bytes<2>(kMaxSlots, 4) <= 227 * 1024 &&
+                  fp8_smem_bytes<8>(kMaxSlots, 1) <= 227 * 1024,
+              "one CTA fits on an SM");
+static_assert((kMaxCluster - 1) * 8 * (kD + 1) * sizeof(float) <= kSlotsShared * kTileBytes,
               "the peers' results fit in rank 0's K slots");
+
+// A position in a ring of n slots: the slot, and the parity of the phase a use of it completes.
+struct Ring {
+  int slot = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++slot == n) {
+      slot = 0;
+      parity ^= 1u;
+    }
+  }
+};
 
 __device__ __forceinline__ float redux_max(float x) {
   float r;
@@ -142,12 +161,16 @@ __global__ void __launch_bounds__(kThreads, 2)
   using K = Kind<GC>;
   constexpr int kRing = K::kRing, GH = K::kGH;
   extern __shared__ uint8_t smem_raw[];
-  DecodeFp8Smem<GC> &sm = *reinterpret_cast<DecodeFp8Smem<GC> *>(
+  const int slots = p.ring_slots;
+  uint8_t *const k_ring = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *const v_ring = k_ring + slots * kTileBytes;
+  DecodeFp8Smem<GC> &sm =
+      *reinterpret_cast<DecodeFp8Smem<GC> *>(v_ring + slots * kTileBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     sm.stop = 0;
-    for (int i = 0; i < kSlots; ++i) {
+    for (int i = 0; i < slots; ++i) {
       mbar_init(&sm.k_full[i], 1);
       mbar_init(&sm.k_empty[i], 1);
       mbar_init(&sm.v_full[i], 1);
@@ -212,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             ld_global_cg_s32(p.block_tables + (int64_t)b * p.table_width + begin / p.block_size);
         if (blk >= 0 && blk < p.num_blocks) {
           const int in_block = (int)(begin % p.block_size);
-          const int n = min(2 * kSlots, min(p.chunk, p.block_size - in_block) / kTile);
+          const int n = min(2 * slots, min(p.chunk, p.block_size - in_block) / kTile);
           spec_h = xg / p.head_groups;
           spec_blk = blk;
           spec_row = (int32_t)((int64_t)blk * p.block_size + in_block);
@@ -233,7 +256,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     // ------------------------------------------------------------------------ loads
     if (lane == 0) {
       const uint64_t policy = policy_evict_first();
-      uint32_t pushed = 0, k_tiles = 0, v_tiles = 0;  // issued
+      uint32_t pushed = 0;
+      Ring kr, vr;                     // the next slot of K and of V
+      int k_issued = 0, v_issued = 0;  // capped at the rings' length
       bool ok = true, first_unit = true;
       int static_next = blockIdx.x;  // without a queue: unit blockIdx.x, then nothing
       // The work counter (queued grid): as in decode.cu, every CTA draws until it draws past the
@@ -264,11 +289,13 @@ __global__ void __launch_bounds__(kThreads, 2)
       bool spec_pending = false;
       if (spec_row >= 0) {
         mbar_arrive_expect_tx(&sm.k_full[0], kTileBytes);
-        tma_load_3d(sm.k[0], &kmap, &sm.k_full[0], 0, spec_row, spec_h, policy);
+        tma_load_3d(k_ring, &kmap, &sm.k_full[0], 0, spec_row, spec_h, policy);
         mbar_arrive_expect_tx(&sm.v_full[0], kTileBytes + kScaleBytes);
-        tma_load_3d(sm.v[0], &vmap, &sm.v_full[0], 0, spec_row, spec_h, policy);
+        tma_load_3d(v_ring, &vmap, &sm.v_full[0], 0, spec_row, spec_h, policy);
         load_scales(0, spec_blk, (int)(spec_row - (int64_t)spec_blk * p.block_size), spec_h);
-        k_tiles = v_tiles = 1;
+        kr.next(slots);
+        vr.next(slots);
+        k_issued = v_issued = 1;
         spec_pending = true;
       }
       while (ok) {
@@ -345,46 +372,63 @@ __global__ void __launch_bounds__(kThreads, 2)
         bulk_copy_g2s(sm.qs[slot],
                       p.q + ((int64_t)un.b * p.num_q_heads + h * p.group + hg * GC) * kD, q_bytes,
                       &sm.unit_full[slot]);
-        const int32_t *table = p.block_tables + (int64_t)un.b * p.table_width;
-        const int tok_begin = un.s * p.chunk;
-        for (int it = first_it; it < un.ntiles; ++it) {
-          const int pos = tok_begin + it * kTile, in_block = pos % p.block_size;
-          const int64_t blk = it == 0 ? first_blk : table[pos / p.block_size];
+        // The table is read a block ahead (an entry's latency is longer than a tile's share of the
+        // bandwidth: with a read per tile the loads ran at one tile per 0.68 us and CTA).
+        const int32_t *entry =
+            p.block_tables + (int64_t)un.b * p.table_width + un.s * p.chunk / p.block_size;
+        int in_block = un.s * p.chunk % p.block_size;
+        int left = (un.ntiles - 1) * kTile + last_rows;  // tokens from the current tile on
+        int32_t blk = first_blk, next_blk = -1;
+        if (left > p.block_size - in_block) next_blk = ld_global_s32(++entry);
+        for (int it = 0; it < un.ntiles; ++it) {
+          if (it > 0) {
+            left -= kTile;
+            in_block += kTile;
+            if (in_block == p.block_size) {
+              in_block = 0;
+              blk = next_blk;
+              if (left > p.block_size) next_blk = ld_global_s32(++entry);
+            }
+          }
+          if (it < first_it) continue;
           const bool blk_ok = blk >= 0 && blk < p.num_blocks;
           if (!blk_ok) record_error(p.err, 2u /* BLOCK_RANGE */);
           // (a row wholly outside the pool: TMA fills zeros, nothing is read)
-          const int32_t row = blk_ok ? (int32_t)(blk * p.block_size + in_block) : -2 * kTile;
-          const int rows_here = it == un.ntiles - 1 ? last_rows : kTile;
+          const int32_t row = blk_ok ? blk * p.block_size + in_block : -2 * kTile;
+          const int rows_here = min(left, kTile);
           const int chunks = rows_here < kTile && blk_ok ? (rows_here + kChunkRows - 1) / kChunkRows
                                                          : 0;  // 0: the whole tile in one load
           const uint32_t bytes = chunks ? chunks * kChunkBytes : kTileBytes;
-          const int ks = k_tiles % kSlots, vs = v_tiles % kSlots;
-          if (k_tiles >= kSlots && !wait_parity(&sm.k_empty[ks], ((k_tiles / kSlots) - 1) & 1, p.err)) {
+          // (a slot's first use finds it empty; later ones wait for the use before, whose phase has
+          // the other parity)
+          if (k_issued == slots && !wait_parity(&sm.k_empty[kr.slot], kr.parity ^ 1u, p.err)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&sm.k_full[ks], bytes);
+          uint8_t *kd = k_ring + kr.slot * kTileBytes, *vd = v_ring + vr.slot * kTileBytes;
+          uint64_t *kbar = &sm.k_full[kr.slot], *vbar = &sm.v_full[vr.slot];
+          mbar_arrive_expect_tx(kbar, bytes);
           if (chunks)
             for (int c = 0; c < chunks; ++c)
-              tma_load_3d(sm.k[ks] + c * kChunkBytes, &kmap8, &sm.k_full[ks], 0,
-                          row + kChunkRows * c, h, policy);
+              tma_load_3d(kd + c * kChunkBytes, &kmap8, kbar, 0, row + kChunkRows * c, h, policy);
           else
-            tma_load_3d(sm.k[ks], &kmap, &sm.k_full[ks], 0, row, h, policy);
-          ++k_tiles;
-          if (v_tiles >= kSlots && !wait_parity(&sm.v_empty[vs], ((v_tiles / kSlots) - 1) & 1, p.err)) {
+            tma_load_3d(kd, &kmap, kbar, 0, row, h, policy);
+          kr.next(slots);
+          k_issued = min(k_issued + 1, slots);
+          if (v_issued == slots && !wait_parity(&sm.v_empty[vr.slot], vr.parity ^ 1u, p.err)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&sm.v_full[vs], bytes + kScaleBytes);
+          mbar_arrive_expect_tx(vbar, bytes + kScaleBytes);
           // (the zero rows of a bad block id take block 0's scales)
-          load_scales(vs, blk_ok ? blk : 0, blk_ok ? in_block : 0, h);
+          load_scales(vr.slot, blk_ok ? blk : 0, blk_ok ? in_block : 0, h);
           if (chunks)
             for (int c = 0; c < chunks; ++c)
-              tma_load_3d(sm.v[vs] + c * kChunkBytes, &vmap8, &sm.v_full[vs], 0,
-                          row + kChunkRows * c, h, policy);
+              tma_load_3d(vd + c * kChunkBytes, &vmap8, vbar, 0, row + kChunkRows * c, h, policy);
           else
-            tma_load_3d(sm.v[vs], &vmap, &sm.v_full[vs], 0, row, h, policy);
-          ++v_tiles;
+            tma_load_3d(vd, &vmap, vbar, 0, row, h, policy);
+          vr.next(slots);
+          v_issued = min(v_issued + 1, slots);
         }
       }
       // a CTA that stopped early still draws past the last unit once, so that the counter goes
@@ -394,10 +438,12 @@ __global__ void __launch_bounds__(kThreads, 2)
       // keep the CTA alive until every copy it issued has landed (these waits ignore the abort
       // bit; the counts are of issued copies)
       bool drained = true;
-      for (uint32_t t = k_tiles > kSlots ? k_tiles - kSlots : 0; drained && t < k_tiles; ++t)
-        drained = wait_own(&sm.k_full[t % kSlots], (t / kSlots) & 1, p.err);
-      for (uint32_t t = v_tiles > kSlots ? v_tiles - kSlots : 0; drained && t < v_tiles; ++t)
-        drained = wait_own(&sm.v_full[t % kSlots], (t / kSlots) & 1, p.err);
+      // (slot i's last use was in this turn of the ring if the position is past it, else in the
+      // turn before)
+      for (int i = 0; drained && i < k_issued; ++i)
+        drained = wait_own(&sm.k_full[i], i < kr.slot ? kr.parity : kr.parity ^ 1u, p.err);
+      for (int i = 0; drained && i < v_issued; ++i)
+        drained = wait_own(&sm.v_full[i], i < vr.slot ? vr.parity : vr.parity ^ 1u, p.err);
       for (uint32_t t = pushed > kRing ? pushed - kRing : 0; drained && t < pushed; ++t)
         drained = wait_own(&sm.unit_full[t % kRing], (t / kRing) & 1, p.err);
     }
@@ -405,12 +451,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   } else if (warp == kSWarp) {
     // ------------------------------------------------------------------------ S = K Q^T
     constexpr uint32_t kId = idesc_e4m3_f32(128, 16, 0, 0);
-    const uint64_t dk = smem_desc_sw128(smem_addr(sm.k[0]), 16, 1024);
+    const uint64_t dk = smem_desc_sw128(smem_addr(k_ring), 16, 1024);
     const uint64_t dq = smem_desc_sw128(smem_addr(sm.q[0]), 16, 1024);
     auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
       return __all_sync(kFull, wait_parity(bar, parity, p.err));
     };
-    uint32_t taken = 0, units = 0, kt = 0, t = 0;  // kt: tiles of the ring, t: tiles computed
+    uint32_t taken = 0, units = 0, t = 0;  // t: tiles computed
+    Ring kr;
     bool ok = true;
     while (ok) {
       const int slot = taken % kRing;
@@ -419,9 +466,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       ++taken;
       if (un.ntiles < 0) break;
       if (un.skip) {  // a speculative load that did not hold: let it land, drop it
-        if (!(ok = wait_all(&sm.k_full[kt % kSlots], (kt / kSlots) & 1))) break;
-        if (lane == 0) mbar_arrive(&sm.k_empty[kt % kSlots]);
-        ++kt;
+        if (!(ok = wait_all(&sm.k_full[kr.slot], kr.parity))) break;
+        if (lane == 0) mbar_arrive(&sm.k_empty[kr.slot]);
+        kr.next(slots);
       }
       if (un.ntiles > 0) {
         // This unit's Q tile was last read by the unit before the last one, all of whose tiles
@@ -472,20 +519,19 @@ __global__ void __launch_bounds__(kThreads, 2)
           mbar_arrive(&sm.unit_empty[slot]);
         }
         ++units;
-        for (int it = 0; it < un.ntiles; ++it, ++t, ++kt) {
-          const int ks = kt % kSlots;
-          if (!(ok = wait_all(&sm.k_full[ks], (kt / kSlots) & 1))) break;
+        for (int it = 0; it < un.ntiles; ++it, ++t, kr.next(slots)) {
+          if (!(ok = wait_all(&sm.k_full[kr.slot], kr.parity))) break;
           // S(t)'s buffer was tile t - 2's, which the softmax has read
           if (it > 0 && t >= 2 && !(ok = wait_all(&sm.p_full[t & 1], ((t - 2) >> 1) & 1))) break;
           tc_fence_after_sync();
           if (elect_one()) {
-            const uint64_t a = dk + ks * (kTileBytes >> 4);
+            const uint64_t a = dk + kr.slot * (kTileBytes >> 4);
             const uint64_t b = dq + qb * (K::kQRows * 128 >> 4);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)  // 32 dims: 32 bytes along the swizzled rows
               umma_e4m3_ss(tmem + 16 * (t & 1), a + 2 * kk, b + 2 * kk, kId, kk > 0);
             umma_commit(&sm.s_full[t & 1]);
-            umma_commit(&sm.k_empty[ks]);
+            umma_commit(&sm.k_empty[kr.slot]);
           }
           __syncwarp();
         }
@@ -501,12 +547,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   } else if (warp == kPvWarp) {
     // ------------------------------------------------------------------------ O += V^T P^T
     constexpr uint32_t kId = idesc_e4m3_f32(128, K::kNO, 1, 0);
-    const uint64_t dv = smem_desc_sw128(smem_addr(sm.v[0]), kTileBytes, 1024);
+    const uint64_t dv = smem_desc_sw128(smem_addr(v_ring), kTileBytes, 1024);
     const uint64_t dp = smem_desc_sw128(smem_addr(sm.p[0]), 16, 1024);
     auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
       return __all_sync(kFull, wait_parity(bar, parity, p.err));
     };
-    uint32_t taken = 0, units = 0, vt = 0, t = 0;
+    uint32_t taken = 0, units = 0, t = 0;
+    Ring vr;
     bool ok = true;
     while (ok) {
       const int slot = taken % kRing;
@@ -517,29 +564,28 @@ __global__ void __launch_bounds__(kThreads, 2)
       ++taken;
       if (ntiles < 0) break;
       if (skip) {
-        if (!(ok = wait_all(&sm.v_full[vt % kSlots], (vt / kSlots) & 1))) break;
-        if (lane == 0) mbar_arrive(&sm.v_empty[vt % kSlots]);
-        ++vt;
+        if (!(ok = wait_all(&sm.v_full[vr.slot], vr.parity))) break;
+        if (lane == 0) mbar_arrive(&sm.v_empty[vr.slot]);
+        vr.next(slots);
       }
       if (ntiles == 0) continue;
       const int ob = units & 1;
       // the unit before the last one's epilogue has read this accumulator
       if (units >= 2 && !(ok = wait_all(&sm.o_free[ob], ((units >> 1) - 1) & 1))) break;
       ++units;
-      for (int it = 0; it < ntiles; ++it, ++t, ++vt) {
-        const int vs = vt % kSlots;
-        if (!(ok = wait_all(&sm.v_full[vs], (vt / kSlots) & 1))) break;
+      for (int it = 0; it < ntiles; ++it, ++t, vr.next(slots)) {
+        if (!(ok = wait_all(&sm.v_full[vr.slot], vr.parity))) break;
         if (!(ok = wait_all(&sm.p_full[t & 1], (t >> 1) & 1))) break;
         tc_fence_after_sync();
         if (elect_one()) {
-          const uint64_t a = dv + vs * (kTileBytes >> 4);
+          const uint64_t a = dv + vr.slot * (kTileBytes >> 4);
           const uint64_t b = dp + (t & 1) * (K::kPRows * 128 >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)  // 32 tokens: 32 rows of V, 32 bytes of P's rows
             umma_e4m3_ss(tmem + K::kOBase + ob * K::kNO, a + kk * (32 * 128 >> 4), b + 2 * kk, kId,
                          it > 0 || kk > 0);
           umma_commit(&sm.pv_done[t & 1]);
-          umma_commit(&sm.v_empty[vs]);
+          umma_commit(&sm.v_empty[vr.slot]);
           if (it == ntiles - 1) umma_commit(&sm.o_full[ob]);
         }
         __syncwarp();
@@ -558,7 +604,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int i = threadIdx.x & 127, half = warp >> 2, quad = warp & 3;
     const int g0 = half * GH;
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-    uint32_t taken = 0, units = 0, vt = 0, t = 0;
+    uint32_t taken = 0, units = 0, t = 0;
+    Ring vr;
     while (true) {
       const int slot = taken % kRing;
       const bool got = wait_parity(&sm.unit_full[slot], (taken / kRing) & 1, p.err);
@@ -568,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (lane == 0) mbar_arrive(&sm.unit_empty[slot]);
       ++taken;
       if (un.ntiles < 0) break;
-      vt += un.skip;
+      if (un.skip) vr.next(slots);
       const int h = un.xg / p.head_groups, hg = un.xg % p.head_groups;
       const int heads = min(GC, p.group - hg * GC) - g0;  // of this thread (may be <= 0)
       int64_t L = p.context_lens[un.b];
@@ -591,12 +638,12 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int g = 0; g < GH; ++g) qsc[g] = sm.qscale[ub][g0 + g];
       }
-      for (int it = 0; it < un.ntiles; ++it, ++t, ++vt) {
-        const int vs = vt % kSlots, buf = t & 1;
+      for (int it = 0; it < un.ntiles; ++it, ++t, vr.next(slots)) {
+        const int vs = vr.slot, buf = t & 1;
         const int n_valid = tok_end - (tok_begin + it * kTile);  // >= 1; < 128 only in a last tile
         const bool valid = i < n_valid;
         // (all lanes of a warp together: the loads of tensor memory are the warp's)
-        ok = __all_sync(kFull, ok && wait_parity(&sm.v_full[vs], (vt / kSlots) & 1, p.err) &&
+        ok = __all_sync(kFull, ok && wait_parity(&sm.v_full[vs], vr.parity, p.err) &&
                                    wait_parity(&sm.s_full[buf], (t >> 1) & 1, p.err));
         float x[GH], inv_vs = 1.f;
         bool over = false;
@@ -682,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 2)
               }
           }
           if (!valid) {  // this token's V row is whatever the slot held: zero it (0 x NaN)
-            uint4 *v = reinterpret_cast<uint4 *>(sm.v[vs] + i * 128 + half * 64);
+            uint4 *v = reinterpret_cast<uint4 *>(v_ring + vs * kTileBytes + i * 128 + half * 64);
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[j] = make_uint4(0, 0, 0, 0);
           }
@@ -759,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (threadIdx.x >= kSoftmaxThreads) return;
   const uint32_t rank = cluster_ctarank();
   const bool lend = p.cluster > K::kLandSplits;
-  float *land_o = lend ? reinterpret_cast<float *>(sm.k[0])  // peer r + 1's outputs at [r][g][d]
+  float *land_o = lend ? reinterpret_cast<float *>(k_ring)  // peer r + 1's outputs at [r][g][d]
                        : reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(&sm) +
                                                    land_offset<GC>());
   float *land_lse = land_o + (size_t)(p.cluster - 1) * GC * kD;
@@ -818,7 +865,7 @@ cudaError_t launch_split_fp8(const CUtensorMap &km, const CUtensorMap &vm, const
   if (dev >= 64 || !configured[dev]) {
     cudaError_t e = cudaFuncSetAttribute(decode_fp8_kernel<GC, W>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)fp8_smem_bytes<GC>(Kind<GC>::kLandSplits));
+                                         (int)fp8_smem_bytes<GC>(kMaxSlots, Kind<GC>::kLandSplits));
     if (e != cudaSuccess) return e;
     // all of the unified L1/shared storage as shared memory, so two CTAs fit on an SM
     e = cudaFuncSetAttribute(decode_fp8_kernel<GC, W>,
@@ -830,7 +877,7 @@ cudaError_t launch_split_fp8(const CUtensorMap &km, const CUtensorMap &vm, const
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)std::min<int64_t>((int64_t)num_sms * 2, prm.units));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = fp8_smem_bytes<GC>(prm.cluster);
+  cfg.dynamicSmemBytes = fp8_smem_bytes<GC>(prm.ring_slots, prm.cluster);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -877,6 +924,7 @@ cudaError_t launch_paged_decode_fp8(const DecodeArgs &a, const DecodePlan &p,
   const bool queued = (int64_t)a.num_sms * 2 < units;
   if (!queued) prm.queue = nullptr;
   prm.cluster = !queued && p.splits >= 2 && p.splits <= kMaxCluster ? p.splits : 0;
+  prm.ring_slots = units <= a.num_sms ? kMaxSlots : kSlotsShared;
   const bool w = p.scores_at != 0;
   auto split = [&](auto launch) { return launch(km, vm, km8, vm8, prm, a.num_sms, stream); };
   const cudaError_t e =
