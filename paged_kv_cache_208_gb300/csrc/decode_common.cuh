@@ -61,8 +61,7 @@ struct DecodeParams {
   uint16_t *k_cache_w;
   uint16_t *v_cache_w;
   int32_t num_kv_heads;
-  // 8-bit cache: [num_blocks, num_kv_heads, block_size / 64], and the slots of a tile ring
-  int32_t ring_slots;
+  // 8-bit cache: [num_blocks, num_kv_heads, block_size / 64]
   const float *k_scale;
   const float *v_scale;
   // for the weights kernel: scores [batch, num_q_heads, score_stride] (log2 domain) and the

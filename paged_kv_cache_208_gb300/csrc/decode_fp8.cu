@@ -46,10 +46,10 @@ namespace {
 
 constexpr int kTile = 128;
 constexpr int kTileBytes = kTile * kD;  // one head's K or V codes of a tile: 16 KiB
-// Slots of the K ring and of the V ring. A slot of V is taken from the load's issue until its PV
-// has completed, some 2 us, so a ring of three moves a tile every 0.65 us: enough when two CTAs
-// share an SM's bandwidth. A grid of no more CTAs than SMs has the SM's shared memory to itself.
-constexpr int kSlotsShared = 3, kMaxSlots = 6;
+// Slots of the K ring and of the V ring. (Six, for grids of one CTA per SM, were no faster -- one
+// CTA's loads arrive at a tile per 0.65 us either way -- and clusters of 5 and more then do not
+// all fit at once.)
+constexpr int kSlots = 3;
 constexpr int kSoftmaxWarps = 8;  // two for each quadrant of tensor memory's lanes
 constexpr int kSoftmaxThreads = kSoftmaxWarps * 32;
 constexpr int kSWarp = 8, kPvWarp = 9, kLoadWarp = 10;
@@ -80,21 +80,30 @@ struct Kind {
 // Q and P tiles have rows of 128 bytes, 128-byte swizzle. N = 16 (or 32) rows are multiplied;
 // those past the allocated ones run into what follows in shared memory (the next buffer; from
 // the last Q tile the queued q rows), and give columns that nothing reads.
-// Before this structure lie the K ring and the V ring, `slots` tiles of 16 KiB each.
+// A unit as the loader hands it out: everything about it that the others need.
+struct Unit8 {
+  int32_t b, s, xg, ntiles;  // ntiles < 0: no more work
+  int32_t tokens;            // of the split
+  int32_t whole;             // the split is the whole context: its result is the output
+  int32_t skip;              // the ring's next tile is a speculative load to be dropped
+};
+
 template <int GC>
 struct DecodeFp8Smem {
   using K = Kind<GC>;
-  uint8_t p[2][K::kPRows * 128];  // 1024-byte aligned (128-byte swizzle atoms)
+  uint8_t k[kSlots][kTileBytes];  // 1024-byte aligned (128-byte swizzle atoms)
+  uint8_t v[kSlots][kTileBytes];
+  uint8_t p[2][K::kPRows * 128];
   uint8_t q[2][K::kQRows * 128];
   uint16_t qs[K::kRing][GC][kD];  // q rows of the queued units, as they came
-  alignas(16) float tile_scale[kMaxSlots][2][4];  // scales of the tile's page: K's, V's
+  alignas(16) float tile_scale[kSlots][2][4];  // scales of the tile's page: K's, V's
   float qscale[2][GC];                         // softmax scale log2(e) over q's power of two
   float warp_max[kSoftmaxWarps][GC / 2];
   float warp_l[2][kSoftmaxWarps][GC / 2];
-  Unit unit[K::kRing];
+  Unit8 unit[K::kRing];
   int32_t stop;  // set by the producer: an earlier wait gave up, this CTA does no work
   uint32_t tmem_base;
-  uint64_t k_full[kMaxSlots], k_empty[kMaxSlots], v_full[kMaxSlots], v_empty[kMaxSlots];
+  uint64_t k_full[kSlots], k_empty[kSlots], v_full[kSlots], v_empty[kSlots];
   uint64_t q_ready[2], s_full[2], p_full[2], pv_done[2], o_full[2], o_free[2];
   uint64_t unit_full[K::kRing], unit_empty[K::kRing];
   uint64_t drain[2];
@@ -106,29 +115,24 @@ __host__ __device__ constexpr size_t land_offset() {
   return (sizeof(DecodeFp8Smem<GC>) + 15) / 16 * 16;
 }
 template <int GC>
-__host__ __device__ constexpr size_t fp8_smem_bytes(int slots, int cluster) {
-  return 2 * (size_t)slots * kTileBytes +
-         (cluster >= 2 && cluster <= Kind<GC>::kLandSplits
+__host__ __device__ constexpr size_t fp8_smem_bytes(int cluster) {
+  return (cluster >= 2 && cluster <= Kind<GC>::kLandSplits
               ? land_offset<GC>() + (size_t)(cluster - 1) * GC * (kD + 1) * sizeof(float)
               : sizeof(DecodeFp8Smem<GC>)) + 1024;  // + 1024: the layout starts 1024-aligned
 }
-// two CTAs per SM: 228 KiB less 1 KiB each that the system keeps; one: 227 KiB
-static_assert(fp8_smem_bytes<2>(kSlotsShared, 4) <= 113 * 1024 &&
-                  fp8_smem_bytes<4>(kSlotsShared, 1) <= 113 * 1024 &&
-                  fp8_smem_bytes<8>(kSlotsShared, 1) <= 113 * 1024,
+// two CTAs per SM: 228 KiB less 1 KiB each that the system keeps
+static_assert(fp8_smem_bytes<2>(4) <= 113 * 1024 && fp8_smem_bytes<4>(1) <= 113 * 1024 &&
+                  fp8_smem_bytes<8>(1) <= 113 * 1024,
               "two CTAs fit on an SM");
-static_assert(fp8_smem_bytes<2>(kMaxSlots, 4) <= 227 * 1024 &&
-                  fp8_smem_bytes<8>(kMaxSlots, 1) <= 227 * 1024,
-              "one CTA fits on an SM");
-static_assert((kMaxCluster - 1) * 8 * (kD + 1) * sizeof(float) <= kSlotsShared * kTileBytes,
+static_assert((kMaxCluster - 1) * 8 * (kD + 1) * sizeof(float) <= kSlots * kTileBytes,
               "the peers' results fit in rank 0's K slots");
 
-// A position in a ring of n slots: the slot, and the parity of the phase a use of it completes.
+// A position in a ring of tiles: the slot, and the parity of the phase a use of it completes.
 struct Ring {
   int slot = 0;
   uint32_t parity = 0;
-  __device__ __forceinline__ void next(int n) {
-    if (++slot == n) {
+  __device__ __forceinline__ void next() {
+    if (++slot == kSlots) {
       slot = 0;
       parity ^= 1u;
     }
@@ -161,16 +165,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   using K = Kind<GC>;
   constexpr int kRing = K::kRing, GH = K::kGH;
   extern __shared__ uint8_t smem_raw[];
-  const int slots = p.ring_slots;
-  uint8_t *const k_ring = reinterpret_cast<uint8_t *>(
+  DecodeFp8Smem<GC> &sm = *reinterpret_cast<DecodeFp8Smem<GC> *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *const v_ring = k_ring + slots * kTileBytes;
-  DecodeFp8Smem<GC> &sm =
-      *reinterpret_cast<DecodeFp8Smem<GC> *>(v_ring + slots * kTileBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     sm.stop = 0;
-    for (int i = 0; i < slots; ++i) {
+    for (int i = 0; i < kSlots; ++i) {
       mbar_init(&sm.k_full[i], 1);
       mbar_init(&sm.k_empty[i], 1);
       mbar_init(&sm.v_full[i], 1);
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.q_ready[i], 1);
-      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.s_full[i], 2);
       mbar_init(&sm.p_full[i], kSoftmaxWarps);
       mbar_init(&sm.pv_done[i], 1);
       mbar_init(&sm.o_full[i], 1);
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             ld_global_cg_s32(p.block_tables + (int64_t)b * p.table_width + begin / p.block_size);
         if (blk >= 0 && blk < p.num_blocks) {
           const int in_block = (int)(begin % p.block_size);
-          const int n = min(2 * slots, min(p.chunk, p.block_size - in_block) / kTile);
+          const int n = min(2 * kSlots, min(p.chunk, p.block_size - in_block) / kTile);
           spec_h = xg / p.head_groups;
           spec_blk = blk;
           spec_row = (int32_t)((int64_t)blk * p.block_size + in_block);
@@ -289,21 +289,20 @@ __global__ void __launch_bounds__(kThreads, 2)
       bool spec_pending = false;
       if (spec_row >= 0) {
         mbar_arrive_expect_tx(&sm.k_full[0], kTileBytes);
-        tma_load_3d(k_ring, &kmap, &sm.k_full[0], 0, spec_row, spec_h, policy);
+        tma_load_3d(sm.k[0], &kmap, &sm.k_full[0], 0, spec_row, spec_h, policy);
         mbar_arrive_expect_tx(&sm.v_full[0], kTileBytes + kScaleBytes);
-        tma_load_3d(v_ring, &vmap, &sm.v_full[0], 0, spec_row, spec_h, policy);
+        tma_load_3d(sm.v[0], &vmap, &sm.v_full[0], 0, spec_row, spec_h, policy);
         load_scales(0, spec_blk, (int)(spec_row - (int64_t)spec_blk * p.block_size), spec_h);
-        kr.next(slots);
-        vr.next(slots);
+        kr.next();
+        vr.next();
         k_issued = v_issued = 1;
         spec_pending = true;
       }
       while (ok) {
         // next unit with work (or one that must write zeros); ntiles < 0 ends the walk
-        Unit un{0, 0, 0, -1, 0, 0};
+        Unit8 un{0, 0, 0, -1, 0, 0, 0};
         int32_t first_blk = -1;   // block id of the unit's first tile
         int first_it = 0;         // tiles of the unit already loaded
-        int last_rows = kTile;    // tokens in the unit's last tile
         while (true) {
           int u;
           if (p.queue) {
@@ -337,8 +336,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
           if (begin < L) {
             const int64_t end = min(L, begin + p.chunk);
-            un = Unit{b, s, xg, (int)((end - begin + kTile - 1) / kTile), 0, 0};
-            last_rows = (int)(end - begin - (int64_t)(un.ntiles - 1) * kTile);
+            un = Unit8{b, s, xg, (int)((end - begin + kTile - 1) / kTile), (int)(end - begin),
+                       p.splits == 1 || (s == 0 && end == L) ? 1 : 0, 0};
             if (spec_pending) {
               if (first_blk == spec_blk) first_it = 1;
               else un.skip = 1;
@@ -349,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (p.cluster || (L == 0 && s == 0 && p.splits == 1)) {
             // nothing to read: zeros (empty context), or in a cluster no result (the unit
             // still leaves its -inf log2-sum-exp for the merge)
-            un = Unit{b, s, xg, 0, 0, spec_pending ? 1 : 0};
+            un = Unit8{b, s, xg, 0, 0, p.splits == 1 ? 1 : 0, spec_pending ? 1 : 0};
             spec_pending = false;
             break;
           }
@@ -377,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int32_t *entry =
             p.block_tables + (int64_t)un.b * p.table_width + un.s * p.chunk / p.block_size;
         int in_block = un.s * p.chunk % p.block_size;
-        int left = (un.ntiles - 1) * kTile + last_rows;  // tokens from the current tile on
+        int left = un.tokens;  // from the current tile on
         int32_t blk = first_blk, next_blk = -1;
         if (left > p.block_size - in_block) next_blk = ld_global_s32(++entry);
         for (int it = 0; it < un.ntiles; ++it) {
@@ -401,11 +400,11 @@ __global__ void __launch_bounds__(kThreads, 2)
           const uint32_t bytes = chunks ? chunks * kChunkBytes : kTileBytes;
           // (a slot's first use finds it empty; later ones wait for the use before, whose phase has
           // the other parity)
-          if (k_issued == slots && !wait_parity(&sm.k_empty[kr.slot], kr.parity ^ 1u, p.err)) {
+          if (k_issued == kSlots && !wait_parity(&sm.k_empty[kr.slot], kr.parity ^ 1u, p.err)) {
             ok = false;
             break;
           }
-          uint8_t *kd = k_ring + kr.slot * kTileBytes, *vd = v_ring + vr.slot * kTileBytes;
+          uint8_t *kd = sm.k[kr.slot], *vd = sm.v[vr.slot];
           uint64_t *kbar = &sm.k_full[kr.slot], *vbar = &sm.v_full[vr.slot];
           mbar_arrive_expect_tx(kbar, bytes);
           if (chunks)
@@ -413,9 +412,9 @@ __global__ void __launch_bounds__(kThreads, 2)
               tma_load_3d(kd + c * kChunkBytes, &kmap8, kbar, 0, row + kChunkRows * c, h, policy);
           else
             tma_load_3d(kd, &kmap, kbar, 0, row, h, policy);
-          kr.next(slots);
-          k_issued = min(k_issued + 1, slots);
-          if (v_issued == slots && !wait_parity(&sm.v_empty[vr.slot], vr.parity ^ 1u, p.err)) {
+          kr.next();
+          k_issued = min(k_issued + 1, kSlots);
+          if (v_issued == kSlots && !wait_parity(&sm.v_empty[vr.slot], vr.parity ^ 1u, p.err)) {
             ok = false;
             break;
           }
@@ -427,8 +426,8 @@ __global__ void __launch_bounds__(kThreads, 2)
               tma_load_3d(vd + c * kChunkBytes, &vmap8, vbar, 0, row + kChunkRows * c, h, policy);
           else
             tma_load_3d(vd, &vmap, vbar, 0, row, h, policy);
-          vr.next(slots);
-          v_issued = min(v_issued + 1, slots);
+          vr.next();
+          v_issued = min(v_issued + 1, kSlots);
         }
       }
       // a CTA that stopped early still draws past the last unit once, so that the counter goes
@@ -451,29 +450,29 @@ __global__ void __launch_bounds__(kThreads, 2)
   } else if (warp == kSWarp) {
     // ------------------------------------------------------------------------ S = K Q^T
     constexpr uint32_t kId = idesc_e4m3_f32(128, 16, 0, 0);
-    const uint64_t dk = smem_desc_sw128(smem_addr(k_ring), 16, 1024);
+    const uint64_t dk = smem_desc_sw128(smem_addr(sm.k[0]), 16, 1024);
     const uint64_t dq = smem_desc_sw128(smem_addr(sm.q[0]), 16, 1024);
     auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
       return __all_sync(kFull, wait_parity(bar, parity, p.err));
     };
     uint32_t taken = 0, units = 0, t = 0;  // t: tiles computed
-    Ring kr;
+    Ring kr, vr;
     bool ok = true;
     while (ok) {
       const int slot = taken % kRing;
       if (!(ok = wait_all(&sm.unit_full[slot], (taken / kRing) & 1))) break;
-      const Unit un = sm.unit[slot];
+      const Unit8 un = sm.unit[slot];
       ++taken;
       if (un.ntiles < 0) break;
       if (un.skip) {  // a speculative load that did not hold: let it land, drop it
         if (!(ok = wait_all(&sm.k_full[kr.slot], kr.parity))) break;
         if (lane == 0) mbar_arrive(&sm.k_empty[kr.slot]);
-        kr.next(slots);
+        kr.next();
+        vr.next();
       }
       if (un.ntiles > 0) {
         // This unit's Q tile was last read by the unit before the last one, all of whose tiles
-        // precede tile t - 1: their S is complete once the softmax has answered tile t - 2 (the
-        // wait that S(t) needs for its buffer too).
+        // precede tile t - 1: their S is complete once the softmax has answered tile t - 2.
         if (t >= 2 && !(ok = wait_all(&sm.p_full[t & 1], ((t - 2) >> 1) & 1))) break;
         const int qb = units & 1;
         const int heads = min(GC, p.group - (un.xg % p.head_groups) * GC);
@@ -519,10 +518,13 @@ __global__ void __launch_bounds__(kThreads, 2)
           mbar_arrive(&sm.unit_empty[slot]);
         }
         ++units;
-        for (int it = 0; it < un.ntiles; ++it, ++t, kr.next(slots)) {
+        for (int it = 0; it < un.ntiles; ++it, ++t, kr.next(), vr.next()) {
+          // S(t)'s buffer was tile t - 2's, which the softmax has read; P(t)'s was tile t - 2's
+          // too, which its PV has read. With V's tile (and the scales) here as well, s_full tells
+          // the softmax threads all they would else wait for one by one, 100 cycles each.
+          if (t >= 2 && !(ok = wait_all(&sm.pv_done[t & 1], ((t - 2) >> 1) & 1))) break;
           if (!(ok = wait_all(&sm.k_full[kr.slot], kr.parity))) break;
-          // S(t)'s buffer was tile t - 2's, which the softmax has read
-          if (it > 0 && t >= 2 && !(ok = wait_all(&sm.p_full[t & 1], ((t - 2) >> 1) & 1))) break;
+          if (!(ok = wait_all(&sm.v_full[vr.slot], vr.parity))) break;
           tc_fence_after_sync();
           if (elect_one()) {
             const uint64_t a = dk + kr.slot * (kTileBytes >> 4);
@@ -530,6 +532,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)  // 32 dims: 32 bytes along the swizzled rows
               umma_e4m3_ss(tmem + 16 * (t & 1), a + 2 * kk, b + 2 * kk, kId, kk > 0);
+            mbar_arrive(&sm.s_full[t & 1]);  // (releases what this thread has seen)
             umma_commit(&sm.s_full[t & 1]);
             umma_commit(&sm.k_empty[kr.slot]);
           }
@@ -547,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   } else if (warp == kPvWarp) {
     // ------------------------------------------------------------------------ O += V^T P^T
     constexpr uint32_t kId = idesc_e4m3_f32(128, K::kNO, 1, 0);
-    const uint64_t dv = smem_desc_sw128(smem_addr(v_ring), kTileBytes, 1024);
+    const uint64_t dv = smem_desc_sw128(smem_addr(sm.v[0]), kTileBytes, 1024);
     const uint64_t dp = smem_desc_sw128(smem_addr(sm.p[0]), 16, 1024);
     auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
       return __all_sync(kFull, wait_parity(bar, parity, p.err));
@@ -566,14 +569,14 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (skip) {
         if (!(ok = wait_all(&sm.v_full[vr.slot], vr.parity))) break;
         if (lane == 0) mbar_arrive(&sm.v_empty[vr.slot]);
-        vr.next(slots);
+        vr.next();
       }
       if (ntiles == 0) continue;
       const int ob = units & 1;
       // the unit before the last one's epilogue has read this accumulator
       if (units >= 2 && !(ok = wait_all(&sm.o_free[ob], ((units >> 1) - 1) & 1))) break;
       ++units;
-      for (int it = 0; it < ntiles; ++it, ++t, vr.next(slots)) {
+      for (int it = 0; it < ntiles; ++it, ++t, vr.next()) {
         if (!(ok = wait_all(&sm.v_full[vr.slot], vr.parity))) break;
         if (!(ok = wait_all(&sm.p_full[t & 1], (t >> 1) & 1))) break;
         tc_fence_after_sync();
@@ -610,18 +613,15 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int slot = taken % kRing;
       const bool got = wait_parity(&sm.unit_full[slot], (taken / kRing) & 1, p.err);
       if (barrier_or(1, kSoftmaxThreads, !got)) break;
-      const Unit un = sm.unit[slot];
+      const Unit8 un = sm.unit[slot];
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.unit_empty[slot]);
       ++taken;
       if (un.ntiles < 0) break;
-      if (un.skip) vr.next(slots);
+      if (un.skip) vr.next();
       const int h = un.xg / p.head_groups, hg = un.xg % p.head_groups;
       const int heads = min(GC, p.group - hg * GC) - g0;  // of this thread (may be <= 0)
-      int64_t L = p.context_lens[un.b];
-      L = L < 0 ? 0 : (L > p.cap ? p.cap : L);
       const int tok_begin = un.s * p.chunk;
-      const int tok_end = (int)min(L, (int64_t)tok_begin + p.chunk);
       const int64_t row0 = (int64_t)un.b * p.num_q_heads + h * p.group + hg * GC + g0;
       const int ub = units & 1;
       const uint32_t o_addr = lanes + K::kOBase + ub * K::kNO + 3 * g0;
@@ -638,13 +638,12 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int g = 0; g < GH; ++g) qsc[g] = sm.qscale[ub][g0 + g];
       }
-      for (int it = 0; it < un.ntiles; ++it, ++t, vr.next(slots)) {
+      for (int it = 0; it < un.ntiles; ++it, ++t, vr.next()) {
         const int vs = vr.slot, buf = t & 1;
-        const int n_valid = tok_end - (tok_begin + it * kTile);  // >= 1; < 128 only in a last tile
+        const int n_valid = un.tokens - it * kTile;  // >= 1; < 128 only in a last tile
         const bool valid = i < n_valid;
         // (all lanes of a warp together: the loads of tensor memory are the warp's)
-        ok = __all_sync(kFull, ok && wait_parity(&sm.v_full[vs], vr.parity, p.err) &&
-                                   wait_parity(&sm.s_full[buf], (t >> 1) & 1, p.err));
+        ok = __all_sync(kFull, ok && wait_parity(&sm.s_full[buf], (t >> 1) & 1, p.err));
         float x[GH], inv_vs = 1.f;
         bool over = false;
         if (ok) {
@@ -704,9 +703,6 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
           }
         }
-        // P(t)'s buffer was tile t - 2's, which its PV has read
-        if (t >= 2)
-          ok = __all_sync(kFull, ok && wait_parity(&sm.pv_done[buf], ((t - 2) >> 1) & 1, p.err));
         if (ok) {
           uint8_t *pt = sm.p[buf] + (i & 15);
           float w[GH + 1];
@@ -729,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 2)
               }
           }
           if (!valid) {  // this token's V row is whatever the slot held: zero it (0 x NaN)
-            uint4 *v = reinterpret_cast<uint4 *>(v_ring + vs * kTileBytes + i * 128 + half * 64);
+            uint4 *v = reinterpret_cast<uint4 *>(sm.v[vs] + i * 128 + half * 64);
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[j] = make_uint4(0, 0, 0, 0);
           }
@@ -780,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           cl_lse[g] = lse;
         } else if (g < heads) {
           const int64_t row = row0 + g;
-          if (p.splits == 1 || (un.s == 0 && tok_end == L)) {
+          if (un.whole) {
             // the unit holds the whole context: the output itself (the merge kernel skips it)
             p.out[row * kD + i] = bf16_bits_rn(out);
             if (W && i == 0) p.lse[row] = lse;
@@ -806,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (threadIdx.x >= kSoftmaxThreads) return;
   const uint32_t rank = cluster_ctarank();
   const bool lend = p.cluster > K::kLandSplits;
-  float *land_o = lend ? reinterpret_cast<float *>(k_ring)  // peer r + 1's outputs at [r][g][d]
+  float *land_o = lend ? reinterpret_cast<float *>(sm.k[0])  // peer r + 1's outputs at [r][g][d]
                        : reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(&sm) +
                                                    land_offset<GC>());
   float *land_lse = land_o + (size_t)(p.cluster - 1) * GC * kD;
@@ -865,7 +861,7 @@ cudaError_t launch_split_fp8(const CUtensorMap &km, const CUtensorMap &vm, const
   if (dev >= 64 || !configured[dev]) {
     cudaError_t e = cudaFuncSetAttribute(decode_fp8_kernel<GC, W>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)fp8_smem_bytes<GC>(kMaxSlots, Kind<GC>::kLandSplits));
+                                         (int)fp8_smem_bytes<GC>(Kind<GC>::kLandSplits));
     if (e != cudaSuccess) return e;
     // all of the unified L1/shared storage as shared memory, so two CTAs fit on an SM
     e = cudaFuncSetAttribute(decode_fp8_kernel<GC, W>,
@@ -877,7 +873,7 @@ cudaError_t launch_split_fp8(const CUtensorMap &km, const CUtensorMap &vm, const
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)std::min<int64_t>((int64_t)num_sms * 2, prm.units));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = fp8_smem_bytes<GC>(prm.ring_slots, prm.cluster);
+  cfg.dynamicSmemBytes = fp8_smem_bytes<GC>(prm.cluster);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -924,7 +920,6 @@ cudaError_t launch_paged_decode_fp8(const DecodeArgs &a, const DecodePlan &p,
   const bool queued = (int64_t)a.num_sms * 2 < units;
   if (!queued) prm.queue = nullptr;
   prm.cluster = !queued && p.splits >= 2 && p.splits <= kMaxCluster ? p.splits : 0;
-  prm.ring_slots = units <= a.num_sms ? kMaxSlots : kSlotsShared;
   const bool w = p.scores_at != 0;
   auto split = [&](auto launch) { return launch(km, vm, km8, vm8, prm, a.num_sms, stream); };
   const cudaError_t e =
