@@ -22,8 +22,7 @@ namespace pkv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPerThread = 8;
-constexpr int kSpan = kThreads * kPerThread;  // positions of a CTA
+constexpr int kSpan = kThreads * 4;  // positions of a CTA: four consecutive ones to a thread
 
 struct WeightsParams {
   const float *scores;
@@ -36,6 +35,7 @@ struct WeightsParams {
   float *out;
   int64_t out_stride;
   int32_t hkv, group;
+  bool vec;  // the rows of in and out are 16-byte aligned
   const unsigned int *err;
 };
 
@@ -47,27 +47,37 @@ __global__ void __launch_bounds__(kThreads) decode_weights_kernel(const WeightsP
   const int64_t b = bh / p.hkv;
   int64_t L = p.context_lens[b];
   L = L < 0 ? 0 : min(L, p.cap);
-  for (int64_t i0 = (int64_t)blockIdx.y * kSpan + threadIdx.x; i0 < L;
-       i0 += (int64_t)gridDim.y * kSpan) {
-    float before[kPerThread], w[kPerThread] = {};
-#pragma unroll
-    for (int j = 0; j < kPerThread; ++j) {
-      const int64_t i = i0 + j * kThreads;
-      before[j] = p.in && i < L ? p.in[bh * p.in_stride + i] : 0.f;
+  const float *const in = p.in ? p.in + bh * p.in_stride : nullptr;
+  float *const out = p.out + bh * p.out_stride;
+  for (int64_t i = (int64_t)blockIdx.y * kSpan + 4 * threadIdx.x; i < L;
+       i += (int64_t)gridDim.y * kSpan) {
+    const float *s = p.scores + bh * p.group * p.score_stride + i;  // 16-byte aligned
+    float4 w = make_float4(0.f, 0.f, 0.f, 0.f), before = w;
+    const bool whole = p.vec && i + 4 <= L;
+    if (in && whole) {
+      before = *reinterpret_cast<const float4 *>(in + i);
+    } else if (in) {
+      before.x = in[i];
+      if (i + 1 < L) before.y = in[i + 1];
+      if (i + 2 < L) before.z = in[i + 2];
+      if (i + 3 < L) before.w = in[i + 3];
     }
-    const float *s = p.scores + bh * p.group * p.score_stride;
     for (int g = 0; g < p.group; ++g, s += p.score_stride) {
       const float lse = p.lse[bh * p.group + g];
-#pragma unroll
-      for (int j = 0; j < kPerThread; ++j) {
-        const int64_t i = i0 + j * kThreads;
-        if (i < L) w[j] += fast_exp2(s[i] - lse);
-      }
+      const float4 x = *reinterpret_cast<const float4 *>(s);  // (entries past L: not used)
+      w.x += fast_exp2(x.x - lse);
+      w.y += fast_exp2(x.y - lse);
+      w.z += fast_exp2(x.z - lse);
+      w.w += fast_exp2(x.w - lse);
     }
-#pragma unroll
-    for (int j = 0; j < kPerThread; ++j) {
-      const int64_t i = i0 + j * kThreads;
-      if (i < L) p.out[bh * p.out_stride + i] = before[j] + w[j];
+    w = make_float4(before.x + w.x, before.y + w.y, before.z + w.z, before.w + w.w);
+    if (whole) {
+      *reinterpret_cast<float4 *>(out + i) = w;
+    } else {
+      out[i] = w.x;
+      if (i + 1 < L) out[i + 1] = w.y;
+      if (i + 2 < L) out[i + 2] = w.z;
+      if (i + 3 < L) out[i + 3] = w.w;
     }
   }
 }
@@ -132,6 +142,8 @@ pkv_status decode_with_weights(Call c, cudaStream_t stream) {
   w.out_stride = c.weights_out_stride;
   w.hkv = a.num_kv_heads;
   w.group = a.num_q_heads / a.num_kv_heads;
+  w.vec = (!w.in || (aligned16(w.in) && w.in_stride % 4 == 0)) && aligned16(w.out) &&
+          w.out_stride % 4 == 0;
   w.err = a.err;
   const int64_t spans = ((int64_t)c.max_context_len + kSpan - 1) / kSpan;
   e = launch_after(decode_weights_kernel,

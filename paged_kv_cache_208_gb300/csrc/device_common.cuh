@@ -467,6 +467,13 @@ __device__ __forceinline__ void record_error(unsigned int *err, unsigned int bit
   if (err) atomicOr(err, bit);
 }
 
+// One 32-byte global store (sm_100 and later); p must be 32-byte aligned.
+__device__ __forceinline__ void st_global_32b(void *p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 // 16 bytes that are read once, by a kernel that started before its predecessor ended (a plain
 // load, not one through the read-only path: the data may be the predecessor's).
 __device__ __forceinline__ uint4 ld_once_u4(const uint4 *p) {

@@ -41,8 +41,35 @@ struct StoreParams {
   float *k_scale, *v_scale;
   int32_t hkv, block_size;
   int64_t num_blocks;
+  bool wide;  // rows and strides of k and v are 32-byte aligned
   unsigned int *err;
 };
+
+// 32 bytes of a bf16 row
+struct Row32 {
+  uint4 lo, hi;
+};
+__device__ __forceinline__ uint32_t absmax8(const uint4 &x) {
+  return __vmaxu2(bf16x2_absmax(x.x, x.y), bf16x2_absmax(x.z, x.w));
+}
+__device__ __forceinline__ uint4 finite8(const uint4 &x) {
+  return make_uint4(bf16x2_finite(x.x), bf16x2_finite(x.y), bf16x2_finite(x.z),
+                    bf16x2_finite(x.w));
+}
+// (one load where the address allows it)
+__device__ __forceinline__ void ld_once_32b(const uint8_t *p, bool wide, uint4 &lo, uint4 &hi) {
+  if (wide) {
+    asm volatile(
+        "ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(lo.x), "=r"(lo.y), "=r"(lo.z), "=r"(lo.w), "=r"(hi.x), "=r"(hi.y), "=r"(hi.z),
+          "=r"(hi.w)
+        : "l"(p)
+        : "memory");
+  } else {
+    lo = ld_once_u4(reinterpret_cast<const uint4 *>(p));
+    hi = ld_once_u4(reinterpret_cast<const uint4 *>(p + 16));
+  }
+}
 
 // Block of position pos of a sequence's table row, or -1 (recorded) for a bad id.
 __device__ __forceinline__ int64_t block_of(const int32_t *table, int64_t pos, int32_t block_size,
@@ -69,13 +96,14 @@ __device__ __forceinline__ void check_lengths(const int32_t *cu, const int32_t *
 
 // One CTA: K or V of a run (up to 64 rows of one group) for `heads_per_cta` consecutive heads, one
 // head at a time while the next one's rows are on their way: thread t holds bytes
-// [16 (t % 16), +16) of rows t / 16 + 8 i. A CTA has 32 KiB in flight and five fit on an SM;
-// going through the heads in one CTA pays the dependent loads of its start (cu_seqlens, the
-// table, 2-3 us) once: 145k tokens of 8 heads take XX us (YY of HBM's rate), 255 us with a CTA of
-// 256 threads for each head, K and V together.
+// [32 (t % 8), +32) of rows t / 8 + 16 i. A CTA has 32 KiB in flight and five fit on an SM; going
+// through the heads in one CTA pays the dependent loads of its start (cu_seqlens, the table,
+// 2-3 us) once. 145k tokens of 8 heads take 127 us (6.6 TB/s): 255 us with a CTA of 256 threads
+// for each head, K and V together; 139 us with 16-byte loads and plain 8-byte stores; 130 us with
+// those stores marked as not read again.
 constexpr int kRunThreads = 128;
 constexpr int kRunWarps = kRunThreads / 32;
-constexpr int kRowsPerPass = kRunThreads / 16;
+constexpr int kRowsPerPass = kRunThreads / 8;
 constexpr int kPasses = kFp8Group / kRowsPerPass;
 
 __global__ void __launch_bounds__(kRunThreads, 5)
@@ -102,17 +130,16 @@ __global__ void __launch_bounds__(kRunThreads, 5)
   const int64_t end = min((int64_t)ctx, (group + 1) * kFp8Group);
   if (j < 0 || begin >= end) return;
   const int rows = (int)(end - begin);
-  const int part = threadIdx.x & 15, row0 = threadIdx.x >> 4;
+  const int part = threadIdx.x & 7, row0 = threadIdx.x >> 3;
   const int64_t stride = is_v ? p.v_stride : p.k_stride;
-  const uint8_t *src = (is_v ? p.v : p.k) + (c0 + begin - start + row0) * stride + part * 16;
-  uint4 x[2][kPasses];
-  auto load = [&](uint4(&y)[kPasses], int h) {
+  const uint8_t *src = (is_v ? p.v : p.k) + (c0 + begin - start + row0) * stride + part * 32;
+  Row32 x[2][kPasses];
+  auto load = [&](Row32(&y)[kPasses], int h) {
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-      y[i] = make_uint4(0, 0, 0, 0);
+      y[i].lo = y[i].hi = make_uint4(0, 0, 0, 0);
       if (row0 + i * kRowsPerPass < rows)
-        y[i] = ld_once_u4(
-            reinterpret_cast<const uint4 *>(src + i * kRowsPerPass * stride + h * (kD * 2)));
+        ld_once_32b(src + i * kRowsPerPass * stride + h * (kD * 2), p.wide, y[i].lo, y[i].hi);
     }
   };
   load(x[0], h0);
@@ -138,18 +165,17 @@ __global__ void __launch_bounds__(kRunThreads, 5)
     buf ^= 1;  // (the next use of this half is two barriers away)
     return m;
   };
-  auto store = [&](const uint4(&y)[kPasses], int h) {
+  auto store = [&](const Row32(&y)[kPasses], int h) {
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < kPasses; ++i)
-      m = __vmaxu2(m, __vmaxu2(bf16x2_absmax(y[i].x, y[i].y), bf16x2_absmax(y[i].z, y[i].w)));
+      m = __vmaxu2(m, __vmaxu2(absmax8(y[i].lo), absmax8(y[i].hi)));
     m = cta_max(m);
     if (m >= 0x7f80u) {  // infinities or NaNs: the largest finite value counts
       m = 0;
 #pragma unroll
       for (int i = 0; i < kPasses; ++i)
-        m = __vmaxu2(m, __vmaxu2(bf16x2_absmax(bf16x2_finite(y[i].x), bf16x2_finite(y[i].y)),
-                                 bf16x2_absmax(bf16x2_finite(y[i].z), bf16x2_finite(y[i].w))));
+        m = __vmaxu2(m, __vmaxu2(absmax8(finite8(y[i].lo)), absmax8(finite8(y[i].hi))));
       m = cta_max(m);
     }
     const int64_t sc = (blk * p.hkv + h) * (p.block_size / kFp8Group) + in_block / kFp8Group;
@@ -179,8 +205,10 @@ __global__ void __launch_bounds__(kRunThreads, 5)
     for (int i = 0; i < kPasses; ++i) {
       const int row = row0 + i * kRowsPerPass;
       if (row < rows)
-        *reinterpret_cast<uint2 *>(dst + row * rstride + part * 8) =
-            make_uint2(quantize4(y[i].x, y[i].y, inv), quantize4(y[i].z, y[i].w, inv));
+        __stcs(reinterpret_cast<uint4 *>(dst + row * rstride + part * 16),
+               make_uint4(quantize4(y[i].lo.x, y[i].lo.y, inv), quantize4(y[i].lo.z, y[i].lo.w, inv),
+                          quantize4(y[i].hi.x, y[i].hi.y, inv),
+                          quantize4(y[i].hi.z, y[i].hi.w, inv)));
     }
   };
   for (int h = h0; h < h1; h += 2) {
@@ -221,11 +249,10 @@ __global__ void __launch_bounds__(kTokenWarps * 32)
   const int64_t sc = (blk * p.hkv + h) * (p.block_size / kFp8Group) + in_block / kFp8Group;
   float *scales = is_v ? p.v_scale : p.k_scale;
   const float old = before ? scales[sc] : 0.f;
-  uint32_t m = __vmaxu2(bf16x2_absmax(x.x, x.y), bf16x2_absmax(x.z, x.w));
+  uint32_t m = absmax8(x);
   m = max(m & 0xffffu, m >> 16);
   if (m >= 0x7f80u) {
-    m = __vmaxu2(bf16x2_absmax(bf16x2_finite(x.x), bf16x2_finite(x.y)),
-                 bf16x2_absmax(bf16x2_finite(x.z), bf16x2_finite(x.w)));
+    m = absmax8(finite8(x));
     m = max(m & 0xffffu, m >> 16);
   }
 #pragma unroll
@@ -264,7 +291,8 @@ struct GatherParams {
 
 // One CTA: K or V of `rows_per_cta` rows of a run (up to 64 positions of one group), all heads: the
 // rows are read and written whole (hkv x 128 bytes in, twice that out), 16 codes to a lane, eight
-// loads of a thread in flight.
+// loads of a thread in flight. A lane's 32 bytes go out as one store: 164k tokens of 8 heads take
+// 151 us (6.7 TB/s), 174 us with two 16-byte stores.
 constexpr int kGatherThreads = 256;
 constexpr int kGatherLoads = 8;
 __global__ void __launch_bounds__(kGatherThreads)
@@ -299,6 +327,7 @@ __global__ void __launch_bounds__(kGatherThreads)
       reinterpret_cast<uint4 *>((is_v ? p.v_out : p.k_out) + (c0 + begin) * rstride * 2);
   const uint32_t cols = (uint32_t)p.hkv * 8u;  // 16-byte pieces of a row, 8 to a head
   const uint32_t all = (uint32_t)rows * cols;
+  const bool whole = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;  // (row lengths are)
   for (uint32_t u0 = threadIdx.x; u0 < all; u0 += kGatherThreads * kGatherLoads) {
     uint4 x[kGatherLoads];
     float scale[kGatherLoads];
@@ -318,8 +347,13 @@ __global__ void __launch_bounds__(kGatherThreads)
       if (u < all) {
         const uint2 a = dequantize4(x[i].x, scale[i]), b = dequantize4(x[i].y, scale[i]);
         const uint2 c = dequantize4(x[i].z, scale[i]), d = dequantize4(x[i].w, scale[i]);
-        dst[2 * (int64_t)u] = make_uint4(a.x, a.y, b.x, b.y);
-        dst[2 * (int64_t)u + 1] = make_uint4(c.x, c.y, d.x, d.y);
+        const uint32_t w[8] = {a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+        if (whole) {
+          st_global_32b(dst + 2 * (int64_t)u, w);
+        } else {
+          dst[2 * (int64_t)u] = make_uint4(w[0], w[1], w[2], w[3]);
+          dst[2 * (int64_t)u + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
       }
     }
   }
@@ -373,6 +407,8 @@ extern "C" pkv_status pkv_kv_store_fp8(const void *k, int64_t k_tok_stride, cons
   prm.hkv = num_kv_heads;
   prm.block_size = block_size;
   prm.num_blocks = num_blocks;
+  prm.wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31u) == 0 &&
+             k_tok_stride % 16 == 0 && v_tok_stride % 16 == 0;
   prm.err = err;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (!cu_seqlens) {

@@ -266,13 +266,6 @@ __device__ __forceinline__ int32_t tile_row(const PrefillParams &p, const Item &
   return (int32_t)(blk * p.block_size + key % p.block_size);
 }
 
-// One 32-byte global store (sm_100 and later); p must be 32-byte aligned.
-__device__ __forceinline__ void st_global_32b(void *p, const uint32_t (&w)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
-               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
-
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&v);
