@@ -23,6 +23,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kSpan = kThreads * 4;  // positions of a CTA: four consecutive ones to a thread
+constexpr int kFirst = 2;            // heads whose loads are issued together
 
 struct WeightsParams {
   const float *scores;
@@ -42,11 +43,20 @@ struct WeightsParams {
 __global__ void __launch_bounds__(kThreads) decode_weights_kernel(const WeightsParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (aborted(p.err)) return;  // an earlier wait gave up: the scores are not complete
+  // what the loads below need, all in flight together: the length, the error word and the first
+  // heads' log-sum-exps
   const int64_t bh = blockIdx.x;
   const int64_t b = bh / p.hkv;
-  int64_t L = p.context_lens[b];
-  L = L < 0 ? 0 : min(L, p.cap);
+  const float *const lse = p.lse + bh * p.group;
+  const int32_t length = ld_global_s32(p.context_lens + b);
+  const uint32_t err = (uint32_t)ld_global_s32(reinterpret_cast<const int32_t *>(p.err));
+  float lse0[kFirst];
+#pragma unroll
+  for (int g = 0; g < kFirst; ++g)
+    lse0[g] = __int_as_float(ld_global_s32(reinterpret_cast<const int32_t *>(lse) +
+                                           min(g, p.group - 1)));
+  if (err & kErrTimeout) return;  // an earlier wait gave up: the scores are not complete
+  const int64_t L = length < 0 ? 0 : min((int64_t)length, p.cap);
   const float *const in = p.in ? p.in + bh * p.in_stride : nullptr;
   float *const out = p.out + bh * p.out_stride;
   for (int64_t i = (int64_t)blockIdx.y * kSpan + 4 * threadIdx.x; i < L;
@@ -62,14 +72,22 @@ __global__ void __launch_bounds__(kThreads) decode_weights_kernel(const WeightsP
       if (i + 2 < L) before.z = in[i + 2];
       if (i + 3 < L) before.w = in[i + 3];
     }
-    for (int g = 0; g < p.group; ++g, s += p.score_stride) {
-      const float lse = p.lse[bh * p.group + g];
-      const float4 x = *reinterpret_cast<const float4 *>(s);  // (entries past L: not used)
-      w.x += fast_exp2(x.x - lse);
-      w.y += fast_exp2(x.y - lse);
-      w.z += fast_exp2(x.z - lse);
-      w.w += fast_exp2(x.w - lse);
-    }
+    float4 x[kFirst];
+#pragma unroll
+    for (int g = 0; g < kFirst; ++g)  // (entries past L: not used)
+      if (g < p.group) x[g] = *reinterpret_cast<const float4 *>(s + g * p.score_stride);
+    auto add = [&](const float4 &y, float z) {
+      w.x += fast_exp2(y.x - z);
+      w.y += fast_exp2(y.y - z);
+      w.z += fast_exp2(y.z - z);
+      w.w += fast_exp2(y.w - z);
+    };
+#pragma unroll
+    for (int g = 0; g < kFirst; ++g)
+      if (g < p.group) add(x[g], lse0[g]);
+#pragma unroll 4
+    for (int g = kFirst; g < p.group; ++g)
+      add(*reinterpret_cast<const float4 *>(s + g * p.score_stride), lse[g]);
     w = make_float4(before.x + w.x, before.y + w.y, before.z + w.z, before.w + w.w);
     if (whole) {
       *reinterpret_cast<float4 *>(out + i) = w;

@@ -9,9 +9,10 @@
 // Two kernels. evict_select_kernel, one CTA per (sequence, head): a radix select over the
 // weights' ordered bits (11 + 11 + 10, histograms in shared memory) finds the smallest kept key
 // and how many of its equals are kept, then one ordered pass with prefix sums writes the kept
-// positions and their weights.
-// evict_copy_kernel, one CTA per (sequence, 64 kept rows, head), moves the K and V rows; it is
-// bound by HBM: each kept row is read once and written once. In an 8-bit cache the 64 rows are
+// positions.
+// evict_copy_kernel, one CTA per (sequence, 64 kept rows, head), moves the K and V rows and the
+// kept weights; it is bound by HBM: each kept row is read once and written once (16 x 32768
+// tokens to 8192, 1.07 GB: 159 us). In an 8-bit cache the 64 rows are
 // one group of the destination, whose scale is the largest of its rows' scales (powers of two:
 // rows of a smaller one lose only what falls below e4m3's normal range).
 #include <algorithm>
@@ -55,20 +56,15 @@ __device__ __forceinline__ uint32_t ordered(uint32_t b) {
   return mag > 0x7f800000u ? 0u : key;
 }
 
-// The number with these bits (key 0: NaN).
-__device__ __forceinline__ float number(uint32_t key) {
-  if (key == 0u) return __uint_as_float(0x7fffffffu);
-  return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xffffffffu));
-}
-
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 // A warp's part of a row, up to kHeld chunks of 128 elements, stays in its lanes' registers as
 // ordered keys, so a row of up to 32768 weights is loaded once, all loads in flight together; a
 // longer row is taken in pieces of 32768 that each pass loads again. What bounds the kernel is
-// its instructions (128 rows of 32768: XX us; 28 us when every element compared 64-bit
-// positions and mapped its key again in every pass, 36 us with the elements loaded one by one).
+// its instructions, about 90 per element (128 rows of 32768: 22 us; 28 us when every element
+// compared 64-bit positions and mapped its key again in every pass, 36 us with the elements
+// loaded one by one).
 constexpr int kHeld = 8;
 constexpr int kPiece = kHeld * 128 * kSelWarps;
 constexpr uint32_t kTopKey = 0xffffffffu;  // a recent position's: above every number's
@@ -166,12 +162,14 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
           }
 #pragma unroll
           for (int c = 0; c < kHeld; ++c) {
+            if (c >= chunks) break;
             const uint32_t i = at0 + c * 128;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              key[c][e] = ordered(key[c][e]);
-              if (i + e >= older && i + e < len && c < chunks) key[c][e] = kTopKey;
-            }
+            for (int e = 0; e < 4; ++e) key[c][e] = ordered(key[c][e]);
+            if (i + 4 > older)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (i + e >= older && i + e < len) key[c][e] = kTopKey;
           }
         }
         if (pass < 3) {
@@ -220,7 +218,6 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
             if (k > prefix || (k == prefix && le < want)) {
               const uint32_t at = la + min(le, want), i = at0 + c * 128 + e;
               kept[at] = (int32_t)i;
-              if (w_out) w_out[at] = k == kTopKey ? w[i] : number(k);
             }
             la += k > prefix;
             le += k == prefix;
@@ -246,10 +243,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
       prefix |= found_bin << shift;
     }
   } else {
-    for (int64_t j = threadIdx.x; j < n; j += kSelThreads) {
-      kept[j] = (int32_t)j;
-      if (w_out) w_out[j] = w[j];
-    }
+    for (int64_t j = threadIdx.x; j < n; j += kSelThreads) kept[j] = (int32_t)j;
   }
   for (int64_t j = n + (int64_t)threadIdx.x; j < p.budget; j += kSelThreads) {
     kept[j] = -1;
@@ -280,17 +274,18 @@ __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const EvictPar
   const int rows = min(kGroup, n - j0);
   const int32_t dst_blk =
       *(p.dst_tables + (int64_t)b * p.dst_width + j0 / p.block_size);
-  if (dst_blk < 0 || dst_blk >= p.num_blocks) {
-    if (threadIdx.x == 0 && h == 0) record_error(p.err, kErrBlock);
-    return;
-  }
+  const bool dst_ok = dst_blk >= 0 && dst_blk < p.num_blocks;
+  if (!dst_ok && threadIdx.x == 0 && h == 0) record_error(p.err, kErrBlock);
   const int dst_in = j0 % p.block_size;
   const int t = threadIdx.x;
   if (t < kGroup) {
     int64_t slot = -1;
     float s[2] = {0.f, 0.f};
     if (t < rows) {
-      const int32_t i = *(p.kept + ((int64_t)b * p.hkv + h) * p.budget + j0 + t);
+      const int64_t bh = (int64_t)b * p.hkv + h;
+      const int32_t i = p.kept[bh * p.budget + j0 + t];
+      if (p.weights_out)
+        p.weights_out[bh * p.weights_out_stride + j0 + t] = p.weights[bh * p.weights_stride + i];
       const int32_t blk = *(p.src_tables + (int64_t)b * p.src_width + i / p.block_size);
       if (blk >= 0 && blk < p.num_blocks) {
         const int in = i % p.block_size;
@@ -310,6 +305,7 @@ __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const EvictPar
       ratio[1][t] = s[1];
     }
   }
+  if (!dst_ok) return;  // (the rows that would go there are dropped, their weights are not)
   __syncthreads();
   if constexpr (FP8) {
     if (t < 64) {  // warp 0: K's largest scale, warp 1: V's
