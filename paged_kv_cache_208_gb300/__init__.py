@@ -2,16 +2,17 @@
 
 The functions here only marshal arguments: they check dtype, device and layout of torch
 tensors, pass raw device pointers and the current CUDA stream to the ``pkv_*`` entry points
-declared in ``include/pkv.h``, and raise ``PkvError`` on a non-zero status. Every step of
-the computation runs in the CUDA library; there is no other implementation to fall back
-to. Importing this package fails if ``libpkv.so`` has not been built
+declared in ``include/pkv.h``, and raise ``PkvError`` on a non-zero status. Most calls go
+through ctypes; those of the 8-bit cache, the attention weights and eviction through a small
+extension module (``binding/pkv_torch.cpp``) that does the same checks in less time. Every step
+of the computation runs in the CUDA library; there is no other implementation to fall back
+to. Importing this package fails if ``libpkv.so`` and that module have not been built
 (``python paged_kv_cache_208_gb300/build.py`` or ``__graft_entry__.build()``).
 
 PyTorch is used for device memory and streams only.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -97,6 +98,11 @@ def _load() -> ctypes.CDLL:
 
 
 _LIB = _load()
+try:
+    from . import _pkv_torch as _torch  # the per-step calls on tensors (binding/pkv_torch.cpp)
+except ImportError as e:
+    raise ImportError(f"{os.path.join(_HERE, '_pkv_torch.so')} is missing or does not load ({e}): "
+                      f"build it with `python {os.path.join(_HERE, 'build.py')}`") from e
 
 
 def lib() -> ctypes.CDLL:
@@ -357,135 +363,15 @@ def qk_norm_rope_store(qkv, positions, q_norm_weight, k_norm_weight, eps, cos_si
 # ----------------------------------------------------------------------------- the 8-bit cache
 FP8_GROUP = 64  # tokens of a block that share a scale
 
-_E4M3, _BF16, _F32, _INT32 = torch.float8_e4m3fn, torch.bfloat16, torch.float32, torch.int32
-
-# These calls run once per layer and step: the checks below take a short path over what is right
-# and look for the message only when something is not. Every tensor has to be on the caches'
-# device, which need not be the current one.
-_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-_HERE_ALREADY = contextlib.nullcontext()
+# The calls below check their tensors and launch in binding/pkv_torch.cpp (every tensor has to be
+# on the caches' device, which need not be the current one; with a stream given, outputs are
+# allocated on it). A status other than OK comes back as an int.
 
 
-def _on(index: int):
-    """Launches go to the tensors' device, whichever is current."""
-    return _HERE_ALREADY if index == _current_device() else torch.cuda.device(index)
-
-
-def _stream_on(stream, index: int) -> int:
-    """The stream's handle; for None the current stream of the device (made current by _on)."""
-    if stream is None and _raw_stream is not None:
-        return _raw_stream(index)
-    return _stream(stream)
-
-
-def _need_on(t, name: str, dtype, index: int) -> None:
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
-    _need(t, name, dtype)
-    if t.get_device() != index:
-        raise ValueError(f"{name} is on {t.device}, the caches on cuda:{index}")
-
-
-def _need_cache(k_cache, v_cache, k_scale=None, v_scale=None):
-    """Checks the pools of a bf16 cache, or of an 8-bit one with its scales; returns (device index,
-    num_blocks, block_size, hkv, d)."""
-    if k_scale is None and v_scale is None:
-        pools, dtype = ((k_cache, "k_cache"), (v_cache, "v_cache")), _BF16
-        if (k_cache.dtype is _BF16 and v_cache.dtype is _BF16 and k_cache.dim() == 4
-                and (shape := k_cache.shape) == v_cache.shape and k_cache.is_contiguous()
-                and v_cache.is_contiguous() and (index := k_cache.get_device()) >= 0
-                and v_cache.get_device() == index):
-            return index, *shape
-    else:
-        pools, dtype = ((k_cache, "k_cache"), (v_cache, "v_cache")), _E4M3
-        if (k_cache.dtype is _E4M3 and v_cache.dtype is _E4M3 and k_cache.dim() == 4
-                and (shape := k_cache.shape) == v_cache.shape and k_scale is not None
-                and v_scale is not None and k_scale.dtype is _F32 and v_scale.dtype is _F32
-                and (index := k_cache.get_device()) >= 0 and v_cache.get_device() == index
-                and k_scale.get_device() == index and v_scale.get_device() == index
-                and k_scale.shape == (want := (shape[0], shape[2], shape[1] // FP8_GROUP))
-                and v_scale.shape == want and k_cache.is_contiguous()
-                and v_cache.is_contiguous() and k_scale.is_contiguous()
-                and v_scale.is_contiguous()):
-            return index, *shape
-    if (k_scale is None) != (v_scale is None):
-        raise ValueError("k_scale and v_scale go together")
-    for t, n in pools:
-        _need(t, n, dtype)
-        _need_on(t, n, dtype, k_cache.get_device())
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
-        raise ValueError("caches must be [NB, bs, Hkv, D], the same for K and V")
-    if k_scale is not None:
-        want = [k_cache.shape[0], k_cache.shape[2], k_cache.shape[1] // FP8_GROUP]
-        for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            _need_on(t, n, _F32, k_cache.get_device())
-            if list(t.shape) != want:
-                raise ValueError(f"{n} must be [NB, Hkv, bs / {FP8_GROUP}] = {want}")
-    raise ValueError("caches and scales must be contiguous")
-
-
-def _need_ints(t, name: str, shape: tuple, index: int) -> None:
-    """An int32 tensor of this shape, contiguous, on the caches' device."""
-    if not (t.dtype is _INT32 and t.shape == shape and t.get_device() == index
-            and t.is_contiguous()):
-        _need_on(t, name, _INT32, index)
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)}, got "
-                         f"{list(t.shape)}")
-
-
-def _need_lists(context_lens, block_tables, index: int):
-    """Context lengths [B] and block tables [B, W]; returns (B, W)."""
-    if context_lens.dim() != 1 or block_tables.dim() != 2:
-        raise ValueError("context_lens must be [B] and block tables [B, W] int32 tensors")
-    B, W = block_tables.shape
-    _need_ints(context_lens, "context_lens", (B,), index)
-    _need_ints(block_tables, "block_tables", (B, W), index)
-    return B, W
-
-
-def _need_rows(t, name: str, hkv: int, d: int, index: int) -> int:
-    """[T, Hkv, D] bf16 rows, each token's dense; returns the token stride."""
-    if not (t.dtype is _BF16 and t.get_device() == index and t.dim() == 3 and t.shape[1] == hkv
-            and t.shape[2] == d):
-        _need_on(t, name, _BF16, index)
-        raise ValueError(f"{name} must be [T, {hkv}, {d}]")
-    tok, head, elem = t.stride()
-    if elem != 1 or (head != d and hkv > 1):
-        raise ValueError(f"{name}: each token's heads must be dense")
-    return tok if t.shape[0] > 1 else hkv * d
-
-
-def _need_weights(t, name: str, batch: int, hkv: int, length: int, index: int) -> int:
-    """A [B, Hkv, >= length] float32 tensor of dense rows that lie one stride apart; returns the
-    stride."""
-    if t.dtype is not _F32 or t.get_device() != index:
-        _need_on(t, name, _F32, index)
-    if t.dim() == 3:
-        b, h, n = t.shape
-        sb, sh, sn = t.stride()
-        if (b == batch and h == hkv and n >= length and (sn == 1 or n <= 1)
-                and (b <= 1 or sb == (h * sh if h > 1 else sb))):
-            return sh if h > 1 else sb if b > 1 else n
-    raise ValueError(f"{name} must be [{batch}, {hkv}, >= {length}] with dense, evenly spaced "
-                     "rows")
-
-
-def _weights_args(weights, weights_out, batch, hkv, length, index):
-    """(in pointer, in stride, out pointer, out stride); without weights_out in place."""
-    if weights is None:
-        if weights_out is None:
-            return None, 0, None, 0
-        return None, 0, weights_out.data_ptr(), _need_weights(weights_out, "weights_out", batch,
-                                                              hkv, length, index)
-    in_stride = _need_weights(weights, "weights", batch, hkv, length, index)
-    ptr = weights.data_ptr()
-    if weights_out is None:
-        return ptr, in_stride, ptr, in_stride
-    out_stride = _need_weights(weights_out, "weights_out", batch, hkv, length, index)
-    out = weights_out.data_ptr()
-    if out == ptr and in_stride != out_stride:
-        raise ValueError("weights and weights_out overlap with different strides")
-    return ptr, in_stride, out, out_stride
+def _result(fn: str, r):
+    if type(r) is int:
+        raise PkvError(fn, r)
+    return r
 
 
 def kv_store_fp8(k: torch.Tensor, v: torch.Tensor, context_lens: torch.Tensor,
@@ -499,25 +385,8 @@ def kv_store_fp8(k: torch.Tensor, v: torch.Tensor, context_lens: torch.Tensor,
     block_tables [B, W], cu_seqlens [B + 1] int32; caches [NB, bs, Hkv, D] float8_e4m3fn;
     scales [NB, Hkv, bs / 64] float32. A group of 64 positions keeps one power-of-two scale per
     head; it grows, and the group's earlier rows are re-rounded, when a new row needs it."""
-    if k_scale is None or v_scale is None:
-        raise ValueError("k_scale and v_scale must be given")
-    index, nb, bs, hkv, d = _need_cache(k_cache, v_cache, k_scale, v_scale)
-    ks, vs = _need_rows(k, "k", hkv, d, index), _need_rows(v, "v", hkv, d, index)
-    T = k.shape[0]
-    if v.shape[0] != T:
-        raise ValueError("k and v must hold the same tokens")
-    B, W = _need_lists(context_lens, block_tables, index)
-    cu = None
-    if cu_seqlens is not None:
-        _need_ints(cu_seqlens, "cu_seqlens", (B + 1,), index)
-        cu = cu_seqlens.data_ptr()
-    with _on(index):
-        status = _LIB.pkv_kv_store_fp8(
-            k.data_ptr(), ks, v.data_ptr(), vs, cu, context_lens.data_ptr(),
-            block_tables.data_ptr(), W, B, T, k_cache.data_ptr(), v_cache.data_ptr(),
-            k_scale.data_ptr(), v_scale.data_ptr(), hkv, d, bs, nb, _stream_on(stream, index))
-    if status:
-        raise PkvError("pkv_kv_store_fp8", status)
+    _result("pkv_kv_store_fp8", _torch.kv_store_fp8(
+        k, v, context_lens, block_tables, k_cache, v_cache, k_scale, v_scale, cu_seqlens, stream))
 
 
 def kv_gather_fp8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
@@ -526,32 +395,9 @@ def kv_gather_fp8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.T
                   v_out: torch.Tensor | None = None, stream=None):
     """Rows of an 8-bit cache as packed bf16 (k, v) [total_k, Hkv, D]: positions 0 .. of sequence
     n at rows cu_seqlens_k[n] .. cu_seqlens_k[n + 1], as varlen_prefill_attn takes them."""
-    if k_scale is None or v_scale is None:
-        raise ValueError("k_scale and v_scale must be given")
-    index, nb, bs, hkv, d = _need_cache(k_cache, v_cache, k_scale, v_scale)
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be a [N, W] int32 tensor")
-    N, W = block_table.shape
-    _need_ints(block_table, "block_table", (N, W), index)
-    _need_ints(cu_seqlens_k, "cu_seqlens_k", (N + 1,), index)
-    shape = (int(total_k), hkv, d)
-    outs = []
-    for t, n in ((k_out, "k_out"), (v_out, "v_out")):
-        if t is None:
-            t = torch.empty(shape, dtype=_BF16, device=k_cache.device)
-        elif not (t.dtype is _BF16 and t.shape == shape and t.get_device() == index
-                  and t.is_contiguous()):
-            _need_on(t, n, _BF16, index)
-            raise ValueError(f"{n} must be a contiguous {list(shape)} tensor")
-        outs.append(t)
-    with _on(index):
-        status = _LIB.pkv_kv_gather_fp8(
-            k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-            block_table.data_ptr(), W, cu_seqlens_k.data_ptr(), N, shape[0], outs[0].data_ptr(),
-            outs[1].data_ptr(), hkv, d, bs, nb, _stream_on(stream, index))
-    if status:
-        raise PkvError("pkv_kv_gather_fp8", status)
-    return outs[0], outs[1]
+    return _result("pkv_kv_gather_fp8", _torch.kv_gather_fp8(
+        k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens_k, total_k, k_out, v_out,
+        stream))
 
 
 def _zeroed_workspace(nbytes: int, device, stream) -> torch.Tensor:
@@ -586,31 +432,6 @@ def decode_weights_workspace(batch: int, num_q_heads: int, num_kv_heads: int, he
         return _zeroed_workspace(n, device, stream)
 
 
-def _need_decode(q, d, block_tables, context_lens, out, index):
-    """Checks what every decode call takes; returns (batch, num_q_heads, table width, out)."""
-    if not (q.dtype is _BF16 and q.dim() == 3 and q.get_device() == index and q.is_contiguous()
-            and q.shape[2] == d):
-        _need_on(q, "q", _BF16, index)
-        raise ValueError(f"q must be a contiguous [B, Hq, {d}] tensor")
-    B, W = _need_lists(context_lens, block_tables, index)
-    if q.shape[0] != B:
-        raise ValueError(f"q holds {q.shape[0]} sequences, block_tables {B}")
-    if out is None:
-        out = torch.empty_like(q)
-    elif not (out.dtype is _BF16 and out.shape == q.shape and out.get_device() == index
-              and out.is_contiguous()):
-        _need_on(out, "out", _BF16, index)
-        raise ValueError("out must be a contiguous tensor of q's shape")
-    return B, q.shape[1], W, out
-
-
-def _need_workspace(t, index) -> int:
-    """A contiguous tensor on the caches' device; returns its bytes."""
-    if t.get_device() != index or not t.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
-    return t.numel() * t.element_size()
-
-
 def paged_decode_attn_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                           k_scale: torch.Tensor, v_scale: torch.Tensor,
                           block_tables: torch.Tensor, context_lens: torch.Tensor,
@@ -622,26 +443,9 @@ def paged_decode_attn_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     """paged_decode_attn over an 8-bit cache. q: [B, Hq, D] bf16; caches [NB, bs, Hkv, D]
     float8_e4m3fn with scales [NB, Hkv, bs / 64] float32 (see kv_store_fp8). With weights and / or
     weights_out the attention weights too, as paged_decode_attn_weights gives them."""
-    if k_scale is None or v_scale is None:
-        raise ValueError("k_scale and v_scale must be given")
-    index, nb, bs, hkv, d = _need_cache(k_cache, v_cache, k_scale, v_scale)
-    B, hq, W, out = _need_decode(q, d, block_tables, context_lens, out, index)
-    longest = int(max_context_len)
-    w_in, w_in_stride, w_out, w_out_stride = _weights_args(weights, weights_out, B, hkv, longest,
-                                                           index)
-    with _on(index):
-        if workspace is None:
-            workspace = decode_fp8_workspace(B, hq, hkv, d, longest, num_splits,
-                                             w_out is not None, index, stream)
-        status = _LIB.pkv_paged_decode_attn_fp8(
-            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-            v_scale.data_ptr(), block_tables.data_ptr(), W, context_lens.data_ptr(), B, longest,
-            hq, hkv, d, bs, nb, scale, num_splits, w_in, w_in_stride, w_out, w_out_stride,
-            workspace.data_ptr(), _need_workspace(workspace, index), out.data_ptr(),
-            _stream_on(stream, index))
-    if status:
-        raise PkvError("pkv_paged_decode_attn_fp8", status)
-    return out
+    return _result("pkv_paged_decode_attn_fp8", _torch.paged_decode_attn_fp8(
+        q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, max_context_len, scale,
+        num_splits, weights, weights_out, workspace, out, stream))
 
 
 def paged_decode_attn_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -654,24 +458,9 @@ def paged_decode_attn_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: t
     """paged_decode_attn that also adds each cached token's attention weight, summed over the
     query heads of its KV head, to `weights` [B, Hkv, >= max_context_len] float32: in place, or
     into weights_out (without weights: weights_out receives this step's alone)."""
-    index, nb, bs, hkv, d = _need_cache(k_cache, v_cache)
-    B, hq, W, out = _need_decode(q, d, block_tables, context_lens, out, index)
-    if weights is None and weights_out is None:
-        raise ValueError("weights or weights_out must be given")
-    longest = int(max_context_len)
-    w_in, w_in_stride, w_out, w_out_stride = _weights_args(weights, weights_out, B, hkv, longest,
-                                                           index)
-    with _on(index):
-        if workspace is None:
-            workspace = decode_weights_workspace(B, hq, hkv, d, longest, num_splits, index, stream)
-        status = _LIB.pkv_paged_decode_attn_weights(
-            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), W,
-            context_lens.data_ptr(), B, longest, hq, hkv, d, bs, nb, scale, num_splits, w_in,
-            w_in_stride, w_out, w_out_stride, workspace.data_ptr(),
-            _need_workspace(workspace, index), out.data_ptr(), _stream_on(stream, index))
-    if status:
-        raise PkvError("pkv_paged_decode_attn_weights", status)
-    return out
+    return _result("pkv_paged_decode_attn_weights", _torch.paged_decode_attn_weights(
+        q, k_cache, v_cache, block_tables, context_lens, max_context_len, scale, weights,
+        num_splits, weights_out, workspace, out, stream))
 
 
 # ----------------------------------------------------------------------------- eviction
@@ -689,40 +478,9 @@ def kv_evict(weights: torch.Tensor, context_lens: torch.Tensor, max_context_len:
     caches: bf16 [NB, bs, Hkv, D], or float8_e4m3fn with k_scale and v_scale. Returns (kept
     positions [B, Hkv, budget] int32 (-1 past a sequence's length), their weights
     [B, Hkv, budget], the new context lengths [B] int32)."""
-    index, nb, bs, hkv, d = _need_cache(k_cache, v_cache, k_scale, v_scale)
-    B, W = _need_lists(context_lens, block_tables, index)
-    if dst_block_tables.dim() != 2:
-        raise ValueError("dst_block_tables must be a [B, W'] int32 tensor")
-    dst_width = dst_block_tables.shape[1]
-    _need_ints(dst_block_tables, "dst_block_tables", (B, dst_width), index)
-    budget, recent, longest = int(budget), int(recent), int(max_context_len)
-    w_stride = _need_weights(weights, "weights", B, hkv, longest, index)
-    if budget < 1 or not 0 <= recent <= budget:
-        raise ValueError("budget must be at least 1 and recent between 0 and budget")
-    shape = (B, hkv, budget)
-    if kept is None:
-        kept = torch.empty(shape, dtype=_INT32, device=k_cache.device)
-    else:
-        _need_ints(kept, "kept", shape, index)
-    if weights_out is None:
-        weights_out = torch.empty(shape, dtype=_F32, device=k_cache.device)
-        o_stride = budget
-    else:
-        o_stride = _need_weights(weights_out, "weights_out", B, hkv, budget, index)
-    if new_context_lens is None:
-        new_context_lens = torch.empty_like(context_lens)
-    else:
-        _need_ints(new_context_lens, "new_context_lens", (B,), index)
-    with _on(index):
-        status = _LIB.pkv_kv_evict(
-            weights.data_ptr(), w_stride, context_lens.data_ptr(), B, longest, budget, recent,
-            block_tables.data_ptr(), W, dst_block_tables.data_ptr(), dst_width,
-            k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale), _ptr(v_scale), hkv, d, bs, nb,
-            kept.data_ptr(), weights_out.data_ptr(), o_stride, new_context_lens.data_ptr(),
-            _stream_on(stream, index))
-    if status:
-        raise PkvError("pkv_kv_evict", status)
-    return kept, weights_out, new_context_lens
+    return _result("pkv_kv_evict", _torch.kv_evict(
+        weights, context_lens, max_context_len, block_tables, dst_block_tables, budget, recent,
+        k_cache, v_cache, k_scale, v_scale, kept, weights_out, new_context_lens, stream))
 
 
 # ----------------------------------------------------------------------------- block manager
