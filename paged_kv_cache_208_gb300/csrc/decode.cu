@@ -522,7 +522,11 @@ __global__ void __maxnreg__(96)
         }
       }
       float pa = 0.f, pb = 0.f;
-      if (m_run != -INFINITY) {
+      if constexpr (W) {  // (a NaN score makes its head NaN, also where nothing else is)
+        const float base = m_run == -INFINITY ? 0.f : m_run;
+        pa = fast_exp2(sa - base);
+        pb = fast_exp2(sb - base);
+      } else if (m_run != -INFINITY) {
         pa = fast_exp2(sa - m_run);
         pb = fast_exp2(sb - m_run);
       }
@@ -585,7 +589,15 @@ __global__ void __maxnreg__(96)
 #pragma unroll
       for (int w = 0; w < kConsumerWarps; ++w) M = fmaxf(M, sm.m[w][g]);
       float o = 0.f, lse = -INFINITY;
-      if (M != -INFINITY) {
+      bool any = M != -INFINITY;
+      if constexpr (W) {
+        if (!any) {  // no keys, or NaN scores only
+          M = 0.f;
+#pragma unroll
+          for (int w = 0; w < kConsumerWarps; ++w) any = any || isnan(sm.l[w][g]);
+        }
+      }
+      if (any) {
         float lsum = 0.f, osum = 0.f;
 #pragma unroll
         for (int w = 0; w < kConsumerWarps; ++w) {
@@ -655,7 +667,8 @@ __global__ void __maxnreg__(96)
   float M = cl_lse;
   for (int r = 0; r < p.cluster - 1; ++r) M = fmaxf(M, land_lse[r * GC + g]);
   float acc = 0.f, wsum = 0.f;
-  if (M != -INFINITY) {
+  if (W && M == -INFINITY) M = 0.f;  // no keys, or NaN scores only
+  if (W || M != -INFINITY) {
     const float w0 = fast_exp2(cl_lse - M);  // 0 for a split with no keys
     wsum = w0;
     acc = w0 * cl_o;
@@ -670,7 +683,8 @@ __global__ void __maxnreg__(96)
   const int h = xg / p.head_groups;
   const int64_t row = (int64_t)b * p.num_q_heads + h * p.group + (xg % p.head_groups) * GC + g;
   if (!sm.stop) {
-    p.out[row * kD + d] = bf16_bits_rn(wsum > 0.f ? acc / wsum : 0.f);
+    const bool some = W ? wsum != 0.f : wsum > 0.f;
+    p.out[row * kD + d] = bf16_bits_rn(some ? acc / wsum : 0.f);
     if (W && d == 0) p.lse[row] = M + __log2f(wsum);
   }
 }
@@ -837,7 +851,8 @@ cudaError_t launch_paged_decode(const DecodeArgs &a, const DecodePlan &p, cudaSt
   const cudaError_t e = p.scores_at ? split(two ? launch_split<2, true> : launch_split<1, true>)
                                     : split(two ? launch_split<2, false> : launch_split<1, false>);
   if (e != cudaSuccess || p.splits == 1 || prm.cluster) return e;
-  return launch_combine(a, p, prm, stream);
+  return p.scores_at ? launch_combine<true>(a, p, prm, stream)
+                     : launch_combine<false>(a, p, prm, stream);
 }
 
 }  // namespace pkv

@@ -90,6 +90,9 @@ __device__ __forceinline__ void unit_coords(const DecodeParams &p, int u, int &s
 // One warp per (sequence, query head): out = sum_s 2^(lse_s - lse) o_s over the sequence's
 // splits, lse = log2 sum_s 2^lse_s. A sequence with no token gets zeros; one whose context
 // fits one split was written by the split kernel.
+// kNan: a split with a NaN makes the result NaN also where no other split has a key (the bf16
+// kernel without weights gives zeros there).
+template <bool kNan>
 __global__ void __launch_bounds__(128)
     decode_combine_kernel(const float *__restrict__ part_o, const float *__restrict__ part_lse,
                           const int32_t *__restrict__ context_lens, int32_t batch,
@@ -118,7 +121,8 @@ __global__ void __launch_bounds__(128)
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float wsum = 0.f;
-  if (M != -INFINITY) {
+  if (kNan && M == -INFINITY) M = 0.f;
+  if (kNan || M != -INFINITY) {
     for (int s = 0; s < ns; ++s) {
       const float wgt = fast_exp2(lse[s] - M);
       const float4 o4 = *reinterpret_cast<const float4 *>(part_o + (row * splits + s) * kD + 4 * lane);
@@ -130,7 +134,7 @@ __global__ void __launch_bounds__(128)
     }
   }
   if (lse_out && lane == 0) lse_out[row] = M + __log2f(wsum);  // ns == 0: -inf, not read
-  const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+  const float inv = (kNan ? wsum != 0.f : wsum > 0.f) ? 1.f / wsum : 0.f;
   const uint32_t lo = (uint32_t)bf16_bits_rn(acc.x * inv) | ((uint32_t)bf16_bits_rn(acc.y * inv) << 16);
   const uint32_t hi = (uint32_t)bf16_bits_rn(acc.z * inv) | ((uint32_t)bf16_bits_rn(acc.w * inv) << 16);
   *reinterpret_cast<uint2 *>(out + row * kD + 4 * lane) = make_uint2(lo, hi);
@@ -174,11 +178,12 @@ inline DecodeParams decode_params(const DecodeArgs &a, const DecodePlan &p) {
 }
 
 // The merge kernel of a call whose splits left their partials in the workspace.
+template <bool kNan>
 inline cudaError_t launch_combine(const DecodeArgs &a, const DecodePlan &p, const DecodeParams &prm,
                                   cudaStream_t stream) {
   const int64_t rows_out = (int64_t)a.batch * a.num_q_heads;
   // programmatic dependent launch: the merge grid is set up while the split kernel runs
-  return launch_after(decode_combine_kernel, dim3((unsigned)((rows_out + 3) / 4)), 128, stream,
+  return launch_after(decode_combine_kernel<kNan>, dim3((unsigned)((rows_out + 3) / 4)), 128, stream,
                       (const float *)prm.part_o, (const float *)prm.part_lse, a.context_lens,
                       a.batch, a.num_q_heads, p.chunk, p.splits, prm.cap,
                       static_cast<uint16_t *>(a.out), prm.lse, (const unsigned int *)a.err);

@@ -831,21 +831,18 @@ __global__ void __launch_bounds__(kThreads, 2)
   for (int g = 0; g < GH; ++g) {
     float M = cl_lse[g];
     for (int r = 0; r < p.cluster - 1; ++r) M = fmaxf(M, land_lse[r * GC + g0 + g]);
-    float acc = 0.f, wsum = 0.f;
-    if (M != -INFINITY) {
-      const float w0 = fast_exp2(cl_lse[g] - M);  // 0 for a split with no keys
-      wsum = w0;
-      acc = w0 * cl_o[g];
-      for (int r = 0; r < p.cluster - 1; ++r) {
-        const float wgt = fast_exp2(land_lse[r * GC + g0 + g] - M);
-        wsum += wgt;
-        acc = fmaf(wgt, land_o[((size_t)r * GC + g0 + g) * kD + d], acc);
-      }
+    if (M == -INFINITY) M = 0.f;  // no keys, or NaN scores only
+    float wsum = fast_exp2(cl_lse[g] - M);  // 0 for a split with no keys, NaN for one with a NaN
+    float acc = wsum * cl_o[g];
+    for (int r = 0; r < p.cluster - 1; ++r) {
+      const float wgt = fast_exp2(land_lse[r * GC + g0 + g] - M);
+      wsum += wgt;
+      acc = fmaf(wgt, land_o[((size_t)r * GC + g0 + g) * kD + d], acc);
     }
     const int in_group = hg * GC + g0 + g;
     const int64_t row = (int64_t)b * p.num_q_heads + h * p.group + in_group;
     if (!sm.stop && in_group < p.group) {
-      p.out[row * kD + d] = bf16_bits_rn(wsum > 0.f ? acc / wsum : 0.f);
+      p.out[row * kD + d] = bf16_bits_rn(wsum == 0.f ? 0.f : acc / wsum);
       if (W && d == 0) p.lse[row] = M + __log2f(wsum);
     }
   }
@@ -927,7 +924,7 @@ cudaError_t launch_paged_decode_fp8(const DecodeArgs &a, const DecodePlan &p,
       : p.heads_per_cta == 4 ? split(w ? launch_split_fp8<4, true> : launch_split_fp8<4, false>)
                              : split(w ? launch_split_fp8<2, true> : launch_split_fp8<2, false>);
   if (e != cudaSuccess || p.splits == 1 || prm.cluster) return e;
-  return launch_combine(a, p, prm, stream);
+  return launch_combine<true>(a, p, prm, stream);
 }
 
 }  // namespace pkv

@@ -98,10 +98,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
   __shared__ uint32_t hist[kBins];
   __shared__ uint32_t sums[2][kSelWarps];
   __shared__ uint32_t found_bin, found_above;
-  if (__syncthreads_or(threadIdx.x == 0 && aborted(p.err))) return;
   const int64_t bh = blockIdx.x;
   const int b = (int)(bh / p.hkv), h = (int)(bh % p.hkv);
-  const int32_t L = *(p.context_lens + b);
+  const int32_t L = ld_global_s32(p.context_lens + b);
+  const bool stop = threadIdx.x == 0 && aborted(p.err);  // (both loads in flight together)
+  if (__syncthreads_or(stop)) return;
   const bool bad = L < 0 || L > p.max_context_len ||
                    (int64_t)L > (int64_t)p.src_width * p.block_size ||
                    (int64_t)min(L, p.budget) > (int64_t)p.dst_width * p.block_size;
@@ -269,28 +270,33 @@ __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const EvictPar
   const int h = (int)(blockIdx.x % p.hkv);
   const int64_t bc = blockIdx.x / p.hkv;
   const int c = (int)(bc % chunks), b = (int)(bc / chunks);
-  const int n = *(p.new_lens + b), j0 = c * kGroup;
-  if (j0 >= n || aborted(p.err)) return;
+  const int j0 = c * kGroup, t = threadIdx.x;
+  const int64_t bh = (int64_t)b * p.hkv + h;
+  // what nothing else is needed for, all in flight together (the kept list has `budget` entries)
+  const int dst_at = min(j0 / p.block_size, p.dst_width - 1);
+  const int32_t n = ld_global_s32(p.new_lens + b);
+  const int32_t dst_blk = ld_global_s32(p.dst_tables + (int64_t)b * p.dst_width + dst_at);
+  const bool stop = t == 0 && aborted(p.err);  // an earlier wait gave up somewhere
+  const int32_t kept = t < kGroup && j0 + t < p.budget
+                           ? ld_global_s32(p.kept + bh * p.budget + j0 + t) : -1;
+  // (decided by the CTA together; after an abort the kept list may hold anything)
+  if (__syncthreads_or(stop) || j0 >= n) return;
   const int rows = min(kGroup, n - j0);
-  const int32_t dst_blk =
-      *(p.dst_tables + (int64_t)b * p.dst_width + j0 / p.block_size);
   const bool dst_ok = dst_blk >= 0 && dst_blk < p.num_blocks;
   if (!dst_ok && threadIdx.x == 0 && h == 0) record_error(p.err, kErrBlock);
   const int dst_in = j0 % p.block_size;
-  const int t = threadIdx.x;
+  float s[2] = {0.f, 0.f};
   if (t < kGroup) {
     int64_t slot = -1;
-    float s[2] = {0.f, 0.f};
     if (t < rows) {
-      const int64_t bh = (int64_t)b * p.hkv + h;
-      const int32_t i = p.kept[bh * p.budget + j0 + t];
+      const int32_t blk =
+          ld_global_s32(p.src_tables + (int64_t)b * p.src_width + kept / p.block_size);
       if (p.weights_out)
-        p.weights_out[bh * p.weights_out_stride + j0 + t] = p.weights[bh * p.weights_stride + i];
-      const int32_t blk = *(p.src_tables + (int64_t)b * p.src_width + i / p.block_size);
+        p.weights_out[bh * p.weights_out_stride + j0 + t] = p.weights[bh * p.weights_stride + kept];
       if (blk >= 0 && blk < p.num_blocks) {
-        const int in = i % p.block_size;
+        const int in = kept % p.block_size;
         slot = (int64_t)blk * p.block_size + in;
-        if constexpr (FP8) {
+        if constexpr (FP8) {  // (in flight while the rows are asked for)
           const int64_t at = ((int64_t)blk * p.hkv + h) * (p.block_size / kGroup) + in / kGroup;
           s[0] = p.k_scale[at];
           s[1] = p.v_scale[at];
@@ -300,14 +306,29 @@ __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const EvictPar
       }
     }
     src_slot[t] = slot;
-    if constexpr (FP8) {
-      ratio[0][t] = s[0];
-      ratio[1][t] = s[1];
-    }
   }
   if (!dst_ok) return;  // (the rows that would go there are dropped, their weights are not)
   __syncthreads();
+  const int part = t % kLanes, row0 = t / kLanes;
+  const int64_t rstride = (int64_t)p.hkv * kRowBytes;
+  const int64_t col = (int64_t)h * kRowBytes + part * 16;
+  uint4 x[2][kPasses];
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int row = row0 + i * kRowsPerPass;
+    const int64_t slot = src_slot[row];
+    x[0][i] = x[1][i] = make_uint4(0, 0, 0, 0);
+    if (slot >= 0) {
+      x[0][i] = ld_once_u4(reinterpret_cast<const uint4 *>(p.k_cache + slot * rstride + col));
+      x[1][i] = ld_once_u4(reinterpret_cast<const uint4 *>(p.v_cache + slot * rstride + col));
+    }
+  }
   if constexpr (FP8) {
+    if (t < kGroup) {
+      ratio[0][t] = s[0];
+      ratio[1][t] = s[1];
+    }
+    __syncthreads();
     if (t < 64) {  // warp 0: K's largest scale, warp 1: V's
       const int kv = t >> 5, l = t & 31;
       float m = fmaxf(ratio[kv][l], ratio[kv][l + 32]);
@@ -322,20 +343,6 @@ __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const EvictPar
       }
     }
     __syncthreads();
-  }
-  const int part = t % kLanes, row0 = t / kLanes;
-  const int64_t rstride = (int64_t)p.hkv * kRowBytes;
-  const int64_t col = (int64_t)h * kRowBytes + part * 16;
-  uint4 x[2][kPasses];
-#pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int row = row0 + i * kRowsPerPass;
-    const int64_t slot = src_slot[row];
-    x[0][i] = x[1][i] = make_uint4(0, 0, 0, 0);
-    if (slot >= 0) {
-      x[0][i] = ld_once_u4(reinterpret_cast<const uint4 *>(p.k_cache + slot * rstride + col));
-      x[1][i] = ld_once_u4(reinterpret_cast<const uint4 *>(p.v_cache + slot * rstride + col));
-    }
   }
   const int64_t dst0 = ((int64_t)dst_blk * p.block_size + dst_in) * rstride + col;
 #pragma unroll

@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kTokenWarps * 32)
     if (lane == 0 && h == 0) record_error(p.err, kErrContext);
     return;
   }
-  if (aborted(p.err)) return;
+  if (__any_sync(kFull, aborted(p.err))) return;  // (warp-uniform)
   const int64_t blk = block_of(p.block_tables + (int64_t)n * p.table_width, ctx - 1, p.block_size,
                                p.num_blocks, p.err, lane == 0 && h == 0);
   if (blk < 0) return;

@@ -397,3 +397,127 @@ def test_zero_contexts_give_zeros():
     for splits in (0, 2):
         out = c.run(num_splits=splits, weights_out=torch.zeros((3, 2, 1), device="cuda"))
         assert (out == 0).all()
+
+
+@pytest.mark.gpu
+def test_nan_stays_where_it_is():
+    """A NaN key makes its KV head's outputs of that sequence NaN and nothing else; a NaN value
+    code its dimension; an infinite or NaN query its own head."""
+    c = Case([300, 200, 129], 8, 2, 256, 450)
+    args = c.device()
+    good = c.run(args)
+    codes = f8.host_codes(args[1]).copy()
+    codes[c.tables[1, 0], 77, 1, 5] = 0x7F
+    bad = list(args)
+    bad[1] = torch.from_numpy(codes).cuda().view(torch.float8_e4m3fn)
+    for splits in (0, 1, 3):
+        out, ref = c.run(bad, num_splits=splits), c.run(args, num_splits=splits)
+        assert out[1, 4:].isnan().all()
+        assert torch.equal(out[1, :4], ref[1, :4]) and torch.equal(out[::2], ref[::2])
+    codes = f8.host_codes(args[2]).copy()
+    codes[c.tables[2, 0], 3, 0, 9] = 0xFF
+    bad = list(args)
+    bad[2] = torch.from_numpy(codes).cuda().view(torch.float8_e4m3fn)
+    out = c.run(bad)
+    assert out[2, :4, 9].isnan().all()
+    out[2, :4, 9] = good[2, :4, 9]
+    assert torch.equal(out, good)
+    for value in (float("inf"), float("nan")):
+        bad = list(args)
+        bad[0] = args[0].clone()
+        bad[0][0, 3, 17] = value
+        out = c.run(bad)
+        assert out[0, 3].isnan().all()
+        out[0, 3] = good[0, 3]
+        assert torch.equal(out, good)
+
+
+@pytest.mark.gpu
+def test_nan_on_the_bf16_cache_with_weights():
+    c = Case([300, 1, 129], 8, 2, 256, 455, fp8=False)
+    args = c.device()
+    for seq, pos in ((0, 77), (1, 0)):      # among others, and as the only key
+        bad = list(args)
+        bad[1] = args[1].clone()
+        bad[1][c.tables[seq, 0], pos, 1, 5] = float("nan")
+        for splits in (0, 1, 3, 9):
+            w0, w1 = (torch.zeros((3, 2, 300), device="cuda") for _ in range(2))
+            out = c.run(bad, num_splits=splits, weights_out=w0)
+            ref = c.run(args, num_splits=splits, weights_out=w1)
+            n = int(c.ctx[seq])
+            assert out[seq, 4:].isnan().all() and w0[seq, 1, :n].isnan().all()
+            out[seq, 4:], w0[seq, 1] = ref[seq, 4:], w1[seq, 1]
+            assert torch.equal(out, ref) and torch.equal(w0, w1)
+
+
+@pytest.mark.gpu
+def test_two_streams_at_once():
+    """Two calls that overlap, with a workspace each, give what they give alone."""
+    cases = [Case([700, 30, 1500], 16, 8, 256, 460 + i) for i in range(2)]
+    alone = [c.run(num_splits=12) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    args = [c.device() for c in cases]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            outs[i].append(cases[i].run(args[i], num_splits=12, stream=s))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o in outs[i]:
+            assert torch.equal(o, alone[i])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fp8", [True, False])
+def test_offsets_past_32_bits(fp8):
+    """A pool of more than 2^32 bytes, used at its far end by every call."""
+    hkv, bs = 8, 256
+    nb = 17000 if fp8 else 9000                       # 4.46 and 4.72 GB a pool
+    far = [nb - 1, nb - 2, 3]
+    g = w.rng(470)
+    lens = [300, 100]
+    tables = np.array([[far[0], far[1]], [far[2], -1]], np.int32)
+    rows = [dev(w.host_bf16_normal(g, (400, hkv, D))) for _ in range(2)]
+    cl, bt = dev(np.array(lens, np.int32)), dev(tables)
+    if fp8:
+        kc, vc = (torch.empty((nb, bs, hkv, D), dtype=torch.uint8, device="cuda").view(
+            torch.float8_e4m3fn) for _ in range(2))
+        ks, vs = (torch.empty((nb, hkv, bs // 64), device="cuda") for _ in range(2))
+        cu = dev(np.array([0, 300, 400], np.int32))
+        pkv.kv_store_fp8(*rows, cl, bt, kc, vc, ks, vs, cu_seqlens=cu)
+        k, v = pkv.kv_gather_fp8(kc, vc, ks, vs, bt, cu, 400)
+        codes, scale = np.zeros((4, bs, hkv, D), np.uint8), np.ones((4, hkv, bs // 64))
+        f8.append(host_f64(rows[0])[:300], codes, scale, [0, 1], 0)
+        assert np.array_equal(host_f64(k)[:300], f8.rows(codes, scale, [0, 1], 300))
+        scales = dict(k_scale=ks, v_scale=vs)
+    else:
+        kc, vc = (torch.empty((nb, bs, hkv, D), dtype=torch.bfloat16, device="cuda")
+                  for _ in range(2))
+        k, v = rows
+        slots = np.concatenate([tables[b, np.arange(n) // bs].astype(np.int64) * bs + np.arange(n) % bs
+                                for b, n in enumerate(lens)])
+        pkv.kv_store(k, v, dev(slots), kc, vc)
+        scales = {}
+    q = dev(w.host_bf16_normal(g, (2, 16, D)))
+    weights = torch.zeros((2, hkv, 300), device="cuda")
+    if fp8:
+        out = pkv.paged_decode_attn_fp8(q, kc, vc, ks, vs, bt, cl, 300, SCALE, weights=weights)
+    else:
+        out = pkv.paged_decode_attn_weights(q, kc, vc, bt, cl, 300, SCALE, weights)
+    K, V, Q = host_f64(k), host_f64(v), host_f64(q)
+    for b, (a, e) in enumerate(((0, 300), (300, 400))):
+        for h in range(16):
+            x = SCALE * K[a:e, h // 2] @ Q[b, h]
+            p = np.exp(x - x.max())
+            p /= p.sum()
+            ref = p @ V[a:e, h // 2]
+            err = np.abs(host_f64(out)[b, h] - ref)
+            assert (err <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -12 * (p @ np.abs(V[a:e, h // 2]))).all()
+    dst = dev(np.array([[nb - 5], [nb - 6]], np.int32))
+    kept, _, n2 = pkv.kv_evict(weights, cl, 300, bt, dst, 64, 8, kc, vc, **scales)
+    assert n2.tolist() == [64, 64] and pkv.get_device_errors() == 0
+    if not fp8:
+        at = kept[0, 2].long().cpu().numpy()
+        assert np.array_equal(host_f64(kc[nb - 5, :64, 2]), K[:300][at, 2])
