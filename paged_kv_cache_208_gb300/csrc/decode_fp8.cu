@@ -35,8 +35,8 @@
 // S(t + 1) is computed while the softmax works on tile t; O has two, so a unit's first PV does
 // not wait for the last unit's epilogue.
 //
-// Rows of a context's last tile past its tokens are not loaded (8-row chunks); V's are zeroed in
-// shared memory, as 0 x NaN from a stale row would poison O.
+// Of a context's last tile only the boxes (of 32 and 16 rows) with its tokens are loaded; V's rows
+// past them are zeroed in shared memory, as 0 x NaN from a stale row would poison O.
 #include "decode_common.cuh"
 #include "fp8_cache.cuh"
 #include "tcgen05.cuh"
@@ -50,6 +50,10 @@ constexpr int kTileBytes = kTile * kD;  // one head's K or V codes of a tile: 16
 // CTA's loads arrive at a tile per 0.65 us either way -- and clusters of 5 and more then do not
 // all fit at once.)
 constexpr int kSlots = 3;
+// Boxes of a context's last tile: as many of 32 rows as fit, the rest in one more of 32 or of 16
+// rows. One thread issues every load, and each costs it about 250 cycles: in boxes of 8 rows a tile
+// of 60 rows took 16 of them (300 contexts of 1 to 500 tokens, 32 / 8 heads: 53.1 us, so 49.8).
+constexpr int kBoxRows = 32, kSmallBoxRows = 16;
 constexpr int kSoftmaxWarps = 8;  // two for each quadrant of tensor memory's lanes
 constexpr int kSoftmaxThreads = kSoftmaxWarps * 32;
 constexpr int kSWarp = 8, kPvWarp = 9, kLoadWarp = 10;
@@ -160,8 +164,10 @@ template <int GC, bool W>
 __global__ void __launch_bounds__(kThreads, 2)
     decode_fp8_kernel(const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap,
-                      const __grid_constant__ CUtensorMap kmap8,
-                      const __grid_constant__ CUtensorMap vmap8, const DecodeParams p) {
+                      const __grid_constant__ CUtensorMap kmap32,
+                      const __grid_constant__ CUtensorMap vmap32,
+                      const __grid_constant__ CUtensorMap kmap16,
+                      const __grid_constant__ CUtensorMap vmap16, const DecodeParams p) {
   using K = Kind<GC>;
   constexpr int kRing = K::kRing, GH = K::kGH;
   extern __shared__ uint8_t smem_raw[];
@@ -223,8 +229,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (threadIdx.x == kLoadWarp * 32) {
     prefetch_tensormap(&kmap);
     prefetch_tensormap(&vmap);
-    prefetch_tensormap(&kmap8);
-    prefetch_tensormap(&vmap8);
+    prefetch_tensormap(&kmap32);
+    prefetch_tensormap(&vmap32);
+    prefetch_tensormap(&kmap16);
+    prefetch_tensormap(&vmap16);
     if (!p.queue) {
       int s, b, xg;
       unit_coords(p, blockIdx.x, s, b, xg);
@@ -395,9 +403,20 @@ __global__ void __launch_bounds__(kThreads, 2)
           // (a row wholly outside the pool: TMA fills zeros, nothing is read)
           const int32_t row = blk_ok ? blk * p.block_size + in_block : -2 * kTile;
           const int rows_here = min(left, kTile);
-          const int chunks = rows_here < kTile && blk_ok ? (rows_here + kChunkRows - 1) / kChunkRows
-                                                         : 0;  // 0: the whole tile in one load
-          const uint32_t bytes = chunks ? chunks * kChunkBytes : kTileBytes;
+          // (blocks are whole tiles: a box that runs past the context stays inside the block)
+          const bool whole = rows_here > kTile - kSmallBoxRows || !blk_ok;
+          const int boxes = (rows_here + kBoxRows - kSmallBoxRows - 1) / kBoxRows;
+          const int boxed = boxes * kBoxRows;
+          const bool rest = boxed < rows_here;
+          const uint32_t bytes =
+              whole ? kTileBytes : (uint32_t)(boxed + (rest ? kSmallBoxRows : 0)) * kD;
+          auto load = [&](uint8_t *dst, const CUtensorMap *map, const CUtensorMap *map32,
+                          const CUtensorMap *map16, uint64_t *bar) {
+            if (whole) return tma_load_3d(dst, map, bar, 0, row, h, policy);
+            for (int r = 0; r < boxed; r += kBoxRows)
+              tma_load_3d(dst + r * kD, map32, bar, 0, row + r, h, policy);
+            if (rest) tma_load_3d(dst + boxed * kD, map16, bar, 0, row + boxed, h, policy);
+          };
           // (a slot's first use finds it empty; later ones wait for the use before, whose phase has
           // the other parity)
           if (k_issued == kSlots && !wait_parity(&sm.k_empty[kr.slot], kr.parity ^ 1u, p.err)) {
@@ -407,11 +426,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           uint8_t *kd = sm.k[kr.slot], *vd = sm.v[vr.slot];
           uint64_t *kbar = &sm.k_full[kr.slot], *vbar = &sm.v_full[vr.slot];
           mbar_arrive_expect_tx(kbar, bytes);
-          if (chunks)
-            for (int c = 0; c < chunks; ++c)
-              tma_load_3d(kd + c * kChunkBytes, &kmap8, kbar, 0, row + kChunkRows * c, h, policy);
-          else
-            tma_load_3d(kd, &kmap, kbar, 0, row, h, policy);
+          load(kd, &kmap, &kmap32, &kmap16, kbar);
           kr.next();
           k_issued = min(k_issued + 1, kSlots);
           if (v_issued == kSlots && !wait_parity(&sm.v_empty[vr.slot], vr.parity ^ 1u, p.err)) {
@@ -421,11 +436,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           mbar_arrive_expect_tx(vbar, bytes + kScaleBytes);
           // (the zero rows of a bad block id take block 0's scales)
           load_scales(vr.slot, blk_ok ? blk : 0, blk_ok ? in_block : 0, h);
-          if (chunks)
-            for (int c = 0; c < chunks; ++c)
-              tma_load_3d(vd + c * kChunkBytes, &vmap8, vbar, 0, row + kChunkRows * c, h, policy);
-          else
-            tma_load_3d(vd, &vmap, vbar, 0, row, h, policy);
+          load(vd, &vmap, &vmap32, &vmap16, vbar);
           vr.next();
           v_issued = min(v_issued + 1, kSlots);
         }
@@ -849,9 +860,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 template <int GC, bool W>
-cudaError_t launch_split_fp8(const CUtensorMap &km, const CUtensorMap &vm, const CUtensorMap &km8,
-                             const CUtensorMap &vm8, const DecodeParams &prm, int num_sms,
-                             cudaStream_t stream) {
+cudaError_t launch_split_fp8(const CUtensorMap (&km)[3], const CUtensorMap (&vm)[3],
+                             const DecodeParams &prm, int num_sms, cudaStream_t stream) {
   static bool configured[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -884,7 +894,8 @@ cudaError_t launch_split_fp8(const CUtensorMap &km, const CUtensorMap &vm, const
     attr[1].val.clusterDim.z = 1;
     cfg.numAttrs = 2;
   }
-  return cudaLaunchKernelEx(&cfg, decode_fp8_kernel<GC, W>, km, vm, km8, vm8, prm);
+  return cudaLaunchKernelEx(&cfg, decode_fp8_kernel<GC, W>, km[0], vm[0], km[1], vm[1], km[2], vm[2],
+                            prm);
 }
 
 }  // namespace
@@ -892,21 +903,21 @@ cudaError_t launch_split_fp8(const CUtensorMap &km, const CUtensorMap &vm, const
 cudaError_t launch_paged_decode_fp8(const DecodeArgs &a, const DecodePlan &p,
                                     cudaStream_t stream) {
   // TMA views of the two pools: {128 dims, num_blocks * block_size rows, Hkv heads} of bytes, a
-  // box per tile, and a box per 8 rows for a context's last tile
-  CUtensorMap km, vm, km8, vm8;
+  // box per tile, and smaller boxes for a context's last tile
+  CUtensorMap km[3], vm[3];
   const uint64_t rows = (uint64_t)a.num_blocks * a.block_size;
   const uint64_t dims[3] = {kD, rows, (uint64_t)a.num_kv_heads};
   const uint64_t strides[2] = {(uint64_t)a.num_kv_heads * kD, kD};
-  const uint32_t box[3] = {kD, kTile, 1};
-  const uint32_t box8[3] = {kD, kChunkRows, 1};
-  auto encode = [&](CUtensorMap *map, const void *pool, const uint32_t *bx) {
+  const uint32_t box_rows[3] = {kTile, kBoxRows, kSmallBoxRows};
+  auto encode = [&](CUtensorMap *map, const void *pool, uint32_t rows_in_box) {
+    const uint32_t box[3] = {kD, rows_in_box, 1};
     return encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(pool), dims,
-                             strides, bx, CU_TENSOR_MAP_SWIZZLE_128B,
+                             strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B) == CUDA_SUCCESS;
   };
-  if (!encode(&km, a.k_cache, box) || !encode(&vm, a.v_cache, box) ||
-      !encode(&km8, a.k_cache, box8) || !encode(&vm8, a.v_cache, box8))
-    return cudaErrorInvalidValue;
+  for (int i = 0; i < 3; ++i)
+    if (!encode(&km[i], a.k_cache, box_rows[i]) || !encode(&vm[i], a.v_cache, box_rows[i]))
+      return cudaErrorInvalidValue;
   DecodeParams prm = decode_params(a, p);
   const int64_t units = (int64_t)p.splits * a.batch * prm.xgroups;
   // the work counter runs to units + grid size - 1 (an int): keep that in range
@@ -918,7 +929,7 @@ cudaError_t launch_paged_decode_fp8(const DecodeArgs &a, const DecodePlan &p,
   if (!queued) prm.queue = nullptr;
   prm.cluster = !queued && p.splits >= 2 && p.splits <= kMaxCluster ? p.splits : 0;
   const bool w = p.scores_at != 0;
-  auto split = [&](auto launch) { return launch(km, vm, km8, vm8, prm, a.num_sms, stream); };
+  auto split = [&](auto launch) { return launch(km, vm, prm, a.num_sms, stream); };
   const cudaError_t e =
       p.heads_per_cta == 8   ? split(w ? launch_split_fp8<8, true> : launch_split_fp8<8, false>)
       : p.heads_per_cta == 4 ? split(w ? launch_split_fp8<4, true> : launch_split_fp8<4, false>)
