@@ -12,9 +12,9 @@
 // positions.
 // evict_copy_kernel, one CTA per (sequence, 64 kept rows, head), moves the K and V rows and the
 // kept weights; it is bound by HBM: each kept row is read once and written once (16 x 32768
-// tokens to 8192, 1.07 GB: 159 us). In an 8-bit cache the 64 rows are
-// one group of the destination, whose scale is the largest of its rows' scales (powers of two:
-// rows of a smaller one lose only what falls below e4m3's normal range).
+// tokens to 8192, 1.07 GB: 160 us). In an 8-bit cache the 64 rows are one group of the
+// destination, whose scale is the largest of its rows' scales (powers of two: rows of a smaller
+// one lose only what falls below e4m3's normal range).
 #include <algorithm>
 
 #include "device_common.cuh"
@@ -62,9 +62,9 @@ constexpr int kBins = 2048;
 // A warp's part of a row, up to kHeld chunks of 128 elements, stays in its lanes' registers as
 // ordered keys, so a row of up to 32768 weights is loaded once, all loads in flight together; a
 // longer row is taken in pieces of 32768 that each pass loads again. What bounds the kernel is
-// its instructions, about 90 per element (128 rows of 32768: 22 us; 28 us when every element
-// compared 64-bit positions and mapped its key again in every pass, 36 us with the elements
-// loaded one by one).
+// its instructions (128 rows of 32768: 19 us; 22 us when every chunk took the path of the row's
+// end, 28 us when every element compared 64-bit positions and mapped its key again in every pass,
+// 36 us with the elements loaded one by one).
 constexpr int kHeld = 8;
 constexpr int kPiece = kHeld * 128 * kSelWarps;
 constexpr uint32_t kTopKey = 0xffffffffu;  // a recent position's: above every number's

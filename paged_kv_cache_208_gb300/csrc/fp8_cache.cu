@@ -2,15 +2,15 @@
 // (kv_gather_fp8). The format is in fp8_cache.cuh.
 //
 // Store: the new tokens are each sequence's last positions. One CTA owns one run (the new rows
-// of one sequence that lie in one group of 64 positions) of one KV head, K and V together, so
-// nothing else touches the group's scale: it holds the run's rows in registers, reduces
+// of one sequence that lie in one group of 64 positions) of K or of V and goes through the KV
+// heads, so nothing else touches a group's scale: it holds a head's rows in registers, reduces
 // max |x| over them, takes the larger of the scale that asks for and the scale of the rows the
 // group already held, and writes the codes. Each row is read once and written once:
 // 512 + 256 bytes per token and head, nothing else of that order. When the scale grows, the
 // rows from before the call are re-rounded to it in place (at most 63 rows of 128 bytes).
 // A step of one token per sequence takes a warp per (sequence, head) instead of a CTA.
 //
-// Gather: one CTA per (run, head); 128 bytes in and 256 bytes out per token, head and K or V.
+// Gather: whole rows of all heads, K or V; 128 bytes in and 256 bytes out per token and head.
 //
 // Both are bound by HBM.
 #include <math.h>
