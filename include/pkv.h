@@ -403,12 +403,15 @@ pkv_status pkv_kv_gather_fp8(const void *k_cache, const void *v_cache, const flo
  * paged_decode_attn_fp8 -- pkv_paged_decode_attn over the 8-bit cache: key and value i of
  * sequence b and head h are code * scale of position i. q and out stay bf16; sums
  * are in fp32; q enters within 2^-22 of its head's largest |q|, a softmax weight the value sum within
- * 2^-15 of itself (and 2^-20 absolutely, where the largest is about 1).
+ * 2^-15 of itself or, with its V scale, 2^-25 of the largest weight with its V scale.
  *
  * k_cache, v_cache: [num_blocks, block_size, num_kv_heads, head_dim] e4m3.
  * k_scale, v_scale: [num_blocks, num_kv_heads, block_size / 64] fp32, positive and finite, at
- *                least 2^-100 (pkv_kv_store_fp8 writes powers of two from 2^-90).
- * weights_out:   NULL, or the attention weights too: see pkv_paged_decode_attn_weights.
+ *                least 2^-100 (pkv_kv_store_fp8 writes powers of two from 2^-90). V's scales of
+ *                one context should lie within 2^100 of one another: a weight is formed with its V
+ *                scale, and below 2^-126 of the largest such product it drops out of the sums.
+ * weights_out:   NULL (then weights_in too), or the attention weights as well: see
+ *                pkv_paged_decode_attn_weights.
  * workspace:     pkv_decode_fp8_workspace_bytes(..., weights = weights_out != NULL) bytes, with
  *                the contract of pkv_paged_decode_attn's (its first word zeroed once).
  * Everything else as for pkv_paged_decode_attn.

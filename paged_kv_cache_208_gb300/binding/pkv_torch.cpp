@@ -281,7 +281,7 @@ PyObject *kv_store_fp8(PyObject *const *a) {
   const int64_t ks = rows(k, "k", c), vs = rows(v, "v", c);
   if (k.size(0) != v.size(0)) fail(PyExc_ValueError, "k and v must hold the same tokens");
   const Lists l = lists(a[2], a[3], c.index);
-  const int32_t *cu = given(a[8]) ? ints(a[8], "cu_seqlens", c.index, {l.batch + 1}) : nullptr;
+  const int32_t *cu = given(a[8]) ? ints(a[8], "cu_seqlens", c.index, {(int64_t)l.batch + 1}) : nullptr;
   On on(c.index, a[9]);
   return status_or(pkv_kv_store_fp8(k.data_ptr(), ks, v.data_ptr(), vs, cu, l.context_lens,
                                     l.tables, l.width, l.batch, k.size(0), c.k.data_ptr(),
@@ -418,6 +418,14 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     return F(args);
   } catch (const Fail &f) {
     PyErr_SetString(f.type, f.text.c_str());
+  } catch (const c10::OutOfMemoryError &e) {
+    if (PyObject *torch = PyImport_ImportModule("torch")) {
+      if (PyObject *type = PyObject_GetAttrString(torch, "OutOfMemoryError")) {
+        PyErr_SetString(type, e.what_without_backtrace());
+        Py_DECREF(type);
+      }
+      Py_DECREF(torch);
+    }
   } catch (const std::exception &e) {
     if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
   } catch (...) {

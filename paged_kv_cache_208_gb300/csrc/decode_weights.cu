@@ -120,6 +120,7 @@ pkv_status decode_with_weights(Call c, cudaStream_t stream) {
       a.num_kv_heads <= 0 || a.num_q_heads % a.num_kv_heads != 0 || c.head_dim <= 0 ||
       a.block_size <= 0 || a.num_blocks <= 0 || a.table_width <= 0 || !isfinite(a.scale))
     return PKV_ERR_INVALID_ARG;
+  if (c.weights_in && !c.weights) return PKV_ERR_INVALID_ARG;
   if (c.weights && (c.weights_out_stride < c.max_context_len ||
                     (c.weights_in && c.weights_in_stride < c.max_context_len)))
     return PKV_ERR_INVALID_ARG;

@@ -387,8 +387,9 @@ extern "C" pkv_status pkv_kv_store_fp8(const void *k, int64_t k_tok_stride, cons
   if (k_tok_stride % 8 != 0 || v_tok_stride % 8 != 0 || !aligned16(k) || !aligned16(v) ||
       !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scale) || !aligned16(v_scale))
     return PKV_ERR_UNSUPPORTED;
+  const int num_sms = current_sm_count();
   unsigned int *err = current_error_word();
-  if (!err) return PKV_ERR_CUDA;
+  if (num_sms <= 0 || !err) return PKV_ERR_CUDA;
   StoreParams prm{};
   prm.k = static_cast<const uint8_t *>(k);
   prm.v = static_cast<const uint8_t *>(v);
@@ -423,7 +424,7 @@ extern "C" pkv_status pkv_kv_store_fp8(const void *k, int64_t k_tok_stride, cons
   const int64_t runs = num_tokens / kFp8Group + 2 * (int64_t)num_seqs;
   const int64_t heads_per_cta =
       std::max<int64_t>(1, std::min<int64_t>(num_kv_heads, 2 * runs * num_kv_heads /
-                                                               (10 * (int64_t)current_sm_count())));
+                                                               (10 * (int64_t)num_sms)));
   const int64_t grid = 2 * runs * ((num_kv_heads + heads_per_cta - 1) / heads_per_cta);
   if (grid > INT32_MAX) return PKV_ERR_UNSUPPORTED;
   return launch_after(kv_store_fp8_run_kernel, grid, kRunThreads, st, prm, (int)heads_per_cta) ==
@@ -451,8 +452,9 @@ extern "C" pkv_status pkv_kv_gather_fp8(const void *k_cache, const void *v_cache
   if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scale) || !aligned16(v_scale) ||
       !aligned16(k_out) || !aligned16(v_out))
     return PKV_ERR_UNSUPPORTED;
+  const int num_sms = current_sm_count();
   unsigned int *err = current_error_word();
-  if (!err) return PKV_ERR_CUDA;
+  if (num_sms <= 0 || !err) return PKV_ERR_CUDA;
   GatherParams prm{};
   prm.k_cache = static_cast<const uint8_t *>(k_cache);
   prm.v_cache = static_cast<const uint8_t *>(v_cache);
@@ -472,7 +474,7 @@ extern "C" pkv_status pkv_kv_gather_fp8(const void *k_cache, const void *v_cache
   // runs in parts of fewer rows while there are less than about ten CTAs for an SM
   const int64_t runs = total_k / kFp8Group + 2 * (int64_t)num_seqs;
   int rows_per_cta = kFp8Group;
-  while (rows_per_cta > 8 && 2 * runs * (kFp8Group / rows_per_cta) < 10 * (int64_t)current_sm_count())
+  while (rows_per_cta > 8 && 2 * runs * (kFp8Group / rows_per_cta) < 10 * (int64_t)num_sms)
     rows_per_cta /= 2;
   const int64_t grid = 2 * runs * (kFp8Group / rows_per_cta);
   if (grid > INT32_MAX || num_kv_heads > (1 << 20)) return PKV_ERR_UNSUPPORTED;

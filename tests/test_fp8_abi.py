@@ -87,6 +87,10 @@ def test_decode_argument_checks():
     assert _decode16(wo=None) == pkv.ERR_INVALID_ARG
 
 
+def test_decode_weights_in_needs_weights_out():
+    assert _decode8(wi=FAKE, wis=100, wo=None) == pkv.ERR_INVALID_ARG
+
+
 def test_workspace_queries():
     for n in (L.pkv_decode_fp8_workspace_bytes(4, 16, 8, 64, 300, 0, 0),
               L.pkv_decode_fp8_workspace_bytes(0, 16, 8, 128, 300, 0, 1),
