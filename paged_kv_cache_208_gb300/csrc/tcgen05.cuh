@@ -1,7 +1,7 @@
 // tcgen05.cuh -- inline-PTX wrappers for the 5th-generation tensor cores (sm_100 family):
 // tensor-memory allocation, UMMA issue/commit as a CTA pair uses them on bf16 operands and as
 // one CTA does on e4m3 operands, TMEM loads and stores, and the shared-memory matrix and
-// instruction descriptors with 128-byte swizzle.
+// instruction descriptors with 128-byte swizzle (and one layout without).
 #pragma once
 
 #include <stdint.h>
@@ -142,6 +142,15 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t smem_byte_addr, uin
   return (uint64_t)((smem_byte_addr & 0x3FFFFu) >> 4) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
          ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46)  // descriptor version
          | (2ull << 61);                                           // 128-byte swizzle
+}
+
+// The same without swizzle, for an 8-bit MN-major tile: rows of K of 16 bytes (16 columns), 8 rows
+// to a 128-byte block; k_stride from one 8-row block to the next along K, mn_stride from one 16
+// columns to the next.
+__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t smem_byte_addr, uint32_t k_stride,
+                                                 uint32_t mn_stride) {
+  return (uint64_t)((smem_byte_addr & 0x3FFFFu) >> 4) | ((uint64_t)(k_stride >> 4) << 16) |
+         ((uint64_t)(mn_stride >> 4) << 32) | (1ull << 46);
 }
 
 // One lane of the (converged) warp: the lowest active lane. The UMMAs and the commit that
