@@ -36,8 +36,9 @@
 //
 // Algorithmic HBM bytes per (sequence, KV head, token): 256 (K) + 256 (V).
 //
-// With weights (W) the kernel also leaves every key's scaled score and every query head's
-// log-sum-exp, from which decode_weights.cu makes the attention weights.
+// With weights (W) the kernel also leaves every key's scaled score, and makes the attention weights
+// of them once it knows every query head's log-sum-exp (WeightsPass), or leaves that too for the
+// kernel of decode_weights.cu (decode_forms_weights).
 #include "decode_common.cuh"
 
 namespace pkv {
@@ -72,6 +73,8 @@ struct DecodeSmem {
   // than kLandSplits), rank 0's `acc` is free for them
   uint64_t cl_bar;
   uint64_t cl_ready;
+  uint64_t cl_lse;  // in a peer: the merged log2-sum-exps have landed in `lse`
+  float lse[GC];    // of the whole context, for the weights
 };
 static_assert(kMaxCluster - 1 <= kConsumerWarps, "the peers' results fit in rank 0's acc");
 
@@ -90,6 +93,10 @@ __host__ __device__ constexpr size_t smem_bytes(int cluster) {
               ? land_offset<GC>() + (size_t)(cluster - 1) * GC * (kD + 1) * sizeof(float)
               : sizeof(DecodeSmem<GC>)) + 1024;  // + 1024: the layout starts 1024-aligned
 }
+
+// two CTAs per SM: 228 KiB less 1 KiB each that the system keeps
+static_assert(smem_bytes<1>(kLandSplits) <= 113 * 1024 && smem_bytes<2>(kLandSplits) <= 113 * 1024,
+              "two CTAs fit on an SM");
 
 // Byte offset of 16-byte chunk j (dims 8j..8j+7) of token t inside a swizzled tile. The TMA
 // box is {64 dims, 64 tokens, 2 halves}: half j / 8 of every token in its own 8 KiB plane of
@@ -128,6 +135,7 @@ __global__ void __maxnreg__(96)
     if (p.cluster) {
       mbar_init(&sm.cl_bar, p.cluster - 1);  // one arrival per peer
       mbar_init(&sm.cl_ready, 1);
+      mbar_init(&sm.cl_lse, 1);
     }
     fence_mbar_init();
   }
@@ -136,6 +144,7 @@ __global__ void __maxnreg__(96)
   if (p.cluster) cluster_arrive_relaxed();
   // cluster merge: this CTA's normalised output and log2-sum-exp (consumer thread g * kD + d)
   float cl_o = 0.f, cl_lse = -INFINITY;
+  [[maybe_unused]] int cl_end = 0;  // where its positions end
   // Launched as a programmatic dependent of the stream's previous kernel: everything above
   // (barrier set-up) may overlap its tail; wait for that grid's completion and memory before
   // touching global memory.
@@ -614,14 +623,26 @@ __global__ void __maxnreg__(96)
       if (p.cluster) {  // merged by the cluster's rank 0 at the end
         cl_o = o;
         cl_lse = lse;  // -inf when the unit had no keys
+        cl_end = tok_end;
       } else if (p.splits == 1 || (un.s == 0 && tok_end == L)) {
         // the unit holds the whole context: the output itself (the merge kernel skips rows
         // whose context fits one split)
         p.out[row * kD + d] = bf16_bits_rn(o);
-        if (W && d == 0) p.lse[row] = lse;
+        if (W && d == 0) {
+          if (p.w_out) sm.lse[g] = lse;
+          else p.lse[row] = lse;
+        }
       } else {
         p.part_o[(row * p.splits + un.s) * kD + d] = o;
         if (d == 0) p.part_lse[row * p.splits + un.s] = lse;
+      }
+    }
+    if constexpr (W) {
+      if (p.w_out && !p.cluster) {
+        // (the scores are visible since the merge's barrier, the log2-sum-exps after this one)
+        WeightsPass<GC> pass(p, un.b, h, tok_begin, tok_end, threadIdx.x, kConsumerWarps * 32);
+        named_barrier_sync(2, kConsumerWarps * 32);
+        pass.finish(sm.lse);
       }
     }
     if (!p.queue) break;  // a static grid gives each CTA one unit: nothing follows
@@ -647,6 +668,11 @@ __global__ void __maxnreg__(96)
                                                    land_offset<GC>());
   float *land_lse = land_o + (size_t)(p.cluster - 1) * GC * kD;
   const int g = threadIdx.x / kD, d = threadIdx.x % kD;
+  // With weights: this CTA's share of them (its scores are visible to all its threads since the
+  // merge of its warps).
+  std::conditional_t<W, WeightsPass<GC>, NoWeights> pass(
+      p, (blockIdx.x / p.splits) / p.xgroups, (blockIdx.x / p.splits) % p.xgroups,
+      (int)rank * p.chunk, p.w_out ? cl_end : 0, threadIdx.x, GC * kD);
   if (rank != 0) {
     if (lend && !wait_own(&sm.cl_ready, 0, p.err)) return;
     const uint32_t bar = cluster_addr(smem_addr(&sm.cl_bar), 0);
@@ -654,6 +680,17 @@ __global__ void __maxnreg__(96)
     const int r = (int)rank - 1;
     st_async_f32(cluster_addr(smem_addr(land_o + ((size_t)r * GC + g) * kD + d), 0), cl_o, bar);
     if (d == 0) st_async_f32(cluster_addr(smem_addr(land_lse + r * GC + g), 0), cl_lse, bar);
+    if constexpr (W) {
+      if (p.w_out) {  // the weights of this split, once rank 0 has merged the log2-sum-exps
+        if (threadIdx.x == 0) mbar_arrive_expect_tx(&sm.cl_lse, GC * sizeof(float));
+        if (wait_own(&sm.cl_lse, 0, p.err)) {
+          pass.finish(sm.lse);
+        } else {  // no answer: stay until no other CTA can write here any more
+          cluster_arrive_relaxed();
+          cluster_wait();
+        }
+      }
+    }
     return;
   }
   if (lend) {
@@ -685,7 +722,21 @@ __global__ void __maxnreg__(96)
   if (!sm.stop) {
     const bool some = W ? wsum != 0.f : wsum > 0.f;
     p.out[row * kD + d] = bf16_bits_rn(some ? acc / wsum : 0.f);
-    if (W && d == 0) p.lse[row] = M + __log2f(wsum);
+  }
+  if constexpr (W) {
+    const float lse = M + __log2f(wsum);
+    if (p.w_out) {
+      if (d == 0) {
+        sm.lse[g] = lse;
+        for (int r = 1; r < p.cluster; ++r)
+          st_async_f32(cluster_addr(smem_addr(&sm.lse[g]), r), lse,
+                       cluster_addr(smem_addr(&sm.cl_lse), r));
+      }
+      named_barrier_sync(2, GC * kD);
+      pass.finish(sm.lse);
+    } else if (d == 0 && !sm.stop) {
+      p.lse[row] = lse;
+    }
   }
 }
 
@@ -788,6 +839,19 @@ DecodePlan plan_decode(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
   return p;
 }
 
+bool decode_queued(const DecodeArgs &a, const DecodePlan &p) {
+  return (int64_t)a.num_sms * 2 < (int64_t)p.splits * a.batch * a.num_kv_heads * p.head_groups;
+}
+
+// A unit has to hold all query heads of its KV head, and the CTA has to learn their log2-sum-exps:
+// from its own unit (one split) or from the cluster's merge. (With a kernel of its own for the
+// weights 8 x 1024 over the 8-bit cache takes 9.9 us instead of 9.1, over the bf16 cache 11.4
+// instead of 10.2, and 256 ragged bf16 contexts 179 us instead of 176.)
+bool decode_forms_weights(const DecodeArgs &a, const DecodePlan &p) {
+  return a.weights_out && p.head_groups == 1 &&
+         (p.splits == 1 || (!decode_queued(a, p) && p.splits <= kMaxCluster));
+}
+
 cudaError_t launch_paged_decode(const DecodeArgs &a, const DecodePlan &p, cudaStream_t stream) {
   // TMA views of the two pools: {64 dims, num_blocks * block_size rows, 2 * Hkv half-heads}
   // (the half-head stride, 128 bytes, is the innermost of the two): a tile lands as two
@@ -843,7 +907,7 @@ cudaError_t launch_paged_decode(const DecodeArgs &a, const DecodePlan &p, cudaSt
   // memory and no merge kernel. With the queue the kernel leaves the counters at zero
   // itself, so the call enqueues nothing before it (the kernel follows the previous one as a
   // programmatic dependent).
-  const bool queued = (int64_t)a.num_sms * 2 < units;
+  const bool queued = decode_queued(a, p);
   if (!queued) prm.queue = nullptr;
   prm.cluster = !queued && p.splits >= 2 && p.splits <= kMaxCluster ? p.splits : 0;
   auto split = [&](auto kernel_of) { return kernel_of(km, vm, km8, vm8, prm, a.num_sms, stream); };

@@ -5,6 +5,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "device_common.cuh"
 #include "launch.h"
@@ -69,6 +70,72 @@ struct DecodeParams {
   float *scores;
   int64_t score_stride;
   float *lse;
+  // where the decode kernel forms the weights itself (w_out != nullptr): positions below w_cap
+  const float *w_in;
+  int64_t w_in_stride;
+  float *w_out;
+  int64_t w_out_stride;
+  int32_t w_cap;
+};
+
+// The attention weights of positions [begin, end) of sequence b and KV head h, from the scores that
+// this CTA left (a barrier has made them visible to its threads) and the query heads'
+// log2-sum-exps: decode_weights_kernel's sums, in its order. Thread `tid` of `threads` takes every
+// threads-th position; the first ones' loads are under way once the object is made, before the
+// log2-sum-exps have to be known.
+template <int GC>
+struct WeightsPass {
+  static constexpr int kAhead = GC <= 2 ? 4 : GC == 4 ? 2 : 1;  // positions loaded together
+  const float *s, *in;
+  float *out;
+  int64_t stride;
+  int i0, end, step, group;
+  float x[kAhead][GC], w[kAhead];
+  uint32_t err;
+
+  __device__ __forceinline__ WeightsPass(const DecodeParams &p, int b, int h, int begin, int last,
+                                         int tid, int threads) {
+    const int64_t bh = (int64_t)b * p.num_kv_heads + h;
+    group = p.group;
+    stride = p.score_stride;
+    s = p.scores + bh * group * stride;
+    in = p.w_in ? p.w_in + bh * p.w_in_stride : nullptr;
+    out = p.w_out + bh * p.w_out_stride;
+    i0 = begin + tid;
+    end = min(last, p.w_cap);
+    step = threads;
+    err = (uint32_t)ld_global_s32(reinterpret_cast<const int32_t *>(p.err));
+    load();
+  }
+  __device__ __forceinline__ void load() {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = i0 + k * step;
+      w[k] = in && i < end ? in[i] : 0.f;
+#pragma unroll
+      for (int g = 0; g < GC; ++g) x[k][g] = g < group && i < end ? s[g * stride + i] : -INFINITY;
+    }
+  }
+  __device__ __forceinline__ void finish(const float *lse) {
+    if (err & kErrTimeout) return;  // a wait gave up somewhere: the scores may not be complete
+    while (i0 < end) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int i = i0 + k * step;
+        float sum = 0.f;
+#pragma unroll
+        for (int g = 0; g < GC; ++g)
+          if (g < group) sum += fast_exp2(x[k][g] - lse[g]);
+        if (i < end) out[i] = w[k] + sum;
+      }
+      i0 += kAhead * step;
+      if (i0 < end) load();
+    }
+  }
+};
+
+struct NoWeights {
+  __device__ __forceinline__ NoWeights(const DecodeParams &, int, int, int, int, int, int) {}
 };
 
 // Unit u -> (split s, sequence b, head group xg). A cluster launch orders the units
@@ -173,6 +240,13 @@ inline DecodeParams decode_params(const DecodeArgs &a, const DecodePlan &p) {
     prm.scores = reinterpret_cast<float *>(ws + p.scores_at);
     prm.score_stride = p.score_stride;
     prm.lse = reinterpret_cast<float *>(ws + p.lse_at);
+    if (decode_forms_weights(a, p)) {
+      prm.w_in = a.weights_in;
+      prm.w_in_stride = a.weights_in_stride;
+      prm.w_out = a.weights_out;
+      prm.w_out_stride = a.weights_out_stride;
+      prm.w_cap = a.weights_cap;
+    }
   }
   return prm;
 }

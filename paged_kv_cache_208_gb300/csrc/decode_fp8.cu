@@ -116,7 +116,10 @@ struct DecodeFp8Smem {
   uint64_t q_ready[2], s_full[2], p_full[2], pv_done[2], o_full[2], o_free[2];
   uint64_t unit_full[K::kRing], unit_empty[K::kRing];
   uint64_t drain[2];
-  uint64_t cl_bar, cl_ready;  // cluster merge: the peers' results have landed; the area is lent
+  // cluster merge: the peers' results have landed; the area is lent; in a peer: the merged
+  // log2-sum-exps have landed in `lse`
+  uint64_t cl_bar, cl_ready, cl_lse;
+  float lse[GC];  // of the whole context, for the weights
 };
 
 template <int GC>
@@ -203,6 +206,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (p.cluster) {
       mbar_init(&sm.cl_bar, p.cluster - 1);  // one arrival per peer
       mbar_init(&sm.cl_ready, 1);
+      mbar_init(&sm.cl_lse, 1);
     }
     fence_mbar_init();
   }
@@ -219,6 +223,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   // cluster merge: this CTA's normalised outputs of dimension threadIdx.x % 128 (the thread's
   // heads) and their log2-sum-exps
   float cl_o[GH], cl_lse[GH];
+  [[maybe_unused]] int cl_end = 0;  // where its positions end
 #pragma unroll
   for (int g = 0; g < GH; ++g) {
     cl_o[g] = 0.f;
@@ -824,7 +829,9 @@ __global__ void __launch_bounds__(kThreads, 2)
           out = __fdividef(acc, sum);
           lse = __log2f(sum) - nref[g];
         }
+        if (W && i == 0 && !p.cluster) sm.lse[g0 + g] = lse;
         if (p.cluster) {  // merged by the cluster's rank 0 at the end
+          cl_end = tok_begin + un.tokens;
           cl_o[g] = out;
           cl_lse[g] = lse;
         } else if (g < heads) {
@@ -832,11 +839,20 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (un.whole) {
             // the unit holds the whole context: the output itself (the merge kernel skips it)
             p.out[row * kD + i] = bf16_bits_rn(out);
-            if (W && i == 0) p.lse[row] = lse;
+            if (W && i == 0 && !p.w_out) p.lse[row] = lse;
           } else {
             p.part_o[(row * p.splits + un.s) * kD + i] = out;
             if (i == 0) p.part_lse[row * p.splits + un.s] = lse;
           }
+        }
+      }
+      if constexpr (W) {
+        if (p.w_out && !p.cluster) {
+          // (the scores are visible since the barrier above, the log2-sum-exps after this one)
+          WeightsPass<GC> pass(p, un.b, h, tok_begin, tok_begin + un.tokens, threadIdx.x,
+                               kSoftmaxThreads);
+          named_barrier_sync(3, kSoftmaxThreads);
+          pass.finish(sm.lse);
         }
       }
       if (!p.queue) break;  // a static grid gives each CTA one unit: nothing follows
@@ -860,6 +876,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                                                    land_offset<GC>());
   float *land_lse = land_o + (size_t)(p.cluster - 1) * GC * kD;
   const int d = threadIdx.x & 127, g0 = (threadIdx.x >> 7) * GH;
+  // With weights: this CTA's share of them (its scores are visible to all its threads since the
+  // barrier above).
+  std::conditional_t<W, WeightsPass<GC>, NoWeights> pass(
+      p, (blockIdx.x / p.splits) / p.xgroups, (blockIdx.x / p.splits) % p.xgroups,
+      (int)rank * p.chunk, p.w_out ? cl_end : 0, threadIdx.x, kSoftmaxThreads);
   if (rank != 0) {
     if (lend && !wait_own(&sm.cl_ready, 0, p.err)) return;
     const uint32_t bar = cluster_addr(smem_addr(&sm.cl_bar), 0);
@@ -870,6 +891,17 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int at = r * GC + g0 + g;
       st_async_f32(cluster_addr(smem_addr(land_o + (size_t)at * kD + d), 0), cl_o[g], bar);
       if (d == 0) st_async_f32(cluster_addr(smem_addr(land_lse + at), 0), cl_lse[g], bar);
+    }
+    if constexpr (W) {
+      if (p.w_out) {  // the weights of this split, once rank 0 has merged the log2-sum-exps
+        if (threadIdx.x == 0) mbar_arrive_expect_tx(&sm.cl_lse, GC * sizeof(float));
+        if (wait_own(&sm.cl_lse, 0, p.err)) {
+          pass.finish(sm.lse);
+        } else {  // no answer: stay until no other CTA can write here any more
+          cluster_arrive_relaxed();
+          cluster_wait();
+        }
+      }
     }
     return;
   }
@@ -896,7 +928,20 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int64_t row = (int64_t)b * p.num_q_heads + h * p.group + in_group;
     if (!sm.stop && in_group < p.group) {
       p.out[row * kD + d] = bf16_bits_rn(wsum == 0.f ? 0.f : acc / wsum);
-      if (W && d == 0) p.lse[row] = M + __log2f(wsum);
+      if (W && d == 0 && !p.w_out) p.lse[row] = M + __log2f(wsum);
+    }
+    if (W && d == 0 && p.w_out) {
+      const float lse = M + __log2f(wsum);
+      sm.lse[g0 + g] = lse;
+      for (int r = 1; r < p.cluster; ++r)
+        st_async_f32(cluster_addr(smem_addr(&sm.lse[g0 + g]), r), lse,
+                     cluster_addr(smem_addr(&sm.cl_lse), r));
+    }
+  }
+  if constexpr (W) {
+    if (p.w_out) {
+      named_barrier_sync(3, kSoftmaxThreads);
+      pass.finish(sm.lse);
     }
   }
 }
@@ -967,7 +1012,7 @@ cudaError_t launch_paged_decode_fp8(const DecodeArgs &a, const DecodePlan &p,
   prm.units = (int32_t)units;
   // as for the bf16 cache: with no more units than CTAs each CTA takes one and the splits of a
   // (sequence, head group) meet in a cluster; else the queue, and a merge kernel
-  const bool queued = (int64_t)a.num_sms * 2 < units;
+  const bool queued = decode_queued(a, p);
   if (!queued) prm.queue = nullptr;
   prm.cluster = !queued && p.splits >= 2 && p.splits <= kMaxCluster ? p.splits : 0;
   const bool w = p.scores_at != 0;

@@ -1,5 +1,7 @@
-// decode_weights.cu -- the attention weights of a decode step, and the entry points of decode
-// attention over the 8-bit cache and of decode attention with weights.
+// decode_weights.cu -- the attention weights of a decode step whose split kernel does not form them
+// itself (decode_forms_weights: several units share a KV head, or the splits meet in the merge
+// kernel), and the entry points of decode attention over the 8-bit cache and of decode attention
+// with weights.
 //
 // The split kernel has left every key's scaled score s (log2 domain) and every query head's
 // log2-sum-exp; the weight that KV head h's query heads give to position i is
@@ -138,13 +140,20 @@ pkv_status decode_with_weights(Call c, cudaStream_t stream) {
   a.num_sms = current_sm_count();
   a.err = current_error_word();
   if (a.num_sms <= 0 || !a.err) return PKV_ERR_CUDA;
+  if (c.weights) {
+    a.weights_in = c.weights_in;
+    a.weights_in_stride = c.weights_in_stride;
+    a.weights_out = c.weights_out;
+    a.weights_out_stride = c.weights_out_stride;
+    a.weights_cap = c.max_context_len;
+  }
   const DecodePlan plan = plan_decode(a.batch, a.num_q_heads, a.num_kv_heads, c.max_context_len,
                                       c.num_splits, a.num_sms, c.fp8, c.weights);
   if (!a.workspace || c.workspace_bytes < plan.workspace_bytes || !aligned16(a.workspace))
     return PKV_ERR_WORKSPACE;
   cudaError_t e = c.fp8 ? launch_paged_decode_fp8(a, plan, stream)
                         : launch_paged_decode(a, plan, stream);
-  if (e != cudaSuccess || !c.weights || c.max_context_len == 0)
+  if (e != cudaSuccess || !c.weights || c.max_context_len == 0 || decode_forms_weights(a, plan))
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
   uint8_t *ws = static_cast<uint8_t *>(a.workspace);
   WeightsParams w{};

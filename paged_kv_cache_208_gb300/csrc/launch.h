@@ -64,10 +64,20 @@ struct DecodeArgs {
   // 8-bit cache: [num_blocks, num_kv_heads, block_size / 64]
   const float *k_scale = nullptr;
   const float *v_scale = nullptr;
+  // attention weights [batch, num_kv_heads, >= max_context_len], rows these strides apart
+  const float *weights_in = nullptr;
+  int64_t weights_in_stride = 0;
+  float *weights_out = nullptr;
+  int64_t weights_out_stride = 0;
+  int32_t weights_cap = 0;  // max_context_len
 };
 constexpr size_t kDecodeQueueBytes = 16;  // the workspace's header: the work counters
 cudaError_t launch_paged_decode(const DecodeArgs &a, const DecodePlan &plan,
                                 cudaStream_t stream);
+// the units of a call go through the work queue (else each CTA has one, and splits meet in clusters)
+bool decode_queued(const DecodeArgs &a, const DecodePlan &plan);
+// the decode kernel itself forms the attention weights: no kernel after it does
+bool decode_forms_weights(const DecodeArgs &a, const DecodePlan &plan);
 
 // decode_fp8.cu
 cudaError_t launch_paged_decode_fp8(const DecodeArgs &a, const DecodePlan &plan,
