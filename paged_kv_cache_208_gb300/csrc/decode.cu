@@ -52,11 +52,15 @@ constexpr int kThreads = (kConsumerWarps + 1) * 32;
 constexpr int kTileBytes = kTile * kD * 2;  // one head's K (or V) for 64 tokens: 16 KiB
 constexpr int kPlaneBytes = kTileBytes / 2;  // one 64-dim half of it (a plane of 64 rows)
 
+// The warps merge a unit's heads in shared memory a pair at a time (two CTAs have to fit on an SM).
+template <int GC>
+constexpr int kPair = GC < 2 ? GC : 2;
+
 template <int GC>
 struct DecodeSmem {
   uint8_t k[kStages][kTileBytes];  // must start 1024-byte aligned (128-byte swizzle atoms)
   uint8_t v[kStages][kTileBytes];
-  float acc[kConsumerWarps][GC][kD];
+  float acc[kConsumerWarps][kPair<GC>][kD];
   float m[kConsumerWarps][GC];
   float l[kConsumerWarps][GC];
   uint16_t qs[kRing][GC][kD];  // q rows of the queued units
@@ -76,26 +80,32 @@ struct DecodeSmem {
   uint64_t cl_lse;  // in a peer: the merged log2-sum-exps have landed in `lse`
   float lse[GC];    // of the whole context, for the weights
 };
-static_assert(kMaxCluster - 1 <= kConsumerWarps, "the peers' results fit in rank 0's acc");
 
 // Where a cluster's rank 0 receives its peers' results: with up to kLandSplits splits in an
 // area of its own past the fixed layout (two CTAs still fit on an SM), else in its merge
 // buffer `acc`, lent once its own merge has read it. (splits - 1) x GC x kD outputs, then
 // (splits - 1) x GC log2-sum-exps, fp32.
-constexpr int kLandSplits = 4;
+template <int GC>
+constexpr int kLandSplits = GC <= 2 ? 4 : 1;
+template <int GC>
+constexpr int kMaxSplits = GC <= 2 ? kMaxCluster : 4;  // of a cluster
+template <int GC>
+constexpr bool kLendFits = (kMaxSplits<GC> - 1) * GC * (kD + 1) <= kConsumerWarps * kPair<GC> * kD;
+static_assert(kLendFits<1> && kLendFits<2> && kLendFits<4>, "the peers' results fit");
 template <int GC>
 __host__ __device__ constexpr size_t land_offset() {
   return (sizeof(DecodeSmem<GC>) + 15) / 16 * 16;
 }
 template <int GC>
 __host__ __device__ constexpr size_t smem_bytes(int cluster) {
-  return (cluster >= 2 && cluster <= kLandSplits
+  return (cluster >= 2 && cluster <= kLandSplits<GC>
               ? land_offset<GC>() + (size_t)(cluster - 1) * GC * (kD + 1) * sizeof(float)
               : sizeof(DecodeSmem<GC>)) + 1024;  // + 1024: the layout starts 1024-aligned
 }
 
 // two CTAs per SM: 228 KiB less 1 KiB each that the system keeps
-static_assert(smem_bytes<1>(kLandSplits) <= 113 * 1024 && smem_bytes<2>(kLandSplits) <= 113 * 1024,
+static_assert(smem_bytes<1>(kLandSplits<1>) <= 113 * 1024 &&
+                  smem_bytes<2>(kLandSplits<2>) <= 113 * 1024 && smem_bytes<4>(1) <= 113 * 1024,
               "two CTAs fit on an SM");
 
 // Byte offset of 16-byte chunk j (dims 8j..8j+7) of token t inside a swizzled tile. The TMA
@@ -142,8 +152,15 @@ __global__ void __maxnreg__(96)
   __syncthreads();
   // in a cluster: this CTA's barriers are set up (waited for before the first remote access)
   if (p.cluster) cluster_arrive_relaxed();
-  // cluster merge: this CTA's normalised output and log2-sum-exp (consumer thread g * kD + d)
-  float cl_o = 0.f, cl_lse = -INFINITY;
+  // cluster merge: this CTA's normalised outputs and log2-sum-exps (consumer thread t: heads t / kD,
+  // kPair + t / kD, ..)
+  constexpr int kRounds = GC / kPair<GC>;
+  float cl_o[kRounds], cl_lse[kRounds];
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    cl_o[r] = 0.f;
+    cl_lse[r] = -INFINITY;
+  }
   [[maybe_unused]] int cl_end = 0;  // where its positions end
   // Launched as a programmatic dependent of the stream's previous kernel: everything above
   // (barrier set-up) may overlap its tail; wait for that grid's completion and memory before
@@ -309,8 +326,10 @@ __global__ void __maxnreg__(96)
       }
       const int h = un.xg / p.head_groups;
       const int hq0 = h * p.group + (un.xg % p.head_groups) * GC;
-      mbar_arrive_expect_tx(&sm.unit_full[slot], GC * kD * 2);
-      bulk_copy_g2s(sm.qs[slot], p.q + ((int64_t)un.b * p.num_q_heads + hq0) * kD, GC * kD * 2,
+      const uint32_t q_bytes =
+          (GC <= 2 ? GC : min(GC, p.group - (un.xg % p.head_groups) * GC)) * kD * 2;
+      mbar_arrive_expect_tx(&sm.unit_full[slot], q_bytes);
+      bulk_copy_g2s(sm.qs[slot], p.q + ((int64_t)un.b * p.num_q_heads + hq0) * kD, q_bytes,
                     &sm.unit_full[slot]);
       // the unit that reads the context's last position brings the new token's K and V rows
       // of its head into shared memory now (the pool write happens before its last tile)
@@ -435,6 +454,9 @@ __global__ void __maxnreg__(96)
     if (un.ntiles < 0) break;
     const int h = un.xg / p.head_groups;
     const int hq0 = h * p.group + (un.xg % p.head_groups) * GC;
+    // (four heads a unit, with weights: the last unit of a group may have fewer, whose rows of q
+    // are whatever the slot held)
+    const int heads = GC <= 2 ? GC : min(GC, p.group - (un.xg % p.head_groups) * GC);
     // q's A fragments, held in registers for the unit: load j gives dims [32j, 32j + 32) as
     // a0, a2 of k-step 2j and a0, a2 of k-step 2j + 1 (rows 8-15, a1 and a3, are zero)
     uint32_t qa[4][4];
@@ -454,7 +476,7 @@ __global__ void __maxnreg__(96)
     const int tok_end = (int)min(L, (int64_t)tok_begin + p.chunk);
     // this lane's scores in the buffer for the weights kernel
     float *const score_row =
-        W && gq < GC ? p.scores + ((int64_t)un.b * p.num_q_heads + hq0 + gq) * p.score_stride
+        W && gq < heads ? p.scores + ((int64_t)un.b * p.num_q_heads + hq0 + gq) * p.score_stride
                      : nullptr;
 
     float m_run = -INFINITY;  // running maximum of head gq (the same in the lane's quad)
@@ -500,7 +522,7 @@ __global__ void __maxnreg__(96)
       float sb = (s0[1] + s1[1]) * p.qscale;
       if (W && score_row)
         *reinterpret_cast<float2 *>(score_row + tok_begin + it * kTile + tok) = make_float2(sa, sb);
-      if (gq >= GC) sa = sb = -INFINITY;
+      if (gq >= heads) sa = sb = -INFINITY;
       if (n_valid < kTile) {
         if (tok >= n_valid) sa = -INFINITY;
         if (tok + 1 >= n_valid) sb = -INFINITY;
@@ -573,70 +595,79 @@ __global__ void __maxnreg__(96)
         for (int e = 0; e < 4; e += 2) {
           if constexpr (GC == 1) {  // columns 0 and 1 of one lane
             acc[m][e] += acc[m][e + 1];
-          } else {  // columns 0, 1 and 2, 3: lanes tq = 0 and 1
-            acc[m][e] += __shfl_xor_sync(kFull, acc[m][e], 1);
-            acc[m][e + 1] += __shfl_xor_sync(kFull, acc[m][e + 1], 1);
+          } else {  // column c and c + GC: lanes tq and tq + GC / 2
+            acc[m][e] += __shfl_xor_sync(kFull, acc[m][e], GC / 2);
+            acc[m][e + 1] += __shfl_xor_sync(kFull, acc[m][e + 1], GC / 2);
           }
         }
     }
+    bool stopped = false;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int hh = 2 * tq + e;
-      if (hh < GC) {
+    for (int r = 0; r < kRounds; ++r) {
+      if (r > 0) named_barrier_sync(2, kConsumerWarps * 32);  // the pair before has been read
 #pragma unroll
-        for (int m = 0; m < 8; ++m) {
-          sm.acc[warp][hh][16 * m + gq] = acc[m][e];
-          sm.acc[warp][hh][16 * m + gq + 8] = acc[m][2 + e];
+      for (int e = 0; e < 2; ++e) {
+        const int hh = 2 * (tq - r) + e;  // of the round's pair
+        if (hh >= 0 && hh < kPair<GC>) {
+#pragma unroll
+          for (int m = 0; m < 8; ++m) {
+            sm.acc[warp][hh][16 * m + gq] = acc[m][e];
+            sm.acc[warp][hh][16 * m + gq + 8] = acc[m][2 + e];
+          }
+        }
+      }
+      stopped = barrier_or(1, kConsumerWarps * 32, !ok);  // a wait gave up: stop together
+      if (stopped) break;
+      const int gp = threadIdx.x / kD, g = r * kPair<GC> + gp;
+      const int d = threadIdx.x % kD;
+      if (gp < kPair<GC>) {
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kConsumerWarps; ++w) M = fmaxf(M, sm.m[w][g]);
+        float o = 0.f, lse = -INFINITY;
+        bool any = M != -INFINITY;
+        if constexpr (W) {
+          if (!any) {  // no keys, or NaN scores only
+            M = 0.f;
+#pragma unroll
+            for (int w = 0; w < kConsumerWarps; ++w) any = any || isnan(sm.l[w][g]);
+          }
+        }
+        if (any) {
+          float lsum = 0.f, osum = 0.f;
+#pragma unroll
+          for (int w = 0; w < kConsumerWarps; ++w) {
+            const float f = fast_exp2(sm.m[w][g] - M);
+            lsum = fmaf(sm.l[w][g], f, lsum);
+            osum = fmaf(sm.acc[w][gp][d], f, osum);
+          }
+          // lsum >= 1 (the warp holding the maximum contributes 2^0): the approximate division
+          // and log2 err far below one bf16 rounding of the result
+          o = __fdividef(osum, lsum);
+          lse = M + __log2f(lsum);
+        }
+        const int64_t row = (int64_t)un.b * p.num_q_heads + hq0 + g;
+        if (p.cluster) {  // merged by the cluster's rank 0 at the end
+          cl_o[r] = o;
+          cl_lse[r] = lse;  // -inf when the unit had no keys
+          cl_end = tok_end;
+        } else if (g < heads) {
+          if (p.splits == 1 || (un.s == 0 && tok_end == L)) {
+            // the unit holds the whole context: the output itself (the merge kernel skips rows
+            // whose context fits one split)
+            p.out[row * kD + d] = bf16_bits_rn(o);
+            if (W && d == 0) {
+              if (p.w_out) sm.lse[g] = lse;
+              else p.lse[row] = lse;
+            }
+          } else {
+            p.part_o[(row * p.splits + un.s) * kD + d] = o;
+            if (d == 0) p.part_lse[row * p.splits + un.s] = lse;
+          }
         }
       }
     }
-    if (barrier_or(1, kConsumerWarps * 32, !ok)) break;  // a wait gave up: stop together
-    const int g = threadIdx.x / kD;
-    const int d = threadIdx.x % kD;
-    if (g < GC) {
-      float M = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kConsumerWarps; ++w) M = fmaxf(M, sm.m[w][g]);
-      float o = 0.f, lse = -INFINITY;
-      bool any = M != -INFINITY;
-      if constexpr (W) {
-        if (!any) {  // no keys, or NaN scores only
-          M = 0.f;
-#pragma unroll
-          for (int w = 0; w < kConsumerWarps; ++w) any = any || isnan(sm.l[w][g]);
-        }
-      }
-      if (any) {
-        float lsum = 0.f, osum = 0.f;
-#pragma unroll
-        for (int w = 0; w < kConsumerWarps; ++w) {
-          const float f = fast_exp2(sm.m[w][g] - M);
-          lsum = fmaf(sm.l[w][g], f, lsum);
-          osum = fmaf(sm.acc[w][g][d], f, osum);
-        }
-        // lsum >= 1 (the warp holding the maximum contributes 2^0): the approximate division
-        // and log2 err far below one bf16 rounding of the result
-        o = __fdividef(osum, lsum);
-        lse = M + __log2f(lsum);
-      }
-      const int64_t row = (int64_t)un.b * p.num_q_heads + hq0 + g;
-      if (p.cluster) {  // merged by the cluster's rank 0 at the end
-        cl_o = o;
-        cl_lse = lse;  // -inf when the unit had no keys
-        cl_end = tok_end;
-      } else if (p.splits == 1 || (un.s == 0 && tok_end == L)) {
-        // the unit holds the whole context: the output itself (the merge kernel skips rows
-        // whose context fits one split)
-        p.out[row * kD + d] = bf16_bits_rn(o);
-        if (W && d == 0) {
-          if (p.w_out) sm.lse[g] = lse;
-          else p.lse[row] = lse;
-        }
-      } else {
-        p.part_o[(row * p.splits + un.s) * kD + d] = o;
-        if (d == 0) p.part_lse[row * p.splits + un.s] = lse;
-      }
-    }
+    if (stopped) break;
     if constexpr (W) {
       if (p.w_out && !p.cluster) {
         // (the scores are visible since the merge's barrier, the log2-sum-exps after this one)
@@ -660,26 +691,30 @@ __global__ void __maxnreg__(96)
   // waits are bounded), rank 0 always lends the buffer and every peer always sends, so no
   // store lands in a CTA that has left.
   cluster_wait();  // every CTA's barriers are set up
-  if (threadIdx.x >= GC * kD) return;
+  constexpr int kMergers = kPair<GC> * kD;
+  if (threadIdx.x >= kMergers) return;
   const uint32_t rank = cluster_ctarank();
-  const bool lend = p.cluster > kLandSplits;
+  const bool lend = p.cluster > kLandSplits<GC>;
   float *land_o = lend ? &sm.acc[0][0][0]  // peer r + 1's outputs at [r][g][d], then its lses
                        : reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(&sm) +
                                                    land_offset<GC>());
   float *land_lse = land_o + (size_t)(p.cluster - 1) * GC * kD;
-  const int g = threadIdx.x / kD, d = threadIdx.x % kD;
+  const int gp = threadIdx.x / kD, d = threadIdx.x % kD;  // heads gp, kPair + gp, ..
   // With weights: this CTA's share of them (its scores are visible to all its threads since the
   // merge of its warps).
   std::conditional_t<W, WeightsPass<GC>, NoWeights> pass(
       p, (blockIdx.x / p.splits) / p.xgroups, (blockIdx.x / p.splits) % p.xgroups,
-      (int)rank * p.chunk, p.w_out ? cl_end : 0, threadIdx.x, GC * kD);
+      (int)rank * p.chunk, p.w_out ? cl_end : 0, threadIdx.x, kMergers);
   if (rank != 0) {
     if (lend && !wait_own(&sm.cl_ready, 0, p.err)) return;
     const uint32_t bar = cluster_addr(smem_addr(&sm.cl_bar), 0);
     if (threadIdx.x == 0) mbar_arrive_expect_tx_remote(bar, GC * (kD + 1) * sizeof(float));
-    const int r = (int)rank - 1;
-    st_async_f32(cluster_addr(smem_addr(land_o + ((size_t)r * GC + g) * kD + d), 0), cl_o, bar);
-    if (d == 0) st_async_f32(cluster_addr(smem_addr(land_lse + r * GC + g), 0), cl_lse, bar);
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+      const int at = ((int)rank - 1) * GC + i * kPair<GC> + gp;
+      st_async_f32(cluster_addr(smem_addr(land_o + (size_t)at * kD + d), 0), cl_o[i], bar);
+      if (d == 0) st_async_f32(cluster_addr(smem_addr(land_lse + at), 0), cl_lse[i], bar);
+    }
     if constexpr (W) {
       if (p.w_out) {  // the weights of this split, once rank 0 has merged the log2-sum-exps
         if (threadIdx.x == 0) mbar_arrive_expect_tx(&sm.cl_lse, GC * sizeof(float));
@@ -695,47 +730,54 @@ __global__ void __maxnreg__(96)
   }
   if (lend) {
     // every merging thread has read `acc` (its values are in registers): lend it to the peers
-    named_barrier_sync(2, GC * kD);
+    named_barrier_sync(2, kMergers);
     if (threadIdx.x == 0)
       for (int r = 1; r < p.cluster; ++r)
         mbar_arrive_remote(cluster_addr(smem_addr(&sm.cl_ready), r));
   }
   if (!wait_own(&sm.cl_bar, 0, p.err)) return;
-  float M = cl_lse;
-  for (int r = 0; r < p.cluster - 1; ++r) M = fmaxf(M, land_lse[r * GC + g]);
-  float acc = 0.f, wsum = 0.f;
-  if (W && M == -INFINITY) M = 0.f;  // no keys, or NaN scores only
-  if (W || M != -INFINITY) {
-    const float w0 = fast_exp2(cl_lse - M);  // 0 for a split with no keys
-    wsum = w0;
-    acc = w0 * cl_o;
-    for (int r = 0; r < p.cluster - 1; ++r) {
-      const float wgt = fast_exp2(land_lse[r * GC + g] - M);
-      wsum += wgt;
-      acc = fmaf(wgt, land_o[((size_t)r * GC + g) * kD + d], acc);
-    }
-  }
   const int unit0 = blockIdx.x;  // rank 0 holds split 0
   const int b = (unit0 / p.splits) / p.xgroups, xg = (unit0 / p.splits) % p.xgroups;
-  const int h = xg / p.head_groups;
-  const int64_t row = (int64_t)b * p.num_q_heads + h * p.group + (xg % p.head_groups) * GC + g;
-  if (!sm.stop) {
-    const bool some = W ? wsum != 0.f : wsum > 0.f;
-    p.out[row * kD + d] = bf16_bits_rn(some ? acc / wsum : 0.f);
-  }
-  if constexpr (W) {
-    const float lse = M + __log2f(wsum);
-    if (p.w_out) {
-      if (d == 0) {
+  const int h = xg / p.head_groups, hg = xg % p.head_groups;
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    const int g = i * kPair<GC> + gp;
+    float M = cl_lse[i];
+    for (int r = 0; r < p.cluster - 1; ++r) M = fmaxf(M, land_lse[r * GC + g]);
+    float acc = 0.f, wsum = 0.f;
+    if (W && M == -INFINITY) M = 0.f;  // no keys, or NaN scores only
+    if (W || M != -INFINITY) {
+      const float w0 = fast_exp2(cl_lse[i] - M);  // 0 for a split with no keys
+      wsum = w0;
+      acc = w0 * cl_o[i];
+      for (int r = 0; r < p.cluster - 1; ++r) {
+        const float wgt = fast_exp2(land_lse[r * GC + g] - M);
+        wsum += wgt;
+        acc = fmaf(wgt, land_o[((size_t)r * GC + g) * kD + d], acc);
+      }
+    }
+    const int64_t row = (int64_t)b * p.num_q_heads + h * p.group + hg * GC + g;
+    const bool live = !sm.stop && (GC <= 2 || hg * GC + g < p.group);
+    if (live) {
+      const bool some = W ? wsum != 0.f : wsum > 0.f;
+      p.out[row * kD + d] = bf16_bits_rn(some ? acc / wsum : 0.f);
+    }
+    if constexpr (W) {
+      const float lse = M + __log2f(wsum);
+      if (d == 0 && p.w_out) {
         sm.lse[g] = lse;
         for (int r = 1; r < p.cluster; ++r)
           st_async_f32(cluster_addr(smem_addr(&sm.lse[g]), r), lse,
                        cluster_addr(smem_addr(&sm.cl_lse), r));
+      } else if (d == 0 && live) {
+        p.lse[row] = lse;
       }
-      named_barrier_sync(2, GC * kD);
+    }
+  }
+  if constexpr (W) {
+    if (p.w_out) {
+      named_barrier_sync(2, kMergers);
       pass.finish(sm.lse);
-    } else if (d == 0 && !sm.stop) {
-      p.lse[row] = lse;
     }
   }
 }
@@ -751,7 +793,7 @@ cudaError_t launch_split(const CUtensorMap &km, const CUtensorMap &vm, const CUt
   if (dev < 64 && !configured[dev]) {
     cudaError_t e = cudaFuncSetAttribute(decode_split_kernel<GC, W>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem_bytes<GC>(kLandSplits));
+                                         (int)smem_bytes<GC>(kLandSplits<GC>));
     if (e != cudaSuccess) return e;
     // all of the unified L1/shared storage as shared memory, so two CTAs fit on an SM
     e = cudaFuncSetAttribute(decode_split_kernel<GC, W>,
@@ -791,9 +833,16 @@ DecodePlan plan_decode(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
   DecodePlan p{};
   const int group = num_q_heads / num_kv_heads;
   const int kTile = fp8 ? 128 : 64;
-  // bf16: one or two heads a unit. 8-bit: as many of a group as its 8 MMA columns hold (the
+  // bf16: one or two heads a unit, with weights up to four (the kernel has rows for eight, and with
+  // weights two columns of the second product for each; every unit more reads K and V again: 136 x
+  // 2602 to 5227 tokens with 10 / 2 heads 141 us, 238 with one head a unit; 256 x 2048 ragged with 32 /
+  // 8 heads 197 us, 241 with two). 8-bit: as many of a group as its 8 MMA columns hold (the
   // heads of a unit read each code once), rounded up to a kernel instance.
-  p.heads_per_cta = fp8 ? (group > 4 ? 8 : group > 2 ? 4 : 2) : (group % 2 == 0) ? 2 : 1;
+  p.heads_per_cta = fp8                    ? (group > 4 ? 8 : group > 2 ? 4 : 2)
+                    : weights && group > 2 ? 4
+                    : group % 2 == 0       ? 2
+                                           : 1;
+  p.max_cluster = !fp8 && p.heads_per_cta == 4 ? kMaxSplits<4> : kMaxCluster;
   p.head_groups = (group + p.heads_per_cta - 1) / p.heads_per_cta;
   const int64_t max_ctx = max_context_len > 0 ? max_context_len : 1;
   const int64_t max_tiles = (max_ctx + kTile - 1) / kTile;
@@ -818,7 +867,7 @@ DecodePlan plan_decode(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
     const int64_t units = (int64_t)batch * num_kv_heads * p.head_groups;
     const int64_t max_unit_tiles = units >= 8LL * num_sms ? 32 : 16;
     int64_t S = (max_tiles + max_unit_tiles - 1) / max_unit_tiles;
-    while (S < max_tiles && S < kMaxCluster &&
+    while (S < max_tiles && S < p.max_cluster &&
            units * (S + 1) <= (S + 1 > 4 ? (int64_t)num_sms * (fp8 ? 15 : 10) / 10
                                          : (int64_t)num_sms * (fp8 ? 20 : 17) / 10))
       ++S;
@@ -849,7 +898,7 @@ bool decode_queued(const DecodeArgs &a, const DecodePlan &p) {
 // instead of 10.2, and 256 ragged bf16 contexts 179 us instead of 176.)
 bool decode_forms_weights(const DecodeArgs &a, const DecodePlan &p) {
   return a.weights_out && p.head_groups == 1 &&
-         (p.splits == 1 || (!decode_queued(a, p) && p.splits <= kMaxCluster));
+         (p.splits == 1 || (!decode_queued(a, p) && p.splits <= p.max_cluster));
 }
 
 cudaError_t launch_paged_decode(const DecodeArgs &a, const DecodePlan &p, cudaStream_t stream) {
@@ -909,11 +958,14 @@ cudaError_t launch_paged_decode(const DecodeArgs &a, const DecodePlan &p, cudaSt
   // programmatic dependent).
   const bool queued = decode_queued(a, p);
   if (!queued) prm.queue = nullptr;
-  prm.cluster = !queued && p.splits >= 2 && p.splits <= kMaxCluster ? p.splits : 0;
+  prm.cluster = !queued && p.splits >= 2 && p.splits <= p.max_cluster ? p.splits : 0;
   auto split = [&](auto kernel_of) { return kernel_of(km, vm, km8, vm8, prm, a.num_sms, stream); };
-  const bool two = p.heads_per_cta == 2;
-  const cudaError_t e = p.scores_at ? split(two ? launch_split<2, true> : launch_split<1, true>)
-                                    : split(two ? launch_split<2, false> : launch_split<1, false>);
+  const int gc = p.heads_per_cta;
+  const cudaError_t e =
+      p.scores_at ? split(gc == 4   ? launch_split<4, true>
+                          : gc == 2 ? launch_split<2, true>
+                                    : launch_split<1, true>)
+                  : split(gc == 2 ? launch_split<2, false> : launch_split<1, false>);
   if (e != cudaSuccess || p.splits == 1 || prm.cluster) return e;
   return p.scores_at ? launch_combine<true>(a, p, prm, stream)
                      : launch_combine<false>(a, p, prm, stream);

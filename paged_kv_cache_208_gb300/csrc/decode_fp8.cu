@@ -1014,7 +1014,7 @@ cudaError_t launch_paged_decode_fp8(const DecodeArgs &a, const DecodePlan &p,
   // (sequence, head group) meet in a cluster; else the queue, and a merge kernel
   const bool queued = decode_queued(a, p);
   if (!queued) prm.queue = nullptr;
-  prm.cluster = !queued && p.splits >= 2 && p.splits <= kMaxCluster ? p.splits : 0;
+  prm.cluster = !queued && p.splits >= 2 && p.splits <= p.max_cluster ? p.splits : 0;
   const bool w = p.scores_at != 0;
   auto split = [&](auto launch) { return launch(km, vm, prm, a.num_sms, stream); };
   const cudaError_t e =

@@ -25,6 +25,7 @@ struct DecodePlan {
   int32_t splits;      // splits of the longest context
   int32_t head_groups; // CTAs per KV head (query heads handled two at a time)
   int32_t heads_per_cta;
+  int32_t max_cluster; // splits that may meet in a cluster
   size_t workspace_bytes;
   // with weights: where the log2-sum-exps and the scores [batch, num_q_heads, score_stride]
   // lie in the workspace (0: no weights)

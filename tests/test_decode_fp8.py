@@ -521,3 +521,34 @@ def test_offsets_past_32_bits(fp8):
     if not fp8:
         at = kept[0, 2].long().cpu().numpy()
         assert np.array_equal(host_f64(kc[nb - 5, :64, 2]), K[:300][at, 2])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("num_splits", [0, 1, 3, 4, 6])
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (10, 2), (7, 1)])
+def test_bf16_weights_of_larger_groups(hq, hkv, num_splits):
+    """Four query heads to a unit, a whole group or the last unit with fewer."""
+    c = Case(RAGGED, hq, hkv, 256, 230 + hq, fp8=False)
+    ref, tol, ws, wtol = c.reference()
+    start = torch.rand((len(RAGGED), hkv, max(RAGGED)), device="cuda")
+    weights = start.clone()
+    out = c.run(weights=weights, num_splits=num_splits)
+    check_out(out, ref, tol)
+    check_weights(weights, start, ws, wtol, c.ctx)
+    assert pkv.get_device_errors() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv", [(16, 4), (40, 8)])
+def test_bf16_weights_of_larger_groups_work_queue(hq, hkv):
+    g = w.rng(250 + hq)
+    ctx = g.integers(0, 300, 120)
+    ctx[:3] = 700, 1, 0
+    c = Case(ctx, hq, hkv, 256, 251, fp8=False)
+    ref, tol, ws, wtol = c.reference()
+    for num_splits in (0, 2):
+        weights = torch.zeros((len(ctx), hkv, int(ctx.max())), device="cuda")
+        out = c.run(weights=weights, num_splits=num_splits)
+        check_out(out, ref, tol, str(num_splits))
+        check_weights(weights, torch.zeros_like(weights), ws, wtol, ctx, str(num_splits))
+    assert pkv.get_device_errors() == 0
