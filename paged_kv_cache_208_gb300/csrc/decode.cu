@@ -871,6 +871,12 @@ DecodePlan plan_decode(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
            units * (S + 1) <= (S + 1 > 4 ? (int64_t)num_sms * (fp8 ? 15 : 10) / 10
                                          : (int64_t)num_sms * (fp8 ? 20 : 17) / 10))
       ++S;
+    // Few units of long contexts over the 8-bit cache: a CTA's loads run at a tile per 0.65 us, so
+    // six tiles to a CTA and the merge kernel beat a cluster (1 x 17188 with 2 / 1 heads 16.2 -> 13
+    // us, 8 x 16384 with 8 / 1 17.5 -> 15.7 us; 1 x 8192 with 32 / 8 takes 10.4 us with a cluster of
+    // 8, 12.0 with 16 splits).
+    const int64_t wide = fp8 && !weights ? std::min(max_tiles / 6, num_sms / units) & ~3LL : 0;
+    if (wide >= 16) S = wide;
     const int64_t per = (max_ctx + S - 1) / S;
     p.chunk = (int32_t)((per + kTile - 1) / kTile * kTile);
   }
