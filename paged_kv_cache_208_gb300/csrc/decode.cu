@@ -861,15 +861,20 @@ DecodePlan plan_decode(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
     // Measured on batches 1..64 at 1024 tokens, the best split count is the largest that
     // keeps its splits within one cluster and the grid within about 1.7 CTAs per SM, or
     // within one CTA per SM for clusters of more than 4 (larger clusters do not all fit at
-    // once when SMs hold two CTAs). An 8-bit unit costs less and pays up to two CTAs per SM, or
-    // one and a half with clusters of more than 4 (16 / 2 heads, 33 x 4999: 21.5 us with 4 splits,
-    // 24.8 with 3; 4 x 4096: 9.7 us with 7 splits, 11.3 with 4 or 8).
+    // once when SMs hold two CTAs). An 8-bit unit costs less and pays as long as the clusters all
+    // run at once, with two CTAs per SM: pairs do up to 304 CTAs, larger clusters leave places in
+    // the GPCs empty, differently from device to device (38 x 1633 with 16 / 2 heads: 13.0 us with 3
+    // splits, 18.8 with 4, 304 CTAs, the last of which start when the first have ended; 12 x 2048:
+    // 11.8 with 2, 15.7 with 3, 288; 4 x 4096: 9.3 with 7, 10.7 with 8, 256).
     const int64_t units = (int64_t)batch * num_kv_heads * p.head_groups;
     const int64_t max_unit_tiles = units >= 8LL * num_sms ? 32 : 16;
     int64_t S = (max_tiles + max_unit_tiles - 1) / max_unit_tiles;
     while (S < max_tiles && S < p.max_cluster &&
-           units * (S + 1) <= (S + 1 > 4 ? (int64_t)num_sms * (fp8 ? 15 : 10) / 10
-                                         : (int64_t)num_sms * (fp8 ? 20 : 17) / 10))
+           units * (S + 1) <= (int64_t)num_sms *
+                                  (S + 1 > 4   ? (fp8 ? 160 : 100)
+                                   : S + 1 > 2 ? (fp8 ? 175 : 170)
+                                               : (fp8 ? 200 : 170)) /
+                                  100)
       ++S;
     // Few units of long contexts over the 8-bit cache: a CTA's loads run at a tile per 0.65 us, so
     // six tiles to a CTA and the merge kernel beat a cluster (1 x 17188 with 2 / 1 heads 16.2 -> 13
