@@ -906,9 +906,13 @@ bool decode_queued(const DecodeArgs &a, const DecodePlan &p) {
 // A unit has to hold all query heads of its KV head, and the CTA has to learn their log2-sum-exps:
 // from its own unit (one split) or from the cluster's merge. (With a kernel of its own for the
 // weights 8 x 1024 over the 8-bit cache takes 9.9 us instead of 9.1, over the bf16 cache 11.4
-// instead of 10.2, and 256 ragged bf16 contexts 179 us instead of 176.)
+// instead of 10.2, and 256 ragged bf16 contexts 179 us instead of 176.) With eight heads a unit the
+// pass over a long split's scores by one CTA takes longer than that kernel: 256 ragged contexts up to
+// 1024 with 64 / 8 heads 97 us, 84 with the kernel; 1 x 14274 with 8 / 1, 1792 tokens a split, 23.2
+// and 21.0, but 33 x 4999 with 16 / 2, 1280 tokens, 23.0 and 23.9.
 bool decode_forms_weights(const DecodeArgs &a, const DecodePlan &p) {
   return a.weights_out && p.head_groups == 1 &&
+         (p.heads_per_cta < 8 || (!decode_queued(a, p) && p.chunk <= 1280)) &&
          (p.splits == 1 || (!decode_queued(a, p) && p.splits <= p.max_cluster));
 }
 
