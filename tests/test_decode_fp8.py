@@ -552,3 +552,17 @@ def test_bf16_weights_of_larger_groups_work_queue(hq, hkv):
         check_out(out, ref, tol, str(num_splits))
         check_weights(weights, torch.zeros_like(weights), ws, wtol, ctx, str(num_splits))
     assert pkv.get_device_errors() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv", [(2, 1), (8, 2), (8, 1)])
+def test_fp8_few_long_contexts(hq, hkv):
+    """More splits than a cluster holds, chosen by the call, next to empty and short contexts; with
+    weights the splits of a cluster, whose eight heads leave the weights to a kernel of their own."""
+    c = Case([13700, 0, 12400, 1], hq, hkv, 256, 480 + hq)
+    ref, tol, ws, wtol = c.reference()
+    check_out(c.run(), ref, tol)
+    weights = torch.zeros((4, hkv, 13700), device="cuda")
+    check_out(c.run(weights=weights), ref, tol, "with weights")
+    check_weights(weights, torch.zeros_like(weights), ws, wtol, c.ctx)
+    assert pkv.get_device_errors() == 0
