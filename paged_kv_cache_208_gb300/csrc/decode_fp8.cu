@@ -95,6 +95,7 @@ struct Unit8 {
   int32_t tokens;            // of the split
   int32_t whole;             // the split is the whole context: its result is the output
   int32_t skip;              // the ring's next tile is a speculative load to be dropped
+  int32_t h, head0;          // KV head; first query head of the unit in its group
 };
 
 template <int GC>
@@ -377,17 +378,19 @@ __global__ void __launch_bounds__(kThreads, 2)
           ok = false;
           break;
         }
+        const int h = un.xg / p.head_groups;
+        un.h = h;
+        un.head0 = (un.xg - h * p.head_groups) * GC;
         sm.unit[slot] = un;
         ++pushed;
         if (un.ntiles < 0) {
           mbar_arrive(&sm.unit_full[slot]);
           break;
         }
-        const int h = un.xg / p.head_groups, hg = un.xg % p.head_groups;
-        const uint32_t q_bytes = min(GC, p.group - hg * GC) * kD * 2;
+        const uint32_t q_bytes = min(GC, p.group - un.head0) * kD * 2;
         mbar_arrive_expect_tx(&sm.unit_full[slot], q_bytes);
         bulk_copy_g2s(sm.qs[slot],
-                      p.q + ((int64_t)un.b * p.num_q_heads + h * p.group + hg * GC) * kD, q_bytes,
+                      p.q + ((int64_t)un.b * p.num_q_heads + h * p.group + un.head0) * kD, q_bytes,
                       &sm.unit_full[slot]);
         // The table is read a block ahead (an entry's latency is longer than a tile's share of the
         // bandwidth: with a read per tile the loads ran at one tile per 0.68 us and CTA).
@@ -496,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         // precede tile t - 1: their S is complete once the softmax has answered tile t - 2.
         if (t >= 2 && !(ok = wait_all(&sm.p_full[t & 1], ((t - 2) >> 1) & 1))) break;
         const int qb = units & 1;
-        const int heads = min(GC, p.group - (un.xg % p.head_groups) * GC);
+        const int heads = min(GC, p.group - un.head0);
         uint8_t *qt = sm.q[qb];
         // row r, lane's four dimensions: byte 4 lane of the 128, swizzled by 16-byte chunks
         auto at = [&](int r) {
@@ -640,10 +643,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       ++taken;
       if (un.ntiles < 0) break;
       if (un.skip) vr.next();
-      const int h = un.xg / p.head_groups, hg = un.xg % p.head_groups;
-      const int heads = min(GC, p.group - hg * GC) - g0;  // of this thread (may be <= 0)
+      [[maybe_unused]] const int h = un.h;
+      const int heads = min(GC, p.group - un.head0) - g0;  // of this thread (may be <= 0)
       const int tok_begin = un.s * p.chunk;
-      const int64_t row0 = (int64_t)un.b * p.num_q_heads + h * p.group + hg * GC + g0;
+      const int64_t row0 = (int64_t)un.b * p.num_q_heads + h * p.group + un.head0 + g0;
       const int ub = units & 1;
       const uint32_t o_addr = lanes + K::kOBase + ub * K::kNO + half * K::kHalf;
 
@@ -711,8 +714,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
           for (int g = 0; g < GH; ++g) over = over || x[g] + nref[g] > kTop + kHeadroom;
         }
-        // a token above the reference (always in the unit's first tile): raise it
-        if (barrier_or(2, kSoftmaxThreads, over)) {
+        // a token above the reference (in the unit's first tile there is one): raise it
+        if (it == 0 || barrier_or(2, kSoftmaxThreads, over)) {
 #pragma unroll
           for (int g = 0; g < GH; ++g) {
             const float m = redux_max(ok ? x[g] : -INFINITY);
