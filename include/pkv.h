@@ -403,7 +403,8 @@ pkv_status pkv_kv_gather_fp8(const void *k_cache, const void *v_cache, const flo
  * paged_decode_attn_fp8 -- pkv_paged_decode_attn over the 8-bit cache: key and value i of
  * sequence b and head h are code * scale of position i. q and out stay bf16; sums
  * are in fp32; q enters within 2^-22 of its head's largest |q|, a softmax weight the value sum within
- * 2^-15 of itself or, with its V scale, 2^-25 of the largest weight with its V scale.
+ * 2^-19 of itself or, with its V scale, 2^-30 of its split's largest weight with its V scale (at
+ * most 2^-13 in all over a split of 131072 tokens).
  *
  * k_cache, v_cache: [num_blocks, block_size, num_kv_heads, head_dim] e4m3.
  * k_scale, v_scale: [num_blocks, num_kv_heads, block_size / 64] fp32, positive and finite, at

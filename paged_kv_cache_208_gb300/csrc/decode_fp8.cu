@@ -17,9 +17,14 @@
 //       hi = e4m3(q'), lo = e4m3(32 (q' - hi)). 4 + 4 bits hold bf16's 8: exact down to 2^-14 of
 //       the maximum, within 2^-22 of it below.
 //   P:  w = 2^(s + ev - R + 5) with ev = log2 of V's scale of the group and R a reference that
-//       no s + ev exceeds by more than 3, so w <= 256; w = t1 + t2 / 32 + t3 / 1024, each t the
-//       e4m3 of what the ones before left: within 2^-15 of w, and within 2^-20 absolutely (2^-25
-//       of the reference's own weight).
+//       no s + ev exceeds by more than 3, so w <= 256; w = t1 + t2 / 32 + t3 / 32^2 + t4 / 32^3,
+//       each t the e4m3 of 32 times what the ones before left: within 2^-19 of w (2^-4 and three
+//       times 2^-5) or, where t4 is below e4m3's normal range, 2^-25 (2^-30 of the reference's own
+//       weight). Three parts hold 2^-14 and 2^-20: 131071 equal weights of 2^-24.6 beside a token
+//       with nearly all of the weight gave an output of 3.48 for 2.36 in one split, and 0.9% of
+//       the outputs of 256 ragged contexts rounded to another neighbour than with fp32 weights
+//       (0.05% with four). The columns are there anyway; the fourth conversion costs 0.1 us of 7.2
+//       (8 x 1024), 0.2 of 16.8 (33 x 4999 with 16 / 2 heads), 0.8 of 64.3 (256 up to 1024, 64 / 8).
 // K's scale multiplies the scores. V's scale is in the exponent, so that one accumulator serves
 // groups of any scales: it holds sum w code = 2^(5 - R) sum 2^s v, and l sums w 2^-ev =
 // 2^(5 - R) 2^s in fp32 from the unrounded w; their quotient is the output.
@@ -67,12 +72,12 @@ template <int GC>
 struct Kind {
   // Heads of a softmax thread: the first or the second half of the unit's. Rows of Q (columns of
   // S) are hi then lo of the first half's heads, then of the second's; columns of P (and of O)
-  // likewise t1, t2, t3, the second half's from column kHalf on.
+  // likewise t1 to t4, the second half's from column kHalf on.
   static constexpr int kGH = GC / 2;
   static constexpr int kRing = GC <= 4 ? 4 : 2;  // units in flight
   static constexpr int kQRows = GC <= 4 ? 8 : 16;   // 2 GC rows used
   static constexpr int kNO = GC <= 4 ? 16 : 32;     // N of the second product, P's columns
-  static constexpr int kHalf = kNO / 2;             // a half's columns, 3 GH of them used
+  static constexpr int kHalf = kNO / 2;             // a half's columns, 4 GH of them used
   static constexpr uint32_t kOBase = 32;            // TMEM: S buffers at 0 and 16, then O's
   static constexpr uint32_t kTmemCols = GC <= 4 ? 64 : 128;
   // Where a cluster's rank 0 receives its peers' results: with up to this many splits in an
@@ -86,9 +91,9 @@ struct Kind {
 // queued q rows), and give columns that nothing reads.
 // P tiles are stored by token (MN-major: 16 bytes of a token's columns, 8 tokens to a 128-byte
 // block), so that a softmax thread writes its heads' codes as one word, not byte by byte into the
-// rows of a K-major tile: with eight heads 12 byte stores and their shifts fewer per thread, 33 x
-// 4999 with 16 / 2 heads 20.5 -> 17.5 us, 8 x 1024 7.7 -> 7.3 us. Columns past 3 GH of a half hold
-// anything; nothing reads theirs of O.
+// rows of a K-major tile: with eight heads 16 byte stores and their shifts fewer per thread, 33 x
+// 4999 with 16 / 2 heads 20.5 -> 17.5 us, 8 x 1024 7.7 -> 7.3 us. With two heads a unit a half's
+// columns from the fifth on hold anything; nothing reads theirs of O.
 // A unit as the loader hands it out: everything about it that the others need.
 struct Unit8 {
   int32_t b, s, xg, ntiles;  // ntiles < 0: no more work
@@ -158,16 +163,20 @@ __device__ __forceinline__ float redux_max(float x) {
   return r;
 }
 
-// Three e4m3 parts of a pair of weights (0 <= w <= 256), each pair's codes in 16 bits; every
+constexpr int kParts = 4;  // e4m3 numbers to a softmax weight
+
+// The e4m3 parts of a pair of weights (0 <= w <= 256), each pair's codes in 16 bits; every
 // difference is exact.
-__device__ __forceinline__ void split3(float a, float b, uint32_t (&t)[3]) {
+__device__ __forceinline__ void split_weights(float a, float b, uint32_t (&t)[kParts]) {
   const float2 up = make_float2(32.f, 32.f), down = make_float2(-32.f, -32.f);
   const float2 zero = make_float2(0.f, 0.f);
+  float2 r = make_float2(a, b);
   t[0] = cvt_e4m3x2(a, b);
-  float2 r = ffma2(f16x2_to_f32(cvt_f16x2_e4m3x2(t[0])), down, ffma2(make_float2(a, b), up, zero));
-  t[1] = cvt_e4m3x2(r.x, r.y);
-  r = ffma2(f16x2_to_f32(cvt_f16x2_e4m3x2(t[1])), down, ffma2(r, up, zero));
-  t[2] = cvt_e4m3x2(r.x, r.y);
+#pragma unroll
+  for (int i = 1; i < kParts; ++i) {
+    r = ffma2(f16x2_to_f32(cvt_f16x2_e4m3x2(t[i - 1])), down, ffma2(r, up, zero));
+    t[i] = cvt_e4m3x2(r.x, r.y);
+  }
 }
 
 template <int GC, bool W>
@@ -733,25 +742,26 @@ __global__ void __launch_bounds__(kThreads, 2)
             nref[g] = m;
             l[g] *= alpha[g];
           }
-          if (it > 0) {  // O's columns t1, t2, t3 of head g: wait for the PVs so far, scale
+          if (it > 0) {  // O's columns t1 .. t4 of head g: wait for the PVs so far, scale
             ok = __all_sync(kFull, ok && wait_parity(&sm.pv_done[buf ^ 1], ((t - 1) >> 1) & 1, p.err));
             if (ok) {
               tc_fence_after_sync();
-              uint32_t o[3 * GH];
-              tmem_ld_3(o_addr, o);
 #pragma unroll
-              for (int part = 0; part < 3; ++part)
+              for (int pair = 0; pair < kParts; pair += 2) {
+                uint32_t o[2 * GH];
+                tmem_ld_cols(o_addr + pair * GH, o);
 #pragma unroll
-                for (int g = 0; g < GH; ++g)
-                  o[part * GH + g] = __float_as_uint(__uint_as_float(o[part * GH + g]) * alpha[g]);
-              tmem_st_3(o_addr, o);
+                for (int c = 0; c < 2 * GH; ++c)
+                  o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha[c % GH]);
+                tmem_st_cols(o_addr + pair * GH, o);
+              }
               tmem_st_wait();
             }
           }
         }
         if (ok) {
           float w[GH + 1];
-          uint32_t code[3];
+          uint32_t code[kParts];
 #pragma unroll
           for (int g = 0; g < GH; ++g) {
             if constexpr (GH == 1) {
@@ -769,22 +779,23 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
 #pragma unroll
           for (int g = 0; g < GH; g += 2) {
-            uint32_t part[3];
-            split3(w[g], w[g + 1 < GH ? g + 1 : g], part);
+            uint32_t part[kParts];
+            split_weights(w[g], w[g + 1 < GH ? g + 1 : g], part);
 #pragma unroll
-            for (int j = 0; j < 3; ++j)
+            for (int j = 0; j < kParts; ++j)
               code[j] = g == 0 ? part[j] : __byte_perm(code[j], part[j], 0x5410);
           }
           // the token's row of P: 16 bytes of each group of 16 columns
           if constexpr (GH == 4)
             *reinterpret_cast<uint4 *>(sm.p[buf] + half * (16 * kTile) + i * 16) =
-                make_uint4(code[0], code[1], code[2], 0u);
+                make_uint4(code[0], code[1], code[2], code[3]);
           else if constexpr (GH == 2)
             *reinterpret_cast<uint2 *>(sm.p[buf] + i * 16 + half * 8) =
-                make_uint2(__byte_perm(code[0], code[1], 0x5410), code[2]);
+                make_uint2(__byte_perm(code[0], code[1], 0x5410), __byte_perm(code[2], code[3], 0x5410));
           else
             *reinterpret_cast<uint32_t *>(sm.p[buf] + i * 16 + half * 8) =
-                (code[0] & 255u) | ((code[1] & 255u) << 8) | ((code[2] & 255u) << 16);
+                __byte_perm(__byte_perm(code[0], code[1], 0x0040),
+                            __byte_perm(code[2], code[3], 0x0040), 0x5410);
           if (!valid) {  // this token's V row is whatever the slot held: zero it (0 x NaN)
             uint4 *v = reinterpret_cast<uint4 *>(sm.v[vs] + i * 128 + half * 64);
 #pragma unroll
@@ -809,10 +820,19 @@ __global__ void __launch_bounds__(kThreads, 2)
         ++units;
       }
       if (barrier_or(1, kSoftmaxThreads, !ok)) break;  // a wait gave up: stop together
-      uint32_t o[3 * GH];
+      float acc[GH];  // t1 + (t2 + (t3 + t4 / 32) / 32) / 32
       if (un.ntiles > 0) {
         tc_fence_after_sync();
-        tmem_ld_3(o_addr, o);
+        uint32_t o[2 * GH];
+        tmem_ld_cols(o_addr + 2 * GH, o);
+#pragma unroll
+        for (int g = 0; g < GH; ++g)
+          acc[g] = fmaf(__uint_as_float(o[GH + g]), 1.f / 32.f, __uint_as_float(o[g]));
+        tmem_ld_cols(o_addr, o);
+#pragma unroll
+        for (int g = 0; g < GH; ++g)
+          acc[g] = fmaf(fmaf(acc[g], 1.f / 32.f, __uint_as_float(o[GH + g])), 1.f / 32.f,
+                        __uint_as_float(o[g]));
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.o_free[ub]);
@@ -824,12 +844,9 @@ __global__ void __launch_bounds__(kThreads, 2)
           float sum = 0.f;
 #pragma unroll
           for (int w = 0; w < 4; ++w) sum += sm.warp_l[ub][4 * half + w][g];
-          const float acc = fmaf(__uint_as_float(o[2 * GH + g]), 1.f / 1024.f,
-                                 fmaf(__uint_as_float(o[GH + g]), 1.f / 32.f,
-                                      __uint_as_float(o[g])));
           // sum lies far inside the normal range (2^5 over a scale in [2^-100, 2^120], times the
           // tokens); the approximate division and log2 err far below one bf16 rounding
-          out = __fdividef(acc, sum);
+          out = __fdividef(acc[g], sum);
           lse = __log2f(sum) - nref[g];
         }
         if (W && i == 0 && !p.cluster) sm.lse[g0 + g] = lse;

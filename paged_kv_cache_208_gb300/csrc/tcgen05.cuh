@@ -272,58 +272,22 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[N]) {
         : "memory");
 }
 
-// Three times 1, 2 or 4 columns: exactly 3, 6 or 12 of them, loaded (and waited for) or stored, so
-// that the columns next to them may be another warp's.
+// The same columns stored (tmem_st_wait waits for the stores).
 template <int N>
-__device__ __forceinline__ void tmem_ld_3(uint32_t taddr, uint32_t (&r)[N]) {
-  static_assert(N == 3 || N == 6 || N == 12, "");
-  if constexpr (N == 3)
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%3];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%2}, [%4];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=&r"(r[0]), "=&r"(r[1]), "=r"(r[2])
-        : "r"(taddr), "r"(taddr + 2)
-        : "memory");
-  else if constexpr (N == 6)
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%6];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x2.b32 {%4, %5}, [%7];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=r"(r[4]), "=r"(r[5])
-        : "r"(taddr), "r"(taddr + 4)
-        : "memory");
+__device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t (&r)[N]) {
+  static_assert(N == 2 || N == 4 || N == 8, "");
+  if constexpr (N == 2)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%2], {%0, %1};" ::"r"(r[0]), "r"(r[1]),
+                 "r"(taddr)
+                 : "memory");
+  else if constexpr (N == 4)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%4], {%0, %1, %2, %3};" ::"r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(taddr)
+                 : "memory");
   else
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%12];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%8, %9, %10, %11}, [%13];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]),
-          "=&r"(r[6]), "=&r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11])
-        : "r"(taddr), "r"(taddr + 8)
-        : "memory");
-}
-template <int N>
-__device__ __forceinline__ void tmem_st_3(uint32_t taddr, const uint32_t (&r)[N]) {
-  static_assert(N == 3 || N == 6 || N == 12, "");
-  if constexpr (N == 3)
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x2.b32 [%3], {%0, %1};\n\t"
-        "tcgen05.st.sync.aligned.32x32b.x1.b32 [%4], {%2};" ::"r"(r[0]),
-        "r"(r[1]), "r"(r[2]), "r"(taddr), "r"(taddr + 2)
-        : "memory");
-  else if constexpr (N == 6)
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x4.b32 [%6], {%0, %1, %2, %3};\n\t"
-        "tcgen05.st.sync.aligned.32x32b.x2.b32 [%7], {%4, %5};" ::"r"(r[0]),
-        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(taddr), "r"(taddr + 4)
-        : "memory");
-  else
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%12], {%0, %1, %2, %3, %4, %5, %6, %7};\n\t"
-        "tcgen05.st.sync.aligned.32x32b.x4.b32 [%13], {%8, %9, %10, %11};" ::"r"(r[0]),
-        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(taddr), "r"(taddr + 8)
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
         : "memory");
 }
 
