@@ -589,15 +589,18 @@ __global__ void __maxnreg__(96)
       sm.l[warp][gq] = l_run;
     }
     if constexpr (W) {  // the columns of what P's rounding left join their heads'
+      // (an infinite sum of the rounded weights' products is the sum: what the rounding left of an
+      // infinite V's weight, zero or negative, would make it NaN)
+      auto join = [](float sum, float rest) { return isinf(sum) ? sum : sum + rest; };
 #pragma unroll
       for (int m = 0; m < 8; ++m)
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
           if constexpr (GC == 1) {  // columns 0 and 1 of one lane
-            acc[m][e] += acc[m][e + 1];
+            acc[m][e] = join(acc[m][e], acc[m][e + 1]);
           } else {  // column c and c + GC: lanes tq and tq + GC / 2
-            acc[m][e] += __shfl_xor_sync(kFull, acc[m][e], GC / 2);
-            acc[m][e + 1] += __shfl_xor_sync(kFull, acc[m][e + 1], GC / 2);
+            acc[m][e] = join(acc[m][e], __shfl_xor_sync(kFull, acc[m][e], GC / 2));
+            acc[m][e + 1] = join(acc[m][e + 1], __shfl_xor_sync(kFull, acc[m][e + 1], GC / 2));
           }
         }
     }
