@@ -455,9 +455,17 @@ __global__ void __launch_bounds__(kThreads, 2)
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(vbar, bytes + kScaleBytes);
-          // (the zero rows of a bad block id take block 0's scales)
-          load_scales(vr.slot, blk_ok ? blk : 0, blk_ok ? in_block : 0, h);
+          if (blk_ok) {
+            mbar_arrive_expect_tx(vbar, bytes + kScaleBytes);
+            load_scales(vr.slot, blk, in_block, h);
+          } else {
+            // the zero rows of a bad block id: a scale of 1 (no block's scales are theirs, and
+            // any block's may be unwritten)
+            float4 *const scales = reinterpret_cast<float4 *>(sm.tile_scale[vr.slot]);
+            scales[0] = scales[1] = make_float4(1.f, 1.f, 1.f, 1.f);
+            fence_async_shared();  // (the slot's next scales come by a bulk copy)
+            mbar_arrive_expect_tx(vbar, bytes);
+          }
           load(vd, &vmap, &vmap32, &vmap16, vbar);
           vr.next();
           v_issued = min(v_issued + 1, kSlots);

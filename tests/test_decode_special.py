@@ -1,11 +1,12 @@
-"""Decode attention where a cache holds values that are not finite."""
+"""Decode attention where a cache holds values that are not finite, or a table names blocks that do
+not exist."""
 import numpy as np
 import pytest
 import torch
 
 import workloads as w
 from libbuild import build_and_import
-from test_decode_fp8 import Case
+from test_decode_fp8 import Case, check_out, check_weights
 
 pkv = build_and_import()
 D = 128
@@ -62,3 +63,48 @@ def test_infinite_values_on_the_bf16_cache_with_weights(hq, hkv, many):
         plain = pkv.paged_decode_attn(*args, num_splits=splits)
         assert torch.equal(plain.isinf(), out.isinf()) and torch.equal(plain.isnan(), out.isnan())
     assert pkv.get_device_errors() == 0
+
+
+def _bad_blocks(c, k_scale, v_scale):
+    """Block ids outside the pool in c's tables, whose rows count as zeros, and a block 0 that no
+    table names, with NaN codes and these scales."""
+    g = w.rng(21)
+    nb = c.tables.max() + 4
+    c.tables = np.where(c.tables >= 0, c.tables + 1, -1).astype(np.int32)
+    for i, pool in enumerate(c.pools):
+        if c.fp8:
+            codes, scale = pool
+            nan, one = np.full_like(codes[:1], 0x7F), np.full_like(scale[:1], [k_scale, v_scale][i])
+            c.pools[i] = np.concatenate([nan, codes]), np.concatenate([one, scale])
+        else:
+            c.pools[i] = np.concatenate([np.full_like(pool[:1], w.BF16_NAN_CANARY), pool])
+    for b, n in enumerate(c.ctx):
+        blocks = -(-int(n) // c.bs)
+        for j in range(blocks):
+            if b % 7 == 2 or g.random() < 0.4:       # (some sequences have no good block)
+                c.tables[b, j] = [-1, 1 << 20, -(1 << 31), nb + 900][g.integers(4)]
+                at = slice(j * c.bs, (j + 1) * c.bs)
+                for i in range(2):
+                    c.values[i][b][at] = 0.0
+                if c.v_scale:
+                    c.v_scale[b][at] = 1.0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv,fp8", [(16, 8, True), (8, 2, True), (16, 2, True), (8, 2, False)])
+@pytest.mark.parametrize("k_scale,v_scale,many", [
+    (np.nan, np.inf, False), (1.0, 2.0 ** 60, False), (np.inf, np.nan, False),
+    (np.nan, np.inf, True)])
+def test_bad_block_ids_are_zero_rows(hq, hkv, fp8, k_scale, v_scale, many):
+    """Whatever block 0 holds: the rows of a bad id are zeros, with a score of zero and no value."""
+    ctx = [700, 300, 300, 1, 257, 0, 513, 900, 65, 513]
+    c = Case(ctx * (30 if many else 1), hq, hkv, 256, 700 + hq, fp8=fp8)
+    _bad_blocks(c, k_scale, v_scale)
+    ref, tol, ws, wtol = c.reference()
+    for splits in (0, 1) if many else (0, 1, 3, 9):
+        weights = torch.zeros((len(c.ctx), hkv, 900), device="cuda")
+        check_out(c.run(num_splits=splits, weights=weights), ref, tol, f"splits {splits}")
+        check_weights(weights, torch.zeros_like(weights), ws, wtol, c.ctx)
+        if fp8:
+            check_out(c.run(num_splits=splits), ref, tol, f"splits {splits}, no weights")
+        assert pkv.get_device_errors() == pkv.DEVERR_BLOCK_RANGE
