@@ -413,6 +413,8 @@ pkv_status pkv_kv_gather_fp8(const void *k_cache, const void *v_cache, const flo
  *                scale, and below 2^-126 of the largest such product it drops out of the sums.
  * weights_out:   NULL (then weights_in too), or the attention weights as well: see
  *                pkv_paged_decode_attn_weights.
+ * context_lens:  a context longer than max_context_len sets PKV_DEVERR_CONTEXT_RANGE and counts as
+ *                max_context_len tokens (so too in pkv_paged_decode_attn_weights).
  * workspace:     pkv_decode_fp8_workspace_bytes(..., weights = weights_out != NULL) bytes, with
  *                the contract of pkv_paged_decode_attn's (its first word zeroed once).
  * Everything else as for pkv_paged_decode_attn.

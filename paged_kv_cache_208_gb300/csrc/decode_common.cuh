@@ -70,12 +70,11 @@ struct DecodeParams {
   float *scores;
   int64_t score_stride;
   float *lse;
-  // where the decode kernel forms the weights itself (w_out != nullptr): positions below w_cap
+  // where the decode kernel forms the weights itself (w_out != nullptr)
   const float *w_in;
   int64_t w_in_stride;
   float *w_out;
   int64_t w_out_stride;
-  int32_t w_cap;
 };
 
 // The attention weights of positions [begin, end) of sequence b and KV head h, from the scores that
@@ -102,7 +101,7 @@ struct WeightsPass {
     in = p.w_in ? p.w_in + bh * p.w_in_stride : nullptr;
     out = p.w_out + bh * p.w_out_stride;
     i0 = begin + tid;
-    end = min(last, p.w_cap);
+    end = last;
     step = threads;
     err = (uint32_t)ld_global_s32(reinterpret_cast<const int32_t *>(p.err));
     load();
@@ -222,7 +221,8 @@ inline DecodeParams decode_params(const DecodeArgs &a, const DecodePlan &p) {
   prm.queue = reinterpret_cast<int32_t *>(ws);
   prm.err = a.err;
   prm.num_blocks = a.num_blocks;
-  prm.cap = std::min((int64_t)a.table_width * a.block_size, (int64_t)p.splits * p.chunk);
+  prm.cap = std::min({(int64_t)a.table_width * a.block_size, (int64_t)p.splits * p.chunk,
+                      (int64_t)a.max_context_len});
   prm.table_width = a.table_width;
   prm.batch = a.batch;
   prm.num_q_heads = a.num_q_heads;
@@ -245,7 +245,6 @@ inline DecodeParams decode_params(const DecodeArgs &a, const DecodePlan &p) {
       prm.w_in_stride = a.weights_in_stride;
       prm.w_out = a.weights_out;
       prm.w_out_stride = a.weights_out_stride;
-      prm.w_cap = a.weights_cap;
     }
   }
   return prm;

@@ -145,8 +145,8 @@ pkv_status decode_with_weights(Call c, cudaStream_t stream) {
     a.weights_in_stride = c.weights_in_stride;
     a.weights_out = c.weights_out;
     a.weights_out_stride = c.weights_out_stride;
-    a.weights_cap = c.max_context_len;
   }
+  a.max_context_len = c.max_context_len;
   const DecodePlan plan = plan_decode(a.batch, a.num_q_heads, a.num_kv_heads, c.max_context_len,
                                       c.num_splits, a.num_sms, c.fp8, c.weights);
   if (!a.workspace || c.workspace_bytes < plan.workspace_bytes || !aligned16(a.workspace))

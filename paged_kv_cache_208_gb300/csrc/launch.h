@@ -70,7 +70,8 @@ struct DecodeArgs {
   int64_t weights_in_stride = 0;
   float *weights_out = nullptr;
   int64_t weights_out_stride = 0;
-  int32_t weights_cap = 0;  // max_context_len
+  // a longer context is an error and counts as this long (without it: what the splits hold)
+  int32_t max_context_len = INT32_MAX;
 };
 constexpr size_t kDecodeQueueBytes = 16;  // the workspace's header: the work counters
 cudaError_t launch_paged_decode(const DecodeArgs &a, const DecodePlan &plan,

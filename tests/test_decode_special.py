@@ -1,5 +1,5 @@
-"""Decode attention where a cache holds values that are not finite, or a table names blocks that do
-not exist."""
+"""Decode attention where a cache holds values that are not finite, a table names blocks that do not
+exist, or contexts are longer than the call says."""
 import numpy as np
 import pytest
 import torch
@@ -98,7 +98,8 @@ def _bad_blocks(c, k_scale, v_scale):
 def test_bad_block_ids_are_zero_rows(hq, hkv, fp8, k_scale, v_scale, many):
     """Whatever block 0 holds: the rows of a bad id are zeros, with a score of zero and no value."""
     ctx = [700, 300, 300, 1, 257, 0, 513, 900, 65, 513]
-    c = Case(ctx * (30 if many else 1), hq, hkv, 256, 700 + hq, fp8=fp8)
+    times = 1 + 320 // (10 * hkv) if many else 1    # (many: more units than CTAs)
+    c = Case(ctx * times, hq, hkv, 256, 700 + hq, fp8=fp8)
     _bad_blocks(c, k_scale, v_scale)
     ref, tol, ws, wtol = c.reference()
     for splits in (0, 1) if many else (0, 1, 3, 9):
@@ -108,3 +109,32 @@ def test_bad_block_ids_are_zero_rows(hq, hkv, fp8, k_scale, v_scale, many):
         if fp8:
             check_out(c.run(num_splits=splits), ref, tol, f"splits {splits}, no weights")
         assert pkv.get_device_errors() == pkv.DEVERR_BLOCK_RANGE
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv,fp8", [(16, 8, True), (16, 2, True), (4, 4, False), (8, 2, False)])
+@pytest.mark.parametrize("longest,many", [(0, False), (1, False), (130, False), (500, False),
+                                          (130, True)])
+def test_contexts_above_the_longest(hq, hkv, fp8, longest, many):
+    """A context above max_context_len is reported and counts as that many tokens, whatever its split
+    would hold; weights past them are left alone."""
+    times = 1 + 320 // (6 * hkv) if many else 1     # (many: more units than CTAs)
+    c = Case([150, 3, 700, 130, 1, 0] * times, hq, hkv, 256, 800 + hq, fp8=fp8)
+    args = c.device()
+    at, cut = (6, 7) if fp8 else (4, 5)
+    assert torch.equal(args[at].cpu(), torch.from_numpy(c.ctx).int())
+    args[cut] = longest
+    short = list(args)
+    short[at] = args[at].clamp(max=longest)
+    for splits in (0, 1) if many else (0, 1, 2, 9):
+        w0, w1 = (torch.full((len(c.ctx), hkv, 800), 7.0, device="cuda") for _ in range(2))
+        out = c.run(args, num_splits=splits, weights_out=w0)
+        assert pkv.get_device_errors() == pkv.DEVERR_CONTEXT_RANGE
+        ref = c.run(short, num_splits=splits, weights_out=w1)
+        assert torch.equal(out, ref) and torch.equal(w0, w1)
+        assert (w0[:, :, longest:] == 7).all()
+        if fp8:
+            out = c.run(args, num_splits=splits)
+            assert pkv.get_device_errors() == pkv.DEVERR_CONTEXT_RANGE
+            assert torch.equal(out, c.run(short, num_splits=splits))
+        assert pkv.get_device_errors() == 0
