@@ -475,8 +475,9 @@ pkv_status pkv_paged_decode_attn_weights(
  *   row j of the sequence in the blocks of dst_block_tables (position j, head h, K and V) becomes
  *   row i_j; kept[b, h, j] = i_j; weights_out[b, h, j] = weights[b, h, i_j]; and
  *   new_context_lens[b] = n.
- * Entries j in [n, budget) of kept become -1 and of weights_out 0; pool rows past n are left as
- * they are. Each head keeps tokens of its own, so afterwards position j of two heads may be
+ * Entries j in [n, budget) of kept become -1 and of weights_out 0; pool rows past n and weights_out
+ * past budget are left as they are (zero the latter where the next tokens' weights will add up:
+ * the sequence's decode calls need rows of its next max_context_len). Each head keeps tokens of its own, so afterwards position j of two heads may be
  * different tokens: the cached keys carry their rotary positions with them, and new tokens go on
  * counting positions from the original length, while context lengths, slots and block tables
  * go by the new one. Attention over the compacted rows is attention over the kept tokens.

@@ -477,7 +477,11 @@ def kv_evict(weights: torch.Tensor, context_lens: torch.Tensor, max_context_len:
 
     caches: bf16 [NB, bs, Hkv, D], or float8_e4m3fn with k_scale and v_scale. Returns (kept
     positions [B, Hkv, budget] int32 (-1 past a sequence's length), their weights
-    [B, Hkv, budget], the new context lengths [B] int32)."""
+    [B, Hkv, budget], the new context lengths [B] int32).
+
+    To go on accumulating, give weights_out [B, Hkv, >= the next max_context_len], zeroed: its
+    columns past budget, where the next tokens' weights will add up, are left as they are. The
+    sequence goes on with dst_block_tables and the new lengths."""
     return _result("pkv_kv_evict", _torch.kv_evict(
         weights, context_lens, max_context_len, block_tables, dst_block_tables, budget, recent,
         k_cache, v_cache, k_scale, v_scale, kept, weights_out, new_context_lens, stream))
