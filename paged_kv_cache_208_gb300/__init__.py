@@ -6,8 +6,9 @@ declared in ``include/pkv.h``, and raise ``PkvError`` on a non-zero status. Most
 through ctypes; those of the 8-bit cache, the attention weights and eviction through a small
 extension module (``binding/pkv_torch.cpp``) that does the same checks in less time. Every step
 of the computation runs in the CUDA library; there is no other implementation to fall back
-to. Importing this package fails if ``libpkv.so`` and that module have not been built
-(``python paged_kv_cache_208_gb300/build.py`` or ``__graft_entry__.build()``).
+to. Importing this package fails if ``libpkv.so`` has not been built
+(``python paged_kv_cache_208_gb300/build.py`` or ``__graft_entry__.build()``), and the calls that go
+through that module fail where it is missing.
 
 PyTorch is used for device memory and streams only.
 """
@@ -98,11 +99,24 @@ def _load() -> ctypes.CDLL:
 
 
 _LIB = _load()
+
+
+class _NoBinding:
+    """In place of the extension module where it does not load: its calls raise."""
+
+    def __init__(self, why: ImportError):
+        self._why = why
+
+    def __getattr__(self, name: str):
+        raise ImportError(
+            f"{os.path.join(_HERE, '_pkv_torch.so')} is missing or does not load ({self._why}): "
+            f"build it with `python {os.path.join(_HERE, 'build.py')}`") from self._why
+
+
 try:
     from . import _pkv_torch as _torch  # the per-step calls on tensors (binding/pkv_torch.cpp)
 except ImportError as e:
-    raise ImportError(f"{os.path.join(_HERE, '_pkv_torch.so')} is missing or does not load ({e}): "
-                      f"build it with `python {os.path.join(_HERE, 'build.py')}`") from e
+    _torch = _NoBinding(e)
 
 
 def lib() -> ctypes.CDLL:

@@ -3,12 +3,16 @@ part of the Python binding that works on torch tensors) with the host compiler.
 
 Each .cu file (and each host-only .cpp file) is compiled in parallel to an object file, then linked into a shared library
 next to this file. cudart is linked statically; the driver API is reached at run time
-through cudaGetDriverEntryPointByVersion, so no libcuda is needed at link time.
+through cudaGetDriverEntryPointByVersion, so no libcuda is needed at link time. The library needs
+nvcc alone and is there also where the binding does not compile (an error all the same); without
+torch there is no binding to build.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -74,31 +78,71 @@ def _link_binding(obj: str) -> None:
     os.replace(tmp, BINDING)
 
 
-def _stale() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(BINDING)):
+def _have_torch() -> bool:
+    try:
+        return importlib.util.find_spec("torch") is not None
+    except ValueError:  # (sys.modules["torch"] is None)
+        return False
+
+
+def _torch_version() -> str:
+    """What a binding is built for: another torch or Python needs another one."""
+    return (f"torch {importlib.metadata.version('torch')} at "
+            f"{importlib.util.find_spec('torch').origin}, python {sys.version}")
+
+
+def _noted() -> str:
+    return os.path.join(OBJ_DIR, os.path.basename(BINDING) + ".for")
+
+
+def _note_binding() -> None:
+    with open(_noted(), "w") as f:
+        f.write(_torch_version())
+
+
+def _older(path: str, deps: list[str]) -> bool:
+    return not os.path.exists(path) or any(os.path.getmtime(d) > os.path.getmtime(path)
+                                           for d in deps)
+
+
+def _stale_lib() -> bool:
+    return _older(LIB, glob.glob(os.path.join(CSRC, "*")) + glob.glob(os.path.join(INCLUDE, "*.h")))
+
+
+def _stale_binding() -> bool:
+    if not _have_torch():
+        return False
+    if _older(BINDING, glob.glob(os.path.join(INCLUDE, "*.h")) + [BINDING_SRC]):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    deps = (glob.glob(os.path.join(CSRC, "*")) + glob.glob(os.path.join(INCLUDE, "*.h"))
-            + [BINDING_SRC])
-    return any(os.path.getmtime(d) > t for d in deps)
+    if not os.path.exists(_noted()):
+        return True
+    with open(_noted()) as f:
+        return f.read() != _torch_version()
+
+
+def _stale() -> bool:
+    return _stale_lib() or _stale_binding()
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not _stale():
+    lib, binding = force or _stale_lib(), _have_torch() and (force or _stale_binding())
+    if not lib and not binding:
         return LIB
     os.makedirs(OBJ_DIR, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cpp")))
     with cf.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
-        binding = ex.submit(_compile_binding)
-        objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
-        binding = binding.result()
-    tmp = LIB + f".tmp{os.getpid()}"
-    r = subprocess.run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs], capture_output=True,
-                       text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    _link_binding(binding)
+        obj = ex.submit(_compile_binding) if binding else None
+        objs = list(ex.map(lambda s: _compile(s, verbose), srcs)) if lib else []
+    if lib:
+        tmp = LIB + f".tmp{os.getpid()}"
+        r = subprocess.run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs], capture_output=True,
+                           text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, LIB)
+    if obj:
+        _link_binding(obj.result())
+        _note_binding()
     return LIB
 
 
