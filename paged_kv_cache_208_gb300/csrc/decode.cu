@@ -5,8 +5,8 @@
 // through the sequence's block table. GQA: query head hq reads KV head hq / G.
 //
 // Work unit: sequence b, KV head h, up to two of the G query heads of h (so each K/V byte is
-// read once for both heads of a Qwen3 group), and one split: the logical tokens
-// [s * chunk, min((s + 1) * chunk, ctx_b)). chunk is a multiple of the 64-token tile and the
+// read once for both heads of a Qwen3 group) or, with weights, up to four, and one split: the
+// logical tokens [s * chunk, min((s + 1) * chunk, ctx_b)). chunk is a multiple of the 64-token tile and the
 // block size a multiple of 256, so a tile never straddles a block.
 //
 // Persistent kernel: two CTAs per SM take units from a global queue (an atomic counter at the
@@ -51,6 +51,14 @@ constexpr int kRing = 4;
 constexpr int kThreads = (kConsumerWarps + 1) * 32;
 constexpr int kTileBytes = kTile * kD * 2;  // one head's K (or V) for 64 tokens: 16 KiB
 constexpr int kPlaneBytes = kTileBytes / 2;  // one 64-dim half of it (a plane of 64 rows)
+constexpr int kChunkRows = 8;   // a context's last tile is loaded in 8-row chunks
+constexpr int kChunkBytes = kChunkRows * 128;
+
+struct Unit {
+  int32_t b, s, xg, ntiles;  // ntiles < 0: no more work
+  int32_t store;             // store the sequence's new token (its last position) first
+  int32_t skip;              // 1: the ring's next tile is a discarded speculative load
+};
 
 // The warps merge a unit's heads in shared memory a pair at a time (two CTAs have to fit on an SM).
 template <int GC>
@@ -866,9 +874,10 @@ DecodePlan plan_decode(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
     // within one CTA per SM for clusters of more than 4 (larger clusters do not all fit at
     // once when SMs hold two CTAs). An 8-bit unit costs less and pays as long as the clusters all
     // run at once, with two CTAs per SM: pairs do up to 304 CTAs, larger clusters leave places in
-    // the GPCs empty, differently from device to device (38 x 1633 with 16 / 2 heads: 13.0 us with 3
+    // the GPCs empty. The limits are measured at 152 SMs (38 x 1633 with 16 / 2 heads: 13.0 us with 3
     // splits, 18.8 with 4, 304 CTAs, the last of which start when the first have ended; 12 x 2048:
-    // 11.8 with 2, 15.7 with 3, 288; 4 x 4096: 9.3 with 7, 10.7 with 8, 256).
+    // 11.8 with 2, 15.7 with 3, 288; 4 x 4096: 9.3 with 7, 10.7 with 8, 256); another device's
+    // clusters may need others, which costs time there, nothing else.
     const int64_t units = (int64_t)batch * num_kv_heads * p.head_groups;
     const int64_t max_unit_tiles = units >= 8LL * num_sms ? 32 : 16;
     int64_t S = (max_tiles + max_unit_tiles - 1) / max_unit_tiles;
@@ -882,7 +891,9 @@ DecodePlan plan_decode(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
     // Few units of long contexts over the 8-bit cache: a CTA's loads run at a tile per 0.65 us, so
     // six tiles to a CTA and the merge kernel beat a cluster (1 x 17188 with 2 / 1 heads 16.2 -> 13
     // us, 8 x 16384 with 8 / 1 17.5 -> 15.7 us; 1 x 8192 with 32 / 8 takes 10.4 us with a cluster of
-    // 8, 12.0 with 16 splits).
+    // 8, 12.0 with 16 splits). Rounded down to a multiple of four, which leaves some SMs without a
+    // CTA: 2 x 32768 with 16 / 2 takes 17.0 us with 36 asked for (eight tiles to a CTA), 18.4 with 38
+    // (seven), 8 x 16384 with 8 / 1 15.1 with 16, 16.3 with 19.
     const int64_t wide = fp8 && !weights ? std::min(max_tiles / 6, num_sms / units) & ~3LL : 0;
     if (wide >= 16) S = wide;
     const int64_t per = (max_ctx + S - 1) / S;

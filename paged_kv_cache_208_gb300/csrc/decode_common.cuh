@@ -15,17 +15,9 @@ namespace {
 
 constexpr int kD = 128;
 constexpr int kMaxCluster = 8;  // largest portable thread-block cluster
-constexpr int kChunkRows = 8;   // a context's last tile is loaded in 8-row chunks
-constexpr int kChunkBytes = kChunkRows * 128;
 constexpr unsigned int kErrWorkspace = 64u;  // PKV_DEVERR_WORKSPACE
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr unsigned kFull = 0xffffffffu;
-
-struct Unit {
-  int32_t b, s, xg, ntiles;  // ntiles < 0: no more work
-  int32_t store;             // store the sequence's new token (its last position) first
-  int32_t skip;              // 1: the ring's next tile is a discarded speculative load
-};
 
 struct DecodeParams {
   const uint16_t *q;

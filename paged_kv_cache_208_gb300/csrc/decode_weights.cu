@@ -1,6 +1,7 @@
 // decode_weights.cu -- the attention weights of a decode step whose split kernel does not form them
-// itself (decode_forms_weights: several units share a KV head, or the splits meet in the merge
-// kernel), and the entry points of decode attention over the 8-bit cache and of decode attention
+// itself (decode_forms_weights: several units share a KV head, the splits meet in the merge kernel,
+// or eight heads a unit come with the work queue or splits of more than 1280 tokens), and the entry
+// points of decode attention over the 8-bit cache and of decode attention
 // with weights.
 //
 // The split kernel has left every key's scaled score s (log2 domain) and every query head's

@@ -19,12 +19,12 @@ cudaError_t launch_kv_store(const void *k, int64_t k_tok_stride, const void *v,
                             void *k_cache, void *v_cache, int64_t num_slots, int64_t row_elems,
                             unsigned int *err, int num_sms, cudaStream_t stream);
 
-// decode.cu (the kernel template: decode_kernel.cuh)
+// decode.cu
 struct DecodePlan {
-  int32_t chunk;       // logical tokens per split (multiple of 64)
+  int32_t chunk;       // logical tokens per split (a multiple of the tile: 64, of an 8-bit cache 128)
   int32_t splits;      // splits of the longest context
-  int32_t head_groups; // CTAs per KV head (query heads handled two at a time)
-  int32_t heads_per_cta;
+  int32_t head_groups; // units per KV head and split
+  int32_t heads_per_cta;  // query heads of a unit: at most 2, with weights 4, of an 8-bit cache 8
   int32_t max_cluster; // splits that may meet in a cluster
   size_t workspace_bytes;
   // with weights: where the log2-sum-exps and the scores [batch, num_q_heads, score_stride]
