@@ -857,10 +857,13 @@ DecodePlan plan_decode(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
   p.head_groups = (group + p.heads_per_cta - 1) / p.heads_per_cta;
   const int64_t max_ctx = max_context_len > 0 ? max_context_len : 1;
   const int64_t max_tiles = (max_ctx + kTile - 1) / kTile;
+  // whole tiles, and an int (a bound near INT32_MAX in one split takes two)
+  auto whole_tiles = [&](int64_t tokens) {
+    return (int32_t)std::min((tokens + kTile - 1) / kTile * kTile, (int64_t)(INT32_MAX / kTile * kTile));
+  };
   if (num_splits > 0) {
     const int64_t S = num_splits < max_tiles ? num_splits : max_tiles;
-    const int64_t per = (max_ctx + S - 1) / S;
-    p.chunk = (int32_t)((per + kTile - 1) / kTile * kTile);
+    p.chunk = whole_tiles((max_ctx + S - 1) / S);
   } else {
     // At most 16 tiles per unit (a CTA streams its unit through a 3-tile ring, so long
     // units cap the bandwidth of a skewed batch; the work queue balances short ones), or 32
@@ -896,8 +899,7 @@ DecodePlan plan_decode(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
     // (seven), 8 x 16384 with 8 / 1 15.1 with 16, 16.3 with 19.
     const int64_t wide = fp8 && !weights ? std::min(max_tiles / 6, num_sms / units) & ~3LL : 0;
     if (wide >= 16) S = wide;
-    const int64_t per = (max_ctx + S - 1) / S;
-    p.chunk = (int32_t)((per + kTile - 1) / kTile * kTile);
+    p.chunk = whole_tiles((max_ctx + S - 1) / S);
   }
   p.splits = (int32_t)((max_ctx + p.chunk - 1) / p.chunk);
   const size_t partials =

@@ -138,3 +138,21 @@ def test_contexts_above_the_longest(hq, hkv, fp8, longest, many):
             assert pkv.get_device_errors() == pkv.DEVERR_CONTEXT_RANGE
             assert torch.equal(out, c.run(short, num_splits=splits))
         assert pkv.get_device_errors() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("longest", [2 ** 31 - 1, 2 ** 31 - 128, 2 ** 31 - 129])
+def test_no_bound_on_the_longest_context(fp8, longest):
+    """max_context_len as large as an int: one split of that many tokens is not a multiple of a tile
+    that an int holds."""
+    c = Case([150, 3, 700, 0], 8, 2, 256, 900, fp8=fp8)
+    args = c.device()
+    args[7 if fp8 else 5] = longest
+    out = c.run(args, num_splits=1) if fp8 else pkv.paged_decode_attn(*args, num_splits=1)
+    ref, tol, _, _ = c.reference()
+    # (the bf16 kernel rounds its weights to bf16, as it does their sum)
+    more = 0 if fp8 else np.stack([
+        np.abs(np.repeat(v, 4, axis=1)).max(axis=0, initial=0) for v in c.values[1]]) * 2.0 ** -8
+    check_out(out, ref, tol + more)
+    assert pkv.get_device_errors() == 0
