@@ -558,9 +558,12 @@ class BlockManager:
     def take(self, n: int):
         """n fresh blocks that hold no tokens' prefix: the destination of kv_evict, or a further
         block of a sequence that was evicted from. Release them with deallocate."""
-        blocks = (ctypes.c_int32 * max(1, int(n)))()
-        _check("pkv_bm_take", _LIB.pkv_bm_take(self._h, int(n), blocks))
-        return list(blocks[:int(n)])
+        n = int(n)
+        if n > self.num_blocks:  # (an int32 may not hold it, nor memory an array of it)
+            raise PkvError("pkv_bm_take", ERR_NO_BLOCKS)
+        blocks = (ctypes.c_int32 * max(1, n))()
+        _check("pkv_bm_take", _LIB.pkv_bm_take(self._h, n, blocks))
+        return list(blocks[:max(0, n)])
 
     def deallocate(self, table) -> None:
         t, n = self._ints(table)
