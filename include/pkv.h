@@ -368,9 +368,10 @@ pkv_status pkv_qk_norm_rope_store(const void *qkv, int64_t qkv_tok_stride, int64
  * block_tables:  [num_seqs, block_table_width] int32. A block that the call writes belongs to
  *                one sequence of the call (blocks shared with others, e.g. a cached prefix, hold
  *                earlier positions only).
- * A bad cu_seqlens entry (PKV_DEVERR_SEQLEN_RANGE) or context length
- * (PKV_DEVERR_CONTEXT_RANGE) skips the sequence, a bad block id (PKV_DEVERR_BLOCK_RANGE) the
- * rows that go there.
+ * A bad context length (PKV_DEVERR_CONTEXT_RANGE) skips the sequence, a bad block id
+ * (PKV_DEVERR_BLOCK_RANGE) the rows that go there, a bad cu_seqlens entry
+ * (PKV_DEVERR_SEQLEN_RANGE) its sequence and, where cu_seqlens decreases, maybe rows of others (a
+ * row's sequence is looked up in the sorted list).
  * Implemented: head_dim == 128, block_size a multiple of 256, 16-byte aligned pointers.
  */
 pkv_status pkv_kv_store_fp8(const void *k, int64_t k_tok_stride, const void *v,
@@ -389,7 +390,7 @@ pkv_status pkv_kv_store_fp8(const void *k, int64_t k_tok_stride, const void *v,
  * are exact in bf16 for the scales that pkv_kv_store_fp8 writes. Rows of no sequence are left
  * as they are; rows of a bad block id become zeros (PKV_DEVERR_BLOCK_RANGE).
  * block_table: [num_seqs, block_table_width] int32 (blocks may be shared); cu_seqlens_k:
- * [num_seqs + 1] int32, within [0, total_k].
+ * [num_seqs + 1] int32, non-decreasing, within [0, total_k] (a bad entry as in pkv_kv_store_fp8).
  * Implemented: head_dim == 128, block_size a multiple of 256, 16-byte aligned pointers.
  */
 pkv_status pkv_kv_gather_fp8(const void *k_cache, const void *v_cache, const float *k_scale,
@@ -404,7 +405,9 @@ pkv_status pkv_kv_gather_fp8(const void *k_cache, const void *v_cache, const flo
  * sequence b and head h are code * scale of position i. q and out stay bf16; sums
  * are in fp32; q enters within 2^-22 of its head's largest |q|, a softmax weight the value sum within
  * 2^-19 of itself or, with its V scale, 2^-30 of its split's largest weight with its V scale (at
- * most 2^-13 in all over a split of 131072 tokens).
+ * most 2^-13 in all over a split of 131072 tokens). Weights are powers of two of a score + log2 of
+ * the V scale, in fp32: with V scales beyond 2^-32 or 2^32, as the store gives groups of zeros or of
+ * very large values, they (and weights_out) are off by up to 2^-15 of themselves.
  *
  * k_cache, v_cache: [num_blocks, block_size, num_kv_heads, head_dim] e4m3.
  * k_scale, v_scale: [num_blocks, num_kv_heads, block_size / 64] fp32, positive and finite, at
