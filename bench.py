@@ -47,6 +47,7 @@ FALLBACK_BF16_TFLOPS = 1900.0
 # bench reports that traffic only while the sources still hash the same.
 DECODE_PROFILE = os.path.join(ROOT, "profiles", "decode_split_qwen3_decode_batch.md")
 DECODE_SOURCES = ("paged_kv_cache_208_gb300/csrc/decode.cu",
+                  "paged_kv_cache_208_gb300/csrc/decode_common.cuh",
                   "paged_kv_cache_208_gb300/csrc/device_common.cuh")
 MIN_TIMED_SECONDS = 2.0   # the headline's K-step blocks are repeated until they cover this
 WORKLOAD = ("qwen3-0.6b decode step: 28 layers x (kv_store of 256 new tokens + paged decode "
