@@ -67,6 +67,8 @@ typedef int32_t pkv_status;
                                          held a value that a zeroed counter cannot give: it
                                          was not zero when the call started, and outputs may
                                          be missing. Zero it again (cudaMemsetAsync). */
+#define PKV_DEVERR_NODE_RANGE 128u    /* kv_accept: an accepted node that is not in the tree or not
+                                         after the one before it, or a bad number of them */
 
 /* Human-readable name of a status code. Never NULL; the string is static. */
 const char *pkv_status_string(pkv_status status);
@@ -515,6 +517,132 @@ pkv_status pkv_kv_evict(const float *weights, int64_t weights_stride,
                         int32_t block_size, int64_t num_blocks, int32_t *kept,
                         float *weights_out, int64_t weights_out_stride,
                         int32_t *new_context_lens, void *stream);
+
+/* ------------------------------------------------------------------ speculative decoding
+ *
+ * A step that verifies drafted tokens: each sequence brings n of them, the nodes of a tree, whose
+ * root is the token that was sampled last. Their K/V rows are appended to the cache like any other
+ * new tokens' (node i at position L - n + i of a context of L tokens, whatever its depth; its
+ * rotary position is L - n + depth), all nodes attend at once (pkv_paged_tree_attn), and the
+ * rows of the path that is accepted move up behind the context (pkv_kv_accept). Nodes are
+ * numbered parents first.
+ *
+ * paged_tree_attn -- attention of every sequence's drafted tokens. With n = cu_seqlens_q[b + 1] -
+ * cu_seqlens_q[b] nodes, L = context_lens[b] (the nodes included) and P = L - n, node i of
+ * sequence b sees the positions j < P and P + j for the nodes j < n that its mask names; over
+ * those, for query head hq of KV head h = hq / (num_q_heads / num_kv_heads),
+ *     out[cu_seqlens_q[b] + i, hq, :] = softmax_j(scale * q . k_j) v_j          (bf16, RNE)
+ * A node that sees nothing gets zeros. Scores, softmax and sums are in fp32; a weight enters
+ * the value sum within 2^-16 of itself.
+ *
+ * q:             [total_q, num_q_heads, head_dim] bf16, token stride q_tok_stride elements. Rows
+ *                behind cu_seqlens_q[num_seqs] are not read, and their outputs left as they are.
+ * cu_seqlens_q:  [num_seqs + 1] int32, non-decreasing, within [0, total_q]. max_seqlen_q: upper
+ *                bound of n. A sequence with a bad entry, or longer than that, is left out
+ *                (PKV_DEVERR_SEQLEN_RANGE).
+ * context_lens:  [num_seqs] int32 in [n, max_context_len]. Another length, or one longer than the
+ *                block table's row, gives the sequence's nodes zeros (PKV_DEVERR_CONTEXT_RANGE).
+ * tree_mask:     NULL: a chain, node i sees the nodes 0 .. i. Else [total_q, mask_words] 64-bit
+ *                words: node i sees node 64 w + k where bit k of word w of its row is set. A
+ *                tree's rows name the node itself and its ancestors; other masks are as good.
+ *                Bits at n and above are ignored. 64 * mask_words >= max_seqlen_q.
+ * block_tables:  [num_seqs, block_table_width] int32; blocks may be shared, as a cached prefix is.
+ *                A bad block id (PKV_DEVERR_BLOCK_RANGE) counts as keys and values of zeros.
+ * workspace:     pkv_tree_workspace_bytes(...) bytes, 16-byte aligned, private to this call while
+ *                it runs; its contents need no initialisation.
+ * out:           [total_q, num_q_heads, head_dim] bf16, contiguous.
+ * Implemented: head_dim == 128, block_size a multiple of 256, q_tok_stride a multiple of 8, 16-byte
+ * aligned q, pools, scales and out; any num_q_heads / num_kv_heads.
+ */
+size_t pkv_tree_workspace_bytes(int32_t num_seqs, int32_t max_seqlen_q, int32_t num_q_heads,
+                                int32_t num_kv_heads, int32_t head_dim, int32_t max_context_len);
+pkv_status pkv_paged_tree_attn(const void *q, int64_t q_tok_stride, int64_t total_q,
+                               const void *k_cache, const void *v_cache,
+                               const int32_t *block_tables, int32_t block_table_width,
+                               const int32_t *context_lens, const int32_t *cu_seqlens_q,
+                               int32_t num_seqs, int32_t max_seqlen_q, int32_t max_context_len,
+                               const int64_t *tree_mask, int32_t mask_words, int32_t num_q_heads,
+                               int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                               int64_t num_blocks, float scale, void *workspace,
+                               size_t workspace_bytes, void *out, void *stream);
+
+/*
+ * paged_tree_attn_fp8 -- the same over the 8-bit cache (k_scale, v_scale: its scales, as for
+ * pkv_paged_decode_attn_fp8).
+ */
+pkv_status pkv_paged_tree_attn_fp8(const void *q, int64_t q_tok_stride, int64_t total_q,
+                                   const void *k_cache, const void *v_cache, const float *k_scale,
+                                   const float *v_scale, const int32_t *block_tables,
+                                   int32_t block_table_width, const int32_t *context_lens,
+                                   const int32_t *cu_seqlens_q, int32_t num_seqs,
+                                   int32_t max_seqlen_q, int32_t max_context_len,
+                                   const int64_t *tree_mask, int32_t mask_words,
+                                   int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                   int32_t block_size, int64_t num_blocks, float scale,
+                                   void *workspace, size_t workspace_bytes, void *out,
+                                   void *stream);
+
+/*
+ * kv_accept -- keep the accepted nodes of every sequence's tree: with P = context_lens[b] - n (n
+ * as above) and the accepted nodes a_0 < a_1 < .. < a_(m-1), m = num_accepted[b],
+ *     row P + j becomes row P + a_j  (K and V, every head),     new_context_lens[b] = P + m.
+ * The rows behind that are dead: the next step's tokens overwrite them.
+ *
+ * accepted:      [num_seqs, accepted_width] int32, ascending nodes; num_accepted: [num_seqs] int32
+ *                in [0, min(n, accepted_width)]. Another number counts as 0, and a path ends before
+ *                a node that is not above the one before it or not below n
+ *                (PKV_DEVERR_NODE_RANGE).
+ * cu_seqlens_q:  [num_seqs + 1] int32; only the differences count. A negative one
+ *                (PKV_DEVERR_SEQLEN_RANGE), or a context length that is below n or longer than the
+ *                table (PKV_DEVERR_CONTEXT_RANGE), empties the sequence (new length 0).
+ * block_tables:  the blocks that hold the nodes must belong to one sequence each. A bad block
+ *                id (PKV_DEVERR_BLOCK_RANGE): zero rows where it is read, nothing where written.
+ * k_scale, v_scale: both NULL for bf16 pools; for an 8-bit cache its scales. There a group of 64
+ *                positions that accepted rows lie in takes the largest of its scale s0 and the
+ *                scales of the groups they come from, s; its rows from before the tree become
+ *                e4m3(code * s0 / s), a row of a group with scale s1 e4m3(code * s1 / s).
+ * new_context_lens: [num_seqs] int32, not context_lens (PKV_ERR_INVALID_ARG): the calls of the
+ *                step's other layers read that.
+ * Implemented: head_dim == 128, block_size a multiple of 64 (bf16) or 256 (8-bit), 16-byte aligned
+ * pools.
+ */
+pkv_status pkv_kv_accept(const int32_t *accepted, int32_t accepted_width,
+                         const int32_t *num_accepted, const int32_t *cu_seqlens_q,
+                         const int32_t *context_lens, const int32_t *block_tables,
+                         int32_t block_table_width, int32_t num_seqs, void *k_cache,
+                         void *v_cache, float *k_scale, float *v_scale, int32_t num_kv_heads,
+                         int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                         int32_t *new_context_lens, void *stream);
+
+/*
+ * qk_norm_rope_store_fp8 -- pkv_qk_norm_rope_store for the 8-bit cache: RMSNorm (QK 归一化) and RoPE
+ * of the new tokens' query and key heads, K and V appended as pkv_kv_store_fp8 appends them.
+ *
+ * qkv, positions, cos_sin_cache, eps, q_out as there; cu_seqlens, context_lens, block_tables and
+ * the cache as in pkv_kv_store_fp8. For each query / key head x, in fp32 throughout:
+ *     n = x * rsqrt(mean(x^2) + eps) * w          (without weights: n = x)
+ *     y_i = n_i c_i - n_{i+h} s_i,  y_{i+h} = n_{i+h} c_i + n_i s_i
+ * and y is rounded once: q_out = bf16(y); K's codes are e4m3(y / s) with the group's scale s from the
+ * largest finite |y| of its new rows. (pkv_qk_norm_rope_store rounds n and a key's y to bf16.) V is
+ * appended as it is.
+ *
+ * q_norm_weight, k_norm_weight: [head_dim] bf16, or both NULL for a model without QK norm.
+ * positions:     [num_tokens] int64, the rotary positions (of a drafted token its depth counts,
+ *                not its place in the cache). One outside [0, max_position) skips the token's query
+ *                and key heads (PKV_DEVERR_POSITION_RANGE).
+ * cu_seqlens:    NULL: row b is position context_lens[b] - 1 of sequence b; a context length of 0
+ *                stores nothing, q_out is written all the same. Else tokens of no sequence, and those
+ *                of a sequence with bad lengths, are left out, their q_out as it was.
+ * Implemented: head_dim == 128, block_size a multiple of 256, qkv_tok_stride a multiple of 8, 16-byte
+ * aligned pointers.
+ */
+pkv_status pkv_qk_norm_rope_store_fp8(
+    const void *qkv, int64_t qkv_tok_stride, int64_t num_tokens, const int64_t *positions,
+    const void *q_norm_weight, const void *k_norm_weight, float eps, const float *cos_sin_cache,
+    int64_t max_position, const int32_t *cu_seqlens, const int32_t *context_lens,
+    const int32_t *block_tables, int32_t block_table_width, int32_t num_seqs, void *q_out,
+    void *k_cache, void *v_cache, float *k_scale, float *v_scale, int32_t num_q_heads,
+    int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int64_t num_blocks, void *stream);
 
 /* ------------------------------------------------------------------ block manager (host)
  *

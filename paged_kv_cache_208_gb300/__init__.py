@@ -3,7 +3,7 @@
 The functions here only marshal arguments: they check dtype, device and layout of torch
 tensors, pass raw device pointers and the current CUDA stream to the ``pkv_*`` entry points
 declared in ``include/pkv.h``, and raise ``PkvError`` on a non-zero status. Most calls go
-through ctypes; those of the 8-bit cache, the attention weights and eviction through a small
+through ctypes; those of the 8-bit cache, the attention weights, eviction and drafted tokens through a small
 extension module (``binding/pkv_torch.cpp``) that does the same checks in less time. Every step
 of the computation runs in the CUDA library; there is no other implementation to fall back
 to. Importing this package fails if ``libpkv.so`` has not been built
@@ -25,7 +25,7 @@ LIB_PATH = os.path.join(_HERE, "libpkv.so")
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_NO_BLOCKS = range(6)
 DEVERR_SLOT_RANGE, DEVERR_BLOCK_RANGE, DEVERR_CONTEXT_RANGE = 1, 2, 4
 DEVERR_SEQLEN_RANGE, DEVERR_TIMEOUT, DEVERR_POSITION_RANGE = 8, 16, 32
-DEVERR_WORKSPACE = 64
+DEVERR_WORKSPACE, DEVERR_NODE_RANGE = 64, 128
 
 # symbol -> (restype, argtypes); mirrors include/pkv.h
 _P, _I32, _I64, _F, _SZ = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float,
@@ -64,6 +64,17 @@ SIGNATURES = {
                                              _SZ, _P, _P]),
     "pkv_kv_evict": (_I32, [_P, _I64, _P, _I32, _I32, _I32, _I32, _P, _I32, _P, _I32, _P, _P, _P,
                             _P, _I32, _I32, _I32, _I64, _P, _P, _I64, _P, _P]),
+    "pkv_tree_workspace_bytes": (_SZ, [_I32] * 6),
+    "pkv_paged_tree_attn": (_I32, [_P, _I64, _I64, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _P,
+                                   _I32, _I32, _I32, _I32, _I32, _I64, _F, _P, _SZ, _P, _P]),
+    "pkv_paged_tree_attn_fp8": (_I32, [_P, _I64, _I64, _P, _P, _P, _P, _P, _I32, _P, _P, _I32,
+                                       _I32, _I32, _P, _I32, _I32, _I32, _I32, _I32, _I64, _F, _P,
+                                       _SZ, _P, _P]),
+    "pkv_kv_accept": (_I32, [_P, _I32, _P, _P, _P, _P, _I32, _I32, _P, _P, _P, _P, _I32, _I32,
+                             _I32, _I64, _P, _P]),
+    "pkv_qk_norm_rope_store_fp8": (_I32, [_P, _I64, _I64, _P, _P, _P, _F, _P, _I64, _P, _P, _P,
+                                          _I32, _I32, _P, _P, _P, _P, _P, _I32, _I32, _I32, _I32,
+                                          _I64, _P]),
     "pkv_bm_take": (_I32, [_P, _I32, _P]),
     "pkv_bm_create": (_P, [_I32, _I32]),
     "pkv_bm_destroy": (None, [_P]),
@@ -499,6 +510,94 @@ def kv_evict(weights: torch.Tensor, context_lens: torch.Tensor, max_context_len:
     return _result("pkv_kv_evict", _torch.kv_evict(
         weights, context_lens, max_context_len, block_tables, dst_block_tables, budget, recent,
         k_cache, v_cache, k_scale, v_scale, kept, weights_out, new_context_lens, stream))
+
+
+# ----------------------------------------------------------------------------- speculative decoding
+def tree_workspace(num_seqs: int, max_seqlen_q: int, num_q_heads: int, num_kv_heads: int,
+                   head_dim: int, max_context_len: int, device="cuda", stream=None) -> torch.Tensor:
+    """A workspace for paged_tree_attn and paged_tree_attn_fp8 (nothing in it has to be
+    initialised), allocated on `stream` (the current stream when None)."""
+    with torch.cuda.device(device):
+        n = int(_LIB.pkv_tree_workspace_bytes(num_seqs, max_seqlen_q, num_q_heads, num_kv_heads,
+                                              head_dim, max_context_len))
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        with torch.cuda.stream(stream):
+            return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def paged_tree_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    block_tables: torch.Tensor, context_lens: torch.Tensor, max_context_len: int,
+                    cu_seqlens_q: torch.Tensor, max_seqlen_q: int, scale: float,
+                    tree_mask: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
+    """Attention of drafted tokens: the last n = cu_seqlens_q[b + 1] - cu_seqlens_q[b] <=
+    max_seqlen_q positions of context b are the nodes of a tree, rows cu_seqlens_q[b] .. of q. Each
+    attends to the context before the tree and to the nodes that its row of tree_mask names (a
+    node itself and its ancestors); without tree_mask the nodes are a chain.
+
+    q: [Tq, Hq, D] bf16 with dense rows (token stride may be larger); caches [NB, bs, Hkv, D] bf16;
+    block_tables [B, W], context_lens [B] (the nodes included), cu_seqlens_q [B + 1] int32;
+    tree_mask [Tq, >= max_seqlen_q / 64] int64, bit k of word w for node 64 w + k. Rows of q behind
+    the last sequence are left out (their rows of `out` as they were)."""
+    return _result("pkv_paged_tree_attn", _torch.paged_tree_attn(
+        q, k_cache, v_cache, None, None, block_tables, context_lens, max_context_len, cu_seqlens_q,
+        max_seqlen_q, scale, tree_mask, workspace, out, stream))
+
+
+def paged_tree_attn_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                        k_scale: torch.Tensor, v_scale: torch.Tensor, block_tables: torch.Tensor,
+                        context_lens: torch.Tensor, max_context_len: int,
+                        cu_seqlens_q: torch.Tensor, max_seqlen_q: int, scale: float,
+                        tree_mask: torch.Tensor | None = None,
+                        workspace: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                        stream=None) -> torch.Tensor:
+    """paged_tree_attn over an 8-bit cache: caches [NB, bs, Hkv, D] float8_e4m3fn with scales
+    [NB, Hkv, bs / 64] float32 (see kv_store_fp8)."""
+    if k_scale is None or v_scale is None:
+        raise ValueError("k_scale and v_scale must be given")
+    return _result("pkv_paged_tree_attn_fp8", _torch.paged_tree_attn(
+        q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, max_context_len,
+        cu_seqlens_q, max_seqlen_q, scale, tree_mask, workspace, out, stream))
+
+
+def kv_accept(accepted: torch.Tensor, num_accepted: torch.Tensor, cu_seqlens_q: torch.Tensor,
+              context_lens: torch.Tensor, block_tables: torch.Tensor, k_cache: torch.Tensor,
+              v_cache: torch.Tensor, k_scale: torch.Tensor | None = None,
+              v_scale: torch.Tensor | None = None,
+              new_context_lens: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Keep the accepted nodes of every sequence's tree (as paged_tree_attn lays it out): their K
+    and V rows move up behind the context, in place. accepted: [B, A] int32, ascending nodes, of
+    which num_accepted [B] int32 count (a path from the root: itself ascending). Returns the new
+    context lengths [B] int32 (another tensor than context_lens, which the step's other layers
+    still read).
+
+    caches: bf16 [NB, bs, Hkv, D], or float8_e4m3fn with k_scale and v_scale (a group that rows with
+    a larger scale come into takes that scale, its rows are re-rounded)."""
+    return _result("pkv_kv_accept", _torch.kv_accept(
+        accepted, num_accepted, cu_seqlens_q, context_lens, block_tables, k_cache, v_cache, k_scale,
+        v_scale, new_context_lens, stream))
+
+
+def qk_norm_rope_store_fp8(qkv: torch.Tensor, positions: torch.Tensor, cos_sin_cache: torch.Tensor,
+                           context_lens: torch.Tensor, block_tables: torch.Tensor,
+                           k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                           v_scale: torch.Tensor, num_q_heads: int,
+                           q_norm_weight: torch.Tensor | None = None,
+                           k_norm_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                           cu_seqlens: torch.Tensor | None = None,
+                           q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """RMSNorm (with both weights) and RoPE of the new tokens' query and key heads; K and V are
+    appended to an 8-bit cache as kv_store_fp8 does, q is returned.
+
+    qkv: [T, (Hq + 2 Hkv) * D] bf16 (rows may be a strided view); positions [T] int64, the rotary
+    positions; cos_sin_cache [max_position, D] float32; weights [D] bf16 or None;
+    context_lens, block_tables, cu_seqlens, caches and scales as for kv_store_fp8. Returns q
+    [T, Hq, D] bf16. Unlike qk_norm_rope_store nothing is rounded before the rotated values are."""
+    return _result("pkv_qk_norm_rope_store_fp8", _torch.qk_norm_rope_store_fp8(
+        qkv, positions, cos_sin_cache, context_lens, block_tables, k_cache, v_cache, k_scale,
+        v_scale, num_q_heads, q_norm_weight, k_norm_weight, eps, cu_seqlens, q_out, stream))
 
 
 # ----------------------------------------------------------------------------- block manager

@@ -407,6 +407,117 @@ PyObject *kv_evict(PyObject *const *a) {
   return ko && wo && lo ? Py_BuildValue("(NNN)", ko, wo, lo) : nullptr;
 }
 
+// q of drafted tokens [T, Hq, D], each token's heads dense; the token stride.
+int64_t query_rows(const at::Tensor &q, const Cache &c) {
+  need(q, "q", at::kBFloat16, c.index);
+  if (q.dim() != 3 || q.size(2) != c.d)
+    fail(PyExc_ValueError, "q must be [T, Hq, ", c.d, "], got ", q.sizes());
+  if (q.size(0) > 0 && (q.stride(2) != 1 || (q.size(1) > 1 && q.stride(1) != c.d)))
+    fail(PyExc_ValueError, "q: each token's heads must be dense");
+  return q.size(0) > 1 ? q.stride(0) : q.size(1) * c.d;
+}
+
+PyObject *paged_tree_attn(PyObject *const *a) {
+  const Cache c = cache(a[1], a[2], a[3], a[4]);
+  const at::Tensor &q = tensor(a[0], "q");
+  const int64_t q_stride = query_rows(q, c), total = q.size(0);
+  const int32_t hq = size32(q.size(1), "number of query heads");
+  const Lists l = lists(a[6], a[5], c.index);
+  const int32_t longest = integer32(a[7], "max_context_len");
+  const int32_t *cu = ints(a[8], "cu_seqlens_q", c.index, {(int64_t)l.batch + 1});
+  const int32_t most = integer32(a[9], "max_seqlen_q");
+  const float scale = number(a[10], "scale");
+  const int64_t *mask = nullptr;
+  int32_t words = 0;
+  if (given(a[11])) {
+    const at::Tensor &m = tensor(a[11], "tree_mask");
+    if (m.dim() != 2) fail(PyExc_ValueError, "tree_mask must be a [T, words] int64 tensor");
+    words = size32(m.size(1), "tree_mask");
+    need_shape(m, "tree_mask", at::kLong, c.index, {total, m.size(1)});
+    if (64 * (int64_t)words < most)
+      fail(PyExc_ValueError, "tree_mask has ", words, " words of 64 nodes for max_seqlen_q ", most);
+    mask = m.data_ptr<int64_t>();
+  }
+  On on(c.index, a[14]);
+  const at::Tensor out = output(a[13], "out", {total, hq, c.d}, at::kBFloat16, c.index);
+  at::Tensor ws;
+  if (given(a[12])) {
+    ws = tensor(a[12], "workspace");
+    if (!ws.is_cuda() || ws.get_device() != c.index || !ws.is_contiguous())
+      fail(PyExc_ValueError, "workspace must be a contiguous tensor on cuda:", c.index);
+  } else {
+    const size_t n = pkv_tree_workspace_bytes(l.batch, most, hq, c.hkv, c.d, longest);
+    ws = empty({(int64_t)std::max<size_t>(n, 16)}, at::kByte, c.index);
+  }
+  const pkv_status s =
+      c.k_scale ? pkv_paged_tree_attn_fp8(q.data_ptr(), q_stride, total, c.k.data_ptr(),
+                                          c.v.data_ptr(), c.k_scale, c.v_scale, l.tables, l.width,
+                                          l.context_lens, cu, l.batch, most, longest, mask, words,
+                                          hq, c.hkv, c.d, c.block_size, c.num_blocks, scale,
+                                          ws.data_ptr(), ws.nbytes(), out.data_ptr(), on.stream)
+                : pkv_paged_tree_attn(q.data_ptr(), q_stride, total, c.k.data_ptr(),
+                                      c.v.data_ptr(), l.tables, l.width, l.context_lens, cu,
+                                      l.batch, most, longest, mask, words, hq, c.hkv, c.d,
+                                      c.block_size, c.num_blocks, scale, ws.data_ptr(),
+                                      ws.nbytes(), out.data_ptr(), on.stream);
+  return s == PKV_OK ? object(a[13], out) : PyLong_FromLong(s);
+}
+
+PyObject *kv_accept(PyObject *const *a) {
+  const Cache c = cache(a[5], a[6], a[7], a[8]);
+  const Lists l = lists(a[3], a[4], c.index);
+  int32_t width = 0;
+  const int32_t *accepted = table(a[0], "accepted", c.index, l.batch, width);
+  const int32_t *many = ints(a[1], "num_accepted", c.index, {l.batch});
+  const int32_t *cu = ints(a[2], "cu_seqlens_q", c.index, {(int64_t)l.batch + 1});
+  On on(c.index, a[10]);
+  const at::Tensor lens = output(a[9], "new_context_lens", {l.batch}, at::kInt, c.index);
+  const pkv_status s =
+      pkv_kv_accept(accepted, width, many, cu, l.context_lens, l.tables, l.width, l.batch,
+                    c.k.data_ptr(), c.v.data_ptr(), c.k_scale_w, c.v_scale_w, c.hkv, c.d,
+                    c.block_size, c.num_blocks, lens.data_ptr<int32_t>(), on.stream);
+  return s == PKV_OK ? object(a[9], lens) : PyLong_FromLong(s);
+}
+
+PyObject *qk_norm_rope_store_fp8(PyObject *const *a) {
+  need_fp8(a[7], a[8]);
+  const Cache c = cache(a[5], a[6], a[7], a[8]);
+  const Lists l = lists(a[3], a[4], c.index);
+  const int32_t hq = integer32(a[9], "num_q_heads");
+  if (hq < 1) fail(PyExc_ValueError, "num_q_heads must be at least 1");
+  const at::Tensor &qkv = tensor(a[0], "qkv");
+  need(qkv, "qkv", at::kBFloat16, c.index);
+  const int64_t width = ((int64_t)hq + 2 * (int64_t)c.hkv) * c.d;
+  if (qkv.dim() != 2 || qkv.size(1) != width || qkv.stride(1) != 1)
+    fail(PyExc_ValueError, "qkv must be [T, ", width, "] with dense rows, got ", qkv.sizes());
+  const int64_t T = qkv.size(0);
+  const at::Tensor &positions = tensor(a[1], "positions");
+  need_shape(positions, "positions", at::kLong, c.index, {T});
+  const at::Tensor &cos_sin = tensor(a[2], "cos_sin_cache");
+  if (cos_sin.dim() != 2) fail(PyExc_ValueError, "cos_sin_cache must be [max_position, D]");
+  need_shape(cos_sin, "cos_sin_cache", at::kFloat, c.index, {cos_sin.size(0), c.d});
+  const void *w[2] = {nullptr, nullptr};
+  if (given(a[10]) != given(a[11]))
+    fail(PyExc_ValueError, "q_norm_weight and k_norm_weight go together");
+  for (int i = 0; i < 2; ++i)
+    if (given(a[10 + i])) {
+      const char *name = i ? "k_norm_weight" : "q_norm_weight";
+      const at::Tensor &t = tensor(a[10 + i], name);
+      need_shape(t, name, at::kBFloat16, c.index, {c.d});
+      w[i] = t.data_ptr();
+    }
+  const float eps = number(a[12], "eps");
+  const int32_t *cu = given(a[13]) ? ints(a[13], "cu_seqlens", c.index, {(int64_t)l.batch + 1}) : nullptr;
+  On on(c.index, a[15]);
+  const at::Tensor q = output(a[14], "q_out", {T, hq, c.d}, at::kBFloat16, c.index);
+  const pkv_status s = pkv_qk_norm_rope_store_fp8(
+      qkv.data_ptr(), T > 1 ? qkv.stride(0) : width, T, positions.data_ptr<int64_t>(), w[0], w[1],
+      eps, cos_sin.data_ptr<float>(), cos_sin.size(0), cu, l.context_lens, l.tables, l.width,
+      l.batch, q.data_ptr(), c.k.data_ptr(), c.v.data_ptr(), c.k_scale_w, c.v_scale_w, hq, c.hkv,
+      c.d, c.block_size, c.num_blocks, on.stream);
+  return s == PKV_OK ? object(a[14], q) : PyLong_FromLong(s);
+}
+
 // A Python function of exactly N arguments; no C++ exception leaves it.
 template <PyObject *(*F)(PyObject *const *), Py_ssize_t N>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
@@ -445,6 +556,9 @@ PyMethodDef g_methods[] = {
     {"paged_decode_attn_fp8", method<paged_decode_attn_fp8, 15>(), METH_FASTCALL, nullptr},
     {"paged_decode_attn_weights", method<paged_decode_attn_weights, 13>(), METH_FASTCALL, nullptr},
     {"kv_evict", method<kv_evict, 15>(), METH_FASTCALL, nullptr},
+    {"paged_tree_attn", method<paged_tree_attn, 15>(), METH_FASTCALL, nullptr},
+    {"kv_accept", method<kv_accept, 11>(), METH_FASTCALL, nullptr},
+    {"qk_norm_rope_store_fp8", method<qk_norm_rope_store_fp8, 16>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_pkv_torch", nullptr, -1, g_methods,

@@ -1,0 +1,238 @@
+// kv_accept.cu -- after the drafted tokens of a step have been judged: the rows of the accepted
+// path of each sequence's tree move up behind the context, in place.
+//
+// The nodes of sequence b are positions P .. L - 1, P = L - n. Row P + j becomes row P + a_j for
+// the accepted nodes a_0 < a_1 < .. of the path. Ascending nodes have a_j >= j, so no row is
+// written that a later one still reads: rows are moved in passes of ascending j, each pass read
+// whole before it is written. In an 8-bit cache the rows that come into a group of 64 positions
+// may bring larger scales: the group then takes the largest, and what it holds is re-rounded.
+//
+// One CTA owns K or V of a sequence for some of its heads. The bytes are few (the moved rows, read
+// and written once), so what counts is the chain of dependent loads: lengths, list and table,
+// rows. Each step of it is taken for all rows at once.
+#include <math.h>
+
+#include <algorithm>
+
+#include "device_common.cuh"
+#include "fp8_cache.cuh"
+#include "launch.h"
+#include "pkv.h"
+
+namespace pkv {
+namespace {
+
+constexpr int kD = 128;
+constexpr int kThreads = 256;
+constexpr int kRows = 64;       // rows of a round: in an 8-bit cache those of one group
+constexpr int kMaxHeads = 8;    // heads of a CTA
+constexpr int kLoads = 8;       // 16-byte pieces of a thread in flight
+
+struct AcceptParams {
+  const int32_t *accepted;
+  int32_t accepted_width;
+  const int32_t *num_accepted;
+  const int32_t *cu;
+  const int32_t *context_lens;
+  const int32_t *block_tables;
+  int32_t table_width;
+  uint8_t *k_cache, *v_cache;
+  float *k_scale, *v_scale;
+  int32_t hkv, block_size, heads_per_cta;
+  int64_t num_blocks;
+  int32_t *new_context_lens;
+  unsigned int *err;
+};
+
+__device__ __forceinline__ uint4 rescale16(uint4 w, float ratio) {
+  return make_uint4(rescale4(w.x, ratio), rescale4(w.y, ratio), rescale4(w.z, ratio),
+                    rescale4(w.w, ratio));
+}
+
+template <bool F8>
+__global__ void __launch_bounds__(kThreads) kv_accept_kernel(const AcceptParams p) {
+  constexpr int kPieces = F8 ? 8 : 16;  // of a head's row
+  __shared__ int64_t src_row[kRows], dst_row[kRows];  // pool rows; -1: a bad block
+  __shared__ float src_scale[F8 ? kRows : 1][kMaxHeads];
+  __shared__ float old_scale[kMaxHeads], new_scale[kMaxHeads];
+  __shared__ int32_t count;
+  const int tid = threadIdx.x;
+  const int parts = (p.hkv + p.heads_per_cta - 1) / p.heads_per_cta;
+  const int part = blockIdx.x % parts;
+  const bool is_v = (blockIdx.x / parts) & 1;
+  const int b = blockIdx.x / parts / 2;
+  const int h0 = part * p.heads_per_cta, heads = min(p.heads_per_cta, p.hkv - h0);
+  const bool first = part == 0 && !is_v;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int64_t c0 = *(p.cu + b), c1 = *(p.cu + b + 1), L = *(p.context_lens + b);
+  int many = *(p.num_accepted + b);
+  const int64_t n = c1 - c0, start = L - n;
+  if (n < 0 || start < 0 || L > (int64_t)p.table_width * p.block_size) {
+    if (first && tid == 0) {
+      record_error(p.err, n < 0 ? PKV_DEVERR_SEQLEN_RANGE : PKV_DEVERR_CONTEXT_RANGE);
+      p.new_context_lens[b] = 0;
+    }
+    return;
+  }
+  if (many < 0 || many > n || many > p.accepted_width) {
+    if (first && tid == 0) record_error(p.err, PKV_DEVERR_NODE_RANGE);
+    many = 0;
+  }
+  const int32_t *list = p.accepted + (int64_t)b * p.accepted_width;
+  // the path ends before the first entry that is no later node of the tree
+  if (tid == 0) count = many;
+  __syncthreads();
+  for (int j = tid; j < many; j += kThreads) {
+    const int32_t a = *(list + j), before = j ? *(list + j - 1) : -1;
+    if (a <= before || a >= n) {
+      atomicMin(&count, j);
+      if (first) record_error(p.err, PKV_DEVERR_NODE_RANGE);
+    }
+  }
+  __syncthreads();
+  many = count;
+  if (first && tid == 0) p.new_context_lens[b] = (int32_t)start + many;
+  if (many == 0 || aborted(p.err)) return;
+  const int32_t *table = p.block_tables + (int64_t)b * p.table_width;
+  auto pool_row = [&](int64_t pos) -> int64_t {
+    const int64_t blk = *(table + pos / p.block_size);
+    if (blk < 0 || blk >= p.num_blocks) {
+      record_error(p.err, PKV_DEVERR_BLOCK_RANGE);
+      return -1;
+    }
+    return blk * p.block_size + pos % p.block_size;
+  };
+  uint8_t *const pool = is_v ? p.v_cache : p.k_cache;
+  float *const scales = is_v ? p.v_scale : p.k_scale;
+  const int groups = p.block_size / kFp8Group;
+  auto scale_at = [&](int64_t row, int h) -> int64_t {
+    return (row / p.block_size * p.hkv + h) * groups + row % p.block_size / kFp8Group;
+  };
+  const int64_t row_bytes = (int64_t)p.hkv * kPieces * 16;
+  const int pieces = heads * kPieces;  // of a row
+  auto piece_of = [&](int64_t row, int i) {
+    return reinterpret_cast<uint4 *>(pool + row * row_bytes + h0 * kPieces * 16) + i;
+  };
+  for (int j0 = 0, rows; j0 < many; j0 += rows) {
+    rows = min(kRows, many - j0);
+    // (of an 8-bit cache: the rows that go to one group)
+    if (F8) rows = min(rows, kFp8Group - (int)((start + j0) % kFp8Group));
+    if (tid < rows) {
+      src_row[tid] = pool_row(start + *(list + j0 + tid));
+      dst_row[tid] = pool_row(start + j0 + tid);
+    }
+    __syncthreads();
+    const int64_t d0 = dst_row[0];
+    if (F8 && d0 >= 0) {
+      if (tid < heads) {
+        old_scale[tid] = scales[scale_at(d0, h0 + tid)];
+        new_scale[tid] = old_scale[tid];
+      }
+      for (int i = tid; i < rows * heads; i += kThreads)
+        src_scale[i / heads][i % heads] =
+            src_row[i / heads] >= 0 ? scales[scale_at(src_row[i / heads], h0 + i % heads)] : 0.f;
+      __syncthreads();
+      if (tid < heads) {
+        float s = old_scale[tid];
+        for (int i = 0; i < rows; ++i) s = fmaxf(s, src_scale[i][tid]);
+        new_scale[tid] = s;
+        if (s > old_scale[tid]) scales[scale_at(d0, h0 + tid)] = s;
+      }
+      __syncthreads();
+      // the rows of the group from before the tree, at the scale that grew
+      const int before = j0 == 0 ? (int)(start % kFp8Group) : 0;
+      for (int i = tid; i < before * pieces; i += kThreads) {
+        const int h = i % pieces / kPieces;
+        if (new_scale[h] > old_scale[h]) {
+          uint4 *w = piece_of(d0 - before + i / pieces, i % pieces);
+          *w = rescale16(*w, old_scale[h] / new_scale[h]);
+        }
+      }
+    }
+    const int all = rows * pieces;
+    for (int i0 = 0; i0 < all; i0 += kThreads * kLoads) {
+      uint4 x[kLoads];
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) {
+        const int i = i0 + u * kThreads + tid;
+        x[u] = make_uint4(0, 0, 0, 0);
+        if (i < all && src_row[i / pieces] >= 0) x[u] = *piece_of(src_row[i / pieces], i % pieces);
+      }
+      __syncthreads();  // (each pass is read before it is written)
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) {
+        const int i = i0 + u * kThreads + tid, r = i / pieces;
+        if (i >= all || dst_row[r] < 0) continue;
+        bool same = src_row[r] == dst_row[r];
+        if (F8) {
+          const int h = i % pieces / kPieces;
+          const float ratio = src_scale[r][h] / new_scale[h];
+          if (ratio < 1.f) {
+            x[u] = rescale16(x[u], ratio);
+            same = false;
+          }
+        }
+        if (!same) *piece_of(dst_row[r], i % pieces) = x[u];
+      }
+      __syncthreads();
+    }
+  }
+}
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+}  // namespace
+}  // namespace pkv
+
+extern "C" pkv_status pkv_kv_accept(const int32_t *accepted, int32_t accepted_width,
+                                    const int32_t *num_accepted, const int32_t *cu_seqlens_q,
+                                    const int32_t *context_lens, const int32_t *block_tables,
+                                    int32_t block_table_width, int32_t num_seqs, void *k_cache,
+                                    void *v_cache, float *k_scale, float *v_scale,
+                                    int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                    int64_t num_blocks, int32_t *new_context_lens, void *stream) {
+  using namespace pkv;
+  if (num_seqs < 0 || accepted_width < 0 || num_kv_heads <= 0 || head_dim <= 0 ||
+      block_size <= 0 || num_blocks <= 0 || block_table_width <= 0)
+    return PKV_ERR_INVALID_ARG;
+  if (num_seqs == 0) return PKV_OK;
+  if (!num_accepted || !cu_seqlens_q || !context_lens || !block_tables || !k_cache || !v_cache ||
+      !new_context_lens || (accepted_width > 0 && !accepted) || !k_scale != !v_scale)
+    return PKV_ERR_INVALID_ARG;
+  // (the calls of a step's other layers read the old lengths)
+  if (new_context_lens == context_lens) return PKV_ERR_INVALID_ARG;
+  if (head_dim != kD || block_size % (k_scale ? 256 : kFp8Group) != 0) return PKV_ERR_UNSUPPORTED;
+  if (!aligned16(k_cache) || !aligned16(v_cache)) return PKV_ERR_UNSUPPORTED;
+  const int num_sms = current_sm_count();
+  unsigned int *err = current_error_word();
+  if (num_sms <= 0 || !err) return PKV_ERR_CUDA;
+  AcceptParams prm{};
+  prm.accepted = accepted;
+  prm.accepted_width = accepted_width;
+  prm.num_accepted = num_accepted;
+  prm.cu = cu_seqlens_q;
+  prm.context_lens = context_lens;
+  prm.block_tables = block_tables;
+  prm.table_width = block_table_width;
+  prm.k_cache = static_cast<uint8_t *>(k_cache);
+  prm.v_cache = static_cast<uint8_t *>(v_cache);
+  prm.k_scale = k_scale;
+  prm.v_scale = v_scale;
+  prm.hkv = num_kv_heads;
+  prm.block_size = block_size;
+  prm.num_blocks = num_blocks;
+  prm.new_context_lens = new_context_lens;
+  prm.err = err;
+  // as many heads to a CTA as still leave every SM about four CTAs
+  prm.heads_per_cta = (int32_t)std::max<int64_t>(
+      1, std::min<int64_t>(kMaxHeads, 2 * (int64_t)num_seqs * num_kv_heads / (4 * num_sms)));
+  const int64_t grid =
+      2 * (int64_t)num_seqs * ((num_kv_heads + prm.heads_per_cta - 1) / prm.heads_per_cta);
+  if (grid > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e =
+      k_scale ? launch_after(kv_accept_kernel<true>, (unsigned)grid, kThreads, st, prm)
+              : launch_after(kv_accept_kernel<false>, (unsigned)grid, kThreads, st, prm);
+  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
