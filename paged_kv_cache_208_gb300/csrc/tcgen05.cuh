@@ -145,6 +145,19 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       : "memory");
 }
 
+// The same, with the lanes whose bits are set in `off` left as they are.
+__device__ __forceinline__ void umma_f16_ts_lanes(uint32_t d_tmem, uint32_t a_tmem,
+                                                  uint64_t b_desc, uint32_t idesc,
+                                                  const uint32_t (&off)[4], bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %6, %7, %8}, p;\n\t}" ::"r"(
+          d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate), "r"(off[0]), "r"(off[1]),
+      "r"(off[2]), "r"(off[3])
+      : "memory");
+}
+
 // Arrive (once) on this CTA's mbarrier when every UMMA this thread issued so far has completed.
 __device__ __forceinline__ void umma_commit(uint64_t *bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
@@ -271,12 +284,38 @@ __device__ __forceinline__ void tmem_st16x2_16(uint32_t taddr, const uint32_t (&
       : "memory");
 }
 
-template <int kSplit>
-__device__ __forceinline__ void tmem_st16x2_8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x32bx2.x8.b32 [%0], %1, {%2,%3,%4,%5,%6,%7,%8,%9};" ::"r"(taddr),
-      "n"(kSplit), PKV_W8(0)
-      : "memory");
+// Two threads per lane again, C columns each (8, 16, 32 or 64), the second's C further; waited for.
+template <int C>
+__device__ __forceinline__ void tmem_ld16x2(uint32_t taddr, uint32_t (&x)[C / 8][8]) {
+  static_assert(C == 8 || C == 16 || C == 32 || C == 64, "");
+#pragma unroll
+  for (int k = 0; k < C / 8; ++k) {
+    uint32_t (&r)[8] = x[k];
+    asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8], %9;"
+                 : PKV_R8(0)
+                 : "r"(taddr + 8 * k), "n"(C));
+  }
+  // (the registers pass through the asm: no use of them comes before the wait)
+#pragma unroll
+  for (int k = 0; k < C / 8; ++k) {
+    uint32_t (&r)[8] = x[k];
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : PKV_RW8(0)::"memory");
+  }
+}
+
+// N columns (4 or 8) of each of two threads per lane, the second's kSplit further.
+template <int kSplit, int N>
+__device__ __forceinline__ void tmem_st16x2(uint32_t taddr, const uint32_t (&r)[N]) {
+  static_assert(N == 4 || N == 8, "");
+  if constexpr (N == 8)
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x32bx2.x8.b32 [%0], %1, {%2,%3,%4,%5,%6,%7,%8,%9};" ::"r"(taddr),
+        "n"(kSplit), PKV_W8(0)
+        : "memory");
+  else
+    asm volatile("tcgen05.st.sync.aligned.16x32bx2.x4.b32 [%0], %1, {%2,%3,%4,%5};" ::"r"(taddr),
+                 "n"(kSplit), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
 }
 
 // This warp's 32 TMEM lanes, N consecutive 32-bit columns (2, 4 or 8), waited for.

@@ -4,47 +4,64 @@
 //
 // The rows that share a KV head -- (node, query head of the group) pairs -- attend over the same
 // keys, so all of them together are the M of a matrix product: K and V are read once for up to
-// 128 rows (64 nodes of two heads, 16 of eight). With some tens of rows a key of 512 bytes
-// costs 512 * rows multiplications, far below what the tensor cores do in the time of its load:
-// the kernel is bound by HBM, and its work is cut so that every SM reads the same number of keys.
+// 128 rows (64 nodes of two heads, 16 of eight). With some tens of rows the tensor cores are through
+// with a key long before the next one has been loaded: the kernel is bound by HBM, and its work
+// is cut so that every SM reads the same number of keys.
 //
-// Work. A unit is (sequence, KV head, tile of 128 rows); its length is its context in granules
-// of 64 keys. All units in a row make one axis of granules, which the workers share out
-// evenly: worker w takes [w T / W, (w + 1) T / W), whatever the units' lengths. The lengths are
-// device data, so every CTA sums them up at its start (one scan over the sequences) and walks its
-// own part. A unit that lies within a worker's part is written out directly; what a cut leaves is
-// normalised, goes to the workspace with its log2-sum-exp, and tree_combine_kernel merges it.
-// Which parts there are depends on the lengths alone, so the same call gives the same bits.
-// Where trees have more rows than a tile, `group` neighbouring CTAs are one worker and take the
-// row tiles of the same keys at the same time: K and V then come from L2 for all but one of them.
+// Work. A unit is a sequence's row tile (128 rows of each of `heads` neighbouring KV heads), its
+// length the context in granules of 64 keys. All units in a row make one axis of granules, which the
+// workers share out evenly, whatever the units' lengths; a worker is a group of CTAs that take the
+// heads of a unit (whose values lie in the same DRAM pages) and, where trees have more rows than a
+// tile, up to four row tiles of the same keys at the same time (K and V then come from L2 for all
+// but one of them). The lengths are device data, so every CTA sums them up at its start (one scan
+// over the sequences) and walks its own part. A unit within a worker's part is written out
+// directly; what a cut leaves is normalised and goes to the workspace with its log2-sum-exp, and
+// tree_combine_kernel merges it. Which parts there are depends on the lengths alone, so the same
+// call gives the same bits.
 //
 // Per tile of 128 keys (M = 128 rows, one CTA):
 //   S = Q K^T    Q in tensor memory (the A operand), K rows in shared memory
 //   softmax      8 warps, two threads to a row: running maximum and sum in fp32, P = 2^(s - m)
-//                written back over S as two bf16 parts (P = hi + lo within 2^-17 of itself): the
-//                second product's cost is hidden behind the loads, and the output differs from
-//                one with fp32 weights in its last rounding only
+//                written back over S
 //   O += P V     P from tensor memory, V rows in shared memory
-// S has two buffers, Q two (the next unit's is loaded while this one's tiles are in work).
-// O is rescaled only when a row's maximum grows by more than 2^8, as in prefill.cu.
+// S has two buffers, Q two (the next item's is loaded while this one's tiles are in work). O is
+// rescaled only when a row's maximum grows by more than 2^8, as in prefill.cu.
+//
+// What P is rounded to:
+//   bf16 cache, one row tile at a time: two bf16 parts, P = hi + lo within 2^-17 of itself. The
+//                second product's time is hidden behind the loads (a tile's 64 KiB take an SM about
+//                2700 cycles, its products 1536), and the output is that of fp32 weights.
+//   bf16 cache, several row tiles: bf16. The tensor cores are the limit there (the same keys once per
+//                tile), and two parts would cost half as much again.
+//   8-bit cache: fp16 (2^-11), see below.
+//
+// The 8-bit cache. An e4m3 code is an fp16 value, so the codes are widened in shared memory (by the
+// warps that load Q) and the products are those of fp16: exact in K and V. Q is divided by a power of
+// two of its row (its largest |q| becomes 1 to 2) and rounded to fp16, which keeps bf16's digits
+// down to 2^-14 of that and is off by 2^-25 of it at most below. The K scale of a key's group and the
+// row's power multiply the scores. The V scale is part of P: with v = log2 of it, m runs over s + v,
+// P' = 2^(s + v - m + 6) (between 2^-20 and 2^14 in fp16's normal range), and l sums P' / 2^(v + 6).
 //
 // Rows. 16 rows make a chunk: nb = 16 / G nodes with their G query heads (with more than 16 heads
-// one node and 16 of them). Chunk c of a tile lies in 16 of the 128 TMEM lanes that warp c reads,
-// lane quadrant c % 4: with few rows the softmax is spread over all four SM sub-partitions.
+// one node and 16 of them). Chunk c of a tile lies in 16 of the 128 TMEM lanes that softmax warp c
+// reads, lane quadrant c % 4: with few rows the softmax is spread over all four SM sub-partitions.
 //
 // Warps (512 threads): 0-7 softmax and epilogue (warp c: chunk c), 8 work walk and K loads, 9 S
-// products, 10 V loads, 11 PV products, 12-15 Q into tensor memory. Loads are TMA with 128-byte
-// swizzle, 64 keys to a box (a granule never straddles a block).
+// products, 10 V loads, 11 PV products, 12-15 Q into tensor memory, a look through the nodes' V rows,
+// and the widening of an 8-bit cache. Loads are TMA with 128-byte swizzle, 64 keys to a box (a granule
+// never straddles a block). K and V have two slots each: more (3 + 3, 4 + 3) made every case slower,
+// K tiles far ahead taking their turn before V tiles that are needed sooner.
 // TMEM (512 columns): Q [0, 64) [64, 128), S [128, 256) [256, 384), O [384, 512).
 //
 // Masked places. A key that a row does not see is left out of its maximum and gets P = 0; V rows
 // past the context are zeroed in shared memory. A node that others do not see may hold
-// infinities or NaNs, and 0 x NaN would reach them: the V warp looks through the nodes' rows, puts
-// zeros in the place of what is not finite, and the rows that do see such a node are put right
-// in memory (not_finite_fix).
+// infinities or NaNs, and 0 x NaN would reach them: the nodes' V rows are looked through, what is
+// not finite becomes zero there, and the rows that do see such a node are put right in memory
+// (not_finite_fix).
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "device_common.cuh"
 #include "fp8_cache.cuh"
@@ -59,106 +76,29 @@ constexpr int kD = 128;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleLog2 = 8.0f;
-constexpr int kWarps = 4;
-
-struct TreeParams {
-  const uint16_t *q;
-  int64_t q_stride;
-  int64_t total_q;
-  const uint8_t *k_cache, *v_cache;
-  const float *k_scale, *v_scale;  // of an 8-bit cache
-  const int32_t *block_tables;
-  int32_t table_width;
-  const int32_t *context_lens;
-  const int32_t *cu;
-  int32_t max_nodes, max_context;
-  const uint64_t *mask;
-  int32_t mask_words;
-  int32_t hq, hkv, block_size;
-  int64_t num_blocks;
-  int32_t num_seqs;
-  float scale_log2;  // of the scale's magnitude
-  uint32_t q_sign;   // flips the signs of two bf16 where the scale is negative
-  uint16_t *out;
-  unsigned int *err;
-};
-
-template <bool F8>
-__global__ void __launch_bounds__(kWarps * 32) tree_attn_kernel(const TreeParams p) {
-  const int lane = threadIdx.x & 31;
-  const int b = blockIdx.y;
-  const int unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int node = unit / p.hq, hq = unit % p.hq, h = hq / (p.hq / p.hkv);
-  const int64_t c0 = p.cu[b], n = p.cu[b + 1] - c0;
-  if (c0 < 0 || n < 0 || c0 + n > p.total_q || n > p.max_nodes) {
-    if (unit == 0 && lane == 0) record_error(p.err, PKV_DEVERR_SEQLEN_RANGE);
-    return;
-  }
-  if (node >= n) return;
-  int64_t L = p.context_lens[b];
-  if (L < n || L > p.max_context || L > (int64_t)p.table_width * p.block_size) {
-    if (unit == 0 && lane == 0) record_error(p.err, PKV_DEVERR_CONTEXT_RANGE);
-    L = 0;
-  }
-  const uint2 qw = *reinterpret_cast<const uint2 *>(p.q + (c0 + node) * p.q_stride + hq * kD + 4 * lane);
-  const float q[4] = {bf16_lo(qw.x), bf16_hi(qw.x), bf16_lo(qw.y), bf16_hi(qw.y)};
-  const uint64_t *mask = p.mask ? p.mask + (c0 + node) * p.mask_words : nullptr;
-  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int64_t i = 0; i < L; ++i) {
-    const int64_t j = i - (L - n);
-    if (j >= 0 && !(mask ? mask[j >> 6] >> (j & 63) & 1 : j <= node)) continue;
-    const int64_t blk = p.block_tables[(int64_t)b * p.table_width + i / p.block_size];
-    const bool ok = blk >= 0 && blk < p.num_blocks;
-    if (!ok && lane == 0) record_error(p.err, PKV_DEVERR_BLOCK_RANGE);
-    const int64_t at = ((blk * p.block_size + i % p.block_size) * p.hkv + h) * kD + 4 * lane;
-    float k[4] = {0.f, 0.f, 0.f, 0.f}, v[4] = {0.f, 0.f, 0.f, 0.f};
-    if (ok && !F8) {
-      const uint2 kw = *reinterpret_cast<const uint2 *>(p.k_cache + 2 * at);
-      const uint2 vw = *reinterpret_cast<const uint2 *>(p.v_cache + 2 * at);
-      k[0] = bf16_lo(kw.x), k[1] = bf16_hi(kw.x), k[2] = bf16_lo(kw.y), k[3] = bf16_hi(kw.y);
-      v[0] = bf16_lo(vw.x), v[1] = bf16_hi(vw.x), v[2] = bf16_lo(vw.y), v[3] = bf16_hi(vw.y);
-    } else if (ok) {
-      const int groups = p.block_size / kFp8Group;
-      const int64_t sc = (blk * p.hkv + h) * groups + i % p.block_size / kFp8Group;
-      const uint32_t kw = *reinterpret_cast<const uint32_t *>(p.k_cache + at);
-      const uint32_t vw = *reinterpret_cast<const uint32_t *>(p.v_cache + at);
-      const float ks = p.k_scale[sc], vs = p.v_scale[sc];
-      const float2 k0 = f16x2_to_f32(cvt_f16x2_e4m3x2(kw)), k1 = f16x2_to_f32(cvt_f16x2_e4m3x2_hi(kw));
-      const float2 v0 = f16x2_to_f32(cvt_f16x2_e4m3x2(vw)), v1 = f16x2_to_f32(cvt_f16x2_e4m3x2_hi(vw));
-      k[0] = k0.x * ks, k[1] = k0.y * ks, k[2] = k1.x * ks, k[3] = k1.y * ks;
-      v[0] = v0.x * vs, v[1] = v0.y * vs, v[2] = v1.x * vs, v[3] = v1.y * vs;
-    }
-    float s = q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3];
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
-    s *= p.scale_log2;
-    const float top = fmaxf(m, s);
-    const float old = m == -INFINITY ? 0.f : exp2f(m - top), w = exp2f(s - top);
-    m = top;
-    l = l * old + w;
-#pragma unroll
-    for (int d = 0; d < 4; ++d) o[d] = o[d] * old + w * v[d];
-  }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  *reinterpret_cast<uint2 *>(p.out + ((c0 + node) * p.hq + hq) * kD + 4 * lane) =
-      make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
-}
 
 constexpr int kTile = 128;    // keys
 constexpr int kGranule = 64;  // keys of a TMA box, and what the work is measured in
+static_assert(kGranule == kFp8Group, "a granule has one scale");
 constexpr int kChunkRows = 16;
 constexpr int kChunks = 8;    // of a row tile
 constexpr int kSoftmaxWarps = 8;
 constexpr int kKWarp = 8, kSWarp = 9, kVWarp = 10, kPvWarp = 11, kQWarp0 = 12;
 constexpr int kThreads = 16 * 32;
-constexpr int kKSlots = 4, kVSlots = 3;
+constexpr int kSlots = 2;     // of K and of V
+constexpr int kRawSlots = 2;  // of each pool's codes, 8-bit cache
 constexpr uint32_t kTileBytes = kTile * kD * 2;
 constexpr uint32_t kPlane = kTileBytes / 2;         // 64 dims of the tile's keys, 128-byte rows
-constexpr uint32_t kGranuleBytes = kGranule * 128;  // of a plane
+constexpr uint32_t kGranuleBytes = kGranule * 128;  // of a plane, or of an 8-bit pool
+constexpr uint32_t kRawBytes = kTile * kD;
+constexpr int kScaleTiles = 8;  // a tile's scales stay until its softmax: six tiles at most
 constexpr int kRing = 4;
 constexpr uint32_t kQCol = 0, kSCol = 128, kOCol = 384, kTmemCols = 512;
 constexpr int kItemConsumers = kSoftmaxWarps + 3 + 4;  // S, V, PV and Q warps
-constexpr int kMaxGroup = 4;
+constexpr int kMaxGroup = 8, kMaxTiles = 4;  // CTAs, and row tiles, of a worker
+constexpr int kOffset8 = 6;     // log2 of what P' is larger by, 8-bit cache
+
+enum Mode { kTwoParts, kOnePart, kFp8 };
 
 // A worker's share of a unit.
 struct Item {
@@ -182,44 +122,110 @@ struct CutInfo {
 };
 static_assert(sizeof(CutInfo) == 64, "");
 
+struct RawSmem {  // 8-bit cache
+  uint8_t k[kRawSlots][kRawBytes], v[kRawSlots][kRawBytes];
+  alignas(16) float scale[kScaleTiles][2][2][4];  // [tile][granule][K, V]: four groups' around it
+  float q_power[kRing][kChunks * kChunkRows];     // log2 of what the rows of q were divided by
+  uint64_t k_full[kRawSlots], k_empty[kRawSlots], v_full[kRawSlots], v_empty[kRawSlots];
+};
+struct NoRaw {};
+
+template <Mode M>
 struct TreeSmem {
-  uint8_t k[kKSlots][kTileBytes];  // 1024-byte aligned (128-byte swizzle atoms)
-  uint8_t v[kVSlots][kTileBytes];
+  uint8_t k[kSlots][kTileBytes];  // 1024-byte aligned (128-byte swizzle atoms)
+  uint8_t v[kSlots][kTileBytes];
+  std::conditional_t<M == kFp8, RawSmem, NoRaw> raw;
   Item items[kRing];
   int32_t dirty[kRing];            // of the item in this ring slot
-  uint64_t k_full[kKSlots], k_empty[kKSlots], v_full[kVSlots], v_empty[kVSlots];
-  uint64_t v_fixed[kVSlots];       // rows past the context zeroed, nodes looked through
+  uint64_t k_full[kSlots], k_empty[kSlots], v_full[kSlots], v_empty[kSlots];
+  // bf16: a V tile that holds nodes has landed; they have been looked through, rows past the
+  // context zeroed
+  uint64_t v_ready[kSlots], v_fixed[kSlots];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], p_full[2], o_full[2], o_free, drain[2];
-  uint64_t item_full[kRing], item_empty[kRing], scanned[kRing];
+  uint64_t item_full[kRing], item_empty[kRing];
+  uint64_t scanned[kRing];         // `dirty` is known
   uint32_t tmem_base;
   int32_t stop;
-  int64_t warp_sums[16];
-  int32_t start_b;                 // the sequence that the CTA's part starts in
-  int64_t start_at, total;         // where that sequence starts on the axis; the axis' length
+  int32_t warp_sums[16];
+  // the sequence that the CTA's part starts in, and where that starts on the axis
+  int32_t start_b, start_at, start_q0, start_n, start_L;
+  int32_t total;                   // the axis' length
 };
+static_assert(sizeof(TreeSmem<kFp8>) + 1024 <= 232448, "fits the SM");
 
-static_assert(sizeof(TreeSmem) + 1024 <= 232448, "fits the SM");
-
-struct FlashParams {
-  TreeParams t;
-  int32_t group, workers;  // CTAs of a worker; workers
-  int32_t hb, nb, parts;   // heads and nodes of a chunk; chunks that share its nodes
+struct TreeParams {
+  const uint16_t *q;
+  int64_t q_stride;
+  int64_t total_q;
+  const uint8_t *k_cache, *v_cache;
+  const float *k_scale, *v_scale;  // of an 8-bit cache
+  const int32_t *block_tables;
+  int32_t table_width;
+  const int32_t *context_lens;
+  const int32_t *cu;
+  int32_t max_nodes, max_context;
+  const uint64_t *mask;
+  int32_t mask_words;
+  int32_t hq, hkv, group_heads, block_size;  // group_heads: query heads of a KV head
+  int64_t num_blocks;
+  int32_t num_seqs;
+  float scale_log2;  // of the scale's magnitude
+  uint32_t q_sign;   // flips the signs of two bf16 where the scale is negative
+  uint16_t *out;
   bool out_32b;
-  CutInfo *cuts;           // one per CTA
-  float *part_o, *part_lse;  // [CTA][2][rows][kD], [CTA][2][rows]
+  unsigned int *err;
+  // how the work is cut
+  int32_t workers, group;        // workers, and the CTAs of one: `heads` KV heads of `at_once` tiles
+  int32_t heads, at_once;
+  int32_t per_tile;              // hkv / heads: units that share a row tile
+  int32_t hb, nb, parts;         // heads and nodes of a chunk; chunks that share its nodes
+  uint32_t nb_magic, hb_magic;   // x / nb is the high word of x * nb_magic, for x < 2^24
+  CutInfo *cuts;                 // one per CTA
+  float *part_o, *part_lse;      // [CTA][2][part_rows][kD], [CTA][2][part_rows]
   int32_t part_rows;
+
+  __device__ __forceinline__ int chunks_of(int n) const {
+    return nb == 1 ? n * parts : (int)__umulhi(n + nb - 1, nb_magic);  // (nb > 1: one part)
+  }
+  // the first node and head (of the group) of a chunk
+  __device__ __forceinline__ int first_node(int chunk) const {
+    return nb > 1 ? chunk * nb : parts == 1 ? chunk : chunk / parts;
+  }
+  __device__ __forceinline__ int first_head(int chunk) const {
+    return parts == 1 ? 0 : chunk % parts * kChunkRows;
+  }
+  // row r of a chunk: its node, from the chunk's first one
+  __device__ __forceinline__ int node_of(int r) const {
+    return hb == 1 ? r : (int)__umulhi(r, hb_magic);
+  }
+  // The axis in `workers` parts, the first `rest` of them one granule longer.
+  __device__ __forceinline__ static int32_t part_start(int w, int32_t each, int32_t rest) {
+    return w * each + min(w, rest);
+  }
+  __device__ __forceinline__ static int32_t part_of(int32_t x, int32_t each, int32_t rest) {
+    const int32_t longer = rest * (each + 1);
+    return x < longer ? x / (each + 1) : rest + (x - longer) / each;
+  }
 };
 
 // Rows of a sequence as the work is counted: its nodes (0: none, or a bad cu_seqlens) and its
 // context (0 also for a bad length, whose rows become zeros).
 struct Seq {
   int32_t q0, n, L;
-  int64_t units, length;  // row tiles (of `group` CTAs) x KV heads, granules of one
-  __device__ __forceinline__ int64_t cost() const { return units * length; }
+  int32_t units, length;  // what its workers have to do, and the granules of each
+  __device__ __forceinline__ int32_t cost() const { return units * length; }
+  __device__ __forceinline__ void set(const TreeParams &p, int32_t first, int32_t nodes,
+                                      int32_t context) {
+    q0 = first;
+    n = nodes;
+    L = context;
+    const int tiles = (p.chunks_of(n) + kChunks - 1) / kChunks;
+    units = p.per_tile * (p.at_once == 1 ? tiles : (tiles + p.at_once - 1) / p.at_once);
+    length = max(1, (L + kGranule - 1) / kGranule);
+  }
 };
-__device__ __forceinline__ Seq sequence(const FlashParams &f, int b, bool record) {
-  const TreeParams &p = f.t;
+__device__ __forceinline__ Seq sequence(const TreeParams &p, int b, bool record) {
   Seq s{};
   const int64_t c0 = ld_global_s32(p.cu + b), c1 = ld_global_s32(p.cu + b + 1);
   const int64_t L = ld_global_s32(p.context_lens + b);
@@ -231,13 +237,7 @@ __device__ __forceinline__ Seq sequence(const FlashParams &f, int b, bool record
   if (n == 0) return s;
   const bool ok = L >= n && L <= p.max_context && L <= (int64_t)p.table_width * p.block_size;
   if (!ok && record) record_error(p.err, PKV_DEVERR_CONTEXT_RANGE);
-  s.q0 = (int32_t)c0;
-  s.n = (int32_t)n;
-  s.L = ok ? (int32_t)L : 0;
-  const int chunks = (s.n + f.nb - 1) / f.nb * f.parts;
-  const int per = kChunks * f.group;
-  s.units = (int64_t)p.hkv * ((chunks + per - 1) / per);
-  s.length = max(1, (s.L + kGranule - 1) / kGranule);
+  s.set(p, (int32_t)c0, (int32_t)n, ok ? (int32_t)L : 0);
   return s;
 }
 
@@ -250,9 +250,10 @@ __device__ __forceinline__ uint64_t mask_word(const TreeParams &p, int64_t row, 
 
 // V rows of the nodes that a row sees may hold values that are not finite, which the products left
 // out: what they add up to replaces the row's result. dims [d0, d0 + count), count a multiple of 4.
+template <Mode M>
 __device__ __forceinline__ void not_finite_fix(const TreeParams &p, int b, int h, int n, int L,
-                                            int64_t row, int node, uint16_t *out, int d0,
-                                            int count) {
+                                               int64_t row, int node, uint16_t *out, int d0,
+                                               int count) {
 #pragma unroll 1
   for (int d = d0; d < d0 + count; d += 4) {
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
@@ -263,8 +264,15 @@ __device__ __forceinline__ void not_finite_fix(const TreeParams &p, int b, int h
       const int64_t blk = p.block_tables[(int64_t)b * p.table_width + pos / p.block_size];
       if (blk < 0 || blk >= p.num_blocks) continue;
       const int64_t at = ((blk * p.block_size + pos % p.block_size) * p.hkv + h) * kD + d;
-      const uint2 w = *reinterpret_cast<const uint2 *>(p.v_cache + 2 * at);
-      const float x[4] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
+      float x[4];
+      if constexpr (M == kFp8) {
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(p.v_cache + at);
+        const float2 lo = f16x2_to_f32(cvt_f16x2_e4m3x2(w)), hi = f16x2_to_f32(cvt_f16x2_e4m3x2_hi(w));
+        x[0] = lo.x, x[1] = lo.y, x[2] = hi.x, x[3] = hi.y;
+      } else {
+        const uint2 w = *reinterpret_cast<const uint2 *>(p.v_cache + 2 * at);
+        x[0] = bf16_lo(w.x), x[1] = bf16_hi(w.x), x[2] = bf16_lo(w.y), x[3] = bf16_hi(w.y);
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (!isfinite(x[i])) sum[i] += x[i];
@@ -277,33 +285,33 @@ __device__ __forceinline__ void not_finite_fix(const TreeParams &p, int b, int h
 
 // Walks a worker's part of the axis, one item at a time (one thread).
 struct Walk {
-  int64_t x, x1, at;  // where the walk is, where the part ends, where sequence b starts
+  int32_t x, x1, at;  // where the walk is, where the part ends, where sequence b starts
   int b;
   Seq s;
-  __device__ __forceinline__ bool next(const FlashParams &f, int rank, Item &it, int64_t &unit,
-                                       int64_t &off) {
+  __device__ __forceinline__ bool next(const TreeParams &p, int head, int row_tile, Item &it,
+                                       int32_t &unit) {
     while (x < x1) {
       while (x >= at + s.cost()) {
         at += s.cost();
-        s = sequence(f, ++b, false);
+        s = sequence(p, ++b, false);
       }
-      const int64_t rel = x - at;
-      const int64_t u = rel / s.length;
-      off = rel - u * s.length;
-      const int64_t take = min(s.length - off, x1 - x);
+      const int32_t rel = x - at;
+      const int32_t u = s.units == 1 ? 0 : rel / s.length;
+      const int32_t off = rel - u * s.length;
+      const int32_t take = min(s.length - off, x1 - x);
       unit = x - off;
       x += take;
-      const int chunks = (s.n + f.nb - 1) / f.nb * f.parts;
+      const int tile = u < p.per_tile ? 0 : u / p.per_tile;
       it.last = 0;
       it.b = b;
-      it.h = (int32_t)(u % f.t.hkv);
+      it.h = (u - tile * p.per_tile) * p.heads + head;
       it.q0 = s.q0;
       it.n = s.n;
       it.L = s.L;
-      it.c0 = ((int32_t)(u / f.t.hkv) * f.group + rank) * kChunks;
-      it.chunks = min(kChunks, chunks - it.c0);
-      it.key0 = (int32_t)min((int64_t)s.L, off * kGranule);
-      it.key1 = (int32_t)min((int64_t)s.L, (off + take) * kGranule);
+      it.c0 = (tile * p.at_once + row_tile) * kChunks;
+      it.chunks = min(kChunks, p.chunks_of(s.n) - it.c0);
+      it.key0 = min(s.L, off * kGranule);
+      it.key1 = (int32_t)min((int64_t)s.L, (int64_t)(off + take) * kGranule);
       it.tiles = (it.key1 - it.key0 + kTile - 1) / kTile;
       it.to = off > 0 ? 0 : take < s.length ? 1 : 2;
       if (it.chunks > 0) return true;  // (this CTA's row tile of a smaller tree is empty)
@@ -312,55 +320,94 @@ struct Walk {
   }
 };
 
-// First pool row of the granule at position pos; a bad block id is flagged and gives a row wholly
-// outside the pool (TMA fills zeros). The block id is read once per block.
-struct RowOf {
-  int32_t at = -1;
-  int64_t blk = -1;
-  __device__ __forceinline__ int32_t operator()(const TreeParams &p, int b, int32_t pos) {
-    const int32_t i = pos / p.block_size;
-    if (i != at) {
-      at = i;
-      blk = ld_global_s32(p.block_tables + (int64_t)b * p.table_width + i);
-      if (blk < 0 || blk >= p.num_blocks) {
-        record_error(p.err, PKV_DEVERR_BLOCK_RANGE);
-        blk = -1;
-      }
+// First pool rows of an item's granules, one after the other; a bad block id is flagged and gives a
+// row wholly outside the pool (TMA fills zeros). A block's id is read once.
+struct Rows {
+  const int32_t *next_id;
+  int32_t blk, in_block;
+  __device__ __forceinline__ void read(const TreeParams &p) {
+    blk = ld_global_s32(next_id++);
+    if (blk < 0 || blk >= p.num_blocks) {
+      record_error(p.err, PKV_DEVERR_BLOCK_RANGE);
+      blk = -1;
     }
-    return blk < 0 ? -2 * kTile : (int32_t)(blk * p.block_size + pos % p.block_size);
+  }
+  __device__ __forceinline__ void start(const TreeParams &p, int b, int32_t pos) {
+    const int32_t i = pos / p.block_size;
+    next_id = p.block_tables + (int64_t)b * p.table_width + i;
+    in_block = pos - i * p.block_size;
+    read(p);
+  }
+  __device__ __forceinline__ int32_t next(const TreeParams &p) {
+    if (in_block == p.block_size) {
+      in_block = 0;
+      read(p);
+    }
+    const int32_t row = blk < 0 ? -2 * kTile : blk * p.block_size + in_block;
+    in_block += kGranule;
+    return row;
   }
 };
 
-__device__ __forceinline__ const Item *wait_item(TreeSmem &sm, uint32_t taken, unsigned int *err) {
+template <class Smem>
+__device__ __forceinline__ const Item *wait_item(Smem &sm, uint32_t taken, unsigned int *err) {
   const int slot = taken % kRing;
   return __all_sync(kFull, wait_parity(&sm.item_full[slot], (taken / kRing) & 1, err))
              ? &sm.items[slot]
              : nullptr;
 }
-__device__ __forceinline__ void release_item(TreeSmem &sm, uint32_t taken, int lane) {
+template <class Smem>
+__device__ __forceinline__ void release_item(Smem &sm, uint32_t taken, int lane) {
   __syncwarp();
   if (lane == 0) mbar_arrive(&sm.item_empty[taken % kRing]);
 }
 
+// Sixteen e4m3 codes as fp16, in two 16-byte pieces.
+__device__ __forceinline__ void widen16(const uint4 x, uint4 &lo, uint4 &hi) {
+  lo = make_uint4(cvt_f16x2_e4m3x2(x.x), cvt_f16x2_e4m3x2_hi(x.x), cvt_f16x2_e4m3x2(x.y),
+                  cvt_f16x2_e4m3x2_hi(x.y));
+  hi = make_uint4(cvt_f16x2_e4m3x2(x.z), cvt_f16x2_e4m3x2_hi(x.z), cvt_f16x2_e4m3x2(x.w),
+                  cvt_f16x2_e4m3x2_hi(x.w));
+}
+// whether four codes hold a NaN; and the codes with NaNs replaced by zero
+__device__ __forceinline__ bool has_nan4(uint32_t w) {
+  return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
+}
+__device__ __forceinline__ uint32_t no_nan4(uint32_t w) {
+  return w & ~__vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <Mode M>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_flash_kernel(const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap,
-                      const __grid_constant__ FlashParams f) {
-  const TreeParams &p = f.t;
+                      const __grid_constant__ TreeParams p) {
+  constexpr bool F8 = M == kFp8;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   extern __shared__ uint8_t smem_raw[];
-  TreeSmem &sm = *reinterpret_cast<TreeSmem *>(
+  TreeSmem<M> &sm = *reinterpret_cast<TreeSmem<M> *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   if (tid == 0) {
-    for (int i = 0; i < kKSlots; ++i) {
-      mbar_init(&sm.k_full[i], 1);
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&sm.k_full[i], F8 ? 2 : 1);  // (8-bit: two warps widen K, two V)
       mbar_init(&sm.k_empty[i], 1);
-    }
-    for (int i = 0; i < kVSlots; ++i) {
-      mbar_init(&sm.v_full[i], 1);
+      mbar_init(&sm.v_full[i], F8 ? 2 : 1);
       mbar_init(&sm.v_empty[i], 1);
-      mbar_init(&sm.v_fixed[i], 1);
+      mbar_init(&sm.v_ready[i], 1);
+      mbar_init(&sm.v_fixed[i], 4);
     }
+    if constexpr (F8)
+      for (int i = 0; i < kRawSlots; ++i) {
+        mbar_init(&sm.raw.k_full[i], 1);
+        mbar_init(&sm.raw.k_empty[i], 2);
+        mbar_init(&sm.raw.v_full[i], 1);
+        mbar_init(&sm.raw.v_empty[i], 2);
+      }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.q_full[i], 4);
       mbar_init(&sm.q_empty[i], 1);
@@ -373,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&sm.item_full[i], 1);
       mbar_init(&sm.item_empty[i], kItemConsumers);
-      mbar_init(&sm.scanned[i], 1);
+      mbar_init(&sm.scanned[i], 4);
     }
     sm.start_b = 0;
     sm.start_at = 0;
@@ -385,62 +432,82 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&sm.tmem_base, kTmemCols);
     tmem_relinquish();
   }
+  const int worker = blockIdx.x / p.group, rank = blockIdx.x - worker * p.group;
+  const int rank_tile = p.at_once == 1 ? 0 : rank / p.heads;
+  const int rank_head = rank - rank_tile * p.heads;
   // everything above may overlap the stream's previous kernel
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  // The axis: every sequence's granules, summed over the batch. Thread t adds up one sequence of
-  // every kThreads; the sequence that the worker's part starts in is found on the way when the
-  // batch fits the block, else by a second pass.
-  const int worker = blockIdx.x / f.group, rank = blockIdx.x % f.group;
-  auto scan = [&](int base, int64_t &mine) -> int64_t {  // exclusive prefix; sm.total: the sum
-    const int b = base + tid;
-    mine = b < p.num_seqs ? sequence(f, b, blockIdx.x == 0).cost() : 0;
-    int64_t x = mine;
+  // The axis: every sequence's granules, summed over the batch. Up to 32 sequences are one to a
+  // lane, and each warp scans them by itself; else one to a thread, kThreads at a time. The
+  // sequence that the worker's part starts in is found on the way when the batch is scanned at
+  // once, else by a second pass.
+  const bool stop = tid == 0 && aborted(p.err);
+  Seq own{};
+  int32_t mine = 0, prefix = 0, total = 0;
+  auto warp_scan = [&](int b, bool record) -> int32_t {  // inclusive, over the warp
+    own = Seq{};
+    if (b < p.num_seqs) own = sequence(p, b, record);
+    mine = own.cost();
+    int32_t x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(kFull, x, o);
+      const int32_t y = __shfl_up_sync(kFull, x, o);
       if (lane >= o) x += y;
     }
+    return x;
+  };
+  auto block_scan = [&](int base) -> int32_t {  // exclusive, over the block; its sum to sm.total
+    const int32_t x = warp_scan(base + tid, blockIdx.x == 0);
     __syncthreads();
     if (lane == 31) sm.warp_sums[warp] = x;
     __syncthreads();
-    int64_t before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) before += sm.warp_sums[w];
-      all += sm.warp_sums[w];
-    }
+    const int32_t v = lane < kThreads / 32 ? sm.warp_sums[lane] : 0;
+    const int32_t before = __reduce_add_sync(kFull, lane < warp ? v : 0);
+    const int32_t all = __reduce_add_sync(kFull, v);
     if (tid == 0) sm.total = all;
     return before + x - mine;
   };
-  int64_t total = 0, mine = 0, prefix = 0;
-  for (int base = 0; base < p.num_seqs; base += kThreads) {
-    prefix = scan(base, mine);
-    __syncthreads();
-    total += sm.total;
-  }
-  const int64_t workers = min((int64_t)f.workers, total);
-  const bool works = worker < workers;
-  const int64_t x0 = works ? worker * total / workers : 0;
-  const int64_t x1 = works ? (worker + 1) * total / workers : 0;
-  if (p.num_seqs <= kThreads) {
-    if (mine > 0 && prefix <= x0 && x0 < prefix + mine) {
-      sm.start_b = tid;
-      sm.start_at = prefix;
-    }
+  const bool one_warp = p.num_seqs <= 32;
+  if (one_warp) {
+    const int32_t x = warp_scan(lane, blockIdx.x == 0 && warp == 0);
+    total = __shfl_sync(kFull, x, 31);
+    prefix = x - mine;
   } else {
-    int64_t carry = 0;
     for (int base = 0; base < p.num_seqs; base += kThreads) {
-      prefix = carry + scan(base, mine);
-      if (mine > 0 && prefix <= x0 && x0 < prefix + mine) {
-        sm.start_b = base + tid;
-        sm.start_at = prefix;
-      }
+      prefix = block_scan(base);
+      __syncthreads();
+      total += sm.total;
+    }
+  }
+  const int32_t workers = min(p.workers, total);
+  const bool works = worker < workers;
+  const int32_t each = works ? total / workers : 0, rest = total - each * workers;
+  const int32_t x0 = works ? TreeParams::part_start(worker, each, rest) : 0;
+  const int32_t x1 = works ? TreeParams::part_start(worker + 1, each, rest) : 0;
+  auto found = [&](int b) {
+    if (mine > 0 && prefix <= x0 && x0 < prefix + mine) {
+      sm.start_b = b;
+      sm.start_at = prefix;
+      sm.start_q0 = own.q0;
+      sm.start_n = own.n;
+      sm.start_L = own.L;
+    }
+  };
+  if (one_warp) {
+    if (warp == kKWarp) found(lane);  // (the warp that needs it)
+  } else if (p.num_seqs <= kThreads) {
+    found(tid);
+  } else {
+    int32_t carry = 0;
+    for (int base = 0; base < p.num_seqs; base += kThreads) {
+      prefix = carry + block_scan(base);
+      found(base + tid);
       __syncthreads();
       carry += sm.total;
     }
   }
-  if (tid == 0) sm.stop = aborted(p.err) ? 1 : 0;
+  if (tid == 0) sm.stop = stop;
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -453,208 +520,312 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kKWarp) {
       // ------------------------------------------------------------ work walk and K loads
       if (lane == 0) {
-        const uint64_t policy = f.group == 1 ? policy_evict_first() : policy_evict_last();
+        const uint64_t policy = p.at_once == 1 ? policy_evict_first() : policy_evict_last();
         Walk w{x0, x1, sm.start_at, sm.start_b, {}};
-        if (works) w.s = sequence(f, w.b, false);
+        if (works) w.s.set(p, sm.start_q0, sm.start_n, sm.start_L);
         uint32_t pushed = 0, g = 0;
         bool ok = true;
-        CutInfo cut{};
-        // the next item is handed out before this one's tiles are loaded
-        Item it, nx;
-        int64_t unit, off;
-        auto push = [&](Item &d) -> bool {
-          const bool more = w.next(f, rank, d, unit, off);
-          if (!more) {
-            d = Item{};
-            d.last = 1;
-          }
-          const int slot = pushed % kRing;
-          if (pushed >= kRing && !wait_parity(&sm.item_empty[slot], ((pushed / kRing) - 1) & 1, p.err))
-            return false;
-          sm.items[slot] = d;
-          sm.dirty[slot] = 0;
-          mbar_arrive(&sm.item_full[slot]);
-          ++pushed;
-          return true;
-        };
-        ok = push(it);
-        // the first unit's cut, if it is that unit's first one: worker - 1 has the part before
-        if (ok && !it.last && it.to == 0 && unit + off == x0 &&
-            unit >= (worker - 1) * total / workers) {
-          const int64_t end = unit + w.s.length - 1;
-          cut.parts = (int32_t)(((end + 1) * workers - 1) / total) - worker + 2;
-          cut.b = it.b;
-          cut.h = it.h;
-          cut.q0 = it.q0;
-          cut.n = it.n;
-          cut.L = it.L;
-          cut.c0 = it.c0;
-          cut.chunks = it.chunks;
-        }
-        {
-          int4 *dst = reinterpret_cast<int4 *>(f.cuts + blockIdx.x);
-          dst[0] = make_int4(cut.parts, cut.b, cut.h, cut.q0);
-          dst[1] = make_int4(cut.n, cut.L, cut.c0, cut.chunks);
-        }
-        RowOf row_of;
-        int last_b = -1;
+        int32_t unit;
+        // An item is handed out while the one before it is loaded, after that one's second tile
+        // (the walk starts with an item of no tiles in hand).
+        Item it{}, nx;
+        Rows rows;
         while (ok && !it.last) {
-          ok = push(nx);
-          if (!ok) break;
-          if (it.b != last_b) row_of.at = -1;
-          last_b = it.b;
-          for (int j = 0; j < it.tiles; ++j, ++g) {
-            const int slot = g % kKSlots;
-            if (g >= kKSlots && !wait_parity(&sm.k_empty[slot], ((g / kKSlots) - 1) & 1, p.err)) {
-              ok = false;
-              break;
-            }
-            const int32_t pos = it.key0 + j * kTile;
-            const int granules = it.key1 - pos > kGranule ? 2 : 1;
-            mbar_arrive_expect_tx(&sm.k_full[slot], granules * 2 * kGranuleBytes);
-            for (int r = 0; r < granules; ++r) {
-              const int32_t row = row_of(p, it.b, pos + r * kGranule);
+          if (it.tiles > 0) rows.start(p, it.b, it.key0);
+          const int steps = max(1, it.tiles), push_at = min(1, steps - 1);
+          for (int j = 0; j < steps && ok; ++j) {
+            if (j < it.tiles) {
+              constexpr int kN = F8 ? kRawSlots : kSlots;
+              const int slot = g % kN;
+              uint64_t *full, *empty;
+              if constexpr (F8) full = &sm.raw.k_full[slot], empty = &sm.raw.k_empty[slot];
+              else full = &sm.k_full[slot], empty = &sm.k_empty[slot];
+              ok = g < kN || wait_parity(empty, ((g / kN) - 1) & 1, p.err);
+              if (!ok) break;  // (g counts the copies that were issued)
+              const int32_t pos = it.key0 + j * kTile;
+              const int granules = it.key1 - pos > kGranule ? 2 : 1;
+              if constexpr (!F8) mbar_arrive_expect_tx(full, granules * 2 * kGranuleBytes);
+              for (int r = 0; r < granules; ++r) {
+                const int32_t row = rows.next(p);
+                if constexpr (F8) {
+                  // with the granule's scales of K and V and those of three groups beside it (16
+                  // bytes); the zeros of a bad block have a scale of 1
+                  float(*dst)[4] = sm.raw.scale[g % kScaleTiles][r];
+                  const uint32_t bytes = row < 0 ? kGranuleBytes : kGranuleBytes + 32;
+                  if (row < 0)
+                    for (int e = 0; e < 8; ++e) dst[e >> 2][e & 3] = 1.f;
+                  if (r + 1 < granules) mbar_expect_tx(full, bytes);
+                  else mbar_arrive_expect_tx(full, bytes);
+                  tma_load_3d(sm.raw.k[slot] + r * kGranuleBytes, &kmap, full, 0, row, it.h, policy);
+                  if (row >= 0) {
+                    const int64_t at =
+                        ((int64_t)rows.blk * p.hkv + it.h) * (p.block_size / kFp8Group) +
+                        ((rows.in_block - kGranule) / kGranule & ~3);
+                    bulk_copy_g2s(dst[0], p.k_scale + at, 16, full);
+                    bulk_copy_g2s(dst[1], p.v_scale + at, 16, full);
+                  }
+                } else {
 #pragma unroll
-              for (int hf = 0; hf < 2; ++hf)
-                tma_load_3d(sm.k[slot] + hf * kPlane + r * kGranuleBytes, &kmap, &sm.k_full[slot], 0,
-                            row, 2 * it.h + hf, policy);
+                  for (int hf = 0; hf < 2; ++hf)
+                    tma_load_3d(sm.k[slot] + hf * kPlane + r * kGranuleBytes, &kmap, full, 0, row,
+                                2 * it.h + hf, policy);
+                }
+              }
+              ++g;
+            }
+            if (j == push_at) {
+              const bool more = w.next(p, rank_head, rank_tile, nx, unit);
+              if (!more) {
+                nx = Item{};
+                nx.last = 1;
+              }
+              const int slot = pushed % kRing;
+              ok = pushed < kRing ||
+                   wait_parity(&sm.item_empty[slot], ((pushed / kRing) - 1) & 1, p.err);
+              if (!ok) break;
+              sm.items[slot] = nx;
+              sm.dirty[slot] = 0;
+              mbar_arrive(&sm.item_full[slot]);
+              if (pushed++ == 0) {
+                // the first unit's cut, if it is that unit's first one: worker - 1 has the part
+                // before
+                CutInfo cut{};
+                if (more && nx.to == 0 && unit >= TreeParams::part_start(worker - 1, each, rest)) {
+                  cut.parts = TreeParams::part_of(unit + w.s.length - 1, each, rest) - worker + 2;
+                  cut.b = nx.b;
+                  cut.h = nx.h;
+                  cut.q0 = nx.q0;
+                  cut.n = nx.n;
+                  cut.L = nx.L;
+                  cut.c0 = nx.c0;
+                  cut.chunks = nx.chunks;
+                }
+                int4 *dst = reinterpret_cast<int4 *>(p.cuts + blockIdx.x);
+                dst[0] = make_int4(cut.parts, cut.b, cut.h, cut.q0);
+                dst[1] = make_int4(cut.n, cut.L, cut.c0, cut.chunks);
+              }
             }
           }
           it = nx;
         }
         // keep the CTA alive until every copy it issued has landed
+        constexpr uint32_t kN = F8 ? kRawSlots : kSlots;
         bool drained = true;
-        for (uint32_t t = g > kKSlots ? g - kKSlots : 0; drained && t < g; ++t)
-          drained = wait_own(&sm.k_full[t % kKSlots], (t / kKSlots) & 1, p.err);
+        for (uint32_t t = g > kN ? g - kN : 0; drained && t < g; ++t) {
+          if constexpr (F8) drained = wait_own(&sm.raw.k_full[t % kN], (t / kN) & 1, p.err);
+          else drained = wait_own(&sm.k_full[t % kN], (t / kN) & 1, p.err);
+        }
       }
       __syncwarp();
     } else if (warp == kVWarp) {
       // ------------------------------------------------------------ V loads
-      uint64_t policy = 0;
-      if (lane == 0) policy = f.group == 1 ? policy_evict_first() : policy_evict_last();
-      uint32_t taken = 0, g = 0;
-      bool ok = true;
-      RowOf row_of;
-      int last_b = -1;
-      while (ok) {
-        const Item *ip = wait_item(sm, taken, p.err);
-        if (!ip) break;
-        const Item it = *ip;
-        if (it.b != last_b) row_of.at = -1;
-        last_b = it.b;
-        const int root = it.L - it.n;
-        bool dirty = false;
-        for (int j = 0; j < it.tiles && ok && !it.last; ++j, ++g) {
-          const int slot = g % kVSlots;
-          const int32_t pos = it.key0 + j * kTile;
-          const int keys = min(kTile, it.key1 - pos);
-          if (lane == 0) {
-            if (g >= kVSlots) ok = wait_parity(&sm.v_empty[slot], ((g / kVSlots) - 1) & 1, p.err);
-            if (ok) {
-              const int granules = keys > kGranule ? 2 : 1;
-              mbar_arrive_expect_tx(&sm.v_full[slot], granules * 2 * kGranuleBytes);
-              for (int r = 0; r < granules; ++r) {
-                const int32_t row = row_of(p, it.b, pos + r * kGranule);
+      if (lane == 0) {
+        const uint64_t policy = p.at_once == 1 ? policy_evict_first() : policy_evict_last();
+        constexpr uint32_t kN = F8 ? kRawSlots : kSlots;
+        uint32_t taken = 0, g = 0;
+        bool ok = true;
+        Rows rows;
+        while (ok) {
+          const int ring = taken % kRing;
+          if (!wait_parity(&sm.item_full[ring], (taken / kRing) & 1, p.err)) break;
+          const Item it = sm.items[ring];
+          mbar_arrive(&sm.item_empty[ring]);
+          ++taken;
+          if (it.last) break;
+          if (it.tiles > 0) rows.start(p, it.b, it.key0);
+          for (int j = 0; j < it.tiles; ++j, ++g) {
+            const int slot = g % kN;
+            uint64_t *full, *empty;
+            if constexpr (F8) full = &sm.raw.v_full[slot], empty = &sm.raw.v_empty[slot];
+            else full = &sm.v_full[slot], empty = &sm.v_empty[slot];
+            ok = g < kN || wait_parity(empty, ((g / kN) - 1) & 1, p.err);
+            if (!ok) break;
+            const int32_t pos = it.key0 + j * kTile;
+            const int granules = it.key1 - pos > kGranule ? 2 : 1;
+            mbar_arrive_expect_tx(full, granules * (F8 ? kGranuleBytes : 2 * kGranuleBytes));
+            for (int r = 0; r < granules; ++r) {
+              const int32_t row = rows.next(p);
+              if constexpr (F8) {
+                tma_load_3d(sm.raw.v[slot] + r * kGranuleBytes, &vmap, full, 0, row, it.h, policy);
+              } else {
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf)
-                  tma_load_3d(sm.v[slot] + hf * kPlane + r * kGranuleBytes, &vmap,
-                              &sm.v_full[slot], 0, row, 2 * it.h + hf, policy);
+                  tma_load_3d(sm.v[slot] + hf * kPlane + r * kGranuleBytes, &vmap, full, 0, row,
+                              2 * it.h + hf, policy);
               }
             }
           }
-          ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
-          if (!ok) break;  // (g counts the copies that were issued)
-          if (pos + kTile > root) {
-            ok = __all_sync(kFull, wait_parity(&sm.v_full[slot], (g / kVSlots) & 1, p.err));
-            if (!ok) {
-              ++g;  // (its copies have been issued)
-              break;
-            }
-            // 16-byte pieces: those of nodes looked through, those past the keys zeroed
-            const int from = max(0, root - pos), up = (keys + 15) & ~15;
-            bool here = false;
-            for (int i = lane + from * 16; i < up * 16; i += 32) {
-              uint4 *w = reinterpret_cast<uint4 *>(sm.v[slot] + ((i & 15) >> 3) * kPlane +
-                                                   (i >> 4) * 128 + (i & 7) * 16);
-              if ((i >> 4) >= keys) {
-                *w = make_uint4(0, 0, 0, 0);
-              } else {
-                const uint4 x = *w;
-                const uint4 y = make_uint4(bf16x2_finite(x.x), bf16x2_finite(x.y),
-                                           bf16x2_finite(x.z), bf16x2_finite(x.w));
-                if (x.x != y.x || x.y != y.y || x.z != y.z || x.w != y.w) {
-                  *w = y;
-                  here = true;
-                }
-              }
-            }
-            dirty |= __any_sync(kFull, here);
-            fence_async_shared();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.v_fixed[slot]);
-          }
         }
-        const bool last = it.last;
-        if (lane == 0) {
-          if (dirty) sm.dirty[taken % kRing] = 1;
-          mbar_arrive(&sm.scanned[taken % kRing]);
-        }
-        release_item(sm, taken, lane);
-        ++taken;
-        if (last) break;
-      }
-      if (lane == 0) {
         bool drained = true;
-        for (uint32_t t = g > kVSlots ? g - kVSlots : 0; drained && t < g; ++t)
-          drained = wait_own(&sm.v_full[t % kVSlots], (t / kVSlots) & 1, p.err);
+        for (uint32_t t = g > kN ? g - kN : 0; drained && t < g; ++t) {
+          if constexpr (F8) drained = wait_own(&sm.raw.v_full[t % kN], (t / kN) & 1, p.err);
+          else drained = wait_own(&sm.v_full[t % kN], (t / kN) & 1, p.err);
+        }
       }
       __syncwarp();
     } else if (warp >= kQWarp0) {
-      // ------------------------------------------------------------ Q into tensor memory
-      // thread = TMEM lane: row (lane & 15) of chunk quad + 4 (lane / 16). A negative scale is
-      // taken out of the scores here, by the sign of q.
+      // ------------------------------------------------------------ Q; V looked through; codes
+      // For Q thread = TMEM lane: row (lane & 15) of chunk quad + 4 (lane / 16). A negative scale is
+      // taken out of the scores by the sign of q.
       const int quad = warp & 3, c = quad + 4 * (lane >> 4), r = lane & 15;
-      const int i = r / f.hb, group = p.hq / p.hkv;
-      uint32_t taken = 0, used = 0;
-      while (true) {
-        const Item *ip = wait_item(sm, taken, p.err);
-        if (!ip) break;
-        const int last = ip->last, tiles = ip->tiles, chunk = ip->c0 + c;
-        const bool store = quad < ip->chunks;  // (warp-uniform)
-        const int node = chunk / f.parts * f.nb + i;
-        const int head = (chunk % f.parts) * kChunkRows + r % f.hb;
-        const bool row = c < ip->chunks && i < f.nb && node < ip->n && head < group;
+      const int i = p.node_of(r), head_r = r - i * p.hb;
+      const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
+      uint32_t used = 0, g = 0, fix_parity = 0;
+      // Q of item k. `last`: there is none.
+      auto load_q = [&](uint32_t k, bool &last) -> bool {
+        const Item *ip = wait_item(sm, k, p.err);
+        if (!ip) return false;
+        last = ip->last;
+        if (last || ip->tiles == 0) return true;
+        const int chunk = ip->c0 + c;
+        const int node = p.first_node(chunk) + i, head = p.first_head(chunk) + head_r;
+        const bool row = c < ip->chunks && i < p.nb && node < ip->n && head < p.group_heads;
         const uint4 *src = reinterpret_cast<const uint4 *>(
-            p.q + (int64_t)(ip->q0 + node) * p.q_stride + (ip->h * group + head) * kD);
-        release_item(sm, taken, lane);
-        ++taken;
-        if (last) break;
-        if (tiles == 0) continue;
+            p.q + (int64_t)(ip->q0 + node) * p.q_stride + (ip->h * p.group_heads + head) * kD);
         const int buf = used & 1;
         if (used >= 2 &&
             !__all_sync(kFull, wait_parity(&sm.q_empty[buf], ((used >> 1) - 1) & 1, p.err)))
-          break;
+          return false;
         ++used;
         tc_fence_after_sync();
-        if (store) {
-#pragma unroll
+        if (quad < ip->chunks) {  // (warp-uniform)
+          float inv = 1.f;
+          if constexpr (F8) {
+            uint32_t top = 0;
+#pragma unroll 4
+            for (int e = 0; e < 16; ++e) {
+              const uint4 x = row ? ld_once_u4(src + e) : make_uint4(0, 0, 0, 0);
+              top = __vmaxu2(top, __vmaxu2(bf16x2_absmax(x.x, x.y), bf16x2_absmax(x.z, x.w)));
+            }
+            top = max(top & 0xffffu, top >> 16);
+            // the exponent of the largest |q| (of zeros and of what is not finite: some other)
+            const int e = min(max((int)(top >> 7) - 127, -120), 120);
+            inv = pow2f(-e);
+            sm.raw.q_power[k % kRing][c * kChunkRows + r] = (float)e;
+          }
+#pragma unroll 1
           for (int hf = 0; hf < 2; ++hf) {
             uint32_t w[32];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const uint4 x = row ? ld_once_u4(src + 8 * hf + k) : make_uint4(0, 0, 0, 0);
-              w[4 * k] = x.x ^ p.q_sign;
-              w[4 * k + 1] = x.y ^ p.q_sign;
-              w[4 * k + 2] = x.z ^ p.q_sign;
-              w[4 * k + 3] = x.w ^ p.q_sign;
+            for (int e = 0; e < 8; ++e) {
+              uint4 x = row ? ld_once_u4(src + 8 * hf + e) : make_uint4(0, 0, 0, 0);
+              x = make_uint4(x.x ^ p.q_sign, x.y ^ p.q_sign, x.z ^ p.q_sign, x.w ^ p.q_sign);
+              if constexpr (F8)
+                x = make_uint4(pack_f16x2(bf16_lo(x.x) * inv, bf16_hi(x.x) * inv),
+                               pack_f16x2(bf16_lo(x.y) * inv, bf16_hi(x.y) * inv),
+                               pack_f16x2(bf16_lo(x.z) * inv, bf16_hi(x.z) * inv),
+                               pack_f16x2(bf16_lo(x.w) * inv, bf16_hi(x.w) * inv));
+              w[4 * e] = x.x;
+              w[4 * e + 1] = x.y;
+              w[4 * e + 2] = x.z;
+              w[4 * e + 3] = x.w;
             }
-            tmem_st32(tmem + ((uint32_t)(quad * 32) << 16) + kQCol + 64 * buf + 32 * hf, w);
+            tmem_st32(lane_addr + kQCol + 64 * buf + 32 * hf, w);
           }
           tmem_st_wait();
         }
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.q_full[buf]);
+        return true;
+      };
+      bool last = false, ok = load_q(0, last);
+      for (uint32_t k = 0; ok && !last; ++k) {
+        const Item &it = sm.items[k % kRing];
+        const int tiles = it.tiles, key0 = it.key0, key1 = it.key1, root = it.L - it.n;
+        bool found = false;
+        if constexpr (F8) {
+          // Warps 12 and 13 widen K, 14 and 15 V: 16 codes of a row at a time, rows 8 apart in a
+          // quarter warp so that neither side has bank conflicts.
+          const bool is_v = warp >= kQWarp0 + 2;
+          const int part = warp & 1;  // the rows of granule 0 or 1
+          uint64_t *const raw_full = is_v ? sm.raw.v_full : sm.raw.k_full;
+          uint64_t *const raw_empty = is_v ? sm.raw.v_empty : sm.raw.k_empty;
+          uint64_t *const full = is_v ? sm.v_full : sm.k_full;
+          uint64_t *const empty = is_v ? sm.v_empty : sm.k_empty;
+          for (int j = 0; j < tiles && ok; ++j, ++g) {
+            // (the next item's Q before this one's last tile: it is needed right after)
+            if (j == tiles - 1) ok = load_q(k + 1, last);
+            const int raw = g % kRawSlots, slot = g % kSlots;
+            ok = ok && __all_sync(kFull, wait_parity(&raw_full[raw], (g / kRawSlots) & 1, p.err));
+            if (ok && g >= kSlots)
+              ok = __all_sync(kFull, wait_parity(&empty[slot], ((g / kSlots) - 1) & 1, p.err));
+            if (!ok) break;
+            const int pos = key0 + j * kTile, keys = min(kTile, key1 - pos);
+            const uint8_t *const src = (is_v ? sm.raw.v : sm.raw.k)[raw] + part * kGranuleBytes;
+            uint8_t *const dst = (is_v ? sm.v : sm.k)[slot] + part * kGranuleBytes;
+            const int rows_up = min(kGranule, ((keys + 15) & ~15) - part * kGranule);
+            const bool nodes = is_v && pos + kTile > root;
+#pragma unroll 2
+            for (int e = 0; e < rows_up; e += 8) {
+              const int row = e + (lane & 7);  // (rows past the keys: V's become zeros)
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                const int a = (lane >> 3) + 4 * z;  // 16 codes of it
+                uint4 x = *reinterpret_cast<const uint4 *>(src + row * 128 + ((a ^ (row & 7)) << 4));
+                if (nodes) {
+                  const int key = part * kGranule + row;
+                  if (key >= keys) x = make_uint4(0, 0, 0, 0);
+                  if (pos + key >= root &&
+                      (has_nan4(x.x) || has_nan4(x.y) || has_nan4(x.z) || has_nan4(x.w))) {
+                    x = make_uint4(no_nan4(x.x), no_nan4(x.y), no_nan4(x.z), no_nan4(x.w));
+                    found = true;
+                  }
+                }
+                uint4 lo, hi;
+                widen16(x, lo, hi);
+                uint8_t *const to = dst + (a >> 2) * kPlane + row * 128;
+                const int piece = 2 * (a & 3);
+                *reinterpret_cast<uint4 *>(to + ((piece ^ (row & 7)) << 4)) = lo;
+                *reinterpret_cast<uint4 *>(to + (((piece + 1) ^ (row & 7)) << 4)) = hi;
+              }
+            }
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&full[slot]);
+              mbar_arrive(&raw_empty[raw]);
+            }
+          }
+          if (tiles == 0) ok = load_q(k + 1, last);
+        } else {
+          ok = load_q(k + 1, last);
+          // The tiles that hold nodes (one that ends inside a step of 16 keys among them): nodes'
+          // rows looked through, 16 bytes at a time, rows past the keys zeroed, by the four warps.
+          // The PV warp says when such a tile has landed: it waits for all of them in turn.
+          const int t = tid - kQWarp0 * 32;
+          for (int j = max(0, (root - key0) / kTile); j < tiles && ok; ++j) {
+            const int pos = key0 + j * kTile, keys = min(kTile, key1 - pos);
+            if (pos + kTile <= root) continue;
+            const uint32_t slot = (g + j) % kSlots;
+            ok = __all_sync(kFull, wait_parity(&sm.v_ready[slot], (fix_parity >> slot) & 1, p.err));
+            if (!ok) break;
+            fix_parity ^= 1u << slot;
+            for (int e = t + max(0, root - pos) * 16; e < ((keys + 15) & ~15) * 16; e += 128) {
+              uint4 *w = reinterpret_cast<uint4 *>(sm.v[slot] + ((e & 15) >> 3) * kPlane +
+                                                   (e >> 4) * 128 + (e & 7) * 16);
+              if ((e >> 4) >= keys) {
+                *w = make_uint4(0, 0, 0, 0);
+                continue;
+              }
+              const uint4 x = *w;
+              const uint32_t top = __vmaxu2(bf16x2_absmax(x.x, x.y), bf16x2_absmax(x.z, x.w));
+              if (max(top & 0xffffu, top >> 16) >= 0x7f80u) {
+                *w = make_uint4(bf16x2_finite(x.x), bf16x2_finite(x.y), bf16x2_finite(x.z),
+                                bf16x2_finite(x.w));
+                found = true;
+              }
+            }
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.v_fixed[slot]);
+          }
+          g += tiles;
+        }
+        if (__any_sync(kFull, found) && lane == 0) sm.dirty[k % kRing] = 1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.scanned[k % kRing]);
+        release_item(sm, k, lane);
       }
     } else if (warp == kSWarp || warp == kPvWarp) {
       // ------------------------------------------------------------ UMMA issuers
@@ -678,53 +849,64 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (last) break;
         if (tiles == 0) continue;
         for (int j = 0; j < tiles && ok; ++j, ++g) {
-          const uint32_t sb = g & 1;
+          const uint32_t sb = g & 1, slot = g % kSlots;
           const int pos = key0 + j * kTile;
           const int steps = (min(kTile, key1 - pos) + 15) / 16;
           if (s_role) {  // S over as many columns as there are keys, in steps of 16
-            const uint32_t ks = g % kKSlots, qb = used & 1;
-            ok = wait_all(&sm.k_full[ks], (g / kKSlots) & 1);
+            const uint32_t qb = used & 1;
+            ok = wait_all(&sm.k_full[slot], (g / kSlots) & 1);
             if (ok && j == 0) ok = wait_all(&sm.q_full[qb], (used >> 1) & 1);
             // the buffer's previous P has been read by its PV
             if (ok && g >= 2) ok = wait_all(&sm.o_full[sb], ((g >> 1) - 1) & 1);
             if (!ok) break;
             tc_fence_after_sync();
             if (elect_one()) {
-              const uint32_t idesc = idesc_bf16_f32(128, 16 * steps, 0, 0);
-              const uint64_t dk = dk0 + ks * (kTileBytes >> 4);
+              const uint32_t idesc =
+                  F8 ? idesc_f16_f32(128, 16 * steps, 0, 0) : idesc_bf16_f32(128, 16 * steps, 0, 0);
+              const uint64_t dk = dk0 + slot * (kTileBytes >> 4);
 #pragma unroll
               for (int kk = 0; kk < kD / 16; ++kk)
                 umma_f16_ts(tmem + kSCol + 128 * sb, tmem + kQCol + 64 * qb + 8 * kk,
                             dk + (((kk >> 2) * kPlane + (kk & 3) * 32) >> 4), idesc, kk > 0);
               umma_commit(&sm.s_full[sb]);
-              umma_commit(&sm.k_empty[ks]);
+              umma_commit(&sm.k_empty[slot]);
               if (j == tiles - 1) umma_commit(&sm.q_empty[qb]);
             }
           } else {
-            const uint32_t vs = g % kVSlots;
-            const bool fix = pos + kTile > root;
-            ok = wait_all(&sm.p_full[sb], (g >> 1) & 1);
+            const bool nodes = !F8 && pos + kTile > root;
+            ok = wait_all(&sm.v_full[slot], (g / kSlots) & 1);
+            if (ok && nodes && lane == 0) mbar_arrive(&sm.v_ready[slot]);
+            if (ok) ok = wait_all(&sm.p_full[sb], (g >> 1) & 1);
             // the item's first PV overwrites O: the previous item's O must have been read
             if (ok && j == 0 && used > 0) ok = wait_all(&sm.o_free, (used - 1) & 1);
-            if (ok) ok = wait_all(&sm.v_full[vs], (g / kVSlots) & 1);
-            if (ok && fix) {
-              ok = wait_all(&sm.v_fixed[vs], (fix_parity >> vs) & 1);
-              fix_parity ^= 1u << vs;
+            if (ok && nodes) {
+              ok = wait_all(&sm.v_fixed[slot], (fix_parity >> slot) & 1);
+              fix_parity ^= 1u << slot;
             }
             if (!ok) break;
             tc_fence_after_sync();
             if (elect_one()) {
-              constexpr uint32_t kIdesc = idesc_bf16_f32(128, kD, 0, 1);  // V: MN-major
-              const uint64_t dv = dv0 + vs * (kTileBytes >> 4);
+              constexpr uint32_t kIdesc =  // V: MN-major
+                  F8 ? idesc_f16_f32(128, kD, 0, 1) : idesc_bf16_f32(128, kD, 0, 1);
+              const uint64_t dv = dv0 + slot * (kTileBytes >> 4);
               const uint32_t pc = tmem + kSCol + 128 * sb;
-              for (int kk = 0; kk < steps; ++kk) {
+              auto step = [&](int kk) {
                 umma_f16_ts(tmem + kOCol, pc + 8 * kk, dv + ((kk * 16 * 128) >> 4), kIdesc,
                             j > 0 || kk > 0);
-                umma_f16_ts(tmem + kOCol, pc + 64 + 8 * kk, dv + ((kk * 16 * 128) >> 4), kIdesc,
-                            true);
+                if constexpr (M == kTwoParts)
+                  umma_f16_ts(tmem + kOCol, pc + 64 + 8 * kk, dv + ((kk * 16 * 128) >> 4), kIdesc,
+                              true);
+              };
+              // (in a loop an issue takes 67 cycles, about as long as the product)
+              if (steps == kTile / 16) {
+#pragma unroll
+                for (int kk = 0; kk < kTile / 16; ++kk) step(kk);
+              } else {
+#pragma unroll 1
+                for (int kk = 0; kk < steps; ++kk) step(kk);
               }
               umma_commit(&sm.o_full[sb]);
-              umma_commit(&sm.v_empty[vs]);
+              umma_commit(&sm.v_empty[slot]);
             }
           }
           __syncwarp();
@@ -737,38 +919,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       __all_sync(kFull, wait_own(bar, 0, p.err));
     } else {
-      // ------------------------------------------------------------ softmax warps
+      // ------------------------------------------------------------ softmax and epilogue
       asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-      const int c = warp, ch = lane >> 4, r = lane & 15;  // chunk, column half, row
+      const int c = warp, ch = lane >> 4, r = lane & 15;  // chunk, half of the keys, row
       const uint32_t lane_addr = tmem + ((uint32_t)((c & 3) * 32 + (c >> 2) * 16) << 16);
-      const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
-      const int i = r / f.hb, group = p.hq / p.hkv;
+      const int i = p.node_of(r), head_r = r - i * p.hb;
       uint32_t taken = 0, g = 0;
       bool ok = true;
       while (ok) {
         const Item *ip = wait_item(sm, taken, p.err);
-        if (!ip) break;
-        if (ip->last) {
-          release_item(sm, taken, lane);
-          break;
-        }
-        const int tiles = ip->tiles, key0 = ip->key0, key1 = ip->key1, root = ip->L - ip->n;
+        if (!ip || ip->last) break;
+        const int ring = taken % kRing;
+        const int tiles = ip->tiles, key0 = ip->key0, key1 = ip->key1, n = ip->n, root = ip->L - n;
         const bool mine = c < ip->chunks;  // (warp-uniform)
-        const int chunk = ip->c0 + c, node = chunk / f.parts * f.nb + i;
+        const int chunk = ip->c0 + c, node = p.first_node(chunk) + i;
+        const int head = p.first_head(chunk) + head_r;
         const int64_t q_row = (int64_t)ip->q0 + node;
-        const int head = (chunk % f.parts) * kChunkRows + r % f.hb;
-        const bool row = mine && i < f.nb && node < ip->n && head < group;
+        const bool row = mine && i < p.nb && node < n && head < p.group_heads;
+        uint16_t *const dst = p.out + (q_row * p.hq + ip->h * p.group_heads + head) * kD + 64 * ch;
         if (tiles == 0) {  // nothing to see: zeros
-          if (row) {
-            uint4 *dst = reinterpret_cast<uint4 *>(
-                p.out + (q_row * p.hq + ip->h * group + head) * kD + 64 * ch);
-            for (int k = 0; k < 8; ++k) dst[k] = make_uint4(0, 0, 0, 0);
-          }
+          if (row)
+            for (int k = 0; k < 8; ++k) reinterpret_cast<uint4 *>(dst)[k] = make_uint4(0, 0, 0, 0);
           release_item(sm, taken, lane);
           ++taken;
           continue;
         }
-        float m_run = -INFINITY, l_run = 0.f;
+        // what the row sees of its tree's first 64 nodes, loaded ahead of the tiles that need it
+        const uint64_t first_word = row && key1 > root ? mask_word(p, q_row, node, 0) : 0;
+        auto word = [&](int w) -> uint64_t {
+          return w == 0 ? first_word : row && 64 * w < n ? mask_word(p, q_row, node, w) : 0;
+        };
+        float m_run = -INFINITY, l_run = 0.f, row_scale = p.scale_log2;
         for (int j = 0; j < tiles; ++j, ++g) {
           const uint32_t sb = g & 1, s_col = kSCol + 128 * sb;
           // warp-uniform results: the TMEM loads and stores below are .sync.aligned
@@ -776,43 +957,47 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           if (mine) {
             tc_fence_after_sync();
-            // the keys of this thread's half that the row sees
+            uint32_t x[8][8];  // keys 64 ch + 8 k + e
+            tmem_ld16x2<64>(lane_addr + s_col, x);
             const int pos = key0 + j * kTile + 64 * ch;
-            uint64_t sees = ~0ull;
-            if (pos + 64 > key1) sees = pos >= key1 ? 0 : ~0ull >> (64 - (key1 - pos));
-            if (pos + 64 > root && sees != 0) {
-              const int base = pos - root, w = base >> 6, sh = base & 63;  // (w = -1 before the root)
-              uint64_t bits = w < 0 ? ~0ull : row ? mask_word(p, q_row, node, w) : 0;
-              if (sh) {
-                const uint64_t up = row ? mask_word(p, q_row, node, w + 1) : 0;
-                bits = bits >> sh | up << (64 - sh);
-              }
-              sees &= bits;
-            }
-            uint32_t x[2][32];  // keys 64 ch + 32 k + e
-#pragma unroll
-            for (int k = 0; k < 2; ++k) tmem_ld16x2_32<64>(lane_addr + s_col + 32 * k, x[k]);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) tmem_ld_wait(x[k]);
-            if (sees != ~0ull) {
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const uint32_t bits = (uint32_t)(sees >> 32 * k);
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (!(bits >> e & 1)) x[k][e] = __float_as_uint(-INFINITY);
+            // 8-bit cache: the group's scales (a group past the keys has none)
+            float factor = row_scale, v_log2 = 0.f, per_v = 1.f;
+            if constexpr (F8) {
+              if (j == 0)
+                row_scale = factor = p.scale_log2 * pow2f((int)sm.raw.q_power[ring][c * kChunkRows + r]);
+              if (pos < key1) {
+                const float(*sc)[4] = sm.raw.scale[g % kScaleTiles][ch];
+                factor = fmaxf(factor * sc[0][pos / kGranule & 3], 1e-38f);  // (see scale_log2)
+                const float v = sc[1][pos / kGranule & 3];
+                v_log2 = log2_approx(v) + kOffset8;
+                per_v = 1.f / (v * (1 << kOffset8));
               }
             }
-            float mx[2];
+            // the keys of this thread's that the row sees
+            if (pos + 64 > min(key1, root)) {
+              uint64_t sees = pos >= key1 ? 0 : pos + 64 > key1 ? ~0ull >> (64 - (key1 - pos)) : ~0ull;
+              if (pos + 64 > root && sees != 0) {
+                const int base = pos - root, w = base >> 6, sh = base & 63;  // (w = -1: before the root)
+                uint64_t bits = w < 0 ? ~0ull : word(w);
+                if (sh) bits = bits >> sh | word(w + 1) << (64 - sh);
+                sees &= bits;
+              }
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              mx[k] = -INFINITY;
+              for (int k = 0; k < 8; ++k)
 #pragma unroll
-              for (int e = 0; e < 32; e += 2)
-                mx[k] = fmax3(mx[k], __uint_as_float(x[k][e]), __uint_as_float(x[k][e + 1]));
+                for (int e = 0; e < 8; ++e)
+                  if (!((uint32_t)(sees >> (32 * (k / 4))) >> (8 * (k & 3) + e) & 1))
+                    x[k][e] = __float_as_uint(-INFINITY);
             }
-            float m_tile = fmaxf(mx[0], mx[1]);
-            m_tile = fmaxf(m_tile, __shfl_xor_sync(kFull, m_tile, 16)) * p.scale_log2;
+            float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+#pragma unroll
+              for (int e = 0; e < 8; e += 2)
+                mx[k & 1] = fmax3(mx[k & 1], __uint_as_float(x[k][e]), __uint_as_float(x[k][e + 1]));
+            float m_tile = fmaxf(mx[0], mx[1]) * factor;
+            if constexpr (F8) m_tile += v_log2 - kOffset8;
+            m_tile = fmaxf(m_tile, __shfl_xor_sync(kFull, m_tile, 16));
             const float m_new = fmaxf(m_run, m_tile);
             const bool rescale = m_new > m_run + kRescaleLog2;
             float alpha = 1.f;
@@ -821,7 +1006,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               m_run = m_new;
               l_run *= alpha;
             }
-            const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
+            const float offset = v_log2 - (m_run == -INFINITY ? 0.f : m_run);
             // O holds the item's tiles before this one: rescale it (never on the first tile)
             if (j > 0 && __any_sync(kFull, rescale)) {
               ok = __all_sync(kFull, wait_parity(&sm.o_full[(g - 1) & 1], ((g - 1) >> 1) & 1, p.err));
@@ -837,29 +1022,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_st16x2_32<64>(lane_addr + kOCol + 32 * k, o);
               }
             }
-            // P = hi + lo, two keys to a column: hi over the first 64 columns of S, lo over the
-            // rest (this warp has read all of its rows' S)
-            const float2 nm2 = make_float2(neg_m, neg_m);
+            // P, two keys to a column, over the first half of S; a second part over the rest (this
+            // warp has read its rows' S)
+            const float2 mul2 = make_float2(factor, factor), add2 = make_float2(offset, offset);
             float2 rs0 = make_float2(0.f, 0.f), rs1 = make_float2(0.f, 0.f);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               uint32_t hi[8], lo[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                const int at = 16 * (k & 1) + 2 * e;
-                const float2 t = ffma2(make_float2(__uint_as_float(x[k >> 1][at]),
-                                                   __uint_as_float(x[k >> 1][at + 1])), sl2, nm2);
+                const float2 t = ffma2(
+                    make_float2(__uint_as_float(x[2 * k + e / 4][2 * e % 8]),
+                                __uint_as_float(x[2 * k + e / 4][2 * e % 8 + 1])), mul2, add2);
                 const float2 pe = make_float2(fast_exp2(t.x), fast_exp2(t.y));
                 if (e & 1) rs1 = fadd2(rs1, pe);
                 else rs0 = fadd2(rs0, pe);
-                hi[e] = pack_bf16x2(pe.x, pe.y);
-                lo[e] = pack_bf16x2(pe.x - bf16_lo(hi[e]), pe.y - bf16_hi(hi[e]));
+                if constexpr (F8) {
+                  hi[e] = pack_f16x2(pe.x, pe.y);
+                } else {
+                  hi[e] = pack_bf16x2(pe.x, pe.y);
+                  if constexpr (M == kTwoParts)
+                    lo[e] = pack_bf16x2(pe.x - bf16_lo(hi[e]), pe.y - bf16_hi(hi[e]));
+                }
               }
-              tmem_st16x2_8<32>(lane_addr + s_col + 8 * k, hi);
-              tmem_st16x2_8<32>(lane_addr + s_col + 64 + 8 * k, lo);
+              tmem_st16x2<32>(lane_addr + s_col + 8 * k, hi);
+              if constexpr (M == kTwoParts) tmem_st16x2<32>(lane_addr + s_col + 64 + 8 * k, lo);
             }
             tmem_st_wait();
-            l_run += (rs0.x + rs0.y) + (rs1.x + rs1.y);
+            l_run += ((rs0.x + rs0.y) + (rs1.x + rs1.y)) * per_v;
             tc_fence_before_sync();
           }
           __syncwarp();
@@ -869,10 +1059,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // O, once the last PV is done
         const Item &it = *ip;
         const float l = l_run + __shfl_xor_sync(kFull, l_run, 16);
-        if (!__all_sync(kFull, wait_parity(&sm.o_full[(g - 1) & 1], ((g - 1) >> 1) & 1, p.err)))
-          break;
+        ok = __all_sync(kFull, wait_parity(&sm.o_full[(g - 1) & 1], ((g - 1) >> 1) & 1, p.err) &&
+                                   wait_parity(&sm.scanned[ring], (taken / kRing) & 1, p.err));
+        if (!ok) break;
+        const bool dirty = sm.dirty[ring] != 0;
         tc_fence_after_sync();
-        uint32_t o[2][32];
+        uint32_t o[2][32];  // dims 64 ch + 32 k + e
         if (mine) {
 #pragma unroll
           for (int k = 0; k < 2; ++k) tmem_ld16x2_32<64>(lane_addr + kOCol + 32 * k, o[k]);
@@ -882,48 +1074,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.o_free);
-        if (!__all_sync(kFull, wait_parity(&sm.scanned[taken % kRing],
-                                           (taken / kRing) & 1, p.err)))
-          break;
-        const bool dirty = sm.dirty[taken % kRing] != 0;
-        const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // (NaN stays)
-        if (it.to == 2) {
-          if (row) {
-            uint16_t *dst = p.out + ((int64_t)(it.q0 + node) * p.hq + it.h * group + head) * kD;
+        // (NaN stays; a row that sees nothing gets zeros)
+        float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
+        if constexpr (F8) inv *= 1.f / (1 << kOffset8);
+        const int64_t slot = 2 * (int64_t)blockIdx.x + it.to;
+        if (it.to < 2 && warp == 0 && lane == 0) p.cuts[blockIdx.x].dirty[it.to] = dirty;
+        if (row && it.to == 2) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t w[8];
+          for (int k = 0; k < 4; ++k) {
+            uint32_t w[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                w[e] = pack_bf16x2(__uint_as_float(o[k >> 1][16 * (k & 1) + 2 * e]) * inv,
-                                   __uint_as_float(o[k >> 1][16 * (k & 1) + 2 * e + 1]) * inv);
-              uint4 *d = reinterpret_cast<uint4 *>(dst + 64 * ch + 16 * k);
-              if (f.out_32b) {
-                st_global_32b(d, w);
-              } else {
-                d[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                d[1] = make_uint4(w[4], w[5], w[6], w[7]);
-              }
+            for (int e = 0; e < 8; ++e)
+              w[e] = pack_bf16x2(__uint_as_float(o[k >> 1][16 * (k & 1) + 2 * e]) * inv,
+                                 __uint_as_float(o[k >> 1][16 * (k & 1) + 2 * e + 1]) * inv);
+            uint4 *d = reinterpret_cast<uint4 *>(dst + 16 * k);
+            if (p.out_32b) {
+              st_global_32b(d, w);
+            } else {
+              d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+              d[1] = make_uint4(w[4], w[5], w[6], w[7]);
             }
-            if (dirty)
-              not_finite_fix(p, it.b, it.h, it.n, it.L, it.q0 + node, node, dst, 64 * ch, 64);
           }
-        } else {
-          const int64_t slot = 2 * (int64_t)blockIdx.x + it.to;
-          if (row) {
-            const int64_t at = slot * f.part_rows + c * kChunkRows + r;
-            float *dst = f.part_o + at * kD + 64 * ch;
+          if (dirty) not_finite_fix<M>(p, it.b, it.h, n, it.L, q_row, node, dst - 64 * ch, 64 * ch, 64);
+        } else if (row) {
+          const int64_t at = slot * p.part_rows + c * kChunkRows + r;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              uint32_t w[8];
+          for (int k = 0; k < 8; ++k) {
+            uint32_t w[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                w[e] = __float_as_uint(__uint_as_float(o[k >> 2][8 * (k & 3) + e]) * inv);
-              st_global_32b(dst + 8 * k, w);
-            }
-            if (ch == 0) f.part_lse[at] = l > 0.f ? m_run + log2_approx(l) : l == 0.f ? -INFINITY : l;
+            for (int e = 0; e < 8; ++e)
+              w[e] = __float_as_uint(__uint_as_float(o[k >> 2][8 * (k & 3) + e]) * inv);
+            st_global_32b(p.part_o + at * kD + 64 * ch + 8 * k, w);
           }
-          if (warp == 0 && lane == 0) f.cuts[blockIdx.x].dirty[it.to] = dirty;
+          if (ch == 0) p.part_lse[at] = l > 0.f ? m_run + log2_approx(l) : l == 0.f ? -INFINITY : l;
         }
         release_item(sm, taken, lane);
         ++taken;
@@ -941,27 +1124,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Merges the parts of the units that a cut between two workers went through. Block (x, y): the
 // unit whose first cut is where CTA x starts, rows [8 y, +8) of its tile, a warp each.
 constexpr int kCombineRows = 8;
-__global__ void __launch_bounds__(kCombineRows * 32) tree_combine_kernel(const __grid_constant__ FlashParams f) {
+template <Mode M>
+__global__ void __launch_bounds__(kCombineRows * 32)
+    tree_combine_kernel(const __grid_constant__ TreeParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const TreeParams &p = f.t;
-  const CutInfo cut = f.cuts[blockIdx.x];
+  const CutInfo cut = p.cuts[blockIdx.x];
   if (aborted(p.err) || cut.parts == 0) return;
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.y * kCombineRows + (threadIdx.x >> 5);  // row of the tile
-  const int c = t / kChunkRows, r = t % kChunkRows, i = r / f.hb, group = p.hq / p.hkv;
-  const int chunk = cut.c0 + c, node = chunk / f.parts * f.nb + i;
-  const int head = (chunk % f.parts) * kChunkRows + r % f.hb;
-  if (c >= cut.chunks || i >= f.nb || node >= cut.n || head >= group) return;
+  const int c = t / kChunkRows, r = t % kChunkRows, i = p.node_of(r);
+  const int chunk = cut.c0 + c, node = p.first_node(chunk) + i;
+  const int head = p.first_head(chunk) + r - i * p.hb;
+  if (c >= cut.chunks || i >= p.nb || node >= cut.n || head >= p.group_heads) return;
   // part 0 is the last item of the worker before, the others are their workers' first items
   auto slot = [&](int k) -> int64_t {
-    return 2 * ((int64_t)blockIdx.x + (int64_t)(k - 1) * f.group) + (k == 0 ? 1 : 0);
+    return 2 * ((int64_t)blockIdx.x + (int64_t)(k - 1) * p.group) + (k == 0 ? 1 : 0);
   };
   float m = -INFINITY;
   bool dirty = false;
   for (int k = lane; k < cut.parts; k += 32) {
-    m = fmaxf(m, f.part_lse[slot(k) * f.part_rows + t]);
-    dirty |= f.cuts[slot(k) >> 1].dirty[slot(k) & 1] != 0;
+    m = fmaxf(m, p.part_lse[slot(k) * p.part_rows + t]);
+    dirty |= p.cuts[slot(k) >> 1].dirty[slot(k) & 1] != 0;
   }
   dirty = __any_sync(kFull, dirty);
 #pragma unroll
@@ -970,9 +1154,9 @@ __global__ void __launch_bounds__(kCombineRows * 32) tree_combine_kernel(const _
   float sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
   for (int k = 0; k < cut.parts; ++k) {
-    const int64_t at = slot(k) * f.part_rows + t;
-    const float w = fast_exp2(f.part_lse[at] - base);
-    const float4 x = *reinterpret_cast<const float4 *>(f.part_o + at * kD + 4 * lane);
+    const int64_t at = slot(k) * p.part_rows + t;
+    const float w = fast_exp2(p.part_lse[at] - base);
+    const float4 x = *reinterpret_cast<const float4 *>(p.part_o + at * kD + 4 * lane);
     sum += w;
     o[0] += w * x.x;
     o[1] += w * x.y;
@@ -980,17 +1164,18 @@ __global__ void __launch_bounds__(kCombineRows * 32) tree_combine_kernel(const _
     o[3] += w * x.w;
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  uint16_t *dst = p.out + ((int64_t)(cut.q0 + node) * p.hq + cut.h * group + head) * kD;
+  uint16_t *dst = p.out + ((int64_t)(cut.q0 + node) * p.hq + cut.h * p.group_heads + head) * kD;
   *reinterpret_cast<uint2 *>(dst + 4 * lane) =
       make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
   if (dirty)
-    not_finite_fix(p, cut.b, cut.h, cut.n, cut.L, cut.q0 + node, node, dst, 4 * lane, 4);
+    not_finite_fix<M>(p, cut.b, cut.h, cut.n, cut.L, cut.q0 + node, node, dst, 4 * lane, 4);
 }
 
 // How a call's work is cut, from what the host knows.
 struct TreePlan {
   int32_t hb, nb, parts;  // heads and nodes of a chunk, chunks that share its nodes
-  int32_t group, workers, part_rows;
+  int32_t workers, group, heads, at_once, part_rows;
+  int64_t longest;        // bound of the axis
   size_t part_o, part_lse, bytes;  // of the workspace
 };
 TreePlan plan_tree(int32_t num_seqs, int32_t max_nodes, int32_t hq, int32_t hkv,
@@ -1002,10 +1187,13 @@ TreePlan plan_tree(int32_t num_seqs, int32_t max_nodes, int32_t hq, int32_t hkv,
   t.parts = (g + kChunkRows - 1) / kChunkRows;
   const int64_t chunks = ((int64_t)max_nodes + t.nb - 1) / t.nb * t.parts;
   const int64_t tiles = std::max<int64_t>(1, (chunks + kChunks - 1) / kChunks);
-  t.group = (int32_t)std::min<int64_t>(kMaxGroup, tiles);
-  const int64_t units = (int64_t)num_seqs * hkv * ((tiles + t.group - 1) / t.group);
-  const int64_t most = units * std::max(1, (int)(((int64_t)max_context + kGranule - 1) / kGranule));
-  t.workers = (int32_t)std::max<int64_t>(1, std::min<int64_t>(num_sms / t.group, most));
+  t.at_once = (int)std::min<int64_t>(kMaxTiles, tiles);
+  t.heads = 1;
+  while (t.heads * 2 * t.at_once <= kMaxGroup && hkv % (t.heads * 2) == 0) t.heads *= 2;
+  t.group = t.heads * t.at_once;
+  const int64_t units = (int64_t)num_seqs * (hkv / t.heads) * ((tiles + t.at_once - 1) / t.at_once);
+  t.longest = units * std::max(1, (int)(((int64_t)max_context + kGranule - 1) / kGranule));
+  t.workers = (int32_t)std::max<int64_t>(1, std::min<int64_t>(num_sms / t.group, t.longest));
   t.part_rows = (int32_t)(std::min<int64_t>(kChunks, std::max<int64_t>(1, chunks)) * kChunkRows);
   const size_t ctas = (size_t)t.workers * t.group;
   t.part_o = ctas * sizeof(CutInfo);
@@ -1014,38 +1202,44 @@ TreePlan plan_tree(int32_t num_seqs, int32_t max_nodes, int32_t hq, int32_t hkv,
   return t;
 }
 
-cudaError_t launch_flash(const TreeParams &p, const TreePlan &t, void *workspace,
-                         cudaStream_t stream) {
+template <Mode M>
+cudaError_t launch_tree(TreeParams p, const TreePlan &t, void *workspace, cudaStream_t stream) {
   CUtensorMap km, vm;
-  const uint64_t dims[3] = {64, (uint64_t)p.num_blocks * p.block_size, (uint64_t)p.hkv * 2};
-  const uint64_t strides[2] = {(uint64_t)p.hkv * kD * 2, 128};
-  const uint32_t box[3] = {64, kGranule, 1};
+  const uint64_t rows = (uint64_t)p.num_blocks * p.block_size;
+  const uint64_t wide[3] = {64, rows, (uint64_t)p.hkv * 2}, narrow[3] = {kD, rows, (uint64_t)p.hkv};
+  const uint64_t wide_strides[2] = {(uint64_t)p.hkv * kD * 2, 128};
+  const uint64_t narrow_strides[2] = {(uint64_t)p.hkv * kD, kD};
+  const uint32_t wide_box[3] = {64, kGranule, 1}, narrow_box[3] = {kD, kGranule, 1};
   auto encode = [&](CUtensorMap *map, const uint8_t *pool) {
-    return encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint8_t *>(pool),
-                             dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
-                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B) == CUDA_SUCCESS;
+    return encode_tensor_map(
+               map, M == kFp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+               const_cast<uint8_t *>(pool), M == kFp8 ? narrow : wide,
+               M == kFp8 ? narrow_strides : wide_strides, M == kFp8 ? narrow_box : wide_box,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) == CUDA_SUCCESS;
   };
   if (!encode(&km, p.k_cache) || !encode(&vm, p.v_cache)) return cudaErrorInvalidValue;
-  FlashParams f{};
-  f.t = p;
-  f.group = t.group;
-  f.workers = t.workers;
-  f.hb = t.hb;
-  f.nb = t.nb;
-  f.parts = t.parts;
-  f.out_32b = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
+  p.group = t.group;
+  p.heads = t.heads;
+  p.at_once = t.at_once;
+  p.per_tile = p.hkv / t.heads;
+  p.nb_magic = t.nb > 1 ? (uint32_t)((1ull << 32) / t.nb + 1) : 0;
+  p.hb_magic = t.hb > 1 ? (uint32_t)((1ull << 32) / t.hb + 1) : 0;
+  p.workers = t.workers;
+  p.hb = t.hb;
+  p.nb = t.nb;
+  p.parts = t.parts;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
-  f.cuts = reinterpret_cast<CutInfo *>(ws);
-  f.part_o = reinterpret_cast<float *>(ws + t.part_o);
-  f.part_lse = reinterpret_cast<float *>(ws + t.part_lse);
-  f.part_rows = t.part_rows;
-  const size_t smem = sizeof(TreeSmem) + 1024;
+  p.cuts = reinterpret_cast<CutInfo *>(ws);
+  p.part_o = reinterpret_cast<float *>(ws + t.part_o);
+  p.part_lse = reinterpret_cast<float *>(ws + t.part_lse);
+  p.part_rows = t.part_rows;
+  const size_t smem = sizeof(TreeSmem<M>) + 1024;
   static bool ready[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !ready[dev]) {
-    e = cudaFuncSetAttribute(tree_flash_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(tree_flash_kernel<M>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)smem);
     if (e != cudaSuccess) return e;
     if (dev < 64) ready[dev] = true;
@@ -1060,11 +1254,11 @@ cudaError_t launch_flash(const TreeParams &p, const TreePlan &t, void *workspace
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, tree_flash_kernel, km, vm, f);
+  e = cudaLaunchKernelEx(&cfg, tree_flash_kernel<M>, km, vm, p);
   if (e != cudaSuccess || t.workers == 1) return e;
-  return launch_after(tree_combine_kernel,
-                      dim3(cfg.gridDim.x, (unsigned)(t.part_rows / kCombineRows)),
-                      kCombineRows * 32, stream, f);
+  return launch_after(tree_combine_kernel<M>,
+                      dim3((unsigned)(t.workers * t.group), (unsigned)(t.part_rows / kCombineRows)),
+                      kCombineRows * 32, stream, p);
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -1099,9 +1293,8 @@ pkv_status tree_attn(const void *q, int64_t q_tok_stride, int64_t total_q, const
   if (!err || num_sms <= 0) return PKV_ERR_CUDA;
   const TreePlan plan =
       plan_tree(num_seqs, max_seqlen_q, num_q_heads, num_kv_heads, max_context_len, num_sms);
+  if (plan.longest > (1 << 30) || max_seqlen_q > (1 << 20)) return PKV_ERR_UNSUPPORTED;
   if (!workspace || !aligned16(workspace) || workspace_bytes < plan.bytes) return PKV_ERR_WORKSPACE;
-  const int64_t units = ((int64_t)max_seqlen_q * num_q_heads + kWarps - 1) / kWarps;
-  if (units > INT32_MAX || num_seqs > 65535) return PKV_ERR_UNSUPPORTED;
   TreeParams prm{};
   prm.q = static_cast<const uint16_t *>(q);
   prm.q_stride = q_tok_stride;
@@ -1120,6 +1313,7 @@ pkv_status tree_attn(const void *q, int64_t q_tok_stride, int64_t total_q, const
   prm.mask_words = mask_words;
   prm.hq = num_q_heads;
   prm.hkv = num_kv_heads;
+  prm.group_heads = num_q_heads / num_kv_heads;
   prm.block_size = block_size;
   prm.num_blocks = num_blocks;
   prm.num_seqs = num_seqs;
@@ -1127,11 +1321,13 @@ pkv_status tree_attn(const void *q, int64_t q_tok_stride, int64_t total_q, const
   prm.scale_log2 = std::min(std::max(fabsf(scale) * kLog2e, 1e-37f), 1e37f);
   prm.q_sign = scale < 0.f ? 0x80008000u : 0u;
   prm.out = static_cast<uint16_t *>(out);
+  prm.out_32b = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
   prm.err = err;
-  const dim3 grid((unsigned)units, (unsigned)num_seqs);
-  if (fp8) tree_attn_kernel<true><<<grid, kWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(prm);
-  else return launch_flash(prm, plan, workspace, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
-  return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = fp8                 ? launch_tree<kFp8>(prm, plan, workspace, st)
+                        : plan.at_once == 1 ? launch_tree<kTwoParts>(prm, plan, workspace, st)
+                                            : launch_tree<kOnePart>(prm, plan, workspace, st);
+  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 }  // namespace
