@@ -35,12 +35,14 @@
 //                tile), and two parts would cost half as much again.
 //   8-bit cache: fp16 (2^-11), see below.
 //
-// The 8-bit cache. An e4m3 code is an fp16 value, so the codes are widened in shared memory (by the
-// warps that load Q) and the products are those of fp16: exact in K and V. Q is divided by a power of
-// two of its row (its largest |q| becomes 1 to 2) and rounded to fp16, which keeps bf16's digits
-// down to 2^-14 of that and is off by 2^-25 of it at most below. The K scale of a key's group and the
-// row's power multiply the scores. The V scale is part of P: with v = log2 of it, m runs over s + v,
-// P' = 2^(s + v - m + 6) (between 2^-20 and 2^14 in fp16's normal range), and l sums P' / 2^(v + 6).
+// The 8-bit cache. S is a product of e4m3 operands, K as it lies: a row of Q, multiplied by a power of
+// two (its largest |q| becomes 128 to 256), enters as two e4m3 parts, which hold a bf16 value
+// exactly down to 2^-9 of that largest one and are off by 2^-17 of it at most below. V is widened to
+// fp16 in shared memory (an e4m3 code is an fp16 value) and multiplied by P in fp16. (Widening K too
+// is bound by shared memory: 192 KiB through it per tile, 1536 cycles, where a tile's loads take
+// 1350; this way 144.) The K scale of a key's group and the row's power multiply the scores. The V scale
+// is part of P: with v = log2 of it, m runs over s + v, P' = 2^(s + v - m + 6) (between 2^-20 and
+// 2^14 in fp16's normal range), and l sums P' / 2^(v + 6).
 //
 // Rows. 16 rows make a chunk: nb = 16 / G nodes with their G query heads (with more than 16 heads
 // one node and 16 of them). Chunk c of a tile lies in 16 of the 128 TMEM lanes that softmax warp c
@@ -48,7 +50,7 @@
 //
 // Warps (512 threads): 0-7 softmax and epilogue (warp c: chunk c), 8 work walk and K loads, 9 S
 // products, 10 V loads, 11 PV products, 12-15 Q into tensor memory, a look through the nodes' V rows,
-// and the widening of an 8-bit cache. Loads are TMA with 128-byte swizzle, 64 keys to a box (a granule
+// and the widening of an 8-bit cache's V. Loads are TMA with 128-byte swizzle, 64 keys to a box (a granule
 // never straddles a block). K and V have two slots each: more (3 + 3, 4 + 3) made every case slower,
 // K tiles far ahead taking their turn before V tiles that are needed sooner.
 // TMEM (512 columns): Q [0, 64) [64, 128), S [128, 256) [256, 384), O [384, 512).
@@ -86,7 +88,7 @@ constexpr int kSoftmaxWarps = 8;
 constexpr int kKWarp = 8, kSWarp = 9, kVWarp = 10, kPvWarp = 11, kQWarp0 = 12;
 constexpr int kThreads = 16 * 32;
 constexpr int kSlots = 2;     // of K and of V
-constexpr int kRawSlots = 2;  // of each pool's codes, 8-bit cache
+constexpr int kRawSlots = 3;  // of each pool's codes, 8-bit cache
 constexpr uint32_t kTileBytes = kTile * kD * 2;
 constexpr uint32_t kPlane = kTileBytes / 2;         // 64 dims of the tile's keys, 128-byte rows
 constexpr uint32_t kGranuleBytes = kGranule * 128;  // of a plane, or of an 8-bit pool
@@ -123,21 +125,23 @@ struct CutInfo {
 static_assert(sizeof(CutInfo) == 64, "");
 
 struct RawSmem {  // 8-bit cache
-  uint8_t k[kRawSlots][kRawBytes], v[kRawSlots][kRawBytes];
+  uint8_t v[kRawSlots][kRawBytes];
   alignas(16) float scale[kScaleTiles][2][2][4];  // [tile][granule][K, V]: four groups' around it
   float q_power[kRing][kChunks * kChunkRows];     // log2 of what the rows of q were divided by
-  uint64_t k_full[kRawSlots], k_empty[kRawSlots], v_full[kRawSlots], v_empty[kRawSlots];
+  uint64_t v_full[kRawSlots], v_empty[kRawSlots];
 };
 struct NoRaw {};
 
 template <Mode M>
 struct TreeSmem {
-  uint8_t k[kSlots][kTileBytes];  // 1024-byte aligned (128-byte swizzle atoms)
+  static constexpr int kKSlots = M == kFp8 ? kRawSlots : kSlots;
+  static constexpr uint32_t kKBytes = M == kFp8 ? kRawBytes : kTileBytes;
+  uint8_t k[kKSlots][kKBytes];  // 1024-byte aligned (128-byte swizzle atoms)
   uint8_t v[kSlots][kTileBytes];
   std::conditional_t<M == kFp8, RawSmem, NoRaw> raw;
   Item items[kRing];
   int32_t dirty[kRing];            // of the item in this ring slot
-  uint64_t k_full[kSlots], k_empty[kSlots], v_full[kSlots], v_empty[kSlots];
+  uint64_t k_full[kKSlots], k_empty[kKSlots], v_full[kSlots], v_empty[kSlots];
   // bf16: a V tile that holds nodes has landed; they have been looked through, rows past the
   // context zeroed
   uint64_t v_ready[kSlots], v_fixed[kSlots];
@@ -388,25 +392,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ CUtensorMap vmap,
                       const __grid_constant__ TreeParams p) {
   constexpr bool F8 = M == kFp8;
+  constexpr int kKSlots = TreeSmem<M>::kKSlots;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   extern __shared__ uint8_t smem_raw[];
   TreeSmem<M> &sm = *reinterpret_cast<TreeSmem<M> *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   if (tid == 0) {
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&sm.k_full[i], F8 ? 2 : 1);  // (8-bit: two warps widen K, two V)
+    for (int i = 0; i < kKSlots; ++i) {
+      mbar_init(&sm.k_full[i], 1);
       mbar_init(&sm.k_empty[i], 1);
-      mbar_init(&sm.v_full[i], F8 ? 2 : 1);
+    }
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&sm.v_full[i], F8 ? 4 : 1);  // (8-bit: four warps widen a tile)
       mbar_init(&sm.v_empty[i], 1);
       mbar_init(&sm.v_ready[i], 1);
       mbar_init(&sm.v_fixed[i], 4);
     }
     if constexpr (F8)
       for (int i = 0; i < kRawSlots; ++i) {
-        mbar_init(&sm.raw.k_full[i], 1);
-        mbar_init(&sm.raw.k_empty[i], 2);
         mbar_init(&sm.raw.v_full[i], 1);
-        mbar_init(&sm.raw.v_empty[i], 2);
+        mbar_init(&sm.raw.v_empty[i], 4);
       }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.q_full[i], 4);
@@ -535,12 +540,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int steps = max(1, it.tiles), push_at = min(1, steps - 1);
           for (int j = 0; j < steps && ok; ++j) {
             if (j < it.tiles) {
-              constexpr int kN = F8 ? kRawSlots : kSlots;
-              const int slot = g % kN;
-              uint64_t *full, *empty;
-              if constexpr (F8) full = &sm.raw.k_full[slot], empty = &sm.raw.k_empty[slot];
-              else full = &sm.k_full[slot], empty = &sm.k_empty[slot];
-              ok = g < kN || wait_parity(empty, ((g / kN) - 1) & 1, p.err);
+              const int slot = g % kKSlots;
+              uint64_t *const full = &sm.k_full[slot];
+              ok = g < kKSlots ||
+                   wait_parity(&sm.k_empty[slot], ((g / kKSlots) - 1) & 1, p.err);
               if (!ok) break;  // (g counts the copies that were issued)
               const int32_t pos = it.key0 + j * kTile;
               const int granules = it.key1 - pos > kGranule ? 2 : 1;
@@ -556,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = 0; e < 8; ++e) dst[e >> 2][e & 3] = 1.f;
                   if (r + 1 < granules) mbar_expect_tx(full, bytes);
                   else mbar_arrive_expect_tx(full, bytes);
-                  tma_load_3d(sm.raw.k[slot] + r * kGranuleBytes, &kmap, full, 0, row, it.h, policy);
+                  tma_load_3d(sm.k[slot] + r * kGranuleBytes, &kmap, full, 0, row, it.h, policy);
                   if (row >= 0) {
                     const int64_t at =
                         ((int64_t)rows.blk * p.hkv + it.h) * (p.block_size / kFp8Group) +
@@ -609,12 +612,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           it = nx;
         }
         // keep the CTA alive until every copy it issued has landed
-        constexpr uint32_t kN = F8 ? kRawSlots : kSlots;
         bool drained = true;
-        for (uint32_t t = g > kN ? g - kN : 0; drained && t < g; ++t) {
-          if constexpr (F8) drained = wait_own(&sm.raw.k_full[t % kN], (t / kN) & 1, p.err);
-          else drained = wait_own(&sm.k_full[t % kN], (t / kN) & 1, p.err);
-        }
+        for (uint32_t t = g > kKSlots ? g - kKSlots : 0; drained && t < g; ++t)
+          drained = wait_own(&sm.k_full[t % kKSlots], (t / kKSlots) & 1, p.err);
       }
       __syncwarp();
     } else if (warp == kVWarp) {
@@ -689,7 +689,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++used;
         tc_fence_after_sync();
         if (quad < ip->chunks) {  // (warp-uniform)
-          float inv = 1.f;
           if constexpr (F8) {
             uint32_t top = 0;
 #pragma unroll 4
@@ -698,29 +697,46 @@ __global__ void __launch_bounds__(kThreads, 1)
               top = __vmaxu2(top, __vmaxu2(bf16x2_absmax(x.x, x.y), bf16x2_absmax(x.z, x.w)));
             }
             top = max(top & 0xffffu, top >> 16);
-            // the exponent of the largest |q| (of zeros and of what is not finite: some other)
-            const int e = min(max((int)(top >> 7) - 127, -120), 120);
-            inv = pow2f(-e);
-            sm.raw.q_power[k % kRing][c * kChunkRows + r] = (float)e;
-          }
+            // what takes the largest |q| to 2^7; a row with infinities or NaNs becomes NaN
+            const int e7 = min(max((int)(top >> 7) - 134, -120), 120);
+            const float mul = pow2f(-e7);
+            const uint32_t bad = top >= 0x7f80u ? 0x7f7f7f7fu : 0u;
+            sm.raw.q_power[k % kRing][c * kChunkRows + r] = (float)e7;
 #pragma unroll 1
-          for (int hf = 0; hf < 2; ++hf) {
-            uint32_t w[32];
+            for (int q4 = 0; q4 < 4; ++q4) {  // 32 dims: 8 columns of each part
+              uint32_t hi[8], lo[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              uint4 x = row ? ld_once_u4(src + 8 * hf + e) : make_uint4(0, 0, 0, 0);
-              x = make_uint4(x.x ^ p.q_sign, x.y ^ p.q_sign, x.z ^ p.q_sign, x.w ^ p.q_sign);
-              if constexpr (F8)
-                x = make_uint4(pack_f16x2(bf16_lo(x.x) * inv, bf16_hi(x.x) * inv),
-                               pack_f16x2(bf16_lo(x.y) * inv, bf16_hi(x.y) * inv),
-                               pack_f16x2(bf16_lo(x.z) * inv, bf16_hi(x.z) * inv),
-                               pack_f16x2(bf16_lo(x.w) * inv, bf16_hi(x.w) * inv));
-              w[4 * e] = x.x;
-              w[4 * e + 1] = x.y;
-              w[4 * e + 2] = x.z;
-              w[4 * e + 3] = x.w;
+              for (int e = 0; e < 4; ++e) {
+                const uint4 x = row ? ld_once_u4(src + 4 * q4 + e) : make_uint4(0, 0, 0, 0);
+                const uint32_t w[4] = {x.x ^ p.q_sign, x.y ^ p.q_sign, x.z ^ p.q_sign, x.w ^ p.q_sign};
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  const float f[4] = {bf16_lo(w[2 * z]) * mul, bf16_hi(w[2 * z]) * mul,
+                                      bf16_lo(w[2 * z + 1]) * mul, bf16_hi(w[2 * z + 1]) * mul};
+                  const uint32_t a = cvt_e4m3x2(f[0], f[1]), b = cvt_e4m3x2(f[2], f[3]);
+                  const float2 fa = f16x2_to_f32(cvt_f16x2_e4m3x2(a)), fb = f16x2_to_f32(cvt_f16x2_e4m3x2(b));
+                  hi[2 * e + z] = a | b << 16 | bad;
+                  lo[2 * e + z] = cvt_e4m3x2(f[0] - fa.x, f[1] - fa.y) |
+                                  cvt_e4m3x2(f[2] - fb.x, f[3] - fb.y) << 16;
+                }
+              }
+              tmem_st_cols(lane_addr + kQCol + 64 * buf + 8 * q4, hi);
+              tmem_st_cols(lane_addr + kQCol + 64 * buf + 32 + 8 * q4, lo);
             }
-            tmem_st32(lane_addr + kQCol + 64 * buf + 32 * hf, w);
+          } else {
+#pragma unroll 1
+            for (int hf = 0; hf < 2; ++hf) {
+              uint32_t w[32];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const uint4 x = row ? ld_once_u4(src + 8 * hf + e) : make_uint4(0, 0, 0, 0);
+                w[4 * e] = x.x ^ p.q_sign;
+                w[4 * e + 1] = x.y ^ p.q_sign;
+                w[4 * e + 2] = x.z ^ p.q_sign;
+                w[4 * e + 3] = x.w ^ p.q_sign;
+              }
+              tmem_st32(lane_addr + kQCol + 64 * buf + 32 * hf, w);
+            }
           }
           tmem_st_wait();
         }
@@ -735,56 +751,56 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int tiles = it.tiles, key0 = it.key0, key1 = it.key1, root = it.L - it.n;
         bool found = false;
         if constexpr (F8) {
-          // Warps 12 and 13 widen K, 14 and 15 V: 16 codes of a row at a time, rows 8 apart in a
-          // quarter warp so that neither side has bank conflicts.
-          const bool is_v = warp >= kQWarp0 + 2;
-          const int part = warp & 1;  // the rows of granule 0 or 1
-          uint64_t *const raw_full = is_v ? sm.raw.v_full : sm.raw.k_full;
-          uint64_t *const raw_empty = is_v ? sm.raw.v_empty : sm.raw.k_empty;
-          uint64_t *const full = is_v ? sm.v_full : sm.k_full;
-          uint64_t *const empty = is_v ? sm.v_empty : sm.k_empty;
+          // Each warp widens 32 rows of a V tile: 16 codes of a row at a time, rows next to one
+          // another in a quarter warp so that neither side has bank conflicts.
           for (int j = 0; j < tiles && ok; ++j, ++g) {
             // (the next item's Q before this one's last tile: it is needed right after)
             if (j == tiles - 1) ok = load_q(k + 1, last);
             const int raw = g % kRawSlots, slot = g % kSlots;
-            ok = ok && __all_sync(kFull, wait_parity(&raw_full[raw], (g / kRawSlots) & 1, p.err));
+            ok = ok && __all_sync(kFull, wait_parity(&sm.raw.v_full[raw], (g / kRawSlots) & 1, p.err));
             if (ok && g >= kSlots)
-              ok = __all_sync(kFull, wait_parity(&empty[slot], ((g / kSlots) - 1) & 1, p.err));
+              ok = __all_sync(kFull, wait_parity(&sm.v_empty[slot], ((g / kSlots) - 1) & 1, p.err));
             if (!ok) break;
             const int pos = key0 + j * kTile, keys = min(kTile, key1 - pos);
-            const uint8_t *const src = (is_v ? sm.raw.v : sm.raw.k)[raw] + part * kGranuleBytes;
-            uint8_t *const dst = (is_v ? sm.v : sm.k)[slot] + part * kGranuleBytes;
-            const int rows_up = min(kGranule, ((keys + 15) & ~15) - part * kGranule);
-            const bool nodes = is_v && pos + kTile > root;
-#pragma unroll 2
-            for (int e = 0; e < rows_up; e += 8) {
-              const int row = e + (lane & 7);  // (rows past the keys: V's become zeros)
+            const int first = 32 * quad, rows_up = min(32, ((keys + 15) & ~15) - first);
+            const uint8_t *const src = sm.raw.v[raw] + first * 128;
+            uint8_t *const dst = sm.v[slot] + first * 128;
+            const bool nodes = pos + kTile > root;
+            // 16 rows x 8 pieces of 16 codes: four pieces of a lane in flight
+            const int low = lane & 7, a0 = lane >> 3;
+            for (int e = 0; e < rows_up; e += 16) {
+              uint4 x[4];  // rows e + low and e + 8 + low, pieces a0 and a0 + 4
 #pragma unroll
-              for (int z = 0; z < 2; ++z) {
-                const int a = (lane >> 3) + 4 * z;  // 16 codes of it
-                uint4 x = *reinterpret_cast<const uint4 *>(src + row * 128 + ((a ^ (row & 7)) << 4));
-                if (nodes) {
-                  const int key = part * kGranule + row;
-                  if (key >= keys) x = make_uint4(0, 0, 0, 0);
-                  if (pos + key >= root &&
-                      (has_nan4(x.x) || has_nan4(x.y) || has_nan4(x.z) || has_nan4(x.w))) {
-                    x = make_uint4(no_nan4(x.x), no_nan4(x.y), no_nan4(x.z), no_nan4(x.w));
+              for (int u = 0; u < 4; ++u)
+                x[u] = *reinterpret_cast<const uint4 *>(src + (e + 8 * (u >> 1) + low) * 128 +
+                                                        (((a0 + 4 * (u & 1)) ^ low) << 4));
+              if (nodes) {  // rows past the keys become zeros, and NaNs of nodes
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                  const int key = first + e + 8 * (u >> 1) + low;
+                  if (key >= keys) x[u] = make_uint4(0, 0, 0, 0);
+                  if (pos + key >= root && (has_nan4(x[u].x) || has_nan4(x[u].y) ||
+                                            has_nan4(x[u].z) || has_nan4(x[u].w))) {
+                    x[u] = make_uint4(no_nan4(x[u].x), no_nan4(x[u].y), no_nan4(x[u].z),
+                                      no_nan4(x[u].w));
                     found = true;
                   }
                 }
+              }
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
                 uint4 lo, hi;
-                widen16(x, lo, hi);
-                uint8_t *const to = dst + (a >> 2) * kPlane + row * 128;
-                const int piece = 2 * (a & 3);
-                *reinterpret_cast<uint4 *>(to + ((piece ^ (row & 7)) << 4)) = lo;
-                *reinterpret_cast<uint4 *>(to + (((piece + 1) ^ (row & 7)) << 4)) = hi;
+                widen16(x[u], lo, hi);
+                uint8_t *const to = dst + (u & 1) * kPlane + (e + 8 * (u >> 1) + low) * 128;
+                *reinterpret_cast<uint4 *>(to + (((2 * a0) ^ low) << 4)) = lo;
+                *reinterpret_cast<uint4 *>(to + (((2 * a0 + 1) ^ low) << 4)) = hi;
               }
             }
             fence_async_shared();
             __syncwarp();
             if (lane == 0) {
-              mbar_arrive(&full[slot]);
-              mbar_arrive(&raw_empty[raw]);
+              mbar_arrive(&sm.v_full[slot]);
+              mbar_arrive(&sm.raw.v_empty[raw]);
             }
           }
           if (tiles == 0) ok = load_q(k + 1, last);
@@ -849,25 +865,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (last) break;
         if (tiles == 0) continue;
         for (int j = 0; j < tiles && ok; ++j, ++g) {
-          const uint32_t sb = g & 1, slot = g % kSlots;
+          const uint32_t sb = g & 1, slot = g % (s_role ? kKSlots : kSlots);
           const int pos = key0 + j * kTile;
           const int steps = (min(kTile, key1 - pos) + 15) / 16;
           if (s_role) {  // S over as many columns as there are keys, in steps of 16
             const uint32_t qb = used & 1;
-            ok = wait_all(&sm.k_full[slot], (g / kSlots) & 1);
+            ok = wait_all(&sm.k_full[slot], (g / kKSlots) & 1);
             if (ok && j == 0) ok = wait_all(&sm.q_full[qb], (used >> 1) & 1);
             // the buffer's previous P has been read by its PV
             if (ok && g >= 2) ok = wait_all(&sm.o_full[sb], ((g >> 1) - 1) & 1);
             if (!ok) break;
             tc_fence_after_sync();
             if (elect_one()) {
-              const uint32_t idesc =
-                  F8 ? idesc_f16_f32(128, 16 * steps, 0, 0) : idesc_bf16_f32(128, 16 * steps, 0, 0);
-              const uint64_t dk = dk0 + slot * (kTileBytes >> 4);
+              const uint64_t dk = dk0 + slot * (TreeSmem<M>::kKBytes >> 4);
+              const uint32_t sc = tmem + kSCol + 128 * sb, qc = tmem + kQCol + 64 * qb;
+              if constexpr (F8) {
+                const uint32_t idesc = idesc_e4m3_f32(128, 16 * steps, 0, 0);
 #pragma unroll
-              for (int kk = 0; kk < kD / 16; ++kk)
-                umma_f16_ts(tmem + kSCol + 128 * sb, tmem + kQCol + 64 * qb + 8 * kk,
-                            dk + (((kk >> 2) * kPlane + (kk & 3) * 32) >> 4), idesc, kk > 0);
+                for (int kk = 0; kk < 2 * (kD / 32); ++kk)  // 32 dims of a part of Q
+                  umma_e4m3_ts(sc, qc + 8 * kk, dk + ((kk & 3) * 32 >> 4), idesc, kk > 0);
+              } else {
+                const uint32_t idesc = idesc_bf16_f32(128, 16 * steps, 0, 0);
+#pragma unroll
+                for (int kk = 0; kk < kD / 16; ++kk)
+                  umma_f16_ts(sc, qc + 8 * kk, dk + (((kk >> 2) * kPlane + (kk & 3) * 32) >> 4),
+                              idesc, kk > 0);
+              }
               umma_commit(&sm.s_full[sb]);
               umma_commit(&sm.k_empty[slot]);
               if (j == tiles - 1) umma_commit(&sm.q_empty[qb]);
