@@ -150,7 +150,8 @@ struct TreeSmem {
   uint64_t item_full[kRing], item_empty[kRing];
   uint64_t scanned[kRing];         // `dirty` is known
   uint32_t tmem_base;
-  int32_t stop;
+  int32_t stop, gone;              // gone: a softmax warp has given up waiting
+  float max_of[2][kSoftmaxWarps][kChunkRows], sum_of[kSoftmaxWarps][kChunkRows];  // shared chunks
   int32_t warp_sums[16];
   // the sequence that the CTA's part starts in, and where that starts on the axis
   int32_t start_b, start_at, start_q0, start_n, start_L;
@@ -429,6 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     sm.start_b = 0;
     sm.start_at = 0;
+    sm.gone = 0;
     fence_mbar_init();
     prefetch_tensormap(&kmap);
     prefetch_tensormap(&vmap);
@@ -520,8 +522,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the kernel that follows may be set up (not before this CTA has its tensor memory)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!sm.stop) {
-    // (the branches below do not meet before the end: what follows setmaxnreg has its registers)
-    if (warp >= kSoftmaxWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == kKWarp) {
       // ------------------------------------------------------------ work walk and K loads
       if (lane == 0) {
@@ -912,13 +912,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               constexpr uint32_t kIdesc =  // V: MN-major
                   F8 ? idesc_f16_f32(128, kD, 0, 1) : idesc_bf16_f32(128, kD, 0, 1);
               const uint64_t dv = dv0 + slot * (kTileBytes >> 4);
-              const uint32_t pc = tmem + kSCol + 128 * sb;
+              const uint32_t p0 = tmem + kSCol + 128 * sb;  // a granule's P over its own S columns
               auto step = [&](int kk) {
-                umma_f16_ts(tmem + kOCol, pc + 8 * kk, dv + ((kk * 16 * 128) >> 4), kIdesc,
+                const uint32_t pc = p0 + 64 * (kk >> 2) + 8 * (kk & 3);
+                umma_f16_ts(tmem + kOCol, pc, dv + ((kk * 16 * 128) >> 4), kIdesc,
                             j > 0 || kk > 0);
                 if constexpr (M == kTwoParts)
-                  umma_f16_ts(tmem + kOCol, pc + 64 + 8 * kk, dv + ((kk * 16 * 128) >> 4), kIdesc,
-                              true);
+                  umma_f16_ts(tmem + kOCol, pc + 32, dv + ((kk * 16 * 128) >> 4), kIdesc, true);
               };
               // (in a loop an issue takes 67 cycles, about as long as the product)
               if (steps == kTile / 16) {
@@ -943,26 +943,54 @@ __global__ void __launch_bounds__(kThreads, 1)
       __all_sync(kFull, wait_own(bar, 0, p.err));
     } else {
       // ------------------------------------------------------------ softmax and epilogue
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-      const int c = warp, ch = lane >> 4, r = lane & 15;  // chunk, half of the keys, row
-      const uint32_t lane_addr = tmem + ((uint32_t)((c & 3) * 32 + (c >> 2) * 16) << 16);
+      // A pass is a granule of a tile: 32 of its keys to a thread. A warp goes through both granules
+      // of its own chunk's rows; with up to four chunks warps c and c + 4 share chunk c (both reach
+      // its lanes), a granule each. The loops over passes stay loops: unrolled, a tile's code does not
+      // fit the instruction caches beside the other warps'.
+      const int ch = lane >> 4, r = lane & 15;  // half of the granule's keys, row
       const int i = p.node_of(r), head_r = r - i * p.hb;
       uint32_t taken = 0, g = 0;
-      bool ok = true;
-      while (ok) {
+      // Two warps that share a chunk meet in named barriers. A warp that has given up waiting
+      // meets its partner once more (`gone`), wherever that one is.
+      const uint32_t pair = 1 + (warp & 3);
+      auto gone = [&]() {
+        if (lane == 0) sm.gone = 1;
+        barrier_or(pair, 64, true);
+        named_barrier_sync(pair, 64);
+      };
+      // OR over the pair. 0: no, 1: yes, -1: the partner is gone.
+      auto either = [&](bool mine) -> int {
+        if (!barrier_or(pair, 64, mine)) return 0;
+        named_barrier_sync(pair, 64);
+        return *reinterpret_cast<volatile int32_t *>(&sm.gone) ? -1 : 1;
+      };
+      while (true) {
         const Item *ip = wait_item(sm, taken, p.err);
-        if (!ip || ip->last) break;
+        if (!ip) {
+          gone();
+          break;
+        }
+        if (ip->last) {
+          either(false);
+          break;
+        }
         const int ring = taken % kRing;
         const int tiles = ip->tiles, key0 = ip->key0, key1 = ip->key1, n = ip->n, root = ip->L - n;
+        const bool shared = ip->chunks <= kChunks / 2;
+        const int c = shared ? warp & 3 : warp;
+        const int pass0 = shared ? warp >> 2 : 0, pass1 = shared ? pass0 + 1 : 2;
         const bool mine = c < ip->chunks;  // (warp-uniform)
         const int chunk = ip->c0 + c, node = p.first_node(chunk) + i;
         const int head = p.first_head(chunk) + head_r;
         const int64_t q_row = (int64_t)ip->q0 + node;
         const bool row = mine && i < p.nb && node < n && head < p.group_heads;
-        uint16_t *const dst = p.out + (q_row * p.hq + ip->h * p.group_heads + head) * kD + 64 * ch;
+        uint16_t *const dst = p.out + (q_row * p.hq + ip->h * p.group_heads + head) * kD;
+        const uint32_t lane_addr = tmem + ((uint32_t)((c & 3) * 32 + (c >> 2) * 16) << 16);
         if (tiles == 0) {  // nothing to see: zeros
           if (row)
-            for (int k = 0; k < 8; ++k) reinterpret_cast<uint4 *>(dst)[k] = make_uint4(0, 0, 0, 0);
+            for (int k = pass0; k < pass1; ++k)
+              for (int e = 0; e < 4; ++e)
+                reinterpret_cast<uint4 *>(dst + 64 * k + 32 * ch)[e] = make_uint4(0, 0, 0, 0);
           release_item(sm, taken, lane);
           ++taken;
           continue;
@@ -973,90 +1001,126 @@ __global__ void __launch_bounds__(kThreads, 1)
           return w == 0 ? first_word : row && 64 * w < n ? mask_word(p, q_row, node, w) : 0;
         };
         float m_run = -INFINITY, l_run = 0.f, row_scale = p.scale_log2;
+        bool ok = true, alone = false;
         for (int j = 0; j < tiles; ++j, ++g) {
-          const uint32_t sb = g & 1, s_col = kSCol + 128 * sb;
+          const uint32_t sb = g & 1, s_addr = lane_addr + kSCol + 128 * sb;
           // warp-uniform results: the TMEM loads and stores below are .sync.aligned
           ok = __all_sync(kFull, wait_parity(&sm.s_full[sb], (g >> 1) & 1, p.err));
           if (!ok) break;
           if (mine) {
             tc_fence_after_sync();
-            uint32_t x[8][8];  // keys 64 ch + 8 k + e
-            tmem_ld16x2<64>(lane_addr + s_col, x);
-            const int pos = key0 + j * kTile + 64 * ch;
-            // 8-bit cache: the group's scales (a group past the keys has none)
-            float factor = row_scale, v_log2 = 0.f, per_v = 1.f;
-            if constexpr (F8) {
+            if constexpr (F8)
               if (j == 0)
-                row_scale = factor = p.scale_log2 * pow2f((int)sm.raw.q_power[ring][c * kChunkRows + r]);
-              if (pos < key1) {
-                const float(*sc)[4] = sm.raw.scale[g % kScaleTiles][ch];
-                factor = fmaxf(factor * sc[0][pos / kGranule & 3], 1e-38f);  // (see scale_log2)
-                const float v = sc[1][pos / kGranule & 3];
-                v_log2 = log2_approx(v) + kOffset8;
-                per_v = 1.f / (v * (1 << kOffset8));
+                row_scale = p.scale_log2 * pow2f((int)sm.raw.q_power[ring][c * kChunkRows + r]);
+            // 8-bit cache: what multiplies the scores of pass k, log2 of its V scale (a granule past
+            // the keys has no scales)
+            auto factors = [&](int k, float &factor, float &v_scale) {
+              factor = row_scale;
+              v_scale = 1.f;
+              if constexpr (F8) {
+                const int pos = key0 + j * kTile + 64 * k;
+                if (pos < key1) {
+                  const float(*sc)[4] = sm.raw.scale[g % kScaleTiles][k];
+                  factor = fmaxf(factor * sc[0][pos / kGranule & 3], 1e-38f);  // (see scale_log2)
+                  v_scale = sc[1][pos / kGranule & 3];
+                }
               }
-            }
-            // the keys of this thread's that the row sees
-            if (pos + 64 > min(key1, root)) {
-              uint64_t sees = pos >= key1 ? 0 : pos + 64 > key1 ? ~0ull >> (64 - (key1 - pos)) : ~0ull;
-              if (pos + 64 > root && sees != 0) {
-                const int base = pos - root, w = base >> 6, sh = base & 63;  // (w = -1: before the root)
-                uint64_t bits = w < 0 ? ~0ull : word(w);
-                if (sh) bits = bits >> sh | word(w + 1) << (64 - sh);
-                sees &= bits;
+            };
+            float m_tile = -INFINITY;
+#pragma unroll 1
+            for (int k = pass0; k < pass1; ++k) {
+              uint32_t x[32];  // keys 64 k + 32 ch + e
+              tmem_ld16x2_32<32>(s_addr + 64 * k, x);
+              const int pos = key0 + j * kTile + 64 * k + 32 * ch;
+              float factor, v_scale;
+              factors(k, factor, v_scale);
+              tmem_ld_wait(x);
+              if (key0 + j * kTile + 64 * (k + 1) > min(key1, root)) {
+                // the keys of this thread's that the row sees; the others' scores become -inf
+                uint32_t sees = pos >= key1 ? 0 : pos + 32 > key1 ? ~0u >> (32 - (key1 - pos)) : ~0u;
+                if (pos + 32 > root && sees != 0) {
+                  const int base = pos - root, w = base >> 6, sh = base & 63;  // (w = -1: before it)
+                  uint64_t bits = w < 0 ? ~0ull : word(w);
+                  if (sh) bits = bits >> sh | word(w + 1) << (64 - sh);
+                  sees &= (uint32_t)bits;
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (!(sees >> e & 1)) x[e] = __float_as_uint(-INFINITY);
+                tmem_st16x2_32<32>(s_addr + 64 * k, x);
+                tmem_st_wait();
               }
+              float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  if (!((uint32_t)(sees >> (32 * (k / 4))) >> (8 * (k & 3) + e) & 1))
-                    x[k][e] = __float_as_uint(-INFINITY);
+              for (int e = 0; e < 32; e += 4) {
+                mx[0] = fmax3(mx[0], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                mx[1] = fmax3(mx[1], __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+              }
+              float m = fmaxf(mx[0], mx[1]) * factor;
+              if constexpr (F8) m += log2_approx(v_scale);
+              m_tile = fmaxf(m_tile, m);
             }
-            float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-#pragma unroll
-              for (int e = 0; e < 8; e += 2)
-                mx[k & 1] = fmax3(mx[k & 1], __uint_as_float(x[k][e]), __uint_as_float(x[k][e + 1]));
-            float m_tile = fmaxf(mx[0], mx[1]) * factor;
-            if constexpr (F8) m_tile += v_log2 - kOffset8;
             m_tile = fmaxf(m_tile, __shfl_xor_sync(kFull, m_tile, 16));
-            const float m_new = fmaxf(m_run, m_tile);
-            const bool rescale = m_new > m_run + kRescaleLog2;
-            float alpha = 1.f;
-            if (rescale) {
-              alpha = fast_exp2(m_run - m_new);
+            bool grows = m_tile > m_run + kRescaleLog2;
+            int any;
+            if (shared) {
+              if (ch == 0) sm.max_of[sb][warp][r] = m_tile;
+              any = either(__any_sync(kFull, grows));
+              if (any < 0) {
+                alone = true;
+                break;
+              }
+              if (any) {
+                m_tile = fmaxf(m_tile, sm.max_of[sb][warp ^ 4][r]);
+                grows = m_tile > m_run + kRescaleLog2;
+              }
+            } else {
+              any = __any_sync(kFull, grows);
+            }
+            if (any) {
+              const float m_new = grows ? m_tile : m_run;
+              const float alpha = grows ? fast_exp2(m_run - m_new) : 1.f;
               m_run = m_new;
               l_run *= alpha;
-            }
-            const float offset = v_log2 - (m_run == -INFINITY ? 0.f : m_run);
-            // O holds the item's tiles before this one: rescale it (never on the first tile)
-            if (j > 0 && __any_sync(kFull, rescale)) {
-              ok = __all_sync(kFull, wait_parity(&sm.o_full[(g - 1) & 1], ((g - 1) >> 1) & 1, p.err));
-              if (!ok) break;
-              tc_fence_after_sync();
+              // O holds the item's tiles before this one: rescale it (never on the first tile)
+              if (j > 0) {
+                ok = __all_sync(kFull, wait_parity(&sm.o_full[(g - 1) & 1], ((g - 1) >> 1) & 1, p.err));
+                if (!ok) break;
+                tc_fence_after_sync();
 #pragma unroll 1
-              for (int k = 0; k < 2; ++k) {
-                uint32_t o[32];
-                tmem_ld16x2_32<64>(lane_addr + kOCol + 32 * k, o);
-                tmem_ld_wait(o);
+                for (int k = pass0; k < pass1; ++k) {
+                  uint32_t o[32];
+                  tmem_ld16x2_32<32>(lane_addr + kOCol + 64 * k, o);
+                  tmem_ld_wait(o);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                tmem_st16x2_32<64>(lane_addr + kOCol + 32 * k, o);
+                  for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                  tmem_st16x2_32<32>(lane_addr + kOCol + 64 * k, o);
+                }
               }
             }
-            // P, two keys to a column, over the first half of S; a second part over the rest (this
-            // warp has read its rows' S)
-            const float2 mul2 = make_float2(factor, factor), add2 = make_float2(offset, offset);
-            float2 rs0 = make_float2(0.f, 0.f), rs1 = make_float2(0.f, 0.f);
+            // P, two keys to a column, over the first half of the pass's S columns; a second part
+            // over the other half
+            const float base = m_run == -INFINITY ? 0.f : m_run;
+#pragma unroll 1
+            for (int k = pass0; k < pass1; ++k) {
+              uint32_t x[32];
+              tmem_ld16x2_32<32>(s_addr + 64 * k, x);
+              float factor, v_scale;
+              factors(k, factor, v_scale);
+              float offset = -base, per_v = 1.f;
+              if constexpr (F8) {
+                offset += log2_approx(v_scale) + kOffset8;
+                per_v = rcp_approx(v_scale * (1 << kOffset8));
+              }
+              const float2 mul2 = make_float2(factor, factor), add2 = make_float2(offset, offset);
+              float2 rs0 = make_float2(0.f, 0.f), rs1 = make_float2(0.f, 0.f);
+              tmem_ld_wait(x);
+              uint32_t hi[16];
+              [[maybe_unused]] uint32_t lo[16];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t hi[8], lo[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
+              for (int e = 0; e < 16; ++e) {
                 const float2 t = ffma2(
-                    make_float2(__uint_as_float(x[2 * k + e / 4][2 * e % 8]),
-                                __uint_as_float(x[2 * k + e / 4][2 * e % 8 + 1])), mul2, add2);
+                    make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), mul2, add2);
                 const float2 pe = make_float2(fast_exp2(t.x), fast_exp2(t.y));
                 if (e & 1) rs1 = fadd2(rs1, pe);
                 else rs0 = fadd2(rs0, pe);
@@ -1068,68 +1132,82 @@ __global__ void __launch_bounds__(kThreads, 1)
                     lo[e] = pack_bf16x2(pe.x - bf16_lo(hi[e]), pe.y - bf16_hi(hi[e]));
                 }
               }
-              tmem_st16x2<32>(lane_addr + s_col + 8 * k, hi);
-              if constexpr (M == kTwoParts) tmem_st16x2<32>(lane_addr + s_col + 64 + 8 * k, lo);
+              tmem_st16x2_16<16>(s_addr + 64 * k, hi);
+              if constexpr (M == kTwoParts) tmem_st16x2_16<16>(s_addr + 64 * k + 32, lo);
+              l_run += ((rs0.x + rs0.y) + (rs1.x + rs1.y)) * per_v;
             }
             tmem_st_wait();
-            l_run += ((rs0.x + rs0.y) + (rs1.x + rs1.y)) * per_v;
             tc_fence_before_sync();
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.p_full[sb]);
         }
-        if (!ok) break;
+        if (alone) break;
         // O, once the last PV is done
-        const Item &it = *ip;
-        const float l = l_run + __shfl_xor_sync(kFull, l_run, 16);
-        ok = __all_sync(kFull, wait_parity(&sm.o_full[(g - 1) & 1], ((g - 1) >> 1) & 1, p.err) &&
-                                   wait_parity(&sm.scanned[ring], (taken / kRing) & 1, p.err));
-        if (!ok) break;
-        const bool dirty = sm.dirty[ring] != 0;
-        tc_fence_after_sync();
-        uint32_t o[2][32];  // dims 64 ch + 32 k + e
-        if (mine) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k) tmem_ld16x2_32<64>(lane_addr + kOCol + 32 * k, o[k]);
-#pragma unroll
-          for (int k = 0; k < 2; ++k) tmem_ld_wait(o[k]);
+        float l = l_run + __shfl_xor_sync(kFull, l_run, 16);
+        ok = ok && __all_sync(kFull, wait_parity(&sm.o_full[(g - 1) & 1], ((g - 1) >> 1) & 1, p.err) &&
+                                         wait_parity(&sm.scanned[ring], (taken / kRing) & 1, p.err));
+        if (!ok) {
+          gone();
+          break;
         }
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.o_free);
+        if (shared && mine) {
+          if (ch == 0) sm.sum_of[warp][r] = l;
+          if (either(false) < 0) break;
+          l += sm.sum_of[warp ^ 4][r];
+        }
+        const Item &it = *ip;
+        const bool dirty = sm.dirty[ring] != 0;
         // (NaN stays; a row that sees nothing gets zeros)
         float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
         if constexpr (F8) inv *= 1.f / (1 << kOffset8);
         const int64_t slot = 2 * (int64_t)blockIdx.x + it.to;
-        if (it.to < 2 && warp == 0 && lane == 0) p.cuts[blockIdx.x].dirty[it.to] = dirty;
-        if (row && it.to == 2) {
+        const int64_t at = slot * p.part_rows + c * kChunkRows + r;
+        tc_fence_after_sync();
+#pragma unroll 1
+        for (int k = pass0; k < pass1; ++k) {
+          uint32_t o[32];  // dims 64 k + 32 ch + e
+          if (mine) {
+            tmem_ld16x2_32<32>(lane_addr + kOCol + 64 * k, o);
+            tmem_ld_wait(o);
+          }
+          if (k == pass1 - 1) {
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.o_free);
+          }
+          if (!row) continue;
+          if (it.to == 2) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t w[8];
+            for (int z = 0; z < 2; ++z) {
+              uint32_t w[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              w[e] = pack_bf16x2(__uint_as_float(o[k >> 1][16 * (k & 1) + 2 * e]) * inv,
-                                 __uint_as_float(o[k >> 1][16 * (k & 1) + 2 * e + 1]) * inv);
-            uint4 *d = reinterpret_cast<uint4 *>(dst + 16 * k);
-            if (p.out_32b) {
-              st_global_32b(d, w);
-            } else {
-              d[0] = make_uint4(w[0], w[1], w[2], w[3]);
-              d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+              for (int e = 0; e < 8; ++e)
+                w[e] = pack_bf16x2(__uint_as_float(o[16 * z + 2 * e]) * inv,
+                                   __uint_as_float(o[16 * z + 2 * e + 1]) * inv);
+              uint4 *d = reinterpret_cast<uint4 *>(dst + 64 * k + 32 * ch + 16 * z);
+              if (p.out_32b) {
+                st_global_32b(d, w);
+              } else {
+                d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+              }
+            }
+            if (dirty) not_finite_fix<M>(p, it.b, it.h, n, it.L, q_row, node, dst, 64 * k + 32 * ch, 32);
+          } else {
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              uint32_t w[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(__uint_as_float(o[8 * z + e]) * inv);
+              st_global_32b(p.part_o + at * kD + 64 * k + 32 * ch + 8 * z, w);
             }
           }
-          if (dirty) not_finite_fix<M>(p, it.b, it.h, n, it.L, q_row, node, dst - 64 * ch, 64 * ch, 64);
-        } else if (row) {
-          const int64_t at = slot * p.part_rows + c * kChunkRows + r;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            uint32_t w[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              w[e] = __float_as_uint(__uint_as_float(o[k >> 2][8 * (k & 3) + e]) * inv);
-            st_global_32b(p.part_o + at * kD + 64 * ch + 8 * k, w);
-          }
-          if (ch == 0) p.part_lse[at] = l > 0.f ? m_run + log2_approx(l) : l == 0.f ? -INFINITY : l;
+        }
+        if (it.to < 2) {
+          if (row && ch == 0 && pass0 == 0)
+            p.part_lse[at] = l > 0.f ? m_run + log2_approx(l) : l == 0.f ? -INFINITY : l;
+          if (warp == 0 && lane == 0) p.cuts[blockIdx.x].dirty[it.to] = dirty;
         }
         release_item(sm, taken, lane);
         ++taken;

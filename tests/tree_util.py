@@ -152,11 +152,20 @@ class Case:
         return pkv.paged_tree_attn(self.q, self.k, self.v, *args, **a)
 
 
-def assert_close(got, ref, size, fp8):
+def bf16_weights(nodes, group):
+    """Whether a call with trees of up to so many nodes rounds its weights to bf16 (bf16 cache): the
+    rows of a KV head, in chunks of 16, are more than a tile of 8 chunks."""
+    heads = min(group, 16)
+    return cdiv(nodes, 16 // heads) * cdiv(group, 16) > 8
+
+
+def assert_close(got, ref, size, fp8, bf16=False):
     """bf16 rounding is off by 2^-8 of the value at most. A weight is off by 2^-12 of itself from its
-    score (128 products in fp32, |score| up to a few tens) and by 2^-16 (8-bit cache: 2^-11) from
-    its rounding; the sum and the normaliser each take that error of sum w |v|."""
-    bound = 2.0 ** -8 * ref.abs() + (2.0 ** -9 if fp8 else 2.0 ** -10) * size + 1e-30
+    score (128 products in fp32, |score| up to a few tens) and by 2^-16 (8-bit cache: 2^-11, where
+    weights are rounded to bf16: 2^-8) from its rounding. The sum and the normaliser each take the
+    first of these errors of sum w |v|, the sum alone the rounding's."""
+    weights = 2.0 ** -9 if fp8 else 2.0 ** -10 + (2.0 ** -8 if bf16 else 0)
+    bound = 2.0 ** -8 * ref.abs() + weights * size + 1e-30
     off = (got.double() - ref).abs()
     bad = ~(off <= bound)
     assert not bad.any(), (int(bad.sum()), float((off / bound)[bad].max()) if bad.any() else 0,
