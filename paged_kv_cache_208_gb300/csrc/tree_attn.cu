@@ -155,7 +155,6 @@ struct TreeSmem {
   int32_t warp_sums[16];
   // the sequence that the CTA's part starts in, and where that starts on the axis
   int32_t start_b, start_at, start_q0, start_n, start_L;
-  int32_t total;                   // the axis' length
 };
 static_assert(sizeof(TreeSmem<kFp8>) + 1024 <= 232448, "fits the SM");
 
@@ -256,9 +255,9 @@ __device__ __forceinline__ uint64_t mask_word(const TreeParams &p, int64_t row, 
 // V rows of the nodes that a row sees may hold values that are not finite, which the products left
 // out: what they add up to replaces the row's result. dims [d0, d0 + count), count a multiple of 4.
 template <Mode M>
-__device__ __forceinline__ void not_finite_fix(const TreeParams &p, int b, int h, int n, int L,
-                                               int64_t row, int node, uint16_t *out, int d0,
-                                               int count) {
+__device__ __noinline__ void not_finite_fix(const TreeParams &p, int b, int h, int n, int L,
+                                            int64_t row, int node, uint16_t *out, int d0,
+                                            int count) {
 #pragma unroll 1
   for (int d = d0; d < d0 + count; d += 4) {
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
@@ -354,10 +353,38 @@ struct Rows {
   }
 };
 
+// wait_parity in fewer instructions (this kernel has some thirty waits, and its warps run code of their
+// own side by side: what does not fit the instruction caches costs more than the waits): the clock
+// and the abort bit are looked at once in 256 polls, each of which waits for some time itself.
+__device__ __noinline__ bool wait_longer(uint32_t bar, uint32_t parity, unsigned int *err) {
+  uint64_t since = 0;
+  for (uint32_t n = 1;; ++n) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if (n & 255) continue;
+    if (aborted(err)) return false;
+    const uint64_t now = global_timer_ns();
+    if (since == 0) since = now;
+    if (now - since > kWaitLimitNs) {
+      record_error(err, kErrTimeout);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, unsigned int *err) {
+  return mbar_try_wait(bar, parity) || wait_longer(smem_addr(bar), parity, err);
+}
+
 template <class Smem>
 __device__ __forceinline__ const Item *wait_item(Smem &sm, uint32_t taken, unsigned int *err) {
   const int slot = taken % kRing;
-  return __all_sync(kFull, wait_parity(&sm.item_full[slot], (taken / kRing) & 1, err))
+  return __all_sync(kFull, wait_bar(&sm.item_full[slot], (taken / kRing) & 1, err))
              ? &sm.items[slot]
              : nullptr;
 }
@@ -374,10 +401,7 @@ __device__ __forceinline__ void widen16(const uint4 x, uint4 &lo, uint4 &hi) {
   hi = make_uint4(cvt_f16x2_e4m3x2(x.z), cvt_f16x2_e4m3x2_hi(x.z), cvt_f16x2_e4m3x2(x.w),
                   cvt_f16x2_e4m3x2_hi(x.w));
 }
-// whether four codes hold a NaN; and the codes with NaNs replaced by zero
-__device__ __forceinline__ bool has_nan4(uint32_t w) {
-  return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
-}
+// four codes with NaNs replaced by zero
 __device__ __forceinline__ uint32_t no_nan4(uint32_t w) {
   return w & ~__vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
 }
@@ -450,69 +474,54 @@ __global__ void __launch_bounds__(kThreads, 1)
   // sequence that the worker's part starts in is found on the way when the batch is scanned at
   // once, else by a second pass.
   const bool stop = tid == 0 && aborted(p.err);
-  Seq own{};
-  int32_t mine = 0, prefix = 0, total = 0;
-  auto warp_scan = [&](int b, bool record) -> int32_t {  // inclusive, over the warp
-    own = Seq{};
-    if (b < p.num_seqs) own = sequence(p, b, record);
-    mine = own.cost();
-    int32_t x = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int32_t y = __shfl_up_sync(kFull, x, o);
-      if (lane >= o) x += y;
-    }
-    return x;
-  };
-  auto block_scan = [&](int base) -> int32_t {  // exclusive, over the block; its sum to sm.total
-    const int32_t x = warp_scan(base + tid, blockIdx.x == 0);
-    __syncthreads();
-    if (lane == 31) sm.warp_sums[warp] = x;
-    __syncthreads();
-    const int32_t v = lane < kThreads / 32 ? sm.warp_sums[lane] : 0;
-    const int32_t before = __reduce_add_sync(kFull, lane < warp ? v : 0);
-    const int32_t all = __reduce_add_sync(kFull, v);
-    if (tid == 0) sm.total = all;
-    return before + x - mine;
-  };
-  const bool one_warp = p.num_seqs <= 32;
-  if (one_warp) {
-    const int32_t x = warp_scan(lane, blockIdx.x == 0 && warp == 0);
-    total = __shfl_sync(kFull, x, 31);
-    prefix = x - mine;
-  } else {
-    for (int base = 0; base < p.num_seqs; base += kThreads) {
-      prefix = block_scan(base);
-      __syncthreads();
-      total += sm.total;
-    }
-  }
-  const int32_t workers = min(p.workers, total);
-  const bool works = worker < workers;
-  const int32_t each = works ? total / workers : 0, rest = total - each * workers;
-  const int32_t x0 = works ? TreeParams::part_start(worker, each, rest) : 0;
-  const int32_t x1 = works ? TreeParams::part_start(worker + 1, each, rest) : 0;
-  auto found = [&](int b) {
-    if (mine > 0 && prefix <= x0 && x0 < prefix + mine) {
-      sm.start_b = b;
-      sm.start_at = prefix;
-      sm.start_q0 = own.q0;
-      sm.start_n = own.n;
-      sm.start_L = own.L;
-    }
-  };
-  if (one_warp) {
-    if (warp == kKWarp) found(lane);  // (the warp that needs it)
-  } else if (p.num_seqs <= kThreads) {
-    found(tid);
-  } else {
+  const bool one_warp = p.num_seqs <= 32, at_once = p.num_seqs <= kThreads;
+  bool works = false;
+  int32_t total = 0, each = 0, rest = 0, x0 = 0, x1 = 0;
+  for (int pass = 0; pass < 2; ++pass) {
     int32_t carry = 0;
     for (int base = 0; base < p.num_seqs; base += kThreads) {
-      prefix = carry + block_scan(base);
-      found(base + tid);
-      __syncthreads();
-      carry += sm.total;
+      const int b = base + (one_warp ? lane : tid);
+      Seq own{};
+      if (b < p.num_seqs) own = sequence(p, b, blockIdx.x == 0 && (!one_warp || warp == 0));
+      const int32_t mine = own.cost();
+      int32_t x = mine, sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int32_t y = __shfl_up_sync(kFull, x, o);
+        if (lane >= o) x += y;
+      }
+      if (one_warp) {
+        sum = __shfl_sync(kFull, x, 31);
+      } else {
+        __syncthreads();
+        if (lane == 31) sm.warp_sums[warp] = x;
+        __syncthreads();
+        const int32_t v = lane < kThreads / 32 ? sm.warp_sums[lane] : 0;
+        x += __reduce_add_sync(kFull, lane < warp ? v : 0);
+        sum = __reduce_add_sync(kFull, v);
+      }
+      const int32_t prefix = carry + x - mine;
+      carry += sum;
+      if (pass == 0 && base + kThreads >= p.num_seqs) {  // the axis' length is known
+        total = carry;
+        const int32_t workers = min(p.workers, total);
+        works = worker < workers;
+        each = works ? total / workers : 0;
+        rest = total - each * workers;
+        x0 = works ? TreeParams::part_start(worker, each, rest) : 0;
+        x1 = works ? TreeParams::part_start(worker + 1, each, rest) : 0;
+      }
+      // (batches scanned at once: by the warp that needs it, or by all)
+      if ((pass == 1 || at_once) && (!one_warp || warp == kKWarp) && mine > 0 && prefix <= x0 &&
+          x0 < prefix + mine) {
+        sm.start_b = b;
+        sm.start_at = prefix;
+        sm.start_q0 = own.q0;
+        sm.start_n = own.n;
+        sm.start_L = own.L;
+      }
     }
+    if (at_once) break;
   }
   if (tid == 0) sm.stop = stop;
   tc_fence_before_sync();
@@ -543,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int slot = g % kKSlots;
               uint64_t *const full = &sm.k_full[slot];
               ok = g < kKSlots ||
-                   wait_parity(&sm.k_empty[slot], ((g / kKSlots) - 1) & 1, p.err);
+                   wait_bar(&sm.k_empty[slot], ((g / kKSlots) - 1) & 1, p.err);
               if (!ok) break;  // (g counts the copies that were issued)
               const int32_t pos = it.key0 + j * kTile;
               const int granules = it.key1 - pos > kGranule ? 2 : 1;
@@ -584,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               const int slot = pushed % kRing;
               ok = pushed < kRing ||
-                   wait_parity(&sm.item_empty[slot], ((pushed / kRing) - 1) & 1, p.err);
+                   wait_bar(&sm.item_empty[slot], ((pushed / kRing) - 1) & 1, p.err);
               if (!ok) break;
               sm.items[slot] = nx;
               sm.dirty[slot] = 0;
@@ -627,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         Rows rows;
         while (ok) {
           const int ring = taken % kRing;
-          if (!wait_parity(&sm.item_full[ring], (taken / kRing) & 1, p.err)) break;
+          if (!wait_bar(&sm.item_full[ring], (taken / kRing) & 1, p.err)) break;
           const Item it = sm.items[ring];
           mbar_arrive(&sm.item_empty[ring]);
           ++taken;
@@ -638,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint64_t *full, *empty;
             if constexpr (F8) full = &sm.raw.v_full[slot], empty = &sm.raw.v_empty[slot];
             else full = &sm.v_full[slot], empty = &sm.v_empty[slot];
-            ok = g < kN || wait_parity(empty, ((g / kN) - 1) & 1, p.err);
+            ok = g < kN || wait_bar(empty, ((g / kN) - 1) & 1, p.err);
             if (!ok) break;
             const int32_t pos = it.key0 + j * kTile;
             const int granules = it.key1 - pos > kGranule ? 2 : 1;
@@ -672,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
       uint32_t used = 0, g = 0, fix_parity = 0;
       // Q of item k. `last`: there is none.
-      auto load_q = [&](uint32_t k, bool &last) -> bool {
+      auto load_q = [&](int k, bool &last) -> bool {
         const Item *ip = wait_item(sm, k, p.err);
         if (!ip) return false;
         last = ip->last;
@@ -684,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             p.q + (int64_t)(ip->q0 + node) * p.q_stride + (ip->h * p.group_heads + head) * kD);
         const int buf = used & 1;
         if (used >= 2 &&
-            !__all_sync(kFull, wait_parity(&sm.q_empty[buf], ((used >> 1) - 1) & 1, p.err)))
+            !__all_sync(kFull, wait_bar(&sm.q_empty[buf], ((used >> 1) - 1) & 1, p.err)))
           return false;
         ++used;
         tc_fence_after_sync();
@@ -745,48 +754,73 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&sm.q_full[buf]);
         return true;
       };
-      bool last = false, ok = load_q(0, last);
-      for (uint32_t k = 0; ok && !last; ++k) {
-        const Item &it = sm.items[k % kRing];
-        const int tiles = it.tiles, key0 = it.key0, key1 = it.key1, root = it.L - it.n;
+      // (Item -1 has no tiles, it only brings the first Q.)
+      bool last = false, ok = true;
+      for (int k = -1; ok && !last; ++k) {
+        const Item &it = sm.items[(k + kRing) % kRing];
+        const int tiles = k < 0 ? 0 : it.tiles, key0 = it.key0, key1 = it.key1, root = it.L - it.n;
         bool found = false;
-        if constexpr (F8) {
-          // Each warp widens 32 rows of a V tile: 16 codes of a row at a time, rows next to one
-          // another in a quarter warp so that neither side has bank conflicts.
-          for (int j = 0; j < tiles && ok; ++j, ++g) {
-            // (the next item's Q before this one's last tile: it is needed right after)
-            if (j == tiles - 1) ok = load_q(k + 1, last);
-            const int raw = g % kRawSlots, slot = g % kSlots;
-            ok = ok && __all_sync(kFull, wait_parity(&sm.raw.v_full[raw], (g / kRawSlots) & 1, p.err));
-            if (ok && g >= kSlots)
-              ok = __all_sync(kFull, wait_parity(&sm.v_empty[slot], ((g / kSlots) - 1) & 1, p.err));
-            if (!ok) break;
-            const int pos = key0 + j * kTile, keys = min(kTile, key1 - pos);
-            const int first = 32 * quad, rows_up = min(32, ((keys + 15) & ~15) - first);
-            const uint8_t *const src = sm.raw.v[raw] + first * 128;
-            uint8_t *const dst = sm.v[slot] + first * 128;
-            const bool nodes = pos + kTile > root;
-            // 16 rows x 8 pieces of 16 codes: four pieces of a lane in flight
+        // 8-bit cache: each warp widens 32 rows of every V tile; the next item's Q before the last
+        // one, it is needed right after. Else the next item's Q, then the tiles that hold nodes
+        // (one that ends inside a step of 16 keys among them) are looked through: the PV warp says
+        // when such a tile has landed, it waits for all of them in turn.
+        const int from = F8 || tiles == 0 ? 0 : max(0, (root - key0) / kTile);
+        const int q_at = F8 ? max(0, tiles - 1) : from;
+        for (int j = from; j < max(from + 1, tiles) && ok; ++j) {
+          if (j == q_at) ok = load_q(k + 1, last);
+          if (j >= tiles || !ok) break;
+          const int pos = key0 + j * kTile, keys = min(kTile, key1 - pos);
+          const bool nodes = pos + kTile > root;
+          if (!F8 && !nodes) continue;
+          const uint32_t at = g + j, slot = at % kSlots;
+          uint8_t *tile;  // this warp's 32 rows of it
+          if constexpr (F8) {
+            tile = sm.raw.v[at % kRawSlots] + 32 * quad * 128;
+            ok = __all_sync(kFull, wait_bar(&sm.raw.v_full[at % kRawSlots], (at / kRawSlots) & 1, p.err));
+            if (ok && at >= kSlots)
+              ok = __all_sync(kFull, wait_bar(&sm.v_empty[slot], ((at / kSlots) - 1) & 1, p.err));
+          } else {
+            tile = sm.v[slot] + 32 * quad * 128;
+            ok = __all_sync(kFull, wait_bar(&sm.v_ready[slot], (fix_parity >> slot) & 1, p.err));
+            fix_parity ^= 1u << slot;
+          }
+          if (!ok) break;
+          const int up = min(32, ((keys + 15) & ~15) - 32 * quad);  // rows that are multiplied
+          if (nodes) {
+            // 16 bytes at a time: rows past the keys zeroed, what is not finite in nodes' rows too
+            const int first = max(0, root - pos - 32 * quad);  // the first node's row
+#pragma unroll 1
+            for (int h = 0; h < (F8 ? 1 : 2); ++h) {
+#pragma unroll 1
+              for (int e = lane + first * 8; e < up * 8; e += 32) {
+                uint4 *w = reinterpret_cast<uint4 *>(tile + h * kPlane + e * 16);
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (32 * quad + (e >> 3) < keys) {
+                  x = *w;
+                  const uint4 y = F8 ? make_uint4(no_nan4(x.x), no_nan4(x.y), no_nan4(x.z), no_nan4(x.w))
+                                     : make_uint4(bf16x2_finite(x.x), bf16x2_finite(x.y),
+                                                  bf16x2_finite(x.z), bf16x2_finite(x.w));
+                  if (((x.x ^ y.x) | (x.y ^ y.y) | (x.z ^ y.z) | (x.w ^ y.w)) == 0) continue;
+                  x = y;
+                  found = true;
+                }
+                *w = x;
+              }
+            }
+            __syncwarp();
+          }
+          if constexpr (F8) {
+            // 16 rows x 8 pieces of 16 codes, four pieces of a lane in flight; rows next to one
+            // another in a quarter warp, so that neither side has bank conflicts
+            uint8_t *const dst = sm.v[slot] + 32 * quad * 128;
             const int low = lane & 7, a0 = lane >> 3;
-            for (int e = 0; e < rows_up; e += 16) {
+#pragma unroll 1
+            for (int e = 0; e < up; e += 16) {
               uint4 x[4];  // rows e + low and e + 8 + low, pieces a0 and a0 + 4
 #pragma unroll
               for (int u = 0; u < 4; ++u)
-                x[u] = *reinterpret_cast<const uint4 *>(src + (e + 8 * (u >> 1) + low) * 128 +
+                x[u] = *reinterpret_cast<const uint4 *>(tile + (e + 8 * (u >> 1) + low) * 128 +
                                                         (((a0 + 4 * (u & 1)) ^ low) << 4));
-              if (nodes) {  // rows past the keys become zeros, and NaNs of nodes
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                  const int key = first + e + 8 * (u >> 1) + low;
-                  if (key >= keys) x[u] = make_uint4(0, 0, 0, 0);
-                  if (pos + key >= root && (has_nan4(x[u].x) || has_nan4(x[u].y) ||
-                                            has_nan4(x[u].z) || has_nan4(x[u].w))) {
-                    x[u] = make_uint4(no_nan4(x[u].x), no_nan4(x[u].y), no_nan4(x[u].z),
-                                      no_nan4(x[u].w));
-                    found = true;
-                  }
-                }
-              }
 #pragma unroll
               for (int u = 0; u < 4; ++u) {
                 uint4 lo, hi;
@@ -796,48 +830,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *reinterpret_cast<uint4 *>(to + (((2 * a0 + 1) ^ low) << 4)) = hi;
               }
             }
-            fence_async_shared();
-            __syncwarp();
-            if (lane == 0) {
+          }
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (F8) {
               mbar_arrive(&sm.v_full[slot]);
-              mbar_arrive(&sm.raw.v_empty[raw]);
+              mbar_arrive(&sm.raw.v_empty[at % kRawSlots]);
+            } else {
+              mbar_arrive(&sm.v_fixed[slot]);
             }
           }
-          if (tiles == 0) ok = load_q(k + 1, last);
-        } else {
-          ok = load_q(k + 1, last);
-          // The tiles that hold nodes (one that ends inside a step of 16 keys among them): nodes'
-          // rows looked through, 16 bytes at a time, rows past the keys zeroed, by the four warps.
-          // The PV warp says when such a tile has landed: it waits for all of them in turn.
-          const int t = tid - kQWarp0 * 32;
-          for (int j = max(0, (root - key0) / kTile); j < tiles && ok; ++j) {
-            const int pos = key0 + j * kTile, keys = min(kTile, key1 - pos);
-            if (pos + kTile <= root) continue;
-            const uint32_t slot = (g + j) % kSlots;
-            ok = __all_sync(kFull, wait_parity(&sm.v_ready[slot], (fix_parity >> slot) & 1, p.err));
-            if (!ok) break;
-            fix_parity ^= 1u << slot;
-            for (int e = t + max(0, root - pos) * 16; e < ((keys + 15) & ~15) * 16; e += 128) {
-              uint4 *w = reinterpret_cast<uint4 *>(sm.v[slot] + ((e & 15) >> 3) * kPlane +
-                                                   (e >> 4) * 128 + (e & 7) * 16);
-              if ((e >> 4) >= keys) {
-                *w = make_uint4(0, 0, 0, 0);
-                continue;
-              }
-              const uint4 x = *w;
-              const uint32_t top = __vmaxu2(bf16x2_absmax(x.x, x.y), bf16x2_absmax(x.z, x.w));
-              if (max(top & 0xffffu, top >> 16) >= 0x7f80u) {
-                *w = make_uint4(bf16x2_finite(x.x), bf16x2_finite(x.y), bf16x2_finite(x.z),
-                                bf16x2_finite(x.w));
-                found = true;
-              }
-            }
-            fence_async_shared();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.v_fixed[slot]);
-          }
-          g += tiles;
         }
+        if (k < 0 || !ok) continue;
+        g += tiles;
         if (__any_sync(kFull, found) && lane == 0) sm.dirty[k % kRing] = 1;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.scanned[k % kRing]);
@@ -848,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The warp runs its loop converged and one elected lane issues (commits track the issuing
       // thread's UMMAs).
       auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
-        return __all_sync(kFull, wait_parity(bar, parity, p.err));
+        return __all_sync(kFull, wait_bar(bar, parity, p.err));
       };
       const bool s_role = warp == kSWarp;
       const uint64_t dk0 = smem_desc_sw128(smem_addr(sm.k[0]), 16, 1024);
@@ -1005,7 +1011,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < tiles; ++j, ++g) {
           const uint32_t sb = g & 1, s_addr = lane_addr + kSCol + 128 * sb;
           // warp-uniform results: the TMEM loads and stores below are .sync.aligned
-          ok = __all_sync(kFull, wait_parity(&sm.s_full[sb], (g >> 1) & 1, p.err));
+          ok = __all_sync(kFull, wait_bar(&sm.s_full[sb], (g >> 1) & 1, p.err));
           if (!ok) break;
           if (mine) {
             tc_fence_after_sync();
@@ -1084,7 +1090,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               l_run *= alpha;
               // O holds the item's tiles before this one: rescale it (never on the first tile)
               if (j > 0) {
-                ok = __all_sync(kFull, wait_parity(&sm.o_full[(g - 1) & 1], ((g - 1) >> 1) & 1, p.err));
+                ok = __all_sync(kFull, wait_bar(&sm.o_full[(g - 1) & 1], ((g - 1) >> 1) & 1, p.err));
                 if (!ok) break;
                 tc_fence_after_sync();
 #pragma unroll 1
@@ -1145,8 +1151,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (alone) break;
         // O, once the last PV is done
         float l = l_run + __shfl_xor_sync(kFull, l_run, 16);
-        ok = ok && __all_sync(kFull, wait_parity(&sm.o_full[(g - 1) & 1], ((g - 1) >> 1) & 1, p.err) &&
-                                         wait_parity(&sm.scanned[ring], (taken / kRing) & 1, p.err));
+        ok = ok && __all_sync(kFull, wait_bar(&sm.o_full[(g - 1) & 1], ((g - 1) >> 1) & 1, p.err) &&
+                                         wait_bar(&sm.scanned[ring], (taken / kRing) & 1, p.err));
         if (!ok) {
           gone();
           break;
