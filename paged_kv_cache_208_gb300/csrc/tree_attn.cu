@@ -115,12 +115,12 @@ struct Item {
 };
 static_assert(sizeof(Item) == 64, "");
 
-// What tree_combine_kernel has to know of a CTA's first item.
+// What tree_combine_kernel has to know of a unit's row tile that is cut.
 struct CutInfo {
-  int32_t parts;       // 0: this CTA's part starts with a unit, or is not the unit's first cut
+  int32_t parts;       // 0: not cut
+  int32_t worker;      // that has the unit's start
   int32_t b, h, q0, n, L, c0, chunks;
-  int32_t dirty[2];    // the slots' items met values that are not finite
-  int32_t pad[6];
+  int32_t pad[7];
 };
 static_assert(sizeof(CutInfo) == 64, "");
 
@@ -152,9 +152,9 @@ struct TreeSmem {
   uint32_t tmem_base;
   int32_t stop, gone;              // gone: a softmax warp has given up waiting
   float max_of[2][kSoftmaxWarps][kChunkRows], sum_of[kSoftmaxWarps][kChunkRows];  // shared chunks
-  int32_t warp_sums[16];
+  int2 warp_sums[16];
   // the sequence that the CTA's part starts in, and where that starts on the axis
-  int32_t start_b, start_at, start_q0, start_n, start_L;
+  int32_t start_b, start_at, start_units, start_q0, start_n, start_L;
 };
 static_assert(sizeof(TreeSmem<kFp8>) + 1024 <= 232448, "fits the SM");
 
@@ -185,9 +185,15 @@ struct TreeParams {
   int32_t per_tile;              // hkv / heads: units that share a row tile
   int32_t hb, nb, parts;         // heads and nodes of a chunk; chunks that share its nodes
   uint32_t nb_magic, hb_magic;   // x / nb is the high word of x * nb_magic, for x < 2^24
-  CutInfo *cuts;                 // one per CTA
+  // cuts: one for each unit and CTA of a worker (by_unit: there are no more units than workers), or
+  // one for each CTA, the unit that its part ends in. dirty: the CTAs' slots with items that met values
+  // that are not finite.
+  bool by_unit;
+  int32_t max_units;
+  CutInfo *cuts;
+  int32_t *dirty;
   float *part_o, *part_lse;      // [CTA][2][part_rows][kD], [CTA][2][part_rows]
-  int32_t part_rows;
+  int32_t part_rows, row_warps;  // row_warps: of tree_combine_kernel, for a row
 
   __device__ __forceinline__ int chunks_of(int n) const {
     return nb == 1 ? n * parts : (int)__umulhi(n + nb - 1, nb_magic);  // (nb > 1: one part)
@@ -290,20 +296,24 @@ __device__ __noinline__ void not_finite_fix(const TreeParams &p, int b, int h, i
 // Walks a worker's part of the axis, one item at a time (one thread).
 struct Walk {
   int32_t x, x1, at;  // where the walk is, where the part ends, where sequence b starts
+  int32_t units_at;   // units before sequence b
   int b;
   Seq s;
+  // unit: the item's unit, start: where that starts
   __device__ __forceinline__ bool next(const TreeParams &p, int head, int row_tile, Item &it,
-                                       int32_t &unit) {
-    while (x < x1) {
+                                       int32_t &unit, int32_t &start) {
+    if (x < x1) {
       while (x >= at + s.cost()) {
         at += s.cost();
+        units_at += s.units;
         s = sequence(p, ++b, false);
       }
       const int32_t rel = x - at;
       const int32_t u = s.units == 1 ? 0 : rel / s.length;
       const int32_t off = rel - u * s.length;
       const int32_t take = min(s.length - off, x1 - x);
-      unit = x - off;
+      unit = units_at + u;
+      start = x - off;
       x += take;
       const int tile = u < p.per_tile ? 0 : u / p.per_tile;
       it.last = 0;
@@ -318,7 +328,7 @@ struct Walk {
       it.key1 = (int32_t)min((int64_t)s.L, (int64_t)(off + take) * kGranule);
       it.tiles = (it.key1 - it.key0 + kTile - 1) / kTile;
       it.to = off > 0 ? 0 : take < s.length ? 1 : 2;
-      if (it.chunks > 0) return true;  // (this CTA's row tile of a smaller tree is empty)
+      return true;
     }
     return false;
   }
@@ -476,34 +486,41 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool stop = tid == 0 && aborted(p.err);
   const bool one_warp = p.num_seqs <= 32, at_once = p.num_seqs <= kThreads;
   bool works = false;
-  int32_t total = 0, each = 0, rest = 0, x0 = 0, x1 = 0;
+  int32_t total = 0, each = 0, rest = 0, x0 = 0, x1 = 0, all_units = 0;
   for (int pass = 0; pass < 2; ++pass) {
-    int32_t carry = 0;
+    int32_t carry = 0, units_carry = 0;
     for (int base = 0; base < p.num_seqs; base += kThreads) {
       const int b = base + (one_warp ? lane : tid);
       Seq own{};
       if (b < p.num_seqs) own = sequence(p, b, blockIdx.x == 0 && (!one_warp || warp == 0));
       const int32_t mine = own.cost();
-      int32_t x = mine, sum;
+      // (what has no unit has no cost)
+      int32_t x = mine, units = own.units;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int32_t y = __shfl_up_sync(kFull, x, o);
-        if (lane >= o) x += y;
+        const int32_t y = __shfl_up_sync(kFull, x, o), z = __shfl_up_sync(kFull, units, o);
+        if (lane >= o) {
+          x += y;
+          units += z;
+        }
       }
-      if (one_warp) {
-        sum = __shfl_sync(kFull, x, 31);
-      } else {
+      int32_t sum = __shfl_sync(kFull, x, 31), units_sum = __shfl_sync(kFull, units, 31);
+      if (!one_warp) {
         __syncthreads();
-        if (lane == 31) sm.warp_sums[warp] = x;
+        if (lane == 31) sm.warp_sums[warp] = make_int2(x, units);
         __syncthreads();
-        const int32_t v = lane < kThreads / 32 ? sm.warp_sums[lane] : 0;
-        x += __reduce_add_sync(kFull, lane < warp ? v : 0);
-        sum = __reduce_add_sync(kFull, v);
+        const int2 v = lane < kThreads / 32 ? sm.warp_sums[lane] : make_int2(0, 0);
+        x += __reduce_add_sync(kFull, lane < warp ? v.x : 0);
+        units += __reduce_add_sync(kFull, lane < warp ? v.y : 0);
+        sum = __reduce_add_sync(kFull, v.x);
+        units_sum = __reduce_add_sync(kFull, v.y);
       }
-      const int32_t prefix = carry + x - mine;
+      const int32_t prefix = carry + x - mine, units_at = units_carry + units - own.units;
       carry += sum;
+      units_carry += units_sum;
       if (pass == 0 && base + kThreads >= p.num_seqs) {  // the axis' length is known
         total = carry;
+        all_units = units_carry;
         const int32_t workers = min(p.workers, total);
         works = worker < workers;
         each = works ? total / workers : 0;
@@ -516,6 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           x0 < prefix + mine) {
         sm.start_b = b;
         sm.start_at = prefix;
+        sm.start_units = units_at;
         sm.start_q0 = own.q0;
         sm.start_n = own.n;
         sm.start_L = own.L;
@@ -535,14 +553,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------------ work walk and K loads
       if (lane == 0) {
         const uint64_t policy = p.at_once == 1 ? policy_evict_first() : policy_evict_last();
-        Walk w{x0, x1, sm.start_at, sm.start_b, {}};
+        Walk w{x0, x1, sm.start_at, sm.start_units, sm.start_b, {}};
         if (works) w.s.set(p, sm.start_q0, sm.start_n, sm.start_L);
         uint32_t pushed = 0, g = 0;
         bool ok = true;
-        int32_t unit;
+        bool told = false;
+        if (p.by_unit)  // no unit there
+          for (int u = all_units * p.group + blockIdx.x; u < p.max_units * p.group; u += gridDim.x)
+            p.cuts[u].parts = 0;
         // An item is handed out while the one before it is loaded, after that one's second tile
         // (the walk starts with an item of no tiles in hand).
-        Item it{}, nx;
+        Item it{}, nx{};
         Rows rows;
         while (ok && !it.last) {
           if (it.tiles > 0) rows.start(p, it.b, it.key0);
@@ -586,7 +607,23 @@ __global__ void __launch_bounds__(kThreads, 1)
               ++g;
             }
             if (j == push_at) {
-              const bool more = w.next(p, rank_head, rank_tile, nx, unit);
+              bool more;
+              do {
+                int32_t unit, start;
+                more = w.next(p, rank_head, rank_tile, nx, unit, start);
+                // the CTA with a unit's start says whether it is cut (one without rows: not)
+                const bool cut = more && nx.to == 1 && nx.chunks > 0;
+                if (more ? cut || (p.by_unit && nx.to != 0) : !p.by_unit && !told) {
+                  int4 *dst = reinterpret_cast<int4 *>(
+                      p.cuts + (p.by_unit ? unit * p.group + rank : (int)blockIdx.x));
+                  const int parts =
+                      cut ? TreeParams::part_of(start + w.s.length - 1, each, rest) - worker + 1 : 0;
+                  dst[0] = make_int4(parts, worker, nx.b, nx.h);
+                  dst[1] = make_int4(nx.q0, nx.n, nx.L, nx.c0);
+                  dst[2] = make_int4(nx.chunks, 0, 0, 0);
+                  told = true;
+                }
+              } while (more && nx.chunks <= 0);  // (this CTA's row tile of a smaller tree is empty)
               if (!more) {
                 nx = Item{};
                 nx.last = 1;
@@ -598,24 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               sm.items[slot] = nx;
               sm.dirty[slot] = 0;
               mbar_arrive(&sm.item_full[slot]);
-              if (pushed++ == 0) {
-                // the first unit's cut, if it is that unit's first one: worker - 1 has the part
-                // before
-                CutInfo cut{};
-                if (more && nx.to == 0 && unit >= TreeParams::part_start(worker - 1, each, rest)) {
-                  cut.parts = TreeParams::part_of(unit + w.s.length - 1, each, rest) - worker + 2;
-                  cut.b = nx.b;
-                  cut.h = nx.h;
-                  cut.q0 = nx.q0;
-                  cut.n = nx.n;
-                  cut.L = nx.L;
-                  cut.c0 = nx.c0;
-                  cut.chunks = nx.chunks;
-                }
-                int4 *dst = reinterpret_cast<int4 *>(p.cuts + blockIdx.x);
-                dst[0] = make_int4(cut.parts, cut.b, cut.h, cut.q0);
-                dst[1] = make_int4(cut.n, cut.L, cut.c0, cut.chunks);
-              }
+              ++pushed;
             }
           }
           it = nx;
@@ -1213,7 +1233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (it.to < 2) {
           if (row && ch == 0 && pass0 == 0)
             p.part_lse[at] = l > 0.f ? m_run + log2_approx(l) : l == 0.f ? -INFINITY : l;
-          if (warp == 0 && lane == 0) p.cuts[blockIdx.x].dirty[it.to] = dirty;
+          if (warp == 0 && lane == 0) p.dirty[slot] = dirty;
         }
         release_item(sm, taken, lane);
         ++taken;
@@ -1228,62 +1248,109 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kSWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Merges the parts of the units that a cut between two workers went through. Block (x, y): the
-// unit whose first cut is where CTA x starts, rows [8 y, +8) of its tile, a warp each.
-constexpr int kCombineRows = 8;
+// Merges the parts of the units that a cut between two workers went through. Block (x, y): cut x,
+// kCombineWarps / p.row_warps rows of its tile. A row's warps take its parts in turn, four in flight,
+// each with a running maximum; what they have is merged in shared memory. The time is that of
+// dependent loads (the cut, then all parts at once) and of blocks that find no cut: there are as many
+// cuts as units, or workers where that is fewer.
+constexpr int kCombineWarps = 8, kInFlight = 4;
 template <Mode M>
-__global__ void __launch_bounds__(kCombineRows * 32)
+__global__ void __launch_bounds__(kCombineWarps * 32)
     tree_combine_kernel(const __grid_constant__ TreeParams p) {
+  __shared__ float4 outs[kCombineWarps][32];
+  __shared__ float2 stats[kCombineWarps];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const CutInfo cut = p.cuts[blockIdx.x];
   if (aborted(p.err) || cut.parts == 0) return;
-  const int lane = threadIdx.x & 31;
-  const int t = blockIdx.y * kCombineRows + (threadIdx.x >> 5);  // row of the tile
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row_in = warp / p.row_warps, sub = warp - row_in * p.row_warps;
+  const int t = blockIdx.y * (kCombineWarps / p.row_warps) + row_in;  // row of the tile
   const int c = t / kChunkRows, r = t % kChunkRows, i = p.node_of(r);
   const int chunk = cut.c0 + c, node = p.first_node(chunk) + i;
   const int head = p.first_head(chunk) + r - i * p.hb;
-  if (c >= cut.chunks || i >= p.nb || node >= cut.n || head >= p.group_heads) return;
-  // part 0 is the last item of the worker before, the others are their workers' first items
+  const bool row = c < cut.chunks && i < p.nb && node < cut.n && head < p.group_heads;
+  // part 0 is its worker's last item, the others are their workers' first ones
+  const int rank = blockIdx.x % p.group;
   auto slot = [&](int k) -> int64_t {
-    return 2 * ((int64_t)blockIdx.x + (int64_t)(k - 1) * p.group) + (k == 0 ? 1 : 0);
+    return 2 * ((int64_t)(cut.worker + k) * p.group + rank) + (k == 0 ? 1 : 0);
   };
-  float m = -INFINITY;
-  bool dirty = false;
-  for (int k = lane; k < cut.parts; k += 32) {
-    m = fmaxf(m, p.part_lse[slot(k) * p.part_rows + t]);
-    dirty |= p.cuts[slot(k) >> 1].dirty[slot(k) & 1] != 0;
-  }
-  dirty = __any_sync(kFull, dirty);
+  float m = -INFINITY, sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+  if (row) {
+#pragma unroll 1
+    for (int k0 = sub; k0 < cut.parts; k0 += kInFlight * p.row_warps) {
+      float lse[kInFlight];
+      float4 x[kInFlight];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-  const float base = m == -INFINITY ? 0.f : m;
-  float sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int k = 0; k < cut.parts; ++k) {
-    const int64_t at = slot(k) * p.part_rows + t;
-    const float w = fast_exp2(p.part_lse[at] - base);
-    const float4 x = *reinterpret_cast<const float4 *>(p.part_o + at * kD + 4 * lane);
-    sum += w;
-    o[0] += w * x.x;
-    o[1] += w * x.y;
-    o[2] += w * x.z;
-    o[3] += w * x.w;
+      for (int u = 0; u < kInFlight; ++u) {
+        const int k = k0 + u * p.row_warps;
+        lse[u] = -INFINITY;
+        x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k < cut.parts) {
+          const int64_t at = slot(k) * p.part_rows + t;
+          lse[u] = p.part_lse[at];
+          x[u] = *reinterpret_cast<const float4 *>(p.part_o + at * kD + 4 * lane);
+        }
+      }
+      float top = m;
+#pragma unroll
+      for (int u = 0; u < kInFlight; ++u) top = fmaxf(top, lse[u]);
+      const float base = top == -INFINITY ? 0.f : top, old = fast_exp2(m - base);
+      m = top;
+      sum *= old;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) o[d] *= old;
+#pragma unroll
+      for (int u = 0; u < kInFlight; ++u) {
+        const float w = fast_exp2(lse[u] - base);  // (NaN stays)
+        sum += w;
+        o[0] += w * x[u].x;
+        o[1] += w * x[u].y;
+        o[2] += w * x[u].z;
+        o[3] += w * x[u].w;
+      }
+    }
   }
+  if (p.row_warps > 1) {
+    outs[warp][lane] = make_float4(o[0], o[1], o[2], o[3]);
+    if (lane == 0) stats[warp] = make_float2(m, sum);
+    __syncthreads();
+    if (sub != 0) return;
+    float top = m;
+    for (int k = 1; k < p.row_warps; ++k) top = fmaxf(top, stats[warp + k].x);
+    const float base = top == -INFINITY ? 0.f : top;
+    sum = 0.f;
+    o[0] = o[1] = o[2] = o[3] = 0.f;
+    for (int k = 0; k < p.row_warps; ++k) {
+      const float2 st = stats[warp + k];
+      const float4 x = outs[warp + k][lane];
+      const float w = fast_exp2(st.x - base);
+      sum += w * st.y;
+      o[0] += w * x.x;
+      o[1] += w * x.y;
+      o[2] += w * x.z;
+      o[3] += w * x.w;
+    }
+  }
+  if (!row) return;
+  bool dirty = false;
+  for (int k = lane; k < cut.parts; k += 32) dirty |= p.dirty[slot(k)] != 0;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   uint16_t *dst = p.out + ((int64_t)(cut.q0 + node) * p.hq + cut.h * p.group_heads + head) * kD;
   *reinterpret_cast<uint2 *>(dst + 4 * lane) =
       make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
-  if (dirty)
+  if (__any_sync(kFull, dirty))
     not_finite_fix<M>(p, cut.b, cut.h, cut.n, cut.L, cut.q0 + node, node, dst, 4 * lane, 4);
 }
 
 // How a call's work is cut, from what the host knows.
 struct TreePlan {
   int32_t hb, nb, parts;  // heads and nodes of a chunk, chunks that share its nodes
-  int32_t workers, group, heads, at_once, part_rows;
-  int64_t longest;        // bound of the axis
-  size_t part_o, part_lse, bytes;  // of the workspace
+  int32_t workers, group, heads, at_once, part_rows, row_warps;
+  int64_t longest, units;  // bounds of the axis and of the units
+  bool by_unit;
+  int32_t cuts;
+  size_t dirty, part_o, part_lse, bytes;  // of the workspace
 };
 TreePlan plan_tree(int32_t num_seqs, int32_t max_nodes, int32_t hq, int32_t hkv,
                    int32_t max_context, int num_sms) {
@@ -1298,14 +1365,22 @@ TreePlan plan_tree(int32_t num_seqs, int32_t max_nodes, int32_t hq, int32_t hkv,
   t.heads = 1;
   while (t.heads * 2 * t.at_once <= kMaxGroup && hkv % (t.heads * 2) == 0) t.heads *= 2;
   t.group = t.heads * t.at_once;
-  const int64_t units = (int64_t)num_seqs * (hkv / t.heads) * ((tiles + t.at_once - 1) / t.at_once);
+  const int64_t units = t.units =
+      (int64_t)num_seqs * (hkv / t.heads) * ((tiles + t.at_once - 1) / t.at_once);
   t.longest = units * std::max(1, (int)(((int64_t)max_context + kGranule - 1) / kGranule));
   t.workers = (int32_t)std::max<int64_t>(1, std::min<int64_t>(num_sms / t.group, t.longest));
   t.part_rows = (int32_t)(std::min<int64_t>(kChunks, std::max<int64_t>(1, chunks)) * kChunkRows);
+  // as many warps to a row as leave each about four of its parts (of units of equal length)
+  t.row_warps = 1;
+  while (units > 0 && t.row_warps < kCombineWarps && t.workers / units >= 4 * t.row_warps)
+    t.row_warps *= 2;
   const size_t ctas = (size_t)t.workers * t.group;
-  t.part_o = ctas * sizeof(CutInfo);
+  t.by_unit = units <= t.workers;
+  t.cuts = (int32_t)(t.by_unit ? std::max<int64_t>(1, units) * t.group : (int64_t)ctas);
+  t.dirty = (size_t)t.cuts * sizeof(CutInfo);
+  t.part_o = (t.dirty + ctas * 2 * sizeof(int32_t) + 31) / 32 * 32;
   t.part_lse = t.part_o + ctas * 2 * t.part_rows * kD * sizeof(float);
-  t.bytes = align16(t.part_lse + ctas * 2 * t.part_rows * sizeof(float));
+  t.bytes = align16(t.part_lse + ctas * 2 * t.part_rows * sizeof(float)) + 16;  // (see launch_tree)
   return t;
 }
 
@@ -1335,11 +1410,17 @@ cudaError_t launch_tree(TreeParams p, const TreePlan &t, void *workspace, cudaSt
   p.hb = t.hb;
   p.nb = t.nb;
   p.parts = t.parts;
-  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  // (the caller's 16 bytes of alignment made the 32 that the partial results are stored with)
+  uint8_t *ws =
+      reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(workspace) + 31) & ~uintptr_t(31));
   p.cuts = reinterpret_cast<CutInfo *>(ws);
+  p.by_unit = t.by_unit;
+  p.max_units = (int32_t)t.units;
+  p.dirty = reinterpret_cast<int32_t *>(ws + t.dirty);
   p.part_o = reinterpret_cast<float *>(ws + t.part_o);
   p.part_lse = reinterpret_cast<float *>(ws + t.part_lse);
   p.part_rows = t.part_rows;
+  p.row_warps = t.row_warps;
   const size_t smem = sizeof(TreeSmem<M>) + 1024;
   static bool ready[64] = {};
   int dev = 0;
@@ -1364,8 +1445,8 @@ cudaError_t launch_tree(TreeParams p, const TreePlan &t, void *workspace, cudaSt
   e = cudaLaunchKernelEx(&cfg, tree_flash_kernel<M>, km, vm, p);
   if (e != cudaSuccess || t.workers == 1) return e;
   return launch_after(tree_combine_kernel<M>,
-                      dim3((unsigned)(t.workers * t.group), (unsigned)(t.part_rows / kCombineRows)),
-                      kCombineRows * 32, stream, p);
+                      dim3((unsigned)t.cuts, (unsigned)(t.part_rows * t.row_warps / kCombineWarps)),
+                      kCombineWarps * 32, stream, p);
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
