@@ -88,7 +88,7 @@ constexpr int kSoftmaxWarps = 8;
 constexpr int kKWarp = 8, kSWarp = 9, kVWarp = 10, kPvWarp = 11, kQWarp0 = 12;
 constexpr int kThreads = 16 * 32;
 constexpr int kSlots = 2;     // of K and of V
-constexpr int kRawSlots = 3;  // of each pool's codes, 8-bit cache
+constexpr int kRawSlots = 2;  // of each pool's codes, 8-bit cache
 constexpr uint32_t kTileBytes = kTile * kD * 2;
 constexpr uint32_t kPlane = kTileBytes / 2;         // 64 dims of the tile's keys, 128-byte rows
 constexpr uint32_t kGranuleBytes = kGranule * 128;  // of a plane, or of an 8-bit pool
@@ -150,8 +150,7 @@ struct TreeSmem {
   uint64_t item_full[kRing], item_empty[kRing];
   uint64_t scanned[kRing];         // `dirty` is known
   uint32_t tmem_base;
-  int32_t stop, gone;              // gone: a softmax warp has given up waiting
-  float max_of[2][kSoftmaxWarps][kChunkRows], sum_of[kSoftmaxWarps][kChunkRows];  // shared chunks
+  int32_t stop;
   int2 warp_sums[16];
   // the sequence that the CTA's part starts in, and where that starts on the axis
   int32_t start_b, start_at, start_units, start_q0, start_n, start_L;
@@ -464,7 +463,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     sm.start_b = 0;
     sm.start_at = 0;
-    sm.gone = 0;
     fence_mbar_init();
     prefetch_tensormap(&kmap);
     prefetch_tensormap(&vmap);
@@ -969,54 +967,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       __all_sync(kFull, wait_own(bar, 0, p.err));
     } else {
       // ------------------------------------------------------------ softmax and epilogue
-      // A pass is a granule of a tile: 32 of its keys to a thread. A warp goes through both granules
-      // of its own chunk's rows; with up to four chunks warps c and c + 4 share chunk c (both reach
-      // its lanes), a granule each. The loops over passes stay loops: unrolled, a tile's code does not
-      // fit the instruction caches beside the other warps'.
-      const int ch = lane >> 4, r = lane & 15;  // half of the granule's keys, row
+      // A warp goes through a tile a granule at a time, 32 of its keys to a thread. The loops over
+      // granules stay loops: unrolled, a tile's code does not fit the instruction caches beside the
+      // other warps'. (Two warps to a chunk, a granule each, where there are few: slower for the same
+      // reason, and by what they have to agree on.)
+      const int c = warp, ch = lane >> 4, r = lane & 15;  // chunk, half of the granule's keys, row
       const int i = p.node_of(r), head_r = r - i * p.hb;
+      const uint32_t lane_addr = tmem + ((uint32_t)((c & 3) * 32 + (c >> 2) * 16) << 16);
       uint32_t taken = 0, g = 0;
-      // Two warps that share a chunk meet in named barriers. A warp that has given up waiting
-      // meets its partner once more (`gone`), wherever that one is.
-      const uint32_t pair = 1 + (warp & 3);
-      auto gone = [&]() {
-        if (lane == 0) sm.gone = 1;
-        barrier_or(pair, 64, true);
-        named_barrier_sync(pair, 64);
-      };
-      // OR over the pair. 0: no, 1: yes, -1: the partner is gone.
-      auto either = [&](bool mine) -> int {
-        if (!barrier_or(pair, 64, mine)) return 0;
-        named_barrier_sync(pair, 64);
-        return *reinterpret_cast<volatile int32_t *>(&sm.gone) ? -1 : 1;
-      };
-      while (true) {
+      bool ok = true;
+      while (ok) {
         const Item *ip = wait_item(sm, taken, p.err);
-        if (!ip) {
-          gone();
-          break;
-        }
-        if (ip->last) {
-          either(false);
-          break;
-        }
+        if (!ip || ip->last) break;
         const int ring = taken % kRing;
         const int tiles = ip->tiles, key0 = ip->key0, key1 = ip->key1, n = ip->n, root = ip->L - n;
-        const bool shared = ip->chunks <= kChunks / 2;
-        const int c = shared ? warp & 3 : warp;
-        const int pass0 = shared ? warp >> 2 : 0, pass1 = shared ? pass0 + 1 : 2;
         const bool mine = c < ip->chunks;  // (warp-uniform)
         const int chunk = ip->c0 + c, node = p.first_node(chunk) + i;
         const int head = p.first_head(chunk) + head_r;
         const int64_t q_row = (int64_t)ip->q0 + node;
         const bool row = mine && i < p.nb && node < n && head < p.group_heads;
         uint16_t *const dst = p.out + (q_row * p.hq + ip->h * p.group_heads + head) * kD;
-        const uint32_t lane_addr = tmem + ((uint32_t)((c & 3) * 32 + (c >> 2) * 16) << 16);
         if (tiles == 0) {  // nothing to see: zeros
           if (row)
-            for (int k = pass0; k < pass1; ++k)
-              for (int e = 0; e < 4; ++e)
-                reinterpret_cast<uint4 *>(dst + 64 * k + 32 * ch)[e] = make_uint4(0, 0, 0, 0);
+            for (int e = 0; e < 8; ++e)
+              reinterpret_cast<uint4 *>(dst + 64 * ch)[e] = make_uint4(0, 0, 0, 0);
           release_item(sm, taken, lane);
           ++taken;
           continue;
@@ -1027,7 +1001,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           return w == 0 ? first_word : row && 64 * w < n ? mask_word(p, q_row, node, w) : 0;
         };
         float m_run = -INFINITY, l_run = 0.f, row_scale = p.scale_log2;
-        bool ok = true, alone = false;
         for (int j = 0; j < tiles; ++j, ++g) {
           const uint32_t sb = g & 1, s_addr = lane_addr + kSCol + 128 * sb;
           // warp-uniform results: the TMEM loads and stores below are .sync.aligned
@@ -1038,7 +1011,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (F8)
               if (j == 0)
                 row_scale = p.scale_log2 * pow2f((int)sm.raw.q_power[ring][c * kChunkRows + r]);
-            // 8-bit cache: what multiplies the scores of pass k, log2 of its V scale (a granule past
+            // 8-bit cache: what multiplies the scores of granule k, log2 of its V scale (a granule past
             // the keys has no scales)
             auto factors = [&](int k, float &factor, float &v_scale) {
               factor = row_scale;
@@ -1054,7 +1027,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             float m_tile = -INFINITY;
 #pragma unroll 1
-            for (int k = pass0; k < pass1; ++k) {
+            for (int k = 0; k < 2; ++k) {
               uint32_t x[32];  // keys 64 k + 32 ch + e
               tmem_ld16x2_32<32>(s_addr + 64 * k, x);
               const int pos = key0 + j * kTile + 64 * k + 32 * ch;
@@ -1087,26 +1060,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               m_tile = fmaxf(m_tile, m);
             }
             m_tile = fmaxf(m_tile, __shfl_xor_sync(kFull, m_tile, 16));
-            bool grows = m_tile > m_run + kRescaleLog2;
-            int any;
-            if (shared) {
-              if (ch == 0) sm.max_of[sb][warp][r] = m_tile;
-              any = either(__any_sync(kFull, grows));
-              if (any < 0) {
-                alone = true;
-                break;
-              }
-              if (any) {
-                m_tile = fmaxf(m_tile, sm.max_of[sb][warp ^ 4][r]);
-                grows = m_tile > m_run + kRescaleLog2;
-              }
-            } else {
-              any = __any_sync(kFull, grows);
-            }
-            if (any) {
-              const float m_new = grows ? m_tile : m_run;
-              const float alpha = grows ? fast_exp2(m_run - m_new) : 1.f;
-              m_run = m_new;
+            const bool grows = m_tile > m_run + kRescaleLog2;
+            if (__any_sync(kFull, grows)) {
+              const float alpha = grows ? fast_exp2(m_run - m_tile) : 1.f;
+              if (grows) m_run = m_tile;
               l_run *= alpha;
               // O holds the item's tiles before this one: rescale it (never on the first tile)
               if (j > 0) {
@@ -1114,7 +1071,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 tc_fence_after_sync();
 #pragma unroll 1
-                for (int k = pass0; k < pass1; ++k) {
+                for (int k = 0; k < 2; ++k) {
                   uint32_t o[32];
                   tmem_ld16x2_32<32>(lane_addr + kOCol + 64 * k, o);
                   tmem_ld_wait(o);
@@ -1124,11 +1081,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               }
             }
-            // P, two keys to a column, over the first half of the pass's S columns; a second part
+            // P, two keys to a column, over the first half of the granule's S columns; a second part
             // over the other half
             const float base = m_run == -INFINITY ? 0.f : m_run;
 #pragma unroll 1
-            for (int k = pass0; k < pass1; ++k) {
+            for (int k = 0; k < 2; ++k) {
               uint32_t x[32];
               tmem_ld16x2_32<32>(s_addr + 64 * k, x);
               float factor, v_scale;
@@ -1168,20 +1125,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.p_full[sb]);
         }
-        if (alone) break;
+        if (!ok) break;
         // O, once the last PV is done
-        float l = l_run + __shfl_xor_sync(kFull, l_run, 16);
-        ok = ok && __all_sync(kFull, wait_bar(&sm.o_full[(g - 1) & 1], ((g - 1) >> 1) & 1, p.err) &&
-                                         wait_bar(&sm.scanned[ring], (taken / kRing) & 1, p.err));
-        if (!ok) {
-          gone();
-          break;
-        }
-        if (shared && mine) {
-          if (ch == 0) sm.sum_of[warp][r] = l;
-          if (either(false) < 0) break;
-          l += sm.sum_of[warp ^ 4][r];
-        }
+        const float l = l_run + __shfl_xor_sync(kFull, l_run, 16);
+        ok = __all_sync(kFull, wait_bar(&sm.o_full[(g - 1) & 1], ((g - 1) >> 1) & 1, p.err) &&
+                                   wait_bar(&sm.scanned[ring], (taken / kRing) & 1, p.err));
+        if (!ok) break;
         const Item &it = *ip;
         const bool dirty = sm.dirty[ring] != 0;
         // (NaN stays; a row that sees nothing gets zeros)
@@ -1191,13 +1140,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t at = slot * p.part_rows + c * kChunkRows + r;
         tc_fence_after_sync();
 #pragma unroll 1
-        for (int k = pass0; k < pass1; ++k) {
+        for (int k = 0; k < 2; ++k) {
           uint32_t o[32];  // dims 64 k + 32 ch + e
           if (mine) {
             tmem_ld16x2_32<32>(lane_addr + kOCol + 64 * k, o);
             tmem_ld_wait(o);
           }
-          if (k == pass1 - 1) {
+          if (k == 1) {
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.o_free);
@@ -1231,7 +1180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (it.to < 2) {
-          if (row && ch == 0 && pass0 == 0)
+          if (row && ch == 0)
             p.part_lse[at] = l > 0.f ? m_run + log2_approx(l) : l == 0.f ? -INFINITY : l;
           if (warp == 0 && lane == 0) p.dirty[slot] = dirty;
         }
