@@ -23,7 +23,7 @@ namespace pkv {
 namespace {
 
 constexpr int kD = 128;
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kRows = 64;       // rows of a round: in an 8-bit cache those of one group
 constexpr int kMaxHeads = 8;    // heads of a CTA
 constexpr int kLoads = 8;       // 16-byte pieces of a thread in flight
@@ -38,7 +38,8 @@ struct AcceptParams {
   int32_t table_width;
   uint8_t *k_cache, *v_cache;
   float *k_scale, *v_scale;
-  int32_t hkv, block_size, heads_per_cta;
+  int32_t hkv, block_size;
+  int32_t heads_shift;  // a CTA's heads, as a power of two
   int64_t num_blocks;
   int32_t *new_context_lens;
   unsigned int *err;
@@ -51,20 +52,23 @@ __device__ __forceinline__ uint4 rescale16(uint4 w, float ratio) {
 
 template <bool F8>
 __global__ void __launch_bounds__(kThreads) kv_accept_kernel(const AcceptParams p) {
-  constexpr int kPieces = F8 ? 8 : 16;  // of a head's row
+  constexpr int kShift = F8 ? 3 : 4;  // a head's row has 2^kShift pieces of 16 bytes
   __shared__ int64_t src_row[kRows], dst_row[kRows];  // pool rows; -1: a bad block
   __shared__ float src_scale[F8 ? kRows : 1][kMaxHeads];
   __shared__ float old_scale[kMaxHeads], new_scale[kMaxHeads];
+  __shared__ int32_t path[kThreads];  // the list's first entries
   __shared__ int32_t count;
   const int tid = threadIdx.x;
-  const int parts = (p.hkv + p.heads_per_cta - 1) / p.heads_per_cta;
+  const int per = 1 << p.heads_shift, parts = (p.hkv + per - 1) >> p.heads_shift;
   const int part = blockIdx.x % parts;
   const bool is_v = (blockIdx.x / parts) & 1;
   const int b = blockIdx.x / parts / 2;
-  const int h0 = part * p.heads_per_cta, heads = min(p.heads_per_cta, p.hkv - h0);
+  const int h0 = part * per, heads = min(per, p.hkv - h0);
   const bool first = part == 0 && !is_v;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int32_t *list = p.accepted + (int64_t)b * p.accepted_width;
+  path[tid] = tid < p.accepted_width ? *(list + tid) : -1;
   const int64_t c0 = *(p.cu + b), c1 = *(p.cu + b + 1), L = *(p.context_lens + b);
   int many = *(p.num_accepted + b);
   const int64_t n = c1 - c0, start = L - n;
@@ -79,12 +83,12 @@ __global__ void __launch_bounds__(kThreads) kv_accept_kernel(const AcceptParams 
     if (first && tid == 0) record_error(p.err, PKV_DEVERR_NODE_RANGE);
     many = 0;
   }
-  const int32_t *list = p.accepted + (int64_t)b * p.accepted_width;
+  auto entry = [&](int j) { return j < kThreads ? path[j] : *(list + j); };
   // the path ends before the first entry that is no later node of the tree
   if (tid == 0) count = many;
   __syncthreads();
   for (int j = tid; j < many; j += kThreads) {
-    const int32_t a = *(list + j), before = j ? *(list + j - 1) : -1;
+    const int32_t a = entry(j), before = j ? entry(j - 1) : -1;
     if (a <= before || a >= n) {
       atomicMin(&count, j);
       if (first) record_error(p.err, PKV_DEVERR_NODE_RANGE);
@@ -109,71 +113,69 @@ __global__ void __launch_bounds__(kThreads) kv_accept_kernel(const AcceptParams 
   auto scale_at = [&](int64_t row, int h) -> int64_t {
     return (row / p.block_size * p.hkv + h) * groups + row % p.block_size / kFp8Group;
   };
-  const int64_t row_bytes = (int64_t)p.hkv * kPieces * 16;
-  const int pieces = heads * kPieces;  // of a row
-  auto piece_of = [&](int64_t row, int i) {
-    return reinterpret_cast<uint4 *>(pool + row * row_bytes + h0 * kPieces * 16) + i;
-  };
+  const int64_t row_pieces = (int64_t)p.hkv << kShift;
+  // A thread always has the same piece of a row (kThreads is a multiple of a row's pieces): it
+  // counts those of absent heads too, so that a row's number is a shift.
+  const int shift = p.heads_shift + kShift, piece = tid & ((1 << shift) - 1), h = piece >> kShift;
+  const int row_step = kThreads >> shift, r0 = tid >> shift;
+  const bool any = h < heads;
+  uint4 *const base = reinterpret_cast<uint4 *>(pool) + (h0 << kShift) + piece;
+  auto piece_of = [&](int64_t row) { return base + row * row_pieces; };
   for (int j0 = 0, rows; j0 < many; j0 += rows) {
     rows = min(kRows, many - j0);
     // (of an 8-bit cache: the rows that go to one group)
     if (F8) rows = min(rows, kFp8Group - (int)((start + j0) % kFp8Group));
     if (tid < rows) {
-      src_row[tid] = pool_row(start + *(list + j0 + tid));
+      src_row[tid] = pool_row(start + entry(j0 + tid));
       dst_row[tid] = pool_row(start + j0 + tid);
     }
     __syncthreads();
-    const int64_t d0 = dst_row[0];
-    if (F8 && d0 >= 0) {
-      if (tid < heads) {
-        old_scale[tid] = scales[scale_at(d0, h0 + tid)];
-        new_scale[tid] = old_scale[tid];
-      }
-      for (int i = tid; i < rows * heads; i += kThreads)
-        src_scale[i / heads][i % heads] =
-            src_row[i / heads] >= 0 ? scales[scale_at(src_row[i / heads], h0 + i % heads)] : 0.f;
-      __syncthreads();
-      if (tid < heads) {
-        float s = old_scale[tid];
-        for (int i = 0; i < rows; ++i) s = fmaxf(s, src_scale[i][tid]);
-        new_scale[tid] = s;
-        if (s > old_scale[tid]) scales[scale_at(d0, h0 + tid)] = s;
-      }
-      __syncthreads();
-      // the rows of the group from before the tree, at the scale that grew
-      const int before = j0 == 0 ? (int)(start % kFp8Group) : 0;
-      for (int i = tid; i < before * pieces; i += kThreads) {
-        const int h = i % pieces / kPieces;
-        if (new_scale[h] > old_scale[h]) {
-          uint4 *w = piece_of(d0 - before + i / pieces, i % pieces);
-          *w = rescale16(*w, old_scale[h] / new_scale[h]);
-        }
-      }
-    }
-    const int all = rows * pieces;
-    for (int i0 = 0; i0 < all; i0 += kThreads * kLoads) {
+    for (int i0 = 0; i0 < rows; i0 += row_step * kLoads) {
       uint4 x[kLoads];
 #pragma unroll
       for (int u = 0; u < kLoads; ++u) {
-        const int i = i0 + u * kThreads + tid;
+        const int r = i0 + u * row_step + r0;
         x[u] = make_uint4(0, 0, 0, 0);
-        if (i < all && src_row[i / pieces] >= 0) x[u] = *piece_of(src_row[i / pieces], i % pieces);
+        if (any && r < rows && src_row[r] >= 0) x[u] = *piece_of(src_row[r]);
+      }
+      const int64_t d0 = dst_row[0];
+      if (F8 && i0 == 0 && d0 >= 0) {  // (while the rows are on their way)
+        if (tid < heads) old_scale[tid] = scales[scale_at(d0, h0 + tid)];
+        for (int i = tid; i < rows << p.heads_shift; i += kThreads) {
+          const int r = i >> p.heads_shift, k = i & (per - 1);
+          src_scale[r][k] =
+              k < heads && src_row[r] >= 0 ? scales[scale_at(src_row[r], h0 + k)] : 0.f;
+        }
+        __syncthreads();
+        if (tid < heads) {
+          float s = old_scale[tid];
+          for (int i = 0; i < rows; ++i) s = fmaxf(s, src_scale[i][tid]);
+          new_scale[tid] = s;
+          if (s > old_scale[tid]) scales[scale_at(d0, h0 + tid)] = s;
+        }
+        __syncthreads();
+        // the rows of the group from before the tree, at the scale that grew
+        const int before = j0 == 0 ? (int)(start % kFp8Group) : 0;
+        if (any && new_scale[h] > old_scale[h])
+          for (int r = r0; r < before; r += row_step) {
+            uint4 *w = piece_of(d0 - before + r);
+            *w = rescale16(*w, old_scale[h] / new_scale[h]);
+          }
       }
       __syncthreads();  // (each pass is read before it is written)
 #pragma unroll
       for (int u = 0; u < kLoads; ++u) {
-        const int i = i0 + u * kThreads + tid, r = i / pieces;
-        if (i >= all || dst_row[r] < 0) continue;
+        const int r = i0 + u * row_step + r0;
+        if (!any || r >= rows || dst_row[r] < 0) continue;
         bool same = src_row[r] == dst_row[r];
         if (F8) {
-          const int h = i % pieces / kPieces;
           const float ratio = src_scale[r][h] / new_scale[h];
           if (ratio < 1.f) {
             x[u] = rescale16(x[u], ratio);
             same = false;
           }
         }
-        if (!same) *piece_of(dst_row[r], i % pieces) = x[u];
+        if (!same) *piece_of(dst_row[r]) = x[u];
       }
       __syncthreads();
     }
@@ -224,11 +226,12 @@ extern "C" pkv_status pkv_kv_accept(const int32_t *accepted, int32_t accepted_wi
   prm.num_blocks = num_blocks;
   prm.new_context_lens = new_context_lens;
   prm.err = err;
-  // as many heads to a CTA as still leave every SM about four CTAs
-  prm.heads_per_cta = (int32_t)std::max<int64_t>(
-      1, std::min<int64_t>(kMaxHeads, 2 * (int64_t)num_seqs * num_kv_heads / (4 * num_sms)));
-  const int64_t grid =
-      2 * (int64_t)num_seqs * ((num_kv_heads + prm.heads_per_cta - 1) / prm.heads_per_cta);
+  // as many heads to a CTA as still leave every SM about six CTAs
+  while ((2 << prm.heads_shift) <= kMaxHeads && (1 << prm.heads_shift) < num_kv_heads &&
+         2 * (int64_t)num_seqs * num_kv_heads >> (prm.heads_shift + 1) >= 6 * (int64_t)num_sms)
+    ++prm.heads_shift;
+  const int64_t grid = 2 * (int64_t)num_seqs *
+                       ((num_kv_heads + (1 << prm.heads_shift) - 1) >> prm.heads_shift);
   if (grid > INT32_MAX) return PKV_ERR_UNSUPPORTED;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e =
