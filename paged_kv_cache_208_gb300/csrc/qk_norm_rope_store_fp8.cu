@@ -11,11 +11,20 @@
 // between them; here a key has 4 significant bits left, and a second rounding before those
 // would only add to the error of the first.)
 //
-// As in kv_store_fp8 one CTA owns a run (the new rows of one sequence that lie in one group of 64
-// positions) of some of the K or V heads, so that nothing else touches their scales; other CTAs
-// take the run's query heads. A thread holds the 8 + 8 values of a row that turn into one another.
-// A step of one token per sequence takes half a warp per head row. Bound by HBM: a row is read
-// once, 2 bytes a value, and written once.
+// Bound by HBM: a row is read once, 2 bytes a value, and written once. As in kv_store_fp8 a CTA
+// owns the K or V heads it takes of a run (the new rows of one sequence that lie in one group of 64
+// positions), so that nothing else touches their scales; it goes through them a head at a time, the
+// next one's rows on their way. Four lanes hold a head's row, each the 16 + 16 values that turn
+// into one another, in 32-byte loads. Another CTA takes the run's query heads, a warp to a token,
+// eight heads at a time: what it reads and writes is contiguous, and the lanes of different heads
+// read the same cosines and weights at once.
+// 132k tokens of 16 + 2 x 8 heads take 329 us (6.0 TB/s): 460 us with eight lanes to a row and a
+// quarter of a head's 64 rows in each thread, 357 us with half of them and the next head loaded
+// ahead, 350 us with two values to an instruction, 344 us with the queries by tokens. Three CTAs of
+// 80 registers fit an SM; two of 128 take 348 us, four of 64 spill and take 378 us.
+//
+// A step of one token per sequence takes half a warp per head row: 8 tokens 2.7 us, the latency
+// of a launch and of three loads that depend on one another.
 #include <math.h>
 
 #include <algorithm>
@@ -49,29 +58,93 @@ struct AppendParams {
   float *k_scale, *v_scale;
   int32_t hq, hkv, block_size;
   int64_t num_blocks;
+  bool wide;  // rows and q_out lie at multiples of 32 bytes
   unsigned int *err;
 };
 
-__device__ __forceinline__ void widen8(const uint4 w, float (&f)[8]) {
-  f[0] = bf16_lo(w.x), f[1] = bf16_hi(w.x), f[2] = bf16_lo(w.y), f[3] = bf16_hi(w.y);
-  f[4] = bf16_lo(w.z), f[5] = bf16_hi(w.z), f[6] = bf16_lo(w.w), f[7] = bf16_hi(w.w);
+// Two fp32 values in a 64-bit register: one instruction then works on both.
+__device__ __forceinline__ uint64_t pair_of(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
 }
-__device__ __forceinline__ uint4 round8(const float (&f)[8]) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                    pack_bf16x2(f[6], f[7]));
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
 }
-__device__ __forceinline__ uint2 quantize8(const float (&f)[8], float inv) {
-  return make_uint2(cvt_e4m3x2(f[0] * inv, f[1] * inv) | cvt_e4m3x2(f[2] * inv, f[3] * inv) << 16,
-                    cvt_e4m3x2(f[4] * inv, f[5] * inv) | cvt_e4m3x2(f[6] * inv, f[7] * inv) << 16);
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
 }
-// largest finite |f| of eight values, as fp32 bits, or above
-__device__ __forceinline__ uint32_t finite_max8(uint32_t m, const float (&f)[8]) {
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  return r;
+}
+// 32 bytes that are read once; `wide`: the address is a multiple of 32, not only of 16
+__device__ __forceinline__ void ld_once_32b(const uint8_t *p, uint32_t (&w)[8], bool wide) {
+  if (wide) {
+    asm volatile(
+        "ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]),
+          "=r"(w[7])
+        : "l"(p)
+        : "memory");
+  } else {
+    const uint4 x = ld_once_u4(reinterpret_cast<const uint4 *>(p));
+    const uint4 y = ld_once_u4(reinterpret_cast<const uint4 *>(p) + 1);
+    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w, w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
+  }
+}
+
+// 2 N values, a pair to a register pair
+template <int N>
+struct Pairs {
+  uint64_t v[N];
+};
+template <int N>
+__device__ __forceinline__ Pairs<N> widen(const uint32_t (&w)[N]) {
+  Pairs<N> r;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t a = __float_as_uint(f[i]) & 0x7fffffffu;
-    m = max(m, a < 0x7f800000u ? a : 0u);
+  for (int k = 0; k < N; ++k) r.v[k] = pair_of(bf16_lo(w[k]), bf16_hi(w[k]));
+  return r;
+}
+template <int N>
+__device__ __forceinline__ void round_to_bf16(const Pairs<N> &x, uint32_t (&w)[N]) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const float2 f = unpair(x.v[k]);
+    w[k] = pack_bf16x2(f.x, f.y);
+  }
+}
+// codes of four values
+__device__ __forceinline__ uint32_t quantize4(uint64_t x, uint64_t y, uint64_t inv) {
+  const float2 f = unpair(mul2(x, inv)), g = unpair(mul2(y, inv));
+  return cvt_e4m3x2(f.x, f.y) | cvt_e4m3x2(g.x, g.y) << 16;
+}
+// Largest finite |x|, as fp32 bits. fmaxf passes over NaN; an infinity is rare and sends the values
+// through again.
+template <int N>
+__device__ __noinline__ float finite_max_again(const Pairs<N> x) {
+  float m = 0.f;
+  for (int k = 0; k < N; ++k) {
+    const float2 f = unpair(x.v[k]);
+    if (fabsf(f.x) < INFINITY) m = fmaxf(m, fabsf(f.x));
+    if (fabsf(f.y) < INFINITY) m = fmaxf(m, fabsf(f.y));
   }
   return m;
+}
+template <int N>
+__device__ __forceinline__ float finite_max(const Pairs<N> &x) {
+  float m = 0.f;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const float2 f = unpair(x.v[k]);
+    m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
+  }
+  return m < INFINITY ? m : finite_max_again(x);
 }
 // The scale for a group whose largest finite |x| has the fp32 bits `amax`: fp8_scale_exp's rule
 // with fp32's mantissa.
@@ -79,56 +152,112 @@ __device__ __forceinline__ float scale_of(uint32_t amax) {
   const int e = (int)(amax >> 23) - 135 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0);
   return pow2f(max(e, kFp8MinExp));
 }
-
-// n of the values [8 i, +8) and [64 + 8 i, +8) of a row, given its sum of squares
-__device__ __forceinline__ void normalise(const AppendParams &p, const uint8_t *weight, float ss,
-                                          int i, float (&a)[8], float (&b)[8]) {
-  const float rs = rsqrtf(ss * (1.f / kD) + p.eps);
-  float wa[8], wb[8];
-  widen8(*reinterpret_cast<const uint4 *>(weight + 16 * i), wa);
-  widen8(*reinterpret_cast<const uint4 *>(weight + kD + 16 * i), wb);
+template <int N>
+__device__ __forceinline__ float square_sum(const Pairs<N> &x, uint64_t s = 0) {  // (0.f, 0.f)
 #pragma unroll
-  for (int d = 0; d < 8; ++d) {
-    a[d] = a[d] * rs * wa[d];
-    b[d] = b[d] * rs * wb[d];
+  for (int k = 0; k < N; ++k) s = fma2(x.v[k], x.v[k], s);
+  const float2 f = unpair(s);
+  return f.x + f.y;
+}
+
+// A quarter of a head's row: the values [16 i, +16) and [64 + 16 i, +16).
+struct Quarter {
+  Pairs<8> a, b;
+};
+// n of them, the four lanes of a row together
+__device__ __forceinline__ void normalise(const uint8_t *weight, float eps, int i, Quarter &x) {
+  float ss = square_sum(x.a) + square_sum(x.b);
+  ss += __shfl_xor_sync(kFull, ss, 1);
+  ss += __shfl_xor_sync(kFull, ss, 2);
+  const float rs = rsqrtf(ss * (1.f / kD) + eps);
+  const uint64_t rs2 = pair_of(rs, rs);
+#pragma unroll
+  for (int k = 0; k < 8; k += 4) {
+    const uint4 u = *reinterpret_cast<const uint4 *>(weight + 32 * i + 4 * k);
+    const uint4 v = *reinterpret_cast<const uint4 *>(weight + kD + 32 * i + 4 * k);
+    const Pairs<4> wa = widen<4>({u.x, u.y, u.z, u.w}), wb = widen<4>({v.x, v.y, v.z, v.w});
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      x.a.v[k + d] = mul2(mul2(x.a.v[k + d], rs2), wa.v[d]);
+      x.b.v[k + d] = mul2(mul2(x.b.v[k + d], rs2), wb.v[d]);
+    }
   }
 }
 // y of them, the position's row of the cos/sin cache being `cs`
-__device__ __forceinline__ void rotate(const float *cs, int i, float (&a)[8], float (&b)[8]) {
+__device__ __forceinline__ void rotate(const float *cs, int i, Quarter &x) {
 #pragma unroll
-  for (int d = 0; d < 8; d += 4) {
-    const float4 c = *reinterpret_cast<const float4 *>(cs + 8 * i + d);
-    const float4 s = *reinterpret_cast<const float4 *>(cs + kD / 2 + 8 * i + d);
-    const float cc[4] = {c.x, c.y, c.z, c.w}, sc[4] = {s.x, s.y, s.z, s.w};
+  for (int k = 0; k < 8; k += 2) {
+    const float4 c = *reinterpret_cast<const float4 *>(cs + 16 * i + 2 * k);
+    const float4 s = *reinterpret_cast<const float4 *>(cs + kD / 2 + 16 * i + 2 * k);
+    const uint64_t cc[2] = {pair_of(c.x, c.y), pair_of(c.z, c.w)};
+    const uint64_t sn[2] = {pair_of(s.x, s.y), pair_of(s.z, s.w)};
+    const uint64_t minus[2] = {pair_of(-s.x, -s.y), pair_of(-s.z, -s.w)};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float x = a[d + k], y = b[d + k];
-      a[d + k] = x * cc[k] - y * sc[k];
-      b[d + k] = y * cc[k] + x * sc[k];
+    for (int d = 0; d < 2; ++d) {
+      const uint64_t a = x.a.v[k + d], b = x.b.v[k + d];
+      x.a.v[k + d] = fma2(a, cc[d], mul2(b, minus[d]));
+      x.b.v[k + d] = fma2(b, cc[d], mul2(a, sn[d]));
     }
   }
 }
 
-constexpr int kRunThreads = 128;
+constexpr int kRunThreads = 256;
 constexpr int kRunWarps = kRunThreads / 32;
-constexpr int kRowsPerPass = kRunThreads / 8;
-constexpr int kPasses = kFp8Group / kRowsPerPass;
+static_assert(kRunThreads == 4 * kFp8Group);
 
-// The CTAs of a run: parts of its query, key and value heads.
-__global__ void __launch_bounds__(kRunThreads)
+// The query heads of rows t0 .. t0 + rows - 1, a warp to a row at a time, which lies contiguous in
+// memory, and four lanes to a head.
+__device__ __forceinline__ void append_queries(const AppendParams &p, int64_t t0, int rows, int warp,
+                                               int lane) {
+  const int i4 = lane & 3;
+  for (int r = warp; r < rows; r += kRunWarps) {
+    const int64_t t = t0 + r, pos = *(p.positions + t);
+    const uint8_t *const src = p.qkv + t * p.tok_stride + 32 * i4;
+    uint8_t *const dst = p.q_out + t * p.hq * (2 * kD) + 32 * i4;
+    if (pos < 0 || pos >= p.max_position) {
+      if (lane == 0) record_error(p.err, PKV_DEVERR_POSITION_RANGE);
+      continue;
+    }
+#pragma unroll 1
+    for (int g = 0; g < p.hq; g += 8) {
+      const int h = g + (lane >> 2);
+      uint32_t w[2][8];
+      const uint8_t *const from = src + min(h, p.hq - 1) * (2 * kD);
+      ld_once_32b(from, w[0], p.wide);
+      ld_once_32b(from + kD, w[1], p.wide);
+      Quarter x{widen(w[0]), widen(w[1])};
+      if (p.q_weight) normalise(p.q_weight, p.eps, i4, x);
+      rotate(p.cos_sin + pos * kD, i4, x);
+      if (h >= p.hq) continue;
+      round_to_bf16(x.a, w[0]);
+      round_to_bf16(x.b, w[1]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        uint8_t *const d = dst + h * (2 * kD) + e * kD;
+        if (p.wide) {
+          st_global_32b(d, w[e]);
+        } else {
+          reinterpret_cast<uint4 *>(d)[0] = make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
+          reinterpret_cast<uint4 *>(d)[1] = make_uint4(w[e][4], w[e][5], w[e][6], w[e][7]);
+        }
+      }
+    }
+  }
+}
+
+// The CTAs of a run: one for its query heads, the others for parts of its key and value heads.
+__global__ void __launch_bounds__(kRunThreads, 3)
     append_run_kernel(const AppendParams p, int heads_per_cta) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ uint32_t warp_max[2][kRunWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int qparts = (p.hq + heads_per_cta - 1) / heads_per_cta;
-  const int kparts = (p.hkv + heads_per_cta - 1) / heads_per_cta;
-  const int parts = qparts + 2 * kparts;
+  const int heads = p.hq + 2 * p.hkv;  // of a projection row: queries, keys, values
+  const int parts = 1 + (2 * p.hkv + heads_per_cta - 1) / heads_per_cta;
   const int64_t r = blockIdx.x / parts;
-  int part = (int)(blockIdx.x % parts);
-  const int kind = part < qparts ? 0 : part < qparts + kparts ? 1 : 2;  // query, key, value
-  part -= kind == 0 ? 0 : kind == 1 ? qparts : qparts + kparts;
-  const int h0 = part * heads_per_cta, h1 = min(kind ? p.hkv : p.hq, h0 + heads_per_cta);
+  const int part = (int)(blockIdx.x % parts);
+  const int h0 = p.hq + (part - 1) * heads_per_cta, h1 = min(heads, h0 + heads_per_cta);
+  const bool turned = h0 < p.hq + p.hkv;  // it has key heads
   const int n = find_sequence(p.cu, p.num_seqs, r, lane);
   const int64_t c0 = *(p.cu + n), c1 = *(p.cu + n + 1), ctx = *(p.context_lens + n);
   const int64_t j = r - run_base((int32_t)c0, n);
@@ -147,82 +276,52 @@ __global__ void __launch_bounds__(kRunThreads)
   const int64_t end = min(ctx, (group + 1) * kFp8Group);
   if (j < 0 || begin >= end) return;
   const int rows = (int)(end - begin);
-  const int i8 = tid & 7, row0 = tid >> 3;
-  const int64_t tok0 = c0 + begin - start + row0;
+  if (part == 0) {
+    if (!aborted(p.err)) append_queries(p, c0 + begin - start, rows, warp, lane);
+    return;
+  }
+  const int i4 = tid & 3, row0 = tid >> 2;
+  const bool here = row0 < rows;
+  const int64_t tok = c0 + begin - start + row0;
+  const uint8_t *const src = p.qkv + tok * p.tok_stride + 32 * i4;
+  uint32_t next[2][8] = {};
+  if (here) {
+    ld_once_32b(src + h0 * (2 * kD), next[0], p.wide);
+    ld_once_32b(src + h0 * (2 * kD) + kD, next[1], p.wide);
+  }
+  const float *cs = nullptr;  // of this thread's row; nullptr: past the run, or a bad position
+  if (turned && here) {
+    const int64_t pos = *(p.positions + tok);
+    if (pos >= 0 && pos < p.max_position) cs = p.cos_sin + pos * kD;
+    else if (i4 == 0) record_error(p.err, PKV_DEVERR_POSITION_RANGE);
+  }
+  const int64_t blk = *(p.block_tables + (int64_t)n * p.table_width + begin / p.block_size);
+  const bool blk_ok = blk >= 0 && blk < p.num_blocks;
+  if (!blk_ok && tid == 0) record_error(p.err, PKV_DEVERR_BLOCK_RANGE);
   // an earlier wait gave up somewhere: write nothing (decided by the CTA together)
-  if (__syncthreads_or(tid == 0 && aborted(p.err))) return;
-  const float *cs[kPasses];  // of this thread's rows; nullptr: past the run, or a bad position
-#pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    cs[i] = nullptr;
-    if (kind < 2 && row0 + i * kRowsPerPass < rows) {
-      const int64_t pos = *(p.positions + tok0 + i * kRowsPerPass);
-      if (pos >= 0 && pos < p.max_position) cs[i] = p.cos_sin + pos * kD;
-      else if (i8 == 0) record_error(p.err, PKV_DEVERR_POSITION_RANGE);
-    }
-  }
-  int64_t blk = 0;
-  if (kind) {
-    blk = *(p.block_tables + (int64_t)n * p.table_width + begin / p.block_size);
-    if (blk < 0 || blk >= p.num_blocks) {
-      if (tid == 0) record_error(p.err, PKV_DEVERR_BLOCK_RANGE);
-      return;
-    }
-  }
+  if (__syncthreads_or(tid == 0 && aborted(p.err)) || !blk_ok) return;
   const int in_block = (int)(begin % p.block_size);
   const int before = in_block % kFp8Group;  // rows of the group from before the call
   const int64_t rstride = (int64_t)p.hkv * kD;
-  float *const scales = kind == 2 ? p.v_scale : p.k_scale;
-  uint8_t *const dst0 =
-      (kind == 2 ? p.v_cache : p.k_cache) + (blk * p.block_size + in_block) * rstride;
-  const uint8_t *weight = kind == 0 ? p.q_weight : p.k_weight;
-  const uint8_t *const src = p.qkv + tok0 * p.tok_stride + 16 * i8 +
-                             (kind == 0 ? 0 : kind == 1 ? p.hq : p.hq + p.hkv) * (2 * kD);
+  const int64_t dst0 = (blk * p.block_size + in_block) * rstride;
   int buf = 0;
-  for (int h = h0; h < h1; ++h) {
-    float a[kPasses][8], b[kPasses][8];
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-      if (row0 + i * kRowsPerPass < rows) {
-        const uint8_t *x = src + i * kRowsPerPass * p.tok_stride + h * (2 * kD);
-        lo = ld_once_u4(reinterpret_cast<const uint4 *>(x));
-        hi = ld_once_u4(reinterpret_cast<const uint4 *>(x + kD));
-      }
-      widen8(lo, a[i]);
-      widen8(hi, b[i]);
+#pragma unroll 1
+  for (int row = h0; row < h1; ++row) {
+    const bool is_v = row >= p.hq + p.hkv;
+    const int h = row - p.hq - (is_v ? p.hkv : 0);
+    Quarter x{widen(next[0]), widen(next[1])};
+    if (here && row + 1 < h1) {  // in flight while this head is worked on
+      ld_once_32b(src + (row + 1) * (2 * kD), next[0], p.wide);
+      ld_once_32b(src + (row + 1) * (2 * kD) + kD, next[1], p.wide);
     }
-    if (kind < 2) {
-#pragma unroll
-      for (int i = 0; i < kPasses; ++i) {
-        if (weight) {
-          float ss = 0.f;
-#pragma unroll
-          for (int d = 0; d < 8; ++d) ss = fmaf(a[i][d], a[i][d], fmaf(b[i][d], b[i][d], ss));
-#pragma unroll
-          for (int o = 1; o < 8; o <<= 1) ss += __shfl_xor_sync(kFull, ss, o);
-          normalise(p, weight, ss, i8, a[i], b[i]);
-        }
-        if (cs[i]) rotate(cs[i], i8, a[i], b[i]);
-      }
+    if (!is_v) {
+      if (p.k_weight) normalise(p.k_weight, p.eps, i4, x);
+      if (cs) rotate(cs, i4, x);
     }
-    if (kind == 0) {
-#pragma unroll
-      for (int i = 0; i < kPasses; ++i)
-        if (cs[i]) {
-          uint4 *q = reinterpret_cast<uint4 *>(
-              p.q_out + ((tok0 + i * kRowsPerPass) * p.hq + h) * (2 * kD) + 16 * i8);
-          q[0] = round8(a[i]);
-          q[kD / 16] = round8(b[i]);
-        }
-      continue;
-    }
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i)
-      if (kind == 2 ? row0 + i * kRowsPerPass < rows : cs[i] != nullptr)
-        m = finite_max8(finite_max8(m, a[i]), b[i]);
-    m = __reduce_max_sync(kFull, m);
+    const bool good = is_v ? here : cs != nullptr;
+    float *const scales = is_v ? p.v_scale : p.k_scale;
+    uint32_t m = __reduce_max_sync(
+        kFull, good ? __float_as_uint(fmaxf(finite_max(x.a), finite_max(x.b))) : 0u);
     if (lane == 0) warp_max[buf][warp] = m;
     __syncthreads();
 #pragma unroll
@@ -230,7 +329,7 @@ __global__ void __launch_bounds__(kRunThreads)
     buf ^= 1;  // (the next use of this half is a barrier away)
     const int64_t sc = (blk * p.hkv + h) * (p.block_size / kFp8Group) + in_block / kFp8Group;
     float scale = scale_of(m);
-    uint8_t *dst = dst0 + h * kD;
+    uint8_t *dst = (is_v ? p.v_cache : p.k_cache) + dst0 + h * kD;
     if (before) {
       const float old = scales[sc];
       scale = fmaxf(scale, old);
@@ -249,14 +348,18 @@ __global__ void __launch_bounds__(kRunThreads)
       __syncthreads();  // every thread has read the old scale
     }
     if (tid == 0) scales[sc] = scale;
-    const float inv = 1.f / scale;
+    const uint64_t inv = pair_of(1.f / scale, 1.f / scale);
+    if (good) {
+      uint4 *const d = reinterpret_cast<uint4 *>(dst + row0 * rstride + 16 * i4);
+      uint32_t q[2][4];
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i)
-      if (kind == 2 ? row0 + i * kRowsPerPass < rows : cs[i] != nullptr) {
-        uint8_t *d = dst + (row0 + i * kRowsPerPass) * rstride + 8 * i8;
-        *reinterpret_cast<uint2 *>(d) = quantize8(a[i], inv);
-        *reinterpret_cast<uint2 *>(d + kD / 2) = quantize8(b[i], inv);
+      for (int k = 0; k < 4; ++k) {
+        q[0][k] = quantize4(x.a.v[2 * k], x.a.v[2 * k + 1], inv);
+        q[1][k] = quantize4(x.b.v[2 * k], x.b.v[2 * k + 1], inv);
       }
+      d[0] = make_uint4(q[0][0], q[0][1], q[0][2], q[0][3]);
+      d[kD / 32] = make_uint4(q[1][0], q[1][1], q[1][2], q[1][3]);
+    }
   }
 }
 
@@ -272,39 +375,46 @@ __global__ void __launch_bounds__(kTokenWarps * 32) append_token_kernel(const Ap
   const int n = any ? (int)(unit / heads) : 0, row = any ? (int)(unit % heads) : 0;
   const int kind = row < p.hq ? 0 : row < p.hq + p.hkv ? 1 : 2;
   const int h = row - (kind == 0 ? 0 : kind == 1 ? p.hq : p.hq + p.hkv);
-  float x[8];
-  widen8(ld_once_u4(reinterpret_cast<const uint4 *>(p.qkv + n * p.tok_stride + row * (2 * kD) + 16 * i)), x);
+  auto eight = [](const uint4 w) { return widen<4>({w.x, w.y, w.z, w.w}); };
+  Pairs<4> x = eight(
+      ld_once_u4(reinterpret_cast<const uint4 *>(p.qkv + n * p.tok_stride + row * (2 * kD) + 16 * i)));
   const int64_t pos = *(p.positions + n), ctx = *(p.context_lens + n);
   const bool pos_ok = pos >= 0 && pos < p.max_position;
   const bool stop = __any_sync(kFull, aborted(p.err));
   if (any && i == 0 && row == 0 && !pos_ok) record_error(p.err, PKV_DEVERR_POSITION_RANGE);
   if (kind < 2) {
     const uint8_t *weight = kind == 0 ? p.q_weight : p.k_weight;
-    float ss = 0.f;
-#pragma unroll
-    for (int d = 0; d < 8; ++d) ss = fmaf(x[d], x[d], ss);
+    float ss = square_sum(x);
 #pragma unroll
     for (int o = 1; o < 16; o <<= 1) ss += __shfl_xor_sync(0xffffu << (lane & 16), ss, o);
     if (weight) {
       const float rs = rsqrtf(ss * (1.f / kD) + p.eps);
-      float w[8];
-      widen8(*reinterpret_cast<const uint4 *>(weight + 16 * i), w);
+      const Pairs<4> w = eight(*reinterpret_cast<const uint4 *>(weight + 16 * i));
 #pragma unroll
-      for (int d = 0; d < 8; ++d) x[d] = x[d] * rs * w[d];
+      for (int k = 0; k < 4; ++k) x.v[k] = mul2(mul2(x.v[k], pair_of(rs, rs)), w.v[k]);
     }
-    float y[8];
+    Pairs<4> y;
 #pragma unroll
-    for (int d = 0; d < 8; ++d) y[d] = __shfl_xor_sync(0xffffu << (lane & 16), x[d], 8);
+    for (int k = 0; k < 4; ++k) y.v[k] = __shfl_xor_sync(0xffffu << (lane & 16), x.v[k], 8);
     if (pos_ok) {
       const float *cs = p.cos_sin + pos * kD + 8 * (i & 7);
+      const float sign = i < 8 ? -1.f : 1.f;
 #pragma unroll
-      for (int d = 0; d < 8; ++d)
-        x[d] = i < 8 ? x[d] * cs[d] - y[d] * cs[kD / 2 + d] : x[d] * cs[d] + y[d] * cs[kD / 2 + d];
+      for (int k = 0; k < 4; k += 2) {
+        const float4 c = *reinterpret_cast<const float4 *>(cs + 2 * k);
+        const float4 s = *reinterpret_cast<const float4 *>(cs + kD / 2 + 2 * k);
+        x.v[k] = fma2(x.v[k], pair_of(c.x, c.y), mul2(y.v[k], pair_of(sign * s.x, sign * s.y)));
+        x.v[k + 1] =
+            fma2(x.v[k + 1], pair_of(c.z, c.w), mul2(y.v[k + 1], pair_of(sign * s.z, sign * s.w)));
+      }
     }
   }
   if (!any || stop || (kind < 2 && !pos_ok)) return;
   if (kind == 0) {
-    *reinterpret_cast<uint4 *>(p.q_out + ((int64_t)n * p.hq + h) * (2 * kD) + 16 * i) = round8(x);
+    uint32_t w[4];
+    round_to_bf16(x, w);
+    *reinterpret_cast<uint4 *>(p.q_out + ((int64_t)n * p.hq + h) * (2 * kD) + 16 * i) =
+        make_uint4(w[0], w[1], w[2], w[3]);
     return;
   }
   if (ctx == 0) return;  // a padding row
@@ -323,7 +433,7 @@ __global__ void __launch_bounds__(kTokenWarps * 32) append_token_kernel(const Ap
   const int64_t sc = (blk * p.hkv + h) * (p.block_size / kFp8Group) + in_block / kFp8Group;
   float *scales = kind == 2 ? p.v_scale : p.k_scale;
   const float old = before ? scales[sc] : 0.f;
-  uint32_t m = finite_max8(0, x);
+  uint32_t m = __float_as_uint(finite_max(x));
 #pragma unroll
   for (int o = 1; o < 16; o <<= 1) m = max(m, __shfl_xor_sync(0xffffu << (lane & 16), m, o));
   const float scale = fmaxf(scale_of(m), old);
@@ -339,7 +449,9 @@ __global__ void __launch_bounds__(kTokenWarps * 32) append_token_kernel(const Ap
       *q = make_uint2(rescale4(w.x, ratio), rescale4(w.y, ratio));
     }
   }
-  *reinterpret_cast<uint2 *>(dst) = quantize8(x, 1.f / scale);
+  const uint64_t inv = pair_of(1.f / scale, 1.f / scale);
+  *reinterpret_cast<uint2 *>(dst) =
+      make_uint2(quantize4(x.v[0], x.v[1], inv), quantize4(x.v[2], x.v[3], inv));
   if (i == 0) scales[sc] = scale;
 }
 
@@ -401,6 +513,8 @@ extern "C" pkv_status pkv_qk_norm_rope_store_fp8(
   prm.hkv = num_kv_heads;
   prm.block_size = block_size;
   prm.num_blocks = num_blocks;
+  prm.wide = qkv_tok_stride % 16 == 0 &&
+             ((reinterpret_cast<uintptr_t>(qkv) | reinterpret_cast<uintptr_t>(q_out)) & 31u) == 0;
   prm.err = err;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (!cu_seqlens) {
@@ -411,12 +525,12 @@ extern "C" pkv_status pkv_qk_norm_rope_store_fp8(
                ? PKV_OK
                : PKV_ERR_CUDA;
   }
-  // as many heads to a CTA as still leave every SM about ten CTAs
+  // As many K and V heads to a CTA as still leave every SM about ten CTAs: a CTA's first loads wait
+  // for three others (2-3 us). At 132k tokens all 16 take 329 us, 8 take 335, 4 take 349.
   const int64_t runs = num_tokens / kFp8Group + 2 * (int64_t)num_seqs;
   const int64_t per = std::max<int64_t>(
-      1, std::min<int64_t>(num_kv_heads, runs * heads / (10 * (int64_t)num_sms)));
-  const int64_t grid =
-      runs * ((num_q_heads + per - 1) / per + 2 * ((num_kv_heads + per - 1) / per));
+      1, std::min<int64_t>(2 * num_kv_heads, runs * heads / (10 * (int64_t)num_sms)));
+  const int64_t grid = runs * (1 + (2 * num_kv_heads + per - 1) / per);
   if (grid > INT32_MAX) return PKV_ERR_UNSUPPORTED;
   return launch_after(append_run_kernel, (unsigned)grid, kRunThreads, st, prm, (int)per) ==
                  cudaSuccess
