@@ -8,8 +8,11 @@
 // may bring larger scales: the group then takes the largest, and what it holds is re-rounded.
 //
 // One CTA owns K or V of a sequence for some of its heads. The bytes are few (the moved rows, read
-// and written once), so what counts is the chain of dependent loads: lengths, list and table,
-// rows. Each step of it is taken for all rows at once.
+// and written once), so what counts is the chain of dependent loads: list and lengths, table, rows
+// (and their scales beside them). Each step of it is taken for all rows at once. 8 small trees take
+// 3.0 us, which is that chain; the paths of 256 trees of 64 nodes (37 MB) 9.2 us, 12.5 us in the
+// 8-bit cache (18 MB and the scales' chain): 14.4 and 18.8 us with CTAs of 256 threads, of which
+// four fit on an SM, divisions in place of shifts, and the rows asked for after the scales.
 #include <math.h>
 
 #include <algorithm>
