@@ -55,6 +55,23 @@
 // K tiles far ahead taking their turn before V tiles that are needed sooner.
 // TMEM (512 columns): Q [0, 64) [64, 128), S [128, 256) [256, 384), O [384, 512).
 //
+// Measured (us; the bytes of K, V, q and out at 6.8 TB/s in brackets):
+//   bf16, 2 heads to a KV head, 8 KV heads: 8 x 1024, chains of 4    17.3 (5.0)
+//         256 sequences of 100 to 2048, trees of 5 to 8 nodes       199 (178)
+//   bf16, 3 to a KV head, 4 of them: 1 x 17188, 13 nodes             17.6 (5.2)
+//   bf16, 4 to a KV head, 8 of them: 16 x 32768, 4 nodes 302 (316), 32 nodes 323 (317), 48 to 64
+//         nodes, two row tiles, 428 (303; their exponentials 232, their products 232)
+//   8-bit, 2 to a KV head, 8 of them: 8 x 1024, 16 nodes             21.4 (2.5)
+//         256 sequences of 100 to 2048, trees of 5 to 8 nodes       205 (89)
+//   8-bit, 8 to a KV head, 2 of them: 33 x 100 to 4999               58.4 (7.5)
+// A call of a few keys takes 6.7 us (two launches, the scan, the chain of loads). Long bf16 contexts
+// go at the memory's rate. What bounds the rest is the chain of a tile's steps (S, softmax, P V, the
+// hand-over of a buffer between two warps four times): about 1.05 us a tile and two of them under
+// way; leaving out the widening, the exponentials or three quarters of the products one at a
+// time takes 3 % off an 8-bit call, all of them together 15 %. And code: the warps run some twelve
+// different loops side by side, and each KiB more in them has cost about 2 % of a call, in whichever
+// warp it was; that is why waits are a function, loops are not unrolled and nothing is written twice.
+//
 // Masked places. A key that a row does not see is left out of its maximum and gets P = 0; V rows
 // past the context are zeroed in shared memory. A node that others do not see may hold
 // infinities or NaNs, and 0 x NaN would reach them: the nodes' V rows are looked through, what is
@@ -149,6 +166,7 @@ struct TreeSmem {
   uint64_t s_full[2], p_full[2], o_full[2], o_free, drain[2];
   uint64_t item_full[kRing], item_empty[kRing];
   uint64_t scanned[kRing];         // `dirty` is known
+  uint64_t done[kRing];            // the item's last PV is
   uint32_t tmem_base;
   int32_t stop;
   int2 warp_sums[16];
@@ -460,6 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.item_full[i], 1);
       mbar_init(&sm.item_empty[i], kItemConsumers);
       mbar_init(&sm.scanned[i], 4);
+      mbar_init(&sm.done[i], 1);
     }
     sm.start_b = 0;
     sm.start_at = 0;
@@ -969,8 +988,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------------ softmax and epilogue
       // A warp goes through a tile a granule at a time, 32 of its keys to a thread. The loops over
       // granules stay loops: unrolled, a tile's code does not fit the instruction caches beside the
-      // other warps'. (Two warps to a chunk, a granule each, where there are few: slower for the same
-      // reason, and by what they have to agree on.)
+      // other warps'. (Two warps to a chunk where there are few, a granule or a tile each in turn:
+      // slower for the same reason, and by what they have to agree on.) Warps whose chunk the item
+      // does not have wait for its end, and the first warp arrives for them.
       const int c = warp, ch = lane >> 4, r = lane & 15;  // chunk, half of the granule's keys, row
       const int i = p.node_of(r), head_r = r - i * p.hb;
       const uint32_t lane_addr = tmem + ((uint32_t)((c & 3) * 32 + (c >> 2) * 16) << 16);
@@ -991,10 +1011,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (row)
             for (int e = 0; e < 8; ++e)
               reinterpret_cast<uint4 *>(dst + 64 * ch)[e] = make_uint4(0, 0, 0, 0);
+        } else if (!mine) {  // it has no rows: the first warp arrives for it, tile by tile
+          g += tiles;
+          ok = __all_sync(kFull, wait_bar(&sm.done[ring], (taken / kRing) & 1, p.err));
+          if (!ok) break;
+          if (lane == 0) mbar_arrive(&sm.o_free);
+        }
+        if (tiles == 0 || !mine) {
+          if (tiles == 0 && warp == 0 && lane == 0) mbar_arrive(&sm.done[ring]);
           release_item(sm, taken, lane);
           ++taken;
           continue;
         }
+        const uint32_t arrivals = warp == 0 ? kSoftmaxWarps + 1 - ip->chunks : 1;
         // what the row sees of its tree's first 64 nodes, loaded ahead of the tiles that need it
         const uint64_t first_word = row && key1 > root ? mask_word(p, q_row, node, 0) : 0;
         auto word = [&](int w) -> uint64_t {
@@ -1006,124 +1035,122 @@ __global__ void __launch_bounds__(kThreads, 1)
           // warp-uniform results: the TMEM loads and stores below are .sync.aligned
           ok = __all_sync(kFull, wait_bar(&sm.s_full[sb], (g >> 1) & 1, p.err));
           if (!ok) break;
-          if (mine) {
-            tc_fence_after_sync();
-            if constexpr (F8)
-              if (j == 0)
-                row_scale = p.scale_log2 * pow2f((int)sm.raw.q_power[ring][c * kChunkRows + r]);
-            // 8-bit cache: what multiplies the scores of granule k, log2 of its V scale (a granule past
-            // the keys has no scales)
-            auto factors = [&](int k, float &factor, float &v_scale) {
-              factor = row_scale;
-              v_scale = 1.f;
-              if constexpr (F8) {
-                const int pos = key0 + j * kTile + 64 * k;
-                if (pos < key1) {
-                  const float(*sc)[4] = sm.raw.scale[g % kScaleTiles][k];
-                  factor = fmaxf(factor * sc[0][pos / kGranule & 3], 1e-38f);  // (see scale_log2)
-                  v_scale = sc[1][pos / kGranule & 3];
-                }
-              }
-            };
-            float m_tile = -INFINITY;
-#pragma unroll 1
-            for (int k = 0; k < 2; ++k) {
-              uint32_t x[32];  // keys 64 k + 32 ch + e
-              tmem_ld16x2_32<32>(s_addr + 64 * k, x);
-              const int pos = key0 + j * kTile + 64 * k + 32 * ch;
-              float factor, v_scale;
-              factors(k, factor, v_scale);
-              tmem_ld_wait(x);
-              if (key0 + j * kTile + 64 * (k + 1) > min(key1, root)) {
-                // the keys of this thread's that the row sees; the others' scores become -inf
-                uint32_t sees = pos >= key1 ? 0 : pos + 32 > key1 ? ~0u >> (32 - (key1 - pos)) : ~0u;
-                if (pos + 32 > root && sees != 0) {
-                  const int base = pos - root, w = base >> 6, sh = base & 63;  // (w = -1: before it)
-                  uint64_t bits = w < 0 ? ~0ull : word(w);
-                  if (sh) bits = bits >> sh | word(w + 1) << (64 - sh);
-                  sees &= (uint32_t)bits;
-                }
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (!(sees >> e & 1)) x[e] = __float_as_uint(-INFINITY);
-                tmem_st16x2_32<32>(s_addr + 64 * k, x);
-                tmem_st_wait();
-              }
-              float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                mx[0] = fmax3(mx[0], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-                mx[1] = fmax3(mx[1], __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
-              }
-              float m = fmaxf(mx[0], mx[1]) * factor;
-              if constexpr (F8) m += log2_approx(v_scale);
-              m_tile = fmaxf(m_tile, m);
-            }
-            m_tile = fmaxf(m_tile, __shfl_xor_sync(kFull, m_tile, 16));
-            const bool grows = m_tile > m_run + kRescaleLog2;
-            if (__any_sync(kFull, grows)) {
-              const float alpha = grows ? fast_exp2(m_run - m_tile) : 1.f;
-              if (grows) m_run = m_tile;
-              l_run *= alpha;
-              // O holds the item's tiles before this one: rescale it (never on the first tile)
-              if (j > 0) {
-                ok = __all_sync(kFull, wait_bar(&sm.o_full[(g - 1) & 1], ((g - 1) >> 1) & 1, p.err));
-                if (!ok) break;
-                tc_fence_after_sync();
-#pragma unroll 1
-                for (int k = 0; k < 2; ++k) {
-                  uint32_t o[32];
-                  tmem_ld16x2_32<32>(lane_addr + kOCol + 64 * k, o);
-                  tmem_ld_wait(o);
-#pragma unroll
-                  for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                  tmem_st16x2_32<32>(lane_addr + kOCol + 64 * k, o);
-                }
+          tc_fence_after_sync();
+          if constexpr (F8)
+            if (j == 0)
+              row_scale = p.scale_log2 * pow2f((int)sm.raw.q_power[ring][c * kChunkRows + r]);
+          // 8-bit cache: what multiplies the scores of granule k, log2 of its V scale (a granule past
+          // the keys has no scales)
+          auto factors = [&](int k, float &factor, float &v_scale) {
+            factor = row_scale;
+            v_scale = 1.f;
+            if constexpr (F8) {
+              const int pos = key0 + j * kTile + 64 * k;
+              if (pos < key1) {
+                const float(*sc)[4] = sm.raw.scale[g % kScaleTiles][k];
+                factor = fmaxf(factor * sc[0][pos / kGranule & 3], 1e-38f);  // (see scale_log2)
+                v_scale = sc[1][pos / kGranule & 3];
               }
             }
-            // P, two keys to a column, over the first half of the granule's S columns; a second part
-            // over the other half
-            const float base = m_run == -INFINITY ? 0.f : m_run;
+          };
+          float m_tile = -INFINITY;
 #pragma unroll 1
-            for (int k = 0; k < 2; ++k) {
-              uint32_t x[32];
-              tmem_ld16x2_32<32>(s_addr + 64 * k, x);
-              float factor, v_scale;
-              factors(k, factor, v_scale);
-              float offset = -base, per_v = 1.f;
-              if constexpr (F8) {
-                offset += log2_approx(v_scale) + kOffset8;
-                per_v = rcp_approx(v_scale * (1 << kOffset8));
+          for (int k = 0; k < 2; ++k) {
+            uint32_t x[32];  // keys 64 k + 32 ch + e
+            tmem_ld16x2_32<32>(s_addr + 64 * k, x);
+            const int pos = key0 + j * kTile + 64 * k + 32 * ch;
+            float factor, v_scale;
+            factors(k, factor, v_scale);
+            tmem_ld_wait(x);
+            if (key0 + j * kTile + 64 * (k + 1) > min(key1, root)) {
+              // the keys of this thread's that the row sees; the others' scores become -inf
+              uint32_t sees = pos >= key1 ? 0 : pos + 32 > key1 ? ~0u >> (32 - (key1 - pos)) : ~0u;
+              if (pos + 32 > root && sees != 0) {
+                const int base = pos - root, w = base >> 6, sh = base & 63;  // (w = -1: before it)
+                uint64_t bits = w < 0 ? ~0ull : word(w);
+                if (sh) bits = bits >> sh | word(w + 1) << (64 - sh);
+                sees &= (uint32_t)bits;
               }
-              const float2 mul2 = make_float2(factor, factor), add2 = make_float2(offset, offset);
-              float2 rs0 = make_float2(0.f, 0.f), rs1 = make_float2(0.f, 0.f);
-              tmem_ld_wait(x);
-              uint32_t hi[16];
-              [[maybe_unused]] uint32_t lo[16];
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const float2 t = ffma2(
-                    make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), mul2, add2);
-                const float2 pe = make_float2(fast_exp2(t.x), fast_exp2(t.y));
-                if (e & 1) rs1 = fadd2(rs1, pe);
-                else rs0 = fadd2(rs0, pe);
-                if constexpr (F8) {
-                  hi[e] = pack_f16x2(pe.x, pe.y);
-                } else {
-                  hi[e] = pack_bf16x2(pe.x, pe.y);
-                  if constexpr (M == kTwoParts)
-                    lo[e] = pack_bf16x2(pe.x - bf16_lo(hi[e]), pe.y - bf16_hi(hi[e]));
-                }
-              }
-              tmem_st16x2_16<16>(s_addr + 64 * k, hi);
-              if constexpr (M == kTwoParts) tmem_st16x2_16<16>(s_addr + 64 * k + 32, lo);
-              l_run += ((rs0.x + rs0.y) + (rs1.x + rs1.y)) * per_v;
+              for (int e = 0; e < 32; ++e)
+                if (!(sees >> e & 1)) x[e] = __float_as_uint(-INFINITY);
+              tmem_st16x2_32<32>(s_addr + 64 * k, x);
+              tmem_st_wait();
             }
-            tmem_st_wait();
-            tc_fence_before_sync();
+            float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              mx[0] = fmax3(mx[0], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+              mx[1] = fmax3(mx[1], __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+            }
+            float m = fmaxf(mx[0], mx[1]) * factor;
+            if constexpr (F8) m += log2_approx(v_scale);
+            m_tile = fmaxf(m_tile, m);
           }
+          m_tile = fmaxf(m_tile, __shfl_xor_sync(kFull, m_tile, 16));
+          const bool grows = m_tile > m_run + kRescaleLog2;
+          if (__any_sync(kFull, grows)) {
+            const float alpha = grows ? fast_exp2(m_run - m_tile) : 1.f;
+            if (grows) m_run = m_tile;
+            l_run *= alpha;
+            // O holds the item's tiles before this one: rescale it (never on the first tile)
+            if (j > 0) {
+              ok = __all_sync(kFull, wait_bar(&sm.o_full[(g - 1) & 1], ((g - 1) >> 1) & 1, p.err));
+              if (!ok) break;
+              tc_fence_after_sync();
+#pragma unroll 1
+              for (int k = 0; k < 2; ++k) {
+                uint32_t o[32];
+                tmem_ld16x2_32<32>(lane_addr + kOCol + 64 * k, o);
+                tmem_ld_wait(o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                tmem_st16x2_32<32>(lane_addr + kOCol + 64 * k, o);
+              }
+            }
+          }
+          // P, two keys to a column, over the first half of the granule's S columns; a second part
+          // over the other half
+          const float base = m_run == -INFINITY ? 0.f : m_run;
+#pragma unroll 1
+          for (int k = 0; k < 2; ++k) {
+            uint32_t x[32];
+            tmem_ld16x2_32<32>(s_addr + 64 * k, x);
+            float factor, v_scale;
+            factors(k, factor, v_scale);
+            float offset = -base, per_v = 1.f;
+            if constexpr (F8) {
+              offset += log2_approx(v_scale) + kOffset8;
+              per_v = rcp_approx(v_scale * (1 << kOffset8));
+            }
+            const float2 mul2 = make_float2(factor, factor), add2 = make_float2(offset, offset);
+            float2 rs0 = make_float2(0.f, 0.f), rs1 = make_float2(0.f, 0.f);
+            tmem_ld_wait(x);
+            uint32_t hi[16];
+            [[maybe_unused]] uint32_t lo[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float2 t = ffma2(
+                  make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), mul2, add2);
+              const float2 pe = make_float2(fast_exp2(t.x), fast_exp2(t.y));
+              if (e & 1) rs1 = fadd2(rs1, pe);
+              else rs0 = fadd2(rs0, pe);
+              if constexpr (F8) {
+                hi[e] = pack_f16x2(pe.x, pe.y);
+              } else {
+                hi[e] = pack_bf16x2(pe.x, pe.y);
+                if constexpr (M == kTwoParts)
+                  lo[e] = pack_bf16x2(pe.x - bf16_lo(hi[e]), pe.y - bf16_hi(hi[e]));
+              }
+            }
+            tmem_st16x2_16<16>(s_addr + 64 * k, hi);
+            if constexpr (M == kTwoParts) tmem_st16x2_16<16>(s_addr + 64 * k + 32, lo);
+            l_run += ((rs0.x + rs0.y) + (rs1.x + rs1.y)) * per_v;
+          }
+          tmem_st_wait();
+          tc_fence_before_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.p_full[sb]);
+          if (lane == 0) mbar_arrive_count(&sm.p_full[sb], arrivals);
         }
         if (!ok) break;
         // O, once the last PV is done
@@ -1131,6 +1158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(kFull, wait_bar(&sm.o_full[(g - 1) & 1], ((g - 1) >> 1) & 1, p.err) &&
                                    wait_bar(&sm.scanned[ring], (taken / kRing) & 1, p.err));
         if (!ok) break;
+        if (warp == 0 && lane == 0) mbar_arrive(&sm.done[ring]);
         const Item &it = *ip;
         const bool dirty = sm.dirty[ring] != 0;
         // (NaN stays; a row that sees nothing gets zeros)
@@ -1142,10 +1170,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int k = 0; k < 2; ++k) {
           uint32_t o[32];  // dims 64 k + 32 ch + e
-          if (mine) {
-            tmem_ld16x2_32<32>(lane_addr + kOCol + 64 * k, o);
-            tmem_ld_wait(o);
-          }
+          tmem_ld16x2_32<32>(lane_addr + kOCol + 64 * k, o);
+          tmem_ld_wait(o);
           if (k == 1) {
             tc_fence_before_sync();
             __syncwarp();
