@@ -533,7 +533,9 @@ pkv_status pkv_kv_evict(const float *weights, int64_t weights_stride,
  * those, for query head hq of KV head h = hq / (num_q_heads / num_kv_heads),
  *     out[cu_seqlens_q[b] + i, hq, :] = softmax_j(scale * q . k_j) v_j          (bf16, RNE)
  * A node that sees nothing gets zeros. Scores, softmax and sums are in fp32; a weight enters
- * the value sum within 2^-16 of itself.
+ * the value sum within 2^-16 of itself, or rounded to bf16 (2^-9) where a KV head can have more rows
+ * of q than a tile of 128: that is, where max_seqlen_q > 8 * floor(16 / g), g = num_q_heads /
+ * num_kv_heads query heads to a KV head (g <= 16; with more heads 128 / g nodes or fewer).
  *
  * q:             [total_q, num_q_heads, head_dim] bf16, token stride q_tok_stride elements. Rows
  *                behind cu_seqlens_q[num_seqs] are not read, and their outputs left as they are.
@@ -550,9 +552,12 @@ pkv_status pkv_kv_evict(const float *weights, int64_t weights_stride,
  *                A bad block id (PKV_DEVERR_BLOCK_RANGE) counts as keys and values of zeros.
  * workspace:     pkv_tree_workspace_bytes(...) bytes, 16-byte aligned, private to this call while
  *                it runs; its contents need no initialisation.
- * out:           [total_q, num_q_heads, head_dim] bf16, contiguous.
- * Implemented: head_dim == 128, block_size a multiple of 256, q_tok_stride a multiple of 8, 16-byte
- * aligned q, pools, scales and out; any num_q_heads / num_kv_heads.
+ * out:           [total_q, num_q_heads, head_dim] bf16, contiguous; may not overlap q.
+ * Implemented: head_dim == 128, block_size a multiple of 256, num_blocks * block_size < 2^31,
+ * max_seqlen_q <= 2^20, q_tok_stride a multiple of 8, 16-byte aligned q, pools, scales and out; any
+ * num_q_heads / num_kv_heads; as long as the batch's work -- for every sequence ceil(max_context_len /
+ * 64), times the 128-row tiles of its nodes and the KV heads, as one CTA or several take them together --
+ * stays below 2^30.
  */
 size_t pkv_tree_workspace_bytes(int32_t num_seqs, int32_t max_seqlen_q, int32_t num_q_heads,
                                 int32_t num_kv_heads, int32_t head_dim, int32_t max_context_len);
@@ -568,7 +573,9 @@ pkv_status pkv_paged_tree_attn(const void *q, int64_t q_tok_stride, int64_t tota
 
 /*
  * paged_tree_attn_fp8 -- the same over the 8-bit cache (k_scale, v_scale: its scales, as for
- * pkv_paged_decode_attn_fp8).
+ * pkv_paged_decode_attn_fp8). Scores are products of K's codes with a row of q in two e4m3 parts, exact
+ * for values down to 2^-9 of the row's largest |q| and within 2^-17 of that largest one below (a row
+ * with an infinity or a NaN gives NaN); weights enter the value sum within 2^-11 of themselves.
  */
 pkv_status pkv_paged_tree_attn_fp8(const void *q, int64_t q_tok_stride, int64_t total_q,
                                    const void *k_cache, const void *v_cache, const float *k_scale,
@@ -601,8 +608,8 @@ pkv_status pkv_paged_tree_attn_fp8(const void *q, int64_t q_tok_stride, int64_t 
  *                positions that accepted rows lie in takes the largest of its scale s0 and the
  *                scales of the groups they come from, s; its rows from before the tree become
  *                e4m3(code * s0 / s), a row of a group with scale s1 e4m3(code * s1 / s).
- * new_context_lens: [num_seqs] int32, not context_lens (PKV_ERR_INVALID_ARG): the calls of the
- *                step's other layers read that.
+ * new_context_lens: [num_seqs] int32, apart from the other lists (PKV_ERR_INVALID_ARG): the calls of
+ *                the step's other layers read context_lens.
  * Implemented: head_dim == 128, block_size a multiple of 64 (bf16) or 256 (8-bit), 16-byte aligned
  * pools.
  */
@@ -618,7 +625,7 @@ pkv_status pkv_kv_accept(const int32_t *accepted, int32_t accepted_width,
  * qk_norm_rope_store_fp8 -- pkv_qk_norm_rope_store for the 8-bit cache: RMSNorm (QK 归一化) and RoPE
  * of the new tokens' query and key heads, K and V appended as pkv_kv_store_fp8 appends them.
  *
- * qkv, positions, cos_sin_cache, eps, q_out as there; cu_seqlens, context_lens, block_tables and
+ * qkv, positions, cos_sin_cache, eps, q_out as there (q_out may not overlap qkv); cu_seqlens, context_lens, block_tables and
  * the cache as in pkv_kv_store_fp8. For each query / key head x, in fp32 throughout:
  *     n = x * rsqrt(mean(x^2) + eps) * w          (without weights: n = x)
  *     y_i = n_i c_i - n_{i+h} s_i,  y_{i+h} = n_{i+h} c_i + n_i s_i

@@ -75,6 +75,8 @@ __global__ void __launch_bounds__(kThreads) kv_accept_kernel(const AcceptParams 
   const int64_t c0 = *(p.cu + b), c1 = *(p.cu + b + 1), L = *(p.context_lens + b);
   int many = *(p.num_accepted + b);
   const int64_t n = c1 - c0, start = L - n;
+  // an earlier wait gave up somewhere: write nothing (decided by the CTA together)
+  if (__syncthreads_or(tid == 0 && aborted(p.err))) return;
   if (n < 0 || start < 0 || L > (int64_t)p.table_width * p.block_size) {
     if (first && tid == 0) {
       record_error(p.err, n < 0 ? PKV_DEVERR_SEQLEN_RANGE : PKV_DEVERR_CONTEXT_RANGE);
@@ -100,7 +102,7 @@ __global__ void __launch_bounds__(kThreads) kv_accept_kernel(const AcceptParams 
   __syncthreads();
   many = count;
   if (first && tid == 0) p.new_context_lens[b] = (int32_t)start + many;
-  if (many == 0 || aborted(p.err)) return;
+  if (many == 0) return;
   const int32_t *table = p.block_tables + (int64_t)b * p.table_width;
   auto pool_row = [&](int64_t pos) -> int64_t {
     const int64_t blk = *(table + pos / p.block_size);
@@ -205,8 +207,14 @@ extern "C" pkv_status pkv_kv_accept(const int32_t *accepted, int32_t accepted_wi
   if (!num_accepted || !cu_seqlens_q || !context_lens || !block_tables || !k_cache || !v_cache ||
       !new_context_lens || (accepted_width > 0 && !accepted) || !k_scale != !v_scale)
     return PKV_ERR_INVALID_ARG;
-  // (the calls of a step's other layers read the old lengths)
-  if (new_context_lens == context_lens) return PKV_ERR_INVALID_ARG;
+  // (the calls of a step's other layers read the old lengths, and the CTAs of a sequence its numbers)
+  const int64_t ints = 4 * (int64_t)num_seqs;
+  if (overlap(new_context_lens, 1, 0, ints, context_lens, ints) ||
+      overlap(new_context_lens, 1, 0, ints, num_accepted, ints) ||
+      overlap(new_context_lens, 1, 0, ints, cu_seqlens_q, ints + 4) ||
+      overlap(new_context_lens, 1, 0, ints, accepted, ints * accepted_width) ||
+      overlap(new_context_lens, 1, 0, ints, block_tables, ints * block_table_width))
+    return PKV_ERR_INVALID_ARG;
   if (head_dim != kD || block_size % (k_scale ? 256 : kFp8Group) != 0) return PKV_ERR_UNSUPPORTED;
   if (!aligned16(k_cache) || !aligned16(v_cache)) return PKV_ERR_UNSUPPORTED;
   const int num_sms = current_sm_count();

@@ -13,6 +13,16 @@ namespace pkv {
 
 inline size_t align16(size_t x) { return (x + 15) & ~size_t(15); }
 
+// Do the `rows` rows of `bytes` bytes at a, `stride` bytes apart, reach into the `size` bytes at b?
+// (A gap between rows counts as theirs.)
+inline bool overlap(const void *a, int64_t rows, __int128 stride, int64_t bytes, const void *b,
+                    int64_t size) {
+  if (rows <= 0 || bytes <= 0 || size <= 0) return false;
+  const __int128 x = (__int128)reinterpret_cast<uintptr_t>(a);
+  const __int128 y = (__int128)reinterpret_cast<uintptr_t>(b);
+  return x < y + size && y < x + (__int128)(rows - 1) * stride + bytes;
+}
+
 // kv_store.cu
 cudaError_t launch_kv_store(const void *k, int64_t k_tok_stride, const void *v,
                             int64_t v_tok_stride, const int64_t *slot_mapping, int64_t num_tokens,

@@ -486,6 +486,9 @@ extern "C" pkv_status pkv_qk_norm_rope_store_fp8(
       !aligned16(k_norm_weight) || !aligned16(cos_sin_cache) || !aligned16(q_out) ||
       !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scale) || !aligned16(v_scale))
     return PKV_ERR_UNSUPPORTED;
+  if (overlap(qkv, num_tokens, 2 * (__int128)qkv_tok_stride, 2 * heads * head_dim, q_out,
+              2 * num_tokens * num_q_heads * head_dim))
+    return PKV_ERR_INVALID_ARG;
   const int num_sms = current_sm_count();
   unsigned int *err = current_error_word();
   if (num_sms <= 0 || !err) return PKV_ERR_CUDA;

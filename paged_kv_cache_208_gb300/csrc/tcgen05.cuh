@@ -136,16 +136,8 @@ __device__ __forceinline__ void umma_e4m3_ts(uint32_t d_tmem, uint32_t a_tmem, u
       : "memory");
 }
 
-// D[tmem] (+)= A * B, kind::f16 (bf16 or, by idesc, fp16 in, fp32 accumulate), M = 128, K = 16.
-__device__ __forceinline__ void umma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                            uint32_t idesc, bool accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
-      : "memory");
-}
-// The same with A read from tensor memory.
+// D[tmem] (+)= A * B, kind::f16 (bf16 or, by idesc, fp16 in, fp32 accumulate), M = 128, K = 16, A in
+// tensor memory.
 __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
                                             uint32_t idesc, bool accumulate) {
   asm volatile(
@@ -279,40 +271,6 @@ __device__ __forceinline__ void tmem_st16x2_16(uint32_t taddr, const uint32_t (&
       "{%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17};" ::"r"(taddr),
       "n"(kSplit), PKV_W8(0), PKV_W8(8)
       : "memory");
-}
-
-// Two threads per lane again, C columns each (8, 16, 32 or 64), the second's C further; waited for.
-template <int C>
-__device__ __forceinline__ void tmem_ld16x2(uint32_t taddr, uint32_t (&x)[C / 8][8]) {
-  static_assert(C == 8 || C == 16 || C == 32 || C == 64, "");
-#pragma unroll
-  for (int k = 0; k < C / 8; ++k) {
-    uint32_t (&r)[8] = x[k];
-    asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8], %9;"
-                 : PKV_R8(0)
-                 : "r"(taddr + 8 * k), "n"(C));
-  }
-  // (the registers pass through the asm: no use of them comes before the wait)
-#pragma unroll
-  for (int k = 0; k < C / 8; ++k) {
-    uint32_t (&r)[8] = x[k];
-    asm volatile("tcgen05.wait::ld.sync.aligned;" : PKV_RW8(0)::"memory");
-  }
-}
-
-// N columns (4 or 8) of each of two threads per lane, the second's kSplit further.
-template <int kSplit, int N>
-__device__ __forceinline__ void tmem_st16x2(uint32_t taddr, const uint32_t (&r)[N]) {
-  static_assert(N == 4 || N == 8, "");
-  if constexpr (N == 8)
-    asm volatile(
-        "tcgen05.st.sync.aligned.16x32bx2.x8.b32 [%0], %1, {%2,%3,%4,%5,%6,%7,%8,%9};" ::"r"(taddr),
-        "n"(kSplit), PKV_W8(0)
-        : "memory");
-  else
-    asm volatile("tcgen05.st.sync.aligned.16x32bx2.x4.b32 [%0], %1, {%2,%3,%4,%5};" ::"r"(taddr),
-                 "n"(kSplit), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
-                 : "memory");
 }
 
 // This warp's 32 TMEM lanes, N consecutive 32-bit columns (2, 4 or 8), waited for.

@@ -1446,17 +1446,21 @@ pkv_status tree_attn(const void *q, int64_t q_tok_stride, int64_t total_q, const
       (fp8 && (!k_scale || !v_scale)))
     return PKV_ERR_INVALID_ARG;
   if (head_dim != kD || block_size % 256 != 0 || total_q > INT32_MAX ||
-      num_blocks * (int64_t)block_size > INT32_MAX)
+      max_seqlen_q > (1 << 20) || num_blocks > INT32_MAX / block_size)
     return PKV_ERR_UNSUPPORTED;
   if (q_tok_stride % 8 != 0 || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) ||
       !aligned16(out) || (fp8 && (!aligned16(k_scale) || !aligned16(v_scale))))
     return PKV_ERR_UNSUPPORTED;
+  // (a CTA reads rows of q whose outputs another one has written)
+  if (overlap(q, total_q, 2 * (__int128)q_tok_stride, 2 * (int64_t)num_q_heads * head_dim, out,
+              2 * total_q * num_q_heads * head_dim))
+    return PKV_ERR_INVALID_ARG;
   unsigned int *err = current_error_word();
   const int num_sms = current_sm_count();
   if (!err || num_sms <= 0) return PKV_ERR_CUDA;
   const TreePlan plan =
       plan_tree(num_seqs, max_seqlen_q, num_q_heads, num_kv_heads, max_context_len, num_sms);
-  if (plan.longest > (1 << 30) || max_seqlen_q > (1 << 20)) return PKV_ERR_UNSUPPORTED;
+  if (plan.longest > (1 << 30)) return PKV_ERR_UNSUPPORTED;
   if (!workspace || !aligned16(workspace) || workspace_bytes < plan.bytes) return PKV_ERR_WORKSPACE;
   TreeParams prm{};
   prm.q = static_cast<const uint16_t *>(q);

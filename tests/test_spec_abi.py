@@ -37,6 +37,26 @@ def test_tree_argument_checks():
             assert _tree(fp8, **kw) == pkv.ERR_UNSUPPORTED, kw
     assert _tree(True, ks=None) == _tree(True, vs=None) == pkv.ERR_INVALID_ARG
     assert _tree(True, ks=ODD) == pkv.ERR_UNSUPPORTED
+    assert _tree(False, nb=1 << 61) == pkv.ERR_UNSUPPORTED
+    assert _tree(False, mq=(1 << 20) + 1, mw=1 << 15) == pkv.ERR_UNSUPPORTED
+
+
+def test_outputs_that_overlap_inputs():
+    at = ctypes.c_void_p
+    last = 0x10000 + 2 * (8 * 2048 + 16 * 128)  # behind the last row of q
+    for fp8 in (False, True):
+        for out in (0x10000, last - 16, 0x10000 - 2 * 9 * 2048 + 16):
+            assert _tree(fp8, q=at(0x10000), out=at(out)) == pkv.ERR_INVALID_ARG, hex(out)
+        for out in (last, 0x10000 - 2 * 9 * 2048):  # (refused too, for want of a device or a workspace)
+            assert _tree(fp8, q=at(0x10000), out=at(out), wsb=0) in (pkv.ERR_CUDA, pkv.ERR_WORKSPACE)
+        huge = (1 << 62) - 8
+        assert _tree(fp8, q=at(0x10000), out=at(last), qs=huge) == pkv.ERR_INVALID_ARG
+    last = 0x10000 + 2 * (8 * 4104 + 4096)
+    for out in (0x10000, last - 16):
+        assert _append(x=at(0x10000), s=4104, q=at(out)) == pkv.ERR_INVALID_ARG
+    for kw in (dict(num=OTHER), dict(cu=OTHER), dict(cl=OTHER), dict(bt=OTHER), dict(acc=OTHER),
+               dict(cu=at(0x2000 - 8)), dict(acc=at(0x2000 - 36)), dict(bt=at(0x2000 - 28))):
+        assert _accept(**kw) == pkv.ERR_INVALID_ARG, kw
 
 
 def test_tree_workspace_of_bad_sizes():
