@@ -482,6 +482,16 @@ __device__ __forceinline__ uint4 ld_once_u4(const uint4 *p) {
   return r;
 }
 
+// The same for data that are read again.
+__device__ __forceinline__ uint4 ld_u4(const uint4 *p) {
+  uint4 r;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
+
 __device__ __forceinline__ uint4 ld_stream_u4(const uint4 *p) {
   uint4 r;
   asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"

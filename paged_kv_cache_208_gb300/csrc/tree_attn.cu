@@ -14,7 +14,12 @@
 // heads of a unit (whose values lie in the same DRAM pages) and, where trees have more rows than a
 // tile, up to four row tiles of the same keys at the same time (K and V then come from L2 for all
 // but one of them). The lengths are device data, so every CTA sums them up at its start (one scan
-// over the sequences) and walks its own part. A unit within a worker's part is written out
+// over the sequences) and walks its own part. A cut costs an item more, its part of the rows in fp32 and
+// the merge: a part's start that lies within 8 granules of a unit's end moves there, and where there
+// are no more units than workers, none more than 12 granules longer than an equal part, a worker takes
+// a whole one (us, with and without: 33 x 512, 31 nodes of 16 / 2 heads 19.5 and 26.8, 16 x 1024, 4
+// nodes of 16 / 8 19.0 and 21.5, 8-bit 33 x 100 to 4999 46 and 50; the other way 10 x 4096 37.1 and
+// 35.1, which moved starts make uneven). A unit within a worker's part is written out
 // directly; what a cut leaves is normalised and goes to the workspace with its log2-sum-exp, and
 // tree_combine_kernel merges it. Which parts there are depends on the lengths alone, so the same
 // call gives the same bits.
@@ -56,19 +61,21 @@
 // TMEM (512 columns): Q [0, 64) [64, 128), S [128, 256) [256, 384), O [384, 512).
 //
 // Measured (us; the bytes of K, V, q and out at 6.8 TB/s in brackets):
-//   bf16, 2 heads to a KV head, 8 KV heads: 8 x 1024, chains of 4    17.3 (5.0)
-//         256 sequences of 100 to 2048, trees of 5 to 8 nodes       199 (178)
-//   bf16, 3 to a KV head, 4 of them: 1 x 17188, 13 nodes             17.6 (5.2)
+//   bf16, 2 heads to a KV head, 8 KV heads: 8 x 1024, chains of 4    16.9 (5.0)
+//         256 sequences of 100 to 2048, trees of 5 to 8 nodes       200 (178)
+//   bf16, 3 to a KV head, 4 of them: 1 x 17188, 13 nodes             17.7 (5.2)
 //   bf16, 4 to a KV head, 8 of them: 16 x 32768, 4 nodes 302 (316), 32 nodes 323 (317), 48 to 64
-//         nodes, two row tiles, 428 (303; their exponentials 232, their products 232)
-//   8-bit, 2 to a KV head, 8 of them: 8 x 1024, 16 nodes             21.4 (2.5)
-//         256 sequences of 100 to 2048, trees of 5 to 8 nodes       205 (89)
-//   8-bit, 8 to a KV head, 2 of them: 33 x 100 to 4999               58.4 (7.5)
+//         nodes, two row tiles, 429 (303; their exponentials 232, their products 232)
+//   8-bit, 2 to a KV head, 8 of them: 8 x 1024, 16 nodes             17.9 (2.5)
+//         256 sequences of 100 to 2048, trees of 5 to 8 nodes       182 (89)
+//   8-bit, 8 to a KV head, 2 of them: 33 x 100 to 4999               46.3 (7.5)
 // A call of a few keys takes 6.7 us (two launches, the scan, the chain of loads). Long bf16 contexts
 // go at the memory's rate. What bounds the rest is the chain of a tile's steps (S, softmax, P V, the
 // hand-over of a buffer between two warps four times): about 1.05 us a tile and two of them under
 // way; leaving out the widening, the exponentials or three quarters of the products one at a
-// time takes 3 % off an 8-bit call, all of them together 15 %. And code: the warps run some twelve
+// time takes 3 % off a long 8-bit call, all of them together 15 %. An item more costs about 5 us where it
+// has one tile (a row of q takes a trip to memory, the softmax warps wait for the last product before
+// they write). And code: the warps run some twelve
 // different loops side by side, and each KiB more in them has cost about 2 % of a call, in whichever
 // warp it was; that is why waits are a function, loops are not unrolled and nothing is written twice.
 //
@@ -115,6 +122,8 @@ constexpr int kRing = 4;
 constexpr uint32_t kQCol = 0, kSCol = 128, kOCol = 384, kTmemCols = 512;
 constexpr int kItemConsumers = kSoftmaxWarps + 3 + 4;  // S, V, PV and Q warps
 constexpr int kMaxGroup = 8, kMaxTiles = 4;  // CTAs, and row tiles, of a worker
+constexpr int kNear = 8;        // granules that a part may grow or shrink by at an end
+constexpr int kWhole = 12;      // granules that a unit may be longer than a part without being cut
 constexpr int kOffset8 = 6;     // log2 of what P' is larger by, 8-bit cache
 
 enum Mode { kTwoParts, kOnePart, kFp8 };
@@ -169,9 +178,10 @@ struct TreeSmem {
   uint64_t done[kRing];            // the item's last PV is
   uint32_t tmem_base;
   int32_t stop;
-  int2 warp_sums[16];
+  int3 warp_sums[kThreads / 32];  // granules, units, the longest unit
   // the sequence that the CTA's part starts in, and where that starts on the axis
   int32_t start_b, start_at, start_units, start_q0, start_n, start_L;
+  int32_t x0, x1;  // the part
 };
 static_assert(sizeof(TreeSmem<kFp8>) + 1024 <= 232448, "fits the SM");
 
@@ -233,6 +243,14 @@ struct TreeParams {
   __device__ __forceinline__ static int32_t part_of(int32_t x, int32_t each, int32_t rest) {
     const int32_t longer = rest * (each + 1);
     return x < longer ? x / (each + 1) : rest + (x - longer) / each;
+  }
+  // A part's start at x in the unit [start, end) moves to an end of the unit that is near.
+  __device__ __forceinline__ static int32_t nearness(int32_t each) {
+    return min(kNear, max(0, (each - 1) / 2));
+  }
+  __device__ __forceinline__ static int32_t moved(int32_t x, int32_t start, int32_t end,
+                                                  int32_t near) {
+    return x - start <= near ? start : end - x <= near ? end : x;
   }
 };
 
@@ -503,7 +521,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool stop = tid == 0 && aborted(p.err);
   const bool one_warp = p.num_seqs <= 32, at_once = p.num_seqs <= kThreads;
   bool works = false;
-  int32_t total = 0, each = 0, rest = 0, x0 = 0, x1 = 0, all_units = 0;
+  bool whole = false;  // there are no more units than workers, and a worker takes one
+  int32_t total = 0, each = 0, rest = 0, x0 = 0, x1 = 0, all_units = 0, longest = 0;
   for (int pass = 0; pass < 2; ++pass) {
     int32_t carry = 0, units_carry = 0;
     for (int base = 0; base < p.num_seqs; base += kThreads) {
@@ -522,32 +541,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       int32_t sum = __shfl_sync(kFull, x, 31), units_sum = __shfl_sync(kFull, units, 31);
+      int32_t most = __reduce_max_sync(kFull, own.length);
       if (!one_warp) {
         __syncthreads();
-        if (lane == 31) sm.warp_sums[warp] = make_int2(x, units);
+        if (lane == 31) sm.warp_sums[warp] = make_int3(x, units, most);
         __syncthreads();
-        const int2 v = lane < kThreads / 32 ? sm.warp_sums[lane] : make_int2(0, 0);
+        const int3 v = lane < kThreads / 32 ? sm.warp_sums[lane] : make_int3(0, 0, 0);
         x += __reduce_add_sync(kFull, lane < warp ? v.x : 0);
         units += __reduce_add_sync(kFull, lane < warp ? v.y : 0);
         sum = __reduce_add_sync(kFull, v.x);
         units_sum = __reduce_add_sync(kFull, v.y);
+        most = __reduce_max_sync(kFull, v.z);
       }
       const int32_t prefix = carry + x - mine, units_at = units_carry + units - own.units;
       carry += sum;
       units_carry += units_sum;
+      longest = max(longest, most);
       if (pass == 0 && base + kThreads >= p.num_seqs) {  // the axis' length is known
         total = carry;
         all_units = units_carry;
         const int32_t workers = min(p.workers, total);
-        works = worker < workers;
-        each = works ? total / workers : 0;
+        each = total > 0 ? total / workers : 0;
         rest = total - each * workers;
-        x0 = works ? TreeParams::part_start(worker, each, rest) : 0;
-        x1 = works ? TreeParams::part_start(worker + 1, each, rest) : 0;
+        whole = all_units <= workers && longest <= each + kWhole;
+        works = worker < (whole ? all_units : workers);
+        x0 = works && !whole ? TreeParams::part_start(worker, each, rest) : 0;
+        x1 = works && !whole ? TreeParams::part_start(worker + 1, each, rest) : 0;
       }
       // (batches scanned at once: by the warp that needs it, or by all)
-      if ((pass == 1 || at_once) && (!one_warp || warp == kKWarp) && mine > 0 && prefix <= x0 &&
-          x0 < prefix + mine) {
+      if ((pass == 0 && !at_once) || (one_warp && warp != kKWarp)) continue;
+      const auto within = [&](int32_t y) {
+        return whole ? units_at <= worker && worker < units_at + own.units
+                     : mine > 0 && prefix <= y && y < prefix + mine;
+      };
+      const auto move = [&](int32_t y) {
+        if (whole) return prefix + (worker - units_at) * own.length;
+        const int32_t start = prefix + (y - prefix) / own.length * own.length;
+        return TreeParams::moved(y, start, start + own.length, TreeParams::nearness(each));
+      };
+      if (works && within(x1)) sm.x1 = move(x1) + (whole ? own.length : 0);
+      if (within(x0)) {
+        sm.x0 = move(x0);
         sm.start_b = b;
         sm.start_at = prefix;
         sm.start_units = units_at;
@@ -570,6 +604,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------------ work walk and K loads
       if (lane == 0) {
         const uint64_t policy = p.at_once == 1 ? policy_evict_first() : policy_evict_last();
+        if (works) {
+          x0 = sm.x0;
+          if (x1 < total) x1 = sm.x1;
+        }
         Walk w{x0, x1, sm.start_at, sm.start_units, sm.start_b, {}};
         if (works) w.s.set(p, sm.start_q0, sm.start_n, sm.start_L);
         uint32_t pushed = 0, g = 0;
@@ -633,8 +671,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (more ? cut || (p.by_unit && nx.to != 0) : !p.by_unit && !told) {
                   int4 *dst = reinterpret_cast<int4 *>(
                       p.cuts + (p.by_unit ? unit * p.group + rank : (int)blockIdx.x));
-                  const int parts =
-                      cut ? TreeParams::part_of(start + w.s.length - 1, each, rest) - worker + 1 : 0;
+                  int parts = 0;
+                  if (cut) {  // up to the last worker with a start in the unit, unless that has moved out
+                    const int32_t end = start + w.s.length;
+                    const int past = TreeParams::part_of(end - 1, each, rest);
+                    parts = past - worker + 1;
+                    if (TreeParams::moved(TreeParams::part_start(past, each, rest), start, end,
+                                          TreeParams::nearness(each)) == end)
+                      --parts;
+                  }
                   dst[0] = make_int4(parts, worker, nx.b, nx.h);
                   dst[1] = make_int4(nx.q0, nx.n, nx.L, nx.c0);
                   dst[2] = make_int4(nx.chunks, 0, 0, 0);
@@ -736,10 +781,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after_sync();
         if (quad < ip->chunks) {  // (warp-uniform)
           if constexpr (F8) {
-            uint32_t top = 0;
-#pragma unroll 4
+            uint32_t top = 0;  // (the row's loads all at once; the second time they come from L1)
+#pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const uint4 x = row ? ld_once_u4(src + e) : make_uint4(0, 0, 0, 0);
+              const uint4 x = row ? ld_u4(src + e) : make_uint4(0, 0, 0, 0);
               top = __vmaxu2(top, __vmaxu2(bf16x2_absmax(x.x, x.y), bf16x2_absmax(x.z, x.w)));
             }
             top = max(top & 0xffffu, top >> 16);
@@ -753,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint32_t hi[8], lo[8];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const uint4 x = row ? ld_once_u4(src + 4 * q4 + e) : make_uint4(0, 0, 0, 0);
+                const uint4 x = row ? ld_u4(src + 4 * q4 + e) : make_uint4(0, 0, 0, 0);
                 const uint32_t w[4] = {x.x ^ p.q_sign, x.y ^ p.q_sign, x.z ^ p.q_sign, x.w ^ p.q_sign};
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {

@@ -60,6 +60,17 @@ def test_two_graphs_that_share_a_workspace(fp8):
 
 
 @BOTH
+@pytest.mark.parametrize("batch", [2, 9, 10, 16, 19, 20, 21, 38, 40])
+def test_batches_around_the_number_of_workers(batch, fp8):
+    """Whole units to a worker, cuts that move to a unit's end, and cuts that stay."""
+    rng = np.random.default_rng(batch)
+    for spread in (0, 40, 700):
+        ctx = [int(n) for n in 900 - rng.integers(0, spread + 1, batch)]
+        c = Case(ctx, [int(n) for n in rng.integers(1, 5, batch)], 16, 8, fp8=fp8, seed=batch)
+        check(c, c.attend(pkv))
+
+
+@BOTH
 def test_any_aligned_workspace_and_output(fp8):
     """16-byte aligned addresses: no more is promised."""
     c = Case([5000, 300], [6, 17], 8, 2, fp8=fp8, seed=5)
