@@ -17,7 +17,7 @@
 // over the sequences) and walks its own part. A cut costs an item more, its part of the rows in fp32 and
 // the merge: a part's start that lies within 8 granules of a unit's end moves there, and where there
 // are no more units than workers, none more than 12 granules longer than an equal part, a worker takes
-// a whole one (us, with and without: 33 x 512, 31 nodes of 16 / 2 heads 19.5 and 26.8, 16 x 1024, 4
+// a whole one (us, with and without: 33 x 1250, 31 nodes of 16 / 2 heads 26 and 32, 16 x 1024, 4
 // nodes of 16 / 8 19.0 and 21.5, 8-bit 33 x 100 to 4999 46 and 50; the other way 10 x 4096 37.1 and
 // 35.1, which moved starts make uneven). A unit within a worker's part is written out
 // directly; what a cut leaves is normalised and goes to the workspace with its log2-sum-exp, and
@@ -69,7 +69,7 @@
 //   8-bit, 2 to a KV head, 8 of them: 8 x 1024, 16 nodes             17.9 (2.5)
 //         256 sequences of 100 to 2048, trees of 5 to 8 nodes       182 (89)
 //   8-bit, 8 to a KV head, 2 of them: 33 x 100 to 4999               46.3 (7.5)
-// A call of a few keys takes 6.7 us (two launches, the scan, the chain of loads). Long bf16 contexts
+// A call of a few keys takes 7 us (the launch, the scan, the chain of loads). Long bf16 contexts
 // go at the memory's rate. What bounds the rest is the chain of a tile's steps (S, softmax, P V, the
 // hand-over of a buffer between two warps four times): about 1.05 us a tile and two of them under
 // way; leaving out the widening, the exponentials or three quarters of the products one at a
@@ -1268,12 +1268,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kSWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Merges the parts of the units that a cut between two workers went through. Block (x, y): cut x,
-// kCombineWarps / p.row_warps rows of its tile. A row's warps take its parts in turn, four in flight,
+// Merges the parts of the units that a cut between two workers went through. Block (x, y): cut x, from
+// the y-th on every gridDim.y-th kCombineWarps / p.row_warps rows of its tile. A row's warps take its parts in turn, four in flight,
 // each with a running maximum; what they have is merged in shared memory. The time is that of
 // dependent loads (the cut, then all parts at once) and of blocks that find no cut: there are as many
-// cuts as units, or workers where that is fewer.
-constexpr int kCombineWarps = 8, kInFlight = 4;
+// cuts as units, or workers where that is fewer. It takes 2 to 4 us of a call; where no unit can be cut
+// (no more units than workers, contexts up to 832) it is not launched (33 x 512, 31 nodes of 16 / 2
+// heads: 19.5 -> 14.5 us).
+constexpr int kCombineWarps = 8, kInFlight = 4, kCombineBlocks = 4;  // (of an SM)
 template <Mode M>
 __global__ void __launch_bounds__(kCombineWarps * 32)
     tree_combine_kernel(const __grid_constant__ TreeParams p) {
@@ -1285,82 +1287,85 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
   if (aborted(p.err) || cut.parts == 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row_in = warp / p.row_warps, sub = warp - row_in * p.row_warps;
-  const int t = blockIdx.y * (kCombineWarps / p.row_warps) + row_in;  // row of the tile
-  const int c = t / kChunkRows, r = t % kChunkRows, i = p.node_of(r);
-  const int chunk = cut.c0 + c, node = p.first_node(chunk) + i;
-  const int head = p.first_head(chunk) + r - i * p.hb;
-  const bool row = c < cut.chunks && i < p.nb && node < cut.n && head < p.group_heads;
   // part 0 is its worker's last item, the others are their workers' first ones
   const int rank = blockIdx.x % p.group;
   auto slot = [&](int k) -> int64_t {
     return 2 * ((int64_t)(cut.worker + k) * p.group + rank) + (k == 0 ? 1 : 0);
   };
-  float m = -INFINITY, sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  if (row) {
-#pragma unroll 1
-    for (int k0 = sub; k0 < cut.parts; k0 += kInFlight * p.row_warps) {
-      float lse[kInFlight];
-      float4 x[kInFlight];
-#pragma unroll
-      for (int u = 0; u < kInFlight; ++u) {
-        const int k = k0 + u * p.row_warps;
-        lse[u] = -INFINITY;
-        x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (k < cut.parts) {
-          const int64_t at = slot(k) * p.part_rows + t;
-          lse[u] = p.part_lse[at];
-          x[u] = *reinterpret_cast<const float4 *>(p.part_o + at * kD + 4 * lane);
-        }
-      }
-      float top = m;
-#pragma unroll
-      for (int u = 0; u < kInFlight; ++u) top = fmaxf(top, lse[u]);
-      const float base = top == -INFINITY ? 0.f : top, old = fast_exp2(m - base);
-      m = top;
-      sum *= old;
-#pragma unroll
-      for (int d = 0; d < 4; ++d) o[d] *= old;
-#pragma unroll
-      for (int u = 0; u < kInFlight; ++u) {
-        const float w = fast_exp2(lse[u] - base);  // (NaN stays)
-        sum += w;
-        o[0] += w * x[u].x;
-        o[1] += w * x[u].y;
-        o[2] += w * x[u].z;
-        o[3] += w * x[u].w;
-      }
-    }
-  }
-  if (p.row_warps > 1) {
-    outs[warp][lane] = make_float4(o[0], o[1], o[2], o[3]);
-    if (lane == 0) stats[warp] = make_float2(m, sum);
-    __syncthreads();
-    if (sub != 0) return;
-    float top = m;
-    for (int k = 1; k < p.row_warps; ++k) top = fmaxf(top, stats[warp + k].x);
-    const float base = top == -INFINITY ? 0.f : top;
-    sum = 0.f;
-    o[0] = o[1] = o[2] = o[3] = 0.f;
-    for (int k = 0; k < p.row_warps; ++k) {
-      const float2 st = stats[warp + k];
-      const float4 x = outs[warp + k][lane];
-      const float w = fast_exp2(st.x - base);
-      sum += w * st.y;
-      o[0] += w * x.x;
-      o[1] += w * x.y;
-      o[2] += w * x.z;
-      o[3] += w * x.w;
-    }
-  }
-  if (!row) return;
   bool dirty = false;
   for (int k = lane; k < cut.parts; k += 32) dirty |= p.dirty[slot(k)] != 0;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  uint16_t *dst = p.out + ((int64_t)(cut.q0 + node) * p.hq + cut.h * p.group_heads + head) * kD;
-  *reinterpret_cast<uint2 *>(dst + 4 * lane) =
-      make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
-  if (__any_sync(kFull, dirty))
-    not_finite_fix<M>(p, cut.b, cut.h, cut.n, cut.L, cut.q0 + node, node, dst, 4 * lane, 4);
+  // (with several warps to a row there are as many blocks as it takes)
+  for (int y = blockIdx.y; y < p.part_rows * p.row_warps / kCombineWarps; y += gridDim.y) {
+    const int t = y * (kCombineWarps / p.row_warps) + row_in;  // row of the tile
+    const int c = t / kChunkRows, r = t % kChunkRows, i = p.node_of(r);
+    const int chunk = cut.c0 + c, node = p.first_node(chunk) + i;
+    const int head = p.first_head(chunk) + r - i * p.hb;
+    const bool row = c < cut.chunks && i < p.nb && node < cut.n && head < p.group_heads;
+    float m = -INFINITY, sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+    if (row) {
+#pragma unroll 1
+      for (int k0 = sub; k0 < cut.parts; k0 += kInFlight * p.row_warps) {
+        float lse[kInFlight];
+        float4 x[kInFlight];
+#pragma unroll
+        for (int u = 0; u < kInFlight; ++u) {
+          const int k = k0 + u * p.row_warps;
+          lse[u] = -INFINITY;
+          x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (k < cut.parts) {
+            const int64_t at = slot(k) * p.part_rows + t;
+            lse[u] = p.part_lse[at];
+            x[u] = *reinterpret_cast<const float4 *>(p.part_o + at * kD + 4 * lane);
+          }
+        }
+        float top = m;
+#pragma unroll
+        for (int u = 0; u < kInFlight; ++u) top = fmaxf(top, lse[u]);
+        const float base = top == -INFINITY ? 0.f : top, old = fast_exp2(m - base);
+        m = top;
+        sum *= old;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) o[d] *= old;
+#pragma unroll
+        for (int u = 0; u < kInFlight; ++u) {
+          const float w = fast_exp2(lse[u] - base);  // (NaN stays)
+          sum += w;
+          o[0] += w * x[u].x;
+          o[1] += w * x[u].y;
+          o[2] += w * x[u].z;
+          o[3] += w * x[u].w;
+        }
+      }
+    }
+    if (p.row_warps > 1) {
+      outs[warp][lane] = make_float4(o[0], o[1], o[2], o[3]);
+      if (lane == 0) stats[warp] = make_float2(m, sum);
+      __syncthreads();
+      if (sub != 0) continue;
+      float top = m;
+      for (int k = 1; k < p.row_warps; ++k) top = fmaxf(top, stats[warp + k].x);
+      const float base = top == -INFINITY ? 0.f : top;
+      sum = 0.f;
+      o[0] = o[1] = o[2] = o[3] = 0.f;
+      for (int k = 0; k < p.row_warps; ++k) {
+        const float2 st = stats[warp + k];
+        const float4 x = outs[warp + k][lane];
+        const float w = fast_exp2(st.x - base);
+        sum += w * st.y;
+        o[0] += w * x.x;
+        o[1] += w * x.y;
+        o[2] += w * x.z;
+        o[3] += w * x.w;
+      }
+    }
+    if (!row) continue;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint16_t *dst = p.out + ((int64_t)(cut.q0 + node) * p.hq + cut.h * p.group_heads + head) * kD;
+    *reinterpret_cast<uint2 *>(dst + 4 * lane) =
+        make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+    if (__any_sync(kFull, dirty))
+      not_finite_fix<M>(p, cut.b, cut.h, cut.n, cut.L, cut.q0 + node, node, dst, 4 * lane, 4);
+  }
 }
 
 // How a call's work is cut, from what the host knows.
@@ -1368,8 +1373,8 @@ struct TreePlan {
   int32_t hb, nb, parts;  // heads and nodes of a chunk, chunks that share its nodes
   int32_t workers, group, heads, at_once, part_rows, row_warps;
   int64_t longest, units;  // bounds of the axis and of the units
-  bool by_unit;
-  int32_t cuts;
+  bool by_unit, uncut;     // uncut: whatever the lengths are, no unit is cut
+  int32_t cuts, cut_blocks;  // and blocks to merge one
   size_t dirty, part_o, part_lse, bytes;  // of the workspace
 };
 TreePlan plan_tree(int32_t num_seqs, int32_t max_nodes, int32_t hq, int32_t hkv,
@@ -1396,7 +1401,12 @@ TreePlan plan_tree(int32_t num_seqs, int32_t max_nodes, int32_t hq, int32_t hkv,
     t.row_warps *= 2;
   const size_t ctas = (size_t)t.workers * t.group;
   t.by_unit = units <= t.workers;
+  t.uncut = t.by_unit && max_context <= (1 + kWhole) * kGranule;
   t.cuts = (int32_t)(t.by_unit ? std::max<int64_t>(1, units) * t.group : (int64_t)ctas);
+  // as many as all its rows take, but no more than run at once unless a row takes several warps
+  t.cut_blocks = t.part_rows * t.row_warps / kCombineWarps;
+  if (t.row_warps == 1)
+    t.cut_blocks = std::max(1, std::min(t.cut_blocks, kCombineBlocks * num_sms / t.cuts));
   t.dirty = (size_t)t.cuts * sizeof(CutInfo);
   t.part_o = (t.dirty + ctas * 2 * sizeof(int32_t) + 31) / 32 * 32;
   t.part_lse = t.part_o + ctas * 2 * t.part_rows * kD * sizeof(float);
@@ -1463,9 +1473,8 @@ cudaError_t launch_tree(TreeParams p, const TreePlan &t, void *workspace, cudaSt
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, tree_flash_kernel<M>, km, vm, p);
-  if (e != cudaSuccess || t.workers == 1) return e;
-  return launch_after(tree_combine_kernel<M>,
-                      dim3((unsigned)t.cuts, (unsigned)(t.part_rows * t.row_warps / kCombineWarps)),
+  if (e != cudaSuccess || t.workers == 1 || t.uncut) return e;
+  return launch_after(tree_combine_kernel<M>, dim3((unsigned)t.cuts, (unsigned)t.cut_blocks),
                       kCombineWarps * 32, stream, p);
 }
 
