@@ -56,8 +56,9 @@
 // Warps (512 threads): 0-7 softmax and epilogue (warp c: chunk c), 8 work walk and K loads, 9 S
 // products, 10 V loads, 11 PV products, 12-15 Q into tensor memory, a look through the nodes' V rows,
 // and the widening of an 8-bit cache's V. Loads are TMA with 128-byte swizzle, 64 keys to a box (a granule
-// never straddles a block). K and V have two slots each: more (3 + 3, 4 + 3) made every case slower,
-// K tiles far ahead taking their turn before V tiles that are needed sooner.
+// never straddles a block). K and V have two slots each: more (3 + 3, 4 + 3) made every bf16 case slower,
+// K tiles far ahead taking their turn before V tiles that are needed sooner. K's codes of an 8-bit cache
+// have four (16 x 32768, 4 nodes 237 -> 221 us; four of V's codes change nothing).
 // TMEM (512 columns): Q [0, 64) [64, 128), S [128, 256) [256, 384), O [384, 512).
 //
 // Measured (us; the bytes of K, V, q and out at 6.8 TB/s in brackets):
@@ -66,12 +67,13 @@
 //   bf16, 3 to a KV head, 4 of them: 1 x 17188, 13 nodes             17.7 (5.2)
 //   bf16, 4 to a KV head, 8 of them: 16 x 32768, 4 nodes 302 (316), 32 nodes 323 (317), 48 to 64
 //         nodes, two row tiles, 429 (303; their exponentials 232, their products 232)
-//   8-bit, 2 to a KV head, 8 of them: 8 x 1024, 16 nodes             17.9 (2.5)
-//         256 sequences of 100 to 2048, trees of 5 to 8 nodes       182 (89)
-//   8-bit, 8 to a KV head, 2 of them: 33 x 100 to 4999               46.3 (7.5)
+//   8-bit, 2 to a KV head, 8 of them: 8 x 1024, 16 nodes             17.8 (2.5)
+//         256 sequences of 100 to 2048, trees of 5 to 8 nodes       181 (89)
+//   8-bit, 8 to a KV head, 2 of them: 33 x 100 to 4999               46.9 (7.5)
+//   8-bit, 4 to a KV head, 8 of them: 16 x 32768, 4 nodes 221 (158), 32 nodes 262, 64 nodes 501
 // A call of a few keys takes 7 us (the launch, the scan, the chain of loads). Long bf16 contexts
 // go at the memory's rate. What bounds the rest is the chain of a tile's steps (S, softmax, P V, the
-// hand-over of a buffer between two warps four times): about 1.05 us a tile and two of them under
+// hand-over of a buffer between two warps four times): about 1 us a tile and two of them under
 // way; leaving out the widening, the exponentials or three quarters of the products one at a
 // time takes 3 % off a long 8-bit call, all of them together 15 %. An item more costs about 5 us where it
 // has one tile (a row of q takes a trip to memory, the softmax warps wait for the last product before
@@ -112,7 +114,8 @@ constexpr int kSoftmaxWarps = 8;
 constexpr int kKWarp = 8, kSWarp = 9, kVWarp = 10, kPvWarp = 11, kQWarp0 = 12;
 constexpr int kThreads = 16 * 32;
 constexpr int kSlots = 2;     // of K and of V
-constexpr int kRawSlots = 2;  // of each pool's codes, 8-bit cache
+constexpr int kRawSlots = 2;  // of V's codes, 8-bit cache
+constexpr int kKSlots8 = 4;   // of K's codes
 constexpr uint32_t kTileBytes = kTile * kD * 2;
 constexpr uint32_t kPlane = kTileBytes / 2;         // 64 dims of the tile's keys, 128-byte rows
 constexpr uint32_t kGranuleBytes = kGranule * 128;  // of a plane, or of an 8-bit pool
@@ -160,7 +163,7 @@ struct NoRaw {};
 
 template <Mode M>
 struct TreeSmem {
-  static constexpr int kKSlots = M == kFp8 ? kRawSlots : kSlots;
+  static constexpr int kKSlots = M == kFp8 ? kKSlots8 : kSlots;
   static constexpr uint32_t kKBytes = M == kFp8 ? kRawBytes : kTileBytes;
   uint8_t k[kKSlots][kKBytes];  // 1024-byte aligned (128-byte swizzle atoms)
   uint8_t v[kSlots][kTileBytes];
