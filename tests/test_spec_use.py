@@ -1,12 +1,16 @@
 """The calls of speculative decoding the way programs make them: several at once, captured graphs that
 share a workspace, batches with padding, and what must not spread from one row to another."""
+import os
+import re
+
 import numpy as np
 import pytest
 import torch
 
-import paged_kv_cache_208_gb300 as pkv
+from libbuild import ROOT, build_and_import
 from tree_util import Case, D, assert_close, bf16_weights, ints
 
+pkv = build_and_import()
 pytestmark = pytest.mark.gpu
 BOTH = pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
 
@@ -222,3 +226,28 @@ def test_appends_of_many_layers_and_streams():
     for other in pools[1:]:
         for x, y in zip(pools[0], other):
             assert torch.equal(x, y)
+
+
+def test_the_step_of_the_readme():
+    with open(os.path.join(ROOT, "README.md")) as f:
+        blocks = re.findall(r"```python\n(.*?)```", f.read(), re.S)
+    (code,) = [b for b in blocks if "kv_accept" in b]
+    c = Case([700, 90, 300], [5, 1, 9], 8, 2, fp8=True, seed=12)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(12)
+    angle = torch.rand((800, D // 2), generator=g, device="cuda") * 6
+    w = torch.ones((D,), dtype=torch.bfloat16, device="cuda")
+    names = dict(pkv=pkv, qkv=torch.randn((15, 12 * D), generator=g, device="cuda").to(torch.bfloat16),
+                 positions=torch.arange(15, device="cuda"), num_q_heads=8, q_weight=w, k_weight=w,
+                 cos_sin=torch.cat([angle.cos(), angle.sin()], 1), context_lens=c.lens,
+                 tables=c.tables, k_cache=c.k, v_cache=c.v, k_scale=c.scales[0], v_scale=c.scales[1],
+                 cu_seqlens_q=c.cu, max_context_len=700, max_nodes=9, scale=c.scale,
+                 tree_mask=c.mask, accepted=ints([[0, 3], [0, -1], [2, 8]]),
+                 num_accepted=ints([2, 1, 2]))
+    layer = code.split("# ...")
+    exec(compile(layer[0], "README.md", "exec"), names)
+    c.q = names["q"]
+    check(c, names["out"])
+    exec(compile("# ..." + layer[1], "README.md", "exec"), names)
+    assert names["new_lens"].tolist() == [697, 90, 293]
+    assert pkv.get_device_errors(reset=True) == 0
