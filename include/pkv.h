@@ -555,9 +555,10 @@ pkv_status pkv_kv_evict(const float *weights, int64_t weights_stride,
  * out:           [total_q, num_q_heads, head_dim] bf16, contiguous; may not overlap q.
  * Implemented: head_dim == 128, block_size a multiple of 256, num_blocks * block_size < 2^31,
  * max_seqlen_q <= 2^20, q_tok_stride a multiple of 8, 16-byte aligned q, pools, scales and out; any
- * num_q_heads / num_kv_heads; as long as the batch's work -- for every sequence ceil(max_context_len /
- * 64), times the 128-row tiles of its nodes and the KV heads, as one CTA or several take them together --
- * stays below 2^30.
+ * num_q_heads / num_kv_heads; contexts below 2^31 - 1024; as long as the batch's work stays below 2^30:
+ * num_seqs times the granules of 64 keys of max_context_len (or of the block table's row, if that is
+ * less), times the 128-row tiles of max_seqlen_q nodes and the KV heads, as many of both as CTAs take
+ * together counting once.
  */
 size_t pkv_tree_workspace_bytes(int32_t num_seqs, int32_t max_seqlen_q, int32_t num_q_heads,
                                 int32_t num_kv_heads, int32_t head_dim, int32_t max_context_len);

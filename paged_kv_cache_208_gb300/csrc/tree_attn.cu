@@ -1515,8 +1515,11 @@ pkv_status tree_attn(const void *q, int64_t q_tok_stride, int64_t total_q, const
   unsigned int *err = current_error_word();
   const int num_sms = current_sm_count();
   if (!err || num_sms <= 0) return PKV_ERR_CUDA;
+  // (positions up to a tile past the context are 32 bits)
+  const int32_t longest = (int32_t)std::min<int64_t>(
+      std::min(max_context_len, INT32_MAX - 1024), (int64_t)block_table_width * block_size);
   const TreePlan plan =
-      plan_tree(num_seqs, max_seqlen_q, num_q_heads, num_kv_heads, max_context_len, num_sms);
+      plan_tree(num_seqs, max_seqlen_q, num_q_heads, num_kv_heads, longest, num_sms);
   if (plan.longest > (1 << 30)) return PKV_ERR_UNSUPPORTED;
   if (!workspace || !aligned16(workspace) || workspace_bytes < plan.bytes) return PKV_ERR_WORKSPACE;
   TreeParams prm{};
@@ -1532,7 +1535,7 @@ pkv_status tree_attn(const void *q, int64_t q_tok_stride, int64_t total_q, const
   prm.context_lens = context_lens;
   prm.cu = cu_seqlens_q;
   prm.max_nodes = max_seqlen_q;
-  prm.max_context = max_context_len;
+  prm.max_context = longest;
   prm.mask = reinterpret_cast<const uint64_t *>(tree_mask);
   prm.mask_words = mask_words;
   prm.hq = num_q_heads;
