@@ -178,7 +178,7 @@ struct TreeSmem {
   uint64_t s_full[2], p_full[2], o_full[2], o_free, drain[2];
   uint64_t item_full[kRing], item_empty[kRing];
   uint64_t scanned[kRing];         // `dirty` is known
-  uint64_t done[kRing];            // the item's last PV is
+  uint64_t past[kRing];            // the item's last S has been waited for
   uint32_t tmem_base;
   int32_t stop;
   int3 warp_sums[kThreads / 32];  // granules, units, the longest unit
@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.item_full[i], 1);
       mbar_init(&sm.item_empty[i], kItemConsumers);
       mbar_init(&sm.scanned[i], 4);
-      mbar_init(&sm.done[i], 1);
+      mbar_init(&sm.past[i], 1);
     }
     sm.start_b = 0;
     sm.start_at = 0;
@@ -1037,11 +1037,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // A warp goes through a tile a granule at a time, 32 of its keys to a thread. The loops over
       // granules stay loops: unrolled, a tile's code does not fit the instruction caches beside the
       // other warps'. (Two warps to a chunk where there are few, a granule or a tile each in turn:
-      // slower for the same reason, and by what they have to agree on.) Warps whose chunk the item
-      // does not have wait for its end, and the first warp arrives for them.
-      const int c = warp, ch = lane >> 4, r = lane & 15;  // chunk, half of the granule's keys, row
+      // slower for the same reason, and by what they have to agree on.)
+      const int ch = lane >> 4, r = lane & 15;  // half of the granule's keys, row
       const int i = p.node_of(r), head_r = r - i * p.hb;
-      const uint32_t lane_addr = tmem + ((uint32_t)((c & 3) * 32 + (c >> 2) * 16) << 16);
       uint32_t taken = 0, g = 0;
       bool ok = true;
       while (ok) {
@@ -1049,6 +1047,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ip || ip->last) break;
         const int ring = taken % kRing;
         const int tiles = ip->tiles, key0 = ip->key0, key1 = ip->key1, n = ip->n, root = ip->L - n;
+        // The chunk: warps c and c + 4 reach the lanes of chunks c and c + 4. They change places from item
+        // to item, so that with up to four chunks one half writes an item out while the other is at
+        // the next one.
+        const int c = (warp + 4 * (taken & 1)) & 7;
+        const uint32_t lane_addr = tmem + ((uint32_t)((c & 3) * 32 + (c >> 2) * 16) << 16);
         const bool mine = c < ip->chunks;  // (warp-uniform)
         const int chunk = ip->c0 + c, node = p.first_node(chunk) + i;
         const int head = p.first_head(chunk) + head_r;
@@ -1059,19 +1062,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (row)
             for (int e = 0; e < 8; ++e)
               reinterpret_cast<uint4 *>(dst + 64 * ch)[e] = make_uint4(0, 0, 0, 0);
-        } else if (!mine) {  // it has no rows: the first warp arrives for it, tile by tile
+        } else if (!mine) {
+          // The first chunk's warp arrives for it. (Its next wait for an S is not before the one
+          // before that is over: a wait knows two phases of a barrier.)
           g += tiles;
-          ok = __all_sync(kFull, wait_bar(&sm.done[ring], (taken / kRing) & 1, p.err));
+          ok = __all_sync(kFull, wait_bar(&sm.past[ring], (taken / kRing) & 1, p.err));
           if (!ok) break;
-          if (lane == 0) mbar_arrive(&sm.o_free);
         }
         if (tiles == 0 || !mine) {
-          if (tiles == 0 && warp == 0 && lane == 0) mbar_arrive(&sm.done[ring]);
+          if (tiles == 0 && c == 0 && lane == 0) mbar_arrive(&sm.past[ring]);
           release_item(sm, taken, lane);
           ++taken;
           continue;
         }
-        const uint32_t arrivals = warp == 0 ? kSoftmaxWarps + 1 - ip->chunks : 1;
+        const uint32_t arrivals = c == 0 ? kSoftmaxWarps + 1 - ip->chunks : 1;
         // what the row sees of its tree's first 64 nodes, loaded ahead of the tiles that need it
         const uint64_t first_word = row && key1 > root ? mask_word(p, q_row, node, 0) : 0;
         auto word = [&](int w) -> uint64_t {
@@ -1083,6 +1087,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // warp-uniform results: the TMEM loads and stores below are .sync.aligned
           ok = __all_sync(kFull, wait_bar(&sm.s_full[sb], (g >> 1) & 1, p.err));
           if (!ok) break;
+          if (j == tiles - 1 && c == 0 && lane == 0) mbar_arrive(&sm.past[ring]);
           tc_fence_after_sync();
           if constexpr (F8)
             if (j == 0)
@@ -1206,7 +1211,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(kFull, wait_bar(&sm.o_full[(g - 1) & 1], ((g - 1) >> 1) & 1, p.err) &&
                                    wait_bar(&sm.scanned[ring], (taken / kRing) & 1, p.err));
         if (!ok) break;
-        if (warp == 0 && lane == 0) mbar_arrive(&sm.done[ring]);
         const Item &it = *ip;
         const bool dirty = sm.dirty[ring] != 0;
         // (NaN stays; a row that sees nothing gets zeros)
@@ -1223,7 +1227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (k == 1) {
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.o_free);
+            if (lane == 0) mbar_arrive_count(&sm.o_free, arrivals);
           }
           if (!row) continue;
           if (it.to == 2) {
@@ -1256,7 +1260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (it.to < 2) {
           if (row && ch == 0)
             p.part_lse[at] = l > 0.f ? m_run + log2_approx(l) : l == 0.f ? -INFINITY : l;
-          if (warp == 0 && lane == 0) p.dirty[slot] = dirty;
+          if (c == 0 && lane == 0) p.dirty[slot] = dirty;
         }
         release_item(sm, taken, lane);
         ++taken;
