@@ -10,9 +10,11 @@
 // One CTA owns K or V of a sequence for some of its heads. The bytes are few (the moved rows, read
 // and written once), so what counts is the chain of dependent loads: list and lengths, table, rows
 // (and their scales beside them). Each step of it is taken for all rows at once. 8 small trees take
-// 3.0 us, which is that chain; the paths of 256 trees of 64 nodes (37 MB) 9.2 us, 12.5 us in the
-// 8-bit cache (18 MB and the scales' chain): 14.4 and 18.8 us with CTAs of 256 threads, of which
-// four fit on an SM, divisions in place of shifts, and the rows asked for after the scales.
+// 2.8 us, which is that chain; the paths of 256 trees of 64 nodes (37 MB) 8.9 us, 9.6 us in the 8-bit
+// cache (18 MB, the scales, the re-rounding of groups whose scale grew): 14.4 and 18.8 us with CTAs of
+// 256 threads, of which four fit on an SM, divisions in place of shifts, and the rows asked for after
+// the scales; 12.1 us in 8 bits with 80 registers a thread, so that a wave held 912 of the 1024 CTAs
+// (four loads at once for the re-rounding: 11.0, by its registers).
 #include <math.h>
 
 #include <algorithm>
@@ -54,11 +56,12 @@ __device__ __forceinline__ uint4 rescale16(uint4 w, float ratio) {
 }
 
 template <bool F8>
-__global__ void __launch_bounds__(kThreads) kv_accept_kernel(const AcceptParams p) {
+__global__ void __launch_bounds__(kThreads, 7) kv_accept_kernel(const AcceptParams p) {
   constexpr int kShift = F8 ? 3 : 4;  // a head's row has 2^kShift pieces of 16 bytes
   __shared__ int64_t src_row[kRows], dst_row[kRows];  // pool rows; -1: a bad block
   __shared__ float src_scale[F8 ? kRows : 1][kMaxHeads];
-  __shared__ float old_scale[kMaxHeads], new_scale[kMaxHeads];
+  __shared__ float old_scale[kMaxHeads];
+  __shared__ uint32_t new_scale[kMaxHeads];  // bits: of positive numbers in the same order
   __shared__ int32_t path[kThreads];  // the list's first entries
   __shared__ int32_t count;
   const int tid = threadIdx.x;
@@ -134,6 +137,7 @@ __global__ void __launch_bounds__(kThreads) kv_accept_kernel(const AcceptParams 
       src_row[tid] = pool_row(start + entry(j0 + tid));
       dst_row[tid] = pool_row(start + j0 + tid);
     }
+    if (F8 && tid < kMaxHeads) new_scale[tid] = 0;
     __syncthreads();
     for (int i0 = 0; i0 < rows; i0 += row_step * kLoads) {
       uint4 x[kLoads];
@@ -145,26 +149,30 @@ __global__ void __launch_bounds__(kThreads) kv_accept_kernel(const AcceptParams 
       }
       const int64_t d0 = dst_row[0];
       if (F8 && i0 == 0 && d0 >= 0) {  // (while the rows are on their way)
-        if (tid < heads) old_scale[tid] = scales[scale_at(d0, h0 + tid)];
+        auto raise = [&](int k, float s) {
+          if (s > 0.f) atomicMax(&new_scale[k], __float_as_uint(s));
+        };
+        if (tid < heads) {
+          old_scale[tid] = scales[scale_at(d0, h0 + tid)];
+          raise(tid, old_scale[tid]);
+        }
         for (int i = tid; i < rows << p.heads_shift; i += kThreads) {
           const int r = i >> p.heads_shift, k = i & (per - 1);
-          src_scale[r][k] =
+          const float s =
               k < heads && src_row[r] >= 0 ? scales[scale_at(src_row[r], h0 + k)] : 0.f;
+          src_scale[r][k] = s;
+          raise(k, s);
         }
         __syncthreads();
-        if (tid < heads) {
-          float s = old_scale[tid];
-          for (int i = 0; i < rows; ++i) s = fmaxf(s, src_scale[i][tid]);
-          new_scale[tid] = s;
-          if (s > old_scale[tid]) scales[scale_at(d0, h0 + tid)] = s;
-        }
-        __syncthreads();
+        if (tid < heads && __uint_as_float(new_scale[tid]) > old_scale[tid])
+          scales[scale_at(d0, h0 + tid)] = __uint_as_float(new_scale[tid]);
         // the rows of the group from before the tree, at the scale that grew
         const int before = j0 == 0 ? (int)(start % kFp8Group) : 0;
-        if (any && new_scale[h] > old_scale[h])
+        const float scale = __uint_as_float(new_scale[h]);
+        if (any && scale > old_scale[h])
           for (int r = r0; r < before; r += row_step) {
             uint4 *w = piece_of(d0 - before + r);
-            *w = rescale16(*w, old_scale[h] / new_scale[h]);
+            *w = rescale16(*w, old_scale[h] / scale);
           }
       }
       __syncthreads();  // (each pass is read before it is written)
@@ -174,7 +182,7 @@ __global__ void __launch_bounds__(kThreads) kv_accept_kernel(const AcceptParams 
         if (!any || r >= rows || dst_row[r] < 0) continue;
         bool same = src_row[r] == dst_row[r];
         if (F8) {
-          const float ratio = src_scale[r][h] / new_scale[h];
+          const float ratio = src_scale[r][h] / __uint_as_float(new_scale[h]);
           if (ratio < 1.f) {
             x[u] = rescale16(x[u], ratio);
             same = false;
