@@ -50,10 +50,11 @@
 // 2^14 in fp16's normal range), and l sums P' / 2^(v + 6).
 //
 // Rows. 16 rows make a chunk: nb = 16 / G nodes with their G query heads (with more than 16 heads
-// one node and 16 of them). Chunk c of a tile lies in 16 of the 128 TMEM lanes that softmax warp c
-// reads, lane quadrant c % 4: with few rows the softmax is spread over all four SM sub-partitions.
+// one node and 16 of them). Chunk c of a tile lies in 16 of the 128 TMEM lanes, in quadrant c % 4, that
+// softmax warps c and c + 4 reach: with few rows the softmax is spread over all four SM
+// sub-partitions, and the warps take turns, an item each.
 //
-// Warps (512 threads): 0-7 softmax and epilogue (warp c: chunk c), 8 work walk and K loads, 9 S
+// Warps (512 threads): 0-7 softmax and epilogue (a chunk each), 8 work walk and K loads, 9 S
 // products, 10 V loads, 11 PV products, 12-15 Q into tensor memory, a look through the nodes' V rows,
 // and the widening of an 8-bit cache's V. Loads are TMA with 128-byte swizzle, 64 keys to a box (a granule
 // never straddles a block). K and V have two slots each: more (3 + 3, 4 + 3) made every bf16 case slower,
@@ -501,8 +502,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.scanned[i], 4);
       mbar_init(&sm.past[i], 1);
     }
-    sm.start_b = 0;
-    sm.start_at = 0;
     fence_mbar_init();
     prefetch_tensormap(&kmap);
     prefetch_tensormap(&vmap);
