@@ -224,7 +224,7 @@ struct TreeParams {
   CutInfo *cuts;
   int32_t *dirty;
   float *part_o, *part_lse;      // [CTA][2][part_rows][kD], [CTA][2][part_rows]
-  int32_t part_rows, row_warps;  // row_warps: of tree_combine_kernel, for a row
+  int32_t part_rows, row_warps, block_warps;  // of tree_combine_kernel: warps for a row, of a block
 
   __device__ __forceinline__ int chunks_of(int n) const {
     return nb == 1 ? n * parts : (int)__umulhi(n + nb - 1, nb_magic);  // (nb > 1: one part)
@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kKWarp) {
       // ------------------------------------------------------------ work walk and K loads
       if (lane == 0) {
-        const uint64_t policy = p.at_once == 1 ? policy_evict_first() : policy_evict_last();
+        const uint64_t policy = policy_evict_first();
         if (works) {
           x0 = sm.x0;
           if (x1 < total) x1 = sm.x1;
@@ -713,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kVWarp) {
       // ------------------------------------------------------------ V loads
       if (lane == 0) {
-        const uint64_t policy = p.at_once == 1 ? policy_evict_first() : policy_evict_last();
+        const uint64_t policy = policy_evict_first();
         constexpr uint32_t kN = F8 ? kRawSlots : kSlots;
         uint32_t taken = 0, g = 0;
         bool ok = true;
@@ -1275,13 +1275,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Merges the parts of the units that a cut between two workers went through. Block (x, y): cut x, from
-// the y-th on every gridDim.y-th kCombineWarps / p.row_warps rows of its tile. A row's warps take its parts in turn, four in flight,
+// the y-th on every gridDim.y-th p.block_warps / p.row_warps rows of its tile. A row's warps take its parts in turn, four in flight,
 // each with a running maximum; what they have is merged in shared memory. The time is that of
 // dependent loads (the cut, then all parts at once) and of blocks that find no cut: there are as many
 // cuts as units, or workers where that is fewer. It takes 2 to 4 us of a call; where no unit can be cut
 // (no more units than workers, contexts up to 832) it is not launched (33 x 512, 31 nodes of 16 / 2
 // heads: 19.5 -> 14.5 us).
-constexpr int kCombineWarps = 8, kInFlight = 4, kCombineBlocks = 4;  // (of an SM)
+constexpr int kCombineWarps = 8, kInFlight = 4;  // warps of a block: at most
 template <Mode M>
 __global__ void __launch_bounds__(kCombineWarps * 32)
     tree_combine_kernel(const __grid_constant__ TreeParams p) {
@@ -1301,8 +1301,8 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
   bool dirty = false;
   for (int k = lane; k < cut.parts; k += 32) dirty |= p.dirty[slot(k)] != 0;
   // (with several warps to a row there are as many blocks as it takes)
-  for (int y = blockIdx.y; y < p.part_rows * p.row_warps / kCombineWarps; y += gridDim.y) {
-    const int t = y * (kCombineWarps / p.row_warps) + row_in;  // row of the tile
+  for (int y = blockIdx.y; y < p.part_rows * p.row_warps / p.block_warps; y += gridDim.y) {
+    const int t = y * (p.block_warps / p.row_warps) + row_in;  // row of the tile
     const int c = t / kChunkRows, r = t % kChunkRows, i = p.node_of(r);
     const int chunk = cut.c0 + c, node = p.first_node(chunk) + i;
     const int head = p.first_head(chunk) + r - i * p.hb;
@@ -1377,7 +1377,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
 // How a call's work is cut, from what the host knows.
 struct TreePlan {
   int32_t hb, nb, parts;  // heads and nodes of a chunk, chunks that share its nodes
-  int32_t workers, group, heads, at_once, part_rows, row_warps;
+  int32_t workers, group, heads, at_once, part_rows, row_warps, block_warps;
   int64_t longest, units;  // bounds of the axis and of the units
   bool by_unit, uncut;     // uncut: whatever the lengths are, no unit is cut
   int32_t cuts, cut_blocks;  // and blocks to merge one
@@ -1409,10 +1409,14 @@ TreePlan plan_tree(int32_t num_seqs, int32_t max_nodes, int32_t hq, int32_t hkv,
   t.by_unit = units <= t.workers;
   t.uncut = t.by_unit && max_context <= (1 + kWhole) * kGranule;
   t.cuts = (int32_t)(t.by_unit ? std::max<int64_t>(1, units) * t.group : (int64_t)ctas);
-  // as many as all its rows take, but no more than run at once unless a row takes several warps
-  t.cut_blocks = t.part_rows * t.row_warps / kCombineWarps;
+  // Blocks of two warps (bf16 cache: of four) fit beside the main kernel's CTA and are there when it
+  // ends (8-bit, 256 ragged 170 us, 172 with four warps, 176 with eight); with many rows more blocks
+  // cost more (8 x 1024, 64 nodes of 16 / 8 heads: 23.8, 23.0, 22.6). As many as all rows take, but no
+  // more than run at once unless a row takes several warps.
+  t.block_warps = std::max(t.part_rows <= 32 ? 2 : 4, t.row_warps);
+  t.cut_blocks = t.part_rows * t.row_warps / t.block_warps;
   if (t.row_warps == 1)
-    t.cut_blocks = std::max(1, std::min(t.cut_blocks, kCombineBlocks * num_sms / t.cuts));
+    t.cut_blocks = std::max(1, std::min(t.cut_blocks, 32 / t.block_warps * num_sms / t.cuts));
   t.dirty = (size_t)t.cuts * sizeof(CutInfo);
   t.part_o = (t.dirty + ctas * 2 * sizeof(int32_t) + 31) / 32 * 32;
   t.part_lse = t.part_o + ctas * 2 * t.part_rows * kD * sizeof(float);
@@ -1457,6 +1461,7 @@ cudaError_t launch_tree(TreeParams p, const TreePlan &t, void *workspace, cudaSt
   p.part_lse = reinterpret_cast<float *>(ws + t.part_lse);
   p.part_rows = t.part_rows;
   p.row_warps = t.row_warps;
+  p.block_warps = t.block_warps;
   const size_t smem = sizeof(TreeSmem<M>) + 1024;
   static bool ready[64] = {};
   int dev = 0;
@@ -1481,7 +1486,7 @@ cudaError_t launch_tree(TreeParams p, const TreePlan &t, void *workspace, cudaSt
   e = cudaLaunchKernelEx(&cfg, tree_flash_kernel<M>, km, vm, p);
   if (e != cudaSuccess || t.workers == 1 || t.uncut) return e;
   return launch_after(tree_combine_kernel<M>, dim3((unsigned)t.cuts, (unsigned)t.cut_blocks),
-                      kCombineWarps * 32, stream, p);
+                      t.block_warps * 32, stream, p);
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
