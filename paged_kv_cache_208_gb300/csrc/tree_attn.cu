@@ -64,13 +64,13 @@
 //
 // Measured (us; the bytes of K, V, q and out at 6.8 TB/s in brackets):
 //   bf16, 2 heads to a KV head, 8 KV heads: 8 x 1024, chains of 4    16.6 (5.0)
-//         256 sequences of 100 to 2048, trees of 5 to 8 nodes       194 (178)
+//         256 sequences of 100 to 2048, trees of 5 to 8 nodes       193 (178)
 //   bf16, 3 to a KV head, 4 of them: 1 x 17188, 13 nodes             17.7 (5.2)
 //   bf16, 4 to a KV head, 8 of them: 16 x 32768, 4 nodes 302 (316), 32 nodes 323 (317), 48 to 64
-//         nodes, two row tiles, 429 (303; their exponentials 232, their products 232)
+//         nodes, two row tiles, 425 (303; their exponentials 232, their products 232)
 //   8-bit, 2 to a KV head, 8 of them: 8 x 1024, 16 nodes             17.4 (2.5)
-//         256 sequences of 100 to 2048, trees of 5 to 8 nodes       175 (89)
-//   8-bit, 8 to a KV head, 2 of them: 33 x 100 to 4999               46.9 (7.5)
+//         256 sequences of 100 to 2048, trees of 5 to 8 nodes       171 (89)
+//   8-bit, 8 to a KV head, 2 of them: 33 x 100 to 4999               46.6 (7.5)
 //   8-bit, 4 to a KV head, 8 of them: 16 x 32768, 4 nodes 221 (158), 32 nodes 262, 64 nodes 501
 // A call of a few keys takes 7 us (the launch, the scan, the chain of loads). Long bf16 contexts
 // go at the memory's rate. What bounds the rest is the chain of a tile's steps (S, softmax, P V, the
