@@ -16,7 +16,7 @@
 // but one of them). The lengths are device data, so every CTA sums them up at its start (one scan
 // over the sequences) and walks its own part. A cut costs an item more, its part of the rows in fp32 and
 // the merge: a part's start that lies within 8 granules of a unit's end moves there, and where there
-// are no more units than workers, none more than 12 granules longer than an equal part, a worker takes
+// are no more units than workers, none more than 7 or 12 granules longer than an equal part, a worker takes
 // a whole one (us, with and without: 33 x 1250, 31 nodes of 16 / 2 heads 26 and 32, 16 x 1024, 4
 // nodes of 16 / 8 19.0 and 21.5, 8-bit 33 x 100 to 4999 46 and 50; the other way 10 x 4096 37.1 and
 // 35.1, which moved starts make uneven). A unit within a worker's part is written out
@@ -127,7 +127,6 @@ constexpr uint32_t kQCol = 0, kSCol = 128, kOCol = 384, kTmemCols = 512;
 constexpr int kItemConsumers = kSoftmaxWarps + 3 + 4;  // S, V, PV and Q warps
 constexpr int kMaxGroup = 8, kMaxTiles = 4;  // CTAs, and row tiles, of a worker
 constexpr int kNear = 8;        // granules that a part may grow or shrink by at an end
-constexpr int kWhole = 12;      // granules that a unit may be longer than a part without being cut
 constexpr int kOffset8 = 6;     // log2 of what P' is larger by, 8-bit cache
 
 enum Mode { kTwoParts, kOnePart, kFp8 };
@@ -225,6 +224,7 @@ struct TreeParams {
   int32_t *dirty;
   float *part_o, *part_lse;      // [CTA][2][part_rows][kD], [CTA][2][part_rows]
   int32_t part_rows, row_warps, block_warps;  // of tree_combine_kernel: warps for a row, of a block
+  int32_t whole;  // granules that a unit may be longer than a part without being cut
 
   __device__ __forceinline__ int chunks_of(int n) const {
     return nb == 1 ? n * parts : (int)__umulhi(n + nb - 1, nb_magic);  // (nb > 1: one part)
@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int32_t workers = min(p.workers, total);
         each = total > 0 ? total / workers : 0;
         rest = total - each * workers;
-        whole = all_units <= workers && longest <= each + kWhole;
+        whole = all_units <= workers && longest <= each + p.whole;
         works = worker < (whole ? all_units : workers);
         x0 = works && !whole ? TreeParams::part_start(worker, each, rest) : 0;
         x1 = works && !whole ? TreeParams::part_start(worker + 1, each, rest) : 0;
@@ -1279,7 +1279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // each with a running maximum; what they have is merged in shared memory. The time is that of
 // dependent loads (the cut, then all parts at once) and of blocks that find no cut: there are as many
 // cuts as units, or workers where that is fewer. It takes 2 to 4 us of a call; where no unit can be cut
-// (no more units than workers, contexts up to 832) it is not launched (33 x 512, 31 nodes of 16 / 2
+// (no more units than workers, contexts up to 512 or 832) it is not launched (33 x 512, 31 nodes of 16 / 2
 // heads: 19.5 -> 14.5 us).
 constexpr int kCombineWarps = 8, kInFlight = 4;  // warps of a block: at most
 template <Mode M>
@@ -1380,6 +1380,7 @@ struct TreePlan {
   int32_t workers, group, heads, at_once, part_rows, row_warps, block_warps;
   int64_t longest, units;  // bounds of the axis and of the units
   bool by_unit, uncut;     // uncut: whatever the lengths are, no unit is cut
+  int32_t whole;             // see TreeParams
   int32_t cuts, cut_blocks;  // and blocks to merge one
   size_t dirty, part_o, part_lse, bytes;  // of the workspace
 };
@@ -1407,7 +1408,10 @@ TreePlan plan_tree(int32_t num_seqs, int32_t max_nodes, int32_t hq, int32_t hkv,
     t.row_warps *= 2;
   const size_t ctas = (size_t)t.workers * t.group;
   t.by_unit = units <= t.workers;
-  t.uncut = t.by_unit && max_context <= (1 + kWhole) * kGranule;
+  // With many more workers than units a unit is worth cutting sooner (us, limits of 7 and 12: 1 x 832
+  // with 16 / 8 heads, 19 workers, 10.7 and 12.6; 8 x 832 16.1 and 14.1).
+  t.whole = t.workers >= 4 * units ? 7 : 12;
+  t.uncut = t.by_unit && max_context <= (1 + t.whole) * kGranule;
   t.cuts = (int32_t)(t.by_unit ? std::max<int64_t>(1, units) * t.group : (int64_t)ctas);
   // Blocks of two warps (bf16 cache: of four) fit beside the main kernel's CTA and are there when it
   // ends (8-bit, 256 ragged 170 us, 172 with four warps, 176 with eight); with many rows more blocks
@@ -1447,6 +1451,7 @@ cudaError_t launch_tree(TreeParams p, const TreePlan &t, void *workspace, cudaSt
   p.nb_magic = t.nb > 1 ? (uint32_t)((1ull << 32) / t.nb + 1) : 0;
   p.hb_magic = t.hb > 1 ? (uint32_t)((1ull << 32) / t.hb + 1) : 0;
   p.workers = t.workers;
+  p.whole = t.whole;
   p.hb = t.hb;
   p.nb = t.nb;
   p.parts = t.parts;
