@@ -16,10 +16,10 @@
 // but one of them). The lengths are device data, so every CTA sums them up at its start (one scan
 // over the sequences) and walks its own part. A cut costs an item more, its part of the rows in fp32 and
 // the merge: a part's start that lies within 8 granules of a unit's end moves there, and where there
-// are no more units than workers, none more than 7 or 12 granules longer than an equal part, a worker takes
-// a whole one (us, with and without: 33 x 1250, 31 nodes of 16 / 2 heads 26 and 32, 16 x 1024, 4
-// nodes of 16 / 8 19.0 and 21.5, 8-bit 33 x 100 to 4999 46 and 50; the other way 10 x 4096 37.1 and
-// 35.1, which moved starts make uneven). A unit within a worker's part is written out
+// are no more units than workers and none is much longer than an equal part, a worker takes a whole
+// one (us, with and without: 33 x 1250, 31 nodes of 16 / 2 heads 26 and 32, 16 x 1024, 4 nodes of
+// 16 / 8 18.4 and 21.5, 8-bit 33 x 100 to 4999 46 and 50; the other way 10 x 4096 37.1 and 35.1, which
+// moved starts make uneven). A unit within a worker's part is written out
 // directly; what a cut leaves is normalised and goes to the workspace with its log2-sum-exp, and
 // tree_combine_kernel merges it. Which parts there are depends on the lengths alone, so the same
 // call gives the same bits.
@@ -63,13 +63,13 @@
 // TMEM (512 columns): Q [0, 64) [64, 128), S [128, 256) [256, 384), O [384, 512).
 //
 // Measured (us; the bytes of K, V, q and out at 6.8 TB/s in brackets):
-//   bf16, 2 heads to a KV head, 8 KV heads: 8 x 1024, chains of 4    16.6 (5.0)
+//   bf16, 2 heads to a KV head, 8 KV heads: 8 x 1024, chains of 4    15.7 (5.0)
 //         256 sequences of 100 to 2048, trees of 5 to 8 nodes       193 (178)
 //   bf16, 3 to a KV head, 4 of them: 1 x 17188, 13 nodes             17.7 (5.2)
 //   bf16, 4 to a KV head, 8 of them: 16 x 32768, 4 nodes 302 (316), 32 nodes 323 (317), 48 to 64
 //         nodes, two row tiles, 425 (303; their exponentials 232, their products 232)
-//   8-bit, 2 to a KV head, 8 of them: 8 x 1024, 16 nodes             17.4 (2.5)
-//         256 sequences of 100 to 2048, trees of 5 to 8 nodes       171 (89)
+//   8-bit, 2 to a KV head, 8 of them: 8 x 1024, 16 nodes             15.7 (2.5)
+//         256 sequences of 100 to 2048, trees of 5 to 8 nodes       170 (89)
 //   8-bit, 8 to a KV head, 2 of them: 33 x 100 to 4999               46.6 (7.5)
 //   8-bit, 4 to a KV head, 8 of them: 16 x 32768, 4 nodes 221 (158), 32 nodes 262, 64 nodes 501
 // A call of a few keys takes 7 us (the launch, the scan, the chain of loads). Long bf16 contexts
@@ -1279,7 +1279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // each with a running maximum; what they have is merged in shared memory. The time is that of
 // dependent loads (the cut, then all parts at once) and of blocks that find no cut: there are as many
 // cuts as units, or workers where that is fewer. It takes 2 to 4 us of a call; where no unit can be cut
-// (no more units than workers, contexts up to 512 or 832) it is not launched (33 x 512, 31 nodes of 16 / 2
+// (no more units than workers, contexts up to 512 to 1536) it is not launched (33 x 512, 31 nodes of 16 / 2
 // heads: 19.5 -> 14.5 us).
 constexpr int kCombineWarps = 8, kInFlight = 4;  // warps of a block: at most
 template <Mode M>
@@ -1408,10 +1408,15 @@ TreePlan plan_tree(int32_t num_seqs, int32_t max_nodes, int32_t hq, int32_t hkv,
     t.row_warps *= 2;
   const size_t ctas = (size_t)t.workers * t.group;
   t.by_unit = units <= t.workers;
-  // With many more workers than units a unit is worth cutting sooner (us, limits of 7 and 12: 1 x 832
-  // with 16 / 8 heads, 19 workers, 10.7 and 12.6; 8 x 832 16.1 and 14.1).
-  t.whole = t.workers >= 4 * units ? 7 : 12;
-  t.uncut = t.by_unit && max_context <= (1 + t.whole) * kGranule;
+  // Contexts short enough are not cut and the merge is not launched, which pays the longer, the fewer
+  // workers are left without a unit (us, whole and cut; 16 / 8 heads, 19 workers): 1 x 832 12.6 and
+  // 10.7; 5 x 1024 14.5 and 16.3, 5 x 1152 15.9 and 15.1; 8 x 1024 15.7 and 17.2, 8 x 1536 20.0 and
+  // 20.3; 16 x 1536 23.6 and 25.2. Where the merge has to be launched for longer ones, a whole unit pays
+  // up to 12 granules (8 x 1536: 21.5 and 20.3), with many workers to spare up to 7.
+  const int64_t spare = units > 0 ? t.workers / units : 0;
+  const int32_t limit = spare >= 8 ? 8 : spare >= 3 ? 16 : spare >= 2 ? 20 : 24;
+  t.uncut = t.by_unit && max_context <= limit * kGranule;
+  t.whole = t.uncut ? limit : spare >= 4 ? 7 : 12;
   t.cuts = (int32_t)(t.by_unit ? std::max<int64_t>(1, units) * t.group : (int64_t)ctas);
   // Blocks of two warps (bf16 cache: of four) fit beside the main kernel's CTA and are there when it
   // ends (8-bit, 256 ragged 170 us, 172 with four warps, 176 with eight); with many rows more blocks

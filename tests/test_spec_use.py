@@ -75,6 +75,14 @@ def test_batches_around_the_number_of_workers(batch, fp8):
 
 
 @BOTH
+@pytest.mark.parametrize("batch", [1, 2, 3, 5, 6, 8, 10, 16])
+@pytest.mark.parametrize("length", [512, 513, 1024, 1025, 1280, 1281, 1536, 1537])
+def test_lengths_up_to_which_nothing_is_cut(batch, length, fp8):
+    c = Case([length] * (batch - 1) + [length - 300], [3] * batch, 16, 8, fp8=fp8, seed=length + batch)
+    check(c, c.attend(pkv))
+
+
+@BOTH
 def test_any_aligned_workspace_and_output(fp8):
     """16-byte aligned addresses: no more is promised."""
     c = Case([5000, 300], [6, 17], 8, 2, fp8=fp8, seed=5)
