@@ -1275,12 +1275,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Merges the parts of the units that a cut between two workers went through. Block (x, y): cut x, from
-// the y-th on every gridDim.y-th p.block_warps / p.row_warps rows of its tile. A row's warps take its parts in turn, four in flight,
-// each with a running maximum; what they have is merged in shared memory. The time is that of
-// dependent loads (the cut, then all parts at once) and of blocks that find no cut: there are as many
-// cuts as units, or workers where that is fewer. It takes 2 to 4 us of a call; where no unit can be cut
-// (no more units than workers, contexts up to 512 to 1536) it is not launched (33 x 512, 31 nodes of 16 / 2
-// heads: 19.5 -> 14.5 us).
+// the y-th on every gridDim.y-th p.block_warps / p.row_warps rows of its tile. A row's warps take its
+// parts in turn, four in flight, each with a running maximum; what they have is merged in shared
+// memory. The time is that of dependent loads (the cut, then all parts at once) and of blocks that
+// find no cut: there are as many cuts as units, or workers where that is fewer. It takes 2 to 4 us of
+// a call; where no unit can be cut (no more units than workers, contexts up to 512 to 1536) it is not
+// launched (33 x 512, 31 nodes of 16 / 2 heads: 19.5 -> 14.5 us).
 constexpr int kCombineWarps = 8, kInFlight = 4;  // warps of a block: at most
 template <Mode M>
 __global__ void __launch_bounds__(kCombineWarps * 32)
