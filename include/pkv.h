@@ -532,10 +532,12 @@ pkv_status pkv_kv_evict(const float *weights, int64_t weights_stride,
  * sequence b sees the positions j < P and P + j for the nodes j < n that its mask names; over
  * those, for query head hq of KV head h = hq / (num_q_heads / num_kv_heads),
  *     out[cu_seqlens_q[b] + i, hq, :] = softmax_j(scale * q . k_j) v_j          (bf16, RNE)
- * A node that sees nothing gets zeros. Scores, softmax and sums are in fp32; a weight enters
- * the value sum within 2^-16 of itself, or rounded to bf16 (2^-9) where a KV head can have more rows
- * of q than a tile of 128: that is, where max_seqlen_q > 8 * floor(16 / g), g = num_q_heads /
- * num_kv_heads query heads to a KV head (g <= 16; with more heads 128 / g nodes or fewer).
+ * A node that sees nothing gets zeros. An infinity in a V row that it sees makes its result there an
+ * infinity, whatever the weight (with one of the other sign, or a NaN: NaN). Scores, softmax and sums
+ * are in fp32; a weight enters the value sum within 2^-16 of itself, or rounded to bf16 (2^-9) where a
+ * KV head can have more rows of q than a tile of 128: that is, where max_seqlen_q > 8 * floor(16 / g),
+ * g = num_q_heads / num_kv_heads query heads to a KV head (g <= 16; with more heads 128 / g nodes or
+ * fewer).
  *
  * q:             [total_q, num_q_heads, head_dim] bf16, token stride q_tok_stride elements. Rows
  *                behind cu_seqlens_q[num_seqs] are not read, and their outputs left as they are.

@@ -332,6 +332,51 @@ __device__ __noinline__ void not_finite_fix(const TreeParams &p, int b, int h, i
   }
 }
 
+// bf16 cache: an infinity in a V row of the context, which all of a chunk's rows see, makes a row's
+// result an infinity, and NaN only with one of the other sign or a NaN. The products do not: a
+// weight enters as a sum whose second term is often zero or negative, and one that is below fp32's
+// range as zero. So where a row with a sound normaliser (`sound`) holds a value that is not finite, the
+// warp looks through the V rows of the item's context positions [key0, end) and puts down what the
+// infinities and NaNs in them add up to. `to`: the row's result (bf16, or fp32 of a part), as lane r
+// and lane 16 + r have it. Four dims to a lane, eight rows in flight.
+__device__ __noinline__ void context_fix(const TreeParams &p, int b, int h, int32_t key0, int32_t end,
+                                         bool sound, void *to, bool part) {
+  const int lane = threadIdx.x & 31;
+  const int32_t *const table = p.block_tables + (int64_t)b * p.table_width;
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int32_t pos = key0; pos < end; pos += 16) {  // (from a multiple of 64: within a block)
+    const int32_t i = pos / p.block_size, blk = table[i];
+    if (blk < 0 || blk >= p.num_blocks) continue;
+    const int64_t row = (int64_t)blk * p.block_size + (pos - i * p.block_size);
+    const uint8_t *const src = p.v_cache + ((row * p.hkv + h) * kD + 4 * lane) * 2;
+    uint2 x[16];
+#pragma unroll
+    for (int u = 0; u < 16; ++u)
+      x[u] = pos + u < end ? *reinterpret_cast<const uint2 *>(src + (int64_t)u * p.hkv * (kD * 2))
+                           : make_uint2(0, 0);
+#pragma unroll
+    for (int u = 0; u < 16; ++u) {
+      const float f[4] = {bf16_lo(x[u].x), bf16_hi(x[u].x), bf16_lo(x[u].y), bf16_hi(x[u].y)};
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+        if (!isfinite(f[d])) sum[d] += f[d];
+    }
+  }
+  __syncwarp();  // the rows' results have been written
+#pragma unroll 1
+  for (int r = 0; r < kChunkRows; ++r) {
+    const uint64_t at = __shfl_sync(kFull, reinterpret_cast<uint64_t>(to), r);
+    if (!__shfl_sync(kFull, sound, r)) continue;
+    for (int d = 0; d < 4; ++d) {
+      if (sum[d] == 0.f) continue;
+      if (part) reinterpret_cast<float *>(at)[4 * lane + d] = sum[d];
+      else reinterpret_cast<uint16_t *>(at)[4 * lane + d] = bf16_bits_rn(sum[d]);
+    }
+  }
+  __syncwarp();
+}
+
 // Walks a worker's part of the axis, one item at a time (one thread).
 struct Walk {
   int32_t x, x1, at;  // where the walk is, where the part ends, where sequence b starts
@@ -1217,6 +1262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (F8) inv *= 1.f / (1 << kOffset8);
         const int64_t slot = 2 * (int64_t)blockIdx.x + it.to;
         const int64_t at = slot * p.part_rows + c * kChunkRows + r;
+        [[maybe_unused]] float2 odd = make_float2(0.f, 0.f);  // NaN: O is not finite somewhere
         tc_fence_after_sync();
 #pragma unroll 1
         for (int k = 0; k < 2; ++k) {
@@ -1229,6 +1275,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive_count(&sm.o_free, arrivals);
           }
           if (!row) continue;
+          if constexpr (!F8) {
+            const float2 zero = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2)
+              odd = ffma2(make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), zero, odd);
+          }
           if (it.to == 2) {
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
@@ -1245,7 +1297,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 d[1] = make_uint4(w[4], w[5], w[6], w[7]);
               }
             }
-            if (dirty) not_finite_fix<M>(p, it.b, it.h, n, it.L, q_row, node, dst, 64 * k + 32 * ch, 32);
           } else {
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
@@ -1255,6 +1306,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               st_global_32b(p.part_o + at * kD + 64 * k + 32 * ch + 8 * z, w);
             }
           }
+        }
+        if constexpr (!F8) {
+          const bool sound = l > 0.f && l < INFINITY;  // (the same in both lanes of a row)
+          if (__any_sync(kFull, sound && !(odd.x + odd.y == 0.f)))
+            context_fix(p, it.b, it.h, key0, min(key1, root), row && sound,
+                        it.to == 2 ? static_cast<void *>(dst) : p.part_o + at * kD, it.to != 2);
+        }
+        if (dirty && it.to == 2 && row) {
+          not_finite_fix<M>(p, it.b, it.h, n, it.L, q_row, node, dst, 32 * ch, 32);
+          not_finite_fix<M>(p, it.b, it.h, n, it.L, q_row, node, dst, 64 + 32 * ch, 32);
         }
         if (it.to < 2) {
           if (row && ch == 0)
@@ -1282,6 +1343,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 // a call; where no unit can be cut (no more units than workers, contexts up to 512 to 1536) it is not
 // launched (33 x 512, 31 nodes of 16 / 2 heads: 19.5 -> 14.5 us).
 constexpr int kCombineWarps = 8, kInFlight = 4;  // warps of a block: at most
+// Where a part holds an infinity and its weight is below fp32's range, the product is NaN: the dims of
+// `odd` (a bit each) become what the parts' values that are not finite add up to. slots: of part 0, and
+// of part k, k step further.
+__device__ __noinline__ void parts_fix(const TreeParams &p, int parts, int64_t slot0, int64_t slot1,
+                                       int step, int t, uint32_t odd, uint16_t *out) {
+#pragma unroll 1
+  for (int d = 0; d < 4; ++d) {
+    if (!(odd >> d & 1)) continue;
+    float sum = 0.f;
+#pragma unroll 1
+    for (int k = 0; k < parts; ++k) {
+      const int64_t slot = k == 0 ? slot0 : slot1 + (int64_t)(k - 1) * step;
+      const float x = p.part_o[(slot * p.part_rows + t) * kD + d + 4 * (threadIdx.x & 31)];
+      if (!isfinite(x)) sum += x;
+    }
+    out[d] = bf16_bits_rn(sum);
+  }
+}
 template <Mode M>
 __global__ void __launch_bounds__(kCombineWarps * 32)
     tree_combine_kernel(const __grid_constant__ TreeParams p) {
@@ -1369,6 +1448,11 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
     uint16_t *dst = p.out + ((int64_t)(cut.q0 + node) * p.hq + cut.h * p.group_heads + head) * kD;
     *reinterpret_cast<uint2 *>(dst + 4 * lane) =
         make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+    uint32_t odd = 0;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) odd |= (uint32_t)isnan(o[d]) << d;
+    if (odd && !isnan(sum))
+      parts_fix(p, cut.parts, slot(0), slot(1), 2 * p.group, t, odd, dst + 4 * lane);
     if (__any_sync(kFull, dirty))
       not_finite_fix<M>(p, cut.b, cut.h, cut.n, cut.L, cut.q0 + node, node, dst, 4 * lane, 4);
   }

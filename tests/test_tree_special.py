@@ -1,0 +1,60 @@
+"""Attention of drafted tokens where values are not finite, vanish or lie far apart."""
+import numpy as np
+import pytest
+import torch
+
+from libbuild import build_and_import
+from tree_util import Case, D, assert_close, bf16_weights, rows_of
+
+pkv = build_and_import()
+pytestmark = pytest.mark.gpu
+INF, NAN = float("inf"), float("nan")
+
+
+def put(c, name, b, pos, h, dim, value):
+    blk, off = int(c.table_host[b, pos // c.bs]), pos % c.bs
+    getattr(c, name)[blk, off, h, dim] = value
+
+
+# one row tile and several, whole units and cut ones
+@pytest.mark.parametrize("ctx,nodes,hq,hkv", [([300, 90], [4, 3], 4, 2), ([17188], [13], 12, 4),
+                                              ([700, 300], [40, 3], 32, 4), ([9000, 400], [70, 9], 8, 2)])
+def test_an_infinite_value_of_the_context_is_an_infinity(ctx, nodes, hq, hkv):
+    """softmax weights are positive: a sum with an infinity is that infinity, with both signs NaN."""
+    c = Case(ctx, nodes, hq, hkv, seed=1)
+    ref, size = c.reference()
+    first = ctx[0] - nodes[0]  # positions of the context below this
+    put(c, "v", 0, 37, 0, 5, INF)
+    put(c, "v", 0, first - 1, 1, 64, -INF)
+    put(c, "v", 0, 3, 1, 9, INF)
+    put(c, "v", 0, first - 2, 1, 9, INF)
+    put(c, "v", 0, 11, 0, 100, INF)
+    put(c, "v", 0, first // 2, 0, 100, -INF)
+    put(c, "v", 0, 12, 0, 101, NAN)
+    put(c, "v", 0, first // 2, 0, 101, INF)
+    pkv.get_device_errors(reset=True)
+    out = c.attend(pkv).float()
+    assert pkv.get_device_errors(reset=True) == 0
+    g, n = hq // hkv, nodes[0]
+    assert (out[:n, :g, 5] == INF).all()
+    assert (out[:n, g:2 * g, 64] == -INF).all()
+    assert (out[:n, g:2 * g, 9] == INF).all()
+    assert torch.isnan(out[:n, :g, 100]).all() and torch.isnan(out[:n, :g, 101]).all()
+    hit = torch.zeros(out.shape, dtype=torch.bool, device="cuda")
+    for h, d in ((0, 5), (1, 64), (1, 9), (0, 100), (0, 101)):
+        hit[:n, h * g:(h + 1) * g, d] = True
+    assert_close(out[~hit], ref[~hit], size[~hit], False, bf16_weights(c.most, g))
+
+
+@pytest.mark.parametrize("ctx,nodes,hq,hkv", [([700], [5], 4, 2), ([17188], [13], 12, 4), ([9000], [70], 8, 2)])
+def test_an_infinite_value_counts_however_small_its_weight(ctx, nodes, hq, hkv):
+    """Scores that spread over hundreds: most weights are below what fp32 holds."""
+    c = Case(ctx, nodes, hq, hkv, seed=2)
+    c.q = (c.q.float() * 100).to(torch.bfloat16)
+    for i in range(0, 60):
+        put(c, "v", 0, i * (ctx[0] - nodes[0]) // 60, i % hkv, i, INF if i % 2 else -INF)
+    out = c.attend(pkv).float()
+    for i in range(60):
+        heads = slice(i % hkv * (hq // hkv), (i % hkv + 1) * (hq // hkv))
+        assert (out[:, heads, i] == (INF if i % 2 else -INF)).all(), i
+        assert torch.isfinite(out[:, heads, 60:]).all()
