@@ -86,7 +86,8 @@
 // past the context are zeroed in shared memory. A node that others do not see may hold
 // infinities or NaNs, and 0 x NaN would reach them: the nodes' V rows are looked through, what is
 // not finite becomes zero there, and the rows that do see such a node are put right in memory
-// (not_finite_fix).
+// (not_finite_fix). Infinities of the context, which all rows see, are put right where they have made a
+// row's result NaN (context_fix, parts_fix).
 #include <math.h>
 
 #include <algorithm>
@@ -1145,9 +1146,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int pos = key0 + j * kTile + 64 * k;
               if (pos < key1) {
                 const float(*sc)[4] = sm.raw.scale[g % kScaleTiles][k];
-                factor = fmaxf(factor * sc[0][pos / kGranule & 3], 1e-38f);  // (see scale_log2)
+                factor *= sc[0][pos / kGranule & 3];
                 v_scale = sc[1][pos / kGranule & 3];
               }
+              // (a row of zeros has a power of 2^-120; see scale_log2)
+              factor = fmaxf(factor, 1e-38f);
             }
           };
           float m_tile = -INFINITY;

@@ -58,3 +58,18 @@ def test_an_infinite_value_counts_however_small_its_weight(ctx, nodes, hq, hkv):
         heads = slice(i % hkv * (hq // hkv), (i % hkv + 1) * (hq // hkv))
         assert (out[:, heads, i] == (INF if i % 2 else -INF)).all(), i
         assert torch.isfinite(out[:, heads, 60:]).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("scale", [0.0, 1e-30, -1e-12, 0.09])
+def test_a_row_of_zeros_is_the_mean(scale, fp8):
+    """Scores of 0, with contexts that end in the first and in the second half of a tile."""
+    c = Case([700, 65, 64, 128, 60, 5000], [6, 3, 2, 5, 1, 4], 6, 2, fp8=fp8, seed=3)
+    c.scale = scale
+    q = c.q.clone()
+    q[::2, ::2] = 0
+    q[1::2, 1] = 0
+    c.q = q
+    out = c.attend(pkv)
+    ref, size = c.reference()
+    assert_close(out, ref, size, fp8)
