@@ -299,7 +299,8 @@ __device__ __forceinline__ uint64_t mask_word(const TreeParams &p, int64_t row, 
 }
 
 // V rows of the nodes that a row sees may hold values that are not finite, which the products left
-// out: what they add up to replaces the row's result. dims [d0, d0 + count), count a multiple of 4.
+// out: what they add up to is added to the row's result (which may be NaN, or an infinity of the
+// context, already). dims [d0, d0 + count), count a multiple of 4.
 template <Mode M>
 __device__ __noinline__ void not_finite_fix(const TreeParams &p, int b, int h, int n, int L,
                                             int64_t row, int node, uint16_t *out, int d0,
@@ -329,7 +330,8 @@ __device__ __noinline__ void not_finite_fix(const TreeParams &p, int b, int h, i
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (!(sum[i] == 0.f)) out[d + i] = bf16_bits_rn(sum[i]);
+      if (!(sum[i] == 0.f))
+        out[d + i] = bf16_bits_rn(__uint_as_float((uint32_t)out[d + i] << 16) + sum[i]);
   }
 }
 

@@ -73,3 +73,32 @@ def test_a_row_of_zeros_is_the_mean(scale, fp8):
     out = c.attend(pkv)
     ref, size = c.reference()
     assert_close(out, ref, size, fp8)
+
+
+# whole units and cut ones, one row tile and several
+@pytest.mark.parametrize("ctx,n,hq,hkv", [(300, 6, 4, 2), (17188, 13, 12, 4), (9000, 70, 8, 2)])
+def test_infinities_of_nodes_leave_what_is_nan_or_infinite_already(ctx, n, hq, hkv):
+    c = Case([ctx, 200], [n, 2], hq, hkv, seed=4)
+    g, node = hq // hkv, 2
+    sees = torch.from_numpy(c.masks[0][:, node]).cuda()
+    assert sees[node + 1:].any() and not sees.all()
+    at = ctx - n + node
+    for dim in (3, 70, 90, 91):
+        put(c, "v", 0, at, 0, dim, INF)
+    put(c, "v", 0, 40, 0, 70, -INF)
+    put(c, "v", 0, ctx - n - 1, 0, 90, NAN)
+    put(c, "v", 0, 41, 0, 91, INF)
+    q = c.q.clone()
+    q[node, 0, 17] = NAN
+    c.q = q
+    out = c.attend(pkv).float()[:n, :g]
+    lost = torch.zeros((n, g), dtype=torch.bool, device="cuda")
+    lost[node, 0] = True
+    assert torch.isnan(out[lost]).all()
+    seen = sees[:, None] & ~lost
+    for dim, want in ((3, INF), (70, NAN), (90, NAN), (91, INF)):
+        x = out[..., dim]
+        assert (torch.isnan(x[seen]) if want != want else x[seen] == want).all(), dim
+        x = x[~sees[:, None] & ~lost]
+        want = {3: 0.0, 70: -INF, 90: NAN, 91: INF}[dim]
+        assert (torch.isnan(x) if want != want else torch.isfinite(x) if want == 0 else x == want).all(), dim
