@@ -553,7 +553,8 @@ pkv_status pkv_kv_evict(const float *weights, int64_t weights_stride,
  * block_tables:  [num_seqs, block_table_width] int32; blocks may be shared, as a cached prefix is.
  *                A bad block id (PKV_DEVERR_BLOCK_RANGE) counts as keys and values of zeros.
  * workspace:     pkv_tree_workspace_bytes(...) bytes, 16-byte aligned, private to this call while
- *                it runs; its contents need no initialisation.
+ *                it runs; its contents need no initialisation. What is enough for some bounds (num_seqs,
+ *                max_seqlen_q, max_context_len) is enough for smaller ones.
  * out:           [total_q, num_q_heads, head_dim] bf16, contiguous; may not overlap q.
  * Implemented: head_dim == 128, block_size a multiple of 256, num_blocks * block_size < 2^31,
  * max_seqlen_q <= 2^20, q_tok_stride a multiple of 8, 16-byte aligned q, pools, scales and out; any

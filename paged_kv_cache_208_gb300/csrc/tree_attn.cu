@@ -1473,6 +1473,10 @@ struct TreePlan {
   int32_t cuts, cut_blocks;  // and blocks to merge one
   size_t dirty, part_o, part_lse, bytes;  // of the workspace
 };
+// x * y, or 2^40 where that is less (no product of sizes overflows)
+int64_t times(int64_t x, int64_t y) {
+  return (int64_t)std::min<__int128>((__int128)x * y, (__int128)1 << 40);
+}
 TreePlan plan_tree(int32_t num_seqs, int32_t max_nodes, int32_t hq, int32_t hkv,
                    int32_t max_context, int num_sms) {
   TreePlan t{};
@@ -1486,16 +1490,17 @@ TreePlan plan_tree(int32_t num_seqs, int32_t max_nodes, int32_t hq, int32_t hkv,
   t.heads = 1;
   while (t.heads * 2 * t.at_once <= kMaxGroup && hkv % (t.heads * 2) == 0) t.heads *= 2;
   t.group = t.heads * t.at_once;
-  const int64_t units = t.units =
-      (int64_t)num_seqs * (hkv / t.heads) * ((tiles + t.at_once - 1) / t.at_once);
-  t.longest = units * std::max(1, (int)(((int64_t)max_context + kGranule - 1) / kGranule));
+  const int64_t rounds = (tiles + t.at_once - 1) / t.at_once;
+  const int64_t units = t.units = times(times(num_seqs, hkv / t.heads), rounds);
+  const int64_t granules = std::max<int64_t>(1, ((int64_t)max_context + kGranule - 1) / kGranule);
+  t.longest = times(units, granules);
   t.workers = (int32_t)std::max<int64_t>(1, std::min<int64_t>(num_sms / t.group, t.longest));
   t.part_rows = (int32_t)(std::min<int64_t>(kChunks, std::max<int64_t>(1, chunks)) * kChunkRows);
   // as many warps to a row as leave each about four of its parts (of units of equal length)
   t.row_warps = 1;
   while (units > 0 && t.row_warps < kCombineWarps && t.workers / units >= 4 * t.row_warps)
     t.row_warps *= 2;
-  const size_t ctas = (size_t)t.workers * t.group;
+  const int32_t ctas = t.workers * t.group;
   t.by_unit = units <= t.workers;
   // Contexts short enough are not cut and the merge is not launched, which pays the longer, the fewer
   // workers are left without a unit (us, whole and cut; 16 / 8 heads, 19 workers): 1 x 832 12.6 and
@@ -1506,7 +1511,7 @@ TreePlan plan_tree(int32_t num_seqs, int32_t max_nodes, int32_t hq, int32_t hkv,
   const int32_t limit = spare >= 8 ? 8 : spare >= 3 ? 16 : spare >= 2 ? 20 : 24;
   t.uncut = t.by_unit && max_context <= limit * kGranule;
   t.whole = t.uncut ? limit : spare >= 4 ? 7 : 12;
-  t.cuts = (int32_t)(t.by_unit ? std::max<int64_t>(1, units) * t.group : (int64_t)ctas);
+  t.cuts = t.by_unit ? (int32_t)std::max<int64_t>(1, units) * t.group : ctas;
   // Blocks of two warps (bf16 cache: of four) fit beside the main kernel's CTA and are there when it
   // ends (8-bit, 256 ragged 170 us, 172 with four warps, 176 with eight); with many rows more blocks
   // cost more (8 x 1024, 64 nodes of 16 / 8 heads: 23.8, 23.0, 22.6). As many as all rows take, but no
@@ -1515,10 +1520,15 @@ TreePlan plan_tree(int32_t num_seqs, int32_t max_nodes, int32_t hq, int32_t hkv,
   t.cut_blocks = t.part_rows * t.row_warps / t.block_warps;
   if (t.row_warps == 1)
     t.cut_blocks = std::max(1, std::min(t.cut_blocks, 32 / t.block_warps * num_sms / t.cuts));
-  t.dirty = (size_t)t.cuts * sizeof(CutInfo);
-  t.part_o = (t.dirty + ctas * 2 * sizeof(int32_t) + 31) / 32 * 32;
-  t.part_lse = t.part_o + ctas * 2 * t.part_rows * kD * sizeof(float);
-  t.bytes = align16(t.part_lse + ctas * 2 * t.part_rows * sizeof(float)) + 16;  // (see launch_tree)
+  // The workspace has room for as many CTAs and cuts as a call of these bounds or smaller ones can have:
+  // a workspace for a program's largest call is large enough for all others, although one more row
+  // tile may leave fewer CTAs (two groups of 76 make 152, three of 50 make 150).
+  const size_t most =
+      (size_t)std::max<int64_t>(ctas, std::min<int64_t>(num_sms, times(t.longest, t.group)));
+  t.dirty = most * sizeof(CutInfo);
+  t.part_o = (t.dirty + most * 2 * sizeof(int32_t) + 31) / 32 * 32;
+  t.part_lse = t.part_o + most * 2 * t.part_rows * kD * sizeof(float);
+  t.bytes = align16(t.part_lse + most * 2 * t.part_rows * sizeof(float)) + 16;  // (see launch_tree)
   return t;
 }
 

@@ -1,4 +1,5 @@
-"""Attention of drafted tokens where values are not finite, vanish or lie far apart."""
+"""Attention of drafted tokens where values are not finite, vanish or lie far apart, and in workspaces of
+other calls."""
 import numpy as np
 import pytest
 import torch
@@ -102,3 +103,28 @@ def test_infinities_of_nodes_leave_what_is_nan_or_infinite_already(ctx, n, hq, h
         x = x[~sees[:, None] & ~lost]
         want = {3: 0.0, 70: -INF, 90: NAN, 91: INF}[dim]
         assert (torch.isnan(x) if want != want else torch.isfinite(x) if want == 0 else x == want).all(), dim
+
+
+@pytest.mark.parametrize("hq,hkv", [(16, 8), (32, 8), (16, 2), (12, 4), (6, 1), (48, 3), (64, 4), (20, 1)])
+def test_a_workspace_is_enough_for_smaller_bounds(hq, hkv):
+    seqs = (1, 2, 3, 8, 19, 20, 33, 64, 256, 1000)
+    nodes = (1, 2, 7, 8, 9, 16, 17, 32, 33, 48, 64, 65, 96, 97, 128, 129, 200, 256, 257, 400, 1000)
+    lens = (1, 64, 65, 128, 500, 4096, 32768, 2 ** 31 - 1)
+    size = np.array([[[pkv.lib().pkv_tree_workspace_bytes(b, n, hq, hkv, D, L) for L in lens] for n in nodes]
+                     for b in seqs])
+    for axis in range(3):
+        assert (np.diff(size, axis=axis) >= 0).all(), axis
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("hq,hkv,large", [(32, 8, 65), (16, 2, 33)])
+def test_one_workspace_for_trees_of_all_sizes(hq, hkv, large, fp8):
+    ws = pkv.tree_workspace(16, large, hq, hkv, D, 4096)
+    ws.fill_(255)
+    rng = np.random.default_rng(13)
+    for n, batch in ((large, 16), (large - 1, 16), (8, 16), (1, 3)):
+        ctx = [int(x) for x in rng.integers(3000, 4097, batch)]
+        c = Case(ctx, [n] * batch, hq, hkv, fp8=fp8, seed=n)
+        out = c.attend(pkv, workspace=ws)
+        ref, size = c.reference()
+        assert_close(out, ref, size, fp8, bf16_weights(n, hq // hkv))
