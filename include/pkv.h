@@ -534,7 +534,7 @@ pkv_status pkv_kv_evict(const float *weights, int64_t weights_stride,
  *     out[cu_seqlens_q[b] + i, hq, :] = softmax_j(scale * q . k_j) v_j          (bf16, RNE)
  * A node that sees nothing gets zeros. An infinity in a V row that it sees makes its result there an
  * infinity, whatever the weight (with one of the other sign, or a NaN: NaN). Scores, softmax and sums
- * are in fp32; a weight enters the value sum within 2^-16 of itself, or rounded to bf16 (2^-9) where a
+ * are in fp32; a weight enters the value sum within 2^-16 of itself, or rounded to bf16 (2^-8) where a
  * KV head can have more rows of q than a tile of 128: that is, where max_seqlen_q > 8 * floor(16 / g),
  * g = num_q_heads / num_kv_heads query heads to a KV head (g <= 16; with more heads 128 / g nodes or
  * fewer).
@@ -579,7 +579,11 @@ pkv_status pkv_paged_tree_attn(const void *q, int64_t q_tok_stride, int64_t tota
  * paged_tree_attn_fp8 -- the same over the 8-bit cache (k_scale, v_scale: its scales, as for
  * pkv_paged_decode_attn_fp8). Scores are products of K's codes with a row of q in two e4m3 parts, exact
  * for values down to 2^-9 of the row's largest |q| and within 2^-17 of that largest one below (a row
- * with an infinity or a NaN gives NaN); weights enter the value sum within 2^-11 of themselves.
+ * with an infinity or a NaN gives NaN). A weight enters the value sum as one fp16 number together with
+ * the V scale of its key's group: within 2^-11 of itself or, with its V scale, 2^-31 of the row's largest
+ * weight with its V scale, whichever is more. (Codes multiplied by weights and scales that are more than
+ * 2^20 below the row's largest lose digits, and more than 2^31 below they drop out of the sum. The sum of the
+ * weights keeps them.) V's scales of one context within 2^100 of one another, as there.
  */
 pkv_status pkv_paged_tree_attn_fp8(const void *q, int64_t q_tok_stride, int64_t total_q,
                                    const void *k_cache, const void *v_cache, const float *k_scale,

@@ -33,10 +33,10 @@
 // rescaled only when a row's maximum grows by more than 2^8, as in prefill.cu.
 //
 // What P is rounded to:
-//   bf16 cache, one row tile at a time: two bf16 parts, P = hi + lo within 2^-17 of itself. The
+//   bf16 cache, one row tile at a time: two bf16 parts, P = hi + lo within 2^-16 of itself. The
 //                second product's time is hidden behind the loads (a tile's 64 KiB take an SM about
 //                2700 cycles, its products 1536), and the output is that of fp32 weights.
-//   bf16 cache, several row tiles: bf16. The tensor cores are the limit there (the same keys once per
+//   bf16 cache, several row tiles: bf16 (2^-8). The tensor cores are the limit there (the same keys once per
 //                tile), and two parts would cost half as much again.
 //   8-bit cache: fp16 (2^-11), see below.
 //
@@ -46,8 +46,10 @@
 // fp16 in shared memory (an e4m3 code is an fp16 value) and multiplied by P in fp16. (Widening K too
 // is bound by shared memory: 192 KiB through it per tile, 1536 cycles, where a tile's loads take
 // 1350; this way 144.) The K scale of a key's group and the row's power multiply the scores. The V scale
-// is part of P: with v = log2 of it, m runs over s + v, P' = 2^(s + v - m + 6) (between 2^-20 and
-// 2^14 in fp16's normal range), and l sums P' / 2^(v + 6).
+// is part of P: with v = log2 of it, m runs over s + v, P' = 2^(s + v - m + 6), and l sums
+// P' / 2^(v + 6), before it is rounded. A row's largest P' lies between 2^6 and 2^14 (m may lag behind by
+// 2^8). fp16 has normal numbers from 2^-14 and steps of 2^-24 below: a P' is off by 2^-11 of itself
+// or 2^-25, which is 2^-31 of the largest.
 //
 // Rows. 16 rows make a chunk: nb = 16 / G nodes with their G query heads (with more than 16 heads
 // one node and 16 of them). Chunk c of a tile lies in 16 of the 128 TMEM lanes, in quadrant c % 4, that

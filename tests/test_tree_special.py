@@ -128,3 +128,40 @@ def test_one_workspace_for_trees_of_all_sizes(hq, hkv, large, fp8):
         out = c.attend(pkv, workspace=ws)
         ref, size = c.reference()
         assert_close(out, ref, size, fp8, bf16_weights(n, hq // hkv))
+
+
+@pytest.mark.parametrize("ctx,n,hq,hkv", [([700, 190, 64], 5, 4, 2), ([9000], 30, 8, 1), ([2500, 1300], 20, 16, 2)])
+def test_scales_of_v_that_lie_far_apart(ctx, n, hq, hkv):
+    """A weight with its V scale is an fp16 number, the largest of a row at least 2^6: it is off by 2^-11 of
+    itself or by 2^-25, 2^-31 of the largest, times its code. Half of the dims are zeros in the groups
+    with large scales, so that what those with small ones add up to is all there is."""
+    rng = np.random.default_rng(5)
+    c = Case(ctx, [n] * len(ctx), hq, hkv, fp8=True, seed=5)
+    scale = c.scales[1]  # [blocks, heads, groups]
+    e = torch.from_numpy(rng.choice([-90, -24, -20, -12, -8, 5], scale.shape)).cuda()
+    scale.copy_(torch.where(torch.isnan(scale), scale, torch.exp2(e.float())))
+    codes = c.v.view(torch.uint8).view(c.nb, c.bs // 64, 64, hkv, D)
+    e = e.transpose(1, 2)  # [blocks, groups, heads]
+    codes[(e == -90)[:, :, None, :].expand(-1, -1, 64, -1)] = 0
+    large = (e >= -8)[:, :, None, :].expand(-1, -1, 64, -1)
+    codes[..., 64:][large] = 0
+    out = c.attend(pkv).double()
+    ref, size = c.reference()
+    floor = torch.zeros_like(ref)
+    t = 0
+    for b, L in enumerate(ctx):
+        sees = torch.ones((n, L), dtype=torch.bool)
+        sees[:, L - n:] = torch.from_numpy(c.masks[b])
+        sees = sees.cuda()[:, None, None, :]
+        q = c.q[t:t + n].double().view(n, hkv, hq // hkv, D)
+        x = torch.einsum("nhgd,lhd->nhgl", q, c.values("k", b)) * c.scale
+        p = torch.softmax(x.masked_fill(~sees, -INF), dim=-1)
+        r = torch.from_numpy(rows_of(c.table_host[b], L, c.bs)).cuda()
+        s = c.scales[1].transpose(1, 2).reshape(-1, hkv)[r // 64].double()  # [L, heads]
+        code = (c.values("v", b) / s[..., None]).abs()
+        top = (p * s.T[None, :, None, :]).amax(-1, keepdim=True)
+        total = torch.einsum("nl,lhd->nhd", sees[:, 0, 0].double(), code)[:, :, None, :]
+        floor[t:t + n] = (2.0 ** -31 * top * total).reshape(n, hq, D)
+        t += n
+    bound = 2.0 ** -8 * ref.abs() + 2.0 ** -9 * size + floor
+    assert ((out - ref).abs() <= bound).all()
