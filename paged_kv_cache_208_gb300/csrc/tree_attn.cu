@@ -87,9 +87,8 @@
 // Masked places. A key that a row does not see is left out of its maximum and gets P = 0; V rows
 // past the context are zeroed in shared memory. A node that others do not see may hold
 // infinities or NaNs, and 0 x NaN would reach them: the nodes' V rows are looked through, what is
-// not finite becomes zero there, and the rows that do see such a node are put right in memory
-// (not_finite_fix). Infinities of the context, which all rows see, are put right where they have made a
-// row's result NaN (context_fix, parts_fix).
+// not finite becomes zero there, and the rows that do see such a node are put right in memory. So are
+// rows of which infinities of the context have made NaN (not_finite_fix, parts_fix).
 #include <math.h>
 
 #include <algorithm>
@@ -219,12 +218,10 @@ struct TreeParams {
   int32_t hb, nb, parts;         // heads and nodes of a chunk; chunks that share its nodes
   uint32_t nb_magic, hb_magic;   // x / nb is the high word of x * nb_magic, for x < 2^24
   // cuts: one for each unit and CTA of a worker (by_unit: there are no more units than workers), or
-  // one for each CTA, the unit that its part ends in. dirty: the CTAs' slots with items that met values
-  // that are not finite.
+  // one for each CTA, the unit that its part ends in.
   bool by_unit;
   int32_t max_units;
   CutInfo *cuts;
-  int32_t *dirty;
   float *part_o, *part_lse;      // [CTA][2][part_rows][kD], [CTA][2][part_rows]
   int32_t part_rows, row_warps, block_warps;  // of tree_combine_kernel: warps for a row, of a block
   int32_t whole;  // granules that a unit may be longer than a part without being cut
@@ -300,83 +297,110 @@ __device__ __forceinline__ uint64_t mask_word(const TreeParams &p, int64_t row, 
   return top < 0 ? 0 : top >= 63 ? ~0ull : (2ull << top) - 1;
 }
 
-// V rows of the nodes that a row sees may hold values that are not finite, which the products left
-// out: what they add up to is added to the row's result (which may be NaN, or an infinity of the
-// context, already). dims [d0, d0 + count), count a multiple of 4.
+// Values of V that are not finite. Those of nodes were left out of the products: what a row sees of
+// them is added to its result. Infinities of the context were not, but the products may have made NaN
+// of them (a weight enters as a sum whose second term is often zero or negative, and one below fp32's
+// range as zero), where an infinity is right as long as there is no NaN and none of the other sign:
+// with `again` a NaN is replaced by what the context's values that are not finite add up to.
+// A warp for a chunk of an item, lane r has row r's `to` (bf16, or fp32 of a part) and whether it is to be
+// put right (`sound`: a row whose normaliser is not is NaN already). Four dims to a lane, eight rows of V in
+// flight: a granule takes 5 us, or 80 with 64 infinite nodes, and the CTA's other warps wait for 2 s.
 template <Mode M>
-__device__ __noinline__ void not_finite_fix(const TreeParams &p, int b, int h, int n, int L,
-                                            int64_t row, int node, uint16_t *out, int d0,
-                                            int count) {
-#pragma unroll 1
-  for (int d = d0; d < d0 + count; d += 4) {
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-    for (int j = 0; j < n; ++j) {
-      if (!(mask_word(p, row, node, j >> 6) >> (j & 63) & 1)) continue;
-      const int64_t pos = (int64_t)L - n + j;
-      const int64_t blk = p.block_tables[(int64_t)b * p.table_width + pos / p.block_size];
-      if (blk < 0 || blk >= p.num_blocks) continue;
-      const int64_t at = ((blk * p.block_size + pos % p.block_size) * p.hkv + h) * kD + d;
-      float x[4];
-      if constexpr (M == kFp8) {
-        const uint32_t w = *reinterpret_cast<const uint32_t *>(p.v_cache + at);
-        const float2 lo = f16x2_to_f32(cvt_f16x2_e4m3x2(w)), hi = f16x2_to_f32(cvt_f16x2_e4m3x2_hi(w));
-        x[0] = lo.x, x[1] = lo.y, x[2] = hi.x, x[3] = hi.y;
-      } else {
-        const uint2 w = *reinterpret_cast<const uint2 *>(p.v_cache + 2 * at);
-        x[0] = bf16_lo(w.x), x[1] = bf16_hi(w.x), x[2] = bf16_lo(w.y), x[3] = bf16_hi(w.y);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (!isfinite(x[i])) sum[i] += x[i];
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (!(sum[i] == 0.f))
-        out[d + i] = bf16_bits_rn(__uint_as_float((uint32_t)out[d + i] << 16) + sum[i]);
-  }
-}
-
-// bf16 cache: an infinity in a V row of the context, which all of a chunk's rows see, makes a row's
-// result an infinity, and NaN only with one of the other sign or a NaN. The products do not: a
-// weight enters as a sum whose second term is often zero or negative, and one that is below fp32's
-// range as zero. So where a row with a sound normaliser (`sound`) holds a value that is not finite, the
-// warp looks through the V rows of the item's context positions [key0, end) and puts down what the
-// infinities and NaNs in them add up to. `to`: the row's result (bf16, or fp32 of a part), as lane r
-// and lane 16 + r have it. Four dims to a lane, eight rows in flight.
-__device__ __noinline__ void context_fix(const TreeParams &p, int b, int h, int32_t key0, int32_t end,
-                                         bool sound, void *to, bool part) {
+__device__ __noinline__ void not_finite_fix(const TreeParams &p, int b, int h, int32_t root, int32_t key0,
+                                            int32_t key1, bool again, bool sound, int64_t q_row,
+                                            int node, void *to, bool part) {
   const int lane = threadIdx.x & 31;
   const int32_t *const table = p.block_tables + (int64_t)b * p.table_width;
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-  for (int32_t pos = key0; pos < end; pos += 16) {  // (from a multiple of 64: within a block)
-    const int32_t i = pos / p.block_size, blk = table[i];
-    if (blk < 0 || blk >= p.num_blocks) continue;
-    const int64_t row = (int64_t)blk * p.block_size + (pos - i * p.block_size);
-    const uint8_t *const src = p.v_cache + ((row * p.hkv + h) * kD + 4 * lane) * 2;
-    uint2 x[16];
-#pragma unroll
-    for (int u = 0; u < 16; ++u)
-      x[u] = pos + u < end ? *reinterpret_cast<const uint2 *>(src + (int64_t)u * p.hkv * (kD * 2))
-                           : make_uint2(0, 0);
-#pragma unroll
-    for (int u = 0; u < 16; ++u) {
-      const float f[4] = {bf16_lo(x[u].x), bf16_hi(x[u].x), bf16_lo(x[u].y), bf16_hi(x[u].y)};
-#pragma unroll
-      for (int d = 0; d < 4; ++d)
-        if (!isfinite(f[d])) sum[d] += f[d];
+  constexpr int kBytes = M == kFp8 ? 1 : 2, kLoads = 8;
+  using Word = std::conditional_t<M == kFp8, uint32_t, uint2>;  // four values
+  auto odd = [](Word x, float (&f)[4]) {  // zeros for finite ones
+    if constexpr (M == kFp8) {
+      const float2 lo = f16x2_to_f32(cvt_f16x2_e4m3x2(x)), hi = f16x2_to_f32(cvt_f16x2_e4m3x2_hi(x));
+      f[0] = lo.x, f[1] = lo.y, f[2] = hi.x, f[3] = hi.y;
+    } else {
+      f[0] = bf16_lo(x.x), f[1] = bf16_hi(x.x), f[2] = bf16_lo(x.y), f[3] = bf16_hi(x.y);
     }
-  }
-  __syncwarp();  // the rows' results have been written
-#pragma unroll 1
-  for (int r = 0; r < kChunkRows; ++r) {
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+      if (isfinite(f[d])) f[d] = 0.f;
+  };
+  auto add = [&](int r, const float (&sum)[4], bool replace) {  // to row r's results
     const uint64_t at = __shfl_sync(kFull, reinterpret_cast<uint64_t>(to), r);
-    if (!__shfl_sync(kFull, sound, r)) continue;
+    if (!__shfl_sync(kFull, sound, r)) return;
+#pragma unroll
     for (int d = 0; d < 4; ++d) {
       if (sum[d] == 0.f) continue;
-      if (part) reinterpret_cast<float *>(at)[4 * lane + d] = sum[d];
-      else reinterpret_cast<uint16_t *>(at)[4 * lane + d] = bf16_bits_rn(sum[d]);
+      float *const x32 = reinterpret_cast<float *>(at) + 4 * lane + d;
+      uint16_t *const x16 = reinterpret_cast<uint16_t *>(at) + 4 * lane + d;
+      const float x = part ? *x32 : __uint_as_float((uint32_t)*x16 << 16);
+      const float y = replace && isnan(x) ? sum[d] : x + sum[d];
+      if (part) *x32 = y;
+      else *x16 = bf16_bits_rn(y);
+    }
+  };
+  __syncwarp();  // the results have been written
+  float all[4] = {0.f, 0.f, 0.f, 0.f};  // of the context
+#pragma unroll 1
+  for (int32_t pos = again ? key0 : max(key0, root & ~(kGranule - 1)); pos < key1; pos += kGranule) {
+    const int count = min(kGranule, key1 - pos), nodes_at = root - pos;
+    const int32_t i = pos / p.block_size, blk = table[i];
+    const bool any = blk >= 0 && blk < p.num_blocks;
+    const int64_t row = (int64_t)blk * p.block_size + (pos - i * p.block_size);
+    const int64_t stride = (int64_t)p.hkv * (kD * kBytes);
+    const uint8_t *const src = p.v_cache + row * stride + (h * kD + 4 * lane) * kBytes;
+    uint64_t bad = 0;
+#pragma unroll 1
+    for (int j = 0; any && j < count; j += kLoads) {
+      Word x[kLoads];
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u)
+        x[u] = j + u < count ? *reinterpret_cast<const Word *>(src + (j + u) * stride) : Word{};
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) {
+        float f[4];
+        odd(x[u], f);
+        if (j + u < nodes_at) {
+#pragma unroll
+          for (int d = 0; d < 4; ++d) all[d] += f[d];
+        } else if (!(f[0] == 0.f && f[1] == 0.f && f[2] == 0.f && f[3] == 0.f)) {
+          bad |= 1ull << (j + u);
+        }
+      }
+    }
+    // (the granule that the item's part of the context ends in)
+    if (again && pos < root && pos + kGranule >= min(root, key1))
+#pragma unroll 1
+      for (int r = 0; r < kChunkRows; ++r) add(r, all, true);
+    bad = (uint64_t)__reduce_or_sync(kFull, (uint32_t)(bad >> 32)) << 32 |
+          __reduce_or_sync(kFull, (uint32_t)bad);
+    if (bad == 0) continue;
+    const int w = -nodes_at >> 6, sh = -nodes_at & 63;  // (w = -1: positions before the tree)
+#pragma unroll 1
+    for (int r = 0; r < kChunkRows; ++r) {
+      const int64_t at = __shfl_sync(kFull, q_row, r);
+      const int i_node = __shfl_sync(kFull, node, r);
+      if (!__shfl_sync(kFull, sound, r)) continue;
+      uint64_t bits = w < 0 ? 0 : mask_word(p, at, i_node, w);
+      if (sh) bits = bits >> sh | mask_word(p, at, i_node, w + 1) << (64 - sh);
+      bits &= bad;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+      while (bits) {
+        Word x[kLoads];
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+          x[u] = bits ? *reinterpret_cast<const Word *>(src + (__ffsll(bits) - 1) * stride) : Word{};
+          bits &= bits - 1;
+        }
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+          float f[4];
+          odd(x[u], f);
+#pragma unroll
+          for (int d = 0; d < 4; ++d) sum[d] += f[d];
+        }
+      }
+      add(r, sum, false);
     }
   }
   __syncwarp();
@@ -1314,20 +1338,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if constexpr (!F8) {
-          const bool sound = l > 0.f && l < INFINITY;  // (the same in both lanes of a row)
-          if (__any_sync(kFull, sound && !(odd.x + odd.y == 0.f)))
-            context_fix(p, it.b, it.h, key0, min(key1, root), row && sound,
-                        it.to == 2 ? static_cast<void *>(dst) : p.part_o + at * kD, it.to != 2);
-        }
-        if (dirty && it.to == 2 && row) {
-          not_finite_fix<M>(p, it.b, it.h, n, it.L, q_row, node, dst, 32 * ch, 32);
-          not_finite_fix<M>(p, it.b, it.h, n, it.L, q_row, node, dst, 64 + 32 * ch, 32);
-        }
+        const bool sound = l > 0.f && l < INFINITY;  // (the same in both lanes of a row)
+        // (an 8-bit cache has NaNs only, which the context's products spread themselves)
+        const bool again = !F8 && __any_sync(kFull, sound && !(odd.x + odd.y == 0.f));
+        if (dirty || again)
+          not_finite_fix<M>(p, it.b, it.h, root, key0, key1, again, row && sound, q_row, node,
+                            it.to == 2 ? static_cast<void *>(dst) : p.part_o + at * kD, it.to != 2);
         if (it.to < 2) {
           if (row && ch == 0)
             p.part_lse[at] = l > 0.f ? m_run + log2_approx(l) : l == 0.f ? -INFINITY : l;
-          if (c == 0 && lane == 0) p.dirty[slot] = dirty;
         }
         release_item(sm, taken, lane);
         ++taken;
@@ -1384,8 +1403,6 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
   auto slot = [&](int k) -> int64_t {
     return 2 * ((int64_t)(cut.worker + k) * p.group + rank) + (k == 0 ? 1 : 0);
   };
-  bool dirty = false;
-  for (int k = lane; k < cut.parts; k += 32) dirty |= p.dirty[slot(k)] != 0;
   // (with several warps to a row there are as many blocks as it takes)
   for (int y = blockIdx.y; y < p.part_rows * p.row_warps / p.block_warps; y += gridDim.y) {
     const int t = y * (p.block_warps / p.row_warps) + row_in;  // row of the tile
@@ -1460,8 +1477,6 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
     for (int d = 0; d < 4; ++d) odd |= (uint32_t)isnan(o[d]) << d;
     if (odd && !isnan(sum))
       parts_fix(p, cut.parts, slot(0), slot(1), 2 * p.group, t, odd, dst + 4 * lane);
-    if (__any_sync(kFull, dirty))
-      not_finite_fix<M>(p, cut.b, cut.h, cut.n, cut.L, cut.q0 + node, node, dst, 4 * lane, 4);
   }
 }
 
@@ -1473,7 +1488,7 @@ struct TreePlan {
   bool by_unit, uncut;     // uncut: whatever the lengths are, no unit is cut
   int32_t whole;             // see TreeParams
   int32_t cuts, cut_blocks;  // and blocks to merge one
-  size_t dirty, part_o, part_lse, bytes;  // of the workspace
+  size_t part_o, part_lse, bytes;  // of the workspace
 };
 // x * y, or 2^40 where that is less (no product of sizes overflows)
 int64_t times(int64_t x, int64_t y) {
@@ -1527,8 +1542,7 @@ TreePlan plan_tree(int32_t num_seqs, int32_t max_nodes, int32_t hq, int32_t hkv,
   // tile may leave fewer CTAs (two groups of 76 make 152, three of 50 make 150).
   const size_t most =
       (size_t)std::max<int64_t>(ctas, std::min<int64_t>(num_sms, times(t.longest, t.group)));
-  t.dirty = most * sizeof(CutInfo);
-  t.part_o = (t.dirty + most * 2 * sizeof(int32_t) + 31) / 32 * 32;
+  t.part_o = most * sizeof(CutInfo);
   t.part_lse = t.part_o + most * 2 * t.part_rows * kD * sizeof(float);
   t.bytes = align16(t.part_lse + most * 2 * t.part_rows * sizeof(float)) + 16;  // (see launch_tree)
   return t;
@@ -1567,7 +1581,6 @@ cudaError_t launch_tree(TreeParams p, const TreePlan &t, void *workspace, cudaSt
   p.cuts = reinterpret_cast<CutInfo *>(ws);
   p.by_unit = t.by_unit;
   p.max_units = (int32_t)t.units;
-  p.dirty = reinterpret_cast<int32_t *>(ws + t.dirty);
   p.part_o = reinterpret_cast<float *>(ws + t.part_o);
   p.part_lse = reinterpret_cast<float *>(ws + t.part_lse);
   p.part_rows = t.part_rows;

@@ -165,3 +165,46 @@ def test_scales_of_v_that_lie_far_apart(ctx, n, hq, hkv):
         t += n
     bound = 2.0 ** -8 * ref.abs() + 2.0 ** -9 * size + floor
     assert ((out - ref).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_a_value_that_is_not_finite_in_a_large_tree(fp8):
+    """2^18 nodes in a chain, behind 700 positions: what they see of it is found in a bounded time."""
+    n, P, bs = 1 << 18, 700, 256
+    L = P + n
+    nb = -(-L // bs)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(6)
+    rand = lambda rows, m: m * torch.randn((rows, 1, D), generator=g, device="cuda")
+    q = rand(n, 1.0).to(torch.bfloat16)
+    k, v = rand(nb * bs, 1.0), rand(nb * bs, 0.3)
+    kind, scales = (torch.float8_e4m3fn if fp8 else torch.bfloat16), ()
+    k, v = k.to(kind), v.to(kind)
+    if fp8:
+        scales = tuple(torch.ones((nb, 1, bs // 64), device="cuda") for _ in range(2))
+    kd, vd = k.double()[:, 0], v.double()[:, 0]
+    v = v.clone()
+    raw = v.view(torch.uint8)
+    early, late = P + 3, P + 200000
+    if fp8:
+        raw[early, 0, 7] = raw[late, 0, 9] = 0x7F
+    else:
+        v[early, 0, 7], v[late, 0, 9] = INF, NAN
+    table = torch.arange(nb, dtype=torch.int32, device="cuda")[None]
+    lens = torch.tensor([L], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    pools = (k.view(nb, bs, 1, D), v.view(nb, bs, 1, D), *scales)
+    pkv.get_device_errors(reset=True)
+    call = pkv.paged_tree_attn_fp8 if fp8 else pkv.paged_tree_attn
+    out = call(q, *pools, table, lens, L, cu, n, D ** -0.5)
+    assert pkv.get_device_errors(reset=True) == 0
+    assert torch.isfinite(out[:3]).all()
+    x = out[3:, 0, 7].float()
+    assert (torch.isnan(x) if fp8 else x == INF).all()
+    assert torch.isfinite(out[:200000, 0, 9]).all() and torch.isnan(out[200000:, 0, 9]).all()
+    dims = torch.tensor([d for d in range(D) if d not in (7, 9)], device="cuda")
+    for i in (0, 2, 3, 63, 64, 127, 128, 70001, 199999, n - 1):
+        s = (kd[:P + i + 1] @ q[i, 0].double()) * D ** -0.5
+        p = torch.softmax(s, 0)
+        ref, size = p @ vd[:P + i + 1], p @ vd[:P + i + 1].abs()
+        assert_close(out[i, 0, dims], ref[dims], size[dims], fp8, True)
