@@ -534,10 +534,9 @@ pkv_status pkv_kv_evict(const float *weights, int64_t weights_stride,
  *     out[cu_seqlens_q[b] + i, hq, :] = softmax_j(scale * q . k_j) v_j          (bf16, RNE)
  * A node that sees nothing gets zeros. An infinity in a V row that it sees makes its result there an
  * infinity, whatever the weight (with one of the other sign, or a NaN: NaN). Scores, softmax and sums
- * are in fp32; a weight enters the value sum within 2^-16 of itself, or rounded to bf16 (2^-8) where a
- * KV head can have more rows of q than a tile of 128: that is, where max_seqlen_q > 8 * floor(16 / g),
- * g = num_q_heads / num_kv_heads query heads to a KV head (g <= 16; with more heads 128 / g nodes or
- * fewer).
+ * are in fp32; a weight enters the value sum within 2^-16 of itself, or rounded to bf16 (2^-8) for a
+ * sequence with more rows of q at a KV head than a tile of 128: that is, where n > 8 * floor(16 / g),
+ * g = num_q_heads / num_kv_heads query heads to a KV head (g <= 16; with more heads, n * ceil(g / 16) > 8).
  *
  * q:             [total_q, num_q_heads, head_dim] bf16, token stride q_tok_stride elements. Rows
  *                behind cu_seqlens_q[num_seqs] are not read, and their outputs left as they are.

@@ -33,11 +33,12 @@
 // rescaled only when a row's maximum grows by more than 2^8, as in prefill.cu.
 //
 // What P is rounded to:
-//   bf16 cache, one row tile at a time: two bf16 parts, P = hi + lo within 2^-16 of itself. The
-//                second product's time is hidden behind the loads (a tile's 64 KiB take an SM about
+//   bf16 cache, a sequence whose rows fit one tile: two bf16 parts, P = hi + lo within 2^-16 of itself.
+//                The second product's time is hidden behind the loads (a tile's 64 KiB take an SM about
 //                2700 cycles, its products 1536), and the output is that of fp32 weights.
-//   bf16 cache, several row tiles: bf16 (2^-8). The tensor cores are the limit there (the same keys once per
-//                tile), and two parts would cost half as much again.
+//   bf16 cache, more rows: bf16 (2^-8). The tensor cores are the limit there (the same keys once per
+//                tile), and two parts would cost half as much again. This goes by the sequence's own
+//                nodes: that others of the call have larger trees costs a small one no precision.
 //   8-bit cache: fp16 (2^-11), see below.
 //
 // The 8-bit cache. S is a product of e4m3 operands, K as it lies: a row of Q, multiplied by a power of
@@ -131,7 +132,7 @@ constexpr int kMaxGroup = 8, kMaxTiles = 4;  // CTAs, and row tiles, of a worker
 constexpr int kNear = 8;        // granules that a part may grow or shrink by at an end
 constexpr int kOffset8 = 6;     // log2 of what P' is larger by, 8-bit cache
 
-enum Mode { kTwoParts, kOnePart, kFp8 };
+enum Mode { kBf16, kFp8 };
 
 // A worker's share of a unit.
 struct Item {
@@ -142,7 +143,8 @@ struct Item {
   int32_t key0, key1;  // positions
   int32_t tiles;
   int32_t to;          // 0, 1: a partial result, into this slot of the CTA's; 2: the output
-  int32_t pad[4];
+  int32_t two;         // bf16 cache: P in two parts
+  int32_t pad[3];
 };
 static_assert(sizeof(Item) == 64, "");
 
@@ -437,6 +439,7 @@ struct Walk {
       it.L = s.L;
       it.c0 = (tile * p.at_once + row_tile) * kChunks;
       it.chunks = min(kChunks, p.chunks_of(s.n) - it.c0);
+      it.two = p.chunks_of(s.n) <= kChunks;
       it.key0 = min(s.L, off * kGranule);
       it.key1 = (int32_t)min((int64_t)s.L, (int64_t)(off + take) * kGranule);
       it.tiles = (it.key1 - it.key0 + kTile - 1) / kTile;
@@ -1024,6 +1027,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ip) break;
         const int last = ip->last, tiles = ip->tiles, key0 = ip->key0, key1 = ip->key1;
         const int root = ip->L - ip->n;
+        [[maybe_unused]] const bool two = ip->two;
         release_item(sm, taken, lane);
         ++taken;
         if (last) break;
@@ -1081,8 +1085,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t pc = p0 + 64 * (kk >> 2) + 8 * (kk & 3);
                 umma_f16_ts(tmem + kOCol, pc, dv + ((kk * 16 * 128) >> 4), kIdesc,
                             j > 0 || kk > 0);
-                if constexpr (M == kTwoParts)
-                  umma_f16_ts(tmem + kOCol, pc + 32, dv + ((kk * 16 * 128) >> 4), kIdesc, true);
+                if constexpr (!F8)
+                  if (two) umma_f16_ts(tmem + kOCol, pc + 32, dv + ((kk * 16 * 128) >> 4), kIdesc, true);
               };
               // (in a loop an issue takes 67 cycles, about as long as the product)
               if (steps == kTile / 16) {
@@ -1126,6 +1130,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int c = (warp + 4 * (taken & 1)) & 7;
         const uint32_t lane_addr = tmem + ((uint32_t)((c & 3) * 32 + (c >> 2) * 16) << 16);
         const bool mine = c < ip->chunks;  // (warp-uniform)
+        [[maybe_unused]] const bool two = ip->two;
         const int chunk = ip->c0 + c, node = p.first_node(chunk) + i;
         const int head = p.first_head(chunk) + head_r;
         const int64_t q_row = (int64_t)ip->q0 + node;
@@ -1255,7 +1260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float2 rs0 = make_float2(0.f, 0.f), rs1 = make_float2(0.f, 0.f);
             tmem_ld_wait(x);
             uint32_t hi[16];
-            [[maybe_unused]] uint32_t lo[16];
+            [[maybe_unused]] uint32_t lo[16];  // (bf16 cache: the second part, used or not)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const float2 t = ffma2(
@@ -1267,12 +1272,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 hi[e] = pack_f16x2(pe.x, pe.y);
               } else {
                 hi[e] = pack_bf16x2(pe.x, pe.y);
-                if constexpr (M == kTwoParts)
-                  lo[e] = pack_bf16x2(pe.x - bf16_lo(hi[e]), pe.y - bf16_hi(hi[e]));
+                x[2 * e] = __float_as_uint(pe.x);
+                x[2 * e + 1] = __float_as_uint(pe.y);
               }
             }
             tmem_st16x2_16<16>(s_addr + 64 * k, hi);
-            if constexpr (M == kTwoParts) tmem_st16x2_16<16>(s_addr + 64 * k + 32, lo);
+            if constexpr (!F8)
+              if (two) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                  lo[e] = pack_bf16x2(__uint_as_float(x[2 * e]) - bf16_lo(hi[e]),
+                                      __uint_as_float(x[2 * e + 1]) - bf16_hi(hi[e]));
+                tmem_st16x2_16<16>(s_addr + 64 * k + 32, lo);
+              }
             l_run += ((rs0.x + rs0.y) + (rs1.x + rs1.y)) * per_v;
           }
           tmem_st_wait();
@@ -1683,9 +1695,8 @@ pkv_status tree_attn(const void *q, int64_t q_tok_stride, int64_t total_q, const
   prm.out_32b = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
   prm.err = err;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = fp8                 ? launch_tree<kFp8>(prm, plan, workspace, st)
-                        : plan.at_once == 1 ? launch_tree<kTwoParts>(prm, plan, workspace, st)
-                                            : launch_tree<kOnePart>(prm, plan, workspace, st);
+  const cudaError_t e = fp8 ? launch_tree<kFp8>(prm, plan, workspace, st)
+                            : launch_tree<kBf16>(prm, plan, workspace, st);
   return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 

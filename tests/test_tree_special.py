@@ -208,3 +208,17 @@ def test_a_value_that_is_not_finite_in_a_large_tree(fp8):
         p = torch.softmax(s, 0)
         ref, size = p @ vd[:P + i + 1], p @ vd[:P + i + 1].abs()
         assert_close(out[i, 0, dims], ref[dims], size[dims], fp8, True)
+
+
+def test_the_weights_of_small_trees_keep_their_precision_beside_large_ones():
+    """Few keys of either sign, so that a weight rounded to bf16 shows."""
+    ctx, nodes = [2, 3, 4, 5, 6, 7, 8, 9, 10, 300], [1, 2, 3, 2, 5, 6, 7, 8, 9, 70]
+    c = Case(ctx, nodes, 8, 2, seed=7)
+    for bound in (70, 300):
+        c.most = bound
+        mask = torch.nn.functional.pad(c.mask, (0, -(-bound // 64) - c.mask.shape[1]))
+        out = c.attend(pkv, tree_mask=mask)
+        ref, size = c.reference()
+        small = sum(nodes[:-1])
+        assert_close(out[:small], ref[:small], size[:small], False, False)
+        assert_close(out[small:], ref[small:], size[small:], False, True)
