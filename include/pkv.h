@@ -542,7 +542,11 @@ pkv_status pkv_kv_evict(const float *weights, int64_t weights_stride,
  *                behind cu_seqlens_q[num_seqs] are not read, and their outputs left as they are.
  * cu_seqlens_q:  [num_seqs + 1] int32, non-decreasing, within [0, total_q]. max_seqlen_q: upper
  *                bound of n. A sequence with a bad entry, or longer than that, is left out
- *                (PKV_DEVERR_SEQLEN_RANGE).
+ *                (PKV_DEVERR_SEQLEN_RANGE). The bound should be near the largest n, and the trees of one
+ *                call of about one size: it says how many CTAs share a KV head's keys (one for every 128
+ *                rows of q, up to four), and those that a smaller tree has no rows for wait. 256
+ *                sequences of 5 to 8 nodes, 16 / 8 heads, take 193 us with a bound of 8 to 64, 301 with
+ *                65 (two CTAs with 65 to 128), 435 with 129, 567 with more than 192.
  * context_lens:  [num_seqs] int32 in [n, max_context_len]. Another length, or one longer than the
  *                block table's row, gives the sequence's nodes zeros (PKV_DEVERR_CONTEXT_RANGE).
  * tree_mask:     NULL: a chain, node i sees the nodes 0 .. i. Else [total_q, mask_words] 64-bit
@@ -557,7 +561,9 @@ pkv_status pkv_kv_evict(const float *weights, int64_t weights_stride,
  * out:           [total_q, num_q_heads, head_dim] bf16, contiguous; may not overlap q.
  * Implemented: head_dim == 128, block_size a multiple of 256, num_blocks * block_size < 2^31,
  * max_seqlen_q <= 2^20, q_tok_stride a multiple of 8, 16-byte aligned q, pools, scales and out; any
- * num_q_heads / num_kv_heads; contexts below 2^31 - 1024; as long as the batch's work stays below 2^30:
+ * num_q_heads / num_kv_heads; contexts below 2^31 - 1024 (a CTA's waits end after 2 s with
+ * PKV_DEVERR_TIMEOUT; its share of a context takes about one for 2^26 keys, or for 2^24 with infinities in
+ * V); as long as the batch's work stays below 2^30:
  * num_seqs times the granules of 64 keys of max_context_len (or of the block table's row, if that is
  * less), times the 128-row tiles of max_seqlen_q nodes and the KV heads, as many of both as CTAs take
  * together counting once.

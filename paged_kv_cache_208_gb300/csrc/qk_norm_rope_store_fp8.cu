@@ -21,10 +21,14 @@
 // 132k tokens of 16 + 2 x 8 heads take 329 us (6.0 TB/s): 460 us with eight lanes to a row and a
 // quarter of a head's 64 rows in each thread, 357 us with half of them and the next head loaded
 // ahead, 350 us with two values to an instruction, 344 us with the queries by tokens. Three CTAs of
-// 80 registers fit an SM; two of 128 take 348 us, four of 64 spill and take 378 us.
+// 80 registers (12 bytes of them spilled) fit an SM; two of 128 take 348 us, four of 64 spill more and take
+// 378 us. A few drafted tokens behind a context are where it is far from its bytes: 256 sequences of 5 to 8 take
+// 26 us (4.3 us of bytes), 45 us where every scale grows, since a CTA's heads follow one another, each with a
+// barrier and an old scale to load.
 //
-// A step of one token per sequence takes half a warp per head row: 8 tokens 2.7 us, the latency
-// of a launch and of three loads that depend on one another.
+// A step of one token per sequence takes half a warp per head row: 8 tokens 2.6 us, the latency
+// of a launch and of three loads that depend on one another; 14 us where a group's scale grows (256 tokens:
+// 4.1 and 19 us), since the half warp then re-rounds the up to 63 rows from before one after the other.
 #include <math.h>
 
 #include <algorithm>

@@ -39,7 +39,8 @@
 //   bf16 cache, more rows: bf16 (2^-8). The tensor cores are the limit there (the same keys once per
 //                tile), and two parts would cost half as much again. This goes by the sequence's own
 //                nodes: that others of the call have larger trees costs a small one no precision.
-//   8-bit cache: fp16 (2^-11), see below.
+//   8-bit cache: fp16 (2^-11), see below. Two parts would make a long call a quarter longer (16 x 32768,
+//                4 nodes 220 -> 267 us, 256 ragged 168 -> 223), for values that e4m3 rounds by 2^-4.
 //
 // The 8-bit cache. S is a product of e4m3 operands, K as it lies: a row of Q, multiplied by a power of
 // two (its largest |q| becomes 128 to 256), enters as two e4m3 parts, which hold a bf16 value
@@ -68,13 +69,18 @@
 // Measured (us; the bytes of K, V, q and out at 6.8 TB/s in brackets):
 //   bf16, 2 heads to a KV head, 8 KV heads: 8 x 1024, chains of 4    15.7 (5.0)
 //         256 sequences of 100 to 2048, trees of 5 to 8 nodes       193 (178)
-//   bf16, 3 to a KV head, 4 of them: 1 x 17188, 13 nodes             17.7 (5.2)
-//   bf16, 4 to a KV head, 8 of them: 16 x 32768, 4 nodes 302 (316), 32 nodes 323 (317), 48 to 64
-//         nodes, two row tiles, 425 (303; their exponentials 232, their products 232)
+//   bf16, 3 to a KV head, 4 of them: 1 x 17188, 13 nodes             17.6 (5.2)
+//   bf16, 4 to a KV head, 8 of them: 16 x 32768, 4 nodes 308 (316), 32 nodes 333 (317); 16 x 30000 to
+//         32768, 48 to 64 nodes, two row tiles, 428, 475 where calls follow one another for long and the
+//         power limit lowers the clock (303; their exponentials 232, their products 232)
 //   8-bit, 2 to a KV head, 8 of them: 8 x 1024, 16 nodes             15.7 (2.5)
-//         256 sequences of 100 to 2048, trees of 5 to 8 nodes       170 (89)
+//         256 sequences of 100 to 2048, trees of 5 to 8 nodes       168 (89)
 //   8-bit, 8 to a KV head, 2 of them: 33 x 100 to 4999               46.6 (7.5)
-//   8-bit, 4 to a KV head, 8 of them: 16 x 32768, 4 nodes 221 (158), 32 nodes 262, 64 nodes 501
+//   8-bit, 4 to a KV head, 8 of them: 16 x 32768, 4 nodes 220 (158), 32 nodes 267, 64 nodes 510
+// The CTAs of a worker are as many as the call's largest tree asks for (max_seqlen_q): those that a
+// smaller one has no rows for wait. The same 256 sequences, 8 to 64 nodes allowed / up to 128 / 192 / more:
+// bf16 193 / 301 / 435 / 567, 8-bit 168 / 325 / 475 / 619; with one tree of two tiles among them (32 / 8
+// heads, 64 nodes) 198 -> 305 and 173 -> 328.
 // A call of a few keys takes 7 us (the launch, the scan, the chain of loads). Long bf16 contexts
 // go at the memory's rate. What bounds the rest is the chain of a tile's steps (S, softmax, P V, the
 // hand-over of a buffer between two warps four times): about 1 us a tile and two of them under
@@ -1531,8 +1537,10 @@ TreePlan plan_tree(int32_t num_seqs, int32_t max_nodes, int32_t hq, int32_t hkv,
     t.row_warps *= 2;
   const int32_t ctas = t.workers * t.group;
   t.by_unit = units <= t.workers;
-  // Contexts short enough are not cut and the merge is not launched, which pays the longer, the fewer
-  // workers are left without a unit (us, whole and cut; 16 / 8 heads, 19 workers): 1 x 832 12.6 and
+  // Contexts short enough (by max_context_len: with 32768 in its place 8 x 1024 takes 17.3 us, 15.5 with
+  // 1024) are not cut and the merge is not launched, which pays the longer, the fewer workers are left
+  // without a unit. The limits were read off these shapes, of 16 / 8 heads and 19 workers, and go for all (us,
+  // whole and cut): 1 x 832 12.6 and
   // 10.7; 5 x 1024 14.5 and 16.3, 5 x 1152 15.9 and 15.1; 8 x 1024 15.7 and 17.2, 8 x 1536 20.0 and
   // 20.3; 16 x 1536 23.6 and 25.2. Where the merge has to be launched for longer ones, a whole unit pays
   // up to 12 granules (8 x 1536: 21.5 and 20.3), with many workers to spare up to 7.
