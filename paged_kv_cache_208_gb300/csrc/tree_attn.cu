@@ -1537,22 +1537,23 @@ TreePlan plan_tree(int32_t num_seqs, int32_t max_nodes, int32_t hq, int32_t hkv,
     t.row_warps *= 2;
   const int32_t ctas = t.workers * t.group;
   t.by_unit = units <= t.workers;
-  // Contexts short enough (by max_context_len: with 32768 in its place 8 x 1024 takes 17.3 us, 15.5 with
-  // 1024) are not cut and the merge is not launched, which pays the longer, the fewer workers are left
-  // without a unit. The limits were read off these shapes, of 16 / 8 heads and 19 workers, and go for all (us,
-  // whole and cut): 1 x 832 12.6 and
-  // 10.7; 5 x 1024 14.5 and 16.3, 5 x 1152 15.9 and 15.1; 8 x 1024 15.7 and 17.2, 8 x 1536 20.0 and
-  // 20.3; 16 x 1536 23.6 and 25.2. Where the merge has to be launched for longer ones, a whole unit pays
-  // up to 12 granules (8 x 1536: 21.5 and 20.3), with many workers to spare up to 7.
+  // Contexts short enough (by max_context_len: 8 x 1024 takes 17.3 us where that is 32768, 15.5 where it
+  // is 1024) are not cut and the merge is not launched, which pays the longer, the fewer workers are left
+  // without a unit. The limits were read off these shapes of 16 / 8 heads, 19 workers, and go for all (us,
+  // whole and cut): 1 x 832 12.6 and 10.7; 5 x 1024 14.5 and 16.3, 5 x 1152 15.9 and 15.1; 8 x 1024 15.7
+  // and 17.2, 8 x 1536 20.0 and 20.3; 16 x 1536 23.6 and 25.2. Where the merge has to be launched for
+  // longer ones, a whole unit pays up to 12 granules (8 x 1536: 21.5 and 20.3), with many workers to
+  // spare up to 7.
   const int64_t spare = units > 0 ? t.workers / units : 0;
   const int32_t limit = spare >= 8 ? 8 : spare >= 3 ? 16 : spare >= 2 ? 20 : 24;
   t.uncut = t.by_unit && max_context <= limit * kGranule;
   t.whole = t.uncut ? limit : spare >= 4 ? 7 : 12;
   t.cuts = t.by_unit ? (int32_t)std::max<int64_t>(1, units) * t.group : ctas;
-  // Blocks of two warps (bf16 cache: of four) fit beside the main kernel's CTA and are there when it
-  // ends (8-bit, 256 ragged 170 us, 172 with four warps, 176 with eight); with many rows more blocks
-  // cost more (8 x 1024, 64 nodes of 16 / 8 heads: 23.8, 23.0, 22.6). As many as all rows take, but no
-  // more than run at once unless a row takes several warps.
+  // Blocks of two warps fit beside the main kernel's CTA over the 8-bit cache (118 of 128 registers a
+  // thread) and are there when it ends (256 ragged 170 us, 172 with four warps, 176 with eight; the bf16
+  // kernel's CTA has all registers); with many rows more blocks cost more (8 x 1024, 64 nodes of 16 / 8
+  // heads: 23.8, 23.0, 22.6). As many as all rows take, but no more than run at once unless a row takes
+  // several warps.
   t.block_warps = std::max(t.part_rows <= 32 ? 2 : 4, t.row_warps);
   t.cut_blocks = t.part_rows * t.row_warps / t.block_warps;
   if (t.row_warps == 1)
