@@ -485,6 +485,29 @@ struct Rows {
   }
 };
 
+// Raise the phase's expected transaction bytes without arriving.
+__device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)),
+               "r"(bytes)
+               : "memory");
+}
+
+// mbar_arrive for `count` arrivals at once.
+__device__ __forceinline__ void mbar_arrive_count(uint64_t *bar, uint32_t count) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(count)
+               : "memory");
+}
+
+// ld_once_u4 for data that are read again.
+__device__ __forceinline__ uint4 ld_u4(const uint4 *p) {
+  uint4 r;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
+
 // wait_parity in fewer instructions (this kernel has some thirty waits, and its warps run code of their
 // own side by side: what does not fit the instruction caches costs more than the waits): the clock
 // and the abort bit are looked at once in 256 polls, each of which waits for some time itself.
